@@ -61,10 +61,13 @@ extern "C" {
 #define SPEC_STATUS_OK 0
 #define SPEC_STATUS_TOKEN_RANGE 1 /* a draft/node token is outside [0, V) */
 #define SPEC_STATUS_BAD_TREE 2    /* parents[] is not a tree rooted at 0, or too deep */
-#define SPEC_STATUS_BAD_LENGTH 3  /* draft_len or hist_len outside its range */
+#define SPEC_STATUS_BAD_LENGTH 3  /* draft_len, hist_len or another length outside its range */
+#define SPEC_STATUS_BAD_PAGE 5    /* a page of the cache outside its pool */
+#define SPEC_STATUS_BAD_INDEX 6   /* a row index outside the rows */
 
 #define SPEC_DTYPE_F32 0
 #define SPEC_DTYPE_BF16 1
+#define SPEC_DTYPE_F16 2 /* rows of the spec_cache_* entry points only */
 
 /* `op` argument of spec_workspace_size */
 #define SPEC_OP_NGRAM 0
@@ -73,6 +76,10 @@ extern "C" {
 #define SPEC_OP_TREE 3
 #define SPEC_OP_DRAW 4
 #define SPEC_OP_FILTER 5 /* spec_filter_rows: B = rows */
+/* `op` argument of spec_cache_workspace_size */
+#define SPEC_OP_CACHE_ATTEND 6
+#define SPEC_OP_CACHE_WEIGHTS 7
+#define SPEC_OP_CACHE_EVICT 8
 
 /* Limits checked on the host. */
 #define SPEC_MAX_K 64        /* draft length of a chain */
@@ -378,6 +385,158 @@ int spec_tree_rerank(const int32_t *parents, const float *conf, const int32_t *n
                      int m, int max_depth, int32_t *sel_nodes, int32_t *sel_parents, int32_t *sel_depth,
                      float *sel_value, int32_t *sel_tok, uint8_t *mask, int32_t *n_sel, int32_t *status,
                      void *stream);
+
+/*
+ * The target's cache in 8 bits, and the verify step's attention over it.
+ *
+ * The verify step's one target forward over k drafted tokens, or over a
+ * flattened draft tree ("Speculative Decoding II": one forward over all
+ * nodes with tree attention), attends from a few rows to a long context.
+ * These entry points hold that context in e4m3, write rows into it, attend
+ * over it with the mask that spec_tree_rerank returns, commit the path that
+ * spec_verify_* accepted, and cut a drafter's small cache out of it by the
+ * attention weight each token received (a lossy cache is fine for a drafter:
+ * verification keeps the target's distribution whatever q is).
+ *
+ * struct spec_cache (HOST memory, read during the call; its pointers are
+ * device memory).  A pool of num_pages pages; a page holds page_size
+ * consecutive positions of one request for every kv head:
+ *   k, v              e4m3 bytes, [num_pages][kv_heads][page_size][head_dim];
+ *                     pages are page_stride bytes apart (a multiple of 16, at
+ *                     least kv_heads * page_size * head_dim); 16-byte aligned.
+ *   k_scale, v_scale  fp32, [num_pages][kv_heads], scale_stride floats apart:
+ *                     a stored byte x stands for x * scale of its page and
+ *                     head.  Positive and within [2^-60, 2^60].
+ *   table             int32 [B][table_stride]: entry i of request b is the
+ *                     page of its positions [i*page_size, (i+1)*page_size).
+ *                     Entries past a request's length are not read.
+ *   page_size is 16, 32, 64, 128 or 256; head_dim a multiple of 16, at most 256.
+ * Keys are stored as they come (rotated by the caller), so the order of
+ * tokens within a cache carries no meaning of its own.
+ *
+ * The scale that a block (page and head) of largest finite magnitude amax
+ * needs is the smallest power of two s with amax <= 448 s, held within
+ * [2^-60, 2^60] (2^-60 for a block of zeros).  A power of two costs e4m3 no
+ * precision, and makes a later change of a block's scale exact but for
+ * values that become subnormal.  Stored value: x / s rounded to nearest
+ * even, magnitudes above 448 s saturated; infinities and NaN are stored as
+ * NaN.
+ *
+ * dtype of the rows: SPEC_DTYPE_BF16 or SPEC_DTYPE_F16 (spec_cache_append
+ * takes SPEC_DTYPE_F32 too).  Strides are in elements, in the order request,
+ * token, head; head_dim values are contiguous.  Any strides are served; rows
+ * that start on 16-byte boundaries are faster.
+ *
+ * status[b] (out int32 [B] or NULL): SPEC_STATUS_BAD_LENGTH (a length or
+ * count out of range), SPEC_STATUS_BAD_PAGE (a page outside the pool) or
+ * SPEC_STATUS_BAD_INDEX (an index outside the rows).
+ *
+ * spec_cache_append -- write rows behind each request's context.
+ *   k, v        the rows: n tokens a request.
+ *   index       NULL, or int32 [B][index_stride]: the i-th row written is
+ *               token index[b][i] (path_nodes of spec_verify_tree: the
+ *               accepted path is committed over the draft's rows).
+ *   n_rows      rows a request at most: n without index, else the entries of
+ *               index (<= index_stride).
+ *   counts      int32 [B] or NULL (= n_rows), each in [0, n_rows]: how many
+ *               rows to write (n_emit of spec_verify_*: root and accepted
+ *               nodes, 0 for a request that failed).
+ *   cache_len   int32 [B]: row i goes to position cache_len[b] + i.  What
+ *               the cache held at or past cache_len is overwritten or stays
+ *               unspecified.  A block that held tokens keeps the larger of
+ *               its scale and the one the new rows need, its tokens rounded
+ *               again when the scale grows.
+ *   new_len     out int32 [B]: cache_len + counts (cache_len for a bad
+ *               request, whose slots from cache_len on are unspecified).
+ *               Other memory than cache_len.
+ *   Pages that are written must not be shared between requests.
+ *
+ * spec_cache_attend -- attention of N rows a request over its cache, the
+ * rows' own keys and values included (append them first).
+ *   q           N tokens, Hq heads (a multiple of kv_heads; query head h
+ *               reads kv head h / (Hq / kv_heads)).
+ *   cache_len   int32 [B]: context length before the N rows; row i's own
+ *               position is cache_len[b] + i.
+ *   n_query     int32 [B] or NULL (= N), each in [0, N]: rows of a request;
+ *               later rows get 0 and lse -inf, as every row of a bad request.
+ *   mask        uint8 [B][N][N] or NULL: row i sees the context and the
+ *               rows j < n_query[b] with mask[b][i][j] != 0.  NULL: j <= i.
+ *   scale       finite; softcap >= 0: scores are s = scale q.k, or
+ *               softcap * tanh(s / softcap) when softcap > 0.
+ *   out         q's dtype: softmax(scores) v; 0 for a row that sees nothing.
+ *   lse         out fp32 [B][N][Hq] or NULL: log of the sum of exp(score),
+ *               -inf for a row that sees nothing.
+ *   A position that a row does not see has no part in the row, whatever it
+ *   holds.  A row that sees a value of NaN is NaN, in its NaN components at
+ *   least.
+ *   workspace   spec_cache_workspace_size(SPEC_OP_CACHE_ATTEND, ...) bytes.
+ *
+ * spec_cache_weights -- the attention weight each cached token received:
+ *   out[b][h][j] = prev[b][h][j] + sum over rows i and the query heads of kv
+ *   head h of exp(score - lse), for j < cache_len[b] + counts[b], where row
+ *   i is token index[b][i] of q and lse (i itself without index), sits at
+ *   position cache_len[b] + i and sees every position up to its own.  Called
+ *   after the commit, with the index and counts of spec_cache_append, the
+ *   rows that count are the accepted ones.  A row whose lse is -inf adds
+ *   nothing.  Later positions are not written, nor is anything of a bad
+ *   request.
+ *   lse         fp32 [B][N][Hq], as spec_cache_attend wrote it.
+ *   prev        fp32, NULL for zeros; prev and out: request b, head h at
+ *               b*stride[0] + h*stride[1] elements; they may be the same
+ *               memory.
+ *   positions   how many a head of prev and out holds: a request of more is
+ *               SPEC_STATUS_BAD_LENGTH.
+ *   workspace   spec_cache_workspace_size(SPEC_OP_CACHE_WEIGHTS, ...) bytes.
+ *
+ * spec_cache_evict -- copy what is worth keeping of each request's cache to
+ * other pages: per kv head the `recent` last positions and, of the others,
+ * those of the largest weight (ties to the lower position, NaN below every
+ * number), min(keep, cache_len[b]) in all, in their order.
+ *   weights     fp32, strides as above, `positions` to a head: a longer
+ *               cache_len[b] is SPEC_STATUS_BAD_LENGTH.
+ *   keep >= 1, 0 <= recent <= keep.
+ *   dst         the cache written (its table: the new pages); the same
+ *               kv_heads, page_size and head_dim.  It may be the same pool,
+ *               its pages other ones than any that are read.  Blocks get the
+ *               scale their tokens need.
+ *   kept        out int32 [B][kv_heads][keep]: positions, then -1.
+ *   kept_weights  out fp32 [B][kv_heads][keep] or NULL: their weights, then 0.
+ *   new_len     out int32 [B]: min(keep, cache_len[b]), 0 for a bad request.
+ *               Other memory than cache_len.
+ *   workspace   spec_cache_workspace_size(SPEC_OP_CACHE_EVICT, ...) bytes.
+ *
+ * spec_cache_workspace_size -- bytes for a call (B, N rows, Hq query heads)
+ * over a cache of this geometry; 0 for invalid arguments and for calls that
+ * need none.  The workspace needs no initialisation.
+ */
+typedef struct spec_cache {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  int64_t page_stride, scale_stride;
+  int32_t num_pages, kv_heads, page_size, head_dim;
+  const int32_t *table;
+  int32_t table_stride;
+} spec_cache;
+
+int spec_cache_append(const spec_cache *cache, const void *k, const int64_t *k_stride, const void *v,
+                      const int64_t *v_stride, int dtype, int B, int n, const int32_t *index, int index_stride,
+                      int n_rows, const int32_t *counts, const int32_t *cache_len, int32_t *new_len,
+                      int32_t *status, void *stream);
+int spec_cache_attend(const spec_cache *cache, const void *q, const int64_t *q_stride, int dtype, int B, int N,
+                      int Hq, const int32_t *cache_len, const int32_t *n_query, const uint8_t *mask, float scale,
+                      float softcap, void *out, const int64_t *out_stride, float *lse, int32_t *status,
+                      void *workspace, size_t workspace_bytes, void *stream);
+int spec_cache_weights(const spec_cache *cache, const void *q, const int64_t *q_stride, int dtype, int B, int N,
+                       int Hq, const float *lse, const int32_t *index, int index_stride, int n_rows,
+                       const int32_t *counts, const int32_t *cache_len, float scale, float softcap,
+                       const float *prev, const int64_t *prev_stride, float *out, const int64_t *out_stride,
+                       int positions, int32_t *status, void *workspace, size_t workspace_bytes, void *stream);
+int spec_cache_evict(const spec_cache *cache, const spec_cache *dst, int B, const int32_t *cache_len,
+                     const float *weights, const int64_t *weights_stride, int positions, int keep, int recent,
+                     int32_t *kept,
+                     float *kept_weights, int32_t *new_len, int32_t *status, void *workspace,
+                     size_t workspace_bytes, void *stream);
+size_t spec_cache_workspace_size(int op, const spec_cache *cache, int B, int N, int Hq);
 
 /*
  * spec_workspace_size -- bytes of workspace a call needs.

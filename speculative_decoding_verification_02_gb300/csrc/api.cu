@@ -235,6 +235,8 @@ const char *spec_status_string(int code) {
     case 100 + SPEC_STATUS_TOKEN_RANGE: return "request has a token outside [0, V)";
     case 100 + SPEC_STATUS_BAD_TREE: return "request has a malformed or too deep tree";
     case 100 + SPEC_STATUS_BAD_LENGTH: return "request has a length outside its range";
+    case 100 + SPEC_STATUS_BAD_PAGE: return "request has a cache page outside the pool";
+    case 100 + SPEC_STATUS_BAD_INDEX: return "request has a row index outside the rows";
     default: return "unknown code";
   }
 }

@@ -1,0 +1,157 @@
+// Shared parts of the 8-bit cache kernels: the pool's geometry, the page
+// table, e4m3 conversions and block scales, and the parameter blocks.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "spec_verify.h"
+
+namespace sv {
+
+// A pool of pages and a page table, as the kernels use them.
+struct CacheView {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  int64_t page_stride, scale_stride;
+  int num_pages, kv_heads, page_shift, head_dim;  // page_size = 1 << page_shift
+  const int32_t *table;
+  int table_stride;
+};
+
+struct CacheAppendParams {
+  CacheView c;
+  const char *k, *v;
+  int64_t ks[3], vs[3];  // element strides: request, token, head
+  int dtype, B, n, n_rows, index_stride;
+  int touched;  // pages that a request's rows can touch at most
+  const int32_t *index, *counts, *cache_len;
+  int32_t *new_len, *status;
+};
+
+struct CacheAttendParams {
+  CacheView c;
+  const char *q;
+  char *out;
+  int64_t qs[3], os[3];
+  int dtype, B, N, Hq, group;  // group: query heads to a kv head
+  const int32_t *cache_len, *n_query;
+  const uint8_t *mask;
+  float scale, softcap;
+  float *lse;
+  int32_t *status;
+};
+
+struct CacheWeightsParams {
+  CacheView c;
+  const char *q;
+  int64_t qs[3];
+  int dtype, B, N, Hq, group, n_rows, index_stride;
+  const float *lse;
+  const int32_t *index, *counts, *cache_len;
+  float scale, softcap;
+  const float *prev;
+  float *out;
+  int64_t prev_s[2], out_s[2];
+  int positions;
+  int32_t *status;
+};
+
+struct CacheEvictParams {
+  CacheView c, d;
+  int B, positions, keep, recent;
+  const int32_t *cache_len;
+  const float *weights;
+  int64_t ws[2];
+  int32_t *kept;
+  float *kept_weights;
+  int32_t *new_len, *status;
+};
+
+cudaError_t launch_cache_append(const CacheAppendParams &P, cudaStream_t st);
+cudaError_t launch_cache_attend(const CacheAttendParams &P, cudaStream_t st);
+cudaError_t launch_cache_weights(const CacheWeightsParams &P, cudaStream_t st);
+cudaError_t launch_cache_evict(const CacheEvictParams &P, cudaStream_t st);
+
+#ifdef __CUDACC__
+
+constexpr int kScaleLow = -60, kScaleHigh = 60;  // exponents that a block's scale can have
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// The smallest power of two s with amax <= 448 s, within the exponents above.
+// 448 = 1.75 * 2^8: the exponent of amax less 8, and one more when its
+// significand is above 1.75.  Exact: it reads amax's bits.
+__device__ __forceinline__ float block_scale(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = max(kScaleLow, min(kScaleHigh, e));
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// |x| for the maximum of a block: infinities and NaN do not count.
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a < INFINITY ? a : 0.0f;
+}
+
+// Two values (already divided by the scale) to e4m3, a in the low byte:
+// nearest even, saturated at 448; infinities become NaN, as NaN does.
+__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
+  uint16_t r;
+  if (fabsf(a) == INFINITY) a = NAN;
+  if (fabsf(b) == INFINITY) b = NAN;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// Two e4m3 bytes (low byte first) to two halves: exact.
+__device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+  return *reinterpret_cast<__half2 *>(&r);
+}
+
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) { return __half22float2(e4m3x2_to_half2(two)); }
+
+template <int DT>
+__device__ __forceinline__ float row_value(const char *p, int64_t i) {
+  if constexpr (DT == SPEC_DTYPE_F32) return reinterpret_cast<const float *>(p)[i];
+  else if constexpr (DT == SPEC_DTYPE_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[i]);
+  else return __half2float(reinterpret_cast<const __half *>(p)[i]);
+}
+
+// Rounded once, to nearest even.
+template <int DT>
+__device__ __forceinline__ void put_value(char *p, int64_t i, float x) {
+  if constexpr (DT == SPEC_DTYPE_BF16) reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16(x);
+  else reinterpret_cast<__half *>(p)[i] = __float2half(x);
+}
+
+// Page of a request's position block `i`, or -1 when the table names a page
+// outside the pool.
+__device__ __forceinline__ int page_at(const CacheView &c, int b, int64_t i) {
+  const int p = c.table[static_cast<int64_t>(b) * c.table_stride + i];
+  return p >= 0 && p < c.num_pages ? p : -1;
+}
+
+// Byte offset of (page, head, slot 0) in the pool.
+__device__ __forceinline__ int64_t block_offset(const CacheView &c, int page, int head) {
+  return page * c.page_stride + (static_cast<int64_t>(head) << c.page_shift) * c.head_dim;
+}
+
+// Positions that a request's table can hold.
+__device__ __forceinline__ int64_t capacity(const CacheView &c) {
+  return static_cast<int64_t>(c.table_stride) << c.page_shift;
+}
+
+// Capped score in units of log 2: x = scale q.k.
+__device__ __forceinline__ float capped_log2(float x, float softcap) {
+  return (softcap > 0.0f ? softcap * tanhf(x / softcap) : x) * kLog2e;
+}
+
+#endif
+
+}  // namespace sv

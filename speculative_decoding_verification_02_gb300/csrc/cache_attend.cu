@@ -1,0 +1,110 @@
+// spec_cache_attend: attention of the drafted rows over the 8-bit cache.
+//
+//   x_j = cap tanh(scale q.k_j / cap) over the positions that the row sees
+//   out = sum_j exp(x_j - m) v_j / sum_j exp(x_j - m),  lse = m + log sum_j exp(x_j - m)
+//
+// in one pass with the running maximum m and sum.
+#include "cache.cuh"
+#include "common.cuh"
+#include "launch.h"
+
+namespace sv {
+namespace {
+
+constexpr int kRowWarps = 4;  // rows to a CTA of the general kernel
+
+// One warp to a row: 32 positions at a time, a lane scoring one of them, then
+// the lanes across the components for the values.
+template <int DT>
+__global__ void __launch_bounds__(32 * kRowWarps) cache_attend_rows_kernel(const CacheAttendParams P) {
+  __shared__ float s_q[kRowWarps][256];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t rows = static_cast<int64_t>(P.B) * P.N * P.Hq;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp;
+  if (r >= rows) return;
+  const int h = static_cast<int>(r % P.Hq), i = static_cast<int>(r / P.Hq % P.N), b = static_cast<int>(r / P.Hq / P.N);
+  const int head = h / P.group, D = P.c.head_dim;
+  const int64_t base = P.cache_len[b];
+  const int n = P.n_query ? P.n_query[b] : P.N;
+  int st = SPEC_STATUS_OK;
+  if (base < 0 || n < 0 || n > P.N || base + n > capacity(P.c)) st = SPEC_STATUS_BAD_LENGTH;
+
+  const char *q = P.q + (b * P.qs[0] + i * P.qs[1] + h * P.qs[2]) * 2;
+  for (int d = lane; d < D; d += 32) s_q[warp][d] = row_value<DT>(q, d);
+  __syncwarp();
+  float m = -INFINITY, sum = 0.0f, acc[8] = {};
+  const int64_t T = st == SPEC_STATUS_OK ? base + n : 0;
+  const bool live = i < n;
+  const uint8_t *mask = P.mask ? P.mask + (static_cast<int64_t>(b) * P.N + i) * P.N : nullptr;
+  for (int64_t t0 = 0; t0 < T; t0 += 32) {
+    const int64_t j = t0 + lane;
+    const int page = j < T ? page_at(P.c, b, j >> P.c.page_shift) : 0;
+    if (__any_sync(~0u, page < 0)) {
+      st = SPEC_STATUS_BAD_PAGE;
+      break;
+    }
+    if (!live) continue;  // (the pages of a request decide its status on every row)
+    const bool sees = j < T && (j < base || (mask ? mask[j - base] != 0 : j - base <= i));
+    const int64_t at = block_offset(P.c, page, head) + (j & ((1 << P.c.page_shift) - 1)) * D;
+    float x = -INFINITY;
+    if (sees) {
+      const uint4 *k = reinterpret_cast<const uint4 *>(P.c.k + at);
+      float dot = 0.0f;
+      for (int g = 0; g < D / 16; ++g) {
+        const uint4 w4 = k[g];
+        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 lo = e4m3x2_to_float2(w[e] & 0xffff), hi = e4m3x2_to_float2(w[e] >> 16);
+          const float *qq = &s_q[warp][g * 16 + e * 4];
+          dot = fmaf(qq[0], lo.x, fmaf(qq[1], lo.y, fmaf(qq[2], hi.x, fmaf(qq[3], hi.y, dot))));
+        }
+      }
+      x = capped_log2(P.scale * dot * P.c.k_scale[page * P.c.scale_stride + head], P.softcap);
+    }
+    float top = x;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    const float next = fmaxf(m, top);
+    const float ref = next == -INFINITY ? 0.0f : next;
+    const float keep = exp2f(m - ref);
+    const float p = sees ? exp2f(x - ref) : 0.0f;
+    m = next;
+    sum = sum * keep + warp_sum(p);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] *= keep;
+    const float vs = sees ? P.c.v_scale[page * P.c.scale_stride + head] : 0.0f;
+    for (unsigned left = __ballot_sync(~0u, sees); left; left &= left - 1) {
+      const int o = __ffs(left) - 1;
+      const float w = __shfl_sync(~0u, p * vs, o);
+      const uint8_t *v = P.c.v + __shfl_sync(~0u, at, o);
+      for (int c = 0; c < 8; ++c) {
+        const int d = lane + 32 * c;
+        if (d < D) acc[c] = fmaf(w, e4m3x2_to_float2(v[d]).x, acc[c]);
+      }
+    }
+  }
+  const bool empty = st != SPEC_STATUS_OK || !live || sum == 0.0f;
+  const float inv = 1.0f / sum;
+  char *out = P.out + (b * P.os[0] + i * P.os[1] + h * P.os[2]) * 2;
+  for (int c = 0; c < 8; ++c) {
+    const int d = lane + 32 * c;
+    if (d < D) put_value<DT>(out, d, empty ? 0.0f : acc[c] * inv);
+  }
+  if (lane == 0) {
+    if (P.lse) P.lse[r] = empty ? -INFINITY : (m + log2f(sum)) * kLn2;
+    if (P.status && i == 0 && h == 0) P.status[b] = st;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_attend(const CacheAttendParams &P, cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(P.B) * P.N * P.Hq;
+  const unsigned grid = static_cast<unsigned>((rows + kRowWarps - 1) / kRowWarps);
+  return trace_launch("cache_attend_rows", st, [&] {
+    if (P.dtype == SPEC_DTYPE_BF16) cache_attend_rows_kernel<SPEC_DTYPE_BF16><<<grid, 32 * kRowWarps, 0, st>>>(P);
+    else cache_attend_rows_kernel<SPEC_DTYPE_F16><<<grid, 32 * kRowWarps, 0, st>>>(P);
+  });
+}
+
+}  // namespace sv
