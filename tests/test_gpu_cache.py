@@ -1,0 +1,582 @@
+"""The 8-bit cache's operators on the GPU against their 64-bit definitions."""
+import math
+
+import pytest
+import torch
+
+import cache_oracle as ref
+
+pytestmark = pytest.mark.gpu
+
+BF, HF = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def api():
+    from speculative_decoding_verification_02_gb300 import api, build
+    build.build()
+    torch.cuda.set_device(0)
+    return api
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def rand_cache(api, pages, H, P, D, seed, spread=3, page_gap=0):
+    """A pool of random codes (NaN among none) whose blocks differ in scale; page_gap: bytes between pages."""
+    g = gen(seed)
+    parts = []
+    for _ in range(2):
+        room = torch.zeros(pages, H * P * D + page_gap, dtype=torch.uint8)
+        x = (torch.randn(pages, H * P * D, generator=g) * 40).clamp(-448, 448).to(ref.F8)
+        room[:, :H * P * D] = x.view(torch.uint8)
+        room = room.cuda()
+        parts.append(torch.as_strided(room, (pages, H, P, D), (H * P * D + page_gap, P * D, D, 1)).view(ref.F8))
+    scales = [torch.exp2(torch.randint(-6 - spread, -5, (pages, H), generator=g).float()).cuda() for _ in range(2)]
+    return [parts[0], parts[1], scales[0], scales[1]]
+
+
+def rand_table(B, W, pages, seed):
+    return torch.randperm(pages, generator=gen(seed))[:B * W].reshape(B, W).to(torch.int32).cuda()
+
+
+def tree_mask(B, n, seed):
+    g = gen(seed)
+    m = torch.zeros(B, n, n, dtype=torch.uint8)
+    for b in range(B):
+        for i in range(n):
+            if i:
+                m[b, i] = m[b, int(torch.randint(0, i, (1,), generator=g))]
+            m[b, i, i] = 1
+    return m.cuda()
+
+
+def check_attend(api, q, cache, table, lens, n_query=None, mask=None, scale=None, cap=0.0, **kw):
+    B, N = q.shape[:2]
+    dev_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    nq = None if n_query is None else torch.tensor(n_query, dtype=torch.int32, device="cuda")
+    o = api.spec_cache_attend(q, cache, table, dev_lens, n_query=nq, mask=mask, scale=scale, softcap=cap, **kw)
+    torch.cuda.synchronize()
+    s = q.shape[3] ** -0.5 if scale is None else scale
+    out, lse, t_out, t_lse = ref.attend(ref.Cache64(cache, table), q, lens, n_query or [N] * B, mask, s, cap)
+    assert o["status"].tolist() == [0] * B
+    got, got_lse = o["out"].cpu().double(), o["lse"].cpu().double()
+    empty = lse == -math.inf
+    assert torch.equal(got_lse == -math.inf, empty)
+    assert bool((got[empty] == 0).all())
+    worst = ((got - out).abs() / t_out.clamp(min=1e-300))[~empty]
+    assert bool((worst <= 1).all()), float(worst.max())
+    worst = ((got_lse - lse).abs() / t_lse)[~empty]
+    assert bool((worst <= 1).all()), float(worst.max())
+    return o
+
+
+# ------------------------------------------------------------------ append
+
+@pytest.mark.parametrize("D,P,H,dtype", [(128, 64, 2, BF), (64, 16, 3, HF), (128, 128, 1, torch.float32), (80, 32, 2, BF), (256, 256, 1, HF),
+                                         (16, 16, 5, BF)])
+@pytest.mark.parametrize("lens,counts", [([0, 5, 63], [1, 9, 9]), ([16, 127, 31], [0, 40, 33]), ([255, 0, 1], [41, 0, 2])])
+def test_append(api, D, P, H, dtype, lens, counts):
+    B, n = 3, 41
+    W = -(-(max(lens) + n) // P)
+    cache = rand_cache(api, B * W + 2, H, P, D, 1)
+    table = rand_table(B, W, B * W + 2, 2)
+    g = gen(3)
+    k = (torch.randn(B, n, H, D, generator=g) * torch.exp(2 * torch.randn(B, n, 1, 1, generator=g))).to(dtype).cuda()
+    v = (torch.randn(B, n, H, D, generator=g) * 3).to(dtype).cuda()
+    want = ref.Cache64(cache, table)
+    for b in range(B):
+        want.append(b, lens[b], k[b, :counts[b]].cpu(), v[b, :counts[b]].cpu())
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o = api.spec_cache_append(cache, table, ln, k, v, counts=torch.tensor(counts, dtype=torch.int32, device="cuda"))
+    assert o["status"].tolist() == [0] * B and o["new_len"].tolist() == [a + c for a, c in zip(lens, counts)]
+    got = ref.Cache64(cache, table)
+    for w in (0, 1):
+        assert torch.equal(got.val[w], want.val[w])  # the untouched pages and slots among them
+        assert torch.equal(got.scale[w], want.scale[w])
+
+
+def test_append_path_strides_and_dtype_of_layout(api):
+    """Rows picked by index, keys and values as slices of one [B, H, n, 3, D] projection, pages apart from one another."""
+    B, n, H, D, P = 2, 12, 2, 128, 16
+    cache = rand_cache(api, 9, H, P, D, 4, page_gap=48)
+    table = rand_table(B, 3, 9, 5)
+    x = torch.randn(B, H, n, 3, D, generator=gen(6)).to(BF).cuda()
+    k, v = x[:, :, :, 1].transpose(1, 2), x[:, :, :, 2].transpose(1, 2)
+    index = torch.tensor([[0, 3, 4, 11, -1], [0, 1, 7, 9, 10]], dtype=torch.int32, device="cuda")
+    counts = torch.tensor([4, 5], dtype=torch.int32, device="cuda")
+    lens = [14, 0]
+    want = ref.Cache64(cache, table)
+    for b in range(B):
+        at = index[b, :int(counts[b])].long()
+        want.append(b, lens[b], k[b][at].cpu(), v[b][at].cpu())
+    o = api.spec_cache_append(cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), k, v, counts=counts, index=index)
+    assert o["new_len"].tolist() == [18, 5] and o["status"].tolist() == [0, 0]
+    got = ref.Cache64(cache, table)
+    for w in (0, 1):
+        assert torch.equal(got.val[w], want.val[w]) and torch.equal(got.scale[w], want.scale[w])
+
+
+@pytest.mark.parametrize("offset", [1, 3])
+def test_append_unaligned_rows(api, offset):
+    B, n, H, D, P = 1, 5, 2, 64, 16
+    cache = rand_cache(api, 2, H, P, D, 7)
+    table = rand_table(B, 2, 2, 8)
+    flat = torch.randn(2 * B * n * H * D + 8, generator=gen(9)).to(BF).cuda()
+    k = flat[offset:offset + B * n * H * D].view(B, n, H, D)
+    v = flat[offset + B * n * H * D:][:B * n * H * D].view(B, n, H, D)
+    want = ref.Cache64(cache, table)
+    want.append(0, 13, k[0].cpu(), v[0].cpu())
+    api.spec_cache_append(cache, table, torch.tensor([13], dtype=torch.int32, device="cuda"), k, v)
+    got = ref.Cache64(cache, table)
+    for w in (0, 1):
+        assert torch.equal(got.val[w], want.val[w]) and torch.equal(got.scale[w], want.scale[w])
+
+
+def test_append_extremes(api):
+    """Zeros, tiny and huge values, infinities and NaN, and a scale that grows over a block of small values."""
+    H, D, P = 1, 32, 16
+    rows = torch.zeros(1, 8, H, D)
+    rows[0, 1] = 1e-30
+    rows[0, 2] = 3e38
+    rows[0, 3, 0, :4] = torch.tensor([math.inf, -math.inf, math.nan, 1.0])
+    rows[0, 4] = torch.linspace(-500, 500, D)
+    rows[0, 5] = 2.0 ** -70
+    rows[0, 6] = 448.0 * 2.0 ** 60
+    rows[0, 7] = 449.0
+    x = rows.cuda()
+    for order in ([0, 4, 7], [1, 5, 0], [4, 2], [3, 4], [0, 3], [6, 4], [1, 4, 2]):
+        cache = rand_cache(api, 1, H, P, D, 10)
+        table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+        want = ref.Cache64(cache, table)
+        n = 0
+        for t in order:  # one row a call
+            want.append(0, n, rows[0, t:t + 1], rows[0, t:t + 1])
+            api.spec_cache_append(cache, table, torch.tensor([n], dtype=torch.int32, device="cuda"), x[:, t:t + 1], x[:, t:t + 1])
+            n += 1
+        got = ref.Cache64(cache, table)
+        for w in (0, 1):
+            assert torch.equal(got.scale[w], want.scale[w]), order
+            assert torch.equal(got.val[w][0, 0, :n].nan_to_num(nan=1e9), want.val[w][0, 0, :n].nan_to_num(nan=1e9)), order
+
+
+# ------------------------------------------------------------------ attend
+
+SHAPES = [  # B, N, H, G, D, P, lens
+    (1, 1, 1, 1, 128, 64, [0]),
+    (1, 1, 2, 4, 128, 64, [1]),
+    (2, 1, 2, 8, 64, 16, [15, 16]),
+    (3, 5, 2, 4, 128, 64, [127, 128, 129]),
+    (2, 9, 1, 4, 128, 32, [500, 3]),
+    (1, 17, 2, 3, 64, 128, [300]),
+    (2, 33, 1, 2, 128, 16, [77, 1000]),
+    (1, 60, 2, 4, 128, 64, [411]),
+    (2, 64, 1, 8, 64, 256, [255, 600]),
+    (1, 150, 1, 2, 128, 64, [64]),
+    (2, 7, 3, 1, 80, 32, [65, 40]),
+    (1, 3, 1, 2, 256, 16, [200]),
+]
+
+
+@pytest.mark.parametrize("B,N,H,G,D,P,lens", SHAPES)
+@pytest.mark.parametrize("dtype,cap", [(BF, 0.0), (HF, 0.0), (BF, 30.0)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_attend(api, B, N, H, G, D, P, lens, dtype, cap, tree):
+    W = -(-(max(lens) + N) // P)
+    cache = rand_cache(api, B * W + 1, H, P, D, 11)
+    table = rand_table(B, W, B * W + 1, 12)
+    q = (torch.randn(B, N, H * G, D, generator=gen(13)) * 2).to(dtype).cuda()
+    check_attend(api, q, cache, table, lens, mask=tree_mask(B, N, 14) if tree else None, cap=cap)
+
+
+def test_attend_long_and_ragged(api):
+    lens = [20000, 0, 777, 4095, 1, 9000]
+    B, N, H, G, D, P = 6, 5, 2, 4, 128, 128
+    W = -(-(max(lens) + N) // P)
+    cache = rand_cache(api, B * W, H, P, D, 15)
+    table = rand_table(B, W, B * W, 16)
+    q = torch.randn(B, N, H * G, D, generator=gen(17)).to(BF).cuda()
+    check_attend(api, q, cache, table, lens, n_query=[5, 5, 0, 3, 1, 4])
+
+
+def test_attend_sharp_and_flat_scores(api):
+    """A far token that holds almost all of the weight, and a context of equal scores."""
+    B, N, H, G, D, P = 2, 2, 1, 4, 128, 64
+    lens = [3000, 5000]
+    W = -(-(max(lens) + N) // P)
+    cache = rand_cache(api, B * W, H, P, D, 18)
+    table = rand_table(B, W, B * W, 19)
+    q = (torch.randn(B, N, H * G, D, generator=gen(20)) * 30).to(BF).cuda()
+    q[1] = 0
+    check_attend(api, q, cache, table, lens)
+    check_attend(api, q, cache, table, lens, scale=0.0)
+    check_attend(api, q, cache, table, lens, scale=-0.05)
+
+
+def test_attend_scales_far_apart(api):
+    """Blocks whose values differ by 2^40, and the largest scale's block first, last and between."""
+    B, N, H, G, D, P = 3, 3, 1, 2, 128, 16
+    lens = [200, 150, 129]
+    W = -(-(max(lens) + N) // P)
+    cache = rand_cache(api, B * W, H, P, D, 21)
+    table = torch.arange(B * W, dtype=torch.int32, device="cuda").reshape(B, W)
+    cache[3][:] = torch.exp2(torch.randint(-40, 1, (B * W, H), generator=gen(22)).float()).cuda()
+    cache[3][0] = 1.0
+    cache[3][W + 9] = 2.0 ** 30
+    cache[3][2 * W + 3] = 2.0 ** -60
+    q = torch.randn(B, N, H * G, D, generator=gen(23)).to(BF).cuda()
+    check_attend(api, q, cache, table, lens)
+
+
+def test_attend_masked_places_hold_anything(api):
+    """NaN in slots behind the context, in pages' unused ends and in rows that a row does not see changes nothing."""
+    B, N, H, G, D, P = 2, 6, 2, 2, 128, 64
+    lens = [70, 0]
+    cache = rand_cache(api, 8, H, P, D, 24)
+    table = rand_table(B, 2, 8, 25)
+    mask = tree_mask(B, N, 26)
+    mask[1, 2] = 0  # a row that sees nothing
+    mask[:, :, 4] = 0
+    mask[:, 4, 4] = 1  # only itself sees row 4
+    q = torch.randn(B, N, H * G, D, generator=gen(27)).to(BF).cuda()
+    clean = check_attend(api, q, cache, table, lens, mask=mask)
+    nan = torch.full((1,), math.nan).to(ref.F8).view(torch.uint8).item()
+    for pool in cache[:2]:
+        raw = pool.view(torch.uint8)
+        for b in range(B):
+            T = lens[b] + N
+            for t in range(T, 2 * P):
+                raw[int(table[b, t // P]), :, t % P] = nan
+            t = lens[b] + 4
+            raw[int(table[b, t // P]), :, t % P] = nan
+    o = api.spec_cache_attend(q, cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), mask=mask)
+    for i in range(N):
+        if i == 4:
+            assert bool(o["out"][:, 4].isnan().all())
+        else:
+            assert torch.equal(o["out"][:, i], clean["out"][:, i]) and torch.equal(o["lse"][:, i], clean["lse"][:, i])
+    assert bool((o["out"][1, 2] == 0).all()) and bool((o["lse"][1, 2] == -math.inf).all())
+
+
+def test_attend_nan_in_the_context_shows(api):
+    cache = rand_cache(api, 4, 1, 64, 128, 28)
+    table = rand_table(1, 4, 4, 29)
+    q = torch.randn(1, 2, 4, 128, generator=gen(30)).to(BF).cuda()
+    ln = torch.tensor([190], dtype=torch.int32, device="cuda")
+    cache[1].view(torch.uint8)[int(table[0, 1]), 0, 7, 5] = 0x7f
+    o = api.spec_cache_attend(q, cache, table, ln)
+    assert bool(o["out"][..., 5].isnan().all())
+    cache[0].view(torch.uint8)[int(table[0, 1]), 0, 7, 5] = 0x7f
+    o = api.spec_cache_attend(q, cache, table, ln)
+    assert bool(o["out"].isnan().all())
+
+
+def test_attend_strides(api):
+    """q as a transposed slice of a fused projection, out likewise, pages apart, offsets that are not of 16 bytes."""
+    B, N, H, G, D, P = 2, 7, 2, 4, 128, 32
+    lens = [100, 33]
+    cache = rand_cache(api, 9, H, P, D, 31, page_gap=64)
+    table = rand_table(B, 4, 9, 32)
+    x = torch.randn(B, H * G, N, D + 3, generator=gen(33)).to(BF).cuda()
+    q = x[..., 1:D + 1].transpose(1, 2)
+    y = torch.full((B, H * G, N, D + 5), 7.0, dtype=BF, device="cuda")
+    out = dict(out=y[..., 3:D + 3].transpose(1, 2), lse=torch.empty(B, N, H * G, device="cuda"),
+               status=torch.empty(B, dtype=torch.int32, device="cuda"))
+    check_attend(api, q, cache, table, lens, out=out)
+    assert bool((y[..., :3] == 7).all()) and bool((y[..., D + 3:] == 7).all())
+
+
+def test_attend_pool_past_two_gigabytes(api):
+    H, P, D = 1, 256, 128
+    pages = (1 << 31) // (H * P * D) + 3
+    pool = [torch.zeros(pages, H, P, D, dtype=torch.uint8, device="cuda").view(ref.F8) for _ in range(2)]
+    cache = pool + [torch.full((pages, H), 2.0 ** -6, device="cuda") for _ in range(2)]
+    table = torch.tensor([[pages - 1, 0, pages - 2]], dtype=torch.int32, device="cuda")
+    few = rand_cache(api, 3, H, P, D, 34)
+    for to, frm in zip(cache, few):
+        to.view(torch.uint8)[table[0].long()] = frm.view(torch.uint8) if to.dtype == ref.F8 else frm.view(torch.uint8)
+    q = torch.randn(1, 4, 2, D, generator=gen(35)).to(BF).cuda()
+    small = torch.arange(3, dtype=torch.int32, device="cuda")[None]
+    a = api.spec_cache_attend(q, cache, table, torch.tensor([700], dtype=torch.int32, device="cuda"))
+    b = api.spec_cache_attend(q, few, small, torch.tensor([700], dtype=torch.int32, device="cuda"))
+    assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
+    k = torch.randn(1, 9, H, D, generator=gen(36)).to(BF).cuda()
+    ln = torch.tensor([250], dtype=torch.int32, device="cuda")
+    api.spec_cache_append(cache, table, ln, k, k)
+    api.spec_cache_append(few, small, ln, k, k)
+    for x, y in zip(cache, few):
+        assert torch.equal(x.view(torch.uint8)[table[0].long()], y.view(torch.uint8))
+
+
+def test_attend_is_the_same_on_every_run_and_stream(api):
+    B, N, H, G, D, P = 4, 9, 2, 4, 128, 64
+    W = 40
+    cache = rand_cache(api, B * W, H, P, D, 37)
+    table = rand_table(B, W, B * W, 38)
+    ln = torch.tensor([2500, 17, 900, 1300], dtype=torch.int32, device="cuda")
+    q = torch.randn(B, N, H * G, D, generator=gen(39)).to(BF).cuda()
+    first = api.spec_cache_attend(q, cache, table, ln)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            again = api.spec_cache_attend(q, cache, table, ln)
+        side.synchronize()
+        assert torch.equal(first["out"], again["out"]) and torch.equal(first["lse"], again["lse"])
+
+
+def test_all_in_a_graph(api):
+    """The four operators captured and replayed on new data of the same shapes."""
+    B, N, H, G, D, P, W = 2, 5, 2, 2, 64, 16, 8
+    cache = rand_cache(api, B * W + B * 2, H, P, D, 40)
+    every = torch.randperm(B * W + B * 2, generator=gen(41)).to(torch.int32).cuda()
+    table, dst = every[:B * W].reshape(B, W), every[B * W:].reshape(B, 2)
+    ln = torch.tensor([40, 61], dtype=torch.int32, device="cuda")
+    k, v, q = (torch.randn(B, N, h, D, generator=gen(42 + h)).to(BF).cuda() for h in (H, H, H * G))
+    prev = torch.zeros(B, H, W * P, device="cuda")
+
+    def step():
+        a = api.spec_cache_append(cache, table, ln, k, v)
+        o = api.spec_cache_attend(q, cache, table, ln)
+        w = api.spec_cache_weights(q, o["lse"], cache, table, ln, prev=prev)
+        e = api.spec_cache_evict(cache, table, a["new_len"], w["weights"], 20, 5, dst)
+        return a, o, w, e
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    k.copy_(torch.randn(B, N, H, D, generator=gen(50)))
+    q.copy_(torch.randn(B, N, H * G, D, generator=gen(51)))
+    ln += 3
+    graph.replay()
+    torch.cuda.synchronize()
+    kept = [{n: t.clone() for n, t in x.items()} for x in captured]
+    eager = step()
+    for x, y in zip(kept, eager):
+        for name in x:
+            assert torch.equal(x[name], y[name]), name
+
+
+# ------------------------------------------------------------------ weights
+
+@pytest.mark.parametrize("B,N,H,G,D,P,lens", [(1, 1, 1, 1, 128, 64, [0]), (2, 1, 2, 4, 128, 64, [63, 700]), (3, 5, 1, 8, 64, 16, [0, 15, 1000]),
+                                              (1, 40, 2, 4, 128, 128, [333]), (2, 3, 2, 2, 80, 32, [31, 64]), (1, 70, 1, 8, 128, 64, [129])])
+@pytest.mark.parametrize("dtype,cap,path", [(BF, 0.0, False), (HF, 0.0, True), (BF, 20.0, True)])
+def test_weights(api, B, N, H, G, D, P, lens, dtype, cap, path):
+    W = -(-(max(lens) + N) // P)
+    cache = rand_cache(api, B * W, H, P, D, 60)
+    table = rand_table(B, W, B * W, 61)
+    g = gen(62)
+    q = torch.randn(B, N, H * G, D, generator=g).to(dtype).cuda()
+    lse = (torch.rand(B, N, H * G, generator=g) * 3 + 3).cuda()
+    lse[0, 0, 0] = -math.inf
+    prev = torch.rand(B, H, W * P, generator=g).cuda()
+    index = counts = None
+    cnt = [N] * B
+    if path:
+        index = torch.stack([torch.randperm(N, generator=g).sort().values for _ in range(B)]).to(torch.int32).cuda()
+        cnt = [int(torch.randint(0, N + 1, (1,), generator=g)) for _ in range(B)]
+        counts = torch.tensor(cnt, dtype=torch.int32, device="cuda")
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o = api.spec_cache_weights(q, lse, cache, table, ln, prev=prev, counts=counts, index=index, softcap=cap)
+    want, tol = ref.weights(ref.Cache64(cache, table), q, lse, lens, cnt, index, D ** -0.5, cap, prev)
+    got = o["weights"].cpu().double()
+    assert o["status"].tolist() == [0] * B
+    worst = (got - want).abs() / tol
+    assert bool((worst <= 1).all()), float(worst.max())
+    for b in range(B):
+        assert torch.equal(o["weights"][b, :, lens[b] + cnt[b]:], prev[b, :, lens[b] + cnt[b]:])  # not written
+    again = api.spec_cache_weights(q, lse, cache, table, ln, prev=prev, counts=counts, index=index, softcap=cap, out=dict(weights=prev))
+    assert torch.equal(again["weights"], o["weights"])  # in place
+    fresh = api.spec_cache_weights(q, lse, cache, table, ln, counts=counts, index=index, softcap=cap)
+    assert fresh["weights"].shape == prev.shape
+
+
+def test_weights_of_an_attention_sum_to_its_rows(api):
+    """Every row's weights sum to 1: the operators agree on what a score is."""
+    B, N, H, G, D, P, W = 2, 4, 2, 3, 128, 64, 5
+    cache = rand_cache(api, B * W, H, P, D, 63)
+    table = rand_table(B, W, B * W, 64)
+    ln = torch.tensor([200, 31], dtype=torch.int32, device="cuda")
+    q = torch.randn(B, N, H * G, D, generator=gen(65)).to(BF).cuda()
+    o = api.spec_cache_attend(q, cache, table, ln, softcap=15.0)
+    w = api.spec_cache_weights(q, o["lse"], cache, table, ln, softcap=15.0)
+    # the two kernels' scores differ by at most what the attention's q is rounded by (2^-18 of a row's largest, 4096 by 128 terms)
+    assert bool(((w["weights"].double().sum(2) - N * G).abs() < N * G * 2.0 ** -9).all())
+
+
+# ------------------------------------------------------------------ evict
+
+def check_evict(api, B, H, D, P, lens, keep, recent, weights, seed=70, **kw):
+    W = max(1, -(-max(lens) // P))
+    Wd = -(-keep // P)
+    cache = rand_cache(api, B * (W + Wd), H, P, D, seed)
+    every = torch.randperm(B * (W + Wd), generator=gen(seed + 1)).to(torch.int32).cuda()
+    table, dst = every[:B * W].reshape(B, W).contiguous(), every[B * W:].reshape(B, Wd).contiguous()
+    before, after = ref.Cache64(cache, table), ref.Cache64(cache, dst)
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o = api.spec_cache_evict(cache, table, ln, weights, keep, recent, dst, **kw)
+    got = ref.Cache64(cache, dst)
+    assert o["status"].tolist() == [0] * B
+    host = weights.cpu()
+    for b in range(B):
+        n = min(keep, lens[b])
+        assert int(o["new_len"][b]) == n
+        kept = ref.evict(before, host, b, lens[b], keep, recent)
+        for h in range(H):
+            assert o["kept"][b, h].tolist() == kept[h] + [-1] * (keep - n)
+            assert torch.equal(o["weights"][b, h, :n].cpu(), host[b, h][kept[h]]) or bool(host[b, h][kept[h]].isnan().any())
+            assert bool((o["weights"][b, h, n:] == 0).all())
+        for which in (0, 1):
+            rows = before.rows(which, b, lens[b])
+            for w in range(-(-n // P)):
+                page, m = int(dst[b, w]), min(P, n - w * P)
+                for h in range(H):
+                    part = rows[h][kept[h][w * P:w * P + m]]
+                    s = ref.block_scale(part)
+                    after.scale[which][page, h] = s
+                    after.val[which][page, h, :m] = ref.e4m3(part / s)
+    for which in (0, 1):
+        assert torch.equal(got.val[which], after.val[which]) and torch.equal(got.scale[which], after.scale[which])
+    return o
+
+
+@pytest.mark.parametrize("D,P,H", [(128, 64, 2), (64, 16, 3), (80, 32, 1), (256, 256, 1)])
+@pytest.mark.parametrize("lens,keep,recent", [([100, 1, 0], 33, 5), ([257, 64, 65], 64, 64), ([31, 400, 300], 1, 0), ([500, 499, 7], 600, 3),
+                                              ([90, 91, 92], 90, 0)])
+def test_evict(api, D, P, H, lens, keep, recent):
+    w = torch.rand(3, H, max(lens), generator=gen(71)).cuda()
+    check_evict(api, 3, H, D, P, lens, keep, recent, w)
+
+
+@pytest.mark.parametrize("kind", ["equal", "few", "signs", "nan", "tiny"])
+def test_evict_ties_and_odd_weights(api, kind):
+    B, H, T = 2, 2, 1500
+    g = gen(72)
+    w = {"equal": torch.ones(B, H, T), "few": torch.randint(0, 3, (B, H, T), generator=g).float(),
+         "signs": torch.randn(B, H, T, generator=g).round(), "nan": torch.rand(B, H, T, generator=g),
+         "tiny": torch.rand(B, H, T, generator=g) * 1e-42}[kind]
+    if kind == "nan":
+        w[:, :, ::3] = math.nan
+        w[:, :, 1] = math.inf
+        w[:, :, 2] = -math.inf
+    if kind == "signs":
+        w[:, :, ::2] = -0.0
+    check_evict(api, B, H, 64, 32, [T, T - 100], 1200, 7, w.cuda())
+
+
+def test_evict_long(api):
+    T = 70001
+    w = torch.exp(torch.randn(1, 2, T + 13, generator=gen(73))).cuda()
+    check_evict(api, 1, 2, 64, 256, [T], 4097, 100, w)
+
+
+def test_evict_to_another_pool_and_strided_weights(api):
+    B, H, D, P, T, keep = 2, 2, 64, 16, 50, 20
+    cache = rand_cache(api, 8, H, P, D, 74)
+    pool = api.spec_cache_new(4, H, P, D)
+    table, dst = rand_table(B, 4, 8, 75), rand_table(B, 2, 4, 76)
+    room = torch.rand(B, T + 3, H, generator=gen(77)).cuda().transpose(1, 2).contiguous()
+    big = torch.zeros(B, 2 * H, T + 9, device="cuda")
+    big[:, ::2, :T + 3] = room
+    w = big[:, ::2, :T + 3]
+    ln = torch.tensor([T, 9], dtype=torch.int32, device="cuda")
+    o = api.spec_cache_evict(cache, table, ln, w, keep, 4, dst, dst_cache=pool)
+    before, got = ref.Cache64(cache, table), ref.Cache64(pool, dst)
+    for b, n in ((0, T), (1, 9)):
+        for h, kept in enumerate(ref.evict(before, w.cpu(), b, n, keep, 4)):
+            assert o["kept"][b, h, :len(kept)].tolist() == kept
+            for which in (0, 1):
+                part = before.rows(which, b, n)[h][kept]
+                want = [ref.e4m3(x / ref.block_scale(x)) * ref.block_scale(x) for x in part.split(P)]
+                assert torch.equal(got.rows(which, b, len(kept))[h], torch.cat(want))
+
+
+# ------------------------------------------------------------------ requests that are wrong
+
+def wrong_requests(api):
+    """Three requests, the second in turn wrong in each way: (lens, counts or rows, table change, index change, status)."""
+    return [("length", api.STATUS_BAD_LENGTH), ("negative", api.STATUS_BAD_LENGTH), ("count", api.STATUS_BAD_LENGTH),
+            ("page", api.STATUS_BAD_PAGE), ("page below", api.STATUS_BAD_PAGE), ("index", api.STATUS_BAD_INDEX)]
+
+
+@pytest.mark.parametrize("kind", ["length", "negative", "count", "page", "page below", "index"])
+def test_wrong_requests_leave_the_others_alone(api, kind):
+    status = dict(wrong_requests(api))[kind]
+    B, N, H, G, D, P, W = 3, 6, 2, 2, 128, 16, 6
+    clean = rand_cache(api, B * W + B, H, P, D, 80)
+    every = torch.randperm(B * W + B, generator=gen(81)).to(torch.int32).cuda()
+    table, dst = every[:B * W].reshape(B, W).contiguous(), every[B * W:].reshape(B, 1).contiguous()
+    lens = torch.tensor([50, 60, 70], dtype=torch.int32, device="cuda")
+    counts = torch.tensor([6, 5, 4], dtype=torch.int32, device="cuda")
+    index = torch.arange(N, dtype=torch.int32, device="cuda").repeat(B, 1).contiguous()
+    k = torch.randn(B, N, H, D, generator=gen(82)).to(BF).cuda()
+    q = torch.randn(B, N, H * G, D, generator=gen(83)).to(BF).cuda()
+    w = torch.rand(B, H, W * P, generator=gen(84)).cuda()
+    lse = torch.full((B, N, H * G), 4.0, device="cuda")
+
+    def all_four(lens, counts, table, index):
+        cache = [x.clone() for x in clean]
+        a = api.spec_cache_append(cache, table, lens, k, k, counts=counts, index=index)
+        o = api.spec_cache_attend(q, cache, table, lens, n_query=counts)
+        s = api.spec_cache_weights(q, lse, cache, table, lens, prev=w, counts=counts, index=index)
+        e = api.spec_cache_evict(cache, table, lens, w, 12, 3, dst)
+        return cache, a, o, s, e
+
+    good = all_four(lens, counts, table, index)
+    if kind == "length":
+        lens = lens.clone()
+        lens[1] = W * P + 1
+    elif kind == "negative":
+        lens = lens.clone()
+        lens[1] = -1
+    elif kind == "count":
+        counts = counts.clone()
+        counts[1] = N + 1
+    elif kind == "index":
+        index = index.clone()
+        index[1, 2] = N
+    else:
+        table = table.clone()
+        table[1, 3] = -1 if kind == "page below" else B * W + B
+    bad = all_four(lens, counts, table, index)
+    _, a, o, s, e = bad
+    assert a["status"].tolist() == [0, status, 0] and int(a["new_len"][1]) == int(lens[1])
+    assert s["status"].tolist() == [0, status, 0] and torch.equal(s["weights"][1], w[1])
+    if kind != "index":
+        assert o["status"].tolist() == [0, status, 0]
+        assert bool((o["out"][1] == 0).all()) and bool((o["lse"][1] == -math.inf).all())
+    if kind not in ("index", "count"):
+        assert e["status"].tolist() == [0, status, 0] and int(e["new_len"][1]) == 0 and bool((e["kept"][1] == -1).all())
+    for i in (0, 2):
+        for x, y in zip(good[1:], bad[1:]):
+            for name in x:
+                assert torch.equal(x[name][i], y[name][i]), (kind, name)
+
+
+def test_bindings_refuse(api):
+    cache = rand_cache(api, 4, 2, 16, 64, 90)
+    table = rand_table(2, 2, 4, 91)
+    ln = torch.zeros(2, dtype=torch.int32, device="cuda")
+    q = torch.zeros(2, 3, 4, 64, dtype=BF, device="cuda")
+    with pytest.raises(TypeError):
+        api.spec_cache_attend(q.float(), cache, table, ln)
+    with pytest.raises(ValueError):
+        api.spec_cache_attend(q[..., :32], cache, table, ln)
+    with pytest.raises(TypeError):
+        api.spec_cache_attend(q, cache, table.long(), ln)
+    with pytest.raises(TypeError):
+        api.spec_cache_attend(q, cache, table, ln, mask=torch.ones(2, 3, 2, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        api.spec_cache_attend(q, [cache[0].transpose(1, 2), *cache[1:]], table, ln)
+    with pytest.raises(api.SpecError):
+        api.spec_cache_attend(q[:, :, :3], cache, table, ln)  # 3 query heads over 2
+    with pytest.raises(ValueError):
+        api.spec_cache_append(cache, table, ln, q, q[:, :, :2])
+    with pytest.raises(api.SpecError):
+        api.spec_cache_evict(cache, table, ln, torch.zeros(2, 2, 32, device="cuda"), 0, 0, table)
+    with pytest.raises(TypeError):
+        api.spec_cache_evict(cache, table, ln, torch.zeros(2, 3, 32, device="cuda"), 4, 0, table)
