@@ -64,6 +64,7 @@ extern "C" {
 #define SPEC_STATUS_BAD_LENGTH 3  /* draft_len, hist_len or another length outside its range */
 #define SPEC_STATUS_BAD_PAGE 5    /* a page of the cache outside its pool */
 #define SPEC_STATUS_BAD_INDEX 6   /* a row index outside the rows */
+#define SPEC_STATUS_TIMEOUT 7     /* a wait inside a kernel ran out; the call's outputs are void */
 
 #define SPEC_DTYPE_F32 0
 #define SPEC_DTYPE_BF16 1

@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libspecverify.so")
 
 SPEC_OK, SPEC_EINVAL, SPEC_EDTYPE, SPEC_EWORKSPACE, SPEC_ECUDA = 0, -1, -2, -3, -4
 STATUS_OK, STATUS_TOKEN_RANGE, STATUS_BAD_TREE, STATUS_BAD_LENGTH = 0, 1, 2, 3
-STATUS_BAD_PAGE, STATUS_BAD_INDEX = 5, 6
+STATUS_BAD_PAGE, STATUS_BAD_INDEX, STATUS_TIMEOUT = 5, 6, 7
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 OP_NGRAM, OP_GREEDY, OP_SAMPLE, OP_TREE, OP_DRAW, OP_FILTER = 0, 1, 2, 3, 4, 5
 OP_CACHE_ATTEND, OP_CACHE_WEIGHTS, OP_CACHE_EVICT = 6, 7, 8

@@ -237,6 +237,7 @@ const char *spec_status_string(int code) {
     case 100 + SPEC_STATUS_BAD_LENGTH: return "request has a length outside its range";
     case 100 + SPEC_STATUS_BAD_PAGE: return "request has a cache page outside the pool";
     case 100 + SPEC_STATUS_BAD_INDEX: return "request has a row index outside the rows";
+    case 100 + SPEC_STATUS_TIMEOUT: return "a wait inside a kernel ran out";
     default: return "unknown code";
   }
 }

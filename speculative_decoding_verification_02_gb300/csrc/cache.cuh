@@ -2,7 +2,9 @@
 // table, e4m3 conversions and block scales, and the parameter blocks.
 #pragma once
 
+#include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -71,7 +73,13 @@ struct CacheEvictParams {
 };
 
 cudaError_t launch_cache_append(const CacheAppendParams &P, cudaStream_t st);
-cudaError_t launch_cache_attend(const CacheAttendParams &P, cudaStream_t st);
+// Heads of 64 and 128 take the tensor-core path and need a workspace.
+bool cache_attend_on_tensor_cores(const CacheAttendParams &P);
+size_t cache_attend_workspace(const CacheAttendParams &P);
+cudaError_t launch_cache_attend(const CacheAttendParams &P, void *workspace, cudaStream_t st);
+// Tensor map of the keys for copies of page_rows rows of one page and head,
+// in the shared-memory swizzle of a row's length (cache_api.cu).
+cudaError_t cache_k_map(const CacheView &c, int page_rows, CUtensorMap *map);
 cudaError_t launch_cache_weights(const CacheWeightsParams &P, cudaStream_t st);
 cudaError_t launch_cache_evict(const CacheEvictParams &P, cudaStream_t st);
 

@@ -50,9 +50,39 @@ bool strides_ok(const int64_t *s, int n) {
   return true;
 }
 
+// SPEC_OK when a call that needs `need` bytes was given them.
+int check_workspace(size_t need, const void *ws, size_t bytes) {
+  return need == 0 || (ws && bytes >= need && on_grain(ws, 256)) ? SPEC_OK : SPEC_EWORKSPACE;
+}
+
 cudaStream_t stream_of(void *s) { return reinterpret_cast<cudaStream_t>(s); }
 
 }  // namespace
+
+cudaError_t cache_k_map(const CacheView &c, int page_rows, CUtensorMap *map) {
+  using Encode = decltype(&cuTensorMapEncodeTiled);
+  static Encode encode = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<Encode>(f);
+  }();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.kv_heads) << c.page_shift,
+                              static_cast<cuuint64_t>(c.num_pages)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.page_stride)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(c.head_dim), static_cast<cuuint32_t>(page_rows), 1};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.k, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace sv
 
 using namespace sv;
@@ -60,7 +90,13 @@ using namespace sv;
 extern "C" {
 
 size_t spec_cache_workspace_size(int op, const spec_cache *cache, int B, int N, int Hq) {
-  (void)op, (void)cache, (void)B, (void)N, (void)Hq;
+  CacheView c;
+  if (check_cache(cache, &c) != SPEC_OK || B < 0 || N < 0) return 0;
+  if (op == SPEC_OP_CACHE_ATTEND && N > 0 && N <= SPEC_MAX_NODES && Hq > 0 && Hq % c.kv_heads == 0) {
+    CacheAttendParams P{};
+    P.c = c, P.B = B, P.N = N, P.Hq = Hq, P.group = Hq / c.kv_heads;
+    return cache_attend_workspace(P);
+  }
   return 0;
 }
 
@@ -109,8 +145,8 @@ int spec_cache_attend(const spec_cache *cache, const void *q, const int64_t *q_s
   P.dtype = dtype, P.B = B, P.N = N, P.Hq = Hq, P.group = Hq / P.c.kv_heads;
   P.cache_len = cache_len, P.n_query = n_query, P.mask = mask, P.scale = scale, P.softcap = softcap;
   P.lse = lse, P.status = status;
-  (void)workspace, (void)workspace_bytes;
-  const cudaError_t e = launch_cache_attend(P, stream_of(stream));
+  if ((rc = check_workspace(cache_attend_workspace(P), workspace, workspace_bytes)) != SPEC_OK) return rc;
+  const cudaError_t e = launch_cache_attend(P, workspace, stream_of(stream));
   return e == cudaSuccess ? SPEC_OK : cache_fail(e, "spec_cache_attend");
 }
 
