@@ -22,7 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspecverify.so")
 SOURCES = ["api.cu", "chain.cu", "chain_fused.cu", "filter.cu", "tree.cu", "rerank.cu", "ngram.cu", "noalloc.cu",
-           "host_analysis.cu", "cache_api.cu", "cache_append.cu", "cache_attend.cu", "cache_weights.cu",
+           "host_analysis.cu", "cache_api.cu", "cache_append.cu", "cache_attend.cu", "cache_attend_bf16.cu",
+           "cache_attend_f16.cu", "cache_weights.cu",
            "cache_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++20", "-Xcompiler", "-fPIC", "-I" + INCLUDE,

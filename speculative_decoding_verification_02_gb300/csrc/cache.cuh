@@ -46,6 +46,20 @@ struct CacheAttendParams {
   int32_t *status;
 };
 
+constexpr int kTilePositions = 128;  // positions to a tile of the tensor-core kernels
+constexpr int kTileRequests = 256;   // requests to one of their launches
+
+// A launch of spec_cache_attend's tensor-core path.
+struct CacheTilePlan {
+  CacheAttendParams p;
+  int first, count;     // requests of this launch
+  int page_rows;        // rows of a page that one copy brings: min(page size, 128)
+  bool q_vec, out_vec;  // rows of q and out start on 8-byte boundaries
+  int *start, *verdict, *dead;  // running sum of the requests' tiles, their status; CTAs that gave up waiting
+  float2 *ml;           // [CTA][2][rows of a unit]: reference and sum of partial rows
+  float *part;          // [CTA][2][rows of a unit][head_dim]
+};
+
 struct CacheWeightsParams {
   CacheView c;
   const char *q;
@@ -77,6 +91,8 @@ cudaError_t launch_cache_append(const CacheAppendParams &P, cudaStream_t st);
 bool cache_attend_on_tensor_cores(const CacheAttendParams &P);
 size_t cache_attend_workspace(const CacheAttendParams &P);
 cudaError_t launch_cache_attend(const CacheAttendParams &P, void *workspace, cudaStream_t st);
+cudaError_t launch_cache_attend_bf16(const CacheTilePlan &A, const CUtensorMap &map, int copies, cudaStream_t st);
+cudaError_t launch_cache_attend_f16(const CacheTilePlan &A, const CUtensorMap &map, int copies, cudaStream_t st);
 // Tensor map of the keys for copies of page_rows rows of one page and head,
 // in the shared-memory swizzle of a row's length (cache_api.cu).
 cudaError_t cache_k_map(const CacheView &c, int page_rows, CUtensorMap *map);

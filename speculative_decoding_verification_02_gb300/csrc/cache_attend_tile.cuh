@@ -1,0 +1,892 @@
+// The tensor-core path of spec_cache_attend (heads of 64 and 128).
+#pragma once
+
+#include <algorithm>
+
+#include "cache.cuh"
+#include "common.cuh"
+#include "launch.h"
+#include "tcgen05.cuh"
+
+namespace sv {
+namespace {
+
+// ---------------------------------------------------------------- tensor cores
+//
+// The rows of a kv head (token i, query head g of its group: row i * group + g)
+// are taken RT at a time, the positions 128 at a time.  The tiles of all
+// (request, head, row tile) units are laid end to end and cut into equal
+// ranges, one to a CTA, so a batch of any lengths fills every SM; a unit that
+// crosses a cut leaves partial sums that cache_attend_merge_kernel joins.
+//
+//   scores  S = Q K^T   kind::f8f6f4.  K goes from the pool to the tensor core
+//           as it is.  A row of q, scaled by a power of two to at most 256, is
+//           the sum of PIECES e4m3 numbers: two hold a bf16's 8 bits and
+//           three an fp16's 11; what is left is at most 2^-10 (half a
+//           subnormal step) against a largest element of at least 128.
+//   values  O += P V    kind::f16, P from tensor memory.  V's bytes become
+//           halves in shared memory, exactly; P is rounded to 11 bits.
+//
+// P carries the V block's scale: with lv = log2(v_scale), e = 2^(x + lv - m + 7)
+// and the sum takes e / v_scale.  The reference m follows the running
+// maximum of x + lv only when that has grown by more than 8, so O in tensor
+// memory is rarely rescaled; e stays within 2^15 and keeps 11 bits down to
+// 2^-29 of the largest.
+//
+// A unit of few rows leaves lanes of the 128-row operand free.  They hold
+// REPL copies of the rows (RT = 128 / REPL); copy w takes the w-th part of each
+// tile's positions, its P zero elsewhere, and the copies are summed at the
+// unit's end.  Each 32 lanes are served by two warps, each of half of the
+// positions, which share their rows' reference.  So eight warps share the
+// exponentials of any number of rows.
+
+constexpr int kTile = 128;         // positions to a tile
+constexpr int kMaxRequests = kTileRequests;
+constexpr int kTileThreads = 480;  // 8 softmax warps, 4 widening V, 1 loading, 2 issuing
+constexpr int kSoft = 256;         // softmax threads
+constexpr int kRing = 8;           // tiles whose scales are held
+
+template <int DT, int D>
+struct TileShape {
+  static constexpr int kPieces = DT == SPEC_DTYPE_BF16 ? 2 : 3;
+  static constexpr int kStage = kTile * D;
+  static constexpr int kStagesK = D == 128 ? 3 : 6;
+  static constexpr int kStagesV = D == 128 ? (kPieces == 2 ? 4 : 3) : 6;
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + kPieces * kTile * D;
+  static constexpr int kV8 = kK + kStagesK * kStage;
+  static constexpr int kV16 = kV8 + kStagesV * kStage;
+  static constexpr int kFold = kV16 + 2 * 2 * kStage;  // the two halves' 128 x 12 floats: the copies' sums, 8 columns at a time
+  static constexpr int kSmall = kFold + 2 * 128 * 12 * 4;
+  static constexpr int kBytes = kSmall + 5248 + 1024;  // (1024: alignment of the base)
+};
+
+// Small arrays, after the operands.
+struct TileSmall {
+  int start[kMaxRequests + 1];
+  float4 ring[kRing][8];  // a 16-position group's k_scale, log2(v_scale), 1 / v_scale
+  float row_factor[128];
+  float weight[128];   // of a copy's row when the copies are summed
+  int64_t out_at[128];  // element offset of a row in out
+  uint32_t poison[2][4];
+  int spoiled[128];    // rows that saw a NaN value
+  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], w_full[2], s_full[2], s_empty[2], p_full[2], pv_done[2];
+  uint64_t q_full, o_free, meet, pair[4], ring_full[kRing], ring_empty[kRing];
+  uint32_t tmem;
+  int dead;
+};
+static_assert(sizeof(TileSmall) <= 5248);
+
+struct Unit {
+  int b, head, row0, rows;  // request, kv head, first row, rows
+  int base, n, T;           // context, query tokens, positions that its rows can see
+  int tile0, tiles;         // its tiles in the launch's order
+};
+
+__device__ __forceinline__ int unit_positions(int base, int n, int group, int row_tile, int rt, bool masked) {
+  return masked ? base + n : base + (min((rt + 1) * row_tile, n * group) - 1) / group + 1;
+}
+
+// The request's lengths, SPEC_STATUS_OK or _BAD_LENGTH.
+__device__ __forceinline__ int request_lengths(const CacheAttendParams &P, int b, int &base, int &n) {
+  base = P.cache_len[b];
+  n = P.n_query ? P.n_query[b] : P.N;
+  if (base < 0 || n < 0 || n > P.N || base + static_cast<int64_t>(n) > capacity(P.c)) return SPEC_STATUS_BAD_LENGTH;
+  return SPEC_STATUS_OK;
+}
+
+__device__ __forceinline__ int request_tiles(const CacheAttendParams &P, int row_tile, int base, int n) {
+  int tiles = 0;
+  for (int rt = 0; rt * row_tile < n * P.group; ++rt)
+    tiles += (unit_positions(base, n, P.group, row_tile, rt, P.mask != nullptr) + kTile - 1) / kTile;
+  return tiles;
+}
+
+// The unit of request b (its tiles begin at `start`, span of them) that holds tile t.
+__device__ Unit unit_of(const CacheTilePlan &A, int row_tile, int b, int start, int span, int t) {
+  const CacheAttendParams &P = A.p;
+  Unit u;
+  u.b = A.first + b;
+  request_lengths(P, u.b, u.base, u.n);
+  const int per_head = span / P.c.kv_heads;
+  u.head = (t - start) / per_head;
+  u.tile0 = start + u.head * per_head;
+  for (int rt = 0;; ++rt) {
+    u.T = unit_positions(u.base, u.n, P.group, row_tile, rt, P.mask != nullptr);
+    u.tiles = (u.T + kTile - 1) / kTile;
+    if (t < u.tile0 + u.tiles || (rt + 1) * row_tile >= u.n * P.group) {
+      u.row0 = rt * row_tile;
+      u.rows = min(row_tile, u.n * P.group - u.row0);
+      return u;
+    }
+    u.tile0 += u.tiles;
+  }
+}
+
+__device__ __noinline__ Unit find_unit(const CacheTilePlan &A, const int *start, int row_tile, int t) {
+  int lo = 0, hi = A.count - 1;  // the last request whose start is <= t has tiles after it: equal starts are empty requests
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (start[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return unit_of(A, row_tile, lo, start[lo], start[lo + 1] - start[lo], t);
+}
+
+__device__ __forceinline__ int cut(int total, int parts, int i) {
+  return static_cast<int>(static_cast<int64_t>(total) * i / parts);
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Which of 32 drafted positions from j0 (negative: context) a row's token sees.
+__device__ __noinline__ uint32_t row_sees(const uint8_t *mask, int token, int n, int j0) {
+  if (!mask) {  // all up to itself
+    const int most = min(token, n - 1) - j0 + 1;
+    return most >= 32 ? ~0u : most <= 0 ? 0u : (1u << most) - 1;
+  }
+  uint32_t bits = 0;
+  for (int e = 0; e < 32; ++e) {
+    const int j = j0 + e;
+    if (j < 0 || (j < n && mask[j] != 0)) bits |= 1u << e;
+  }
+  return bits;
+}
+
+// 16-byte chunk index of a row in the K-major swizzle of its row length.
+template <int D>
+__device__ __forceinline__ int swizzled(int row, int chunk) {
+  return D == 128 ? chunk ^ (row & 7) : chunk ^ (row >> 1 & 3);
+}
+
+// A lane's 2 or 4 consecutive values of a row, from one load.
+template <int DT, int EACH>
+__device__ __forceinline__ void load_each(const char *row, int lane, float *x) {
+  uint32_t w[EACH / 2];
+  if constexpr (EACH == 4) {
+    const uint2 v = reinterpret_cast<const uint2 *>(row)[lane];
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = reinterpret_cast<const uint32_t *>(row)[lane];
+  }
+#pragma unroll
+  for (int e = 0; e < EACH / 2; ++e) {
+    if constexpr (DT == SPEC_DTYPE_BF16) {
+      x[2 * e] = bf16_lo(w[e]), x[2 * e + 1] = bf16_hi(w[e]);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+      x[2 * e] = f.x, x[2 * e + 1] = f.y;
+    }
+  }
+}
+
+// Two values in the rows' type, the first in the low half.
+template <int DT>
+__device__ __forceinline__ uint32_t pair_bits(float lo, float hi) {
+  if constexpr (DT == SPEC_DTYPE_F16) return half2_bits(lo, hi);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int DT, int D, int REPL, bool CAP>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    cache_attend_tile_kernel(const CacheTilePlan A, const __grid_constant__ CUtensorMap k_map) {
+  using S = TileShape<DT, D>;
+  constexpr int RT = 128 / REPL;        // rows to a unit
+  constexpr int OWN = kTile / REPL / 2;  // positions that a thread takes of each tile
+  constexpr uint32_t kCols = 512, kO = 256, kP = 384;  // tensor memory: S at 0 and 128, O, P at 384 and 448
+  extern __shared__ char raw[];
+  char *const smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  TileSmall &sm = *reinterpret_cast<TileSmall *>(smem + S::kSmall);
+  const CacheAttendParams &P = A.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+
+  if (tid == 0) {
+    for (int i = 0; i < S::kStagesK; ++i) bar_init(&sm.k_full[i], 1), bar_init(&sm.k_empty[i], 1);
+    for (int i = 0; i < S::kStagesV; ++i) bar_init(&sm.v_full[i], 1), bar_init(&sm.v_empty[i], 128);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&sm.w_full[i], 128);
+      bar_init(&sm.s_full[i], 1);
+      bar_init(&sm.s_empty[i], kSoft);
+      bar_init(&sm.p_full[i], kSoft);
+      bar_init(&sm.pv_done[i], 1);
+    }
+    bar_init(&sm.q_full, kSoft);
+    bar_init(&sm.o_free, kSoft);
+    bar_init(&sm.meet, kSoft);
+    for (int i = 0; i < 4; ++i) bar_init(&sm.pair[i], 64);
+    for (int i = 0; i < kRing; ++i) bar_init(&sm.ring_full[i], 32), bar_init(&sm.ring_empty[i], kSoft);
+    bar_init_fence();
+    sm.dead = 0;
+  }
+  if (tid < 128) sm.spoiled[tid] = 0;
+  if (warp == 13) tmem_alloc(&sm.tmem, kCols);
+  // Every request's tiles, then their running sum.
+  for (int b = tid; b < A.count; b += kTileThreads) {
+    int base, n;
+    const bool ok = request_lengths(P, A.first + b, base, n) == SPEC_STATUS_OK;
+    sm.start[b + 1] = ok ? request_tiles(P, RT, base, n) * P.c.kv_heads : 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) {
+    int carry = 0;
+    for (int b0 = 0; b0 < A.count; b0 += 32) {
+      int x = b0 + lane < A.count ? sm.start[b0 + lane + 1] : 0;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, x, o);
+        if (lane >= o) x += y;
+      }
+      x += carry;
+      if (b0 + lane < A.count) {
+        sm.start[b0 + lane + 1] = x;
+        if (cta == 0) A.start[b0 + lane + 1] = x;
+      }
+      carry = __shfl_sync(~0u, x, 31);
+    }
+    if (lane == 0) {
+      sm.start[0] = 0;
+      if (cta == 0) A.start[0] = 0;
+    }
+  }
+  __syncthreads();
+  const int total = sm.start[A.count];
+  const int lo = cut(total, ctas, cta), hi = cut(total, ctas, cta + 1);
+  const uint32_t tmem = sm.tmem;
+  volatile int *dead = &sm.dead;
+
+  if (warp == 12) {
+    // ---- loading: a lane to a group of 16 positions (the first 8 lanes), two tiles ahead with the page table
+    const int shift = P.c.page_shift;
+    const int page_rows = A.page_rows;
+    int ahead_t = lo, ahead_end = lo;
+    Unit au{};
+    // the next tile's position of this lane's group, its request and head; -1 past the range or the unit's positions
+    int g_pos[2], g_b[2], g_head[2], g_page[2];
+    auto advance = [&](int slot) {
+      g_page[slot] = -1;
+      g_pos[slot] = -1;
+      if (ahead_t >= hi) return;
+      if (ahead_t >= ahead_end) {
+        au = find_unit(A, sm.start, RT, ahead_t);
+        ahead_end = au.tile0 + au.tiles;
+      }
+      const int pos = (ahead_t - au.tile0) * kTile + lane * 16;
+      g_b[slot] = au.b;
+      g_head[slot] = au.head;
+      if (lane < 8 && pos < au.T) {
+        g_pos[slot] = pos;
+        g_page[slot] = page_at(P.c, au.b, pos >> shift);
+      }
+      ++ahead_t;
+    };
+    float ks = 1.0f, vs = 1.0f, ks1 = 1.0f, vs1 = 1.0f;
+    auto scales = [&](int slot, float &k, float &v) {
+      k = 1.0f, v = 1.0f;
+      if (g_page[slot] >= 0) {
+        const int64_t at = g_page[slot] * P.c.scale_stride + g_head[slot];
+        k = P.c.k_scale[at];
+        v = P.c.v_scale[at];
+      }
+    };
+    advance(0);
+    advance(1);
+    scales(0, ks, vs);
+    for (int t = lo; t < hi; ++t) {
+      const int i = t - lo, cur = 0;
+      // this tile's data, and the loads of the next ones'
+      const int pos = g_pos[cur], page = g_page[cur], head = g_head[cur];
+      scales(1, ks1, vs1);
+      g_pos[0] = g_pos[1], g_b[0] = g_b[1], g_head[0] = g_head[1], g_page[0] = g_page[1];
+      advance(1);
+      const int r = i % kRing;
+      if (i >= kRing && !warp_wait(&sm.ring_empty[r], (i / kRing - 1) & 1, dead)) break;
+      if (lane < 8) sm.ring[r][lane] = make_float4(ks, log2f(vs), 1.0f / vs, 0.0f);
+      bar_arrive(&sm.ring_full[r]);
+      const bool load = pos >= 0 && page >= 0 && (pos & (page_rows - 1)) == 0;
+      const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(~0u, load)) * page_rows * D);
+      const int sk = i % S::kStagesK, sv = i % S::kStagesV;
+      if (i >= S::kStagesK && !warp_wait(&sm.k_empty[sk], (i / S::kStagesK - 1) & 1, dead)) break;
+      if (lane == 0) bar_expect(&sm.k_full[sk], bytes);
+      __syncwarp();
+      const int in_page = pos & ((1 << shift) - 1), in_tile = lane * 16;
+      if (load) tensor_load_3d(smem + S::kK + sk * S::kStage + in_tile * D, &k_map, 0, (head << shift) + in_page, page, &sm.k_full[sk]);
+      if (i >= S::kStagesV && !warp_wait(&sm.v_empty[sv], (i / S::kStagesV - 1) & 1, dead)) break;
+      if (lane == 0) bar_expect(&sm.v_full[sv], bytes);
+      __syncwarp();
+      if (load)
+        bulk_load(smem + S::kV8 + sv * S::kStage + in_tile * D, P.c.v + block_offset(P.c, page, head) + static_cast<int64_t>(in_page) * D,
+                  page_rows * D, &sm.v_full[sv]);
+      ks = ks1, vs = vs1;
+    }
+    __syncwarp();
+    if (*dead) {  // the copies in flight land before the CTA leaves
+      for (int s = 0; s < S::kStagesK; ++s)
+        for (int k = 0; k < 4096 && !bar_try(&sm.k_full[s], 0) && !bar_try(&sm.k_full[s], 1); ++k) {}
+      for (int s = 0; s < S::kStagesV; ++s)
+        for (int k = 0; k < 4096 && !bar_try(&sm.v_full[s], 0) && !bar_try(&sm.v_full[s], 1); ++k) {}
+    }
+  } else if (warp == 13) {
+    // ---- issuing S = Q K^T
+    constexpr uint32_t kId = mma_desc(kTile, false);
+    constexpr uint64_t kSw = D == 128 ? kSwizzle128 : kSwizzle64;
+    const uint64_t q_desc = matrix_desc(smem_u32(smem + S::kQ), 16, 8 * D, kSw);
+    const uint64_t k_desc = matrix_desc(smem_u32(smem + S::kK), 16, 8 * D, kSw);
+    int unit_end = lo, units = 0;
+    for (int t = lo; t < hi; ++t) {
+      const int i = t - lo, sk = i % S::kStagesK;
+      if (t >= unit_end) {
+        const Unit u = find_unit(A, sm.start, RT, t);
+        unit_end = u.tile0 + u.tiles;
+        if (!warp_wait(&sm.q_full, units & 1, dead)) break;
+        ++units;
+      }
+      if (!warp_wait(&sm.k_full[sk], (i / S::kStagesK) & 1, dead)) break;
+      if (i >= 2 && !warp_wait(&sm.s_empty[i & 1], (i / 2 - 1) & 1, dead)) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int piece = 0; piece < S::kPieces; ++piece)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            mma_f8(tmem + (i & 1) * 128, q_desc + ((piece * kTile * D + k * 32) >> 4), k_desc + ((sk * S::kStage + k * 32) >> 4), kId,
+                   piece + k > 0);
+        tc_commit(&sm.k_empty[sk]);
+        tc_commit(&sm.s_full[i & 1]);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 14) {
+    // ---- issuing O += P V
+    constexpr uint32_t kId = mma_desc(D, true);
+    const uint64_t v_desc = matrix_desc(smem_u32(smem + S::kV16), kTile * 128, 1024, kSwizzle128);
+    int unit_end = lo, units = 0;
+    for (int t = lo; t < hi; ++t) {
+      const int i = t - lo, w = i & 1;
+      const bool fresh = t >= unit_end;
+      if (fresh) {
+        const Unit u = find_unit(A, sm.start, RT, t);
+        unit_end = u.tile0 + u.tiles;
+        if (units > 0 && !warp_wait(&sm.o_free, (units - 1) & 1, dead)) break;
+        ++units;
+      }
+      if (!warp_wait(&sm.w_full[w], (i >> 1) & 1, dead)) break;
+      if (!warp_wait(&sm.p_full[w], (i >> 1) & 1, dead)) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_f16_ta(tmem + kO, tmem + kP + w * 64 + k * 8, v_desc + ((w * 2 * S::kStage + k * 2048) >> 4), kId, !(fresh && k == 0));
+        tc_commit(&sm.pv_done[w]);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= 8) {
+    // ---- widening V: 16 bytes of a position to 16 halves, in the MN-major layout of the operand
+    const int w4 = warp - 8;
+    for (int b = cta; b < A.count; b += ctas) {  // and, on the way, the page tables: a request with a bad page gives nothing
+      int base, n;
+      int st = request_lengths(P, A.first + b, base, n);
+      int bad = 0;
+      if (st == SPEC_STATUS_OK)
+        for (int j = tid - 256; static_cast<int64_t>(j) << P.c.page_shift < base + n; j += 128) bad |= page_at(P.c, A.first + b, j) < 0;
+      if (tid == 256) A.verdict[b] = st;
+      asm volatile("bar.sync 2, 128;" ::: "memory");
+      if (bad) A.verdict[b] = SPEC_STATUS_BAD_PAGE;
+    }
+    int unit_end = lo;
+    Unit u{};
+    constexpr int kLanes = D / 16;        // lanes to a position
+    constexpr int kPer = 32 / kLanes;     // positions to a step
+    const int piece = lane % kLanes, sub = lane / kLanes;
+    for (int t = lo; t < hi; ++t) {
+      const int i = t - lo, sv = i % S::kStagesV, w = i & 1;
+      if (t >= unit_end) {
+        u = find_unit(A, sm.start, RT, t);
+        unit_end = u.tile0 + u.tiles;
+      }
+      const int pos0 = (t - u.tile0) * kTile;
+      const bool edge = pos0 + kTile > u.base;
+      if (!warp_wait(&sm.v_full[sv], (i / S::kStagesV) & 1, dead)) break;
+      if (i >= 2 && !warp_wait(&sm.pv_done[w], (i / 2 - 1) & 1, dead)) break;
+      const char *src = smem + S::kV8 + sv * S::kStage;
+      char *dst = smem + S::kV16 + w * 2 * S::kStage;
+      uint32_t poison = 0;
+      auto widen = [&](uint4 x, int row) {
+        uint4 h[2];
+        uint32_t *o = reinterpret_cast<uint32_t *>(h);
+        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const __half2 a = e4m3x2_to_half2(in[c] & 0xffff), b = e4m3x2_to_half2(in[c] >> 16);
+          o[2 * c] = *reinterpret_cast<const uint32_t *>(&a);
+          o[2 * c + 1] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        // columns of 64: 16 KB apart; eight positions: 1024 bytes; chunks of 16 bytes swizzled by the position
+        char *to = dst + (piece >> 2) * (kTile * 128) + (row >> 3) * 1024 + (row & 7) * 128;
+        const int c0 = (piece & 3) * 2;
+        const bool flip = piece >> 2 & 1;  // (the two column groups store their chunks in opposite order: no bank conflict)
+        *reinterpret_cast<uint4 *>(to + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? h[1] : h[0];
+        *reinterpret_cast<uint4 *>(to + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? h[0] : h[1];
+      };
+      constexpr int kSteps = 32 / kPer;
+      if (!edge) {
+#pragma unroll 1
+        for (int step = 0; step < kSteps; step += 4) {
+          uint4 x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const uint4 *>(src + (w4 * 32 + (step + k) * kPer + sub) * D + piece * 16);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) widen(x[k], w4 * 32 + (step + k) * kPer + sub);
+        }
+      } else {  // nothing past the last position, and no NaN where a row may not look
+#pragma unroll 1
+        for (int step = 0; step < kSteps; ++step) {
+          const int row = w4 * 32 + step * kPer + sub, pos = pos0 + row;
+          uint4 x = *reinterpret_cast<const uint4 *>(src + row * D + piece * 16);
+          bool nan = false;
+          if (pos >= u.T) x = make_uint4(0, 0, 0, 0);
+          else if (pos >= u.base) {
+            uint32_t *e = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              // bytes of 0x7f under the sign: 0x80 after adding one
+              const uint32_t hit = ((e[c] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+              nan |= hit != 0;
+              e[c] &= ~(hit | (hit - (hit >> 7)));
+            }
+          }
+          const uint32_t vote = __ballot_sync(~0u, nan);
+#pragma unroll
+          for (int c = 0; c < kPer; ++c)
+            if (vote >> (c * kLanes) & ((1u << kLanes) - 1)) poison |= 1u << (step * kPer + c);
+          widen(x, row);
+        }
+      }
+      if (edge && lane == 0) sm.poison[w][w4] = poison;
+      fence_async_shared();
+      bar_arrive(&sm.v_empty[sv]);
+      bar_arrive(&sm.w_full[w]);
+    }
+  } else {
+    // ---- softmax: two threads to a row (of its copy), each with OWN positions of each tile
+    const int half = warp >> 2, quarter = warp & 3;
+    const int spot = quarter * 32 + lane;                  // lane of tensor memory
+    const int copy = spot / RT, r = spot % RT;             // which copy of the rows, and the row
+    const int col0 = copy * 2 * OWN + half * OWN;          // its positions in the tile
+    const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
+    if (REPL > 1) {
+      const uint32_t zero[16] = {};
+      for (int c = 0; c < 64; c += 16) tmem_st16(tmem + lanes + kP + half * 64 + c, zero);
+      tc_wait_st();
+      tc_fence_before();
+    }
+    const bool negative = P.scale < 0.0f;
+    bool ok = true;
+    uint32_t meetings = 0, pairings = 0;
+    auto together = [&] {  // a barrier of the eight warps, bounded like every wait
+      bar_arrive(&sm.meet);
+      return warp_wait(&sm.meet, meetings++ & 1, dead);
+    };
+    // A unit's rows of q as e4m3 pieces; every earlier score product that reads them has completed.
+    auto write_q = [&](const Unit &u) {
+      constexpr int kEach = D / 32;  // elements to a lane
+#pragma unroll 1
+      for (int first = warp; first < u.rows; first += 32) {
+        float x[4][kEach];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = u.row0 + first + 8 * k;
+          if (first + 8 * k < u.rows) {
+            const char *q = P.q + (u.b * P.qs[0] + row / P.group * P.qs[1] + (u.head * P.group + row % P.group) * P.qs[2]) * 2;
+            if (A.q_vec) load_each<DT, kEach>(q, lane, x[k]);
+            else
+#pragma unroll
+              for (int e = 0; e < kEach; ++e) x[k][e] = row_value<DT>(q, lane * kEach + e);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r0 = first + 8 * k;
+          if (r0 >= u.rows) break;
+          float top = 0.0f;
+#pragma unroll
+          for (int e = 0; e < kEach; ++e) {
+            if (negative) x[k][e] = -x[k][e];
+            top = fmaxf(top, finite_abs(x[k][e]));
+          }
+          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+          // 2^ex with top / 2^ex in [128, 256)
+          const int ex = top > 0.0f ? max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 7, -110) : 0;
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+#pragma unroll
+          for (int e = 0; e < kEach; ++e) x[k][e] *= down;
+#pragma unroll
+          for (int piece = 0; piece < S::kPieces; ++piece) {
+            uint32_t code = 0;
+#pragma unroll
+            for (int e = 0; e < kEach; e += 2) {
+              const uint32_t two = to_e4m3x2(x[k][e], x[k][e + 1]);
+              const float2 back = e4m3x2_to_float2(two);
+              x[k][e] -= back.x;
+              x[k][e + 1] -= back.y;
+              code |= two << (8 * e);
+            }
+#pragma unroll
+            for (int c = 0; c < REPL; ++c) {
+              const int a = c * RT + r0;
+              char *to = smem + S::kQ + piece * kTile * D + a * D + (swizzled<D>(a, lane * kEach >> 4) << 4) + (lane * kEach & 15);
+              if (kEach == 4) *reinterpret_cast<uint32_t *>(to) = code;
+              else *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(code);
+            }
+          }
+          if (lane == 0) sm.row_factor[r0] = fmaxf(fabsf(P.scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(ex + 127) << 23), 1e-30f);
+        }
+      }
+      fence_async_shared();
+      bar_arrive(&sm.q_full);
+      return together();
+    };
+    float *tops = reinterpret_cast<float *>(smem + S::kFold);                 // [2 tiles][2 halves][128]
+    float2 *mls = reinterpret_cast<float2 *>(smem + S::kFold + 4096);         // [2 halves][128]
+    float *fold = reinterpret_cast<float *>(smem + S::kFold) + half * 128 * 12;  // (after the unit's last tile)
+    Unit next{};
+    if (lo < hi) {
+      next = find_unit(A, sm.start, RT, lo);
+      ok = write_q(next);
+    }
+    for (int t = lo; t < hi && ok;) {
+      const Unit u = next;
+      const int t_end = min(hi, u.tile0 + u.tiles);
+      const bool live = r < u.rows;
+      const float factor = live ? sm.row_factor[r] : 0.0f;
+      const int token = live ? (u.row0 + r) / P.group : 0;
+      const uint8_t *mask = P.mask ? P.mask + (static_cast<int64_t>(u.b) * P.N + token) * P.N : nullptr;
+      const float cap2 = P.softcap * kLog2e;                // the cap in units of log 2
+      const float in_cap = CAP ? 2.0f / P.softcap : 0.0f;   // (of x in units of log 2) to 2 x / cap in units of log 2
+      float m = -INFINITY, sum = 0.0f;
+
+      for (; t < t_end; ++t) {
+        const int i = t - lo, sb = i & 1, ring = i % kRing;
+        const int pos0 = (t - u.tile0) * kTile + col0;
+        const bool edge = pos0 + OWN > u.base;
+        if (!(ok = warp_wait(&sm.ring_full[ring], (i / kRing) & 1, dead))) break;
+        float4 sc[(OWN + 15) / 16];
+#pragma unroll
+        for (int g = 0; g < (OWN + 15) / 16; ++g) sc[g] = sm.ring[ring][col0 / 16 + g];
+        bar_arrive(&sm.ring_empty[ring]);
+        if (!(ok = warp_wait(&sm.s_full[sb], (i >> 1) & 1, dead))) break;
+        tc_fence_after();
+        float x[OWN];
+        if (OWN == 16) {
+          tmem_ld16(tmem + lanes + sb * 128 + col0, x);
+        } else {
+#pragma unroll
+          for (int c = 0; c < OWN; c += 32) tmem_ld32(tmem + lanes + sb * 128 + col0 + c, x + c);
+        }
+        tc_wait_ld();
+        tc_fence_before();
+        bar_arrive(&sm.s_empty[sb]);
+
+        // x f is the score in units of log 2; with a cap it is formed here
+        if (CAP) {
+#pragma unroll
+          for (int g = 0; g < OWN / 16; ++g) {
+            const float f = factor * sc[g].x * in_cap;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              // cap tanh(x / cap) = cap (1 - 2 / (1 + exp(2 x / cap)))
+              const float y = x[g * 16 + e] * f;
+              x[g * 16 + e] = cap2 * (1.0f - __fdividef(2.0f, 1.0f + ex2(y > 120.0f ? 120.0f : y)));
+            }
+          }
+        }
+        uint32_t sees[(OWN + 31) / 32];
+        if (edge) {  // (the factor below is never 0, so -inf stays -inf)
+#pragma unroll
+          for (int c = 0; c < (OWN + 31) / 32; ++c) {
+            sees[c] = live ? row_sees(mask, token, u.n, pos0 + c * 32 - u.base) : 0;
+#pragma unroll
+            for (int e = 0; e < (OWN < 32 ? OWN : 32); ++e)
+              if (!(sees[c] >> e & 1)) x[c * 32 + e] = -INFINITY;
+          }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < OWN / 16; ++g) {
+          float high = fmaxf(x[g * 16], x[g * 16 + 1]);
+#pragma unroll
+          for (int e = 2; e < 16; e += 2) high = fmaxf(high, fmaxf(x[g * 16 + e], x[g * 16 + e + 1]));
+          top = fmaxf(top, fmaf(high, CAP ? 1.0f : fmaxf(factor * sc[g].x, 1.2e-38f), sc[g].y));
+        }
+        // the two threads of a row agree on its maximum
+        tops[(sb * 2 + half) * 128 + spot] = top;
+        bar_arrive(&sm.pair[quarter]);
+        if (!(ok = warp_wait(&sm.pair[quarter], pairings++ & 1, dead))) break;
+        top = fmaxf(top, tops[(sb * 2 + 1 - half) * 128 + spot]);
+        // the reference, and O with it when it moves
+        const bool moves = live && top > m + 8.0f;
+        if (__any_sync(~0u, moves)) {
+          const float next_m = moves ? top : m;
+          const float keep = m == -INFINITY ? 0.0f : ex2(m - next_m);
+          m = next_m;
+          sum *= keep;
+          const int done = i - 1;
+          if (t > max(lo, u.tile0)) {
+            if (!(ok = warp_wait(&sm.pv_done[done & 1], (done >> 1) & 1, dead))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+              float o[16];
+              tmem_ld16(tmem + lanes + kO + c, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= keep;
+              tmem_st16(tmem + lanes + kO + c, reinterpret_cast<uint32_t *>(o));
+            }
+            tc_wait_st();
+          }
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;
+        uint32_t p[OWN / 2];
+#pragma unroll
+        for (int g = 0; g < OWN / 16; ++g) {
+          const float shift = sc[g].y - ref + 7.0f, f = CAP ? 1.0f : fmaxf(factor * sc[g].x, 1.2e-38f);
+          float part[4] = {};
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float a = ex2(fmaf(x[g * 16 + e], f, shift)), b = ex2(fmaf(x[g * 16 + e + 1], f, shift));
+            part[e & 2] += a;
+            part[(e & 2) + 1] += b;
+            p[g * 8 + e / 2] = half2_bits(a, b);
+          }
+          sum = fmaf((part[0] + part[1]) + (part[2] + part[3]), sc[g].z, sum);
+        }
+        if (i >= 2 && !(ok = warp_wait(&sm.pv_done[sb], (i / 2 - 1) & 1, dead))) break;  // P's columns are free
+        tc_fence_after();
+        if (OWN == 16) tmem_st8(tmem + lanes + kP + sb * 64 + col0 / 2, p);
+#pragma unroll
+        for (int c = 0; c + 16 <= OWN / 2; c += 16) tmem_st16(tmem + lanes + kP + sb * 64 + col0 / 2 + c, p + c);
+        if (edge) {  // a row that sees a position whose V was NaN
+          if (!(ok = warp_wait(&sm.w_full[sb], (i >> 1) & 1, dead))) break;
+          uint32_t bad = 0;
+#pragma unroll
+          for (int c = 0; c < (OWN + 31) / 32; ++c) {
+            const uint32_t at = sm.poison[sb][col0 / 32 + c] >> (OWN < 32 ? col0 & 31 : 0);
+            bad |= sees[c] & (OWN < 32 ? at & ((1u << OWN) - 1) : at);
+          }
+          if (bad) sm.spoiled[r] = 1;
+        }
+        tc_wait_st();
+        tc_fence_before();
+        bar_arrive(&sm.p_full[sb]);
+      }
+      if (!ok) break;
+
+      if (t < hi) {  // the next unit's q, while this one's last values are being summed
+        next = find_unit(A, sm.start, RT, t);
+        if (!(ok = write_q(next))) break;
+      } else if (!(ok = together())) break;  // (tops has been read)
+      // The unit's end in this CTA: the rows' sums over copies and halves, and what each copy's O is multiplied by.
+      const bool whole = lo <= u.tile0 && t == u.tile0 + u.tiles;
+      const int slot = cta * 2 + (max(lo, u.tile0) != lo ? 1 : 0);
+      mls[half * 128 + spot] = make_float2(m, sum);
+      if (!(ok = together())) break;
+      if (tid < u.rows) {
+        float m_all = -INFINITY, l_all = 0.0f;
+#pragma unroll
+        for (int c = 0; c < REPL; ++c) m_all = fmaxf(m_all, mls[c * RT + tid].x);
+        const float ref = m_all == -INFINITY ? 0.0f : m_all;
+#pragma unroll
+        for (int c = 0; c < REPL; ++c)
+          l_all += (mls[c * RT + tid].y + mls[128 + c * RT + tid].y) * ex2(mls[c * RT + tid].x - ref);
+        float norm = 1.0f;
+        const int row = u.row0 + tid, tok = row / P.group, h = u.head * P.group + row % P.group;
+        if (whole) {
+          norm = l_all == 0.0f ? 0.0f : 1.0f / l_all;
+          if (P.lse)
+            P.lse[(static_cast<int64_t>(u.b) * P.N + tok) * P.Hq + h] = l_all == 0.0f ? -INFINITY : (m_all - 7.0f + log2f(l_all)) * kLn2;
+          sm.out_at[tid] = u.b * P.os[0] + tok * P.os[1] + h * P.os[2];
+        } else {
+          A.ml[static_cast<int64_t>(slot) * RT + tid] = make_float2(m_all, l_all);
+        }
+        if (sm.spoiled[tid]) norm = NAN;
+        sm.spoiled[tid] = 0;
+#pragma unroll
+        for (int c = 0; c < REPL; ++c) sm.weight[c * RT + tid] = norm * ex2(mls[c * RT + tid].x - ref);
+      }
+      const int last = t - 1 - lo;
+      if (!(ok = warp_wait(&sm.pv_done[last & 1], (last >> 1) & 1, dead))) break;
+      tc_fence_after();
+      if (!(ok = together())) break;
+      const float w_own = live ? sm.weight[spot] : 0.0f;
+      auto put4 = [&](int rr, int c, float4 y) {  // four components of a row
+        if (whole) {
+          char *out = P.out + sm.out_at[rr] * 2;
+          if (A.out_vec) {
+            *reinterpret_cast<uint2 *>(out + c * 2) = make_uint2(pair_bits<DT>(y.x, y.y), pair_bits<DT>(y.z, y.w));
+          } else {
+            put_value<DT>(out, c, y.x), put_value<DT>(out, c + 1, y.y), put_value<DT>(out, c + 2, y.z), put_value<DT>(out, c + 3, y.w);
+          }
+        } else {
+          *reinterpret_cast<float4 *>(A.part + (static_cast<int64_t>(slot) * RT + rr) * D + c) = y;
+        }
+      };
+#pragma unroll 1
+      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 8) {
+        float o[8];
+        tmem_ld8(tmem + lanes + kO + c, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= w_own;
+        if (REPL == 1) {
+          if (live) {
+            put4(r, c, make_float4(o[0], o[1], o[2], o[3]));
+            put4(r, c + 4, make_float4(o[4], o[5], o[6], o[7]));
+          }
+        } else {
+          if (!(ok = together())) break;  // the columns before have been read
+          *reinterpret_cast<float4 *>(fold + spot * 12) = make_float4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<float4 *>(fold + spot * 12 + 4) = make_float4(o[4], o[5], o[6], o[7]);
+          if (!(ok = together())) break;
+          const int rr = spot >> 1, at = (spot & 1) * 4;
+          if (rr < u.rows) {
+            float4 y = *reinterpret_cast<const float4 *>(fold + rr * 12 + at);
+#pragma unroll
+            for (int k = 1; k < REPL; ++k) {
+              const float4 z = *reinterpret_cast<const float4 *>(fold + (k * RT + rr) * 12 + at);
+              y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+            }
+            put4(rr, c + at, y);
+          }
+        }
+      }
+      if (!ok) break;
+      tc_fence_before();
+      bar_arrive(&sm.o_free);
+      ok = together();  // the shared arrays have been read
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  pdl_launch_dependents();
+  if (tid == 0) A.dead[cta] = sm.dead;
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_free(tmem, kCols);
+  }
+}
+
+// Joins the partial sums of the units that more than one CTA worked on, a warp
+// to a row, and writes what no unit covers: rows past n_query, bad requests.
+template <int DT, int D>
+__global__ void __launch_bounds__(256) cache_attend_merge_kernel(const CacheTilePlan A, int row_tile, int ctas) {
+  const CacheAttendParams &P = A.p;
+  const int lane = threadIdx.x & 31;
+  const int64_t x = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  pdl_wait();
+  if (x >= static_cast<int64_t>(A.count) * P.N * P.Hq) return;
+  const int h = static_cast<int>(x % P.Hq), i = static_cast<int>(x / P.Hq % P.N), bl = static_cast<int>(x / P.Hq / P.N);
+  const int b = A.first + bl;
+  int st = A.verdict[bl];
+  int gone = 0;
+  for (int c = lane; c < ctas; c += 32) gone |= A.dead[c];
+  if (__any_sync(~0u, gone)) st = SPEC_STATUS_TIMEOUT;
+  if (P.status && i == 0 && h == 0 && lane == 0) P.status[b] = st;
+  constexpr int kEach = D / 32;
+  char *out = P.out + (b * P.os[0] + i * P.os[1] + h * P.os[2]) * 2;
+  const int64_t at_lse = (static_cast<int64_t>(b) * P.N + i) * P.Hq + h;
+  int base, n;
+  request_lengths(P, b, base, n);
+  if (st != SPEC_STATUS_OK || i >= n) {
+    for (int e = 0; e < kEach; ++e) put_value<DT>(out, lane * kEach + e, 0.0f);
+    if (lane == 0 && P.lse) P.lse[at_lse] = -INFINITY;
+    return;
+  }
+  // the row's unit, and the CTAs whose ranges it meets
+  const int total = A.start[A.count], start = A.start[bl], span = A.start[bl + 1] - start;
+  const int head = h / P.group, row = i * P.group + h % P.group, rt = row / row_tile, r = row % row_tile;
+  int tile0 = start + head * (span / P.c.kv_heads);
+  for (int k = 0; k < rt; ++k) tile0 += (unit_positions(base, n, P.group, row_tile, k, P.mask != nullptr) + kTile - 1) / kTile;
+  const int tiles = (unit_positions(base, n, P.group, row_tile, rt, P.mask != nullptr) + kTile - 1) / kTile;
+  int c0 = static_cast<int>(static_cast<int64_t>(tile0) * ctas / total);
+  while (cut(total, ctas, c0 + 1) <= tile0) ++c0;
+  int c1 = c0;
+  while (cut(total, ctas, c1 + 1) < tile0 + tiles) ++c1;
+  if (c0 == c1) return;
+  auto slot_of = [&](int c) {
+    const int s = c * 2 + (c == c0 && cut(total, ctas, c) < tile0 ? 1 : 0);
+    return static_cast<int64_t>(s) * row_tile + r;
+  };
+  auto has = [&](int c) { return cut(total, ctas, c + 1) > cut(total, ctas, c); };
+  float m = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32)
+    if (has(c)) m = fmaxf(m, A.ml[slot_of(c)].x);
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+  const float ref = m == -INFINITY ? 0.0f : m;
+  float acc[kEach] = {}, sum = 0.0f;
+  for (int cc = c0; cc <= c1; cc += 32) {
+    const int c = cc + lane;
+    float w = 0.0f, l = 0.0f;
+    int64_t s = 0;
+    if (c <= c1 && has(c)) {
+      s = slot_of(c);
+      const float2 ml = A.ml[s];
+      w = ex2(ml.x - ref);
+      l = ml.y * w;
+    }
+    sum += warp_sum(l);
+    const int here = min(32, c1 - cc + 1);
+    for (int k = 0; k < here; ++k) {
+      const float wk = __shfl_sync(~0u, w, k);
+      const float *o = A.part + __shfl_sync(~0u, s, k) * D + lane * kEach;
+      if (!has(cc + k)) continue;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) acc[e] = fmaf(o[e], wk, acc[e]);
+    }
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) put_value<DT>(out, lane * kEach + e, acc[e] * inv);
+  if (lane == 0 && P.lse) P.lse[at_lse] = sum == 0.0f ? -INFINITY : (m - 7.0f + log2f(sum)) * kLn2;
+}
+
+template <int DT, int D, int REPL>
+cudaError_t launch_tiles(const CacheTilePlan &A, const CUtensorMap &map, cudaStream_t st) {
+  using S = TileShape<DT, D>;
+  auto kern = A.p.softcap > 0.0f ? cache_attend_tile_kernel<DT, D, REPL, true> : cache_attend_tile_kernel<DT, D, REPL, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  if (e != cudaSuccess) return e;
+  const int ctas = device_sm_count();
+  e = trace_launch("cache_attend_tile", st, [&] { kern<<<ctas, kTileThreads, S::kBytes, st>>>(A, map); });
+  if (e != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(A.count) * A.p.N * A.p.Hq;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = trace_enabled() ? 0 : 1;
+  return trace_launch_ex("cache_attend_merge", st,
+                         [&] { return cudaLaunchKernelEx(&cfg, cache_attend_merge_kernel<DT, D>, A, 128 / REPL, ctas); });
+}
+
+template <int DT, int D>
+cudaError_t launch_tiles(const CacheTilePlan &A, const CUtensorMap &map, int copies, cudaStream_t st) {
+  if (copies == 4) return launch_tiles<DT, D, 4>(A, map, st);
+  if (copies == 2) return launch_tiles<DT, D, 2>(A, map, st);
+  return launch_tiles<DT, D, 1>(A, map, st);
+}
+
+}  // namespace
+}  // namespace sv
