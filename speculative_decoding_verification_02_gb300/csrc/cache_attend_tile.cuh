@@ -36,14 +36,14 @@ namespace {
 // A unit of few rows leaves lanes of the 128-row operand free.  They hold
 // REPL copies of the rows (RT = 128 / REPL); copy w takes the w-th part of each
 // tile's positions, its P zero elsewhere, and the copies are summed at the
-// unit's end.  Each 32 lanes are served by two warps, each of half of the
-// positions, which share their rows' reference.  So eight warps share the
-// exponentials of any number of rows.
+// unit's end.  With four copies four warps do the exponentials, 32 positions
+// to a thread.  With two or one, each 32 lanes are served by two warps, each of
+// half of the positions, which agree on their rows' reference: that costs a
+// barrier, and halves what a thread does between the two products.
 
 constexpr int kTile = 128;         // positions to a tile
 constexpr int kMaxRequests = kTileRequests;
-constexpr int kTileThreads = 480;  // 8 softmax warps, 4 widening V, 1 loading, 2 issuing
-constexpr int kSoft = 256;         // softmax threads
+constexpr int kTileThreads = 512;  // 8 softmax warps (4 of them idle with four copies), 4 widening V, 2 loading, 2 issuing
 constexpr int kRing = 8;           // tiles whose scales are held
 
 template <int DT, int D>
@@ -56,26 +56,33 @@ struct TileShape {
   static constexpr int kK = kQ + kPieces * kTile * D;
   static constexpr int kV8 = kK + kStagesK * kStage;
   static constexpr int kV16 = kV8 + kStagesV * kStage;
-  static constexpr int kFold = kV16 + 2 * 2 * kStage;  // the two halves' 128 x 12 floats: the copies' sums, 8 columns at a time
-  static constexpr int kSmall = kFold + 2 * 128 * 12 * 4;
-  static constexpr int kBytes = kSmall + 5248 + 1024;  // (1024: alignment of the base)
+  static constexpr int kSmall = kV16 + 2 * 2 * kStage;
+  static constexpr int kBytes = kSmall + 12288 + 1024;  // (1024: alignment of the base)
+};
+
+// What a CTA keeps of the launch's requests.
+struct Requests {
+  int start[kMaxRequests + 1];  // running sum of their tiles
+  int2 lens[kMaxRequests];      // context, query tokens
 };
 
 // Small arrays, after the operands.
 struct TileSmall {
-  int start[kMaxRequests + 1];
+  Requests q;
   float4 ring[kRing][8];  // a 16-position group's k_scale, log2(v_scale), 1 / v_scale
+  float tops[2][2][128];  // the two threads' maxima of a row, for two tiles
+  float2 ml[2][128];      // reference and sum of a thread's positions
   float row_factor[128];
   float weight[128];   // of a copy's row when the copies are summed
   int64_t out_at[128];  // element offset of a row in out
   uint32_t poison[2][4];
   int spoiled[128];    // rows that saw a NaN value
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], w_full[2], s_full[2], s_empty[2], p_full[2], pv_done[2];
-  uint64_t q_full, o_free, meet, pair[4], ring_full[kRing], ring_empty[kRing];
+  uint64_t q_full, o_free[2], meet, pair[4], ring_full[kRing], ring_empty[kRing];
   uint32_t tmem;
   int dead;
 };
-static_assert(sizeof(TileSmall) <= 5248);
+static_assert(sizeof(TileSmall) <= 12288);
 
 struct Unit {
   int b, head, row0, rows;  // request, kv head, first row, rows
@@ -102,13 +109,14 @@ __device__ __forceinline__ int request_tiles(const CacheAttendParams &P, int row
   return tiles;
 }
 
-// The unit of request b (its tiles begin at `start`, span of them) that holds tile t.
-__device__ Unit unit_of(const CacheTilePlan &A, int row_tile, int b, int start, int span, int t) {
+// The unit of request b that holds tile t.
+__device__ __forceinline__ Unit unit_of(const CacheTilePlan &A, const Requests &q, int row_tile, int b, int t) {
   const CacheAttendParams &P = A.p;
   Unit u;
   u.b = A.first + b;
-  request_lengths(P, u.b, u.base, u.n);
-  const int per_head = span / P.c.kv_heads;
+  u.base = q.lens[b].x;
+  u.n = q.lens[b].y;
+  const int start = q.start[b], per_head = (q.start[b + 1] - start) / P.c.kv_heads;
   u.head = (t - start) / per_head;
   u.tile0 = start + u.head * per_head;
   for (int rt = 0;; ++rt) {
@@ -123,14 +131,14 @@ __device__ Unit unit_of(const CacheTilePlan &A, int row_tile, int b, int start, 
   }
 }
 
-__device__ __noinline__ Unit find_unit(const CacheTilePlan &A, const int *start, int row_tile, int t) {
+__device__ __noinline__ Unit find_unit(const CacheTilePlan &A, const Requests &q, int row_tile, int t) {
   int lo = 0, hi = A.count - 1;  // the last request whose start is <= t has tiles after it: equal starts are empty requests
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
-    if (start[mid] <= t) lo = mid;
+    if (q.start[mid] <= t) lo = mid;
     else hi = mid - 1;
   }
-  return unit_of(A, row_tile, lo, start[lo], start[lo + 1] - start[lo], t);
+  return unit_of(A, q, row_tile, lo, t);
 }
 
 __device__ __forceinline__ int cut(int total, int parts, int i) {
@@ -193,12 +201,56 @@ __device__ __forceinline__ uint32_t pair_bits(float lo, float hi) {
   return r;
 }
 
+// A loading warp's way through its CTA's tiles: lane l < 8 has positions
+// [16 l, 16 l + 16) of each; this tile's and the next one's.
+struct TileWalk {
+  const CacheTilePlan &A;
+  const Requests &q;
+  int row_tile, t, hi, lane, end;
+  Unit u;
+  int pos[2], page[2], head[2];  // pos -1: past the unit's positions; page -1: none, or outside the pool
+
+  __device__ TileWalk(const CacheTilePlan &a, const Requests &r, int rt, int lo, int h, int l)
+      : A(a), q(r), row_tile(rt), t(lo), hi(h), lane(l), end(lo), u{} {}
+  __device__ __forceinline__ void advance(int slot) {
+    pos[slot] = page[slot] = -1;
+    head[slot] = 0;
+    if (t >= hi) return;
+    if (t >= end) {
+      u = find_unit(A, q, row_tile, t);
+      end = u.tile0 + u.tiles;
+    }
+    const int at = (t - u.tile0) * kTile + lane * 16;
+    head[slot] = u.head;
+    if (lane < 8 && at < u.T) {
+      pos[slot] = at;
+      page[slot] = page_at(A.p.c, u.b, at >> A.p.c.page_shift);
+    }
+    ++t;
+  }
+  __device__ __forceinline__ void shift() {
+    pos[0] = pos[1], page[0] = page[1], head[0] = head[1];
+    advance(1);
+  }
+  // the blocks' scales; 1 where there is no block
+  __device__ __forceinline__ void scales(int slot, float &k, float &v) const {
+    k = v = 1.0f;
+    if (page[slot] >= 0) {
+      const int64_t at = page[slot] * A.p.c.scale_stride + head[slot];
+      k = A.p.c.k_scale[at];
+      v = A.p.c.v_scale[at];
+    }
+  }
+};
+
 template <int DT, int D, int REPL, bool CAP>
 __global__ void __launch_bounds__(kTileThreads, 1)
     cache_attend_tile_kernel(const CacheTilePlan A, const __grid_constant__ CUtensorMap k_map) {
   using S = TileShape<DT, D>;
   constexpr int RT = 128 / REPL;        // rows to a unit
-  constexpr int OWN = kTile / REPL / 2;  // positions that a thread takes of each tile
+  constexpr int HALVES = REPL == 4 ? 1 : 2;  // warps to 32 lanes
+  constexpr int OWN = kTile / REPL / HALVES;  // positions that a thread takes of each tile
+  constexpr int kSoft = 128 * HALVES;         // softmax threads
   constexpr uint32_t kCols = 512, kO = 256, kP = 384;  // tensor memory: S at 0 and 128, O, P at 384 and 448
   extern __shared__ char raw[];
   char *const smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -216,9 +268,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       bar_init(&sm.s_empty[i], kSoft);
       bar_init(&sm.p_full[i], kSoft);
       bar_init(&sm.pv_done[i], 1);
+      bar_init(&sm.o_free[i], kSoft);
     }
     bar_init(&sm.q_full, kSoft);
-    bar_init(&sm.o_free, kSoft);
     bar_init(&sm.meet, kSoft);
     for (int i = 0; i < 4; ++i) bar_init(&sm.pair[i], 64);
     for (int i = 0; i < kRing; ++i) bar_init(&sm.ring_full[i], 32), bar_init(&sm.ring_empty[i], kSoft);
@@ -231,7 +283,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   for (int b = tid; b < A.count; b += kTileThreads) {
     int base, n;
     const bool ok = request_lengths(P, A.first + b, base, n) == SPEC_STATUS_OK;
-    sm.start[b + 1] = ok ? request_tiles(P, RT, base, n) * P.c.kv_heads : 0;
+    sm.q.lens[b] = make_int2(base, n);
+    sm.q.start[b + 1] = ok ? request_tiles(P, RT, base, n) * P.c.kv_heads : 0;
   }
   tc_fence_before();
   __syncthreads();
@@ -239,100 +292,82 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp == 0) {
     int carry = 0;
     for (int b0 = 0; b0 < A.count; b0 += 32) {
-      int x = b0 + lane < A.count ? sm.start[b0 + lane + 1] : 0;
+      int x = b0 + lane < A.count ? sm.q.start[b0 + lane + 1] : 0;
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(~0u, x, o);
         if (lane >= o) x += y;
       }
       x += carry;
       if (b0 + lane < A.count) {
-        sm.start[b0 + lane + 1] = x;
+        sm.q.start[b0 + lane + 1] = x;
         if (cta == 0) A.start[b0 + lane + 1] = x;
       }
       carry = __shfl_sync(~0u, x, 31);
     }
     if (lane == 0) {
-      sm.start[0] = 0;
+      sm.q.start[0] = 0;
       if (cta == 0) A.start[0] = 0;
     }
   }
   __syncthreads();
-  const int total = sm.start[A.count];
+  const int total = sm.q.start[A.count];
   const int lo = cut(total, ctas, cta), hi = cut(total, ctas, cta + 1);
   const uint32_t tmem = sm.tmem;
   volatile int *dead = &sm.dead;
 
   if (warp == 12) {
-    // ---- loading: a lane to a group of 16 positions (the first 8 lanes), two tiles ahead with the page table
-    const int shift = P.c.page_shift;
-    const int page_rows = A.page_rows;
-    int ahead_t = lo, ahead_end = lo;
-    Unit au{};
-    // the next tile's position of this lane's group, its request and head; -1 past the range or the unit's positions
-    int g_pos[2], g_b[2], g_head[2], g_page[2];
-    auto advance = [&](int slot) {
-      g_page[slot] = -1;
-      g_pos[slot] = -1;
-      if (ahead_t >= hi) return;
-      if (ahead_t >= ahead_end) {
-        au = find_unit(A, sm.start, RT, ahead_t);
-        ahead_end = au.tile0 + au.tiles;
-      }
-      const int pos = (ahead_t - au.tile0) * kTile + lane * 16;
-      g_b[slot] = au.b;
-      g_head[slot] = au.head;
-      if (lane < 8 && pos < au.T) {
-        g_pos[slot] = pos;
-        g_page[slot] = page_at(P.c, au.b, pos >> shift);
-      }
-      ++ahead_t;
-    };
-    float ks = 1.0f, vs = 1.0f, ks1 = 1.0f, vs1 = 1.0f;
-    auto scales = [&](int slot, float &k, float &v) {
-      k = 1.0f, v = 1.0f;
-      if (g_page[slot] >= 0) {
-        const int64_t at = g_page[slot] * P.c.scale_stride + g_head[slot];
-        k = P.c.k_scale[at];
-        v = P.c.v_scale[at];
-      }
-    };
-    advance(0);
-    advance(1);
-    scales(0, ks, vs);
-    for (int t = lo; t < hi; ++t) {
-      const int i = t - lo, cur = 0;
-      // this tile's data, and the loads of the next ones'
-      const int pos = g_pos[cur], page = g_page[cur], head = g_head[cur];
-      scales(1, ks1, vs1);
-      g_pos[0] = g_pos[1], g_b[0] = g_b[1], g_head[0] = g_head[1], g_page[0] = g_page[1];
-      advance(1);
-      const int r = i % kRing;
-      if (i >= kRing && !warp_wait(&sm.ring_empty[r], (i / kRing - 1) & 1, dead)) break;
-      if (lane < 8) sm.ring[r][lane] = make_float4(ks, log2f(vs), 1.0f / vs, 0.0f);
-      bar_arrive(&sm.ring_full[r]);
-      const bool load = pos >= 0 && page >= 0 && (pos & (page_rows - 1)) == 0;
-      const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(~0u, load)) * page_rows * D);
-      const int sk = i % S::kStagesK, sv = i % S::kStagesV;
-      if (i >= S::kStagesK && !warp_wait(&sm.k_empty[sk], (i / S::kStagesK - 1) & 1, dead)) break;
+    // ---- loading K: a lane to a group of 16 positions (the first 8 lanes), the page table two tiles ahead
+    TileWalk walk(A, sm.q, RT, lo, hi, lane);
+    walk.advance(0);
+    walk.advance(1);
+    for (int t = lo, sk = 0, lap = 0; t < hi; ++t) {
+      const int pos = walk.pos[0], page = walk.page[0], head = walk.head[0];
+      walk.shift();
+      const bool load = pos >= 0 && page >= 0 && (pos & (A.page_rows - 1)) == 0;
+      const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(~0u, load)) * A.page_rows * D);
+      if (lap > 0 && !warp_wait(&sm.k_empty[sk], (lap - 1) & 1, dead)) break;
       if (lane == 0) bar_expect(&sm.k_full[sk], bytes);
       __syncwarp();
-      const int in_page = pos & ((1 << shift) - 1), in_tile = lane * 16;
-      if (load) tensor_load_3d(smem + S::kK + sk * S::kStage + in_tile * D, &k_map, 0, (head << shift) + in_page, page, &sm.k_full[sk]);
-      if (i >= S::kStagesV && !warp_wait(&sm.v_empty[sv], (i / S::kStagesV - 1) & 1, dead)) break;
+      if (load)
+        tensor_load_3d(smem + S::kK + sk * S::kStage + lane * 16 * D, &k_map, 0,
+                       (head << P.c.page_shift) + (pos & ((1 << P.c.page_shift) - 1)), page, &sm.k_full[sk]);
+      if (++sk == S::kStagesK) sk = 0, ++lap;
+    }
+    __syncwarp();
+    if (*dead)  // the copies in flight land before the CTA leaves
+      for (int s = 0; s < S::kStagesK; ++s)
+        for (int k = 0; k < 4096 && !bar_try(&sm.k_full[s], 0) && !bar_try(&sm.k_full[s], 1); ++k) {}
+  } else if (warp == 15) {
+    // ---- loading V and the blocks' scales, likewise; the scales one tile ahead
+    TileWalk walk(A, sm.q, RT, lo, hi, lane);
+    walk.advance(0);
+    walk.advance(1);
+    float ks, vs, ks1, vs1;
+    walk.scales(0, ks, vs);
+    for (int t = lo, sv = 0, lap = 0; t < hi; ++t) {
+      const int i = t - lo, r = i % kRing;
+      const int pos = walk.pos[0], page = walk.page[0], head = walk.head[0];
+      walk.scales(1, ks1, vs1);
+      walk.shift();
+      if (i >= kRing && !warp_wait(&sm.ring_empty[r], (i / kRing - 1) & 1, dead)) break;
+      if (lane < 8) sm.ring[r][lane] = make_float4(ks, __log2f(vs), __fdividef(1.0f, vs), 0.0f);
+      bar_arrive(&sm.ring_full[r]);
+      const bool load = pos >= 0 && page >= 0 && (pos & (A.page_rows - 1)) == 0;
+      const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(~0u, load)) * A.page_rows * D);
+      if (lap > 0 && !warp_wait(&sm.v_empty[sv], (lap - 1) & 1, dead)) break;
       if (lane == 0) bar_expect(&sm.v_full[sv], bytes);
       __syncwarp();
       if (load)
-        bulk_load(smem + S::kV8 + sv * S::kStage + in_tile * D, P.c.v + block_offset(P.c, page, head) + static_cast<int64_t>(in_page) * D,
-                  page_rows * D, &sm.v_full[sv]);
+        bulk_load(smem + S::kV8 + sv * S::kStage + lane * 16 * D,
+                  P.c.v + block_offset(P.c, page, head) + static_cast<int64_t>(pos & ((1 << P.c.page_shift) - 1)) * D, A.page_rows * D,
+                  &sm.v_full[sv]);
       ks = ks1, vs = vs1;
+      if (++sv == S::kStagesV) sv = 0, ++lap;
     }
     __syncwarp();
-    if (*dead) {  // the copies in flight land before the CTA leaves
-      for (int s = 0; s < S::kStagesK; ++s)
-        for (int k = 0; k < 4096 && !bar_try(&sm.k_full[s], 0) && !bar_try(&sm.k_full[s], 1); ++k) {}
+    if (*dead)
       for (int s = 0; s < S::kStagesV; ++s)
         for (int k = 0; k < 4096 && !bar_try(&sm.v_full[s], 0) && !bar_try(&sm.v_full[s], 1); ++k) {}
-    }
   } else if (warp == 13) {
     // ---- issuing S = Q K^T
     constexpr uint32_t kId = mma_desc(kTile, false);
@@ -340,16 +375,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint64_t q_desc = matrix_desc(smem_u32(smem + S::kQ), 16, 8 * D, kSw);
     const uint64_t k_desc = matrix_desc(smem_u32(smem + S::kK), 16, 8 * D, kSw);
     int unit_end = lo, units = 0;
-    for (int t = lo; t < hi; ++t) {
-      const int i = t - lo, sk = i % S::kStagesK;
+    for (int t = lo, sk = 0, lap = 0; t < hi; ++t) {
+      const int i = t - lo;
       if (t >= unit_end) {
-        const Unit u = find_unit(A, sm.start, RT, t);
+        const Unit u = find_unit(A, sm.q, RT, t);
         unit_end = u.tile0 + u.tiles;
         if (!warp_wait(&sm.q_full, units & 1, dead)) break;
         ++units;
       }
-      if (!warp_wait(&sm.k_full[sk], (i / S::kStagesK) & 1, dead)) break;
-      if (i >= 2 && !warp_wait(&sm.s_empty[i & 1], (i / 2 - 1) & 1, dead)) break;
+      if (i >= 2) {  // S has been read, and P's columns are free: so S full says that P may be written
+        if (!warp_wait(&sm.s_empty[i & 1], (i / 2 - 1) & 1, dead)) break;
+        if (!warp_wait(&sm.pv_done[i & 1], (i / 2 - 1) & 1, dead)) break;
+      }
+      if (!warp_wait(&sm.k_full[sk], lap & 1, dead)) break;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
@@ -362,6 +400,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc_commit(&sm.s_full[i & 1]);
       }
       __syncwarp();
+      if (++sk == S::kStagesK) sk = 0, ++lap;
     }
   } else if (warp == 14) {
     // ---- issuing O += P V
@@ -372,9 +411,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int i = t - lo, w = i & 1;
       const bool fresh = t >= unit_end;
       if (fresh) {
-        const Unit u = find_unit(A, sm.start, RT, t);
+        const Unit u = find_unit(A, sm.q, RT, t);
         unit_end = u.tile0 + u.tiles;
-        if (units > 0 && !warp_wait(&sm.o_free, (units - 1) & 1, dead)) break;
+        if (units > 0 && !warp_wait(&sm.o_free[(units - 1) & 1], (units - 1) >> 1 & 1, dead)) break;
         ++units;
       }
       if (!warp_wait(&sm.w_full[w], (i >> 1) & 1, dead)) break;
@@ -406,16 +445,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr int kLanes = D / 16;        // lanes to a position
     constexpr int kPer = 32 / kLanes;     // positions to a step
     const int piece = lane % kLanes, sub = lane / kLanes;
-    for (int t = lo; t < hi; ++t) {
-      const int i = t - lo, sv = i % S::kStagesV, w = i & 1;
+    int unit = -1, ended1 = -1, ended2 = -1;  // this unit's number; the unit that tile i - 1, i - 2 closed, or -1
+    for (int t = lo, sv = 0, lap = 0; t < hi; ++t) {
+      const int i = t - lo, w = i & 1;
       if (t >= unit_end) {
-        u = find_unit(A, sm.start, RT, t);
+        u = find_unit(A, sm.q, RT, t);
         unit_end = u.tile0 + u.tiles;
+        ++unit;
       }
       const int pos0 = (t - u.tile0) * kTile;
       const bool edge = pos0 + kTile > u.base;
-      if (!warp_wait(&sm.v_full[sv], (i / S::kStagesV) & 1, dead)) break;
       if (i >= 2 && !warp_wait(&sm.pv_done[w], (i / 2 - 1) & 1, dead)) break;
+      // (a unit that ends sums its copies in the halves of its last tile, two tiles before the ones to replace them)
+      if (REPL > 1 && ended2 >= 0 && !warp_wait(&sm.o_free[ended2 & 1], ended2 >> 1 & 1, dead)) break;
+      ended2 = ended1;
+      ended1 = t + 1 == unit_end ? unit : -1;
+      if (!warp_wait(&sm.v_full[sv], lap & 1, dead)) break;
       const char *src = smem + S::kV8 + sv * S::kStage;
       char *dst = smem + S::kV16 + w * 2 * S::kStage;
       uint32_t poison = 0;
@@ -474,17 +519,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       fence_async_shared();
       bar_arrive(&sm.v_empty[sv]);
       bar_arrive(&sm.w_full[w]);
+      if (++sv == S::kStagesV) sv = 0, ++lap;
     }
-  } else {
-    // ---- softmax: two threads to a row (of its copy), each with OWN positions of each tile
+  } else if (warp < 4 * HALVES) {
+    // ---- softmax: one or two threads to a row (of its copy), each with OWN positions of each tile
     const int half = warp >> 2, quarter = warp & 3;
     const int spot = quarter * 32 + lane;                  // lane of tensor memory
     const int copy = spot / RT, r = spot % RT;             // which copy of the rows, and the row
-    const int col0 = copy * 2 * OWN + half * OWN;          // its positions in the tile
+    const int col0 = (copy * HALVES + half) * OWN;          // its positions in the tile
     const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
     if (REPL > 1) {
       const uint32_t zero[16] = {};
-      for (int c = 0; c < 64; c += 16) tmem_st16(tmem + lanes + kP + half * 64 + c, zero);
+      for (int c = half * 64; c < 64 * (HALVES == 1 ? 2 : half + 1); c += 16) tmem_st16(tmem + lanes + kP + c, zero);
       tc_wait_st();
       tc_fence_before();
     }
@@ -497,14 +543,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     // A unit's rows of q as e4m3 pieces; every earlier score product that reads them has completed.
     auto write_q = [&](const Unit &u) {
-      constexpr int kEach = D / 32;  // elements to a lane
+      constexpr int kEach = D / 32, kWarpsQ = 4 * HALVES;  // elements to a lane
 #pragma unroll 1
-      for (int first = warp; first < u.rows; first += 32) {
+      for (int first = warp; first < u.rows; first += 4 * kWarpsQ) {
         float x[4][kEach];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int row = u.row0 + first + 8 * k;
-          if (first + 8 * k < u.rows) {
+          const int row = u.row0 + first + kWarpsQ * k;
+          if (first + kWarpsQ * k < u.rows) {
             const char *q = P.q + (u.b * P.qs[0] + row / P.group * P.qs[1] + (u.head * P.group + row % P.group) * P.qs[2]) * 2;
             if (A.q_vec) load_each<DT, kEach>(q, lane, x[k]);
             else
@@ -514,7 +560,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int r0 = first + 8 * k;
+          const int r0 = first + kWarpsQ * k;
           if (r0 >= u.rows) break;
           float top = 0.0f;
 #pragma unroll
@@ -554,12 +600,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       bar_arrive(&sm.q_full);
       return together();
     };
-    float *tops = reinterpret_cast<float *>(smem + S::kFold);                 // [2 tiles][2 halves][128]
-    float2 *mls = reinterpret_cast<float2 *>(smem + S::kFold + 4096);         // [2 halves][128]
-    float *fold = reinterpret_cast<float *>(smem + S::kFold) + half * 128 * 12;  // (after the unit's last tile)
+    int unit = 0;
     Unit next{};
     if (lo < hi) {
-      next = find_unit(A, sm.start, RT, lo);
+      next = find_unit(A, sm.q, RT, lo);
       ok = write_q(next);
     }
     for (int t = lo; t < hi && ok;) {
@@ -627,10 +671,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           top = fmaxf(top, fmaf(high, CAP ? 1.0f : fmaxf(factor * sc[g].x, 1.2e-38f), sc[g].y));
         }
         // the two threads of a row agree on its maximum
-        tops[(sb * 2 + half) * 128 + spot] = top;
-        bar_arrive(&sm.pair[quarter]);
-        if (!(ok = warp_wait(&sm.pair[quarter], pairings++ & 1, dead))) break;
-        top = fmaxf(top, tops[(sb * 2 + 1 - half) * 128 + spot]);
+        if (HALVES == 2) {
+          sm.tops[sb][half][spot] = top;
+          bar_arrive(&sm.pair[quarter]);
+          if (!(ok = warp_wait(&sm.pair[quarter], pairings++ & 1, dead))) break;
+          top = fmaxf(top, sm.tops[sb][1 - half][spot]);
+        }
         // the reference, and O with it when it moves
         const bool moves = live && top > m + 8.0f;
         if (__any_sync(~0u, moves)) {
@@ -643,7 +689,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (!(ok = warp_wait(&sm.pv_done[done & 1], (done >> 1) & 1, dead))) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+            for (int c = half * (D / HALVES); c < (half + 1) * (D / HALVES); c += 16) {
               float o[16];
               tmem_ld16(tmem + lanes + kO + c, o);
               tc_wait_ld();
@@ -669,8 +715,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           sum = fmaf((part[0] + part[1]) + (part[2] + part[3]), sc[g].z, sum);
         }
-        if (i >= 2 && !(ok = warp_wait(&sm.pv_done[sb], (i / 2 - 1) & 1, dead))) break;  // P's columns are free
-        tc_fence_after();
         if (OWN == 16) tmem_st8(tmem + lanes + kP + sb * 64 + col0 / 2, p);
 #pragma unroll
         for (int c = 0; c + 16 <= OWN / 2; c += 16) tmem_st16(tmem + lanes + kP + sb * 64 + col0 / 2 + c, p + c);
@@ -691,22 +735,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!ok) break;
 
       if (t < hi) {  // the next unit's q, while this one's last values are being summed
-        next = find_unit(A, sm.start, RT, t);
+        next = find_unit(A, sm.q, RT, t);
         if (!(ok = write_q(next))) break;
-      } else if (!(ok = together())) break;  // (tops has been read)
+      }
       // The unit's end in this CTA: the rows' sums over copies and halves, and what each copy's O is multiplied by.
       const bool whole = lo <= u.tile0 && t == u.tile0 + u.tiles;
       const int slot = cta * 2 + (max(lo, u.tile0) != lo ? 1 : 0);
-      mls[half * 128 + spot] = make_float2(m, sum);
+      sm.ml[half][spot] = make_float2(m, sum);
       if (!(ok = together())) break;
       if (tid < u.rows) {
         float m_all = -INFINITY, l_all = 0.0f;
 #pragma unroll
-        for (int c = 0; c < REPL; ++c) m_all = fmaxf(m_all, mls[c * RT + tid].x);
+        for (int c = 0; c < REPL; ++c) m_all = fmaxf(m_all, sm.ml[0][c * RT + tid].x);
         const float ref = m_all == -INFINITY ? 0.0f : m_all;
 #pragma unroll
         for (int c = 0; c < REPL; ++c)
-          l_all += (mls[c * RT + tid].y + mls[128 + c * RT + tid].y) * ex2(mls[c * RT + tid].x - ref);
+          l_all += (sm.ml[0][c * RT + tid].y + (HALVES == 2 ? sm.ml[1][c * RT + tid].y : 0.0f)) * ex2(sm.ml[0][c * RT + tid].x - ref);
         float norm = 1.0f;
         const int row = u.row0 + tid, tok = row / P.group, h = u.head * P.group + row % P.group;
         if (whole) {
@@ -720,7 +764,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (sm.spoiled[tid]) norm = NAN;
         sm.spoiled[tid] = 0;
 #pragma unroll
-        for (int c = 0; c < REPL; ++c) sm.weight[c * RT + tid] = norm * ex2(mls[c * RT + tid].x - ref);
+        for (int c = 0; c < REPL; ++c) sm.weight[c * RT + tid] = norm * ex2(sm.ml[0][c * RT + tid].x - ref);
       }
       const int last = t - 1 - lo;
       if (!(ok = warp_wait(&sm.pv_done[last & 1], (last >> 1) & 1, dead))) break;
@@ -739,38 +783,52 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           *reinterpret_cast<float4 *>(A.part + (static_cast<int64_t>(slot) * RT + rr) * D + c) = y;
         }
       };
+      if (REPL == 1) {
 #pragma unroll 1
-      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 8) {
-        float o[8];
-        tmem_ld8(tmem + lanes + kO + c, o);
-        tc_wait_ld();
+        for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+          float o[16];
+          tmem_ld16(tmem + lanes + kO + c, o);
+          tc_wait_ld();
+          if (live)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] *= w_own;
-        if (REPL == 1) {
-          if (live) {
-            put4(r, c, make_float4(o[0], o[1], o[2], o[3]));
-            put4(r, c + 4, make_float4(o[4], o[5], o[6], o[7]));
+            for (int e = 0; e < 16; e += 4) put4(r, c + e, make_float4(o[e] * w_own, o[e + 1] * w_own, o[e + 2] * w_own, o[e + 3] * w_own));
+        }
+      } else {
+        // 64 columns at a time, over the halves of the last tile (its product is done): [128][16 chunks of 4], swizzled by the row
+        float4 *fold = reinterpret_cast<float4 *>(smem + S::kV16 + (last & 1) * 2 * S::kStage);
+        constexpr int kFoldCols = D == 128 ? 64 : 32;
+        constexpr int kChunks = kFoldCols / 4;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += kFoldCols) {
+          if (c0 > 0 && !(ok = together())) break;  // the columns before have been read
+#pragma unroll 1
+          for (int c = half * (kFoldCols / HALVES); c < (half + 1) * (kFoldCols / HALVES); c += 16) {
+            float o[16];
+            tmem_ld16(tmem + lanes + kO + c0 + c, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              fold[spot * kChunks + ((c / 4 + e) ^ (spot & (kChunks - 1)))] =
+                  make_float4(o[4 * e] * w_own, o[4 * e + 1] * w_own, o[4 * e + 2] * w_own, o[4 * e + 3] * w_own);
           }
-        } else {
-          if (!(ok = together())) break;  // the columns before have been read
-          *reinterpret_cast<float4 *>(fold + spot * 12) = make_float4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<float4 *>(fold + spot * 12 + 4) = make_float4(o[4], o[5], o[6], o[7]);
           if (!(ok = together())) break;
-          const int rr = spot >> 1, at = (spot & 1) * 4;
-          if (rr < u.rows) {
-            float4 y = *reinterpret_cast<const float4 *>(fold + rr * 12 + at);
+          for (int x = tid; x < u.rows * kChunks; x += kSoft) {
+            const int rr = x / kChunks, chunk = x % kChunks;
+            float4 y = fold[rr * kChunks + (chunk ^ (rr & (kChunks - 1)))];
 #pragma unroll
             for (int k = 1; k < REPL; ++k) {
-              const float4 z = *reinterpret_cast<const float4 *>(fold + (k * RT + rr) * 12 + at);
+              const int row = k * RT + rr;
+              const float4 z = fold[row * kChunks + (chunk ^ (row & (kChunks - 1)))];
               y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
             }
-            put4(rr, c + at, y);
+            put4(rr, c0 + chunk * 4, y);
           }
         }
       }
       if (!ok) break;
       tc_fence_before();
-      bar_arrive(&sm.o_free);
+      bar_arrive(&sm.o_free[unit & 1]);
+      ++unit;
       ok = together();  // the shared arrays have been read
     }
   }

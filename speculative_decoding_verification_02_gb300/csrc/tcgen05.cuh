@@ -34,23 +34,22 @@ __device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Waits for the phase of this parity to complete, for a bounded number of
-// tries (each of which the hardware may suspend for about a microsecond);
-// when they run out, or another thread of the CTA gave up before, *dead is set
-// and the answer is false: the caller leaves its loop.
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *dead) {
-  if (bar_try(bar, parity)) return true;
+// A whole warp waits for the phase of this parity to complete, for a bounded
+// number of tries (each of which the hardware may suspend for about a
+// microsecond); when they run out, or another warp of the CTA gave up before,
+// *dead is set and the answer, one for all lanes, is false: the caller leaves
+// its loop.
+static __device__ __noinline__ bool warp_wait_long(uint64_t *bar, uint32_t parity, volatile int *dead) {
   for (int i = 0; i < (1 << 18); ++i) {
-    if (bar_try(bar, parity)) return true;
-    if (*dead) return false;
+    if (__all_sync(~0u, bar_try(bar, parity))) return true;
+    if (__any_sync(~0u, *dead)) return false;
   }
   *dead = 1;
   return false;
 }
-
-// The same by a whole warp, with one answer for its lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *dead) {
-  return __all_sync(~0u, bar_wait(bar, parity, dead));
+  if (__all_sync(~0u, bar_try(bar, parity))) return true;
+  return warp_wait_long(bar, parity, dead);
 }
 
 // ---------------------------------------------------------------- copies
