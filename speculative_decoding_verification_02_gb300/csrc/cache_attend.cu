@@ -118,7 +118,7 @@ int requests_at_once(const CacheAttendParams &P) {
   const int rt = 128 / copies_of(P.N, P.group);
   const int64_t row_tiles = (static_cast<int64_t>(P.N) * P.group + rt - 1) / rt;
   const int64_t tiles = ((static_cast<int64_t>(P.c.table_stride) << P.c.page_shift) / kTilePositions + 1) * row_tiles * P.c.kv_heads;
-  return static_cast<int>(std::min<int64_t>(kTileRequests, 2000000000LL / tiles));
+  return static_cast<int>(std::min<int64_t>(kTileRequests, 2000000000LL / std::max(tiles, row_tiles * rt * P.c.kv_heads)));
 }
 
 size_t lay_out(CacheTilePlan &A, char *ws, int D) {
@@ -131,7 +131,7 @@ size_t lay_out(CacheTilePlan &A, char *ws, int D) {
   };
   A.start = reinterpret_cast<int *>(take(sizeof(int) * (kTileRequests + 1)));
   A.verdict = reinterpret_cast<int *>(take(sizeof(int) * kTileRequests));
-  A.dead = reinterpret_cast<int *>(take(sizeof(int) * ctas));
+  A.range = reinterpret_cast<int2 *>(take(sizeof(int2) * ctas));
   A.ml = reinterpret_cast<float2 *>(take(sizeof(float2) * 2 * ctas * rt));
   A.part = reinterpret_cast<float *>(take(sizeof(float) * 2 * ctas * rt * D));
   return off;

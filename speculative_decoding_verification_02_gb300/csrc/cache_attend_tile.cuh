@@ -43,7 +43,11 @@ namespace {
 
 constexpr int kTile = 128;         // positions to a tile
 constexpr int kMaxRequests = kTileRequests;
-constexpr int kTileThreads = 512;  // 8 softmax warps (4 of them idle with four copies), 4 widening V, 2 loading, 2 issuing
+// 8 softmax warps (4 of them idle with four copies), 4 widening V, 2 loading, 2
+// issuing.  A warp's scheduler is its number modulo 4: the widening warps share
+// two of them and the others the other two, so a scheduler runs few different
+// loops (their instructions compete for its cache).
+constexpr int kTileThreads = 512;
 constexpr int kRing = 8;           // tiles whose scales are held
 
 template <int DT, int D>
@@ -158,9 +162,11 @@ __device__ __noinline__ uint32_t row_sees(const uint8_t *mask, int token, int n,
     return most >= 32 ? ~0u : most <= 0 ? 0u : (1u << most) - 1;
   }
   uint32_t bits = 0;
+#pragma unroll
   for (int e = 0; e < 32; ++e) {
     const int j = j0 + e;
-    if (j < 0 || (j < n && mask[j] != 0)) bits |= 1u << e;
+    const uint8_t x = j >= 0 && j < n ? __ldg(mask + j) : 0;
+    bits |= j < 0 || x ? 1u << e : 0u;
   }
   return bits;
 }
@@ -278,7 +284,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     sm.dead = 0;
   }
   if (tid < 128) sm.spoiled[tid] = 0;
-  if (warp == 13) tmem_alloc(&sm.tmem, kCols);
+  if (warp == 14) tmem_alloc(&sm.tmem, kCols);
   // Every request's tiles, then their running sum.
   for (int b = tid; b < A.count; b += kTileThreads) {
     int base, n;
@@ -315,7 +321,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t tmem = sm.tmem;
   volatile int *dead = &sm.dead;
 
-  if (warp == 12) {
+  if (warp == 10) {
     // ---- loading K: a lane to a group of 16 positions (the first 8 lanes), the page table two tiles ahead
     TileWalk walk(A, sm.q, RT, lo, hi, lane);
     walk.advance(0);
@@ -337,7 +343,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (*dead)  // the copies in flight land before the CTA leaves
       for (int s = 0; s < S::kStagesK; ++s)
         for (int k = 0; k < 4096 && !bar_try(&sm.k_full[s], 0) && !bar_try(&sm.k_full[s], 1); ++k) {}
-  } else if (warp == 15) {
+  } else if (warp == 11) {
     // ---- loading V and the blocks' scales, likewise; the scales one tile ahead
     TileWalk walk(A, sm.q, RT, lo, hi, lane);
     walk.advance(0);
@@ -368,7 +374,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (*dead)
       for (int s = 0; s < S::kStagesV; ++s)
         for (int k = 0; k < 4096 && !bar_try(&sm.v_full[s], 0) && !bar_try(&sm.v_full[s], 1); ++k) {}
-  } else if (warp == 13) {
+  } else if (warp == 14) {
     // ---- issuing S = Q K^T
     constexpr uint32_t kId = mma_desc(kTile, false);
     constexpr uint64_t kSw = D == 128 ? kSwizzle128 : kSwizzle64;
@@ -383,10 +389,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (!warp_wait(&sm.q_full, units & 1, dead)) break;
         ++units;
       }
-      if (i >= 2) {  // S has been read, and P's columns are free: so S full says that P may be written
-        if (!warp_wait(&sm.s_empty[i & 1], (i / 2 - 1) & 1, dead)) break;
-        if (!warp_wait(&sm.pv_done[i & 1], (i / 2 - 1) & 1, dead)) break;
-      }
+      if (i >= 2 && !warp_wait(&sm.s_empty[i & 1], (i / 2 - 1) & 1, dead)) break;
       if (!warp_wait(&sm.k_full[sk], lap & 1, dead)) break;
       tc_fence_after();
       if (elect_one()) {
@@ -402,7 +405,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       __syncwarp();
       if (++sk == S::kStagesK) sk = 0, ++lap;
     }
-  } else if (warp == 14) {
+  } else if (warp == 15) {
     // ---- issuing O += P V
     constexpr uint32_t kId = mma_desc(D, true);
     const uint64_t v_desc = matrix_desc(smem_u32(smem + S::kV16), kTile * 128, 1024, kSwizzle128);
@@ -429,14 +432,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp >= 8) {
     // ---- widening V: 16 bytes of a position to 16 halves, in the MN-major layout of the operand
-    const int w4 = warp - 8;
+    const int w4 = (warp >> 1 & 2) | (warp & 1), wide = w4 * 32 + lane;  // warps 8, 9, 12, 13
     for (int b = cta; b < A.count; b += ctas) {  // and, on the way, the page tables: a request with a bad page gives nothing
       int base, n;
       int st = request_lengths(P, A.first + b, base, n);
       int bad = 0;
       if (st == SPEC_STATUS_OK)
-        for (int j = tid - 256; static_cast<int64_t>(j) << P.c.page_shift < base + n; j += 128) bad |= page_at(P.c, A.first + b, j) < 0;
-      if (tid == 256) A.verdict[b] = st;
+        for (int j = wide; static_cast<int64_t>(j) << P.c.page_shift < base + n; j += 128) bad |= page_at(P.c, A.first + b, j) < 0;
+      if (wide == 0) A.verdict[b] = st;
       asm volatile("bar.sync 2, 128;" ::: "memory");
       if (bad) A.verdict[b] = SPEC_STATUS_BAD_PAGE;
     }
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         *reinterpret_cast<uint4 *>(to + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? h[0] : h[1];
       };
       constexpr int kSteps = 32 / kPer;
-      if (!edge) {
+      if (!edge) [[likely]] {
 #pragma unroll 1
         for (int step = 0; step < kSteps; step += 4) {
           uint4 x[4];
@@ -546,54 +549,68 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       constexpr int kEach = D / 32, kWarpsQ = 4 * HALVES;  // elements to a lane
 #pragma unroll 1
       for (int first = warp; first < u.rows; first += 4 * kWarpsQ) {
-        float x[4][kEach];
+        float x[4][kEach], top[4];
+        int ex[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = u.row0 + first + kWarpsQ * k;
-          if (first + kWarpsQ * k < u.rows) {
-            const char *q = P.q + (u.b * P.qs[0] + row / P.group * P.qs[1] + (u.head * P.group + row % P.group) * P.qs[2]) * 2;
-            if (A.q_vec) load_each<DT, kEach>(q, lane, x[k]);
-            else
+        for (int k = 0; k < 4; ++k) {  // (rows past the last one repeat it)
+          const int row = u.row0 + min(first + kWarpsQ * k, u.rows - 1), tok = row / P.group;
+          const char *q = P.q + (u.b * P.qs[0] + tok * P.qs[1] + (u.head * P.group + row - tok * P.group) * P.qs[2]) * 2;
+          if (A.q_vec) load_each<DT, kEach>(q, lane, x[k]);
+          else
 #pragma unroll
-              for (int e = 0; e < kEach; ++e) x[k][e] = row_value<DT>(q, lane * kEach + e);
-          }
+            for (int e = 0; e < kEach; ++e) x[k][e] = row_value<DT>(q, lane * kEach + e);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int r0 = first + kWarpsQ * k;
-          if (r0 >= u.rows) break;
-          float top = 0.0f;
+          top[k] = 0.0f;
 #pragma unroll
           for (int e = 0; e < kEach; ++e) {
             if (negative) x[k][e] = -x[k][e];
-            top = fmaxf(top, finite_abs(x[k][e]));
+            top[k] = fmaxf(top[k], finite_abs(x[k][e]));
           }
-          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], __shfl_xor_sync(~0u, top[k], o));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
           // 2^ex with top / 2^ex in [128, 256)
-          const int ex = top > 0.0f ? max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 7, -110) : 0;
-          const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+          ex[k] = top[k] > 0.0f ? max(static_cast<int>(__float_as_uint(top[k]) >> 23) - 127 - 7, -110) : 0;
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - ex[k]) << 23);
 #pragma unroll
           for (int e = 0; e < kEach; ++e) x[k][e] *= down;
+        }
 #pragma unroll
-          for (int piece = 0; piece < S::kPieces; ++piece) {
-            uint32_t code = 0;
+        for (int piece = 0; piece < S::kPieces; ++piece) {
+          uint32_t code[4] = {};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
             for (int e = 0; e < kEach; e += 2) {
               const uint32_t two = to_e4m3x2(x[k][e], x[k][e + 1]);
               const float2 back = e4m3x2_to_float2(two);
               x[k][e] -= back.x;
               x[k][e + 1] -= back.y;
-              code |= two << (8 * e);
+              code[k] |= two << (8 * e);
             }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r0 = first + kWarpsQ * k;
+            if (r0 >= u.rows) continue;
 #pragma unroll
             for (int c = 0; c < REPL; ++c) {
               const int a = c * RT + r0;
               char *to = smem + S::kQ + piece * kTile * D + a * D + (swizzled<D>(a, lane * kEach >> 4) << 4) + (lane * kEach & 15);
-              if (kEach == 4) *reinterpret_cast<uint32_t *>(to) = code;
-              else *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(code);
+              if (kEach == 4) *reinterpret_cast<uint32_t *>(to) = code[k];
+              else *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(code[k]);
             }
           }
-          if (lane == 0) sm.row_factor[r0] = fmaxf(fabsf(P.scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(ex + 127) << 23), 1e-30f);
+        }
+        const int mine = first + kWarpsQ * lane;
+        if (lane < 4 && mine < u.rows) {
+          const int e = lane == 0 ? ex[0] : lane == 1 ? ex[1] : lane == 2 ? ex[2] : ex[3];
+          sm.row_factor[mine] = fmaxf(fabsf(P.scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(e + 127) << 23), 1e-30f);
         }
       }
       fence_async_shared();
@@ -653,7 +670,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
         uint32_t sees[(OWN + 31) / 32];
-        if (edge) {  // (the factor below is never 0, so -inf stays -inf)
+        if (edge) [[unlikely]] {  // (the factor below is never 0, so -inf stays -inf)
 #pragma unroll
           for (int c = 0; c < (OWN + 31) / 32; ++c) {
             sees[c] = live ? row_sees(mask, token, u.n, pos0 + c * 32 - u.base) : 0;
@@ -679,7 +696,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         // the reference, and O with it when it moves
         const bool moves = live && top > m + 8.0f;
-        if (__any_sync(~0u, moves)) {
+        if (__any_sync(~0u, moves)) [[unlikely]] {
           const float next_m = moves ? top : m;
           const float keep = m == -INFINITY ? 0.0f : ex2(m - next_m);
           m = next_m;
@@ -715,10 +732,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           sum = fmaf((part[0] + part[1]) + (part[2] + part[3]), sc[g].z, sum);
         }
+        if (i >= 2 && !(ok = warp_wait(&sm.pv_done[sb], (i / 2 - 1) & 1, dead))) break;  // P's columns are free
+        tc_fence_after();
         if (OWN == 16) tmem_st8(tmem + lanes + kP + sb * 64 + col0 / 2, p);
 #pragma unroll
         for (int c = 0; c + 16 <= OWN / 2; c += 16) tmem_st16(tmem + lanes + kP + sb * 64 + col0 / 2 + c, p + c);
-        if (edge) {  // a row that sees a position whose V was NaN
+        if (edge) [[unlikely]] {  // a row that sees a position whose V was NaN
           if (!(ok = warp_wait(&sm.w_full[sb], (i >> 1) & 1, dead))) break;
           uint32_t bad = 0;
 #pragma unroll
@@ -835,8 +854,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc_fence_before();
   __syncthreads();
   pdl_launch_dependents();
-  if (tid == 0) A.dead[cta] = sm.dead;
-  if (warp == 13) {
+  if (tid == 0) A.range[cta] = make_int2(lo, sm.dead);
+  if (warp == 14) {
     tc_fence_after();
     tmem_free(tmem, kCols);
   }
@@ -848,66 +867,75 @@ template <int DT, int D>
 __global__ void __launch_bounds__(256) cache_attend_merge_kernel(const CacheTilePlan A, int row_tile, int ctas) {
   const CacheAttendParams &P = A.p;
   const int lane = threadIdx.x & 31;
-  const int64_t x = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  pdl_wait();
-  if (x >= static_cast<int64_t>(A.count) * P.N * P.Hq) return;
-  const int h = static_cast<int>(x % P.Hq), i = static_cast<int>(x / P.Hq % P.N), bl = static_cast<int>(x / P.Hq / P.N);
+  const int x = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (x >= A.count * P.N * P.Hq) return;
+  const int bl = x / (P.N * P.Hq), y = x - bl * (P.N * P.Hq), i = y / P.Hq, h = y - i * P.Hq, head = h / P.group;
   const int b = A.first + bl;
-  int st = A.verdict[bl];
-  int gone = 0;
-  for (int c = lane; c < ctas; c += 32) gone |= A.dead[c];
-  if (__any_sync(~0u, gone)) st = SPEC_STATUS_TIMEOUT;
-  if (P.status && i == 0 && h == 0 && lane == 0) P.status[b] = st;
   constexpr int kEach = D / 32;
   char *out = P.out + (b * P.os[0] + i * P.os[1] + h * P.os[2]) * 2;
   const int64_t at_lse = (static_cast<int64_t>(b) * P.N + i) * P.Hq + h;
   int base, n;
   request_lengths(P, b, base, n);
+  pdl_wait();
+  // everything the row's place depends on, in one round of loads
+  int st = A.verdict[bl];
+  const int start = A.start[bl], span = A.start[bl + 1] - start;
+  const int row = i * P.group + h - head * P.group, rt = row / row_tile, r = row - rt * row_tile;
+  int tile0 = start + head * (span / P.c.kv_heads);
+  for (int k = 0; k < rt; ++k) tile0 += (unit_positions(base, n, P.group, row_tile, k, P.mask != nullptr) + kTile - 1) / kTile;
+  const int tiles = (unit_positions(base, n, P.group, row_tile, rt, P.mask != nullptr) + kTile - 1) / kTile;
+  // the CTAs whose ranges the unit meets: the last that begins at or before its first tile, and at or before its last
+  int c0 = -1, c1 = -1;
+  bool gone = false;
+  for (int c = lane; c - lane < ctas; c += 32) {
+    const int2 cut_dead = c < ctas ? A.range[c] : make_int2(0x7fffffff, 0);
+    gone |= cut_dead.y != 0;
+    c0 += __popc(__ballot_sync(~0u, cut_dead.x <= tile0));
+    c1 += __popc(__ballot_sync(~0u, cut_dead.x < tile0 + tiles));
+  }
+  if (__any_sync(~0u, gone)) st = SPEC_STATUS_TIMEOUT;
+  if (P.status && i == 0 && h == 0 && lane == 0) P.status[b] = st;
   if (st != SPEC_STATUS_OK || i >= n) {
     for (int e = 0; e < kEach; ++e) put_value<DT>(out, lane * kEach + e, 0.0f);
     if (lane == 0 && P.lse) P.lse[at_lse] = -INFINITY;
     return;
   }
-  // the row's unit, and the CTAs whose ranges it meets
-  const int total = A.start[A.count], start = A.start[bl], span = A.start[bl + 1] - start;
-  const int head = h / P.group, row = i * P.group + h % P.group, rt = row / row_tile, r = row % row_tile;
-  int tile0 = start + head * (span / P.c.kv_heads);
-  for (int k = 0; k < rt; ++k) tile0 += (unit_positions(base, n, P.group, row_tile, k, P.mask != nullptr) + kTile - 1) / kTile;
-  const int tiles = (unit_positions(base, n, P.group, row_tile, rt, P.mask != nullptr) + kTile - 1) / kTile;
-  int c0 = static_cast<int>(static_cast<int64_t>(tile0) * ctas / total);
-  while (cut(total, ctas, c0 + 1) <= tile0) ++c0;
-  int c1 = c0;
-  while (cut(total, ctas, c1 + 1) < tile0 + tiles) ++c1;
   if (c0 == c1) return;
-  auto slot_of = [&](int c) {
-    const int s = c * 2 + (c == c0 && cut(total, ctas, c) < tile0 ? 1 : 0);
-    return static_cast<int64_t>(s) * row_tile + r;
-  };
-  auto has = [&](int c) { return cut(total, ctas, c + 1) > cut(total, ctas, c); };
-  float m = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32)
-    if (has(c)) m = fmaxf(m, A.ml[slot_of(c)].x);
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-  const float ref = m == -INFINITY ? 0.0f : m;
-  float acc[kEach] = {}, sum = 0.0f;
+  float m = -INFINITY, acc[kEach] = {}, sum = 0.0f;
   for (int cc = c0; cc <= c1; cc += 32) {
+    // a lane to a CTA: where it left the row, its reference and sum (slot 1 when the unit began inside its range)
     const int c = cc + lane;
-    float w = 0.0f, l = 0.0f;
-    int64_t s = 0;
-    if (c <= c1 && has(c)) {
-      s = slot_of(c);
-      const float2 ml = A.ml[s];
-      w = ex2(ml.x - ref);
-      l = ml.y * w;
+    int slot = -1;
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (c <= c1) {
+      const int from = A.range[c].x;
+      if (c == c1 || A.range[c + 1].x > from) {
+        slot = (c * 2 + (c == c0 && from < tile0 ? 1 : 0)) * row_tile + r;
+        ml = A.ml[slot];
+      }
     }
-    sum += warp_sum(l);
+    float top = ml.x;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    top = fmaxf(m, top);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    const float w = ex2(ml.x - ref), keep = ex2(m - ref);
+    m = top;
+    sum = sum * keep + warp_sum(ml.y * w);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) acc[e] *= keep;
     const int here = min(32, c1 - cc + 1);
+#pragma unroll 8
     for (int k = 0; k < here; ++k) {
       const float wk = __shfl_sync(~0u, w, k);
-      const float *o = A.part + __shfl_sync(~0u, s, k) * D + lane * kEach;
-      if (!has(cc + k)) continue;
+      const int sk = __shfl_sync(~0u, slot, k);
+      if (sk < 0) continue;
+      const float *o = A.part + static_cast<int64_t>(sk) * D + lane * kEach;
 #pragma unroll
-      for (int e = 0; e < kEach; ++e) acc[e] = fmaf(o[e], wk, acc[e]);
+      for (int e = 0; e < kEach; e += 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(o + e);
+        acc[e] = fmaf(v.x, wk, acc[e]);
+        acc[e + 1] = fmaf(v.y, wk, acc[e + 1]);
+      }
     }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;

@@ -48,7 +48,7 @@ static __device__ __noinline__ bool warp_wait_long(uint64_t *bar, uint32_t parit
   return false;
 }
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *dead) {
-  if (__all_sync(~0u, bar_try(bar, parity))) return true;
+  if (__all_sync(~0u, bar_try(bar, parity))) [[likely]] return true;
   return warp_wait_long(bar, parity, dead);
 }
 
