@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import NamedTuple
 
@@ -510,15 +511,19 @@ class KVCache(NamedTuple):
     v_scale: torch.Tensor
 
 
-class _CacheStruct(ctypes.Structure):
+class _CacheStruct(ctypes.Structure):  # struct spec_cache
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
                 ("page_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int32)]
 
 
-_Strides3 = ctypes.c_int64 * 3
-_Strides2 = ctypes.c_int64 * 2
+# The same struct, and strides, as packed bytes: a third of the time of a ctypes object, which counts in calls of a few
+# microseconds on the GPU.
+_pack_cache = struct.Struct("@PPPPqqiiiiPi4x").pack
+_pack3 = struct.Struct("@qqq").pack
+_pack2 = struct.Struct("@qq").pack
+_F8 = torch.float8_e4m3fn
 _ROW_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
 
 
@@ -529,41 +534,42 @@ def spec_cache_new(pages: int, kv_heads: int, page_size: int, head_dim: int, dev
     return KVCache(k, v, torch.ones(shape[:2], device=device), torch.ones(shape[:2], device=device))
 
 
-def _cache_struct(cache, table, B, name="cache"):
+def _cache_struct(cache, table, B, dev, name="cache"):
+    """(packed struct spec_cache, kv_heads, page_size, head_dim)"""
     k, v, ks, vs = cache
-    dev = k.device
-    if k.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn or ks.dtype != torch.float32 or vs.dtype != torch.float32:
+    if k.dtype is not _F8 or v.dtype is not _F8 or ks.dtype is not torch.float32 or vs.dtype is not torch.float32:
         raise TypeError(f"{name}: k and v must be float8_e4m3fn and their scales float32")
-    shape, st = k.shape, k.stride()
-    if len(shape) != 4 or v.shape != shape or v.stride() != st or ks.shape != shape[:2] or vs.shape != shape[:2]:
+    shape, st, ss = k.shape, k.stride(), ks.stride()
+    if len(shape) != 4 or v.shape != shape or v.stride() != st or ks.shape != shape[:2] or vs.shape != ks.shape:
         raise ValueError(f"{name}: k and v must be [pages, kv_heads, page_size, head_dim] alike, their scales [pages, kv_heads]")
     n, H, P, D = shape
-    if st[3] != 1 or st[2] != D or (H > 1 and st[1] != P * D) or ks.stride() != vs.stride() or (H > 1 and ks.stride(1) != 1):
+    if st[3] != 1 or st[2] != D or (H > 1 and st[1] != P * D) or vs.stride() != ss or (H > 1 and ss[1] != 1):
         raise ValueError(f"{name}: the heads of a page must lie side by side")
-    if not k.is_cuda or v.device != dev or ks.device != dev or vs.device != dev:
-        raise ValueError(f"{name} must live on one CUDA device")
-    if table.dtype != torch.int32 or table.device != dev or table.dim() != 2 or table.shape[0] != B or not table.is_contiguous():
+    if k.device != dev or v.device != dev or ks.device != dev or vs.device != dev or dev.type != "cuda":
+        raise ValueError(f"{name} must live on the rows' CUDA device")
+    if table.dtype is not torch.int32 or table.device != dev or table.dim() != 2 or table.shape[0] != B or not table.is_contiguous():
         raise TypeError(f"the page table must be a contiguous int32 [{B}, pages of a request] tensor on {dev}")
-    return _CacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), st[0] if n > 1 else H * P * D,
-                        ks.stride(0) if n > 1 else H, n, H, P, D, table.data_ptr(), table.shape[1])
+    return _pack_cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), st[0] if n > 1 else H * P * D,
+                       ss[0] if n > 1 else H, n, H, P, D, table.data_ptr(), table.shape[1]), H, P, D
 
 
 def _rows(t, name, dev, dtypes):
     """dtype code and strides of rows [B, tokens, heads, head_dim]."""
-    if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
+    st = t.stride()
+    if len(st) != 4 or (st[3] != 1 and t.shape[3] > 1):
         raise ValueError(f"{name} must be [B, tokens, heads, head_dim] with contiguous heads")
     if t.device != dev:
         raise ValueError(f"{name} must live on {dev}")
     code = _ROW_DTYPES.get(t.dtype)
     if code is None or code not in dtypes:
         raise TypeError(f"{name} cannot be {t.dtype}")
-    return code, _Strides3(*t.stride()[:3])
+    return code, _pack3(st[0], st[1], st[2])
 
 
 def _index_rows(index, counts, B, n, dev):
     """(index, its stride, rows a request at most)"""
-    if counts is not None and (counts.dtype != torch.int32 or counts.device != dev or tuple(counts.shape) != (B,)):
-        raise TypeError(f"counts must be an int32 [{B}] tensor on {dev}")
+    if counts is not None:
+        _lengths(counts, B, "counts", dev)
     if index is None:
         return None, 0, n
     if index.dtype != torch.int32 or index.device != dev or index.dim() != 2 or index.shape[0] != B or index.stride(1) != 1:
@@ -579,17 +585,29 @@ def _on(dev, fn, *args):
     return _call(dev, fn, *args)
 
 
+def _lengths(t, B, name, dev):
+    if t.dtype is not torch.int32 or t.device != dev or t.shape != (B,) or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 [{B}] tensor on {dev}")
+    return t.data_ptr()
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
 def _cache_workspace(op, cs, B, N, Hq, dev, ws, stream):
-    need = lib().spec_cache_workspace_size(op, ctypes.byref(cs), B, N, Hq)
+    need = lib().spec_cache_workspace_size(op, cs, B, N, Hq)
     if ws is None:
         if need == 0:
             return None, 0
-        ws = workspace(need, dev, stream)
+        ws = _workspaces.get((dev.index, stream))  # (workspace()'s, found without making a stream object)
+        if ws is None or ws.numel() < need:
+            ws = workspace(need, dev, torch.cuda.ExternalStream(stream, device=dev))
     return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _raw_stream(stream, dev) -> int:
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def spec_cache_append(cache, table: torch.Tensor, cache_len: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, counts=None,
@@ -598,17 +616,18 @@ def spec_cache_append(cache, table: torch.Tensor, cache_len: torch.Tensor, k: to
     them, or counts int32 [B]; with index int32 [B, rows], row i is token index[b, i] (the accepted path: index = path_nodes,
     counts = n_emit of a verify call) -> new_len [B], status [B]."""
     dev = k.device
+    st = _raw_stream(stream, dev)
     B, n = k.shape[:2]
-    cs = _cache_struct(cache, table, B)
+    cs, H, P, hd = _cache_struct(cache, table, B, dev)
     code, kst = _rows(k, "k", dev, (DTYPE_BF16, DTYPE_F16, DTYPE_F32))
     vcode, vst = _rows(v, "v", dev, (DTYPE_BF16, DTYPE_F16, DTYPE_F32))
-    if v.shape != k.shape or vcode != code or tuple(k.shape[2:]) != (cs.kv_heads, cs.head_dim):
-        raise ValueError(f"k and v must both be [B, n, {cs.kv_heads}, {cs.head_dim}] of one dtype")
-    cache_len = _i32(cache_len, (B,), "cache_len", dev)
+    if v.shape != k.shape or vcode != code or tuple(k.shape[2:]) != (H, hd):
+        raise ValueError(f"k and v must both be [B, n, {H}, {hd}] of one dtype")
+    lp = _lengths(cache_len, B, "cache_len", dev)
     ip, ist, rows = _index_rows(index, counts, B, n, dev)
     o = out or dict(new_len=torch.empty(B, dtype=torch.int32, device=dev), status=torch.empty(B, dtype=torch.int32, device=dev))
-    rc = _on(dev, lib().spec_cache_append, ctypes.byref(cs), k.data_ptr(), kst, v.data_ptr(), vst, code, B, n, ip, ist, rows,
-             _ptr(counts), cache_len.data_ptr(), o["new_len"].data_ptr(), _ptr(o.get("status")), _stream(stream, dev))
+    rc = _on(dev, lib().spec_cache_append, cs, k.data_ptr(), kst, v.data_ptr(), vst, code, B, n, ip, ist, rows,
+             _ptr(counts), lp, o["new_len"].data_ptr(), _ptr(o.get("status")), st)
     _check(rc, "spec_cache_append")
     return o
 
@@ -620,13 +639,14 @@ def spec_cache_attend(q: torch.Tensor, cache, table: torch.Tensor, cache_len: to
     rows j with mask[b, i, j].  n_query int32 [B]: rows of a request (default N).  scale: head_dim ** -0.5 by default.
     -> out (as q), lse fp32 [B, N, Hq], status."""
     dev = q.device
+    st = _raw_stream(stream, dev)
     B, N, Hq, D = q.shape
-    cs = _cache_struct(cache, table, B)
-    if D != cs.head_dim:
-        raise ValueError(f"q must be [B, N, heads, {cs.head_dim}]")
+    cs, H, P, hd = _cache_struct(cache, table, B, dev)
+    if D != hd:
+        raise ValueError(f"q must be [B, N, heads, {hd}]")
     code, qst = _rows(q, "q", dev, (DTYPE_BF16, DTYPE_F16))
-    cache_len = _i32(cache_len, (B,), "cache_len", dev)
-    n_query = _i32(n_query, (B,), "n_query", dev)
+    lp = _lengths(cache_len, B, "cache_len", dev)
+    np_ = None if n_query is None else _lengths(n_query, B, "n_query", dev)
     if mask is not None:
         if mask.dtype not in (torch.uint8, torch.bool) or mask.device != dev or tuple(mask.shape) != (B, N, N):
             raise TypeError(f"mask must be a uint8 [{B}, {N}, {N}] tensor on {dev}")
@@ -634,15 +654,15 @@ def spec_cache_attend(q: torch.Tensor, cache, table: torch.Tensor, cache_len: to
     o = out or dict(out=torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev),
                     lse=torch.empty((B, N, Hq), dtype=torch.float32, device=dev) if lse else None,
                     status=torch.empty(B, dtype=torch.int32, device=dev))
-    ocode, ost = _rows(o["out"], "out", dev, (code,))
+    _, ost = _rows(o["out"], "out", dev, (code,))
     if o["out"].shape != q.shape:
         raise ValueError("out must have q's shape")
     if o.get("lse") is not None:
         _f32_like(o["lse"], (B, N, Hq), "lse", dev)
-    wp, wn = _cache_workspace(OP_CACHE_ATTEND, cs, B, N, Hq, dev, ws, stream)
-    rc = _on(dev, lib().spec_cache_attend, ctypes.byref(cs), q.data_ptr(), qst, code, B, N, Hq, cache_len.data_ptr(),
-             _ptr(n_query), _ptr(mask), D ** -0.5 if scale is None else float(scale), float(softcap), o["out"].data_ptr(), ost,
-             _ptr(o.get("lse")), _ptr(o.get("status")), wp, wn, _stream(stream, dev))
+    wp, wn = _cache_workspace(OP_CACHE_ATTEND, cs, B, N, Hq, dev, ws, st)
+    rc = _on(dev, lib().spec_cache_attend, cs, q.data_ptr(), qst, code, B, N, Hq, lp,
+             np_, _ptr(mask), D ** -0.5 if scale is None else float(scale), float(softcap), o["out"].data_ptr(), ost,
+             _ptr(o.get("lse")), _ptr(o.get("status")), wp, wn, st)
     _check(rc, "spec_cache_attend")
     return o
 
@@ -657,7 +677,8 @@ def _positions(t, name, B, H, dev):
     """Strides of fp32 [B, kv_heads, positions]."""
     if t.dtype != torch.float32 or t.device != dev or t.dim() != 3 or tuple(t.shape[:2]) != (B, H) or (t.shape[2] > 1 and t.stride(2) != 1):
         raise TypeError(f"{name} must be a float32 [{B}, {H}, positions] tensor on {dev} with contiguous positions")
-    return _Strides2(*t.stride()[:2])
+    st = t.stride()
+    return _pack2(st[0], st[1])
 
 
 def spec_cache_weights(q: torch.Tensor, lse: torch.Tensor, cache, table: torch.Tensor, cache_len: torch.Tensor, *, prev=None,
@@ -667,25 +688,26 @@ def spec_cache_weights(q: torch.Tensor, lse: torch.Tensor, cache, table: torch.T
     cache_len + i and seeing every position up to its own -> weights (prev's shape; positions past the rows' are not written:
     zeros in a new tensor), status.  out["weights"] may be prev."""
     dev = q.device
+    st = _raw_stream(stream, dev)
     B, N, Hq, D = q.shape
-    cs = _cache_struct(cache, table, B)
-    if D != cs.head_dim:
-        raise ValueError(f"q must be [B, N, heads, {cs.head_dim}]")
+    cs, H, P, hd = _cache_struct(cache, table, B, dev)
+    if D != hd:
+        raise ValueError(f"q must be [B, N, heads, {hd}]")
     code, qst = _rows(q, "q", dev, (DTYPE_BF16, DTYPE_F16))
-    cache_len = _i32(cache_len, (B,), "cache_len", dev)
-    lp = _f32_like(lse, (B, N, Hq), "lse", dev)
+    lp = _lengths(cache_len, B, "cache_len", dev)
+    zp = _f32_like(lse, (B, N, Hq), "lse", dev)
     ip, ist, rows = _index_rows(index, counts, B, N, dev)
-    pst = None if prev is None else _positions(prev, "prev", B, cs.kv_heads, dev)
+    pst = None if prev is None else _positions(prev, "prev", B, H, dev)
     o = out
     if o is None:
-        w = torch.zeros((B, cs.kv_heads, cs.table_stride * cs.page_size), device=dev) if prev is None else prev.clone()
+        w = torch.zeros((B, H, table.shape[1] * P), device=dev) if prev is None else prev.clone()
         o = dict(weights=w, status=torch.empty(B, dtype=torch.int32, device=dev))
-    ost = _positions(o["weights"], "weights", B, cs.kv_heads, dev)
+    ost = _positions(o["weights"], "weights", B, H, dev)
     room = o["weights"].shape[2] if prev is None else min(prev.shape[2], o["weights"].shape[2])
-    wp, wn = _cache_workspace(OP_CACHE_WEIGHTS, cs, B, rows, Hq, dev, ws, stream)
-    rc = _on(dev, lib().spec_cache_weights, ctypes.byref(cs), q.data_ptr(), qst, code, B, N, Hq, lp, ip, ist, rows, _ptr(counts),
-             cache_len.data_ptr(), D ** -0.5 if scale is None else float(scale), float(softcap), _ptr(prev), pst,
-             o["weights"].data_ptr(), ost, room, _ptr(o.get("status")), wp, wn, _stream(stream, dev))
+    wp, wn = _cache_workspace(OP_CACHE_WEIGHTS, cs, B, rows, Hq, dev, ws, st)
+    rc = _on(dev, lib().spec_cache_weights, cs, q.data_ptr(), qst, code, B, N, Hq, zp, ip, ist, rows, _ptr(counts),
+             lp, D ** -0.5 if scale is None else float(scale), float(softcap), _ptr(prev), pst,
+             o["weights"].data_ptr(), ost, room, _ptr(o.get("status")), wp, wn, st)
     _check(rc, "spec_cache_weights")
     return o
 
@@ -696,18 +718,19 @@ def spec_cache_evict(cache, table: torch.Tensor, cache_len: torch.Tensor, weight
     `recent` last tokens and the others of largest weight (weights fp32 [B, kv_heads, positions]), min(keep, cache_len) in all and
     in their order -> kept int32 [B, kv_heads, keep] (positions, then -1), weights [B, kv_heads, keep] (then 0), new_len, status."""
     dev = weights.device
+    st = _raw_stream(stream, dev)
     B = weights.shape[0]
-    cs = _cache_struct(cache, table, B)
-    ds = _cache_struct(cache if dst_cache is None else dst_cache, dst_table, B, "dst_cache")
-    cache_len = _i32(cache_len, (B,), "cache_len", dev)
-    wst = _positions(weights, "weights", B, cs.kv_heads, dev)
+    cs, H, P, hd = _cache_struct(cache, table, B, dev)
+    ds = _cache_struct(cache if dst_cache is None else dst_cache, dst_table, B, dev, "dst_cache")[0]
+    lp = _lengths(cache_len, B, "cache_len", dev)
+    wst = _positions(weights, "weights", B, H, dev)
     keep = int(keep)
-    o = out or dict(kept=torch.empty((B, cs.kv_heads, max(keep, 0)), dtype=torch.int32, device=dev),
-                    weights=torch.empty((B, cs.kv_heads, max(keep, 0)), device=dev),
+    o = out or dict(kept=torch.empty((B, H, max(keep, 0)), dtype=torch.int32, device=dev),
+                    weights=torch.empty((B, H, max(keep, 0)), device=dev),
                     new_len=torch.empty(B, dtype=torch.int32, device=dev), status=torch.empty(B, dtype=torch.int32, device=dev))
-    wp, wn = _cache_workspace(OP_CACHE_EVICT, cs, B, keep, 0, dev, ws, stream)
-    rc = _on(dev, lib().spec_cache_evict, ctypes.byref(cs), ctypes.byref(ds), B, cache_len.data_ptr(), weights.data_ptr(), wst,
-             weights.shape[2], keep, int(recent), o["kept"].data_ptr(), _ptr(o.get("weights")), o["new_len"].data_ptr(), _ptr(o.get("status")), wp,
-             wn, _stream(stream, dev))
+    wp, wn = _cache_workspace(OP_CACHE_EVICT, cs, B, keep, 0, dev, ws, st)
+    rc = _on(dev, lib().spec_cache_evict, cs, ds, B, lp, weights.data_ptr(), wst,
+             weights.shape[2], keep, int(recent), o["kept"].data_ptr(), _ptr(o.get("weights")), o["new_len"].data_ptr(),
+             _ptr(o.get("status")), wp, wn, st)
     _check(rc, "spec_cache_evict")
     return o

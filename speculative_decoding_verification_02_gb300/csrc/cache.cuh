@@ -55,8 +55,9 @@ struct CacheTilePlan {
   int first, count;     // requests of this launch
   int page_rows;        // rows of a page that one copy brings: min(page size, 128)
   bool q_vec, out_vec;  // rows of q and out start on 8-byte boundaries
-  int *start, *verdict;  // running sum of the requests' tiles, their status
+  int *verdict;          // the requests' status
   int2 *range;           // [CTA] first tile; whether it gave up waiting
+  int4 *begun;           // [CTA] the unit that it began and a later one ended
   float2 *ml;           // [CTA][2][rows of a unit]: reference and sum of partial rows
   float *part;          // [CTA][2][rows of a unit][head_dim]
 };

@@ -129,9 +129,9 @@ size_t lay_out(CacheTilePlan &A, char *ws, int D) {
     off = round256(off + bytes);
     return p;
   };
-  A.start = reinterpret_cast<int *>(take(sizeof(int) * (kTileRequests + 1)));
   A.verdict = reinterpret_cast<int *>(take(sizeof(int) * kTileRequests));
   A.range = reinterpret_cast<int2 *>(take(sizeof(int2) * ctas));
+  A.begun = reinterpret_cast<int4 *>(take(sizeof(int4) * ctas));
   A.ml = reinterpret_cast<float2 *>(take(sizeof(float2) * 2 * ctas * rt));
   A.part = reinterpret_cast<float *>(take(sizeof(float) * 2 * ctas * rt * D));
   return off;

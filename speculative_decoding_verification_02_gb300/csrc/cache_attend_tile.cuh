@@ -2,6 +2,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 
 #include "cache.cuh"
 #include "common.cuh"
@@ -76,13 +77,14 @@ struct TileSmall {
   float4 ring[kRing][8];  // a 16-position group's k_scale, log2(v_scale), 1 / v_scale
   float tops[2][2][128];  // the two threads' maxima of a row, for two tiles
   float2 ml[2][128];      // reference and sum of a thread's positions
+  int4 begun;  // the unit that begins here and ends in a later CTA
   float row_factor[128];
   float weight[128];   // of a copy's row when the copies are summed
   int64_t out_at[128];  // element offset of a row in out
   uint32_t poison[2][4];
   int spoiled[128];    // rows that saw a NaN value
   uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], w_full[2], s_full[2], s_empty[2], p_full[2], pv_done[2];
-  uint64_t q_full, o_free[2], meet, pair[4], ring_full[kRing], ring_empty[kRing];
+  uint64_t q_full, o_free[2], meet, ring_full[kRing], ring_empty[kRing];
   uint32_t tmem;
   int dead;
 };
@@ -249,6 +251,14 @@ struct TileWalk {
   }
 };
 
+// Row x = token * Hq + head of request b as one that sees nothing, by one thread.
+template <int DT, int D>
+__device__ void zero_row(const CacheAttendParams &P, int b, int x) {
+  char *out = P.out + (b * P.os[0] + x / P.Hq * P.os[1] + x % P.Hq * P.os[2]) * 2;
+  for (int d = 0; d < D; ++d) put_value<DT>(out, d, 0.0f);
+  if (P.lse) P.lse[static_cast<int64_t>(b) * P.N * P.Hq + x] = -INFINITY;
+}
+
 template <int DT, int D, int REPL, bool CAP>
 __global__ void __launch_bounds__(kTileThreads, 1)
     cache_attend_tile_kernel(const CacheTilePlan A, const __grid_constant__ CUtensorMap k_map) {
@@ -270,7 +280,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (int i = 0; i < S::kStagesV; ++i) bar_init(&sm.v_full[i], 1), bar_init(&sm.v_empty[i], 128);
     for (int i = 0; i < 2; ++i) {
       bar_init(&sm.w_full[i], 128);
-      bar_init(&sm.s_full[i], 1);
+      bar_init(&sm.s_full[i], 2);
       bar_init(&sm.s_empty[i], kSoft);
       bar_init(&sm.p_full[i], kSoft);
       bar_init(&sm.pv_done[i], 1);
@@ -278,10 +288,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     bar_init(&sm.q_full, kSoft);
     bar_init(&sm.meet, kSoft);
-    for (int i = 0; i < 4; ++i) bar_init(&sm.pair[i], 64);
     for (int i = 0; i < kRing; ++i) bar_init(&sm.ring_full[i], 32), bar_init(&sm.ring_empty[i], kSoft);
     bar_init_fence();
     sm.dead = 0;
+    sm.begun = make_int4(-1, 0, 0, 0);
   }
   if (tid < 128) sm.spoiled[tid] = 0;
   if (warp == 14) tmem_alloc(&sm.tmem, kCols);
@@ -304,16 +314,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (lane >= o) x += y;
       }
       x += carry;
-      if (b0 + lane < A.count) {
-        sm.q.start[b0 + lane + 1] = x;
-        if (cta == 0) A.start[b0 + lane + 1] = x;
-      }
+      if (b0 + lane < A.count) sm.q.start[b0 + lane + 1] = x;
       carry = __shfl_sync(~0u, x, 31);
     }
-    if (lane == 0) {
-      sm.q.start[0] = 0;
-      if (cta == 0) A.start[0] = 0;
-    }
+    if (lane == 0) sm.q.start[0] = 0;
   }
   __syncthreads();
   const int total = sm.q.start[A.count];
@@ -390,6 +394,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ++units;
       }
       if (i >= 2 && !warp_wait(&sm.s_empty[i & 1], (i / 2 - 1) & 1, dead)) break;
+      if (!warp_wait(&sm.ring_full[i % kRing], (i / kRing) & 1, dead)) break;
+      if (lane == 0) bar_arrive(&sm.s_full[i & 1]);  // (with this arrival S full says that the tile's scales are there too)
       if (!warp_wait(&sm.k_full[sk], lap & 1, dead)) break;
       tc_fence_after();
       if (elect_one()) {
@@ -442,6 +448,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (wide == 0) A.verdict[b] = st;
       asm volatile("bar.sync 2, 128;" ::: "memory");
       if (bad) A.verdict[b] = SPEC_STATUS_BAD_PAGE;
+      // rows that no unit covers
+      for (int x = wide + (st == SPEC_STATUS_OK ? n : 0) * P.Hq; x < P.N * P.Hq; x += 128) zero_row<DT, D>(P, A.first + b, x);
     }
     int unit_end = lo;
     Unit u{};
@@ -539,7 +547,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     const bool negative = P.scale < 0.0f;
     bool ok = true;
-    uint32_t meetings = 0, pairings = 0;
+    uint32_t meetings = 0;
     auto together = [&] {  // a barrier of the eight warps, bounded like every wait
       bar_arrive(&sm.meet);
       return warp_wait(&sm.meet, meetings++ & 1, dead);
@@ -638,11 +646,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int i = t - lo, sb = i & 1, ring = i % kRing;
         const int pos0 = (t - u.tile0) * kTile + col0;
         const bool edge = pos0 + OWN > u.base;
-        if (!(ok = warp_wait(&sm.ring_full[ring], (i / kRing) & 1, dead))) break;
-        float4 sc[(OWN + 15) / 16];
-#pragma unroll
-        for (int g = 0; g < (OWN + 15) / 16; ++g) sc[g] = sm.ring[ring][col0 / 16 + g];
-        bar_arrive(&sm.ring_empty[ring]);
         if (!(ok = warp_wait(&sm.s_full[sb], (i >> 1) & 1, dead))) break;
         tc_fence_after();
         float x[OWN];
@@ -652,9 +655,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int c = 0; c < OWN; c += 32) tmem_ld32(tmem + lanes + sb * 128 + col0 + c, x + c);
         }
+        float4 sc[(OWN + 15) / 16];
+#pragma unroll
+        for (int g = 0; g < (OWN + 15) / 16; ++g) sc[g] = sm.ring[ring][col0 / 16 + g];
         tc_wait_ld();
         tc_fence_before();
         bar_arrive(&sm.s_empty[sb]);
+        bar_arrive(&sm.ring_empty[ring]);
 
         // x f is the score in units of log 2; with a cap it is formed here
         if (CAP) {
@@ -690,8 +697,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // the two threads of a row agree on its maximum
         if (HALVES == 2) {
           sm.tops[sb][half][spot] = top;
-          bar_arrive(&sm.pair[quarter]);
-          if (!(ok = warp_wait(&sm.pair[quarter], pairings++ & 1, dead))) break;
+          asm volatile("bar.sync %0, 64;" ::"r"(3 + quarter) : "memory");
           top = fmaxf(top, sm.tops[sb][1 - half][spot]);
         }
         // the reference, and O with it when it moves
@@ -779,6 +785,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           sm.out_at[tid] = u.b * P.os[0] + tok * P.os[1] + h * P.os[2];
         } else {
           A.ml[static_cast<int64_t>(slot) * RT + tid] = make_float2(m_all, l_all);
+          if (tid == 0 && lo <= u.tile0) sm.begun = make_int4(u.b - A.first, u.head, u.row0 * 2 + (slot & 1), u.tile0 + u.tiles);
         }
         if (sm.spoiled[tid]) norm = NAN;
         sm.spoiled[tid] = 0;
@@ -850,67 +857,72 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ++unit;
       ok = together();  // the shared arrays have been read
     }
+    // a warp that gave up lets its partner, which may be waiting for its maxima, go on to give up too
+    if (HALVES == 2 && !ok) asm volatile("bar.arrive %0, 64;" ::"r"(3 + quarter) : "memory");
   }
   tc_fence_before();
   __syncthreads();
   pdl_launch_dependents();
-  if (tid == 0) A.range[cta] = make_int2(lo, sm.dead);
+  if (tid == 0) {
+    A.range[cta] = make_int2(lo, sm.dead);
+    A.begun[cta] = sm.begun;
+  }
   if (warp == 14) {
     tc_fence_after();
     tmem_free(tmem, kCols);
   }
 }
 
-// Joins the partial sums of the units that more than one CTA worked on, a warp
-// to a row, and writes what no unit covers: rows past n_query, bad requests.
+// Joins the partial sums of the units that more than one CTA worked on: block
+// (c, j) takes eight rows, a warp each, of the unit that CTA c began and a later
+// one ended.  The last blocks set the requests' status, and clear the outputs of
+// those with a bad page.
 template <int DT, int D>
 __global__ void __launch_bounds__(256) cache_attend_merge_kernel(const CacheTilePlan A, int row_tile, int ctas) {
   const CacheAttendParams &P = A.p;
-  const int lane = threadIdx.x & 31;
-  const int x = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (x >= A.count * P.N * P.Hq) return;
-  const int bl = x / (P.N * P.Hq), y = x - bl * (P.N * P.Hq), i = y / P.Hq, h = y - i * P.Hq, head = h / P.group;
-  const int b = A.first + bl;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kEach = D / 32;
-  char *out = P.out + (b * P.os[0] + i * P.os[1] + h * P.os[2]) * 2;
-  const int64_t at_lse = (static_cast<int64_t>(b) * P.N + i) * P.Hq + h;
-  int base, n;
-  request_lengths(P, b, base, n);
   pdl_wait();
-  // everything the row's place depends on, in one round of loads
-  int st = A.verdict[bl];
-  const int start = A.start[bl], span = A.start[bl + 1] - start;
-  const int row = i * P.group + h - head * P.group, rt = row / row_tile, r = row - rt * row_tile;
-  int tile0 = start + head * (span / P.c.kv_heads);
-  for (int k = 0; k < rt; ++k) tile0 += (unit_positions(base, n, P.group, row_tile, k, P.mask != nullptr) + kTile - 1) / kTile;
-  const int tiles = (unit_positions(base, n, P.group, row_tile, rt, P.mask != nullptr) + kTile - 1) / kTile;
-  // the CTAs whose ranges the unit meets: the last that begins at or before its first tile, and at or before its last
-  int c0 = -1, c1 = -1;
-  bool gone = false;
-  for (int c = lane; c - lane < ctas; c += 32) {
-    const int2 cut_dead = c < ctas ? A.range[c] : make_int2(0x7fffffff, 0);
-    gone |= cut_dead.y != 0;
-    c0 += __popc(__ballot_sync(~0u, cut_dead.x <= tile0));
-    c1 += __popc(__ballot_sync(~0u, cut_dead.x < tile0 + tiles));
-  }
-  if (__any_sync(~0u, gone)) st = SPEC_STATUS_TIMEOUT;
-  if (P.status && i == 0 && h == 0 && lane == 0) P.status[b] = st;
-  if (st != SPEC_STATUS_OK || i >= n) {
-    for (int e = 0; e < kEach; ++e) put_value<DT>(out, lane * kEach + e, 0.0f);
-    if (lane == 0 && P.lse) P.lse[at_lse] = -INFINITY;
+  const int chunks = row_tile / 8;
+  if (static_cast<int>(blockIdx.x) >= ctas * chunks) {
+    const int bl = (blockIdx.x - ctas * chunks) * 8 + warp, b = A.first + bl;
+    if (bl >= A.count) return;
+    int st = A.verdict[bl];
+    bool gone = false;
+    for (int c = lane; c < ctas; c += 32) gone |= A.range[c].y != 0;
+    if (__any_sync(~0u, gone)) st = SPEC_STATUS_TIMEOUT;
+    if (lane == 0 && P.status) P.status[b] = st;
+    if (st == SPEC_STATUS_BAD_PAGE || st == SPEC_STATUS_TIMEOUT)
+      for (int x = lane; x < P.N * P.Hq; x += 32) zero_row<DT, D>(P, b, x);
     return;
   }
-  if (c0 == c1) return;
+  const int c0 = blockIdx.x / chunks, r = (blockIdx.x % chunks) * 8 + warp;
+  const int4 unit = A.begun[c0];  // request, head, 2 * first row + c0's slot, end of its tiles
+  if (unit.x < 0) return;
+  const int b = A.first + unit.x;
+  int base, n;
+  request_lengths(P, b, base, n);
+  const int row = (unit.z >> 1) + r;
+  if (row >= n * P.group || A.verdict[unit.x] != SPEC_STATUS_OK) return;
+  // the last CTA that begins before the unit's end; nobody gave up
+  int c1 = -1;
+  bool gone = false;
+  for (int c = lane; c - lane < ctas; c += 32) {
+    const int2 range = c < ctas ? A.range[c] : make_int2(0x7fffffff, 0);
+    gone |= range.y != 0;
+    c1 += __popc(__ballot_sync(~0u, range.x < unit.w));
+  }
+  if (__any_sync(~0u, gone)) return;
   float m = -INFINITY, acc[kEach] = {}, sum = 0.0f;
   for (int cc = c0; cc <= c1; cc += 32) {
-    // a lane to a CTA: where it left the row, its reference and sum (slot 1 when the unit began inside its range)
+    // a lane to a CTA: where it left the row, its reference and sum
     const int c = cc + lane;
     int slot = -1;
     float2 ml = make_float2(-INFINITY, 0.0f);
     if (c <= c1) {
       const int from = A.range[c].x;
       if (c == c1 || A.range[c + 1].x > from) {
-        slot = (c * 2 + (c == c0 && from < tile0 ? 1 : 0)) * row_tile + r;
+        slot = (c * 2 + (c == c0 ? unit.z & 1 : 0)) * row_tile + r;
         ml = A.ml[slot];
       }
     }
@@ -938,24 +950,43 @@ __global__ void __launch_bounds__(256) cache_attend_merge_kernel(const CacheTile
       }
     }
   }
+  const int i = row / P.group, h = unit.y * P.group + row % P.group;
+  char *out = P.out + (b * P.os[0] + i * P.os[1] + h * P.os[2]) * 2;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) put_value<DT>(out, lane * kEach + e, acc[e] * inv);
-  if (lane == 0 && P.lse) P.lse[at_lse] = sum == 0.0f ? -INFINITY : (m - 7.0f + log2f(sum)) * kLn2;
+  if (lane == 0 && P.lse)
+    P.lse[(static_cast<int64_t>(b) * P.N + i) * P.Hq + h] = sum == 0.0f ? -INFINITY : (m - 7.0f + log2f(sum)) * kLn2;
+}
+
+// Devices on which a kernel may already use its shared memory.
+template <int DT, int D, int REPL, bool CAP>
+std::atomic<uint64_t> big_smem{0};
+
+template <class F>
+cudaError_t once_per_device(F &&f, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = f();
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 template <int DT, int D, int REPL>
 cudaError_t launch_tiles(const CacheTilePlan &A, const CUtensorMap &map, cudaStream_t st) {
   using S = TileShape<DT, D>;
   auto kern = A.p.softcap > 0.0f ? cache_attend_tile_kernel<DT, D, REPL, true> : cache_attend_tile_kernel<DT, D, REPL, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  cudaError_t e = once_per_device([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes); },
+                                  A.p.softcap > 0.0f ? big_smem<DT, D, REPL, true> : big_smem<DT, D, REPL, false>);
   if (e != cudaSuccess) return e;
   const int ctas = device_sm_count();
   e = trace_launch("cache_attend_tile", st, [&] { kern<<<ctas, kTileThreads, S::kBytes, st>>>(A, map); });
   if (e != cudaSuccess) return e;
-  const int64_t rows = static_cast<int64_t>(A.count) * A.p.N * A.p.Hq;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas * (128 / REPL / 8) + (A.count + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
