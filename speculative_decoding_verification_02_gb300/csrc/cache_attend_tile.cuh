@@ -453,9 +453,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     int unit_end = lo;
     Unit u{};
-    constexpr int kLanes = D / 16;        // lanes to a position
-    constexpr int kPer = 32 / kLanes;     // positions to a step
-    const int piece = lane % kLanes, sub = lane / kLanes;
+    // 16 bytes of a position to a lane, 4 or 8 positions to a step.  Eight lanes in a row take 64 bytes of each of two positions
+    // (of different halves of them when a position has 128), so neither their loads nor their swizzled stores share a bank;
+    // every step's addresses are a lane's own plus a constant.
+    constexpr int kPer = 512 / D;
+    const int part = lane & 3, sub = D == 128 ? (lane >> 4) * 2 + (lane >> 2 & 1) : lane >> 2;
+    const int group = D == 128 ? (lane >> 3 & 1) ^ (lane >> 2 & 1) : 0;  // 64 columns
+    const int from = (w4 * 32 + sub) * D + group * 64 + part * 16;
+    const int to = group * (kTile * 128) + w4 * 4096 + sub * 128 + ((part * 2 ^ sub) << 4);
     int unit = -1, ended1 = -1, ended2 = -1;  // this unit's number; the unit that tile i - 1, i - 2 closed, or -1
     for (int t = lo, sv = 0, lap = 0; t < hi; ++t) {
       const int i = t - lo, w = i & 1;
@@ -475,7 +480,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const char *src = smem + S::kV8 + sv * S::kStage;
       char *dst = smem + S::kV16 + w * 2 * S::kStage;
       uint32_t poison = 0;
-      auto widen = [&](uint4 x, int row) {
+      auto widen = [&](uint4 x, int step) {
         uint4 h[2];
         uint32_t *o = reinterpret_cast<uint32_t *>(h);
         const uint32_t in[4] = {x.x, x.y, x.z, x.w};
@@ -485,28 +490,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           o[2 * c] = *reinterpret_cast<const uint32_t *>(&a);
           o[2 * c + 1] = *reinterpret_cast<const uint32_t *>(&b);
         }
-        // columns of 64: 16 KB apart; eight positions: 1024 bytes; chunks of 16 bytes swizzled by the position
-        char *to = dst + (piece >> 2) * (kTile * 128) + (row >> 3) * 1024 + (row & 7) * 128;
-        const int c0 = (piece & 3) * 2;
-        const bool flip = piece >> 2 & 1;  // (the two column groups store their chunks in opposite order: no bank conflict)
-        *reinterpret_cast<uint4 *>(to + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? h[1] : h[0];
-        *reinterpret_cast<uint4 *>(to + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? h[0] : h[1];
+        // eight positions: 1024 bytes; 16-byte chunks swizzled by the position in them (in the upper four: 4 more)
+        const int at = D == 128 ? (to ^ (step & 1) << 6) + (step >> 1) * 1024 + (step & 1) * 512 : to + step * 1024;
+        *reinterpret_cast<uint4 *>(dst + at) = h[0];
+        *reinterpret_cast<uint4 *>(dst + (at ^ 16)) = h[1];
       };
       constexpr int kSteps = 32 / kPer;
       if (!edge) [[likely]] {
-#pragma unroll 1
+#pragma unroll
         for (int step = 0; step < kSteps; step += 4) {
           uint4 x[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const uint4 *>(src + (w4 * 32 + (step + k) * kPer + sub) * D + piece * 16);
+          for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const uint4 *>(src + from + (step + k) * kPer * D);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) widen(x[k], w4 * 32 + (step + k) * kPer + sub);
+          for (int k = 0; k < 4; ++k) widen(x[k], step + k);
         }
       } else {  // nothing past the last position, and no NaN where a row may not look
 #pragma unroll 1
         for (int step = 0; step < kSteps; ++step) {
-          const int row = w4 * 32 + step * kPer + sub, pos = pos0 + row;
-          uint4 x = *reinterpret_cast<const uint4 *>(src + row * D + piece * 16);
+          const int pos = pos0 + w4 * 32 + step * kPer + sub;
+          uint4 x = *reinterpret_cast<const uint4 *>(src + from + step * kPer * D);
           bool nan = false;
           if (pos >= u.T) x = make_uint4(0, 0, 0, 0);
           else if (pos >= u.base) {
@@ -521,9 +524,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
           const uint32_t vote = __ballot_sync(~0u, nan);
 #pragma unroll
-          for (int c = 0; c < kPer; ++c)
-            if (vote >> (c * kLanes) & ((1u << kLanes) - 1)) poison |= 1u << (step * kPer + c);
-          widen(x, row);
+          for (int c = 0; c < kPer; ++c) {
+            const uint32_t lanes_of = D == 128 ? (c & 1 ? 0xf0f0u : 0x0f0fu) << (c >> 1) * 16 : 0xfu << c * 4;
+            if (vote & lanes_of) poison |= 1u << (step * kPer + c);
+          }
+          widen(x, step);
         }
       }
       if (edge && lane == 0) sm.poison[w][w4] = poison;
