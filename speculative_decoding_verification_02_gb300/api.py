@@ -167,7 +167,11 @@ def workspace(nbytes: int, device, stream=None) -> torch.Tensor:
     overlap and must not."""
     device = torch.device(device)
     s = stream if stream is not None else torch.cuda.current_stream(device)
-    key = (device.index, s.cuda_stream)
+    return _workspace(nbytes, device, s.cuda_stream)
+
+
+def _workspace(nbytes: int, device, stream: int) -> torch.Tensor:
+    key = (device.index, stream)
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < max(nbytes, 1):
         ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)  # needs no initialisation
@@ -545,12 +549,14 @@ def _cache_struct(cache, table, B, dev, name="cache"):
     n, H, P, D = shape
     if st[3] != 1 or st[2] != D or (H > 1 and st[1] != P * D) or vs.stride() != ss or (H > 1 and ss[1] != 1):
         raise ValueError(f"{name}: the heads of a page must lie side by side")
-    if k.device != dev or v.device != dev or ks.device != dev or vs.device != dev or dev.type != "cuda":
+    i = dev.index
+    if dev.type != "cuda" or k.get_device() != i or v.get_device() != i or ks.get_device() != i or vs.get_device() != i:
         raise ValueError(f"{name} must live on the rows' CUDA device")
-    if table.dtype is not torch.int32 or table.device != dev or table.dim() != 2 or table.shape[0] != B or not table.is_contiguous():
+    ts = table.shape
+    if table.dtype is not torch.int32 or table.get_device() != i or len(ts) != 2 or ts[0] != B or not table.is_contiguous():
         raise TypeError(f"the page table must be a contiguous int32 [{B}, pages of a request] tensor on {dev}")
     return _pack_cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), st[0] if n > 1 else H * P * D,
-                       ss[0] if n > 1 else H, n, H, P, D, table.data_ptr(), table.shape[1]), H, P, D
+                       ss[0] if n > 1 else H, n, H, P, D, table.data_ptr(), ts[1]), H, P, D
 
 
 def _rows(t, name, dev, dtypes):
@@ -558,7 +564,7 @@ def _rows(t, name, dev, dtypes):
     st = t.stride()
     if len(st) != 4 or (st[3] != 1 and t.shape[3] > 1):
         raise ValueError(f"{name} must be [B, tokens, heads, head_dim] with contiguous heads")
-    if t.device != dev:
+    if t.get_device() != dev.index:
         raise ValueError(f"{name} must live on {dev}")
     code = _ROW_DTYPES.get(t.dtype)
     if code is None or code not in dtypes:
@@ -586,7 +592,7 @@ def _on(dev, fn, *args):
 
 
 def _lengths(t, B, name, dev):
-    if t.dtype is not torch.int32 or t.device != dev or t.shape != (B,) or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.get_device() != dev.index or t.shape != (B,) or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 [{B}] tensor on {dev}")
     return t.data_ptr()
 
@@ -600,10 +606,8 @@ def _cache_workspace(op, cs, B, N, Hq, dev, ws, stream):
     if ws is None:
         if need == 0:
             return None, 0
-        ws = _workspaces.get((dev.index, stream))  # (workspace()'s, found without making a stream object)
-        if ws is None or ws.numel() < need:
-            ws = workspace(need, dev, torch.cuda.ExternalStream(stream, device=dev))
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+        ws = _workspace(need, dev, stream)
+    return ws.data_ptr(), ws.numel()
 
 
 def _raw_stream(stream, dev) -> int:
@@ -668,7 +672,7 @@ def spec_cache_attend(q: torch.Tensor, cache, table: torch.Tensor, cache_len: to
 
 
 def _f32_like(t, shape, name, dev):
-    if t.dtype != torch.float32 or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not torch.float32 or t.get_device() != dev.index or t.shape != shape or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous float32 {list(shape)} tensor on {dev}")
     return t.data_ptr()
 
