@@ -2,6 +2,7 @@
 // table, e4m3 conversions and block scales, and the parameter blocks.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -100,6 +101,19 @@ cudaError_t launch_cache_attend_f16(const CacheTilePlan &A, const CUtensorMap &m
 cudaError_t cache_k_map(const CacheView &c, int page_rows, CUtensorMap *map);
 cudaError_t launch_cache_weights(const CacheWeightsParams &P, cudaStream_t st);
 cudaError_t launch_cache_evict(const CacheEvictParams &P, cudaStream_t st);
+
+// f() the first time it is called for the current device, as `done` remembers.
+template <class F>
+inline cudaError_t once_per_device(F &&f, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = f();
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 #ifdef __CUDACC__
 

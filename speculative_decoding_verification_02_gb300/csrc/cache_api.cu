@@ -194,7 +194,7 @@ int spec_cache_evict(const spec_cache *cache, const spec_cache *dst, int B, cons
   if (B == 0) return SPEC_OK;
   if (!cache_len || !weights || !kept || !new_len || cache_len == new_len) return SPEC_EINVAL;
   const int64_t pages = (static_cast<int64_t>(keep) + (1 << P.c.page_shift) - 1) >> P.c.page_shift;
-  if (2LL * B * P.c.kv_heads * pages > kMaxGrid) return SPEC_EINVAL;
+  if (2LL * B * P.c.kv_heads * std::max<int64_t>(pages, 16) > kMaxGrid) return SPEC_EINVAL;
   P.B = B, P.positions = positions, P.keep = keep, P.recent = recent, P.cache_len = cache_len, P.weights = weights;
   std::copy(weights_stride, weights_stride + 2, P.ws);
   P.kept = kept, P.kept_weights = kept_weights, P.new_len = new_len, P.status = status;

@@ -38,10 +38,38 @@ __device__ void append_verdict(const CacheAppendParams &P, int b, int64_t base, 
   }
 }
 
+// 16 bytes of a row in registers: 8 values of 16 bits, or 4 of 32.
 template <int DT>
+struct Piece {
+  static constexpr int kSize = DT == SPEC_DTYPE_F32 ? 4 : 2, kValues = 16 / kSize;
+  __device__ static void unpack(const uint4 &w, float *x) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (DT == SPEC_DTYPE_F32) {
+        x[e] = __uint_as_float(u[e]);
+      } else if constexpr (DT == SPEC_DTYPE_BF16) {
+        x[2 * e] = __uint_as_float(u[e] << 16);
+        x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[e]));
+        x[2 * e] = f.x;
+        x[2 * e + 1] = f.y;
+      }
+    }
+  }
+};
+
+// VEC: every row starts on a 16-byte boundary.  A thread keeps up to kHeld
+// pieces of the block in registers between the maximum and the rounding, which
+// at 128 tokens of 128 values is all of them: the rows are read once.
+constexpr int kHeld = 8;
+
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const CacheAppendParams P) {
+  using W = Piece<DT>;
   // block index: ((request, touched page), head, K or V)
-  int64_t x = blockIdx.x;
+  uint32_t x = blockIdx.x;
   const bool is_v = x & 1;
   x >>= 1;
   const int head = static_cast<int>(x % P.c.kv_heads);
@@ -62,55 +90,105 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
   const int hi = static_cast<int>(min(base + cnt - start, static_cast<int64_t>(page_size)));
   if (lo >= hi) return;
   const int page = page_at(P.c, b, block);
-  if (page < 0) return;
 
   const int D = P.c.head_dim, rows = hi - lo;
-  const char *src = is_v ? P.v : P.k;
-  const int64_t es = DT == SPEC_DTYPE_F32 ? 4 : 2;
   const int64_t s0 = is_v ? P.vs[0] : P.ks[0], s1 = is_v ? P.vs[1] : P.ks[1], s2 = is_v ? P.vs[2] : P.ks[2];
   const int first = static_cast<int>(start + lo - base);  // the block's first new row
-  const int32_t *index = P.index ? P.index + static_cast<int64_t>(b) * P.index_stride : nullptr;
-  auto row_of = [&](int r) -> const char * {
-    const int t = index ? index[first + r] : first + r;
-    if (t < 0 || t >= P.n) return nullptr;
-    return src + (b * s0 + t * s1 + head * s2) * es;
+  const char *src = (is_v ? P.v : P.k) + (b * s0 + head * s2) * W::kSize;
+  const int32_t *index = P.index ? P.index + static_cast<int64_t>(b) * P.index_stride + first : nullptr;
+  const int per_row = D / W::kValues, pieces = rows * per_row;
+  // piece i of the block's new rows; false for a row whose index is out of range
+  auto load = [&](int i, uint4 &v) {
+    const int r = i / per_row, t = index ? index[r] : first + r;
+    if (t < 0 || t >= P.n) return false;
+    const char *p = src + t * s1 * W::kSize + (i - r * per_row) * 16;
+    if constexpr (VEC) {
+      v = *reinterpret_cast<const uint4 *>(p);
+    } else if constexpr (W::kSize == 4) {
+      const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
+      v = make_uint4(q[0], q[1], q[2], q[3]);
+    } else {
+      const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+      v = make_uint4(q[0] | q[1] << 16, q[2] | q[3] << 16, q[4] | q[5] << 16, q[6] | q[7] << 16);
+    }
+    return true;
+  };
+  auto piece_max = [](const uint4 &v, float most) {
+    float x[W::kValues];
+    W::unpack(v, x);
+#pragma unroll
+    for (int e = 0; e < W::kValues; ++e) most = fmaxf(most, finite_abs(x[e]));
+    return most;
   };
 
   __shared__ float s_max[kAppendThreads / 32];
+  uint4 held[kHeld];
+  bool real[kHeld];
   float amax = 0.0f;
-  const int pairs = D / 2;
-  for (int i = tid; i < rows * pairs; i += kAppendThreads) {
-    const char *row = row_of(i / pairs);
-    if (!row) continue;
-    const int d = i % pairs * 2;
-    amax = fmaxf(amax, fmaxf(finite_abs(row_value<DT>(row, d)), finite_abs(row_value<DT>(row, d + 1))));
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int i = tid + k * kAppendThreads;
+    held[k] = make_uint4(0, 0, 0, 0);
+    real[k] = i < pieces && load(i, held[k]);
+  }
+  float *scale = (is_v ? P.c.v_scale : P.c.k_scale) + max(page, 0) * P.c.scale_stride + head;
+  const float was = *scale;
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) amax = piece_max(held[k], amax);
+  for (int i = tid + kHeld * kAppendThreads; i < pieces; i += kAppendThreads) {
+    uint4 v;
+    if (load(i, v)) amax = piece_max(v, amax);
   }
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
   if ((tid & 31) == 0) s_max[tid >> 5] = amax;
-  float *scale = (is_v ? P.c.v_scale : P.c.k_scale) + page * P.c.scale_stride + head;
-  const float was = *scale;
   __syncthreads();
-  amax = s_max[0];
-  for (int i = 1; i < kAppendThreads / 32; ++i) amax = fmaxf(amax, s_max[i]);
+  if (page < 0) return;
+#pragma unroll
+  for (int i = 0; i < kAppendThreads / 32; ++i) amax = fmaxf(amax, s_max[i]);
   const float need = block_scale(amax);
   const float now = lo > 0 ? fmaxf(was, need) : need;
+  // a power of two but where a caller's own scale stays: then the quotient is rounded once, as the definition has it
+  const float inv = 1.0f / now;
+  const bool exact = (__float_as_uint(now) & 0x7fffffu) == 0;
+  auto scaled = [&](float x) { return exact ? x * inv : x / now; };
 
   uint8_t *dst = (is_v ? P.c.v : P.c.k) + block_offset(P.c, page, head);
-  if (lo > 0 && now > was) {  // tokens already there, rounded again
-    uint16_t *old = reinterpret_cast<uint16_t *>(dst);
-    for (int i = tid; i < lo * pairs; i += kAppendThreads) {
-      const float2 x2 = e4m3x2_to_float2(old[i]);
-      old[i] = static_cast<uint16_t>(to_e4m3x2(x2.x * was / now, x2.y * was / now));
+  if (lo > 0 && now > was) {  // tokens already there, rounded again (now is a power of two)
+    uint32_t *old = reinterpret_cast<uint32_t *>(dst);
+    for (int i = tid; i < lo * D / 4; i += kAppendThreads) {
+      const uint32_t v = old[i];
+      const float2 a = e4m3x2_to_float2(v & 0xffff), c = e4m3x2_to_float2(v >> 16);
+      old[i] = to_e4m3x2(a.x * was * inv, a.y * was * inv) | to_e4m3x2(c.x * was * inv, c.y * was * inv) << 16;
     }
   }
-  uint16_t *to = reinterpret_cast<uint16_t *>(dst + static_cast<int64_t>(lo) * D);
-  for (int i = tid; i < rows * pairs; i += kAppendThreads) {
-    const char *row = row_of(i / pairs);
-    if (!row) continue;
-    const int d = i % pairs * 2;
-    to[i] = static_cast<uint16_t>(to_e4m3x2(row_value<DT>(row, d) / now, row_value<DT>(row, d + 1) / now));
+  uint8_t *to = dst + static_cast<int64_t>(lo) * D;
+  auto put = [&](int i, const uint4 &v) {
+    float x[W::kValues];
+    W::unpack(v, x);
+    uint32_t code[W::kValues / 4];
+#pragma unroll
+    for (int e = 0; e < W::kValues / 4; ++e)
+      code[e] = to_e4m3x2(scaled(x[4 * e]), scaled(x[4 * e + 1])) | to_e4m3x2(scaled(x[4 * e + 2]), scaled(x[4 * e + 3])) << 16;
+    if constexpr (W::kValues == 8) reinterpret_cast<uint2 *>(to)[i] = make_uint2(code[0], code[1]);
+    else reinterpret_cast<uint32_t *>(to)[i] = code[0];
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (real[k]) put(tid + k * kAppendThreads, held[k]);
+  for (int i = tid + kHeld * kAppendThreads; i < pieces; i += kAppendThreads) {
+    uint4 v;
+    if (load(i, v)) put(i, v);
   }
   if (tid == 0) *scale = now;
+}
+
+template <int DT>
+void launch_append(const CacheAppendParams &P, unsigned grid, cudaStream_t st) {
+  constexpr int kSize = Piece<DT>::kSize;
+  bool vec = reinterpret_cast<uintptr_t>(P.k) % 16 == 0 && reinterpret_cast<uintptr_t>(P.v) % 16 == 0;
+  for (int i = 0; i < 3; ++i) vec = vec && P.ks[i] * kSize % 16 == 0 && P.vs[i] * kSize % 16 == 0;
+  if (vec) cache_append_kernel<DT, true><<<grid, kAppendThreads, 0, st>>>(P);
+  else cache_append_kernel<DT, false><<<grid, kAppendThreads, 0, st>>>(P);
 }
 
 }  // namespace
@@ -118,9 +196,9 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
 cudaError_t launch_cache_append(const CacheAppendParams &P, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(2LL * P.B * P.touched * P.c.kv_heads);
   return trace_launch("cache_append", st, [&] {
-    if (P.dtype == SPEC_DTYPE_F32) cache_append_kernel<SPEC_DTYPE_F32><<<grid, kAppendThreads, 0, st>>>(P);
-    else if (P.dtype == SPEC_DTYPE_BF16) cache_append_kernel<SPEC_DTYPE_BF16><<<grid, kAppendThreads, 0, st>>>(P);
-    else cache_append_kernel<SPEC_DTYPE_F16><<<grid, kAppendThreads, 0, st>>>(P);
+    if (P.dtype == SPEC_DTYPE_F32) launch_append<SPEC_DTYPE_F32>(P, grid, st);
+    else if (P.dtype == SPEC_DTYPE_BF16) launch_append<SPEC_DTYPE_BF16>(P, grid, st);
+    else launch_append<SPEC_DTYPE_F16>(P, grid, st);
   });
 }
 

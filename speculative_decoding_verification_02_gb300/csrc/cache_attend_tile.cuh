@@ -968,18 +968,6 @@ __global__ void __launch_bounds__(256) cache_attend_merge_kernel(const CacheTile
 template <int DT, int D, int REPL, bool CAP>
 std::atomic<uint64_t> big_smem{0};
 
-template <class F>
-cudaError_t once_per_device(F &&f, std::atomic<uint64_t> &done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (bit && done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = f();
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-  return e;
-}
-
 template <int DT, int D, int REPL>
 cudaError_t launch_tiles(const CacheTilePlan &A, const CUtensorMap &map, cudaStream_t st) {
   using S = TileShape<DT, D>;
