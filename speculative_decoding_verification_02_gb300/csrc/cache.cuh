@@ -139,12 +139,15 @@ __device__ __forceinline__ float finite_abs(float x) {
 
 // Two values (already divided by the scale) to e4m3, a in the low byte:
 // nearest even, saturated at 448; infinities become NaN, as NaN does.
-__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
+__device__ __forceinline__ uint32_t finite_e4m3x2(float a, float b) {  // (neither is infinite)
   uint16_t r;
-  if (fabsf(a) == INFINITY) a = NAN;
-  if (fabsf(b) == INFINITY) b = NAN;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
+}
+__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
+  if (fabsf(a) == INFINITY) a = NAN;
+  if (fabsf(b) == INFINITY) b = NAN;
+  return finite_e4m3x2(a, b);
 }
 
 // Two e4m3 bytes (low byte first) to two halves: exact.

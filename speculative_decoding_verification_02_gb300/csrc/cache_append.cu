@@ -42,6 +42,33 @@ __device__ void append_verdict(const CacheAppendParams &P, int b, int64_t base, 
 template <int DT>
 struct Piece {
   static constexpr int kSize = DT == SPEC_DTYPE_F32 ? 4 : 2, kValues = 16 / kSize;
+  // Sign-less bits order as magnitudes do, so the maximum is taken over them, two 16-bit values at a time.  kNext: what carries
+  // the first infinity into the sign's place.
+  static constexpr uint32_t kMagnitude = DT == SPEC_DTYPE_F32 ? 0x7fffffffu : 0x7fff7fffu;
+  static constexpr uint32_t kNext = DT == SPEC_DTYPE_F32 ? 0x00800000u : DT == SPEC_DTYPE_BF16 ? 0x00800080u : 0x04000400u;
+  static constexpr uint32_t kSign = ~kMagnitude;
+
+  // The largest finite magnitudes' bits so far; the answer says whether the piece holds an infinity or NaN.
+  __device__ static bool largest(const uint4 &w, uint32_t &most) {
+    uint32_t u[4] = {w.x & kMagnitude, w.y & kMagnitude, w.z & kMagnitude, w.w & kMagnitude};
+    const uint32_t odd = ((u[0] + kNext) | (u[1] + kNext) | (u[2] + kNext) | (u[3] + kNext)) & kSign;
+    if (odd) [[unlikely]] {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t t = (u[e] + kNext) & kSign;
+        u[e] &= kSize == 4 ? (t ? 0u : ~0u) : ~((t >> 15) * 0xffffu);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) most = kSize == 4 ? max(most, u[e]) : __vmaxu2(most, u[e]);
+    return odd != 0;
+  }
+  __device__ static float magnitude(uint32_t most) {
+    if constexpr (kSize == 4) return __uint_as_float(most);
+    const uint32_t m = max(most & 0xffff, most >> 16);
+    if constexpr (DT == SPEC_DTYPE_BF16) return __uint_as_float(m << 16);
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(m)));
+  }
   __device__ static void unpack(const uint4 &w, float *x) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -113,18 +140,11 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
     }
     return true;
   };
-  auto piece_max = [](const uint4 &v, float most) {
-    float x[W::kValues];
-    W::unpack(v, x);
-#pragma unroll
-    for (int e = 0; e < W::kValues; ++e) most = fmaxf(most, finite_abs(x[e]));
-    return most;
-  };
-
   __shared__ float s_max[kAppendThreads / 32];
   uint4 held[kHeld];
   bool real[kHeld];
-  float amax = 0.0f;
+  uint32_t most = 0;
+  bool odd = false;  // an infinity or NaN among this thread's values
 #pragma unroll
   for (int k = 0; k < kHeld; ++k) {
     const int i = tid + k * kAppendThreads;
@@ -134,11 +154,12 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
   float *scale = (is_v ? P.c.v_scale : P.c.k_scale) + max(page, 0) * P.c.scale_stride + head;
   const float was = *scale;
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k) amax = piece_max(held[k], amax);
+  for (int k = 0; k < kHeld; ++k) odd |= W::largest(held[k], most);
   for (int i = tid + kHeld * kAppendThreads; i < pieces; i += kAppendThreads) {
     uint4 v;
-    if (load(i, v)) amax = piece_max(v, amax);
+    if (load(i, v)) odd |= W::largest(v, most);
   }
+  float amax = W::magnitude(most);
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
   if ((tid & 31) == 0) s_max[tid >> 5] = amax;
   __syncthreads();
@@ -150,7 +171,6 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
   // a power of two but where a caller's own scale stays: then the quotient is rounded once, as the definition has it
   const float inv = 1.0f / now;
   const bool exact = (__float_as_uint(now) & 0x7fffffu) == 0;
-  auto scaled = [&](float x) { return exact ? x * inv : x / now; };
 
   uint8_t *dst = (is_v ? P.c.v : P.c.k) + block_offset(P.c, page, head);
   if (lo > 0 && now > was) {  // tokens already there, rounded again (now is a power of two)
@@ -167,8 +187,15 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
     W::unpack(v, x);
     uint32_t code[W::kValues / 4];
 #pragma unroll
+    for (int e = 0; e < W::kValues; ++e) x[e] *= inv;
+    if (odd || !exact) [[unlikely]] {
+      W::unpack(v, x);
+#pragma unroll
+      for (int e = 0; e < W::kValues; ++e) x[e] = fabsf(x[e]) == INFINITY ? NAN : x[e] / now;
+    }
+#pragma unroll
     for (int e = 0; e < W::kValues / 4; ++e)
-      code[e] = to_e4m3x2(scaled(x[4 * e]), scaled(x[4 * e + 1])) | to_e4m3x2(scaled(x[4 * e + 2]), scaled(x[4 * e + 3])) << 16;
+      code[e] = finite_e4m3x2(x[4 * e], x[4 * e + 1]) | finite_e4m3x2(x[4 * e + 2], x[4 * e + 3]) << 16;
     if constexpr (W::kValues == 8) reinterpret_cast<uint2 *>(to)[i] = make_uint2(code[0], code[1]);
     else reinterpret_cast<uint32_t *>(to)[i] = code[0];
   };

@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
 
+  pdl_launch_dependents();  // (the merge waits for this grid to finish before it reads)
   if (tid == 0) {
     for (int i = 0; i < S::kStagesK; ++i) bar_init(&sm.k_full[i], 1), bar_init(&sm.k_empty[i], 1);
     for (int i = 0; i < S::kStagesV; ++i) bar_init(&sm.v_full[i], 1), bar_init(&sm.v_empty[i], 128);
@@ -867,7 +868,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  pdl_launch_dependents();
   if (tid == 0) {
     A.range[cta] = make_int2(lo, sm.dead);
     A.begun[cta] = sm.begun;

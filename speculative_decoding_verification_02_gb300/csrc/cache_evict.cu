@@ -12,6 +12,7 @@
 #include <cooperative_groups.h>
 
 #include "cache.cuh"
+#include "common.cuh"
 #include "launch.h"
 
 namespace sv {
@@ -54,10 +55,14 @@ __device__ __forceinline__ int block_rank(int v, int *s_warp, int &all) {
 
 // What the CTAs of a cluster read of one another.
 struct SelectShared {
-  int hist[kBins];
+  int hist[kBins];   // this slice's
+  int sum[kBins];    // the bins that this CTA adds up for the cluster
+  int total[kBins];  // the cluster's
   int warp[32];
-  int count[2];  // this slice's positions above the key, and equal to it
+  int2 count;        // this slice's positions above the key, and equal to it
+  int2 counts[32];   // a warp's
   int digit, above;
+  int2 before;       // kept positions, and ties, of the slices before
 };
 
 __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const CacheEvictParams P, int slice_room) {
@@ -67,7 +72,11 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const Cach
   __shared__ SelectShared sh;
   const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int unit = blockIdx.x / ranks, head = unit % P.c.kv_heads, b = unit / P.c.kv_heads;
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto meet = [&] {
+    if (ranks > 1) cluster.sync();
+    else __syncthreads();
+  };
   const int64_t len = P.cache_len[b];
   const bool bad_len = len < 0 || len > min(capacity(P.c), static_cast<int64_t>(P.positions)) ||
                        min(len, static_cast<int64_t>(P.keep)) > capacity(P.d);
@@ -101,8 +110,10 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const Cach
   const int slice = ((M + ranks - 1) / ranks + 31) / 32 * 32;
   const int from = min(rank * slice, M), mine = min(slice, M - from);
   const bool in_shared = slice <= slice_room;
-  if (in_shared)
+  if (in_shared) {
+#pragma unroll 8
     for (int i = tid; i < mine; i += kSelectThreads) s_key[i] = weight_key(w[from + i]);
+  }
   auto key_at = [&](int i) { return in_shared ? s_key[i] : weight_key(w[from + i]); };
 
   // The want-th largest key, digit by digit; `left` of those equal to it are kept.  All keys when all are kept.
@@ -128,74 +139,93 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const Cach
           atomicAdd(&sh.hist[bin], 1);
         }
       }
-      cluster.sync();
-      // thread t: bins from the top, two at a time; the digit is where their running sum reaches `left`
-      int here[2] = {0, 0};
-      const int top = bins - 1 - 2 * tid;
-      if (top > 0) {
-        for (int r = 0; r < ranks; ++r) {
-          const int *other = cluster.map_shared_rank(sh.hist, r);
-          here[0] += other[top];
-          here[1] += other[top - 1];
-        }
+      meet();
+      const int *totals = sh.hist;
+      if (ranks > 1) {  // each CTA adds up its share of the bins and gives the sums to all
+        totals = sh.total;
+        const int share = bins / ranks, first = rank * share;
+        for (int i = tid; i < share; i += kSelectThreads) sh.sum[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < bins; i += kSelectThreads)
+          atomicAdd(&sh.sum[i % share], cluster.map_shared_rank(sh.hist, i / share)[first + i % share]);
+        __syncthreads();
+        for (int i = tid; i < bins; i += kSelectThreads)
+          cluster.map_shared_rank(sh.total, i / share)[first + i % share] = sh.sum[i % share];
+        cluster.sync();
       }
+      // thread t: bins from the top, two at a time; the digit is where their running sum reaches `left`
+      const int top = bins - 1 - 2 * tid;
+      const int here0 = top > 0 ? totals[top] : 0, here1 = top > 0 ? totals[top - 1] : 0;
       int all;
-      const int before = block_rank(here[0] + here[1], sh.warp, all);
-      if (top > 0 && before < left && before + here[0] + here[1] >= left) {
-        const bool second = before + here[0] < left;
+      const int before = block_rank(here0 + here1, sh.warp, all);
+      if (top > 0 && before < left && before + here0 + here1 >= left) {
+        const bool second = before + here0 < left;
         sh.digit = top - second;
-        sh.above = before + (second ? here[0] : 0);
+        sh.above = before + (second ? here0 : 0);
       }
       __syncthreads();
       key |= static_cast<uint32_t>(sh.digit) << shift;
       left -= sh.above;
-      cluster.sync();  // every histogram has been read
     }
   }
-  // How many each slice keeps, then its kept positions in order: those above the key, and of those equal to it the first.
-  int above = 0, equal = 0;
+  // A warp to a run of the slice: how many each keeps, then the kept positions in order -- those above the key, and of those
+  // equal to it the first `left`.
+  const int run = (slice + kSelectThreads - 1) / kSelectThreads * 32;
+  const int run0 = min(warp * run, mine), run1 = min(run0 + run, mine);
+  int2 seen = make_int2(0, 0);
   if (want < M) {
-    for (int i = tid; i < mine; i += kSelectThreads) {
-      const uint32_t u = key_at(i);
-      above += u > key;
-      equal += u == key;
+    for (int i0 = run0; i0 < run1; i0 += 32) {
+      const int i = i0 + lane;
+      const uint32_t u = i < run1 ? key_at(i) : 0;
+      seen.x += __popc(__ballot_sync(~0u, i < run1 && u > key));
+      seen.y += __popc(__ballot_sync(~0u, i < run1 && u == key));
     }
-    int all_above, all_equal;
-    block_rank(above, sh.warp, all_above);
-    block_rank(equal, sh.warp, all_equal);
-    if (tid == 0) sh.count[0] = all_above, sh.count[1] = all_equal;
+  } else {
+    seen.x = run1 - run0;
   }
-  cluster.sync();
-  int out = from;  // (all kept: in place)
-  int ties_before = 0;
-  if (want < M) {
-    out = 0;
-    for (int r = 0; r < rank; ++r) {
-      const int *other = cluster.map_shared_rank(sh.count, r);
-      const int ties = min(other[1], max(left - ties_before, 0));
-      out += other[0] + ties;
-      ties_before += other[1];
+  if (lane == 0) sh.counts[warp] = seen;
+  __syncthreads();
+  // running sums over the warps
+  int2 c = sh.counts[lane];
+  const int2 own = c;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(~0u, c.x, o), y = __shfl_up_sync(~0u, c.y, o);
+    if (lane >= o) c.x += x, c.y += y;
+  }
+  int out = __shfl_sync(~0u, c.x - own.x, warp), ties = __shfl_sync(~0u, c.y - own.y, warp);
+  if (ranks > 1) {
+    if (tid == 31) sh.count = c;
+    cluster.sync();
+    if (warp == 0) {
+      int2 other = lane < rank ? *cluster.map_shared_rank(&sh.count, lane) : make_int2(0, 0);
+      for (int o = 16; o > 0; o >>= 1) {
+        other.x += __shfl_xor_sync(~0u, other.x, o);
+        other.y += __shfl_xor_sync(~0u, other.y, o);
+      }
+      if (lane == 0) sh.before = other;
     }
+    cluster.sync();  // (and no CTA leaves while its counts are read)
+    out += sh.before.x;
+    ties += sh.before.y;
   }
-  cluster.sync();  // no CTA leaves while its counts are read
-  for (int i0 = 0; i0 < mine; i0 += kSelectThreads) {
-    const int i = i0 + tid;
-    const uint32_t u = i < mine ? key_at(i) : 0;
-    bool take = i < mine;
+  out += min(ties, left);  // of the ties before, the kept ones (left is 0 where all are kept: no ties were counted)
+  for (int i0 = run0; i0 < run1; i0 += 32) {
+    const int i = i0 + lane;
+    bool take = i < run1;
     if (want < M) {
-      const bool tie = i < mine && u == key;
-      int ties;
-      const int before = block_rank(tie, sh.warp, ties);
-      take = i < mine && (u > key || (tie && ties_before + before < left));
-      ties_before += ties;
+      const uint32_t u = i < run1 ? key_at(i) : 0;
+      const bool tie = i < run1 && u == key;
+      const uint32_t votes = __ballot_sync(~0u, tie);
+      take = i < run1 && (u > key || (tie && ties + __popc(votes & ((1u << lane) - 1)) < left));
+      ties += __popc(votes);
     }
-    int taken;
-    const int at = block_rank(take, sh.warp, taken);
+    const uint32_t votes = __ballot_sync(~0u, take);
     if (take) {
-      kept[out + at] = from + i;
-      if (kw) kw[out + at] = w[from + i];
+      const int at = out + __popc(votes & ((1u << lane) - 1));
+      kept[at] = from + i;
+      if (kw) kw[at] = w[from + i];
     }
-    out += taken;
+    out += __popc(votes);
   }
 }
 
@@ -212,54 +242,59 @@ __device__ __forceinline__ uint32_t most_of(const uint4 &v) {
   return max(most & 0xff, most >> 8 & 0xff);
 }
 
-constexpr int kGatherHeld = 4;  // 16-byte pieces that a thread holds: 128 rows of 128 bytes to a CTA
+constexpr int kGatherHeld = 4;  // 16-byte pieces that a thread holds
 
-__global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const CacheEvictParams P, int pages) {
+// TEAM threads to a block, so that each has about four pieces of it.
+template <int TEAM>
+__global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const CacheEvictParams P, int pages, uint32_t blocks) {
   __shared__ float s_max[kGatherThreads / 32];
-  __shared__ const uint8_t *s_row[256];
-  __shared__ float s_scale[256];
-  uint32_t x = blockIdx.x;
+  const int tid = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
+  uint32_t x = blockIdx.x * (kGatherThreads / TEAM) + team;
+  const bool real = x < blocks;
+  x = min(x, blocks - 1);
   const bool is_v = x & 1;
   x >>= 1;
   const int w = static_cast<int>(x % pages);
   x /= pages;
   const int head = static_cast<int>(x % P.c.kv_heads), b = static_cast<int>(x / P.c.kv_heads);
-  const int tid = threadIdx.x, D = P.c.head_dim, shift = P.c.page_shift;
-  const int rows = min(P.new_len[b] - (w << shift), 1 << shift);
-  if (rows <= 0) return;
+  const int D = P.c.head_dim, shift = P.c.page_shift;
+  pdl_wait();
+  const int rows = real ? min(P.new_len[b] - (w << shift), 1 << shift) : 0;
   const int32_t *kept = P.kept + (static_cast<int64_t>(b) * P.c.kv_heads + head) * P.keep + (w << shift);
-  if (tid < rows) {
-    const int t = kept[tid], page = page_at(P.c, b, t >> shift);
-    s_row[tid] = (is_v ? P.c.v : P.c.k) + block_offset(P.c, page, head) + static_cast<int64_t>(t & ((1 << shift) - 1)) * D;
-    s_scale[tid] = (is_v ? P.c.v_scale : P.c.k_scale)[page * P.c.scale_stride + head];
-  }
-  __syncthreads();
-  const int per_row = D / 16, pieces = rows * per_row;
+  const uint8_t *pool = is_v ? P.c.v : P.c.k;
+  const float *scales = is_v ? P.c.v_scale : P.c.k_scale;
+  const int per_row = D / 16, pieces = max(rows, 0) * per_row;
+  auto load = [&](int i, uint4 &v, float &s) {
+    const int r = i / per_row, t = kept[r], page = page_at(P.c, b, t >> shift);
+    v = reinterpret_cast<const uint4 *>(pool + block_offset(P.c, page, head) + static_cast<int64_t>(t & ((1 << shift) - 1)) * D)[i - r * per_row];
+    s = scales[page * P.c.scale_stride + head];
+  };
   uint4 held[kGatherHeld];
-  float amax = 0.0f;
+  float from[kGatherHeld], amax = 0.0f;
 #pragma unroll
-  for (int k = 0; k < kGatherHeld; ++k) {
-    const int i = tid + k * kGatherThreads;
-    if (i < pieces) held[k] = reinterpret_cast<const uint4 *>(s_row[i / per_row])[i % per_row];
-  }
-  auto piece_max = [&](int i, const uint4 &v) { amax = fmaxf(amax, e4m3x2_to_float2(most_of(v)).x * s_scale[i / per_row]); };
+  for (int k = 0; k < kGatherHeld; ++k)
+    if (tid + k * TEAM < pieces) load(tid + k * TEAM, held[k], from[k]);
 #pragma unroll
-  for (int k = 0; k < kGatherHeld; ++k) {
-    const int i = tid + k * kGatherThreads;
-    if (i < pieces) piece_max(i, held[k]);
+  for (int k = 0; k < kGatherHeld; ++k)
+    if (tid + k * TEAM < pieces) amax = fmaxf(amax, e4m3x2_to_float2(most_of(held[k])).x * from[k]);
+  for (int i = tid + kGatherHeld * TEAM; i < pieces; i += TEAM) {
+    uint4 v;
+    float s;
+    load(i, v, s);
+    amax = fmaxf(amax, e4m3x2_to_float2(most_of(v)).x * s);
   }
-  for (int i = tid + kGatherHeld * kGatherThreads; i < pieces; i += kGatherThreads)
-    piece_max(i, reinterpret_cast<const uint4 *>(s_row[i / per_row])[i % per_row]);
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-  if ((tid & 31) == 0) s_max[tid >> 5] = amax;
-  __syncthreads();
+  if (TEAM > 32) {
+    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kGatherThreads / 32; ++i) amax = fmaxf(amax, s_max[i]);
+    for (int i = 0; i < TEAM / 32; ++i) amax = fmaxf(amax, s_max[team * (TEAM / 32) + i]);
+  }
+  if (rows <= 0) return;
   const float scale = block_scale(amax), inv = 1.0f / scale;  // (a power of two: exact)
   const int page = page_at(P.d, b, w);
   uint4 *to = reinterpret_cast<uint4 *>((is_v ? P.d.v : P.d.k) + block_offset(P.d, page, head));
-  auto put = [&](int i, uint4 v) {
-    const float s = s_scale[i / per_row];
+  auto put = [&](int i, uint4 v, float s) {
     if (s != scale) {
       uint32_t *u = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
@@ -271,13 +306,31 @@ __global__ void __launch_bounds__(kGatherThreads) cache_gather_kernel(const Cach
     to[i] = v;
   };
 #pragma unroll
-  for (int k = 0; k < kGatherHeld; ++k) {
-    const int i = tid + k * kGatherThreads;
-    if (i < pieces) put(i, held[k]);
+  for (int k = 0; k < kGatherHeld; ++k)
+    if (tid + k * TEAM < pieces) put(tid + k * TEAM, held[k], from[k]);
+  for (int i = tid + kGatherHeld * TEAM; i < pieces; i += TEAM) {
+    uint4 v;
+    float s;
+    load(i, v, s);
+    put(i, v, s);
   }
-  for (int i = tid + kGatherHeld * kGatherThreads; i < pieces; i += kGatherThreads)
-    put(i, reinterpret_cast<const uint4 *>(s_row[i / per_row])[i % per_row]);
   if (tid == 0) (is_v ? P.d.v_scale : P.d.k_scale)[page * P.d.scale_stride + head] = scale;
+}
+
+template <int TEAM>
+cudaError_t launch_gather(const CacheEvictParams &P, cudaStream_t st) {
+  const int pages = (P.keep + (1 << P.c.page_shift) - 1) >> P.c.page_shift;
+  const uint32_t blocks = 2u * P.B * P.c.kv_heads * pages;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((blocks + kGatherThreads / TEAM - 1) / (kGatherThreads / TEAM));
+  cfg.blockDim = dim3(kGatherThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = trace_enabled() ? 0 : 1;
+  return trace_launch_ex("cache_gather", st, [&] { return cudaLaunchKernelEx(&cfg, cache_gather_kernel<TEAM>, P, pages, blocks); });
 }
 
 // CTAs to a (request, head): enough for a slice of a few thousand positions,
@@ -319,10 +372,12 @@ cudaError_t launch_cache_evict(const CacheEvictParams &P, cudaStream_t st) {
   cfg.numAttrs = 1;
   e = trace_launch_ex("cache_select", st, [&] { return cudaLaunchKernelEx(&cfg, cache_select_kernel, P, room); });
   if (e != cudaSuccess) return e;
-  const int pages = (P.keep + (1 << P.c.page_shift) - 1) >> P.c.page_shift;
-  return trace_launch("cache_gather", st, [&] {
-    cache_gather_kernel<<<2 * heads * pages, kGatherThreads, 0, st>>>(P, pages);
-  });
+  // four pieces to a thread
+  const int pieces = (P.c.head_dim << P.c.page_shift) / 16;
+  if (pieces <= 128) return launch_gather<32>(P, st);
+  if (pieces <= 256) return launch_gather<64>(P, st);
+  if (pieces <= 512) return launch_gather<128>(P, st);
+  return launch_gather<256>(P, st);
 }
 
 }  // namespace sv
