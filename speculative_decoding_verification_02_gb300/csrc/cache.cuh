@@ -166,6 +166,27 @@ __device__ __forceinline__ float row_value(const char *p, int64_t i) {
   else return __half2float(reinterpret_cast<const __half *>(p)[i]);
 }
 
+// A lane's 2 or 4 consecutive values of a row, from one load.
+template <int DT, int EACH>
+__device__ __forceinline__ void load_each(const char *row, int lane, float *x) {
+  uint32_t w[EACH / 2];
+  if constexpr (EACH == 4) {
+    const uint2 v = reinterpret_cast<const uint2 *>(row)[lane];
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = reinterpret_cast<const uint32_t *>(row)[lane];
+  }
+#pragma unroll
+  for (int e = 0; e < EACH / 2; ++e) {
+    if constexpr (DT == SPEC_DTYPE_BF16) {
+      x[2 * e] = __uint_as_float(w[e] << 16), x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+      x[2 * e] = f.x, x[2 * e + 1] = f.y;
+    }
+  }
+}
+
 // Rounded once, to nearest even.
 template <int DT>
 __device__ __forceinline__ void put_value(char *p, int64_t i, float x) {

@@ -179,27 +179,6 @@ __device__ __forceinline__ int swizzled(int row, int chunk) {
   return D == 128 ? chunk ^ (row & 7) : chunk ^ (row >> 1 & 3);
 }
 
-// A lane's 2 or 4 consecutive values of a row, from one load.
-template <int DT, int EACH>
-__device__ __forceinline__ void load_each(const char *row, int lane, float *x) {
-  uint32_t w[EACH / 2];
-  if constexpr (EACH == 4) {
-    const uint2 v = reinterpret_cast<const uint2 *>(row)[lane];
-    w[0] = v.x, w[1] = v.y;
-  } else {
-    w[0] = reinterpret_cast<const uint32_t *>(row)[lane];
-  }
-#pragma unroll
-  for (int e = 0; e < EACH / 2; ++e) {
-    if constexpr (DT == SPEC_DTYPE_BF16) {
-      x[2 * e] = bf16_lo(w[e]), x[2 * e + 1] = bf16_hi(w[e]);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
-      x[2 * e] = f.x, x[2 * e + 1] = f.y;
-    }
-  }
-}
-
 // Two values in the rows' type, the first in the low half.
 template <int DT>
 __device__ __forceinline__ uint32_t pair_bits(float lo, float hi) {

@@ -3,10 +3,16 @@
 //   out_j = prev_j + sum over rows of exp(x_rj - lse_r)
 //
 // A thread owns a position, so the sum is over a thread's own registers, in
-// the rows' order: no atomics, the same bits on every run.
+// the rows' order: no atomics, the same bits on every run.  Heads of 64 and 128
+// take the scores from the tensor cores (cache_weights_tile_kernel), other
+// widths a dot product to a thread.
+#include <algorithm>
+#include <atomic>
+
 #include "cache.cuh"
 #include "common.cuh"
 #include "launch.h"
+#include "tcgen05.cuh"
 
 namespace sv {
 namespace {
@@ -89,9 +95,400 @@ __global__ void __launch_bounds__(kSpan) cache_weights_rows_kernel(const CacheWe
   P.out[b * P.out_s[0] + head * P.out_s[1] + j] = prev + total;
 }
 
+// ---------------------------------------------------------------- tensor cores
+//
+// S^T = K Q^T by kind::f8f6f4: 128 positions are the operand's rows, straight
+// from the pool, and the query rows its columns, so that a position's scores
+// are all in one lane of tensor memory.  A row of q, scaled by a power of two
+// to at most 256, is the sum of e4m3 numbers x0 + x1 / 16 + x2 / 256 (the last
+// for fp16 alone), each a column of its own: nothing is lost of a bf16, and
+// what is left of small elements is 2^-14 against a largest of 128 or more.
+//
+// The tiles of all (request, head) units are laid end to end and cut evenly
+// over the CTAs.  Rows are taken RC at a time (16, 32 or 64); further rows of a
+// unit go over its tiles again, adding to what is there.  Two groups of four
+// warps take alternate tiles.  Bound by reading K (head_dim bytes a position
+// and kv head) for few rows, by the exponentials for many.
+
+constexpr int kTile = kTilePositions;
+constexpr int kThreads = 320;  // two groups of 4 summing warps, 1 loading, 1 issuing
+constexpr int kRing = 8;
+constexpr int kMaxRows = 64;   // RC at most
+
+template <int DT, int D>
+struct WeightShape {
+  static constexpr int kPieces = DT == SPEC_DTYPE_BF16 ? 2 : 3;
+  static constexpr int kStage = kTile * D;
+  static constexpr int kStages = D == 128 ? 8 : 12;
+  static constexpr int kQ = 0;
+  static constexpr int kK = kPieces * kMaxRows * D;
+  static constexpr int kSmall = kK + kStages * kStage;
+  static constexpr int kBytes = kSmall + 8192 + 1024;
+};
+
+struct WeightSmall {
+  int start[kTileRequests + 1];  // running sum of the requests' tiles
+  int2 lens[kTileRequests];      // context, rows
+  float2 row[kMaxRows];          // factor of a row's scores, its lse; both in units of log 2
+  int token[kMaxRows];           // its place behind the context
+  float ring[kRing][8];          // k_scale of 16 positions
+  uint64_t k_full[12], k_empty[12], s_full[2], s_empty[2], q_full, meet, ring_full[kRing], ring_empty[kRing];
+  uint32_t tmem;
+  int bad[2], dead;
+};
+static_assert(sizeof(WeightSmall) <= 8192);
+
+struct WeightUnit {
+  int b, head, base, cnt, T, tile0, tiles;  // b: within the launch
+};
+
+__device__ __noinline__ WeightUnit weight_unit(const WeightSmall &sm, int count, int heads, int t) {
+  int lo = 0, hi = count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (sm.start[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  WeightUnit u;
+  u.b = lo;
+  u.base = sm.lens[lo].x;
+  u.cnt = sm.lens[lo].y;
+  u.T = u.base + u.cnt;
+  u.tiles = (u.T + kTile - 1) / kTile;
+  u.head = (t - sm.start[lo]) / u.tiles;
+  u.tile0 = sm.start[lo] + u.head * u.tiles;
+  return u;
+}
+
+__device__ __forceinline__ bool weight_lengths(const CacheWeightsParams &P, int b, int &base, int &cnt) {
+  base = P.cache_len[b];
+  cnt = P.counts ? P.counts[b] : P.n_rows;
+  return base >= 0 && cnt >= 0 && cnt <= P.n_rows &&
+         base + static_cast<int64_t>(cnt) <= min(capacity(P.c), static_cast<int64_t>(P.positions));
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    cache_weights_tile_kernel(const CacheWeightsParams P, int first, int count, int rc, int page_rows, bool q_vec,
+                              const __grid_constant__ CUtensorMap k_map) {
+  using S = WeightShape<DT, D>;
+  extern __shared__ char raw[];
+  char *const smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  WeightSmall &sm = *reinterpret_cast<WeightSmall *>(smem + S::kSmall);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, ctas = gridDim.x, heads = P.c.kv_heads;
+
+  if (tid == 0) {
+    for (int i = 0; i < S::kStages; ++i) bar_init(&sm.k_full[i], 1), bar_init(&sm.k_empty[i], 1);
+    for (int i = 0; i < 2; ++i) bar_init(&sm.s_full[i], 2), bar_init(&sm.s_empty[i], 128);
+    bar_init(&sm.q_full, 256);
+    bar_init(&sm.meet, 256);
+    for (int i = 0; i < kRing; ++i) bar_init(&sm.ring_full[i], 32), bar_init(&sm.ring_empty[i], 128);
+    bar_init_fence();
+    sm.dead = sm.bad[0] = sm.bad[1] = 0;
+  }
+  if (warp == 9) tmem_alloc(&sm.tmem, 512);
+  for (int b = tid; b < count; b += kThreads) {
+    int base, cnt;
+    const bool ok = weight_lengths(P, first + b, base, cnt);
+    sm.lens[b] = make_int2(base, cnt);
+    sm.start[b + 1] = ok ? (base + cnt + kTile - 1) / kTile * heads : 0;
+    // (a request without positions has its status from here)
+    if (cta == 0 && P.status && !(ok && base + cnt > 0)) P.status[first + b] = ok ? SPEC_STATUS_OK : SPEC_STATUS_BAD_LENGTH;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) {
+    int carry = 0;
+    for (int b0 = 0; b0 < count; b0 += 32) {
+      int x = b0 + lane < count ? sm.start[b0 + lane + 1] : 0;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, x, o);
+        if (lane >= o) x += y;
+      }
+      x += carry;
+      if (b0 + lane < count) sm.start[b0 + lane + 1] = x;
+      carry = __shfl_sync(~0u, x, 31);
+    }
+    if (lane == 0) sm.start[0] = 0;
+  }
+  __syncthreads();
+  const int total = sm.start[count];
+  const int lo = static_cast<int>(static_cast<int64_t>(total) * cta / ctas);
+  const int hi = static_cast<int>(static_cast<int64_t>(total) * (cta + 1) / ctas);
+  const uint32_t tmem = sm.tmem;
+  volatile int *dead = &sm.dead;
+  auto chunks_of = [&](const WeightUnit &u) { return max(1, (u.cnt * P.group + rc - 1) / rc); };  // (no rows: prev is copied)
+
+  if (warp == 8) {
+    // ---- loading K and its scales: a lane to 16 positions (the first 8 lanes); the next tile's page is looked up meanwhile
+    const int shift = P.c.page_shift;
+    int stage = 0, lap = 0, i = 0;
+    bool ok = true;
+    for (int t = lo; t < hi && ok;) {
+      const WeightUnit u = weight_unit(sm, count, heads, t);
+      const int end = min(hi, u.tile0 + u.tiles), chunks = chunks_of(u);
+      for (int c = 0; c < chunks && ok; ++c) {
+        auto page_of = [&](int k) {
+          const int pos = (k - u.tile0) * kTile + lane * 16;
+          return k < end && lane < 8 && pos < u.T ? page_at(P.c, first + u.b, pos >> shift) : -1;
+        };
+        auto scale_of = [&](int page) { return page >= 0 ? P.c.k_scale[page * P.c.scale_stride + u.head] : 1.0f; };
+        int page = page_of(t), page1 = page_of(t + 1);
+        float scale = scale_of(page);
+        for (int k = t; k < end; ++k, ++i) {
+          const float scale1 = scale_of(page1);
+          const int page2 = page_of(k + 2), pos = (k - u.tile0) * kTile + lane * 16, r = i % kRing;
+          if (i >= kRing && !(ok = warp_wait(&sm.ring_empty[r], (i / kRing - 1) & 1, dead))) break;
+          if (lane < 8) sm.ring[r][lane] = scale;
+          bar_arrive(&sm.ring_full[r]);
+          const bool load = page >= 0 && (pos & (page_rows - 1)) == 0;
+          const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(~0u, load)) * page_rows * D);
+          if (lap > 0 && !(ok = warp_wait(&sm.k_empty[stage], (lap - 1) & 1, dead))) break;
+          if (lane == 0) bar_expect(&sm.k_full[stage], bytes);
+          __syncwarp();
+          if (load)
+            tensor_load_3d(smem + S::kK + stage * S::kStage + lane * 16 * D, &k_map, 0, (u.head << shift) + (pos & ((1 << shift) - 1)), page,
+                           &sm.k_full[stage]);
+          if (++stage == S::kStages) stage = 0, ++lap;
+          page = page1, page1 = page2, scale = scale1;
+        }
+      }
+      t = end;
+    }
+    __syncwarp();
+    if (*dead)  // the copies in flight land before the CTA leaves
+      for (int s = 0; s < S::kStages; ++s)
+        for (int k = 0; k < 4096 && !bar_try(&sm.k_full[s], 0) && !bar_try(&sm.k_full[s], 1); ++k) {}
+  } else if (warp == 9) {
+    // ---- issuing S^T = K Q^T
+    constexpr uint64_t kSw = D == 128 ? kSwizzle128 : kSwizzle64;
+    const uint32_t idesc = mma_desc(S::kPieces * rc, false);
+    const uint64_t q_desc = matrix_desc(smem_u32(smem + S::kQ), 16, 8 * D, kSw);
+    const uint64_t k_desc = matrix_desc(smem_u32(smem + S::kK), 16, 8 * D, kSw);
+    int stage = 0, lap = 0, i = 0, writes = 0;
+    bool ok = true;
+    for (int t = lo; t < hi && ok;) {
+      const WeightUnit u = weight_unit(sm, count, heads, t);
+      const int end = min(hi, u.tile0 + u.tiles), chunks = chunks_of(u);
+      for (int c = 0; c < chunks && ok; ++c) {
+        if (!(ok = warp_wait(&sm.q_full, writes++ & 1, dead))) break;
+        for (int k = t; k < end; ++k, ++i) {
+          if (i >= 2 && !(ok = warp_wait(&sm.s_empty[i & 1], (i / 2 - 1) & 1, dead))) break;
+          if (!(ok = warp_wait(&sm.ring_full[i % kRing], (i / kRing) & 1, dead))) break;
+          if (lane == 0) bar_arrive(&sm.s_full[i & 1]);  // (with this arrival S full says that the tile's scales are there too)
+          if (!(ok = warp_wait(&sm.k_full[stage], lap & 1, dead))) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e)
+              mma_f8(tmem + (i & 1) * 256, k_desc + ((stage * S::kStage + e * 32) >> 4), q_desc + ((e * 32) >> 4), idesc, e > 0);
+            tc_commit(&sm.k_empty[stage]);
+            tc_commit(&sm.s_full[i & 1]);
+          }
+          __syncwarp();
+          if (++stage == S::kStages) stage = 0, ++lap;
+        }
+      }
+      t = end;
+    }
+  } else {
+    // ---- summing
+    const int side = warp >> 2, quarter = warp & 3, spot = quarter * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
+    const bool negative = P.scale < 0.0f, capped = P.softcap > 0.0f;
+    const float cap2 = P.softcap * kLog2e, in_cap = capped ? 2.0f / P.softcap : 0.0f;
+    uint32_t meetings = 0;
+    auto together = [&] {
+      bar_arrive(&sm.meet);
+      return warp_wait(&sm.meet, meetings++ & 1, dead);
+    };
+    int i = 0, segment = 0;
+    bool ok = true;
+    for (int t = lo; t < hi && ok; ++segment) {
+      const WeightUnit u = weight_unit(sm, count, heads, t);
+      const int end = min(hi, u.tile0 + u.tiles), chunks = chunks_of(u), b = first + u.b, rows = u.cnt * P.group;
+      const int32_t *index = P.index ? P.index + static_cast<int64_t>(b) * P.index_stride : nullptr;
+      // the request's pages and indexes: a bad one takes the request out
+      int bad = 0;
+      for (int k = tid; static_cast<int64_t>(k) << P.c.page_shift < u.T; k += 256) bad |= page_at(P.c, b, k) < 0 ? 1 : 0;
+      if (index)
+        for (int k = tid; k < u.cnt; k += 256) bad |= index[k] < 0 || index[k] >= P.N ? 2 : 0;
+      bad = __reduce_or_sync(~0u, bad);
+      if (lane == 0 && bad) atomicOr(&sm.bad[segment & 1], bad);
+      for (int c = 0; c < chunks && ok; ++c) {
+        const int row0 = c * rc, here = min(rc, rows - row0), padded = (here + 15) / 16 * 16;
+        // every product that reads the rows before has completed for both sides
+        if (!(ok = together())) break;
+        if (c == 0) {
+          bad = sm.bad[segment & 1];
+          if (tid == 0) sm.bad[(segment + 1) & 1] = 0;  // (the segment before's; the next one's is set after the next meeting)
+          if (tid == 0 && u.head == 0 && u.tile0 >= lo && P.status)
+            P.status[b] = bad & 1 ? SPEC_STATUS_BAD_PAGE : bad & 2 ? SPEC_STATUS_BAD_INDEX : SPEC_STATUS_OK;
+        }
+        constexpr int kEach = D / 32;
+#pragma unroll 1
+        for (int r0 = warp; r0 < padded; r0 += 16) {  // two rows side by side
+          float x[2][kEach], top[2];
+          int ex[2], tok[2], at[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int r = r0 + 8 * k, row = row0 + r;
+            tok[k] = row / P.group;
+            const bool real = r < here;
+            at[k] = real ? (index ? index[tok[k]] : tok[k]) : -1;
+            if (at[k] < 0 || at[k] >= P.N) at[k] = -1;
+            const int h = u.head * P.group + row - tok[k] * P.group;
+            const char *q = P.q + (b * P.qs[0] + max(at[k], 0) * P.qs[1] + h * P.qs[2]) * 2;
+            top[k] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) x[k][e] = 0.0f;
+            if (at[k] >= 0) {
+              if (q_vec) load_each<DT, kEach>(q, lane, x[k]);
+              else
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) x[k][e] = row_value<DT>(q, lane * kEach + e);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+              if (negative) x[k][e] = -x[k][e];
+              top[k] = fmaxf(top[k], finite_abs(x[k][e]));
+            }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) top[k] = fmaxf(top[k], __shfl_xor_sync(~0u, top[k], o));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int r = r0 + 8 * k;
+            if (r >= padded) break;
+            // 2^ex with top / 2^ex in [128, 256)
+            ex[k] = top[k] > 0.0f ? max(static_cast<int>(__float_as_uint(top[k]) >> 23) - 127 - 7, -110) : 0;
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - ex[k]) << 23);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) x[k][e] *= down;
+#pragma unroll
+            for (int piece = 0; piece < S::kPieces; ++piece) {
+              uint32_t code = 0;
+#pragma unroll
+              for (int e = 0; e < kEach; e += 2) {
+                const uint32_t two = to_e4m3x2(x[k][e], x[k][e + 1]);
+                const float2 back = e4m3x2_to_float2(two);
+                x[k][e] = (x[k][e] - back.x) * 16.0f;
+                x[k][e + 1] = (x[k][e + 1] - back.y) * 16.0f;
+                code |= two << (8 * e);
+              }
+              const int a = piece * rc + r, chunk = lane * kEach >> 4;
+              char *to = smem + S::kQ + a * D + ((D == 128 ? chunk ^ (a & 7) : chunk ^ (a >> 1 & 3)) << 4) + (lane * kEach & 15);
+              if (kEach == 4) *reinterpret_cast<uint32_t *>(to) = code;
+              else *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(code);
+            }
+            if (lane == 0) {
+              const int h = u.head * P.group + row0 + r - tok[k] * P.group;
+              float z = at[k] >= 0 ? P.lse[(static_cast<int64_t>(b) * P.N + at[k]) * P.Hq + h] : -INFINITY;
+              if (z == -INFINITY) z = INFINITY;  // nothing comes of the row
+              sm.row[r] = make_float2(fabsf(P.scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(ex[k] + 127) << 23), z * kLog2e);
+              sm.token[r] = tok[k];
+            }
+          }
+        }
+        fence_async_shared();
+        bar_arrive(&sm.q_full);
+        if (!(ok = together())) break;
+
+        for (int k = t; k < end; ++k, ++i) {
+          if ((i & 1) != side) continue;
+          const int ring = i % kRing, j = (k - u.tile0) * kTile + spot;
+          const bool mine = j < u.T && !bad;
+          const bool edge = (k - u.tile0) * kTile + kTile > u.base;
+          float *out = P.out + b * P.out_s[0] + u.head * P.out_s[1] + j;
+          float sum = 0.0f, held = 0.0f;
+          if (mine) held = c > 0 ? *out : P.prev ? P.prev[b * P.prev_s[0] + u.head * P.prev_s[1] + j] : 0.0f;
+          if (!(ok = warp_wait(&sm.s_full[side], (i >> 1) & 1, dead))) break;
+          tc_fence_after();
+          const float ks = sm.ring[ring][spot >> 4];
+          bar_arrive(&sm.ring_empty[ring]);
+#pragma unroll 1
+          for (int r = 0; r < padded; r += 16) {
+            float x[16], y[16];
+            const uint32_t at = tmem + lanes + side * 256 + r;
+            tmem_ld16(at, x);
+            tmem_ld16(at + rc, y);
+            if (S::kPieces == 3) {
+              float z[16];
+              tmem_ld16(at + 2 * rc, z);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) y[e] = fmaf(z[e], 1.0f / 16, y[e]);
+            } else {
+              tc_wait_ld();
+            }
+            float part[2] = {};
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 f = sm.row[r + e];
+              float s = fmaf(y[e], 1.0f / 16, x[e]) * (f.x * ks);
+              if (capped) {
+                const float z = s * in_cap;
+                s = cap2 * (1.0f - __fdividef(2.0f, 1.0f + ex2(z > 120.0f ? 120.0f : z)));
+              }
+              float p = ex2(s - f.y);
+              if (edge && j - u.base > sm.token[r + e]) p = 0.0f;
+              part[e & 1] += p;
+            }
+            sum += part[0] + part[1];
+          }
+          tc_fence_before();
+          bar_arrive(&sm.s_empty[side]);
+          if (mine) *out = held + sum;
+        }
+      }
+      t = end;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (sm.dead && P.status)  // a wait ran out: what the CTA worked on is void
+    for (int b = tid; b < count; b += kThreads) P.status[first + b] = SPEC_STATUS_TIMEOUT;
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+std::atomic<uint64_t> weights_ready[4];
+
+template <int DT, int D>
+cudaError_t launch_weight_tiles(const CacheWeightsParams &P, cudaStream_t st) {
+  using S = WeightShape<DT, D>;
+  auto kern = cache_weights_tile_kernel<DT, D>;
+  cudaError_t e = once_per_device([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes); },
+                                  weights_ready[(DT == SPEC_DTYPE_BF16) * 2 + (D == 128)]);
+  if (e != cudaSuccess) return e;
+  const int page_rows = std::min(1 << P.c.page_shift, kTile);
+  CUtensorMap map;
+  if ((e = cache_k_map(P.c, page_rows, &map)) != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(P.n_rows) * P.group;
+  const int rc = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  const bool q_vec = reinterpret_cast<uintptr_t>(P.q) % 8 == 0 && P.qs[0] % 4 == 0 && P.qs[1] % 4 == 0 && P.qs[2] % 4 == 0;
+  for (int first = 0; first < P.B; first += kTileRequests) {
+    const int count = std::min(kTileRequests, P.B - first);
+    e = trace_launch("cache_weights_tile", st,
+                     [&] { kern<<<device_sm_count(), kThreads, S::kBytes, st>>>(P, first, count, rc, page_rows, q_vec, map); });
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
 }  // namespace
 
 cudaError_t launch_cache_weights(const CacheWeightsParams &P, cudaStream_t st) {
+  if (P.c.head_dim == 128) return P.dtype == SPEC_DTYPE_BF16 ? launch_weight_tiles<SPEC_DTYPE_BF16, 128>(P, st) : launch_weight_tiles<SPEC_DTYPE_F16, 128>(P, st);
+  if (P.c.head_dim == 64) return P.dtype == SPEC_DTYPE_BF16 ? launch_weight_tiles<SPEC_DTYPE_BF16, 64>(P, st) : launch_weight_tiles<SPEC_DTYPE_F16, 64>(P, st);
   const int64_t most = static_cast<int64_t>(P.c.table_stride) << P.c.page_shift;
   const int spans = most > 0 ? static_cast<int>((most + kSpan - 1) / kSpan) : 1;
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(spans) * P.c.kv_heads * P.B);

@@ -580,3 +580,51 @@ def test_bindings_refuse(api):
         api.spec_cache_evict(cache, table, ln, torch.zeros(2, 2, 32, device="cuda"), 0, 0, table)
     with pytest.raises(TypeError):
         api.spec_cache_evict(cache, table, ln, torch.zeros(2, 3, 32, device="cuda"), 4, 0, table)
+
+
+def test_weights_without_rows_copies_prev(api):
+    """counts of 0: out is prev over the context, whatever out held."""
+    cache = rand_cache(api, 8, 2, 64, 128, 66)
+    table = rand_table(2, 4, 8, 67)
+    ln = torch.tensor([150, 0], dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 3, 4, 128, generator=gen(68)).to(BF).cuda()
+    lse = torch.zeros(2, 3, 4, device="cuda")
+    prev = torch.rand(2, 2, 256, generator=gen(69)).cuda()
+    out = torch.full((2, 2, 256), -7.0, device="cuda")
+    api.spec_cache_weights(q, lse, cache, table, ln, prev=prev, counts=torch.zeros(2, dtype=torch.int32, device="cuda"), out=dict(weights=out))
+    assert torch.equal(out[0, :, :150], prev[0, :, :150]) and bool((out[0, :, 150:] == -7).all()) and bool((out[1] == -7).all())
+
+
+@pytest.mark.parametrize("N,G,D,dtype", [(1, 1, 128, BF), (40, 8, 64, HF), (7, 3, 128, HF)])
+def test_weights_many_requests(api, N, G, D, dtype):
+    """More requests than a launch takes, most of them short, some without rows."""
+    B, H, P = 300, 1, 16
+    g = gen(95)
+    lens = torch.randint(0, 60, (B,), generator=g).tolist()
+    lens[7] = 700
+    cnt = torch.randint(0, N + 1, (B,), generator=g).tolist()
+    W = -(-(700 + N) // P)
+    cache = rand_cache(api, B * W, H, P, D, 96)
+    table = rand_table(B, W, B * W, 97)
+    q = torch.randn(B, N, H * G, D, generator=g).to(dtype).cuda()
+    lse = (torch.rand(B, N, H * G, generator=g) * 3 + 3).cuda()
+    prev = torch.rand(B, H, W * P, generator=g).cuda()
+    o = api.spec_cache_weights(q, lse, cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), prev=prev,
+                               counts=torch.tensor(cnt, dtype=torch.int32, device="cuda"))
+    want, tol = ref.weights(ref.Cache64(cache, table), q, lse, lens, cnt, None, D ** -0.5, 0.0, prev)
+    assert bool(((o["weights"].cpu().double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("N,G,D,dtype", [(1, 1, 128, BF), (3, 16, 64, HF), (9, 4, 128, BF), (70, 2, 64, BF)])
+def test_attend_many_requests(api, N, G, D, dtype):
+    """More requests than a launch takes, most of them of a tile or two, so that a CTA goes through many units."""
+    B, H, P = 300, 2, 16
+    g = gen(98)
+    lens = torch.randint(0, 200, (B,), generator=g).tolist()
+    lens[3] = 900
+    nq = torch.randint(0, N + 1, (B,), generator=g).tolist()
+    W = -(-(900 + N) // P)
+    cache = rand_cache(api, B * W, H, P, D, 99)
+    table = rand_table(B, W, B * W, 100)
+    q = torch.randn(B, N, H * G, D, generator=g).to(dtype).cuda()
+    check_attend(api, q, cache, table, lens, n_query=nq)
