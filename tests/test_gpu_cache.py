@@ -628,3 +628,41 @@ def test_attend_many_requests(api, N, G, D, dtype):
     table = rand_table(B, W, B * W, 100)
     q = torch.randn(B, N, H * G, D, generator=g).to(dtype).cuda()
     check_attend(api, q, cache, table, lens, n_query=nq)
+
+
+def test_the_whole_step(api):
+    """The example's step: what is committed, weighed and kept is what the definitions give on its own inputs."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "cached_tree_step.py")
+    spec = importlib.util.spec_from_file_location("cached_tree_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    r = example.step(context=300, keep=90, recent=20, page=64, seed=3)
+    torch.cuda.synchronize()
+    n_emit = r["verdict"]["n_emit"]
+    assert torch.equal(r["committed"]["new_len"], r["length"] + n_emit)
+    for name in ("attended", "committed", "weights", "kept", "drafted"):
+        assert r[name]["status"].tolist() == [0] * 4
+    # committed rows are the path's, rounded at their block's scale
+    c64 = ref.Cache64(r["cache"], r["table"])
+    for b in range(4):
+        n, base = int(n_emit[b]), int(r["length"][b])
+        nodes = r["verdict"]["path_nodes"][b, :n].long()
+        for which, x in ((0, r["k"]), (1, r["v"])):
+            got = c64.rows(which, b, base + n)[:, base:]
+            want = x[b, nodes].cpu().double().transpose(0, 1)
+            scale = torch.stack([c64.scale[which][c64.table[b, (base + i) // 64]] for i in range(n)], 1)[:, :, None]
+            assert torch.equal(got, ref.e4m3(want / scale) * scale)
+    # weights of the accepted rows sum to their number; what is kept are the definition's positions
+    G = r["q"].shape[2] // r["k"].shape[2]
+    total = r["weights"]["weights"].double().sum(2)
+    assert bool(((total - n_emit[:, None].double() * G).abs() < 0.02 * G * n_emit[:, None].double()).all())
+    w = r["weights"]["weights"].cpu()
+    for b in range(4):
+        T = int(r["committed"]["new_len"][b])
+        for h, kept in enumerate(ref.evict(c64, w, b, T, 90, 20)):
+            assert r["kept"]["kept"][b, h, :len(kept)].tolist() == kept
+    out, lse, t_out, t_lse = ref.attend(ref.Cache64(r["cache"], r["small_table"]), r["q1"], r["kept"]["new_len"].tolist(), [1] * 4, None,
+                                        128 ** -0.5, 0.0)
+    assert bool(((r["drafted"]["out"].cpu().double() - out).abs() <= t_out).all())
