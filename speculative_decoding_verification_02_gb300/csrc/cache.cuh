@@ -49,6 +49,7 @@ struct CacheAttendParams {
 
 constexpr int kTilePositions = 128;  // positions to a tile of the tensor-core kernels
 constexpr int kTileRequests = 256;   // requests to one of their launches
+constexpr int kTileUnitCost = 3;     // (cache_attend_tile.cuh)
 
 // A launch of spec_cache_attend's tensor-core path.
 struct CacheTilePlan {
@@ -60,7 +61,7 @@ struct CacheTilePlan {
   int2 *range;           // [CTA] first tile; whether it gave up waiting
   int4 *begun;           // [CTA] the unit that it began and a later one ended
   float2 *ml;           // [CTA][2][rows of a unit]: reference and sum of partial rows
-  float *part;          // [CTA][2][rows of a unit][head_dim]
+  float *part;          // [CTA][2][head_dim / 4][rows of a unit][4]
 };
 
 struct CacheWeightsParams {
@@ -167,15 +168,14 @@ __device__ __forceinline__ float row_value(const char *p, int64_t i) {
 }
 
 // A lane's 2 or 4 consecutive values of a row, from one load.
+template <int EACH>
+__device__ __forceinline__ uint2 raw_each(const char *row, int lane) {
+  if constexpr (EACH == 4) return reinterpret_cast<const uint2 *>(row)[lane];
+  else return make_uint2(reinterpret_cast<const uint32_t *>(row)[lane], 0);
+}
 template <int DT, int EACH>
-__device__ __forceinline__ void load_each(const char *row, int lane, float *x) {
-  uint32_t w[EACH / 2];
-  if constexpr (EACH == 4) {
-    const uint2 v = reinterpret_cast<const uint2 *>(row)[lane];
-    w[0] = v.x, w[1] = v.y;
-  } else {
-    w[0] = reinterpret_cast<const uint32_t *>(row)[lane];
-  }
+__device__ __forceinline__ void unpack_each(const uint2 &v, float *x) {
+  const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
   for (int e = 0; e < EACH / 2; ++e) {
     if constexpr (DT == SPEC_DTYPE_BF16) {

@@ -117,7 +117,7 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 int requests_at_once(const CacheAttendParams &P) {
   const int rt = 128 / copies_of(P.N, P.group);
   const int64_t row_tiles = (static_cast<int64_t>(P.N) * P.group + rt - 1) / rt;
-  const int64_t tiles = ((static_cast<int64_t>(P.c.table_stride) << P.c.page_shift) / kTilePositions + 1) * row_tiles * P.c.kv_heads;
+  const int64_t tiles = ((static_cast<int64_t>(P.c.table_stride) << P.c.page_shift) / kTilePositions + 1 + kTileUnitCost) * row_tiles * P.c.kv_heads;
   return static_cast<int>(std::min<int64_t>(kTileRequests, 2000000000LL / std::max(tiles, row_tiles * rt * P.c.kv_heads)));
 }
 

@@ -43,6 +43,9 @@ namespace {
 // barrier, and halves what a thread does between the two products.
 
 constexpr int kTile = 128;         // positions to a tile
+// What a unit costs a CTA besides its tiles (its q, its end), in tiles: the cuts
+// count it, so that a CTA of many short units gets fewer tiles.
+constexpr int kUnitCost = kTileUnitCost;
 constexpr int kMaxRequests = kTileRequests;
 // 8 softmax warps (4 of them idle with four copies), 4 widening V, 2 loading, 2
 // issuing.  A warp's scheduler is its number modulo 4: the widening warps share
@@ -93,7 +96,7 @@ static_assert(sizeof(TileSmall) <= 12288);
 struct Unit {
   int b, head, row0, rows;  // request, kv head, first row, rows
   int base, n, T;           // context, query tokens, positions that its rows can see
-  int tile0, tiles;         // its tiles in the launch's order
+  int start, tile0, tiles;  // its place in the launch's order: kUnitCost from start on, then its tiles
 };
 
 __device__ __forceinline__ int unit_positions(int base, int n, int group, int row_tile, int rt, bool masked) {
@@ -111,11 +114,11 @@ __device__ __forceinline__ int request_lengths(const CacheAttendParams &P, int b
 __device__ __forceinline__ int request_tiles(const CacheAttendParams &P, int row_tile, int base, int n) {
   int tiles = 0;
   for (int rt = 0; rt * row_tile < n * P.group; ++rt)
-    tiles += (unit_positions(base, n, P.group, row_tile, rt, P.mask != nullptr) + kTile - 1) / kTile;
+    tiles += kUnitCost + (unit_positions(base, n, P.group, row_tile, rt, P.mask != nullptr) + kTile - 1) / kTile;
   return tiles;
 }
 
-// The unit of request b that holds tile t.
+// The unit of request b that holds place t.
 __device__ __forceinline__ Unit unit_of(const CacheTilePlan &A, const Requests &q, int row_tile, int b, int t) {
   const CacheAttendParams &P = A.p;
   Unit u;
@@ -124,16 +127,17 @@ __device__ __forceinline__ Unit unit_of(const CacheTilePlan &A, const Requests &
   u.n = q.lens[b].y;
   const int start = q.start[b], per_head = (q.start[b + 1] - start) / P.c.kv_heads;
   u.head = (t - start) / per_head;
-  u.tile0 = start + u.head * per_head;
+  u.start = start + u.head * per_head;
   for (int rt = 0;; ++rt) {
     u.T = unit_positions(u.base, u.n, P.group, row_tile, rt, P.mask != nullptr);
     u.tiles = (u.T + kTile - 1) / kTile;
-    if (t < u.tile0 + u.tiles || (rt + 1) * row_tile >= u.n * P.group) {
+    if (t < u.start + kUnitCost + u.tiles || (rt + 1) * row_tile >= u.n * P.group) {
+      u.tile0 = u.start + kUnitCost;
       u.row0 = rt * row_tile;
       u.rows = min(row_tile, u.n * P.group - u.row0);
       return u;
     }
-    u.tile0 += u.tiles;
+    u.start += kUnitCost + u.tiles;
   }
 }
 
@@ -195,6 +199,7 @@ struct TileWalk {
   const Requests &q;
   int row_tile, t, hi, lane, end;
   Unit u;
+  bool more[2];                  // whether there is a tile
   int pos[2], page[2], head[2];  // pos -1: past the unit's positions; page -1: none, or outside the pool
 
   __device__ TileWalk(const CacheTilePlan &a, const Requests &r, int rt, int lo, int h, int l)
@@ -202,10 +207,12 @@ struct TileWalk {
   __device__ __forceinline__ void advance(int slot) {
     pos[slot] = page[slot] = -1;
     head[slot] = 0;
+    more[slot] = t < hi;
     if (t >= hi) return;
     if (t >= end) {
       u = find_unit(A, q, row_tile, t);
       end = u.tile0 + u.tiles;
+      t = max(t, u.tile0);
     }
     const int at = (t - u.tile0) * kTile + lane * 16;
     head[slot] = u.head;
@@ -216,7 +223,7 @@ struct TileWalk {
     ++t;
   }
   __device__ __forceinline__ void shift() {
-    pos[0] = pos[1], page[0] = page[1], head[0] = head[1];
+    more[0] = more[1], pos[0] = pos[1], page[0] = page[1], head[0] = head[1];
     advance(1);
   }
   // the blocks' scales; 1 where there is no block
@@ -301,7 +308,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   __syncthreads();
   const int total = sm.q.start[A.count];
-  const int lo = cut(total, ctas, cta), hi = cut(total, ctas, cta + 1);
+  const int lo = cut(total, ctas, cta);
+  int hi = cut(total, ctas, cta + 1);
+  if (hi < total) {  // a cut at or before a unit's first tile ends with the unit before
+    const Unit u = find_unit(A, sm.q, RT, hi);
+    if (hi <= u.tile0) hi = u.start;
+  }
   const uint32_t tmem = sm.tmem;
   volatile int *dead = &sm.dead;
 
@@ -310,7 +322,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     TileWalk walk(A, sm.q, RT, lo, hi, lane);
     walk.advance(0);
     walk.advance(1);
-    for (int t = lo, sk = 0, lap = 0; t < hi; ++t) {
+    for (int sk = 0, lap = 0; walk.more[0];) {
       const int pos = walk.pos[0], page = walk.page[0], head = walk.head[0];
       walk.shift();
       const bool load = pos >= 0 && page >= 0 && (pos & (A.page_rows - 1)) == 0;
@@ -334,8 +346,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     walk.advance(1);
     float ks, vs, ks1, vs1;
     walk.scales(0, ks, vs);
-    for (int t = lo, sv = 0, lap = 0; t < hi; ++t) {
-      const int i = t - lo, r = i % kRing;
+    for (int i = 0, sv = 0, lap = 0; walk.more[0]; ++i) {
+      const int r = i % kRing;
       const int pos = walk.pos[0], page = walk.page[0], head = walk.head[0];
       walk.scales(1, ks1, vs1);
       walk.shift();
@@ -365,11 +377,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint64_t q_desc = matrix_desc(smem_u32(smem + S::kQ), 16, 8 * D, kSw);
     const uint64_t k_desc = matrix_desc(smem_u32(smem + S::kK), 16, 8 * D, kSw);
     int unit_end = lo, units = 0;
-    for (int t = lo, sk = 0, lap = 0; t < hi; ++t) {
-      const int i = t - lo;
+    for (int t = lo, i = 0, sk = 0, lap = 0; t < hi; ++t, ++i) {
       if (t >= unit_end) {
         const Unit u = find_unit(A, sm.q, RT, t);
         unit_end = u.tile0 + u.tiles;
+        t = max(t, u.tile0);
         if (!warp_wait(&sm.q_full, units & 1, dead)) break;
         ++units;
       }
@@ -396,12 +408,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr uint32_t kId = mma_desc(D, true);
     const uint64_t v_desc = matrix_desc(smem_u32(smem + S::kV16), kTile * 128, 1024, kSwizzle128);
     int unit_end = lo, units = 0;
-    for (int t = lo; t < hi; ++t) {
-      const int i = t - lo, w = i & 1;
+    for (int t = lo, i = 0; t < hi; ++t, ++i) {
+      const int w = i & 1;
       const bool fresh = t >= unit_end;
       if (fresh) {
         const Unit u = find_unit(A, sm.q, RT, t);
         unit_end = u.tile0 + u.tiles;
+        t = max(t, u.tile0);
         if (units > 0 && !warp_wait(&sm.o_free[(units - 1) & 1], (units - 1) >> 1 & 1, dead)) break;
         ++units;
       }
@@ -442,18 +455,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int from = (w4 * 32 + sub) * D + group * 64 + part * 16;
     const int to = group * (kTile * 128) + w4 * 4096 + sub * 128 + ((part * 2 ^ sub) << 4);
     int unit = -1, ended1 = -1, ended2 = -1;  // this unit's number; the unit that tile i - 1, i - 2 closed, or -1
-    for (int t = lo, sv = 0, lap = 0; t < hi; ++t) {
-      const int i = t - lo, w = i & 1;
+    for (int t = lo, i = 0, sv = 0, lap = 0; t < hi; ++t, ++i) {
+      const int w = i & 1;
       if (t >= unit_end) {
         u = find_unit(A, sm.q, RT, t);
         unit_end = u.tile0 + u.tiles;
+        t = max(t, u.tile0);
         ++unit;
       }
       const int pos0 = (t - u.tile0) * kTile;
       const bool edge = pos0 + kTile > u.base;
       if (i >= 2 && !warp_wait(&sm.pv_done[w], (i / 2 - 1) & 1, dead)) break;
-      // (a unit that ends sums its copies in the halves of its last tile, two tiles before the ones to replace them)
-      if (REPL > 1 && ended2 >= 0 && !warp_wait(&sm.o_free[ended2 & 1], ended2 >> 1 & 1, dead)) break;
+      // (a unit's end goes through the halves of its last tile, two tiles before the ones to replace them)
+      if (ended2 >= 0 && !warp_wait(&sm.o_free[ended2 & 1], ended2 >> 1 & 1, dead)) break;
       ended2 = ended1;
       ended1 = t + 1 == unit_end ? unit : -1;
       if (!warp_wait(&sm.v_full[sv], lap & 1, dead)) break;
@@ -540,18 +554,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // A unit's rows of q as e4m3 pieces; every earlier score product that reads them has completed.
     auto write_q = [&](const Unit &u) {
       constexpr int kEach = D / 32, kWarpsQ = 4 * HALVES;  // elements to a lane
+      // Four rows side by side in a loop that is not unrolled: its instructions are fetched once, and fetching is what a unit's
+      // start and end spend most on.  (Rows past the last one repeat it.)
 #pragma unroll 1
       for (int first = warp; first < u.rows; first += 4 * kWarpsQ) {
         float x[4][kEach], top[4];
         int ex[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // (rows past the last one repeat it)
-          const int row = u.row0 + min(first + kWarpsQ * k, u.rows - 1), tok = row / P.group;
+        for (int k = 0; k < 4; ++k) {
+          const int row = u.row0 + min(first + k * kWarpsQ, u.rows - 1), tok = row / P.group;
           const char *q = P.q + (u.b * P.qs[0] + tok * P.qs[1] + (u.head * P.group + row - tok * P.group) * P.qs[2]) * 2;
-          if (A.q_vec) load_each<DT, kEach>(q, lane, x[k]);
-          else
+          if (A.q_vec) [[likely]] {
+            unpack_each<DT, kEach>(raw_each<kEach>(q, lane), x[k]);
+          } else {
 #pragma unroll
             for (int e = 0; e < kEach; ++e) x[k][e] = row_value<DT>(q, lane * kEach + e);
+          }
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -616,9 +634,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       next = find_unit(A, sm.q, RT, lo);
       ok = write_q(next);
     }
-    for (int t = lo; t < hi && ok;) {
+    for (int t = lo, i = 0; t < hi && ok;) {
       const Unit u = next;
-      const int t_end = min(hi, u.tile0 + u.tiles);
+      t = max(t, u.tile0);
+      const int t_begin = t, t_end = min(hi, u.tile0 + u.tiles);
+      if (t_end < hi) {  // the next unit's q comes closer meanwhile
+        next = find_unit(A, sm.q, RT, t_end);
+        for (int x = tid; x < next.rows * (D / 64); x += kSoft) {
+          const int row = next.row0 + x / (D / 64), tok = row / P.group;
+          const char *q = P.q + (next.b * P.qs[0] + tok * P.qs[1] + (next.head * P.group + row - tok * P.group) * P.qs[2]) * 2;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + x % (D / 64) * 128));
+        }
+      }
       const bool live = r < u.rows;
       const float factor = live ? sm.row_factor[r] : 0.0f;
       const int token = live ? (u.row0 + r) / P.group : 0;
@@ -627,8 +654,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const float in_cap = CAP ? 2.0f / P.softcap : 0.0f;   // (of x in units of log 2) to 2 x / cap in units of log 2
       float m = -INFINITY, sum = 0.0f;
 
-      for (; t < t_end; ++t) {
-        const int i = t - lo, sb = i & 1, ring = i % kRing;
+      for (; t < t_end; ++t, ++i) {
+        const int sb = i & 1, ring = i % kRing;
         const int pos0 = (t - u.tile0) * kTile + col0;
         const bool edge = pos0 + OWN > u.base;
         if (!(ok = warp_wait(&sm.s_full[sb], (i >> 1) & 1, dead))) break;
@@ -693,7 +720,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           m = next_m;
           sum *= keep;
           const int done = i - 1;
-          if (t > max(lo, u.tile0)) {
+          if (t > t_begin) {
             if (!(ok = warp_wait(&sm.pv_done[done & 1], (done >> 1) & 1, dead))) break;
             tc_fence_after();
 #pragma unroll 1
@@ -744,13 +771,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       if (!ok) break;
 
-      if (t < hi) {  // the next unit's q, while this one's last values are being summed
-        next = find_unit(A, sm.q, RT, t);
-        if (!(ok = write_q(next))) break;
-      }
+      // the next unit's q, while this one's last values are being summed
+      if (t < hi && !(ok = write_q(next))) break;
       // The unit's end in this CTA: the rows' sums over copies and halves, and what each copy's O is multiplied by.
-      const bool whole = lo <= u.tile0 && t == u.tile0 + u.tiles;
-      const int slot = cta * 2 + (max(lo, u.tile0) != lo ? 1 : 0);
+      const bool whole = t_begin == u.tile0 && t == u.tile0 + u.tiles;
+      const int slot = cta * 2 + (unit > 0 ? 1 : 0);  // (only a CTA's first unit and its last can be cut)
       sm.ml[half][spot] = make_float2(m, sum);
       if (!(ok = together())) break;
       if (tid < u.rows) {
@@ -770,31 +795,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           sm.out_at[tid] = u.b * P.os[0] + tok * P.os[1] + h * P.os[2];
         } else {
           A.ml[static_cast<int64_t>(slot) * RT + tid] = make_float2(m_all, l_all);
-          if (tid == 0 && lo <= u.tile0) sm.begun = make_int4(u.b - A.first, u.head, u.row0 * 2 + (slot & 1), u.tile0 + u.tiles);
+          if (tid == 0 && t_begin == u.tile0) sm.begun = make_int4(u.b - A.first, u.head, u.row0 * 2 + (slot & 1), u.tile0 + u.tiles);
         }
         if (sm.spoiled[tid]) norm = NAN;
         sm.spoiled[tid] = 0;
 #pragma unroll
         for (int c = 0; c < REPL; ++c) sm.weight[c * RT + tid] = norm * ex2(sm.ml[0][c * RT + tid].x - ref);
       }
-      const int last = t - 1 - lo;
+      const int last = i - 1;
       if (!(ok = warp_wait(&sm.pv_done[last & 1], (last >> 1) & 1, dead))) break;
       tc_fence_after();
       if (!(ok = together())) break;
       const float w_own = live ? sm.weight[spot] : 0.0f;
-      auto put4 = [&](int rr, int c, float4 y) {  // four components of a row
-        if (whole) {
-          char *out = P.out + sm.out_at[rr] * 2;
-          if (A.out_vec) {
-            *reinterpret_cast<uint2 *>(out + c * 2) = make_uint2(pair_bits<DT>(y.x, y.y), pair_bits<DT>(y.z, y.w));
-          } else {
-            put_value<DT>(out, c, y.x), put_value<DT>(out, c + 1, y.y), put_value<DT>(out, c + 2, y.z), put_value<DT>(out, c + 3, y.w);
-          }
-        } else {
-          *reinterpret_cast<float4 *>(A.part + (static_cast<int64_t>(slot) * RT + rr) * D + c) = y;
-        }
-      };
-      if (REPL == 1) {
+      // Partial rows lie column by column, four at a time, so that a warp's rows are side by side: [D / 4][RT].
+      float4 *part = reinterpret_cast<float4 *>(A.part) + static_cast<int64_t>(slot) * RT * (D / 4);
+      if (REPL == 1 && !whole) {
 #pragma unroll 1
         for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
           float o[16];
@@ -802,7 +817,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           tc_wait_ld();
           if (live)
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) put4(r, c + e, make_float4(o[e] * w_own, o[e + 1] * w_own, o[e + 2] * w_own, o[e + 3] * w_own));
+            for (int e = 0; e < 4; ++e)
+              part[(c / 4 + e) * RT + r] = make_float4(o[4 * e] * w_own, o[4 * e + 1] * w_own, o[4 * e + 2] * w_own, o[4 * e + 3] * w_own);
         }
       } else {
         // 64 columns at a time, over the halves of the last tile (its product is done): [128][16 chunks of 4], swizzled by the row
@@ -823,8 +839,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                   make_float4(o[4 * e] * w_own, o[4 * e + 1] * w_own, o[4 * e + 2] * w_own, o[4 * e + 3] * w_own);
           }
           if (!(ok = together())) break;
-          for (int x = tid; x < u.rows * kChunks; x += kSoft) {
-            const int rr = x / kChunks, chunk = x % kChunks;
+          auto folded = [&](int rr, int chunk) {
             float4 y = fold[rr * kChunks + (chunk ^ (rr & (kChunks - 1)))];
 #pragma unroll
             for (int k = 1; k < REPL; ++k) {
@@ -832,7 +847,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               const float4 z = fold[row * kChunks + (chunk ^ (row & (kChunks - 1)))];
               y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
             }
-            put4(rr, c0 + chunk * 4, y);
+            return y;
+          };
+          if (whole) {
+            for (int x = tid; x < u.rows * kChunks; x += kSoft) {
+              const int rr = x / kChunks, c = c0 + x % kChunks * 4;
+              const float4 y = folded(rr, x % kChunks);
+              char *out = P.out + sm.out_at[rr] * 2;
+              if (A.out_vec) {
+                *reinterpret_cast<uint2 *>(out + c * 2) = make_uint2(pair_bits<DT>(y.x, y.y), pair_bits<DT>(y.z, y.w));
+              } else {
+                put_value<DT>(out, c, y.x), put_value<DT>(out, c + 1, y.y), put_value<DT>(out, c + 2, y.z), put_value<DT>(out, c + 3, y.w);
+              }
+            }
+          } else {
+            for (int x = tid; x < RT * kChunks; x += kSoft)
+              if (x % RT < u.rows) part[(c0 / 4 + x / RT) * RT + x % RT] = folded(x % RT, x / RT);
           }
         }
       }
@@ -858,16 +888,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 }
 
 // Joins the partial sums of the units that more than one CTA worked on: block
-// (c, j) takes eight rows, a warp each, of the unit that CTA c began and a later
-// one ended.  The last blocks set the requests' status, and clear the outputs of
-// those with a bad page.
+// (c, j) takes 32 rows, a lane each, of the unit that CTA c began and a later
+// one ended, each warp an eighth of the columns.  The last blocks set the
+// requests' status, and clear the outputs of those with a bad page.
 template <int DT, int D>
 __global__ void __launch_bounds__(256) cache_attend_merge_kernel(const CacheTilePlan A, int row_tile, int ctas) {
   const CacheAttendParams &P = A.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kEach = D / 32;
+  constexpr int kOwn = D / 32;  // float4s of a row to a warp
   pdl_wait();
-  const int chunks = row_tile / 8;
+  const int chunks = row_tile / 32;
   if (static_cast<int>(blockIdx.x) >= ctas * chunks) {
     const int bl = (blockIdx.x - ctas * chunks) * 8 + warp, b = A.first + bl;
     if (bl >= A.count) return;
@@ -880,66 +910,85 @@ __global__ void __launch_bounds__(256) cache_attend_merge_kernel(const CacheTile
       for (int x = lane; x < P.N * P.Hq; x += 32) zero_row<DT, D>(P, b, x);
     return;
   }
-  const int c0 = blockIdx.x / chunks, r = (blockIdx.x % chunks) * 8 + warp;
+  const int c0 = blockIdx.x / chunks, r = (blockIdx.x % chunks) * 32 + lane;
   const int4 unit = A.begun[c0];  // request, head, 2 * first row + c0's slot, end of its tiles
   if (unit.x < 0) return;
   const int b = A.first + unit.x;
   int base, n;
   request_lengths(P, b, base, n);
   const int row = (unit.z >> 1) + r;
-  if (row >= n * P.group || A.verdict[unit.x] != SPEC_STATUS_OK) return;
+  const bool live = row < n * P.group;
+  const bool fine = A.verdict[unit.x] == SPEC_STATUS_OK;
   // the last CTA that begins before the unit's end; nobody gave up
   int c1 = -1;
-  bool gone = false;
+  bool gone = !fine;
   for (int c = lane; c - lane < ctas; c += 32) {
     const int2 range = c < ctas ? A.range[c] : make_int2(0x7fffffff, 0);
     gone |= range.y != 0;
     c1 += __popc(__ballot_sync(~0u, range.x < unit.w));
   }
   if (__any_sync(~0u, gone)) return;
-  float m = -INFINITY, acc[kEach] = {}, sum = 0.0f;
-  for (int cc = c0; cc <= c1; cc += 32) {
-    // a lane to a CTA: where it left the row, its reference and sum
-    const int c = cc + lane;
-    int slot = -1;
-    float2 ml = make_float2(-INFINITY, 0.0f);
-    if (c <= c1) {
-      const int from = A.range[c].x;
-      if (c == c1 || A.range[c + 1].x > from) {
-        slot = (c * 2 + (c == c0 ? unit.z & 1 : 0)) * row_tile + r;
-        ml = A.ml[slot];
+  float m = -INFINITY, sum = 0.0f;
+  float4 acc[kOwn];
+#pragma unroll
+  for (int e = 0; e < kOwn; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  // four CTAs' loads at a time
+#pragma unroll 1
+  for (int cc = c0; cc <= c1; cc += 4) {
+    float2 ml[4];
+    float4 o[4][kOwn];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = cc + k;
+      ml[k] = make_float2(-INFINITY, 0.0f);
+      const bool has = c <= c1 && live && (c == c1 || A.range[c + 1].x > A.range[c].x);
+#pragma unroll
+      for (int e = 0; e < kOwn; ++e) o[k][e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (has) {
+        const int64_t slot = c * 2 + (c == c0 ? unit.z & 1 : 0);
+        ml[k] = A.ml[slot * row_tile + r];
+        const float4 *part = reinterpret_cast<const float4 *>(A.part) + (slot * (D / 4) + warp * kOwn) * row_tile + r;
+#pragma unroll
+        for (int e = 0; e < kOwn; ++e) o[k][e] = part[e * row_tile];
       }
     }
-    float top = ml.x;
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    top = fmaxf(m, top);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    const float w = ex2(ml.x - ref), keep = ex2(m - ref);
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
+    const float ref = top == -INFINITY ? 0.0f : top, keep = ex2(m - ref);
     m = top;
-    sum = sum * keep + warp_sum(ml.y * w);
+    sum *= keep;
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) acc[e] *= keep;
-    const int here = min(32, c1 - cc + 1);
-#pragma unroll 8
-    for (int k = 0; k < here; ++k) {
-      const float wk = __shfl_sync(~0u, w, k);
-      const int sk = __shfl_sync(~0u, slot, k);
-      if (sk < 0) continue;
-      const float *o = A.part + static_cast<int64_t>(sk) * D + lane * kEach;
+    for (int e = 0; e < kOwn; ++e) acc[e].x *= keep, acc[e].y *= keep, acc[e].z *= keep, acc[e].w *= keep;
 #pragma unroll
-      for (int e = 0; e < kEach; e += 2) {
-        const float2 v = *reinterpret_cast<const float2 *>(o + e);
-        acc[e] = fmaf(v.x, wk, acc[e]);
-        acc[e + 1] = fmaf(v.y, wk, acc[e + 1]);
+    for (int k = 0; k < 4; ++k) {
+      const float w = ex2(ml[k].x - ref);
+      sum = fmaf(ml[k].y, w, sum);
+#pragma unroll
+      for (int e = 0; e < kOwn; ++e) {
+        acc[e].x = fmaf(o[k][e].x, w, acc[e].x);
+        acc[e].y = fmaf(o[k][e].y, w, acc[e].y);
+        acc[e].z = fmaf(o[k][e].z, w, acc[e].z);
+        acc[e].w = fmaf(o[k][e].w, w, acc[e].w);
       }
     }
   }
+  if (!live) return;
   const int i = row / P.group, h = unit.y * P.group + row % P.group;
   char *out = P.out + (b * P.os[0] + i * P.os[1] + h * P.os[2]) * 2;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) put_value<DT>(out, lane * kEach + e, acc[e] * inv);
-  if (lane == 0 && P.lse)
+  for (int e = 0; e < kOwn; ++e) {
+    const int d = (warp * kOwn + e) * 4;
+    if (A.out_vec) {
+      *reinterpret_cast<uint2 *>(out + d * 2) =
+          make_uint2(pair_bits<DT>(acc[e].x * inv, acc[e].y * inv), pair_bits<DT>(acc[e].z * inv, acc[e].w * inv));
+    } else {
+      put_value<DT>(out, d, acc[e].x * inv), put_value<DT>(out, d + 1, acc[e].y * inv);
+      put_value<DT>(out, d + 2, acc[e].z * inv), put_value<DT>(out, d + 3, acc[e].w * inv);
+    }
+  }
+  if (warp == 0 && P.lse)
     P.lse[(static_cast<int64_t>(b) * P.N + i) * P.Hq + h] = sum == 0.0f ? -INFINITY : (m - 7.0f + log2f(sum)) * kLn2;
 }
 
@@ -958,7 +1007,7 @@ cudaError_t launch_tiles(const CacheTilePlan &A, const CUtensorMap &map, cudaStr
   e = trace_launch("cache_attend_tile", st, [&] { kern<<<ctas, kTileThreads, S::kBytes, st>>>(A, map); });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas * (128 / REPL / 8) + (A.count + 7) / 8));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas * (128 / REPL / 32) + (A.count + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

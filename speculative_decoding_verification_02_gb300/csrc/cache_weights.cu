@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < kEach; ++e) x[k][e] = 0.0f;
             if (at[k] >= 0) {
-              if (q_vec) load_each<DT, kEach>(q, lane, x[k]);
+              if (q_vec) unpack_each<DT, kEach>(raw_each<kEach>(q, lane), x[k]);
               else
 #pragma unroll
                 for (int e = 0; e < kEach; ++e) x[k][e] = row_value<DT>(q, lane * kEach + e);
