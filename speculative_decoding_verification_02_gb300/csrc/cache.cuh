@@ -49,7 +49,7 @@ struct CacheAttendParams {
 
 constexpr int kTilePositions = 128;  // positions to a tile of the tensor-core kernels
 constexpr int kTileRequests = 256;   // requests to one of their launches
-constexpr int kTileUnitCost = 3;     // (cache_attend_tile.cuh)
+constexpr int kTileUnitCost = 4;     // (cache_attend_tile.cuh)
 
 // A launch of spec_cache_attend's tensor-core path.
 struct CacheTilePlan {
@@ -57,6 +57,7 @@ struct CacheTilePlan {
   int first, count;     // requests of this launch
   int page_rows;        // rows of a page that one copy brings: min(page size, 128)
   bool q_vec, out_vec;  // rows of q and out start on 8-byte boundaries
+  uint32_t group_inverse;  // 2^32 / group, rounded up
   int *verdict;          // the requests' status
   int2 *range;           // [CTA] first tile; whether it gave up waiting
   int4 *begun;           // [CTA] the unit that it began and a later one ended

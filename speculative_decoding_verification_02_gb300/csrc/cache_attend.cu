@@ -140,7 +140,9 @@ size_t lay_out(CacheTilePlan &A, char *ws, int D) {
 }  // namespace
 
 bool cache_attend_on_tensor_cores(const CacheAttendParams &P) {
-  return (P.c.head_dim == 64 || P.c.head_dim == 128) && requests_at_once(P) > 0;
+  // (a row's number times the group stays below 2^32: the multiplication that divides by it is exact)
+  return (P.c.head_dim == 64 || P.c.head_dim == 128) && static_cast<int64_t>(P.N) * P.group * P.group < (1LL << 32) &&
+         requests_at_once(P) > 0;
 }
 
 size_t cache_attend_workspace(const CacheAttendParams &P) {
@@ -157,6 +159,7 @@ cudaError_t launch_cache_attend(const CacheAttendParams &P, void *workspace, cud
     A.page_rows = std::min(1 << P.c.page_shift, kTilePositions);
     A.q_vec = rows_on_grain(P.q, P.qs);
     A.out_vec = rows_on_grain(P.out, P.os);
+    A.group_inverse = static_cast<uint32_t>((0x100000000ull + P.group - 1) / P.group);
     lay_out(A, static_cast<char *>(workspace), P.c.head_dim);
     CUtensorMap map;
     const cudaError_t made = cache_k_map(P.c, A.page_rows, &map);

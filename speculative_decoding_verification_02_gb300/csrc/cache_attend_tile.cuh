@@ -72,6 +72,7 @@ struct TileShape {
 struct Requests {
   int start[kMaxRequests + 1];  // running sum of their tiles
   int2 lens[kMaxRequests];      // context, query tokens
+  int per_head[kMaxRequests];   // tiles of a kv head
 };
 
 // Small arrays, after the operands.
@@ -99,8 +100,14 @@ struct Unit {
   int start, tile0, tiles;  // its place in the launch's order: kUnitCost from start on, then its tiles
 };
 
-__device__ __forceinline__ int unit_positions(int base, int n, int group, int row_tile, int rt, bool masked) {
-  return masked ? base + n : base + (min((rt + 1) * row_tile, n * group) - 1) / group + 1;
+// x / group for the rows of a unit: a multiplication (x * group < 2^32), a few
+// instructions where a division is forty.
+__device__ __forceinline__ int by_group(const CacheTilePlan &A, int x) {
+  return A.p.group == 1 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), A.group_inverse));
+}
+
+__device__ __forceinline__ int unit_positions(const CacheTilePlan &A, int base, int n, int row_tile, int rt) {
+  return A.p.mask ? base + n : base + by_group(A, min((rt + 1) * row_tile, n * A.p.group) - 1) + 1;
 }
 
 // The request's lengths, SPEC_STATUS_OK or _BAD_LENGTH.
@@ -111,10 +118,10 @@ __device__ __forceinline__ int request_lengths(const CacheAttendParams &P, int b
   return SPEC_STATUS_OK;
 }
 
-__device__ __forceinline__ int request_tiles(const CacheAttendParams &P, int row_tile, int base, int n) {
+__device__ __forceinline__ int request_tiles(const CacheTilePlan &A, int row_tile, int base, int n) {
   int tiles = 0;
-  for (int rt = 0; rt * row_tile < n * P.group; ++rt)
-    tiles += kUnitCost + (unit_positions(base, n, P.group, row_tile, rt, P.mask != nullptr) + kTile - 1) / kTile;
+  for (int rt = 0; rt * row_tile < n * A.p.group; ++rt)
+    tiles += kUnitCost + (unit_positions(A, base, n, row_tile, rt) + kTile - 1) / kTile;
   return tiles;
 }
 
@@ -125,11 +132,14 @@ __device__ __forceinline__ Unit unit_of(const CacheTilePlan &A, const Requests &
   u.b = A.first + b;
   u.base = q.lens[b].x;
   u.n = q.lens[b].y;
-  const int start = q.start[b], per_head = (q.start[b + 1] - start) / P.c.kv_heads;
-  u.head = (t - start) / per_head;
+  const int start = q.start[b], per_head = q.per_head[b];
+  // the quotient from floats: off by one at most below 2^24, and put right
+  u.head = static_cast<int>(__fdividef(static_cast<float>(t - start), static_cast<float>(per_head)));
+  while (u.head > 0 && u.head * per_head > t - start) --u.head;
+  while ((u.head + 1) * per_head <= t - start) ++u.head;
   u.start = start + u.head * per_head;
   for (int rt = 0;; ++rt) {
-    u.T = unit_positions(u.base, u.n, P.group, row_tile, rt, P.mask != nullptr);
+    u.T = unit_positions(A, u.base, u.n, row_tile, rt);
     u.tiles = (u.T + kTile - 1) / kTile;
     if (t < u.start + kUnitCost + u.tiles || (rt + 1) * row_tile >= u.n * P.group) {
       u.tile0 = u.start + kUnitCost;
@@ -287,7 +297,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     int base, n;
     const bool ok = request_lengths(P, A.first + b, base, n) == SPEC_STATUS_OK;
     sm.q.lens[b] = make_int2(base, n);
-    sm.q.start[b + 1] = ok ? request_tiles(P, RT, base, n) * P.c.kv_heads : 0;
+    const int tiles = ok ? request_tiles(A, RT, base, n) : 0;
+    sm.q.per_head[b] = max(tiles, 1);
+    sm.q.start[b + 1] = tiles * P.c.kv_heads;
   }
   tc_fence_before();
   __syncthreads();
@@ -562,7 +574,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         int ex[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int row = u.row0 + min(first + k * kWarpsQ, u.rows - 1), tok = row / P.group;
+          const int row = u.row0 + min(first + k * kWarpsQ, u.rows - 1), tok = by_group(A, row);
           const char *q = P.q + (u.b * P.qs[0] + tok * P.qs[1] + (u.head * P.group + row - tok * P.group) * P.qs[2]) * 2;
           if (A.q_vec) [[likely]] {
             unpack_each<DT, kEach>(raw_each<kEach>(q, lane), x[k]);
@@ -638,17 +650,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const Unit u = next;
       t = max(t, u.tile0);
       const int t_begin = t, t_end = min(hi, u.tile0 + u.tiles);
-      if (t_end < hi) {  // the next unit's q comes closer meanwhile
-        next = find_unit(A, sm.q, RT, t_end);
-        for (int x = tid; x < next.rows * (D / 64); x += kSoft) {
-          const int row = next.row0 + x / (D / 64), tok = row / P.group;
-          const char *q = P.q + (next.b * P.qs[0] + tok * P.qs[1] + (next.head * P.group + row - tok * P.group) * P.qs[2]) * 2;
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + x % (D / 64) * 128));
-        }
-      }
       const bool live = r < u.rows;
       const float factor = live ? sm.row_factor[r] : 0.0f;
-      const int token = live ? (u.row0 + r) / P.group : 0;
+      const int token = live ? by_group(A, u.row0 + r) : 0;
       const uint8_t *mask = P.mask ? P.mask + (static_cast<int64_t>(u.b) * P.N + token) * P.N : nullptr;
       const float cap2 = P.softcap * kLog2e;                // the cap in units of log 2
       const float in_cap = CAP ? 2.0f / P.softcap : 0.0f;   // (of x in units of log 2) to 2 x / cap in units of log 2
@@ -772,7 +776,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!ok) break;
 
       // the next unit's q, while this one's last values are being summed
-      if (t < hi && !(ok = write_q(next))) break;
+      if (t < hi) {
+        next = find_unit(A, sm.q, RT, t);
+        if (!(ok = write_q(next))) break;
+      }
       // The unit's end in this CTA: the rows' sums over copies and halves, and what each copy's O is multiplied by.
       const bool whole = t_begin == u.tile0 && t == u.tile0 + u.tiles;
       const int slot = cta * 2 + (unit > 0 ? 1 : 0);  // (only a CTA's first unit and its last can be cut)
@@ -787,11 +794,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int c = 0; c < REPL; ++c)
           l_all += (sm.ml[0][c * RT + tid].y + (HALVES == 2 ? sm.ml[1][c * RT + tid].y : 0.0f)) * ex2(sm.ml[0][c * RT + tid].x - ref);
         float norm = 1.0f;
-        const int row = u.row0 + tid, tok = row / P.group, h = u.head * P.group + row % P.group;
+        const int row = u.row0 + tid, tok = by_group(A, row), h = u.head * P.group + row - tok * P.group;
         if (whole) {
-          norm = l_all == 0.0f ? 0.0f : 1.0f / l_all;
+          norm = l_all == 0.0f ? 0.0f : __fdividef(1.0f, l_all);
           if (P.lse)
-            P.lse[(static_cast<int64_t>(u.b) * P.N + tok) * P.Hq + h] = l_all == 0.0f ? -INFINITY : (m_all - 7.0f + log2f(l_all)) * kLn2;
+            P.lse[(static_cast<int64_t>(u.b) * P.N + tok) * P.Hq + h] = l_all == 0.0f ? -INFINITY : (m_all - 7.0f + __log2f(l_all)) * kLn2;
           sm.out_at[tid] = u.b * P.os[0] + tok * P.os[1] + h * P.os[2];
         } else {
           A.ml[static_cast<int64_t>(slot) * RT + tid] = make_float2(m_all, l_all);
