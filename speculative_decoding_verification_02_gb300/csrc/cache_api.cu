@@ -167,7 +167,7 @@ int spec_cache_weights(const spec_cache *cache, const void *q, const int64_t *q_
   if (B == 0) return SPEC_OK;
   if (!cache_len || !out || (N > 0 && (!q || !lse))) return SPEC_EINVAL;
   // (tiles of a launch, and blocks of the general kernel, are numbered by an int)
-  if (static_cast<int64_t>(B) * P.c.kv_heads * ((static_cast<int64_t>(P.c.table_stride) << P.c.page_shift) / 128 + 1) > kMaxGrid)
+  if (static_cast<int64_t>(B) * P.c.kv_heads * ((static_cast<int64_t>(P.c.table_stride) << P.c.page_shift) / 128 + 8) > kMaxGrid)
     return SPEC_EINVAL;
   P.q = static_cast<const char *>(q);
   std::copy(q_stride, q_stride + 3, P.qs);

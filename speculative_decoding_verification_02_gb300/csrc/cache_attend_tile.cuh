@@ -981,7 +981,7 @@ __global__ void __launch_bounds__(256) cache_attend_merge_kernel(const CacheTile
     }
   }
   if (!live) return;
-  const int i = row / P.group, h = unit.y * P.group + row % P.group;
+  const int i = by_group(A, row), h = unit.y * P.group + row - i * P.group;
   char *out = P.out + (b * P.os[0] + i * P.os[1] + h * P.os[2]) * 2;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll

@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(kSpan) cache_weights_rows_kernel(const CacheWe
 // what is left of small elements is 2^-14 against a largest of 128 or more.
 //
 // The tiles of all (request, head) units are laid end to end and cut evenly
-// over the CTAs.  Rows are taken RC at a time (16, 32 or 64); further rows of a
+// over the CTAs, a unit's start counting as some tiles.  Rows are taken 64 at a
+// time (the operand holds as many as there are, in sixteens); further rows of a
 // unit go over its tiles again, adding to what is there.  Two groups of four
 // warps take alternate tiles.  Bound by reading K (head_dim bytes a position
 // and kv head) for few rows, by the exponentials for many.
@@ -113,7 +114,8 @@ __global__ void __launch_bounds__(kSpan) cache_weights_rows_kernel(const CacheWe
 constexpr int kTile = kTilePositions;
 constexpr int kThreads = 320;  // two groups of 4 summing warps, 1 loading, 1 issuing
 constexpr int kRing = 8;
-constexpr int kMaxRows = 64;   // RC at most
+constexpr int kMaxRows = 64;   // rows at a time
+constexpr int kUnitCost = 3;   // what a unit costs besides its tiles, in tiles
 
 template <int DT, int D>
 struct WeightShape {
@@ -129,17 +131,23 @@ struct WeightShape {
 struct WeightSmall {
   int start[kTileRequests + 1];  // running sum of the requests' tiles
   int2 lens[kTileRequests];      // context, rows
-  float2 row[kMaxRows];          // factor of a row's scores, its lse; both in units of log 2
+  alignas(16) float2 row[kMaxRows];          // factor of a row's scores, its lse negated; both in units of log 2
   int token[kMaxRows];           // its place behind the context
   float ring[kRing][8];          // k_scale of 16 positions
-  uint64_t k_full[12], k_empty[12], s_full[2], s_empty[2], q_full, meet, ring_full[kRing], ring_empty[kRing];
+  uint64_t k_full[12], k_empty[12], s_full[4], s_empty[4], q_full, meet, ring_full[kRing], ring_empty[kRing];
   uint32_t tmem;
   int bad[2], dead;
 };
 static_assert(sizeof(WeightSmall) <= 8192);
 
+// cap tanh(x / cap), x and the answer in units of log 2.
+__device__ __forceinline__ float capped_score(float x, float in_cap, float cap2) {
+  const float z = x * in_cap;
+  return cap2 * (1.0f - __fdividef(2.0f, 1.0f + ex2(z > 120.0f ? 120.0f : z)));
+}
+
 struct WeightUnit {
-  int b, head, base, cnt, T, tile0, tiles;  // b: within the launch
+  int b, head, base, cnt, T, start, tile0, tiles;  // b: within the launch; start: its place, kUnitCost before its tiles
 };
 
 __device__ __noinline__ WeightUnit weight_unit(const WeightSmall &sm, int count, int heads, int t) {
@@ -155,8 +163,12 @@ __device__ __noinline__ WeightUnit weight_unit(const WeightSmall &sm, int count,
   u.cnt = sm.lens[lo].y;
   u.T = u.base + u.cnt;
   u.tiles = (u.T + kTile - 1) / kTile;
-  u.head = (t - sm.start[lo]) / u.tiles;
-  u.tile0 = sm.start[lo] + u.head * u.tiles;
+  const int span = u.tiles + kUnitCost, at = t - sm.start[lo];
+  u.head = static_cast<int>(__fdividef(static_cast<float>(at), static_cast<float>(span)));  // off by one at most, and put right
+  while (u.head > 0 && u.head * span > at) --u.head;
+  while ((u.head + 1) * span <= at) ++u.head;
+  u.start = sm.start[lo] + u.head * span;
+  u.tile0 = u.start + kUnitCost;
   return u;
 }
 
@@ -169,7 +181,7 @@ __device__ __forceinline__ bool weight_lengths(const CacheWeightsParams &P, int 
 
 template <int DT, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    cache_weights_tile_kernel(const CacheWeightsParams P, int first, int count, int rc, int page_rows, bool q_vec,
+    cache_weights_tile_kernel(const CacheWeightsParams P, int first, int count, uint32_t group_inverse, int page_rows, bool q_vec,
                               const __grid_constant__ CUtensorMap k_map) {
   using S = WeightShape<DT, D>;
   extern __shared__ char raw[];
@@ -180,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < S::kStages; ++i) bar_init(&sm.k_full[i], 1), bar_init(&sm.k_empty[i], 1);
-    for (int i = 0; i < 2; ++i) bar_init(&sm.s_full[i], 2), bar_init(&sm.s_empty[i], 128);
+    for (int i = 0; i < 4; ++i) bar_init(&sm.s_full[i], 2), bar_init(&sm.s_empty[i], 128);
     bar_init(&sm.q_full, 256);
     bar_init(&sm.meet, 256);
     for (int i = 0; i < kRing; ++i) bar_init(&sm.ring_full[i], 32), bar_init(&sm.ring_empty[i], 128);
@@ -192,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int base, cnt;
     const bool ok = weight_lengths(P, first + b, base, cnt);
     sm.lens[b] = make_int2(base, cnt);
-    sm.start[b + 1] = ok ? (base + cnt + kTile - 1) / kTile * heads : 0;
+    sm.start[b + 1] = ok && base + cnt > 0 ? ((base + cnt + kTile - 1) / kTile + kUnitCost) * heads : 0;
     // (a request without positions has its status from here)
     if (cta == 0 && P.status && !(ok && base + cnt > 0)) P.status[first + b] = ok ? SPEC_STATUS_OK : SPEC_STATUS_BAD_LENGTH;
   }
@@ -216,10 +228,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const int total = sm.start[count];
   const int lo = static_cast<int>(static_cast<int64_t>(total) * cta / ctas);
-  const int hi = static_cast<int>(static_cast<int64_t>(total) * (cta + 1) / ctas);
+  int hi = static_cast<int>(static_cast<int64_t>(total) * (cta + 1) / ctas);
+  if (hi < total) {  // a cut at or before a unit's first tile ends with the unit before
+    const WeightUnit u = weight_unit(sm, count, heads, hi);
+    if (hi <= u.tile0) hi = u.start;
+  }
   const uint32_t tmem = sm.tmem;
   volatile int *dead = &sm.dead;
-  auto chunks_of = [&](const WeightUnit &u) { return max(1, (u.cnt * P.group + rc - 1) / rc); };  // (no rows: prev is copied)
+  constexpr int kBuffers = S::kPieces == 2 ? 4 : 2, kBufferCols = 512 / kBuffers;  // tensor memory: scores of a tile
+  auto chunks_of = [&](const WeightUnit &u) { return max(1, (u.cnt * P.group + kMaxRows - 1) / kMaxRows); };  // (no rows: prev is copied)
+  auto padded_of = [&](const WeightUnit &u, int c) { return max(16, (min(kMaxRows, u.cnt * P.group - c * kMaxRows) + 15) / 16 * 16); };
 
   if (warp == 8) {
     // ---- loading K and its scales: a lane to 16 positions (the first 8 lanes); the next tile's page is looked up meanwhile
@@ -229,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = lo; t < hi && ok;) {
       const WeightUnit u = weight_unit(sm, count, heads, t);
       const int end = min(hi, u.tile0 + u.tiles), chunks = chunks_of(u);
+      t = max(t, u.tile0);
       for (int c = 0; c < chunks && ok; ++c) {
         auto page_of = [&](int k) {
           const int pos = (k - u.tile0) * kTile + lane * 16;
@@ -264,7 +283,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 9) {
     // ---- issuing S^T = K Q^T
     constexpr uint64_t kSw = D == 128 ? kSwizzle128 : kSwizzle64;
-    const uint32_t idesc = mma_desc(S::kPieces * rc, false);
     const uint64_t q_desc = matrix_desc(smem_u32(smem + S::kQ), 16, 8 * D, kSw);
     const uint64_t k_desc = matrix_desc(smem_u32(smem + S::kK), 16, 8 * D, kSw);
     int stage = 0, lap = 0, i = 0, writes = 0;
@@ -272,20 +290,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = lo; t < hi && ok;) {
       const WeightUnit u = weight_unit(sm, count, heads, t);
       const int end = min(hi, u.tile0 + u.tiles), chunks = chunks_of(u);
+      t = max(t, u.tile0);
       for (int c = 0; c < chunks && ok; ++c) {
         if (!(ok = warp_wait(&sm.q_full, writes++ & 1, dead))) break;
+        const uint32_t idesc = mma_desc(S::kPieces * padded_of(u, c), false);
         for (int k = t; k < end; ++k, ++i) {
-          if (i >= 2 && !(ok = warp_wait(&sm.s_empty[i & 1], (i / 2 - 1) & 1, dead))) break;
+          const int buffer = i % kBuffers;
+          if (i >= kBuffers && !(ok = warp_wait(&sm.s_empty[buffer], (i / kBuffers - 1) & 1, dead))) break;
           if (!(ok = warp_wait(&sm.ring_full[i % kRing], (i / kRing) & 1, dead))) break;
-          if (lane == 0) bar_arrive(&sm.s_full[i & 1]);  // (with this arrival S full says that the tile's scales are there too)
+          if (lane == 0) bar_arrive(&sm.s_full[buffer]);  // (with this arrival S full says that the tile's scales are there too)
           if (!(ok = warp_wait(&sm.k_full[stage], lap & 1, dead))) break;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int e = 0; e < D / 32; ++e)
-              mma_f8(tmem + (i & 1) * 256, k_desc + ((stage * S::kStage + e * 32) >> 4), q_desc + ((e * 32) >> 4), idesc, e > 0);
+              mma_f8(tmem + buffer * kBufferCols, k_desc + ((stage * S::kStage + e * 32) >> 4), q_desc + ((e * 32) >> 4), idesc, e > 0);
             tc_commit(&sm.k_empty[stage]);
-            tc_commit(&sm.s_full[i & 1]);
+            tc_commit(&sm.s_full[buffer]);
           }
           __syncwarp();
           if (++stage == S::kStages) stage = 0, ++lap;
@@ -309,6 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = lo; t < hi && ok; ++segment) {
       const WeightUnit u = weight_unit(sm, count, heads, t);
       const int end = min(hi, u.tile0 + u.tiles), chunks = chunks_of(u), b = first + u.b, rows = u.cnt * P.group;
+      t = max(t, u.tile0);
+      const int t0 = t;
       const int32_t *index = P.index ? P.index + static_cast<int64_t>(b) * P.index_stride : nullptr;
       // the request's pages and indexes: a bad one takes the request out
       int bad = 0;
@@ -318,13 +341,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       bad = __reduce_or_sync(~0u, bad);
       if (lane == 0 && bad) atomicOr(&sm.bad[segment & 1], bad);
       for (int c = 0; c < chunks && ok; ++c) {
-        const int row0 = c * rc, here = min(rc, rows - row0), padded = (here + 15) / 16 * 16;
+        const int row0 = c * kMaxRows, here = min(kMaxRows, rows - row0), padded = padded_of(u, c);
         // every product that reads the rows before has completed for both sides
         if (!(ok = together())) break;
         if (c == 0) {
           bad = sm.bad[segment & 1];
           if (tid == 0) sm.bad[(segment + 1) & 1] = 0;  // (the segment before's; the next one's is set after the next meeting)
-          if (tid == 0 && u.head == 0 && u.tile0 >= lo && P.status)
+          if (tid == 0 && u.head == 0 && t0 == u.tile0 && P.status)
             P.status[b] = bad & 1 ? SPEC_STATUS_BAD_PAGE : bad & 2 ? SPEC_STATUS_BAD_INDEX : SPEC_STATUS_OK;
         }
         constexpr int kEach = D / 32;
@@ -335,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int r = r0 + 8 * k, row = row0 + r;
-            tok[k] = row / P.group;
+            tok[k] = P.group == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), group_inverse));
             const bool real = r < here;
             at[k] = real ? (index ? index[tok[k]] : tok[k]) : -1;
             if (at[k] < 0 || at[k] >= P.N) at[k] = -1;
@@ -382,16 +405,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 x[k][e + 1] = (x[k][e + 1] - back.y) * 16.0f;
                 code |= two << (8 * e);
               }
-              const int a = piece * rc + r, chunk = lane * kEach >> 4;
+              const int a = piece * padded + r, chunk = lane * kEach >> 4;
               char *to = smem + S::kQ + a * D + ((D == 128 ? chunk ^ (a & 7) : chunk ^ (a >> 1 & 3)) << 4) + (lane * kEach & 15);
               if (kEach == 4) *reinterpret_cast<uint32_t *>(to) = code;
               else *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(code);
             }
             if (lane == 0) {
               const int h = u.head * P.group + row0 + r - tok[k] * P.group;
-              float z = at[k] >= 0 ? P.lse[(static_cast<int64_t>(b) * P.N + at[k]) * P.Hq + h] : -INFINITY;
-              if (z == -INFINITY) z = INFINITY;  // nothing comes of the row
-              sm.row[r] = make_float2(fabsf(P.scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(ex[k] + 127) << 23), z * kLog2e);
+              const float z = at[k] >= 0 ? P.lse[(static_cast<int64_t>(b) * P.N + at[k]) * P.Hq + h] : -INFINITY;
+              sm.row[r] = make_float2(fabsf(P.scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(ex[k] + 127) << 23),
+                                      z == -INFINITY ? -INFINITY : -z * kLog2e);  // (nothing comes of a row without positions)
               sm.token[r] = tok[k];
             }
           }
@@ -402,25 +425,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         for (int k = t; k < end; ++k, ++i) {
           if ((i & 1) != side) continue;
-          const int ring = i % kRing, j = (k - u.tile0) * kTile + spot;
+          const int buffer = i % kBuffers, ring = i % kRing, j = (k - u.tile0) * kTile + spot;
           const bool mine = j < u.T && !bad;
           const bool edge = (k - u.tile0) * kTile + kTile > u.base;
           float *out = P.out + b * P.out_s[0] + u.head * P.out_s[1] + j;
           float sum = 0.0f, held = 0.0f;
           if (mine) held = c > 0 ? *out : P.prev ? P.prev[b * P.prev_s[0] + u.head * P.prev_s[1] + j] : 0.0f;
-          if (!(ok = warp_wait(&sm.s_full[side], (i >> 1) & 1, dead))) break;
+          if (!(ok = warp_wait(&sm.s_full[buffer], (i / kBuffers) & 1, dead))) break;
           tc_fence_after();
           const float ks = sm.ring[ring][spot >> 4];
           bar_arrive(&sm.ring_empty[ring]);
 #pragma unroll 1
           for (int r = 0; r < padded; r += 16) {
             float x[16], y[16];
-            const uint32_t at = tmem + lanes + side * 256 + r;
+            const uint32_t at = tmem + lanes + buffer * kBufferCols + r;
             tmem_ld16(at, x);
-            tmem_ld16(at + rc, y);
+            tmem_ld16(at + padded, y);
             if (S::kPieces == 3) {
               float z[16];
-              tmem_ld16(at + 2 * rc, z);
+              tmem_ld16(at + 2 * padded, z);
               tc_wait_ld();
 #pragma unroll
               for (int e = 0; e < 16; ++e) y[e] = fmaf(z[e], 1.0f / 16, y[e]);
@@ -429,21 +452,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float part[2] = {};
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 f = sm.row[r + e];
-              float s = fmaf(y[e], 1.0f / 16, x[e]) * (f.x * ks);
+            for (int e = 0; e < 16; e += 2) {
+              const float4 f = *reinterpret_cast<const float4 *>(&sm.row[r + e]);  // two rows'
+              float s0 = fmaf(y[e], 1.0f / 16, x[e]), s1 = fmaf(y[e + 1], 1.0f / 16, x[e + 1]);
               if (capped) {
-                const float z = s * in_cap;
-                s = cap2 * (1.0f - __fdividef(2.0f, 1.0f + ex2(z > 120.0f ? 120.0f : z)));
+                s0 = capped_score(s0 * (f.x * ks), in_cap, cap2) + f.y;
+                s1 = capped_score(s1 * (f.z * ks), in_cap, cap2) + f.w;
+              } else {
+                s0 = fmaf(s0, f.x * ks, f.y);
+                s1 = fmaf(s1, f.z * ks, f.w);
               }
-              float p = ex2(s - f.y);
-              if (edge && j - u.base > sm.token[r + e]) p = 0.0f;
-              part[e & 1] += p;
+              float p0 = ex2(s0), p1 = ex2(s1);
+              if (edge) [[unlikely]] {
+                if (j - u.base > sm.token[r + e]) p0 = 0.0f;
+                if (j - u.base > sm.token[r + e + 1]) p1 = 0.0f;
+              }
+              part[0] += p0;
+              part[1] += p1;
             }
             sum += part[0] + part[1];
           }
           tc_fence_before();
-          bar_arrive(&sm.s_empty[side]);
+          bar_arrive(&sm.s_empty[buffer]);
           if (mine) *out = held + sum;
         }
       }
@@ -472,13 +502,12 @@ cudaError_t launch_weight_tiles(const CacheWeightsParams &P, cudaStream_t st) {
   const int page_rows = std::min(1 << P.c.page_shift, kTile);
   CUtensorMap map;
   if ((e = cache_k_map(P.c, page_rows, &map)) != cudaSuccess) return e;
-  const int64_t rows = static_cast<int64_t>(P.n_rows) * P.group;
-  const int rc = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  const uint32_t group_inverse = static_cast<uint32_t>((0x100000000ull + P.group - 1) / P.group);
   const bool q_vec = reinterpret_cast<uintptr_t>(P.q) % 8 == 0 && P.qs[0] % 4 == 0 && P.qs[1] % 4 == 0 && P.qs[2] % 4 == 0;
   for (int first = 0; first < P.B; first += kTileRequests) {
     const int count = std::min(kTileRequests, P.B - first);
     e = trace_launch("cache_weights_tile", st,
-                     [&] { kern<<<device_sm_count(), kThreads, S::kBytes, st>>>(P, first, count, rc, page_rows, q_vec, map); });
+                     [&] { kern<<<device_sm_count(), kThreads, S::kBytes, st>>>(P, first, count, group_inverse, page_rows, q_vec, map); });
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -487,8 +516,10 @@ cudaError_t launch_weight_tiles(const CacheWeightsParams &P, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_cache_weights(const CacheWeightsParams &P, cudaStream_t st) {
-  if (P.c.head_dim == 128) return P.dtype == SPEC_DTYPE_BF16 ? launch_weight_tiles<SPEC_DTYPE_BF16, 128>(P, st) : launch_weight_tiles<SPEC_DTYPE_F16, 128>(P, st);
-  if (P.c.head_dim == 64) return P.dtype == SPEC_DTYPE_BF16 ? launch_weight_tiles<SPEC_DTYPE_BF16, 64>(P, st) : launch_weight_tiles<SPEC_DTYPE_F16, 64>(P, st);
+  // (a row's number times the group stays below 2^32: the multiplication that divides by it is exact)
+  const bool tiles = static_cast<int64_t>(P.n_rows) * P.group * P.group < (1LL << 32);
+  if (tiles && P.c.head_dim == 128) return P.dtype == SPEC_DTYPE_BF16 ? launch_weight_tiles<SPEC_DTYPE_BF16, 128>(P, st) : launch_weight_tiles<SPEC_DTYPE_F16, 128>(P, st);
+  if (tiles && P.c.head_dim == 64) return P.dtype == SPEC_DTYPE_BF16 ? launch_weight_tiles<SPEC_DTYPE_BF16, 64>(P, st) : launch_weight_tiles<SPEC_DTYPE_F16, 64>(P, st);
   const int64_t most = static_cast<int64_t>(P.c.table_stride) << P.c.page_shift;
   const int spans = most > 0 ? static_cast<int>((most + kSpan - 1) / kSpan) : 1;
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(spans) * P.c.kv_heads * P.B);
