@@ -214,12 +214,14 @@ struct TileWalk {
 
   __device__ TileWalk(const CacheTilePlan &a, const Requests &r, int rt, int lo, int h, int l)
       : A(a), q(r), row_tile(rt), t(lo), hi(h), lane(l), end(lo), u{} {}
-  __device__ __forceinline__ void advance(int slot) {
+  __device__ __forceinline__ bool advance(int slot) {  // whether a new unit begins
+
     pos[slot] = page[slot] = -1;
     head[slot] = 0;
     more[slot] = t < hi;
-    if (t >= hi) return;
-    if (t >= end) {
+    if (t >= hi) return false;
+    const bool fresh = t >= end;
+    if (fresh) {
       u = find_unit(A, q, row_tile, t);
       end = u.tile0 + u.tiles;
       t = max(t, u.tile0);
@@ -231,10 +233,11 @@ struct TileWalk {
       page[slot] = page_at(A.p.c, u.b, at >> A.p.c.page_shift);
     }
     ++t;
+    return fresh;
   }
-  __device__ __forceinline__ void shift() {
+  __device__ __forceinline__ bool shift() {
     more[0] = more[1], pos[0] = pos[1], page[0] = page[1], head[0] = head[1];
-    advance(1);
+    return advance(1);
   }
   // the blocks' scales; 1 where there is no block
   __device__ __forceinline__ void scales(int slot, float &k, float &v) const {
@@ -336,7 +339,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     walk.advance(1);
     for (int sk = 0, lap = 0; walk.more[0];) {
       const int pos = walk.pos[0], page = walk.page[0], head = walk.head[0];
-      walk.shift();
+      if (walk.shift()) [[unlikely]] {  // a unit some tiles ahead: its rows of q into L2, which the stream of keys keeps emptying
+#pragma unroll 1
+        for (int r = lane; r < walk.u.rows; r += 32) {
+          const int row = walk.u.row0 + r, tok = by_group(A, row);
+          const char *q = P.q + (walk.u.b * P.qs[0] + tok * P.qs[1] + (walk.u.head * P.group + row - tok * P.group) * P.qs[2]) * 2;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+          if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 128));
+        }
+      }
       const bool load = pos >= 0 && page >= 0 && (pos & (A.page_rows - 1)) == 0;
       const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(~0u, load)) * A.page_rows * D);
       if (lap > 0 && !warp_wait(&sm.k_empty[sk], (lap - 1) & 1, dead)) break;
@@ -744,15 +755,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int g = 0; g < OWN / 16; ++g) {
           const float shift = sc[g].y - ref + 7.0f, f = CAP ? 1.0f : fmaxf(factor * sc[g].x, 1.2e-38f);
-          float part[4] = {};
+          // two positions to an instruction, except the exponentials and their rounding
+          const float2 f2 = make_float2(f, f), shift2 = make_float2(shift, shift);
+          float2 part[2] = {};
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
-            const float a = ex2(fmaf(x[g * 16 + e], f, shift)), b = ex2(fmaf(x[g * 16 + e + 1], f, shift));
-            part[e & 2] += a;
-            part[(e & 2) + 1] += b;
-            p[g * 8 + e / 2] = half2_bits(a, b);
+            const float2 y = __ffma2_rn(make_float2(x[g * 16 + e], x[g * 16 + e + 1]), f2, shift2);
+            const float2 z = make_float2(ex2(y.x), ex2(y.y));
+            part[e >> 1 & 1] = __fadd2_rn(part[e >> 1 & 1], z);
+            p[g * 8 + e / 2] = half2_bits(z.x, z.y);
           }
-          sum = fmaf((part[0] + part[1]) + (part[2] + part[3]), sc[g].z, sum);
+          const float2 both = __fadd2_rn(part[0], part[1]);
+          sum = fmaf(both.x + both.y, sc[g].z, sum);
         }
         if (i >= 2 && !(ok = warp_wait(&sm.pv_done[sb], (i / 2 - 1) & 1, dead))) break;  // P's columns are free
         tc_fence_after();
