@@ -58,6 +58,7 @@ struct CacheTilePlan {
   int page_rows;        // rows of a page that one copy brings: min(page size, 128)
   bool q_vec, out_vec;  // rows of q and out start on 8-byte boundaries
   uint32_t group_inverse;  // 2^32 / group, rounded up
+  uint64_t ctas_inverse;   // 2^64 / CTAs, rounded up
   int *verdict;          // the requests' status
   int2 *range;           // [CTA] first tile; whether it gave up waiting
   int4 *begun;           // [CTA] the unit that it began and a later one ended

@@ -159,6 +159,7 @@ cudaError_t launch_cache_attend(const CacheAttendParams &P, void *workspace, cud
     A.page_rows = std::min(1 << P.c.page_shift, kTilePositions);
     A.q_vec = rows_on_grain(P.q, P.qs);
     A.out_vec = rows_on_grain(P.out, P.os);
+    A.ctas_inverse = ~0ull / device_sm_count() + 1;
     A.group_inverse = static_cast<uint32_t>((0x100000000ull + P.group - 1) / P.group);
     lay_out(A, static_cast<char *>(workspace), P.c.head_dim);
     CUtensorMap map;

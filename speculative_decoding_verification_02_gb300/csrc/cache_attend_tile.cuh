@@ -161,8 +161,11 @@ __device__ __noinline__ Unit find_unit(const CacheTilePlan &A, const Requests &q
   return unit_of(A, q, row_tile, lo, t);
 }
 
-__device__ __forceinline__ int cut(int total, int parts, int i) {
-  return static_cast<int>(static_cast<int64_t>(total) * i / parts);
+// Where CTA i's range begins: floor(total * i / CTAs) (by a multiplication, exact
+// below 2^64 / CTAs), or i itself when there is less to do than CTAs, so that no
+// CTA has an empty range before one that has not.
+__device__ __forceinline__ int cut(const CacheTilePlan &A, int total, int ctas, int i) {
+  return total < ctas ? min(i, total) : static_cast<int>(__umul64hi(static_cast<uint64_t>(total) * i, A.ctas_inverse));
 }
 
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
@@ -274,7 +277,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
 
-  pdl_launch_dependents();  // (the merge waits for this grid to finish before it reads)
   if (tid == 0) {
     for (int i = 0; i < S::kStagesK; ++i) bar_init(&sm.k_full[i], 1), bar_init(&sm.k_empty[i], 1);
     for (int i = 0; i < S::kStagesV; ++i) bar_init(&sm.v_full[i], 1), bar_init(&sm.v_empty[i], 128);
@@ -323,8 +325,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   __syncthreads();
   const int total = sm.q.start[A.count];
-  const int lo = cut(total, ctas, cta);
-  int hi = cut(total, ctas, cta + 1);
+  const int lo = cut(A, total, ctas, cta);
+  int hi = cut(A, total, ctas, cta + 1);
   if (hi < total) {  // a cut at or before a unit's first tile ends with the unit before
     const Unit u = find_unit(A, sm.q, RT, hi);
     if (hi <= u.tile0) hi = u.start;
@@ -816,7 +818,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           sm.out_at[tid] = u.b * P.os[0] + tok * P.os[1] + h * P.os[2];
         } else {
           A.ml[static_cast<int64_t>(slot) * RT + tid] = make_float2(m_all, l_all);
-          if (tid == 0 && t_begin == u.tile0) sm.begun = make_int4(u.b - A.first, u.head, u.row0 * 2 + (slot & 1), u.tile0 + u.tiles);
+          if (tid == 0 && t_begin == u.tile0) sm.begun = make_int4(u.b - A.first, u.head << 8 | u.rows, u.row0 * 2 + (slot & 1), u.tile0 + u.tiles);
         }
         if (sm.spoiled[tid]) norm = NAN;
         sm.spoiled[tid] = 0;
@@ -898,6 +900,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  pdl_launch_dependents();  // (not earlier: the merge's blocks would crowd onto the SMs that finish first)
   if (tid == 0) {
     A.range[cta] = make_int2(lo, sm.dead);
     A.begun[cta] = sm.begun;
@@ -911,14 +914,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // Joins the partial sums of the units that more than one CTA worked on: block
 // (c, j) takes 32 rows, a lane each, of the unit that CTA c began and a later
 // one ended, each warp an eighth of the columns.  The last blocks set the
-// requests' status, and clear the outputs of those with a bad page.
+// requests' status, and clear the outputs of those with a bad page.  It lasts
+// about as long as its instructions take to arrive, so there are few, and few
+// loads wait for one another.
 template <int DT, int D>
 __global__ void __launch_bounds__(256) cache_attend_merge_kernel(const CacheTilePlan A, int row_tile, int ctas) {
   const CacheAttendParams &P = A.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kOwn = D / 32;  // float4s of a row to a warp
   pdl_wait();
-  const int chunks = row_tile / 32;
+  const int chunks = row_tile >> 5, shift = chunks >> 1;  // (1, 2 or 4)
   if (static_cast<int>(blockIdx.x) >= ctas * chunks) {
     const int bl = (blockIdx.x - ctas * chunks) * 8 + warp, b = A.first + bl;
     if (bl >= A.count) return;
@@ -931,77 +936,65 @@ __global__ void __launch_bounds__(256) cache_attend_merge_kernel(const CacheTile
       for (int x = lane; x < P.N * P.Hq; x += 32) zero_row<DT, D>(P, b, x);
     return;
   }
-  const int c0 = blockIdx.x / chunks, r = (blockIdx.x % chunks) * 32 + lane;
-  const int4 unit = A.begun[c0];  // request, head, 2 * first row + c0's slot, end of its tiles
+  const int c0 = blockIdx.x >> shift, r = (blockIdx.x & (chunks - 1)) * 32 + lane;
+  const int4 unit = A.begun[c0];  // request, head << 8 | rows, 2 * first row + c0's slot, end of its tiles
   if (unit.x < 0) return;
-  const int b = A.first + unit.x;
-  int base, n;
-  request_lengths(P, b, base, n);
-  const int row = (unit.z >> 1) + r;
-  const bool live = row < n * P.group;
-  const bool fine = A.verdict[unit.x] == SPEC_STATUS_OK;
-  // the last CTA that begins before the unit's end; nobody gave up
-  int c1 = -1;
-  bool gone = !fine;
-  for (int c = lane; c - lane < ctas; c += 32) {
-    const int2 range = c < ctas ? A.range[c] : make_int2(0x7fffffff, 0);
-    gone |= range.y != 0;
-    c1 += __popc(__ballot_sync(~0u, range.x < unit.w));
+  const int verdict = A.verdict[unit.x];
+  // the last CTA that begins before the unit's end
+  int later = 0;
+  for (int c = c0 + 1; c < ctas; c += 160) {
+#pragma unroll
+    for (int k = 0; k < 5; ++k) later += c + k * 32 + lane < ctas && A.range[c + k * 32 + lane].x < unit.w ? 1 : 0;
   }
-  if (__any_sync(~0u, gone)) return;
+  later = __reduce_add_sync(~0u, later);
+  const int rows = unit.y & 255, from = min(r, rows - 1);  // (rows that are not there would be read from DRAM: nothing wrote them)
+  const bool live = r < rows;
+  if ((r & ~31) >= rows) return;
   float m = -INFINITY, sum = 0.0f;
   float4 acc[kOwn];
 #pragma unroll
   for (int e = 0; e < kOwn; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  // four CTAs' loads at a time
+  // four CTAs' parts at a time (past the last one: that one again, without weight)
 #pragma unroll 1
-  for (int cc = c0; cc <= c1; cc += 4) {
+  for (int k = 0; k <= later; k += 4) {
     float2 ml[4];
     float4 o[4][kOwn];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = cc + k;
-      ml[k] = make_float2(-INFINITY, 0.0f);
-      const bool has = c <= c1 && live && (c == c1 || A.range[c + 1].x > A.range[c].x);
+    for (int q = 0; q < 4; ++q) {
+      const int c = c0 + min(k + q, later), slot = c * 2 + (c == c0 ? unit.z & 1 : 0);
+      ml[q] = A.ml[slot * row_tile + from];
+      const float4 *part = reinterpret_cast<const float4 *>(A.part) + (static_cast<int64_t>(slot) * (D / 4) + warp * kOwn) * row_tile + from;
 #pragma unroll
-      for (int e = 0; e < kOwn; ++e) o[k][e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (has) {
-        const int64_t slot = c * 2 + (c == c0 ? unit.z & 1 : 0);
-        ml[k] = A.ml[slot * row_tile + r];
-        const float4 *part = reinterpret_cast<const float4 *>(A.part) + (slot * (D / 4) + warp * kOwn) * row_tile + r;
-#pragma unroll
-        for (int e = 0; e < kOwn; ++e) o[k][e] = part[e * row_tile];
-      }
+      for (int e = 0; e < kOwn; ++e) o[q][e] = part[e * row_tile];
     }
-    float top = m;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
-    const float ref = top == -INFINITY ? 0.0f : top, keep = ex2(m - ref);
+    const float top = fmaxf(fmaxf(fmaxf(m, ml[0].x), ml[1].x), fmaxf(ml[2].x, ml[3].x)), ref = top == -INFINITY ? 0.0f : top;
+    const float keep = ex2(m - ref);
     m = top;
     sum *= keep;
 #pragma unroll
     for (int e = 0; e < kOwn; ++e) acc[e].x *= keep, acc[e].y *= keep, acc[e].z *= keep, acc[e].w *= keep;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float w = ex2(ml[k].x - ref);
-      sum = fmaf(ml[k].y, w, sum);
+    for (int q = 0; q < 4; ++q) {
+      if (k + q > later) break;
+      const float w = ex2(ml[q].x - ref);
+      sum = fmaf(ml[q].y, w, sum);
 #pragma unroll
       for (int e = 0; e < kOwn; ++e) {
-        acc[e].x = fmaf(o[k][e].x, w, acc[e].x);
-        acc[e].y = fmaf(o[k][e].y, w, acc[e].y);
-        acc[e].z = fmaf(o[k][e].z, w, acc[e].z);
-        acc[e].w = fmaf(o[k][e].w, w, acc[e].w);
+        acc[e].x = fmaf(o[q][e].x, w, acc[e].x);
+        acc[e].y = fmaf(o[q][e].y, w, acc[e].y);
+        acc[e].z = fmaf(o[q][e].z, w, acc[e].z);
+        acc[e].w = fmaf(o[q][e].w, w, acc[e].w);
       }
     }
   }
-  if (!live) return;
-  const int i = by_group(A, row), h = unit.y * P.group + row - i * P.group;
+  if (!live || verdict != SPEC_STATUS_OK) return;
+  const int b = A.first + unit.x, row = (unit.z >> 1) + r, i = by_group(A, row), h = (unit.y >> 8) * P.group + row - i * P.group;
   char *out = P.out + (b * P.os[0] + i * P.os[1] + h * P.os[2]) * 2;
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
 #pragma unroll
   for (int e = 0; e < kOwn; ++e) {
     const int d = (warp * kOwn + e) * 4;
-    if (A.out_vec) {
+    if (A.out_vec) [[likely]] {
       *reinterpret_cast<uint2 *>(out + d * 2) =
           make_uint2(pair_bits<DT>(acc[e].x * inv, acc[e].y * inv), pair_bits<DT>(acc[e].z * inv, acc[e].w * inv));
     } else {
@@ -1010,7 +1003,7 @@ __global__ void __launch_bounds__(256) cache_attend_merge_kernel(const CacheTile
     }
   }
   if (warp == 0 && P.lse)
-    P.lse[(static_cast<int64_t>(b) * P.N + i) * P.Hq + h] = sum == 0.0f ? -INFINITY : (m - 7.0f + log2f(sum)) * kLn2;
+    P.lse[(static_cast<int64_t>(b) * P.N + i) * P.Hq + h] = sum == 0.0f ? -INFINITY : (m - 7.0f + __log2f(sum)) * kLn2;
 }
 
 // Devices on which a kernel may already use its shared memory.
