@@ -24,6 +24,9 @@ struct CacheView {
   int table_stride;
 };
 
+// Positions that a request's table can hold.
+inline int64_t capacity_of(const CacheView &c) { return static_cast<int64_t>(c.table_stride) << c.page_shift; }
+
 struct CacheAppendParams {
   CacheView c;
   const char *k, *v;

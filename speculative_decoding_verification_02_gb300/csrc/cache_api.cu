@@ -137,7 +137,7 @@ int spec_cache_attend(const spec_cache *cache, const void *q, const int64_t *q_s
   if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.0f) return SPEC_EINVAL;
   if ((rc = check_rows(dtype, false, q)) != SPEC_OK || (rc = check_rows(dtype, false, out)) != SPEC_OK) return rc;
   if (B == 0 || N == 0) return SPEC_OK;
-  if (!q || !out || !cache_len || static_cast<int64_t>(B) * N * Hq > kMaxGrid) return SPEC_EINVAL;
+  if (!q || !out || !cache_len || static_cast<int64_t>(B) * N * Hq > kMaxGrid / 8) return SPEC_EINVAL;
   P.q = static_cast<const char *>(q);
   P.out = static_cast<char *>(out);
   std::copy(q_stride, q_stride + 3, P.qs);

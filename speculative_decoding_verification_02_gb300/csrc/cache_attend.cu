@@ -4,8 +4,10 @@
 //   out = sum_j exp(x_j - m) v_j / sum_j exp(x_j - m),  lse = m + log sum_j exp(x_j - m)
 //
 // in one pass with the running maximum m and sum.  Heads of 64 and 128 run on
-// the tensor cores (cache_attend_tile.cuh), other widths a warp to a row.
+// the tensor cores (cache_attend_tile.cuh); other widths, and a few rows over
+// many heads or a short context, on the scalar units.
 #include <algorithm>
+#include <cooperative_groups.h>
 
 #include "cache.cuh"
 #include "common.cuh"
@@ -14,92 +16,288 @@
 namespace sv {
 namespace {
 
-constexpr int kRowWarps = 4;  // rows to a CTA of the general kernel
+constexpr int kRowThreads = 256;
+constexpr int kSpanPages = 256;  // pages whose places are held in shared memory at a time
+constexpr int kAtOnce = 4;       // positions that a group of lanes has in flight
 
-// One warp to a row: 32 positions at a time, a lane scoring one of them, then
-// the lanes across the components for the values.
-template <int DT>
-__global__ void __launch_bounds__(32 * kRowWarps) cache_attend_rows_kernel(const CacheAttendParams P) {
-  __shared__ float s_q[kRowWarps][256];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t rows = static_cast<int64_t>(P.B) * P.N * P.Hq;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp;
-  if (r >= rows) return;
-  const int h = static_cast<int>(r % P.Hq), i = static_cast<int>(r / P.Hq % P.N), b = static_cast<int>(r / P.Hq / P.N);
-  const int head = h / P.group, D = P.c.head_dim;
-  const int64_t base = P.cache_len[b];
-  const int n = P.n_query ? P.n_query[b] : P.N;
+// Up to ROWS rows of a kv head to a cluster of CTAs, each with a share of the
+// positions.  LANES lanes score a position, 16 bytes of its key each, and add
+// 16 bytes of its value; every such group of lanes keeps its own running
+// maximum, sum and result, joined in the warp, the CTA and the cluster at the
+// end.  Keys and values are read once and never staged; the arithmetic is
+// scalar, about (3 + 2 ROWS) instructions a 16-byte lane and value, so it keeps
+// up with the memory for a few rows.
+template <int DT, int LANES, int ROWS, bool CAP>
+__global__ void __launch_bounds__(kRowThreads) cache_attend_rows_kernel(const CacheAttendParams P, int chunks) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  __shared__ int64_t s_at[kSpanPages];
+  __shared__ float2 s_scale[kSpanPages];
+  __shared__ float s_acc[kRowThreads / 32][ROWS][LANES * 16];
+  __shared__ float2 s_ml[kRowThreads / 32][ROWS];
+  constexpr int kGroups = 32 / LANES, kAll = kRowThreads / LANES;
+  const int splits = static_cast<int>(cluster.num_blocks()), split = static_cast<int>(cluster.block_rank());
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, part = lane % LANES, group = tid / LANES;
+  int x = blockIdx.x / splits;
+  const int chunk = x % chunks;
+  x /= chunks;
+  const int head = x % P.c.kv_heads, b = x / P.c.kv_heads, D = P.c.head_dim, shift = P.c.page_shift;
+  const bool used = part * 16 < D;
+
+  int base = P.cache_len[b], n = P.n_query ? P.n_query[b] : P.N;
   int st = SPEC_STATUS_OK;
-  if (base < 0 || n < 0 || n > P.N || base + n > capacity(P.c)) st = SPEC_STATUS_BAD_LENGTH;
+  if (base < 0 || n < 0 || n > P.N || base + static_cast<int64_t>(n) > capacity(P.c)) st = SPEC_STATUS_BAD_LENGTH, base = n = 0;
+  // a bad page anywhere takes the request out, for every row alike
+  int bad = 0;
+  for (int i = tid; static_cast<int64_t>(i) << shift < base + n; i += kRowThreads) bad |= page_at(P.c, b, i) < 0;
+  if (__syncthreads_or(bad)) st = SPEC_STATUS_BAD_PAGE;
+  if (P.status && head == 0 && chunk == 0 && split == 0 && tid == 0) P.status[b] = st;
+  if (st != SPEC_STATUS_OK) base = n = 0;
 
-  const char *q = P.q + (b * P.qs[0] + i * P.qs[1] + h * P.qs[2]) * 2;
-  for (int d = lane; d < D; d += 32) s_q[warp][d] = row_value<DT>(q, d);
-  __syncwarp();
-  float m = -INFINITY, sum = 0.0f, acc[8] = {};
-  const int64_t T = st == SPEC_STATUS_OK ? base + n : 0;
-  const bool live = i < n;
-  const uint8_t *mask = P.mask ? P.mask + (static_cast<int64_t>(b) * P.N + i) * P.N : nullptr;
-  for (int64_t t0 = 0; t0 < T; t0 += 32) {
-    const int64_t j = t0 + lane;
-    const int page = j < T ? page_at(P.c, b, j >> P.c.page_shift) : 0;
-    if (__any_sync(~0u, page < 0)) {
-      st = SPEC_STATUS_BAD_PAGE;
-      break;
-    }
-    if (!live) continue;  // (the pages of a request decide its status on every row)
-    const bool sees = j < T && (j < base || (mask ? mask[j - base] != 0 : j - base <= i));
-    const int64_t at = block_offset(P.c, page, head) + (j & ((1 << P.c.page_shift) - 1)) * D;
-    float x = -INFINITY;
-    if (sees) {
-      const uint4 *k = reinterpret_cast<const uint4 *>(P.c.k + at);
-      float dot = 0.0f;
-      for (int g = 0; g < D / 16; ++g) {
-        const uint4 w4 = k[g];
-        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+  const int row0 = chunk * ROWS, rows = min(ROWS, n * P.group - row0);
+  int token[ROWS];
+  float q[ROWS][16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 lo = e4m3x2_to_float2(w[e] & 0xffff), hi = e4m3x2_to_float2(w[e] >> 16);
-          const float *qq = &s_q[warp][g * 16 + e * 4];
-          dot = fmaf(qq[0], lo.x, fmaf(qq[1], lo.y, fmaf(qq[2], hi.x, fmaf(qq[3], hi.y, dot))));
+  for (int k = 0; k < ROWS; ++k) {
+    const int row = row0 + k;
+    token[k] = row / P.group;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) q[k][e] = 0.0f;
+    if (k < rows && used) {
+      const char *src = P.q + (b * P.qs[0] + token[k] * P.qs[1] + (head * P.group + row % P.group) * P.qs[2]) * 2;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) q[k][e] = row_value<DT>(src, part * 16 + e) * (CAP ? P.scale : P.scale * kLog2e);
+    }
+  }
+  // positions of this CTA: whole steps of all its groups
+  const int T = rows > 0 ? (P.mask ? base + n : base + token[0] + 1 + (rows - 1 + row0 % P.group) / P.group) : 0;
+  const int share = ((T + splits - 1) / splits + kAll - 1) / kAll * kAll;
+  const int from = min(T, split * share), to = min(T, from + share);
+  const uint8_t *mask = P.mask ? P.mask + static_cast<int64_t>(b) * P.N * P.N : nullptr;
+
+  const float cap2 = P.softcap * kLog2e, in_cap = CAP ? 2.0f * kLog2e / P.softcap : 0.0f;
+  float m[ROWS], sum[ROWS], acc[ROWS][16];
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    m[k] = -INFINITY, sum[k] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[k][e] = 0.0f;
+  }
+  for (int s0 = from >> shift << shift; s0 < to; s0 += kSpanPages << shift) {
+    const int s1 = min(to, s0 + (kSpanPages << shift));
+    __syncthreads();
+    for (int i = tid; s0 + (i << shift) < s1; i += kRowThreads) {
+      const int page = page_at(P.c, b, (s0 >> shift) + i);
+      const int64_t at = page * P.c.scale_stride + head;
+      s_at[i] = block_offset(P.c, page, head);
+      s_scale[i] = make_float2(P.c.k_scale[at], P.c.v_scale[at]);
+    }
+    __syncthreads();
+    // (every lane of a warp takes as many steps: the shuffles below need them all)
+    for (int t0 = max(from, s0); t0 < s1; t0 += kAll * kAtOnce) {
+      uint4 kk[kAtOnce], vv[kAtOnce];
+      float2 sc[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int t = t0 + u * kAll + group;
+        kk[u] = vv[u] = make_uint4(0, 0, 0, 0);
+        sc[u] = make_float2(0.0f, 0.0f);
+        if (t < s1) {
+          const int i = (t - s0) >> shift;
+          const int64_t at = s_at[i] + (t & ((1 << shift) - 1)) * D + part * 16;
+          sc[u] = s_scale[i];
+          if (used) {
+            kk[u] = ld_stream16(P.c.k + at);
+            vv[u] = ld_stream16(P.c.v + at);
+          }
         }
       }
-      x = capped_log2(P.scale * dot * P.c.k_scale[page * P.c.scale_stride + head], P.softcap);
-    }
-    float top = x;
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    const float next = fmaxf(m, top);
-    const float ref = next == -INFINITY ? 0.0f : next;
-    const float keep = exp2f(m - ref);
-    const float p = sees ? exp2f(x - ref) : 0.0f;
-    m = next;
-    sum = sum * keep + warp_sum(p);
+      float score[kAtOnce][ROWS];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c] *= keep;
-    const float vs = sees ? P.c.v_scale[page * P.c.scale_stride + head] : 0.0f;
-    for (unsigned left = __ballot_sync(~0u, sees); left; left &= left - 1) {
-      const int o = __ffs(left) - 1;
-      const float w = __shfl_sync(~0u, p * vs, o);
-      const uint8_t *v = P.c.v + __shfl_sync(~0u, at, o);
-      for (int c = 0; c < 8; ++c) {
-        const int d = lane + 32 * c;
-        if (d < D) acc[c] = fmaf(w, e4m3x2_to_float2(v[d]).x, acc[c]);
+      for (int u = 0; u < kAtOnce; ++u) {
+        float dot[ROWS] = {};
+        const uint32_t w[4] = {kk[u].x, kk[u].y, kk[u].z, kk[u].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 a = e4m3x2_to_float2(w[e] & 0xffff), c = e4m3x2_to_float2(w[e] >> 16);
+#pragma unroll
+          for (int k = 0; k < ROWS; ++k)
+            dot[k] = fmaf(q[k][4 * e], a.x, fmaf(q[k][4 * e + 1], a.y, fmaf(q[k][4 * e + 2], c.x, fmaf(q[k][4 * e + 3], c.y, dot[k]))));
+        }
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1)
+#pragma unroll
+          for (int k = 0; k < ROWS; ++k) dot[k] += __shfl_xor_sync(~0u, dot[k], o);
+        const int t = t0 + u * kAll + group, j = t - base;
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+          float y = dot[k] * sc[u].x;
+          if (CAP) {  // cap tanh(x / cap) = cap (1 - 2 / (1 + exp(2 x / cap)))
+            const float z = y * in_cap;
+            y = cap2 * (1.0f - __fdividef(2.0f, 1.0f + ex2(z > 120.0f ? 120.0f : z)));
+          }
+          const bool sees = t < s1 && k < rows && (j < 0 || (mask ? mask[static_cast<int64_t>(token[k]) * P.N + j] != 0 : j <= token[k]));
+          score[u][k] = sees ? y : -INFINITY;
+        }
+        if (j >= 0) [[unlikely]] {  // a value that no row may look at, or that is no number, has no part in the others
+          bool any = false;
+#pragma unroll
+          for (int k = 0; k < ROWS; ++k) any |= score[u][k] != -INFINITY;
+          if (!any) vv[u] = make_uint4(0, 0, 0, 0);
+        }
+      }
+      bool moves = false;
+      float next[ROWS];
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) {
+        next[k] = m[k];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) next[k] = fmaxf(next[k], score[u][k]);
+        moves |= next[k] > m[k];
+      }
+      if (__any_sync(~0u, moves)) {
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+          const float keep = next[k] == -INFINITY ? 0.0f : ex2(m[k] - next[k]);
+          m[k] = next[k];
+          sum[k] *= keep;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[k][e] *= keep;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        float p[ROWS];
+        bool part_of[ROWS];
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+          part_of[k] = score[u][k] != -INFINITY;
+          p[k] = part_of[k] ? ex2(score[u][k] - m[k]) : 0.0f;
+          sum[k] += p[k];
+          p[k] *= sc[u].y;
+        }
+        const bool plain = t0 + u * kAll + group < base;  // every row sees it
+        const uint32_t w[4] = {vv[u].x, vv[u].y, vv[u].z, vv[u].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 a = e4m3x2_to_float2(w[e] & 0xffff), c = e4m3x2_to_float2(w[e] >> 16);
+#pragma unroll
+          for (int k = 0; k < ROWS; ++k) {
+            if (ROWS > 1 && !plain && !part_of[k]) continue;
+            acc[k][4 * e] = fmaf(p[k], a.x, acc[k][4 * e]);
+            acc[k][4 * e + 1] = fmaf(p[k], a.y, acc[k][4 * e + 1]);
+            acc[k][4 * e + 2] = fmaf(p[k], c.x, acc[k][4 * e + 2]);
+            acc[k][4 * e + 3] = fmaf(p[k], c.y, acc[k][4 * e + 3]);
+          }
+        }
       }
     }
   }
-  const bool empty = st != SPEC_STATUS_OK || !live || sum == 0.0f;
-  const float inv = 1.0f / sum;
-  char *out = P.out + (b * P.os[0] + i * P.os[1] + h * P.os[2]) * 2;
-  for (int c = 0; c < 8; ++c) {
-    const int d = lane + 32 * c;
-    if (d < D) put_value<DT>(out, d, empty ? 0.0f : acc[c] * inv);
+  // the groups of a warp, then its sums to shared memory
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+#pragma unroll
+    for (int o = LANES; o < 32; o <<= 1) {
+      const float other = __shfl_xor_sync(~0u, m[k], o), both = fmaxf(m[k], other), ref = both == -INFINITY ? 0.0f : both;
+      const float keep = ex2(m[k] - ref);
+      m[k] = both;
+      sum[k] *= keep;
+      sum[k] += __shfl_xor_sync(~0u, sum[k], o);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        acc[k][e] *= keep;
+        acc[k][e] += __shfl_xor_sync(~0u, acc[k][e], o);
+      }
+    }
+    if (lane < LANES) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<float4 *>(&s_acc[warp][k][part * 16 + e]) = make_float4(acc[k][e], acc[k][e + 1], acc[k][e + 2], acc[k][e + 3]);
+      if (lane == 0) s_ml[warp][k] = make_float2(m[k], sum[k]);
+    }
   }
-  if (lane == 0) {
-    if (P.lse) P.lse[r] = empty ? -INFINITY : (m + log2f(sum)) * kLn2;
-    if (P.status && i == 0 && h == 0) P.status[b] = st;
+  __syncthreads();
+  // the warps of every CTA of the cluster, a column to a thread; each CTA takes a share of the rows' columns
+  if (splits > 1) cluster.sync();
+  const int all = ROWS * D;
+  for (int i = split * kRowThreads + tid; i < all; i += splits * kRowThreads) {
+    const int k = i / D, d = i - k * D, row = row0 + k;
+    if (row >= P.N * P.group) break;
+    float top = -INFINITY;
+    for (int s = 0; s < splits; ++s) {
+      const float2 *ml = splits > 1 ? cluster.map_shared_rank(&s_ml[0][0], s) : &s_ml[0][0];
+#pragma unroll
+      for (int w = 0; w < kRowThreads / 32; ++w) top = fmaxf(top, ml[w * ROWS + k].x);
+    }
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float l = 0.0f, o = 0.0f;
+    for (int s = 0; s < splits; ++s) {
+      const float2 *ml = splits > 1 ? cluster.map_shared_rank(&s_ml[0][0], s) : &s_ml[0][0];
+      const float *a = splits > 1 ? cluster.map_shared_rank(&s_acc[0][0][0], s) : &s_acc[0][0][0];
+#pragma unroll
+      for (int w = 0; w < kRowThreads / 32; ++w) {
+        const float2 one = ml[w * ROWS + k];
+        const float weight = ex2(one.x - ref);
+        l = fmaf(one.y, weight, l);
+        o = fmaf(a[(w * ROWS + k) * LANES * 16 + d], weight, o);
+      }
+    }
+    const int i_tok = row / P.group, h = head * P.group + row % P.group;
+    put_value<DT>(P.out + (b * P.os[0] + i_tok * P.os[1] + h * P.os[2]) * 2, d, l == 0.0f ? 0.0f : o / l);
+    if (d == 0 && P.lse) P.lse[(static_cast<int64_t>(b) * P.N + i_tok) * P.Hq + h] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
   }
+  if (splits > 1) cluster.sync();  // no CTA leaves while its sums are read
 }
 
 // ------------------------------------------------------------------- host
+
+int64_t row_units(const CacheAttendParams &P, int rows_to_a_unit) {
+  return static_cast<int64_t>(P.B) * P.c.kv_heads * ((static_cast<int64_t>(P.N) * P.group + rows_to_a_unit - 1) / rows_to_a_unit);
+}
+
+int rows_of(const CacheAttendParams &P) {
+  const int64_t rows = static_cast<int64_t>(P.N) * P.group;
+  return rows <= 1 ? 1 : rows <= 2 ? 2 : 4;
+}
+
+// CTAs to a unit: enough for two to every SM, eight at most, and no share of
+// the positions below 64.
+int row_splits(const CacheAttendParams &P) {
+  const int64_t units = row_units(P, rows_of(P)), most = capacity_of(P.c);
+  int n = 1;
+  while (n < 8 && units * n < 2 * device_sm_count() && most / (2 * n) >= 64) n *= 2;
+  return n;
+}
+
+template <int DT, int LANES, int ROWS>
+cudaError_t launch_rows(const CacheAttendParams &P, cudaStream_t st) {
+  const int splits = row_splits(P);
+  const int chunks = static_cast<int>((static_cast<int64_t>(P.N) * P.group + ROWS - 1) / ROWS);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(row_units(P, ROWS) * splits));
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = splits;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto kern = P.softcap > 0.0f ? cache_attend_rows_kernel<DT, LANES, ROWS, true> : cache_attend_rows_kernel<DT, LANES, ROWS, false>;
+  return trace_launch_ex("cache_attend_rows", st, [&] { return cudaLaunchKernelEx(&cfg, kern, P, chunks); });
+}
+
+template <int DT, int LANES>
+cudaError_t launch_rows(const CacheAttendParams &P, cudaStream_t st) {
+  const int rows = rows_of(P);
+  return rows == 1 ? launch_rows<DT, LANES, 1>(P, st) : rows == 2 ? launch_rows<DT, LANES, 2>(P, st) : launch_rows<DT, LANES, 4>(P, st);
+}
+
+template <int DT>
+cudaError_t launch_rows(const CacheAttendParams &P, cudaStream_t st) {
+  const int D = P.c.head_dim;
+  return D <= 64 ? launch_rows<DT, 4>(P, st) : D <= 128 ? launch_rows<DT, 8>(P, st) : launch_rows<DT, 16>(P, st);
+}
 
 int copies_of(int N, int group) {
   const int64_t rows = static_cast<int64_t>(N) * group;
@@ -117,7 +315,7 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 int requests_at_once(const CacheAttendParams &P) {
   const int rt = 128 / copies_of(P.N, P.group);
   const int64_t row_tiles = (static_cast<int64_t>(P.N) * P.group + rt - 1) / rt;
-  const int64_t tiles = ((static_cast<int64_t>(P.c.table_stride) << P.c.page_shift) / kTilePositions + 1 + kTileUnitCost) * row_tiles * P.c.kv_heads;
+  const int64_t tiles = (capacity_of(P.c) / kTilePositions + 1 + kTileUnitCost) * row_tiles * P.c.kv_heads;
   return static_cast<int>(std::min<int64_t>(kTileRequests, 2000000000LL / std::max(tiles, row_tiles * rt * P.c.kv_heads)));
 }
 
@@ -141,8 +339,17 @@ size_t lay_out(CacheTilePlan &A, char *ws, int D) {
 
 bool cache_attend_on_tensor_cores(const CacheAttendParams &P) {
   // (a row's number times the group stays below 2^32: the multiplication that divides by it is exact)
-  return (P.c.head_dim == 64 || P.c.head_dim == 128) && static_cast<int64_t>(P.N) * P.group * P.group < (1LL << 32) &&
-         requests_at_once(P) > 0;
+  if ((P.c.head_dim != 64 && P.c.head_dim != 128) || static_cast<int64_t>(P.N) * P.group * P.group >= (1LL << 32) ||
+      requests_at_once(P) <= 0)
+    return false;
+  // The tensor cores work on 128 rows whatever there are, and their kernel starts and joins its units slowly; the scalar kernel's
+  // time goes with the rows and the components.  Measured (scalar against tensor cores, us): one row, 64 wide, 32 requests of 16
+  // heads and 1,500 positions 26 and 38, 64 of 8 and 4,000 54 and 58; 128 wide, 1,500: 42 and 45, 4,000: 97 and 72; four rows,
+  // 128 wide, 8 heads: 300 positions 10 and 11, 2,000: 12 and 13, 16,000: 33 and 19.
+  const int64_t rows = static_cast<int64_t>(P.N) * P.group, D = P.c.head_dim;
+  if (rows == 1 && D == 64) return false;
+  const int64_t work = static_cast<int64_t>(P.B) * P.c.kv_heads * capacity_of(P.c) * D * rows;
+  return rows > 4 || work > (rows == 1 ? 100000000 : 16000000);
 }
 
 size_t cache_attend_workspace(const CacheAttendParams &P) {
@@ -173,12 +380,7 @@ cudaError_t launch_cache_attend(const CacheAttendParams &P, void *workspace, cud
     }
     return cudaSuccess;
   }
-  const int64_t rows = static_cast<int64_t>(P.B) * P.N * P.Hq;
-  const unsigned grid = static_cast<unsigned>((rows + kRowWarps - 1) / kRowWarps);
-  return trace_launch("cache_attend_rows", st, [&] {
-    if (P.dtype == SPEC_DTYPE_BF16) cache_attend_rows_kernel<SPEC_DTYPE_BF16><<<grid, 32 * kRowWarps, 0, st>>>(P);
-    else cache_attend_rows_kernel<SPEC_DTYPE_F16><<<grid, 32 * kRowWarps, 0, st>>>(P);
-  });
+  return P.dtype == SPEC_DTYPE_BF16 ? launch_rows<SPEC_DTYPE_BF16>(P, st) : launch_rows<SPEC_DTYPE_F16>(P, st);
 }
 
 }  // namespace sv
