@@ -285,9 +285,9 @@ __device__ __forceinline__ uint4 rescaled(const uint4 &v, float ratio) {
   return r;
 }
 
-constexpr int kGatherHeld = 4;  // 16-byte pieces that a thread holds
+constexpr int kGatherHeld = 2;  // 16-byte pieces that a thread holds
 
-// TEAM threads to a block, so that each has about four pieces of it; PER_ROW:
+// TEAM threads to a block, so that each has about two pieces of it; PER_ROW:
 // pieces of a row, 0: any.
 template <int TEAM, int PER_ROW>
 __global__ void __launch_bounds__(kGatherThreads, 5) cache_gather_kernel(const CacheEvictParams P, int pages, uint32_t blocks) {
@@ -416,11 +416,11 @@ cudaError_t launch_cache_evict(const CacheEvictParams &P, cudaStream_t st) {
   cfg.numAttrs = 1;
   e = trace_launch_ex("cache_select", st, [&] { return cudaLaunchKernelEx(&cfg, kern, P, room); });
   if (e != cudaSuccess) return e;
-  // four pieces to a thread
+  // two pieces to a thread
   const int pieces = (P.c.head_dim << P.c.page_shift) / 16;
-  if (pieces <= 128) return launch_gather<32>(P, st);
-  if (pieces <= 256) return launch_gather<64>(P, st);
-  if (pieces <= 512) return launch_gather<128>(P, st);
+  if (pieces <= 64) return launch_gather<32>(P, st);
+  if (pieces <= 128) return launch_gather<64>(P, st);
+  if (pieces <= 256) return launch_gather<128>(P, st);
   return launch_gather<256>(P, st);
 }
 
