@@ -107,21 +107,23 @@ __global__ void __launch_bounds__(kSpan) cache_weights_rows_kernel(const CacheWe
 // The tiles of all (request, head) units are laid end to end and cut evenly
 // over the CTAs, a unit's start counting as some tiles.  Rows are taken 64 at a
 // time (the operand holds as many as there are, in sixteens); further rows of a
-// unit go over its tiles again, adding to what is there.  Two groups of four
-// warps take alternate tiles.  Bound by reading K (head_dim bytes a position
+// unit go over its tiles again, adding to what is there.  A tile is 256
+// positions, two operands of 128, a side of four warps to each: with 128 to a
+// tile the loading and the issuing warp took longer over one (about 900 cycles,
+// most of them waits that were over already) than its bytes take to arrive.  Bound by reading K (head_dim bytes a position
 // and kv head) for few rows, by the exponentials for many.
 
-constexpr int kTile = kTilePositions;
-constexpr int kThreads = 320;  // two groups of 4 summing warps, 1 loading, 1 issuing
+constexpr int kTile = 256;      // positions to a tile
+constexpr int kThreads = 320;  // two sides of 4 summing warps, 1 loading, 1 issuing
 constexpr int kRing = 8;
 constexpr int kMaxRows = 64;   // rows at a time
-constexpr int kUnitCost = 3;   // what a unit costs besides its tiles, in tiles
+constexpr int kUnitCost = 2;   // what a unit costs besides its tiles, in tiles
 
 template <int DT, int D>
 struct WeightShape {
   static constexpr int kPieces = DT == SPEC_DTYPE_BF16 ? 2 : 3;
   static constexpr int kStage = kTile * D;
-  static constexpr int kStages = D == 128 ? 8 : 12;
+  static constexpr int kStages = D == 128 ? 4 : 6;
   static constexpr int kQ = 0;
   static constexpr int kK = kPieces * kMaxRows * D;
   static constexpr int kSmall = kK + kStages * kStage;
@@ -133,8 +135,8 @@ struct WeightSmall {
   int2 lens[kTileRequests];      // context, rows
   alignas(16) float2 row[kMaxRows];          // factor of a row's scores, its lse negated; both in units of log 2
   int token[kMaxRows];           // its place behind the context
-  float ring[kRing][8];          // k_scale of 16 positions
-  uint64_t k_full[12], k_empty[12], s_full[4], s_empty[4], q_full, meet, ring_full[kRing], ring_empty[kRing];
+  float ring[kRing][16];         // k_scale of 16 positions
+  uint64_t k_full[6], k_empty[6], s_full[2], s_empty[2], q_full, meet, ring_full[kRing], ring_empty[kRing];
   uint32_t tmem;
   int bad[2], dead;
 };
@@ -192,10 +194,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < S::kStages; ++i) bar_init(&sm.k_full[i], 1), bar_init(&sm.k_empty[i], 1);
-    for (int i = 0; i < 4; ++i) bar_init(&sm.s_full[i], 2), bar_init(&sm.s_empty[i], 128);
+    for (int i = 0; i < 2; ++i) bar_init(&sm.s_full[i], 2), bar_init(&sm.s_empty[i], 256);
     bar_init(&sm.q_full, 256);
     bar_init(&sm.meet, 256);
-    for (int i = 0; i < kRing; ++i) bar_init(&sm.ring_full[i], 32), bar_init(&sm.ring_empty[i], 128);
+    for (int i = 0; i < kRing; ++i) bar_init(&sm.ring_full[i], 32), bar_init(&sm.ring_empty[i], 256);
     bar_init_fence();
     sm.dead = sm.bad[0] = sm.bad[1] = 0;
   }
@@ -235,12 +237,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint32_t tmem = sm.tmem;
   volatile int *dead = &sm.dead;
-  constexpr int kBuffers = S::kPieces == 2 ? 4 : 2, kBufferCols = 512 / kBuffers;  // tensor memory: scores of a tile
+  constexpr int kBuffers = S::kPieces == 2 ? 2 : 1, kSideCols = 256 / kBuffers;  // tensor memory: scores of a tile's sides
   auto chunks_of = [&](const WeightUnit &u) { return max(1, (u.cnt * P.group + kMaxRows - 1) / kMaxRows); };  // (no rows: prev is copied)
   auto padded_of = [&](const WeightUnit &u, int c) { return max(16, (min(kMaxRows, u.cnt * P.group - c * kMaxRows) + 15) / 16 * 16); };
 
   if (warp == 8) {
-    // ---- loading K and its scales: a lane to 16 positions (the first 8 lanes); the next tile's page is looked up meanwhile
+    // ---- loading K and its scales: a lane to 16 positions (the first 16 lanes); the next tile's page is looked up meanwhile
     const int shift = P.c.page_shift;
     int stage = 0, lap = 0, i = 0;
     bool ok = true;
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < chunks && ok; ++c) {
         auto page_of = [&](int k) {
           const int pos = (k - u.tile0) * kTile + lane * 16;
-          return k < end && lane < 8 && pos < u.T ? page_at(P.c, first + u.b, pos >> shift) : -1;
+          return k < end && lane < 16 && pos < u.T ? page_at(P.c, first + u.b, pos >> shift) : -1;
         };
         auto scale_of = [&](int page) { return page >= 0 ? P.c.k_scale[page * P.c.scale_stride + u.head] : 1.0f; };
         int page = page_of(t), page1 = page_of(t + 1);
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float scale1 = scale_of(page1);
           const int page2 = page_of(k + 2), pos = (k - u.tile0) * kTile + lane * 16, r = i % kRing;
           if (i >= kRing && !(ok = warp_wait(&sm.ring_empty[r], (i / kRing - 1) & 1, dead))) break;
-          if (lane < 8) sm.ring[r][lane] = scale;
+          if (lane < 16) sm.ring[r][lane] = scale;
           bar_arrive(&sm.ring_full[r]);
           const bool load = page >= 0 && (pos & (page_rows - 1)) == 0;
           const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(~0u, load)) * page_rows * D);
@@ -304,7 +306,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) {
 #pragma unroll
             for (int e = 0; e < D / 32; ++e)
-              mma_f8(tmem + buffer * kBufferCols, k_desc + ((stage * S::kStage + e * 32) >> 4), q_desc + ((e * 32) >> 4), idesc, e > 0);
+#pragma unroll
+              for (int half = 0; half < 2; ++half)  // (in turn: a product waits for the one before on its own accumulator)
+                mma_f8(tmem + (buffer * 2 + half) * kSideCols, k_desc + ((stage * S::kStage + half * 128 * D + e * 32) >> 4),
+                       q_desc + ((e * 32) >> 4), idesc, e > 0);
             tc_commit(&sm.k_empty[stage]);
             tc_commit(&sm.s_full[buffer]);
           }
@@ -424,8 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = together())) break;
 
         for (int k = t; k < end; ++k, ++i) {
-          if ((i & 1) != side) continue;
-          const int buffer = i % kBuffers, ring = i % kRing, j = (k - u.tile0) * kTile + spot;
+          const int buffer = i % kBuffers, ring = i % kRing, j = (k - u.tile0) * kTile + side * 128 + spot;
           const bool mine = j < u.T && !bad;
           const bool edge = (k - u.tile0) * kTile + kTile > u.base;
           float *out = P.out + b * P.out_s[0] + u.head * P.out_s[1] + j;
@@ -433,12 +437,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (mine) held = c > 0 ? *out : P.prev ? P.prev[b * P.prev_s[0] + u.head * P.prev_s[1] + j] : 0.0f;
           if (!(ok = warp_wait(&sm.s_full[buffer], (i / kBuffers) & 1, dead))) break;
           tc_fence_after();
-          const float ks = sm.ring[ring][spot >> 4];
+          const float ks = sm.ring[ring][side * 8 + (spot >> 4)];
           bar_arrive(&sm.ring_empty[ring]);
 #pragma unroll 1
           for (int r = 0; r < padded; r += 16) {
             float x[16], y[16];
-            const uint32_t at = tmem + lanes + buffer * kBufferCols + r;
+            const uint32_t at = tmem + lanes + (buffer * 2 + side) * kSideCols + r;
             tmem_ld16(at, x);
             tmem_ld16(at + padded, y);
             if (S::kPieces == 3) {
@@ -499,7 +503,7 @@ cudaError_t launch_weight_tiles(const CacheWeightsParams &P, cudaStream_t st) {
   cudaError_t e = once_per_device([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes); },
                                   weights_ready[(DT == SPEC_DTYPE_BF16) * 2 + (D == 128)]);
   if (e != cudaSuccess) return e;
-  const int page_rows = std::min(1 << P.c.page_shift, kTile);
+  const int page_rows = std::min(1 << P.c.page_shift, kTilePositions);
   CUtensorMap map;
   if ((e = cache_k_map(P.c, page_rows, &map)) != cudaSuccess) return e;
   const uint32_t group_inverse = static_cast<uint32_t>((0x100000000ull + P.group - 1) / P.group);
