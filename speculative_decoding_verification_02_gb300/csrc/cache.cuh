@@ -52,7 +52,7 @@ struct CacheAttendParams {
 
 constexpr int kTilePositions = 128;  // positions to a tile of the tensor-core kernels
 constexpr int kTileRequests = 256;   // requests to one of their launches
-constexpr int kTileUnitCost = 4;     // (cache_attend_tile.cuh)
+constexpr int kTileUnitCost = 8;     // (cache_attend_tile.cuh)
 
 // A launch of spec_cache_attend's tensor-core path.
 struct CacheTilePlan {

@@ -117,7 +117,7 @@ constexpr int kTile = 256;      // positions to a tile
 constexpr int kThreads = 320;  // two sides of 4 summing warps, 1 loading, 1 issuing
 constexpr int kRing = 8;
 constexpr int kMaxRows = 64;   // rows at a time
-constexpr int kUnitCost = 2;   // what a unit costs besides its tiles, in tiles
+constexpr int kUnitCost = 4;   // what a unit costs besides its tiles, in tiles
 
 template <int DT, int D>
 struct WeightShape {
