@@ -92,7 +92,8 @@ struct Piece {
 // at 128 tokens of 128 values is all of them: the rows are read once.
 constexpr int kHeld = 8;
 
-template <int DT, bool VEC>
+// PER_ROW: pieces of a row (a power of two), 0: any.
+template <int DT, bool VEC, int PER_ROW>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const CacheAppendParams P) {
   using W = Piece<DT>;
   // block index: ((request, touched page), head, K or V)
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
   const int first = static_cast<int>(start + lo - base);  // the block's first new row
   const char *src = (is_v ? P.v : P.k) + (b * s0 + head * s2) * W::kSize;
   const int32_t *index = P.index ? P.index + static_cast<int64_t>(b) * P.index_stride + first : nullptr;
-  const int per_row = D / W::kValues, pieces = rows * per_row;
+  const int per_row = PER_ROW ? PER_ROW : D / W::kValues, pieces = rows * per_row;
   // piece i of the block's new rows; false for a row whose index is out of range
   auto load = [&](int i, uint4 &v) {
     const int r = i / per_row, t = index ? index[r] : first + r;
@@ -211,11 +212,14 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
 
 template <int DT>
 void launch_append(const CacheAppendParams &P, unsigned grid, cudaStream_t st) {
+  constexpr int kRow128 = 128 / Piece<DT>::kValues, kRow64 = 64 / Piece<DT>::kValues;
   constexpr int kSize = Piece<DT>::kSize;
   bool vec = reinterpret_cast<uintptr_t>(P.k) % 16 == 0 && reinterpret_cast<uintptr_t>(P.v) % 16 == 0;
   for (int i = 0; i < 3; ++i) vec = vec && P.ks[i] * kSize % 16 == 0 && P.vs[i] * kSize % 16 == 0;
-  if (vec) cache_append_kernel<DT, true><<<grid, kAppendThreads, 0, st>>>(P);
-  else cache_append_kernel<DT, false><<<grid, kAppendThreads, 0, st>>>(P);
+  if (vec && P.c.head_dim == 128) cache_append_kernel<DT, true, kRow128><<<grid, kAppendThreads, 0, st>>>(P);
+  else if (vec && P.c.head_dim == 64) cache_append_kernel<DT, true, kRow64><<<grid, kAppendThreads, 0, st>>>(P);
+  else if (vec) cache_append_kernel<DT, true, 0><<<grid, kAppendThreads, 0, st>>>(P);
+  else cache_append_kernel<DT, false, 0><<<grid, kAppendThreads, 0, st>>>(P);
 }
 
 }  // namespace
