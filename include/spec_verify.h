@@ -462,8 +462,8 @@ int spec_tree_rerank(const int32_t *parents, const float *conf, const int32_t *n
  *               later rows get 0 and lse -inf, as every row of a bad request.
  *   mask        uint8 [B][N][N] or NULL: row i sees the context and the
  *               rows j < n_query[b] with mask[b][i][j] != 0.  NULL: j <= i.
- *   scale       finite; softcap >= 0: scores are s = scale q.k, or
- *               softcap * tanh(s / softcap) when softcap > 0.
+ *   scale       finite; softcap 0 or at least 1e-18: scores are s = scale q.k,
+ *               or softcap * tanh(s / softcap) when softcap > 0.
  *   out         q's dtype: softmax(scores) v; 0 for a row that sees nothing.
  *   lse         out fp32 [B][N][Hq] or NULL: log of the sum of exp(score),
  *               -inf for a row that sees nothing.

@@ -55,6 +55,9 @@ int check_workspace(size_t need, const void *ws, size_t bytes) {
   return need == 0 || (ws && bytes >= need && on_grain(ws, 256)) ? SPEC_OK : SPEC_EWORKSPACE;
 }
 
+// (a smaller cap would overflow its reciprocal times a score)
+bool cap_ok(float softcap) { return softcap == 0.0f || (std::isfinite(softcap) && softcap >= 1e-18f); }
+
 cudaStream_t stream_of(void *s) { return reinterpret_cast<cudaStream_t>(s); }
 
 }  // namespace
@@ -134,7 +137,7 @@ int spec_cache_attend(const spec_cache *cache, const void *q, const int64_t *q_s
   if (rc != SPEC_OK) return rc;
   if (B < 0 || N < 0 || N > SPEC_MAX_NODES || Hq < 1 || Hq % P.c.kv_heads || !strides_ok(q_stride, 3) || !strides_ok(out_stride, 3))
     return SPEC_EINVAL;
-  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.0f) return SPEC_EINVAL;
+  if (!std::isfinite(scale) || !cap_ok(softcap)) return SPEC_EINVAL;
   if ((rc = check_rows(dtype, false, q)) != SPEC_OK || (rc = check_rows(dtype, false, out)) != SPEC_OK) return rc;
   if (B == 0 || N == 0) return SPEC_OK;
   if (!q || !out || !cache_len || static_cast<int64_t>(B) * N * Hq > kMaxGrid / 8) return SPEC_EINVAL;
@@ -162,7 +165,7 @@ int spec_cache_weights(const spec_cache *cache, const void *q, const int64_t *q_
       !strides_ok(q_stride, 3) || !strides_ok(out_stride, 2) || (prev && !strides_ok(prev_stride, 2)))
     return SPEC_EINVAL;
   if ((index ? n_rows > index_stride : n_rows != N) || positions < 0) return SPEC_EINVAL;
-  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.0f) return SPEC_EINVAL;
+  if (!std::isfinite(scale) || !cap_ok(softcap)) return SPEC_EINVAL;
   if ((rc = check_rows(dtype, false, q)) != SPEC_OK) return rc;
   if (B == 0) return SPEC_OK;
   if (!cache_len || !out || (N > 0 && (!q || !lse))) return SPEC_EINVAL;

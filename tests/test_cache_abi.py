@@ -90,7 +90,7 @@ def test_no_cache(api):
     (append, dict(ks=None)), (append, dict(vs=s3(-1, 0, 0))), (append, dict(dtype=0, k=FAKE + 2)),
     (attend, dict(B=-1)), (attend, dict(N=-1)), (attend, dict(N=4097)), (attend, dict(Hq=0)), (attend, dict(Hq=12)),
     (attend, dict(q=None)), (attend, dict(out=None)), (attend, dict(len=None)), (attend, dict(scale=float("nan"))),
-    (attend, dict(scale=float("inf"))), (attend, dict(cap=-1.0)), (attend, dict(cap=float("nan"))), (attend, dict(q=FAKE + 1)),
+    (attend, dict(scale=float("inf"))), (attend, dict(cap=-1.0)), (attend, dict(cap=1e-30)), (attend, dict(cap=float("inf"))), (attend, dict(cap=float("nan"))), (attend, dict(q=FAKE + 1)),
     (attend, dict(qs=s3(0, -1, 0))), (attend, dict(os=None)),
     (weights, dict(B=-1)), (weights, dict(N=4097)), (weights, dict(rows=8)), (weights, dict(index=FAKE, ist=8)), (weights, dict(Hq=9)),
     (weights, dict(q=None)), (weights, dict(lse=None)), (weights, dict(out=None)), (weights, dict(len=None)),

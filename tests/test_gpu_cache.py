@@ -190,6 +190,36 @@ def test_attend(api, B, N, H, G, D, P, lens, dtype, cap, tree):
     check_attend(api, q, cache, table, lens, mask=tree_mask(B, N, 14) if tree else None, cap=cap)
 
 
+@pytest.mark.parametrize("D,G,N,dtype,cap", [(64, 1, 1, BF, 0.0), (128, 1, 1, HF, 0.0), (64, 2, 1, HF, 25.0), (128, 4, 1, BF, 25.0), (128, 1, 3, BF, 0.0),
+                                             (64, 1, 4, BF, 0.0), (96, 3, 2, HF, 0.0), (240, 1, 2, BF, 10.0)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_attend_few_rows(api, D, G, N, dtype, cap, tree):
+    """One to six rows: the scalar kernel, its clusters, requests without positions and shares that are empty."""
+    B, H, P = 5, 2, 16
+    lens = [0, 1, 130, 1025, 3000]
+    W = -(-(max(lens) + N) // P)
+    cache = rand_cache(api, B * W, H, P, D, 111)
+    table = rand_table(B, W, B * W, 112)
+    q = (torch.randn(B, N, H * G, D, generator=gen(113)) * 2).to(dtype).cuda()
+    check_attend(api, q, cache, table, lens, n_query=[N, N, max(N - 1, 0), N, N], mask=tree_mask(B, N, 114) if tree else None, cap=cap)
+
+
+@pytest.mark.parametrize("N,G,D", [(1, 1, 128), (9, 4, 128), (40, 4, 64)])
+def test_scales_that_are_no_powers_of_two(api, N, G, D):
+    """A cache that another program wrote: any positive scale is served by the operators that read it."""
+    B, H, P, W = 2, 2, 32, 12
+    lens = [300, 65]
+    cache = rand_cache(api, B * W, H, P, D, 115)
+    for i in (2, 3):
+        cache[i] *= 1 + 0.7 * torch.rand(cache[i].shape, generator=gen(116)).cuda()
+    table = rand_table(B, W, B * W, 117)
+    q = torch.randn(B, N, H * G, D, generator=gen(118)).to(BF).cuda()
+    o = check_attend(api, q, cache, table, lens)
+    w = api.spec_cache_weights(q, o["lse"], cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    want, tol = ref.weights(ref.Cache64(cache, table), q, o["lse"], lens, [N] * B, None, D ** -0.5, 0.0, torch.zeros_like(w["weights"]))
+    assert bool(((w["weights"].cpu().double() - want).abs() <= tol).all())
+
+
 def test_attend_long_and_ragged(api):
     lens = [20000, 0, 777, 4095, 1, 9000]
     B, N, H, G, D, P = 6, 5, 2, 4, 128, 128
