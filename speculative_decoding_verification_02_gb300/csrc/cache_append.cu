@@ -3,9 +3,12 @@
 //   s'   = max(s if the block held tokens, smallest 2^e with amax(new rows) <= 448 2^e)
 //   byte = RN_e4m3(x / s')   for the new rows; old rows again when s' > s
 //
-// Bound by memory: 2 bytes read and 1 written a value.  A block's scale needs
-// all of its new rows, so the unit of work is one block (request, page, head,
-// K or V).
+// 2 bytes are read and 1 written a value.  A block's scale needs all of its new
+// rows, so the unit of work is one block (request, page, head, K or V), a CTA to
+// each.  Four prompts of 3,000 to 8,001 tokens, 8 heads of 128 in bf16: 31 us,
+// 4.8 TB/s, bound by instruction issue (73% of the slots); with a division for
+// each 16 bytes' row it was 36 us, reading the rows twice 73 us.  A batch's nine
+// rows a request: 9 us for 64 requests, a block's chain of loads.
 #include "cache.cuh"
 #include "launch.h"
 
