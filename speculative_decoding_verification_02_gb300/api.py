@@ -586,7 +586,7 @@ def _index_rows(index, counts, B, n, dev):
 
 def _on(dev, fn, *args):
     """fn(*args) with dev current."""
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         return fn(*args)
     return _call(dev, fn, *args)
 
@@ -602,7 +602,7 @@ def _ptr(t):
 
 
 def _cache_workspace(op, cs, B, N, Hq, dev, ws, stream):
-    need = lib().spec_cache_workspace_size(op, cs, B, N, Hq)
+    need = (_lib or lib()).spec_cache_workspace_size(op, cs, B, N, Hq)
     if ws is None:
         if need == 0:
             return None, 0
@@ -630,7 +630,7 @@ def spec_cache_append(cache, table: torch.Tensor, cache_len: torch.Tensor, k: to
     lp = _lengths(cache_len, B, "cache_len", dev)
     ip, ist, rows = _index_rows(index, counts, B, n, dev)
     o = out or dict(new_len=torch.empty(B, dtype=torch.int32, device=dev), status=torch.empty(B, dtype=torch.int32, device=dev))
-    rc = _on(dev, lib().spec_cache_append, cs, k.data_ptr(), kst, v.data_ptr(), vst, code, B, n, ip, ist, rows,
+    rc = _on(dev, (_lib or lib()).spec_cache_append, cs, k.data_ptr(), kst, v.data_ptr(), vst, code, B, n, ip, ist, rows,
              _ptr(counts), lp, o["new_len"].data_ptr(), _ptr(o.get("status")), st)
     _check(rc, "spec_cache_append")
     return o
@@ -664,7 +664,7 @@ def spec_cache_attend(q: torch.Tensor, cache, table: torch.Tensor, cache_len: to
     if o.get("lse") is not None:
         _f32_like(o["lse"], (B, N, Hq), "lse", dev)
     wp, wn = _cache_workspace(OP_CACHE_ATTEND, cs, B, N, Hq, dev, ws, st)
-    rc = _on(dev, lib().spec_cache_attend, cs, q.data_ptr(), qst, code, B, N, Hq, lp,
+    rc = _on(dev, (_lib or lib()).spec_cache_attend, cs, q.data_ptr(), qst, code, B, N, Hq, lp,
              np_, _ptr(mask), D ** -0.5 if scale is None else float(scale), float(softcap), o["out"].data_ptr(), ost,
              _ptr(o.get("lse")), _ptr(o.get("status")), wp, wn, st)
     _check(rc, "spec_cache_attend")
@@ -709,7 +709,7 @@ def spec_cache_weights(q: torch.Tensor, lse: torch.Tensor, cache, table: torch.T
     ost = _positions(o["weights"], "weights", B, H, dev)
     room = o["weights"].shape[2] if prev is None else min(prev.shape[2], o["weights"].shape[2])
     wp, wn = _cache_workspace(OP_CACHE_WEIGHTS, cs, B, rows, Hq, dev, ws, st)
-    rc = _on(dev, lib().spec_cache_weights, cs, q.data_ptr(), qst, code, B, N, Hq, zp, ip, ist, rows, _ptr(counts),
+    rc = _on(dev, (_lib or lib()).spec_cache_weights, cs, q.data_ptr(), qst, code, B, N, Hq, zp, ip, ist, rows, _ptr(counts),
              lp, D ** -0.5 if scale is None else float(scale), float(softcap), _ptr(prev), pst,
              o["weights"].data_ptr(), ost, room, _ptr(o.get("status")), wp, wn, st)
     _check(rc, "spec_cache_weights")
@@ -733,7 +733,7 @@ def spec_cache_evict(cache, table: torch.Tensor, cache_len: torch.Tensor, weight
                     weights=torch.empty((B, H, max(keep, 0)), device=dev),
                     new_len=torch.empty(B, dtype=torch.int32, device=dev), status=torch.empty(B, dtype=torch.int32, device=dev))
     wp, wn = _cache_workspace(OP_CACHE_EVICT, cs, B, keep, 0, dev, ws, st)
-    rc = _on(dev, lib().spec_cache_evict, cs, ds, B, lp, weights.data_ptr(), wst,
+    rc = _on(dev, (_lib or lib()).spec_cache_evict, cs, ds, B, lp, weights.data_ptr(), wst,
              weights.shape[2], keep, int(recent), o["kept"].data_ptr(), _ptr(o.get("weights")), o["new_len"].data_ptr(),
              _ptr(o.get("status")), wp, wn, st)
     _check(rc, "spec_cache_evict")

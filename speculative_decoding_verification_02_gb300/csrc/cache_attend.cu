@@ -37,6 +37,8 @@ __global__ void __launch_bounds__(kRowThreads) cache_attend_rows_kernel(const Ca
   __shared__ float2 s_scale[kSpanPages];
   __shared__ float s_acc[kRowThreads / 32][ROWS][LANES * 16];
   __shared__ float2 s_ml[kRowThreads / 32][ROWS];
+  __shared__ float s_all[ROWS][LANES * 16];
+  __shared__ float2 s_all_ml[ROWS];
   constexpr int kGroups = 32 / LANES, kAll = kRowThreads / LANES;
   const int splits = static_cast<int>(cluster.num_blocks()), split = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, part = lane % LANES, group = tid / LANES;
@@ -219,36 +221,60 @@ __global__ void __launch_bounds__(kRowThreads) cache_attend_rows_kernel(const Ca
     }
   }
   __syncthreads();
-  // the warps of every CTA of the cluster, a column to a thread; each CTA takes a share of the rows' columns
-  if (splits > 1) cluster.sync();
+  // the CTA's warps, a column to a thread
   const int all = ROWS * D;
-  for (int i = split * kRowThreads + tid; i < all; i += splits * kRowThreads) {
-    const int k = i / D, d = i - k * D, row = row0 + k;
-    if (row >= P.N * P.group) break;
-    float top = -INFINITY;
-    for (int s = 0; s < splits; ++s) {
-      const float2 *ml = splits > 1 ? cluster.map_shared_rank(&s_ml[0][0], s) : &s_ml[0][0];
+  auto put = [&](int k, int d, float top, float l, float o) {
+    const int row = row0 + k, i_tok = row / P.group, h = head * P.group + row % P.group;
+    if (row >= P.N * P.group) return;
+    put_value<DT>(P.out + (b * P.os[0] + i_tok * P.os[1] + h * P.os[2]) * 2, d, l == 0.0f ? 0.0f : __fdividef(o, l));
+    if (d == 0 && P.lse) P.lse[(static_cast<int64_t>(b) * P.N + i_tok) * P.Hq + h] = l == 0.0f ? -INFINITY : (top + __log2f(l)) * kLn2;
+  };
+  for (int i = tid; i < all; i += kRowThreads) {
+    const int k = i / D, d = i - k * D;
+    float top = -INFINITY, l = 0.0f, o = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kRowThreads / 32; ++w) top = fmaxf(top, ml[w * ROWS + k].x);
-    }
+    for (int w = 0; w < kRowThreads / 32; ++w) top = fmaxf(top, s_ml[w][k].x);
     const float ref = top == -INFINITY ? 0.0f : top;
-    float l = 0.0f, o = 0.0f;
-    for (int s = 0; s < splits; ++s) {
-      const float2 *ml = splits > 1 ? cluster.map_shared_rank(&s_ml[0][0], s) : &s_ml[0][0];
-      const float *a = splits > 1 ? cluster.map_shared_rank(&s_acc[0][0][0], s) : &s_acc[0][0][0];
 #pragma unroll
-      for (int w = 0; w < kRowThreads / 32; ++w) {
-        const float2 one = ml[w * ROWS + k];
-        const float weight = ex2(one.x - ref);
-        l = fmaf(one.y, weight, l);
-        o = fmaf(a[(w * ROWS + k) * LANES * 16 + d], weight, o);
+    for (int w = 0; w < kRowThreads / 32; ++w) {
+      const float weight = ex2(s_ml[w][k].x - ref);
+      l = fmaf(s_ml[w][k].y, weight, l);
+      o = fmaf(s_acc[w][k][d], weight, o);
+    }
+    if (splits == 1) {
+      put(k, d, top, l, o);
+    } else {
+      s_all[k][d] = o;
+      if (d == 0) s_all_ml[k] = make_float2(top, l);
+    }
+  }
+  if (splits == 1) return;
+  // the cluster's CTAs, each joining a share of the columns
+  cluster.sync();
+  for (int i = split * kRowThreads + tid; i < all; i += splits * kRowThreads) {
+    const int k = i / D, d = i - k * D;
+    float2 ml[8];
+    float o[8], top = -INFINITY, l = 0.0f, sum_o = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      ml[c] = make_float2(-INFINITY, 0.0f), o[c] = 0.0f;
+      if (c < splits) {
+        ml[c] = *cluster.map_shared_rank(&s_all_ml[k], c);
+        o[c] = *cluster.map_shared_rank(&s_all[k][d], c);
       }
     }
-    const int i_tok = row / P.group, h = head * P.group + row % P.group;
-    put_value<DT>(P.out + (b * P.os[0] + i_tok * P.os[1] + h * P.os[2]) * 2, d, l == 0.0f ? 0.0f : o / l);
-    if (d == 0 && P.lse) P.lse[(static_cast<int64_t>(b) * P.N + i_tok) * P.Hq + h] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) top = fmaxf(top, ml[c].x);
+    const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float weight = ex2(ml[c].x - ref);
+      l = fmaf(ml[c].y, weight, l);
+      sum_o = fmaf(o[c], weight, sum_o);
+    }
+    put(k, d, top, l, sum_o);
   }
-  if (splits > 1) cluster.sync();  // no CTA leaves while its sums are read
+  cluster.sync();  // no CTA leaves while its sums are read
 }
 
 // ------------------------------------------------------------------- host
