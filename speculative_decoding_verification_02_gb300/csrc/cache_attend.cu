@@ -28,7 +28,7 @@ constexpr int kAtOnce = 4;       // positions that a group of lanes has in fligh
 // all, without a workspace; the arithmetic is scalar, so its time goes with the
 // rows.  32 requests of one row, 16 heads of 64, 375 to 1,501 positions, capped:
 // 25 us, 2.4 TB/s (the tensor-core kernel: 50 us); one request of four rows,
-// 8 heads of 128, 2,000 positions: 13.5 us (16 us).
+// 8 heads of 128, 2,000 positions: 13.3 us (16 us).
 template <int DT, int LANES, int ROWS, bool CAP>
 __global__ void __launch_bounds__(kRowThreads) cache_attend_rows_kernel(const CacheAttendParams P, int chunks) {
   namespace cg = cooperative_groups;
