@@ -481,7 +481,8 @@ int spec_tree_rerank(const int32_t *parents, const float *conf, const int32_t *n
  *   rows that count are the accepted ones.  A row whose lse is -inf adds
  *   nothing.  Later positions are not written, nor is anything of a bad
  *   request.
- *   lse         fp32 [B][N][Hq], as spec_cache_attend wrote it.
+ *   lse         fp32, as spec_cache_attend wrote it, or with other strides
+ *               (request, token, head).
  *   prev        fp32, NULL for zeros; prev and out: request b, head h at
  *               b*stride[0] + h*stride[1] elements; they may be the same
  *               memory.
@@ -528,8 +529,8 @@ int spec_cache_attend(const spec_cache *cache, const void *q, const int64_t *q_s
                       float softcap, void *out, const int64_t *out_stride, float *lse, int32_t *status,
                       void *workspace, size_t workspace_bytes, void *stream);
 int spec_cache_weights(const spec_cache *cache, const void *q, const int64_t *q_stride, int dtype, int B, int N,
-                       int Hq, const float *lse, const int32_t *index, int index_stride, int n_rows,
-                       const int32_t *counts, const int32_t *cache_len, float scale, float softcap,
+                       int Hq, const float *lse, const int64_t *lse_stride, const int32_t *index, int index_stride,
+                       int n_rows, const int32_t *counts, const int32_t *cache_len, float scale, float softcap,
                        const float *prev, const int64_t *prev_stride, float *out, const int64_t *out_stride,
                        int positions, int32_t *status, void *workspace, size_t workspace_bytes, void *stream);
 int spec_cache_evict(const spec_cache *cache, const spec_cache *dst, int B, const int32_t *cache_len,

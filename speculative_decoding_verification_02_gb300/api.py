@@ -83,7 +83,7 @@ def lib():
         L.spec_alpha_estimate.argtypes = [P, P, I, I, P, P]
         L.spec_cache_append.argtypes = [P, P, P, P, P, I, I, I, P, I, I, P, P, P, P, P]
         L.spec_cache_attend.argtypes = [P, P, P, I, I, I, I, P, P, P, F, F, P, P, P, P, P, Z, P]
-        L.spec_cache_weights.argtypes = [P, P, P, I, I, I, I, P, P, I, I, P, P, F, F, P, P, P, P, I, P, P, Z, P]
+        L.spec_cache_weights.argtypes = [P, P, P, I, I, I, I, P, P, P, I, I, P, P, F, F, P, P, P, P, I, P, P, Z, P]
         L.spec_cache_evict.argtypes = [P, P, I, P, P, P, I, I, I, P, P, P, P, P, Z, P]
         L.spec_cache_workspace_size.argtypes = [I, P, I, I, I]
         L.spec_cache_workspace_size.restype = Z
@@ -699,7 +699,8 @@ def spec_cache_weights(q: torch.Tensor, lse: torch.Tensor, cache, table: torch.T
         raise ValueError(f"q must be [B, N, heads, {hd}]")
     code, qst = _rows(q, "q", dev, (DTYPE_BF16, DTYPE_F16))
     lp = _lengths(cache_len, B, "cache_len", dev)
-    zp = _f32_like(lse, (B, N, Hq), "lse", dev)
+    if lse.dtype is not torch.float32 or lse.device != dev or lse.shape != (B, N, Hq):
+        raise TypeError(f"lse must be a float32 {[B, N, Hq]} tensor on {dev}")
     ip, ist, rows = _index_rows(index, counts, B, N, dev)
     pst = None if prev is None else _positions(prev, "prev", B, H, dev)
     o = out
@@ -709,8 +710,8 @@ def spec_cache_weights(q: torch.Tensor, lse: torch.Tensor, cache, table: torch.T
     ost = _positions(o["weights"], "weights", B, H, dev)
     room = o["weights"].shape[2] if prev is None else min(prev.shape[2], o["weights"].shape[2])
     wp, wn = _cache_workspace(OP_CACHE_WEIGHTS, cs, B, rows, Hq, dev, ws, st)
-    rc = _on(dev, (_lib or lib()).spec_cache_weights, cs, q.data_ptr(), qst, code, B, N, Hq, zp, ip, ist, rows, _ptr(counts),
-             lp, D ** -0.5 if scale is None else float(scale), float(softcap), _ptr(prev), pst,
+    rc = _on(dev, (_lib or lib()).spec_cache_weights, cs, q.data_ptr(), qst, code, B, N, Hq, lse.data_ptr(), _pack3(*lse.stride()), ip, ist,
+             rows, _ptr(counts), lp, D ** -0.5 if scale is None else float(scale), float(softcap), _ptr(prev), pst,
              o["weights"].data_ptr(), ost, room, _ptr(o.get("status")), wp, wn, st)
     _check(rc, "spec_cache_weights")
     return o

@@ -75,6 +75,7 @@ struct CacheWeightsParams {
   int64_t qs[3];
   int dtype, B, N, Hq, group, n_rows, index_stride;
   const float *lse;
+  int64_t ls[3];
   const int32_t *index, *counts, *cache_len;
   float scale, softcap;
   const float *prev;

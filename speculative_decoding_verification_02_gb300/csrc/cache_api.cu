@@ -154,15 +154,15 @@ int spec_cache_attend(const spec_cache *cache, const void *q, const int64_t *q_s
 }
 
 int spec_cache_weights(const spec_cache *cache, const void *q, const int64_t *q_stride, int dtype, int B, int N,
-                       int Hq, const float *lse, const int32_t *index, int index_stride, int n_rows,
-                       const int32_t *counts, const int32_t *cache_len, float scale, float softcap,
+                       int Hq, const float *lse, const int64_t *lse_stride, const int32_t *index, int index_stride,
+                       int n_rows, const int32_t *counts, const int32_t *cache_len, float scale, float softcap,
                        const float *prev, const int64_t *prev_stride, float *out, const int64_t *out_stride,
                        int positions, int32_t *status, void *workspace, size_t workspace_bytes, void *stream) {
   CacheWeightsParams P{};
   int rc = check_cache(cache, &P.c);
   if (rc != SPEC_OK) return rc;
   if (B < 0 || N < 0 || N > SPEC_MAX_NODES || n_rows < 0 || n_rows > SPEC_MAX_NODES || Hq < 1 || Hq % P.c.kv_heads ||
-      !strides_ok(q_stride, 3) || !strides_ok(out_stride, 2) || (prev && !strides_ok(prev_stride, 2)))
+      !strides_ok(q_stride, 3) || !strides_ok(lse_stride, 3) || !strides_ok(out_stride, 2) || (prev && !strides_ok(prev_stride, 2)))
     return SPEC_EINVAL;
   if ((index ? n_rows > index_stride : n_rows != N) || positions < 0) return SPEC_EINVAL;
   if (!std::isfinite(scale) || !cap_ok(softcap)) return SPEC_EINVAL;
@@ -174,6 +174,7 @@ int spec_cache_weights(const spec_cache *cache, const void *q, const int64_t *q_
     return SPEC_EINVAL;
   P.q = static_cast<const char *>(q);
   std::copy(q_stride, q_stride + 3, P.qs);
+  std::copy(lse_stride, lse_stride + 3, P.ls);
   std::copy(out_stride, out_stride + 2, P.out_s);
   if (prev) std::copy(prev_stride, prev_stride + 2, P.prev_s);
   P.dtype = dtype, P.B = B, P.N = N, P.Hq = Hq, P.group = Hq / P.c.kv_heads, P.n_rows = n_rows, P.index_stride = index_stride;

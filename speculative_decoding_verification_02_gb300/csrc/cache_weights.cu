@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kSpan) cache_weights_rows_kernel(const CacheWe
       const int t = P.index ? P.index[static_cast<int64_t>(b) * P.index_stride + i] : i;
       s_q[e / D][e % D] = row_value<DT>(P.q + (b * P.qs[0] + t * P.qs[1] + h * P.qs[2]) * 2, e % D);
       if (e % D == 0) {
-        s_lse[e / D] = P.lse[(static_cast<int64_t>(b) * P.N + t) * P.Hq + h] * kLog2e;
+        s_lse[e / D] = P.lse[b * P.ls[0] + t * P.ls[1] + h * P.ls[2]] * kLog2e;
         s_row[e / D] = i;
       }
     }
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lane == 0) {
               const int h = u.head * P.group + row0 + r - tok[k] * P.group;
-              const float z = at[k] >= 0 ? P.lse[(static_cast<int64_t>(b) * P.N + at[k]) * P.Hq + h] : -INFINITY;
+              const float z = at[k] >= 0 ? P.lse[b * P.ls[0] + at[k] * P.ls[1] + h * P.ls[2]] : -INFINITY;
               sm.row[r] = make_float2(fabsf(P.scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(ex[k] + 127) << 23),
                                       z == -INFINITY ? -INFINITY : -z * kLog2e);  // (nothing comes of a row without positions)
               sm.token[r] = tok[k];

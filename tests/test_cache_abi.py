@@ -54,8 +54,8 @@ def attend(api, c=None, **kw):
 
 
 def weights(api, c=None, **kw):
-    a = dict(q=FAKE, qs=s3(1 << 16, 1 << 12, 128), dtype=1, B=2, N=9, Hq=32, lse=FAKE, index=None, ist=0, rows=9, counts=None,
-             len=FAKE, scale=0.1, cap=0.0, prev=None, ps=None, out=FAKE, os=s2(2048, 256), pos=256, status=None, ws=FAKE,
+    a = dict(q=FAKE, qs=s3(1 << 16, 1 << 12, 128), dtype=1, B=2, N=9, Hq=32, lse=FAKE, ls=s3(288, 32, 1), index=None, ist=0, rows=9,
+             counts=None, len=FAKE, scale=0.1, cap=0.0, prev=None, ps=None, out=FAKE, os=s2(2048, 256), pos=256, status=None, ws=FAKE,
              wsb=1 << 40, stream=None)
     a.update(kw)
     c = c or cache(api)
@@ -95,7 +95,7 @@ def test_no_cache(api):
     (weights, dict(B=-1)), (weights, dict(N=4097)), (weights, dict(rows=8)), (weights, dict(index=FAKE, ist=8)), (weights, dict(Hq=9)),
     (weights, dict(q=None)), (weights, dict(lse=None)), (weights, dict(out=None)), (weights, dict(len=None)),
     (weights, dict(cap=-0.5)), (weights, dict(scale=float("nan"))), (weights, dict(prev=FAKE)), (weights, dict(pos=-1)),
-    (weights, dict(os=s2(-1, 0))),
+    (weights, dict(os=s2(-1, 0))), (weights, dict(ls=None)), (weights, dict(ls=s3(288, 32, -1))),
     (evict, dict(B=-1)), (evict, dict(keep=0)), (evict, dict(keep=-3)), (evict, dict(recent=-1)), (evict, dict(recent=17)),
     (evict, dict(len=None)), (evict, dict(w=None)), (evict, dict(kept=None)), (evict, dict(new=None)), (evict, dict(new=FAKE)),
     (evict, dict(pos=-1)), (evict, dict(ws=None)),

@@ -425,6 +425,24 @@ def test_weights(api, B, N, H, G, D, P, lens, dtype, cap, path):
     assert fresh["weights"].shape == prev.shape
 
 
+@pytest.mark.parametrize("D", [64, 80, 128])
+def test_weights_of_normalisers_in_any_strides(api, D):
+    """Heads outermost, a slice of wider rows, one request's for all: the same bits as of a contiguous copy."""
+    B, N, H, G, P, W = 3, 5, 2, 3, 32, 9
+    cache = rand_cache(api, B * W, H, P, D, 110)
+    table = rand_table(B, W, B * W, 111)
+    g = gen(112)
+    q = torch.randn(B, N, H * G, D, generator=g).to(BF).cuda()
+    ln = torch.tensor([0, 100, 283], dtype=torch.int32, device="cuda")
+    wide = (torch.rand(H * G + 1, N, 2 * B, generator=g) * 3 + 3).cuda()
+    for lse in (wide[1:, :, ::2].permute(2, 1, 0), wide.reshape(2 * B, N, H * G + 1)[1:B + 1, :, 1:], wide[:-1, :, 1].T.expand(B, N, H * G)):
+        assert lse.shape == (B, N, H * G) and not lse.is_contiguous()
+        got = api.spec_cache_weights(q, lse, cache, table, ln)
+        want = api.spec_cache_weights(q, lse.contiguous(), cache, table, ln)
+        assert got["status"].tolist() == [0] * B and torch.equal(got["weights"], want["weights"])
+        assert bool((got["weights"].sum(-1) > 0).all())
+
+
 def test_weights_of_an_attention_sum_to_its_rows(api):
     """Every row's weights sum to 1: the operators agree on what a score is."""
     B, N, H, G, D, P, W = 2, 4, 2, 3, 128, 64, 5
