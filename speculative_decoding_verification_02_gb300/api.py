@@ -527,7 +527,7 @@ class _CacheStruct(ctypes.Structure):  # struct spec_cache
 _pack_cache = struct.Struct("@PPPPqqiiiiPi4x").pack
 _pack3 = struct.Struct("@qqq").pack
 _pack2 = struct.Struct("@qq").pack
-_F8 = torch.float8_e4m3fn
+_F8, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
 _ROW_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
 
 
@@ -541,19 +541,19 @@ def spec_cache_new(pages: int, kv_heads: int, page_size: int, head_dim: int, dev
 def _cache_struct(cache, table, B, dev, name="cache"):
     """(packed struct spec_cache, kv_heads, page_size, head_dim)"""
     k, v, ks, vs = cache
-    if k.dtype is not _F8 or v.dtype is not _F8 or ks.dtype is not torch.float32 or vs.dtype is not torch.float32:
+    if not (k.dtype is v.dtype is _F8 and ks.dtype is vs.dtype is _F32):
         raise TypeError(f"{name}: k and v must be float8_e4m3fn and their scales float32")
-    shape, st, ss = k.shape, k.stride(), ks.stride()
-    if len(shape) != 4 or v.shape != shape or v.stride() != st or ks.shape != shape[:2] or vs.shape != ks.shape:
+    shape, st, of, ss = k.shape, k.stride(), ks.shape, ks.stride()
+    if len(shape) != 4 or v.shape != shape or v.stride() != st or of != shape[:2] or vs.shape != of:
         raise ValueError(f"{name}: k and v must be [pages, kv_heads, page_size, head_dim] alike, their scales [pages, kv_heads]")
     n, H, P, D = shape
     if st[3] != 1 or st[2] != D or (H > 1 and st[1] != P * D) or vs.stride() != ss or (H > 1 and ss[1] != 1):
         raise ValueError(f"{name}: the heads of a page must lie side by side")
-    i = dev.index
-    if dev.type != "cuda" or k.get_device() != i or v.get_device() != i or ks.get_device() != i or vs.get_device() != i:
+    i = dev.index  # (None for tensors of the host, whose get_device() is -1)
+    if not k.get_device() == v.get_device() == ks.get_device() == vs.get_device() == i:
         raise ValueError(f"{name} must live on the rows' CUDA device")
     ts = table.shape
-    if table.dtype is not torch.int32 or table.get_device() != i or len(ts) != 2 or ts[0] != B or not table.is_contiguous():
+    if table.dtype is not _I32 or table.get_device() != i or len(ts) != 2 or ts[0] != B or not table.is_contiguous():
         raise TypeError(f"the page table must be a contiguous int32 [{B}, pages of a request] tensor on {dev}")
     return _pack_cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), st[0] if n > 1 else H * P * D,
                        ss[0] if n > 1 else H, n, H, P, D, table.data_ptr(), ts[1]), H, P, D
@@ -578,10 +578,10 @@ def _index_rows(index, counts, B, n, dev):
         _lengths(counts, B, "counts", dev)
     if index is None:
         return None, 0, n
-    if index.dtype != torch.int32 or index.device != dev or index.dim() != 2 or index.shape[0] != B or index.stride(1) != 1:
+    shape, st = index.shape, index.stride()
+    if index.dtype is not _I32 or index.get_device() != dev.index or len(shape) != 2 or shape[0] != B or (st[1] != 1 and shape[1] > 1):
         raise TypeError(f"index must be an int32 [{B}, rows] tensor on {dev}")
-    rows = index.shape[1]
-    return index.data_ptr(), index.stride(0) if B > 1 else rows, rows
+    return index.data_ptr(), st[0] if B > 1 else shape[1], shape[1]
 
 
 def _on(dev, fn, *args):
@@ -592,9 +592,14 @@ def _on(dev, fn, *args):
 
 
 def _lengths(t, B, name, dev):
-    if t.dtype is not torch.int32 or t.get_device() != dev.index or t.shape != (B,) or not t.is_contiguous():
+    if t.dtype is not _I32 or t.get_device() != dev.index or t.shape != (B,) or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 [{B}] tensor on {dev}")
     return t.data_ptr()
+
+
+def _status(o, B, dev):
+    t = o.get("status")
+    return None if t is None else _lengths(t, B, "status", dev)
 
 
 def _ptr(t):
@@ -610,8 +615,14 @@ def _cache_workspace(op, cs, B, N, Hq, dev, ws, stream):
     return ws.data_ptr(), ws.numel()
 
 
-def _raw_stream(stream, dev) -> int:
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
+def _raw_stream(dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _on_stream(stream, fn, *args, **kw):
+    """fn with stream current: the tensors that it makes and the copies that it takes belong to that stream, as its kernels do."""
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
 
 
 def spec_cache_append(cache, table: torch.Tensor, cache_len: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, counts=None,
@@ -620,18 +631,21 @@ def spec_cache_append(cache, table: torch.Tensor, cache_len: torch.Tensor, k: to
     them, or counts int32 [B]; with index int32 [B, rows], row i is token index[b, i] (the accepted path: index = path_nodes,
     counts = n_emit of a verify call) -> new_len [B], status [B]."""
     dev = k.device
-    st = _raw_stream(stream, dev)
-    B, n = k.shape[:2]
-    cs, H, P, hd = _cache_struct(cache, table, B, dev)
+    if stream is not None:
+        return _on_stream(stream, spec_cache_append, cache, table, cache_len, k, v, counts=counts, index=index, out=out)
+    st = _raw_stream(dev)
     code, kst = _rows(k, "k", dev, (DTYPE_BF16, DTYPE_F16, DTYPE_F32))
     vcode, vst = _rows(v, "v", dev, (DTYPE_BF16, DTYPE_F16, DTYPE_F32))
-    if v.shape != k.shape or vcode != code or tuple(k.shape[2:]) != (H, hd):
+    shape = k.shape
+    B, n, heads, D = shape
+    cs, H, P, hd = _cache_struct(cache, table, B, dev)
+    if v.shape != shape or vcode != code or heads != H or D != hd:
         raise ValueError(f"k and v must both be [B, n, {H}, {hd}] of one dtype")
     lp = _lengths(cache_len, B, "cache_len", dev)
     ip, ist, rows = _index_rows(index, counts, B, n, dev)
     o = out or dict(new_len=torch.empty(B, dtype=torch.int32, device=dev), status=torch.empty(B, dtype=torch.int32, device=dev))
     rc = _on(dev, (_lib or lib()).spec_cache_append, cs, k.data_ptr(), kst, v.data_ptr(), vst, code, B, n, ip, ist, rows,
-             _ptr(counts), lp, o["new_len"].data_ptr(), _ptr(o.get("status")), st)
+             _ptr(counts), lp, _lengths(o["new_len"], B, "new_len", dev), _status(o, B, dev), st)
     _check(rc, "spec_cache_append")
     return o
 
@@ -643,7 +657,10 @@ def spec_cache_attend(q: torch.Tensor, cache, table: torch.Tensor, cache_len: to
     rows j with mask[b, i, j].  n_query int32 [B]: rows of a request (default N).  scale: head_dim ** -0.5 by default.
     -> out (as q), lse fp32 [B, N, Hq], status."""
     dev = q.device
-    st = _raw_stream(stream, dev)
+    if stream is not None:
+        return _on_stream(stream, spec_cache_attend, q, cache, table, cache_len, n_query=n_query, mask=mask, scale=scale,
+                          softcap=softcap, lse=lse, out=out, ws=ws)
+    st = _raw_stream(dev)
     B, N, Hq, D = q.shape
     cs, H, P, hd = _cache_struct(cache, table, B, dev)
     if D != hd:
@@ -666,7 +683,7 @@ def spec_cache_attend(q: torch.Tensor, cache, table: torch.Tensor, cache_len: to
     wp, wn = _cache_workspace(OP_CACHE_ATTEND, cs, B, N, Hq, dev, ws, st)
     rc = _on(dev, (_lib or lib()).spec_cache_attend, cs, q.data_ptr(), qst, code, B, N, Hq, lp,
              np_, _ptr(mask), D ** -0.5 if scale is None else float(scale), float(softcap), o["out"].data_ptr(), ost,
-             _ptr(o.get("lse")), _ptr(o.get("status")), wp, wn, st)
+             _ptr(o.get("lse")), _status(o, B, dev), wp, wn, st)
     _check(rc, "spec_cache_attend")
     return o
 
@@ -692,7 +709,10 @@ def spec_cache_weights(q: torch.Tensor, lse: torch.Tensor, cache, table: torch.T
     cache_len + i and seeing every position up to its own -> weights (prev's shape; positions past the rows' are not written:
     zeros in a new tensor), status.  out["weights"] may be prev."""
     dev = q.device
-    st = _raw_stream(stream, dev)
+    if stream is not None:
+        return _on_stream(stream, spec_cache_weights, q, lse, cache, table, cache_len, prev=prev, counts=counts, index=index,
+                          scale=scale, softcap=softcap, out=out, ws=ws)
+    st = _raw_stream(dev)
     B, N, Hq, D = q.shape
     cs, H, P, hd = _cache_struct(cache, table, B, dev)
     if D != hd:
@@ -712,7 +732,7 @@ def spec_cache_weights(q: torch.Tensor, lse: torch.Tensor, cache, table: torch.T
     wp, wn = _cache_workspace(OP_CACHE_WEIGHTS, cs, B, rows, Hq, dev, ws, st)
     rc = _on(dev, (_lib or lib()).spec_cache_weights, cs, q.data_ptr(), qst, code, B, N, Hq, lse.data_ptr(), _pack3(*lse.stride()), ip, ist,
              rows, _ptr(counts), lp, D ** -0.5 if scale is None else float(scale), float(softcap), _ptr(prev), pst,
-             o["weights"].data_ptr(), ost, room, _ptr(o.get("status")), wp, wn, st)
+             o["weights"].data_ptr(), ost, room, _status(o, B, dev), wp, wn, st)
     _check(rc, "spec_cache_weights")
     return o
 
@@ -723,7 +743,10 @@ def spec_cache_evict(cache, table: torch.Tensor, cache_len: torch.Tensor, weight
     `recent` last tokens and the others of largest weight (weights fp32 [B, kv_heads, positions]), min(keep, cache_len) in all and
     in their order -> kept int32 [B, kv_heads, keep] (positions, then -1), weights [B, kv_heads, keep] (then 0), new_len, status."""
     dev = weights.device
-    st = _raw_stream(stream, dev)
+    if stream is not None:
+        return _on_stream(stream, spec_cache_evict, cache, table, cache_len, weights, keep, recent, dst_table,
+                          dst_cache=dst_cache, out=out, ws=ws)
+    st = _raw_stream(dev)
     B = weights.shape[0]
     cs, H, P, hd = _cache_struct(cache, table, B, dev)
     ds = _cache_struct(cache if dst_cache is None else dst_cache, dst_table, B, dev, "dst_cache")[0]
@@ -733,9 +756,14 @@ def spec_cache_evict(cache, table: torch.Tensor, cache_len: torch.Tensor, weight
     o = out or dict(kept=torch.empty((B, H, max(keep, 0)), dtype=torch.int32, device=dev),
                     weights=torch.empty((B, H, max(keep, 0)), device=dev),
                     new_len=torch.empty(B, dtype=torch.int32, device=dev), status=torch.empty(B, dtype=torch.int32, device=dev))
+    kept, of = o["kept"], (B, H, max(keep, 0))
+    if kept.dtype is not _I32 or kept.get_device() != dev.index or kept.shape != of or not kept.is_contiguous():
+        raise TypeError(f"kept must be a contiguous int32 {list(of)} tensor on {dev}")
+    if o.get("weights") is not None:
+        _f32_like(o["weights"], of, "the kept weights", dev)
     wp, wn = _cache_workspace(OP_CACHE_EVICT, cs, B, keep, 0, dev, ws, st)
     rc = _on(dev, (_lib or lib()).spec_cache_evict, cs, ds, B, lp, weights.data_ptr(), wst,
-             weights.shape[2], keep, int(recent), o["kept"].data_ptr(), _ptr(o.get("weights")), o["new_len"].data_ptr(),
-             _ptr(o.get("status")), wp, wn, st)
+             weights.shape[2], keep, int(recent), o["kept"].data_ptr(), _ptr(o.get("weights")),
+             _lengths(o["new_len"], B, "new_len", dev), _status(o, B, dev), wp, wn, st)
     _check(rc, "spec_cache_evict")
     return o

@@ -630,6 +630,68 @@ def test_bindings_refuse(api):
         api.spec_cache_evict(cache, table, ln, torch.zeros(2, 3, 32, device="cuda"), 4, 0, table)
 
 
+@pytest.mark.parametrize("name", ["new_len", "status", "kept", "weights", "lse", "out"])
+def test_bindings_refuse_outputs_that_do_not_fit(api, name):
+    cache = rand_cache(api, 4, 2, 16, 64, 92)
+    table = torch.tensor([[0], [1]], dtype=torch.int32, device="cuda")
+    ln = torch.tensor([2, 0], dtype=torch.int32, device="cuda")
+    q = torch.zeros(2, 3, 4, 64, dtype=BF, device="cuda")
+    w = torch.zeros(2, 2, 16, device="cuda")
+    a = api.spec_cache_append(cache, table, ln, q[:, :, :2], q[:, :, 2:])
+    o = api.spec_cache_attend(q, cache, table, ln)
+    s = api.spec_cache_weights(q, o["lse"], cache, table, ln, prev=w)
+    e = api.spec_cache_evict(cache, table, ln, w, 4, 0, table + 2)
+    calls = [(a, lambda x: api.spec_cache_append(cache, table, ln, q[:, :, :2], q[:, :, 2:], out=x)),
+             (o, lambda x: api.spec_cache_attend(q, cache, table, ln, out=x)),
+             (s, lambda x: api.spec_cache_weights(q, o["lse"], cache, table, ln, prev=w, out=x)),
+             (e, lambda x: api.spec_cache_evict(cache, table, ln, w, 4, 0, table + 2, out=x))]
+    tried = 0
+    for good, call in calls:
+        call(good)
+        if name not in good:
+            continue
+        for bad in (good[name][:1], good[name].double(), good[name].cpu()):
+            tried += 1
+            with pytest.raises((TypeError, ValueError)):
+                call(dict(good, **{name: bad}))
+    assert tried >= 3
+
+
+def test_a_call_belongs_to_its_stream(api):
+    """What a call copies or fills first is done on the stream it is given, whatever the current one is busy with."""
+    B, N, H, G, P, D, W = 2, 4, 2, 2, 32, 64, 5
+    cache = rand_cache(api, B * W, H, P, D, 93)
+    table = rand_table(B, W, B * W, 94)
+    ln = torch.tensor([100, 37], dtype=torch.int32, device="cuda")
+    q = torch.randn(B, N, H * G, D, generator=gen(95)).to(BF).cuda()
+    mask = tree_mask(B, N, 96).transpose(1, 2).contiguous().cuda().transpose(1, 2)  # a copy is taken of it
+    prev = torch.rand(B, H, W * P, generator=gen(97)).cuda()
+
+    def calls(**kw):
+        o = api.spec_cache_attend(q, cache, table, ln, mask=mask, **kw)
+        yield o
+        yield api.spec_cache_weights(q, want["lse"], cache, table, ln, prev=prev, **kw)
+        yield api.spec_cache_weights(q, want["lse"], cache, table, ln, **kw)
+        yield api.spec_cache_evict(cache, table, ln, prev, 20, 4, dst, dst_cache=other, **kw)
+        yield api.spec_cache_append(other, table, ln, q[:, :, :2], q[:, :, 2:], **kw)
+
+    other = rand_cache(api, B * W, H, P, D, 98)
+    dst = table[:, :1].contiguous()
+    want = api.spec_cache_attend(q, cache, table, ln, mask=mask)
+    first = list(calls())
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)
+    second = list(calls(stream=side))
+    side.synchronize()
+    with torch.cuda.stream(side):
+        got = [{k: t.cpu() for k, t in o.items()} for o in second]
+    torch.cuda.synchronize()
+    for x, y, z in zip(first, got, second):
+        for k in x:
+            assert torch.equal(x[k].cpu(), y[k]) and torch.equal(x[k], z[k]), k
+
+
 def test_weights_without_rows_copies_prev(api):
     """counts of 0: out is prev over the context, whatever out held."""
     cache = rand_cache(api, 8, 2, 64, 128, 66)
