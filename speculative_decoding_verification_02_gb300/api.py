@@ -606,13 +606,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _cache_workspace(op, cs, B, N, Hq, dev, ws, stream):
-    need = (_lib or lib()).spec_cache_workspace_size(op, cs, B, N, Hq)
-    if ws is None:
-        if need == 0:
-            return None, 0
-        ws = _workspace(need, dev, stream)
-    return ws.data_ptr(), ws.numel()
+def _with_workspace(fn, what, op, cs, B, N, Hq, dev, ws, stream, *args):
+    """fn(*args, workspace, its size, stream) with the stream's workspace as it is; the size that the call needs is asked for only
+    when that is too small (the library looks at it before it does anything)."""
+    have = ws if ws is not None else _workspaces.get((dev.index, stream))
+    p, n = (None, 0) if have is None else (have.data_ptr(), have.numel())
+    rc = _on(dev, fn, *args, p, n, stream)
+    if rc == SPEC_EWORKSPACE and ws is None:
+        have = _workspace(_on(dev, lib().spec_cache_workspace_size, op, cs, B, N, Hq), dev, stream)
+        rc = _on(dev, fn, *args, have.data_ptr(), have.numel(), stream)
+    _check(rc, what)
 
 
 def _raw_stream(dev) -> int:
@@ -655,7 +658,8 @@ def spec_cache_attend(q: torch.Tensor, cache, table: torch.Tensor, cache_len: to
     """Attention of q [B, N, Hq, head_dim] (bf16 or fp16), the N rows whose keys and values lie behind each request's
     cache_len tokens: row i sees the context and the rows up to itself, or with mask uint8 [B, N, N] (spec_tree_rerank's) the
     rows j with mask[b, i, j].  n_query int32 [B]: rows of a request (default N).  scale: head_dim ** -0.5 by default.
-    -> out (as q), lse fp32 [B, N, Hq], status."""
+    -> out (as q), lse fp32 [B, N, Hq], status.  ws: the caller's own workspace, for a call captured into a graph that outlives
+    larger calls on its stream (they replace the stream's)."""
     dev = q.device
     if stream is not None:
         return _on_stream(stream, spec_cache_attend, q, cache, table, cache_len, n_query=n_query, mask=mask, scale=scale,
@@ -680,11 +684,9 @@ def spec_cache_attend(q: torch.Tensor, cache, table: torch.Tensor, cache_len: to
         raise ValueError("out must have q's shape")
     if o.get("lse") is not None:
         _f32_like(o["lse"], (B, N, Hq), "lse", dev)
-    wp, wn = _cache_workspace(OP_CACHE_ATTEND, cs, B, N, Hq, dev, ws, st)
-    rc = _on(dev, (_lib or lib()).spec_cache_attend, cs, q.data_ptr(), qst, code, B, N, Hq, lp,
-             np_, _ptr(mask), D ** -0.5 if scale is None else float(scale), float(softcap), o["out"].data_ptr(), ost,
-             _ptr(o.get("lse")), _status(o, B, dev), wp, wn, st)
-    _check(rc, "spec_cache_attend")
+    _with_workspace((_lib or lib()).spec_cache_attend, "spec_cache_attend", OP_CACHE_ATTEND, cs, B, N, Hq, dev, ws, st,
+                    cs, q.data_ptr(), qst, code, B, N, Hq, lp, np_, _ptr(mask), D ** -0.5 if scale is None else float(scale),
+                    float(softcap), o["out"].data_ptr(), ost, _ptr(o.get("lse")), _status(o, B, dev))
     return o
 
 
@@ -729,11 +731,10 @@ def spec_cache_weights(q: torch.Tensor, lse: torch.Tensor, cache, table: torch.T
         o = dict(weights=w, status=torch.empty(B, dtype=torch.int32, device=dev))
     ost = _positions(o["weights"], "weights", B, H, dev)
     room = o["weights"].shape[2] if prev is None else min(prev.shape[2], o["weights"].shape[2])
-    wp, wn = _cache_workspace(OP_CACHE_WEIGHTS, cs, B, rows, Hq, dev, ws, st)
-    rc = _on(dev, (_lib or lib()).spec_cache_weights, cs, q.data_ptr(), qst, code, B, N, Hq, lse.data_ptr(), _pack3(*lse.stride()), ip, ist,
-             rows, _ptr(counts), lp, D ** -0.5 if scale is None else float(scale), float(softcap), _ptr(prev), pst,
-             o["weights"].data_ptr(), ost, room, _status(o, B, dev), wp, wn, st)
-    _check(rc, "spec_cache_weights")
+    _with_workspace((_lib or lib()).spec_cache_weights, "spec_cache_weights", OP_CACHE_WEIGHTS, cs, B, rows, Hq, dev, ws, st,
+                    cs, q.data_ptr(), qst, code, B, N, Hq, lse.data_ptr(), _pack3(*lse.stride()), ip, ist, rows, _ptr(counts),
+                    lp, D ** -0.5 if scale is None else float(scale), float(softcap), _ptr(prev), pst,
+                    o["weights"].data_ptr(), ost, room, _status(o, B, dev))
     return o
 
 
@@ -761,9 +762,7 @@ def spec_cache_evict(cache, table: torch.Tensor, cache_len: torch.Tensor, weight
         raise TypeError(f"kept must be a contiguous int32 {list(of)} tensor on {dev}")
     if o.get("weights") is not None:
         _f32_like(o["weights"], of, "the kept weights", dev)
-    wp, wn = _cache_workspace(OP_CACHE_EVICT, cs, B, keep, 0, dev, ws, st)
-    rc = _on(dev, (_lib or lib()).spec_cache_evict, cs, ds, B, lp, weights.data_ptr(), wst,
-             weights.shape[2], keep, int(recent), o["kept"].data_ptr(), _ptr(o.get("weights")),
-             _lengths(o["new_len"], B, "new_len", dev), _status(o, B, dev), wp, wn, st)
-    _check(rc, "spec_cache_evict")
+    _with_workspace((_lib or lib()).spec_cache_evict, "spec_cache_evict", OP_CACHE_EVICT, cs, B, keep, 0, dev, ws, st,
+                    cs, ds, B, lp, weights.data_ptr(), wst, weights.shape[2], keep, int(recent), kept.data_ptr(),
+                    _ptr(o.get("weights")), _lengths(o["new_len"], B, "new_len", dev), _status(o, B, dev))
     return o

@@ -657,6 +657,28 @@ def test_bindings_refuse_outputs_that_do_not_fit(api, name):
     assert tried >= 3
 
 
+def test_workspace_of_the_caller_and_of_a_stream(api):
+    """Too small a workspace of the caller's is refused; a stream's own grows."""
+    B, N, H, G, P, D, W = 2, 9, 2, 4, 64, 128, 40
+    cache = rand_cache(api, B * W, H, P, D, 99)
+    table = rand_table(B, W, B * W, 100)
+    ln = torch.tensor([2500, 1200], dtype=torch.int32, device="cuda")
+    q = torch.randn(B, N, H * G, D, generator=gen(101)).to(BF).cuda()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    few = api.spec_cache_attend(q[:, :1].contiguous(), cache, table, ln, stream=side)
+    got = api.spec_cache_attend(q, cache, table, ln, stream=side)
+    side.synchronize()
+    cs = api._cache_struct(cache, table, B, q.device)[0]
+    need = api.lib().spec_cache_workspace_size(api.OP_CACHE_ATTEND, cs, B, N, H * G)
+    assert need > 0 and few["status"].tolist() == [0, 0]
+    with pytest.raises(api.SpecError):
+        api.spec_cache_attend(q, cache, table, ln, ws=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    own = api.spec_cache_attend(q, cache, table, ln, ws=torch.empty(need, dtype=torch.uint8, device="cuda"))
+    for x in ("out", "lse", "status"):
+        assert torch.equal(got[x], own[x]), x
+
+
 def test_a_call_belongs_to_its_stream(api):
     """What a call copies or fills first is done on the stream it is given, whatever the current one is busy with."""
     B, N, H, G, P, D, W = 2, 4, 2, 2, 32, 64, 5
