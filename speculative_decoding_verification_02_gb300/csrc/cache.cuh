@@ -10,6 +10,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "common.cuh"
 #include "spec_verify.h"
 
 namespace sv {
@@ -220,6 +221,28 @@ __device__ __forceinline__ int64_t capacity(const CacheView &c) {
 // Capped score in units of log 2: x = scale q.k.
 __device__ __forceinline__ float capped_log2(float x, float softcap) {
   return (softcap > 0.0f ? softcap * tanhf(x / softcap) : x) * kLog2e;
+}
+
+// Several scores in units of log 2 capped: cap tanh(x / cap), inv_cap = 1 / cap.  A formula of exponentials alone is off by a fixed
+// part of the cap, 2^-22 and more, which at a cap of 30 is 1e-5 of a small score and of its weight.  So up to half the cap
+// x P((x / cap)^2) is taken, P the polynomial through tanh(u) / u at the Chebyshev points of u^2 in [0, 1/4] (3e-8 off), and only a
+// warp that holds a larger score goes on to 1 - 2 / (1 + exp(2 u)).  Every lane of the warp calls.
+template <int N>
+__device__ __forceinline__ void cap_scores(float *x, float inv_cap, float cap) {
+  float most = 0.0f;
+#pragma unroll
+  for (int e = 0; e < N; ++e) most = fmaxf(most, fabsf(x[e]));
+  const bool far = __any_sync(~0u, most * inv_cap > 0.5f);
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const float u = x[e] * inv_cap, w = u * u;
+    float y = x[e] * fmaf(fmaf(fmaf(fmaf(0.017131345f, w, -0.052984238f), w, 0.13324751f), w, -0.33333069f), w, 1.0f);
+    if (far) [[unlikely]] {
+      const float z = u * (2.0f * kLog2e);
+      if (fabsf(u) > 0.5f) y = cap * (1.0f - __fdividef(2.0f, 1.0f + ex2(z > 120.0f ? 120.0f : z)));
+    }
+    x[e] = y;
+  }
 }
 
 #endif

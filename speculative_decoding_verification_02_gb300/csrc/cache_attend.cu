@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kRowThreads) cache_attend_rows_kernel(const Ca
     if (k < rows && used) {
       const char *src = P.q + (b * P.qs[0] + token[k] * P.qs[1] + (head * P.group + row % P.group) * P.qs[2]) * 2;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) q[k][e] = row_value<DT>(src, part * 16 + e) * (CAP ? P.scale : P.scale * kLog2e);
+      for (int e = 0; e < 16; ++e) q[k][e] = row_value<DT>(src, part * 16 + e) * (P.scale * kLog2e);
     }
   }
   // positions of this CTA: whole steps of all its groups
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kRowThreads) cache_attend_rows_kernel(const Ca
   const int from = min(T, split * share), to = min(T, from + share);
   const uint8_t *mask = P.mask ? P.mask + static_cast<int64_t>(b) * P.N * P.N : nullptr;
 
-  const float cap2 = P.softcap * kLog2e, in_cap = CAP ? 2.0f * kLog2e / P.softcap : 0.0f;
+  const float cap2 = P.softcap * kLog2e, in_cap = CAP ? 1.0f / cap2 : 0.0f;
   float m[ROWS], sum[ROWS], acc[ROWS][16];
 #pragma unroll
   for (int k = 0; k < ROWS; ++k) {
@@ -135,19 +135,34 @@ __global__ void __launch_bounds__(kRowThreads) cache_attend_rows_kernel(const Ca
         const int t = t0 + u * kAll + group, j = t - base;
 #pragma unroll
         for (int k = 0; k < ROWS; ++k) {
-          float y = dot[k] * sc[u].x;
-          if (CAP) {  // cap tanh(x / cap) = cap (1 - 2 / (1 + exp(2 x / cap)))
-            const float z = y * in_cap;
-            y = cap2 * (1.0f - __fdividef(2.0f, 1.0f + ex2(z > 120.0f ? 120.0f : z)));
+          const float y = dot[k] * sc[u].x;
+          if (CAP) {  // capped, and masked, when all are there
+            score[u][k] = y;
+            continue;
           }
           const bool sees = t < s1 && k < rows && (j < 0 || (mask ? mask[static_cast<int64_t>(token[k]) * P.N + j] != 0 : j <= token[k]));
           score[u][k] = sees ? y : -INFINITY;
         }
-        if (j >= 0) [[unlikely]] {  // a value that no row may look at, or that is no number, has no part in the others
+        if (!CAP && j >= 0) [[unlikely]] {  // a value that no row may look at, or that is no number, has no part in the others
           bool any = false;
 #pragma unroll
           for (int k = 0; k < ROWS; ++k) any |= score[u][k] != -INFINITY;
           if (!any) vv[u] = make_uint4(0, 0, 0, 0);
+        }
+      }
+      if (CAP) {
+        cap_scores<kAtOnce * ROWS>(&score[0][0], in_cap, cap2);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int t = t0 + u * kAll + group, j = t - base;
+          bool any = false;
+#pragma unroll
+          for (int k = 0; k < ROWS; ++k) {
+            const bool sees = t < s1 && k < rows && (j < 0 || (mask ? mask[static_cast<int64_t>(token[k]) * P.N + j] != 0 : j <= token[k]));
+            if (!sees) score[u][k] = -INFINITY;
+            any |= sees;
+          }
+          if (j >= 0 && !any) vv[u] = make_uint4(0, 0, 0, 0);
         }
       }
       bool moves = false;

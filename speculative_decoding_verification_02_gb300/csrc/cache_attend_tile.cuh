@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int token = live ? by_group(A, u.row0 + r) : 0;
       const uint8_t *mask = P.mask ? P.mask + (static_cast<int64_t>(u.b) * P.N + token) * P.N : nullptr;
       const float cap2 = P.softcap * kLog2e;                // the cap in units of log 2
-      const float in_cap = CAP ? 2.0f / P.softcap : 0.0f;   // (of x in units of log 2) to 2 x / cap in units of log 2
+      const float in_cap = CAP ? 1.0f / cap2 : 0.0f;
       float m = -INFINITY, sum = 0.0f;
 
       for (; t < t_end; ++t, ++i) {
@@ -704,13 +704,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (CAP) {
 #pragma unroll
           for (int g = 0; g < OWN / 16; ++g) {
-            const float f = factor * sc[g].x * in_cap;
+            const float f = factor * sc[g].x;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              // cap tanh(x / cap) = cap (1 - 2 / (1 + exp(2 x / cap)))
-              const float y = x[g * 16 + e] * f;
-              x[g * 16 + e] = cap2 * (1.0f - __fdividef(2.0f, 1.0f + ex2(y > 120.0f ? 120.0f : y)));
-            }
+            for (int e = 0; e < 16; ++e) x[g * 16 + e] *= f;
+            cap_scores<16>(x + g * 16, in_cap, cap2);
           }
         }
         uint32_t sees[(OWN + 31) / 32];

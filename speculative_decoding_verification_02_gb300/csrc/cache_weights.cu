@@ -145,12 +145,6 @@ struct WeightSmall {
 };
 static_assert(sizeof(WeightSmall) <= 8192);
 
-// cap tanh(x / cap), x and the answer in units of log 2.
-__device__ __forceinline__ float capped_score(float x, float in_cap, float cap2) {
-  const float z = x * in_cap;
-  return cap2 * (1.0f - __fdividef(2.0f, 1.0f + ex2(z > 120.0f ? 120.0f : z)));
-}
-
 struct WeightUnit {
   int b, head, base, cnt, T, start, tile0, tiles;  // b: within the launch; start: its place, kUnitCost before its tiles
 };
@@ -184,7 +178,7 @@ __device__ __forceinline__ bool weight_lengths(const CacheWeightsParams &P, int 
          base + static_cast<int64_t>(cnt) <= min(capacity(P.c), static_cast<int64_t>(P.positions));
 }
 
-template <int DT, int D>
+template <int DT, int D, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_weights_tile_kernel(const CacheWeightsParams P, int first, int count, uint32_t group_inverse, int page_rows, bool q_vec,
                               const __grid_constant__ CUtensorMap k_map) {
@@ -326,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- summing
     const int side = warp >> 2, quarter = warp & 3, spot = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
-    const bool negative = P.scale < 0.0f, capped = P.softcap > 0.0f;
-    const float cap2 = P.softcap * kLog2e, in_cap = capped ? 2.0f / P.softcap : 0.0f;
+    const bool negative = P.scale < 0.0f;
+    const float cap2 = P.softcap * kLog2e, in_cap = CAP ? 1.0f / cap2 : 0.0f;
     uint32_t meetings = 0;
     auto together = [&] {
       bar_arrive(&sm.meet);
@@ -457,17 +451,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               tc_wait_ld();
             }
+            if (CAP) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = fmaf(y[e], 1.0f / 16, x[e]) * (sm.row[r + e].x * ks);
+              cap_scores<16>(x, in_cap, cap2);
+            }
             float part[2] = {};
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
               const float4 f = *reinterpret_cast<const float4 *>(&sm.row[r + e]);  // two rows'
-              float s0 = fmaf(y[e], 1.0f / 16, x[e]), s1 = fmaf(y[e + 1], 1.0f / 16, x[e + 1]);
-              if (capped) {
-                s0 = capped_score(s0 * (f.x * ks), in_cap, cap2) + f.y;
-                s1 = capped_score(s1 * (f.z * ks), in_cap, cap2) + f.w;
+              float s0, s1;
+              if (CAP) {
+                s0 = x[e] + f.y;
+                s1 = x[e + 1] + f.w;
               } else {
-                s0 = fmaf(s0, f.x * ks, f.y);
-                s1 = fmaf(s1, f.z * ks, f.w);
+                s0 = fmaf(fmaf(y[e], 1.0f / 16, x[e]), f.x * ks, f.y);
+                s1 = fmaf(fmaf(y[e + 1], 1.0f / 16, x[e + 1]), f.z * ks, f.w);
               }
               float p0 = ex2(s0), p1 = ex2(s1);
               if (edge) [[unlikely]] {
@@ -497,14 +496,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-std::atomic<uint64_t> weights_ready[4];
+std::atomic<uint64_t> weights_ready[8];
 
-template <int DT, int D>
+template <int DT, int D, bool CAP>
 cudaError_t launch_weight_tiles(const CacheWeightsParams &P, cudaStream_t st) {
   using S = WeightShape<DT, D>;
-  auto kern = cache_weights_tile_kernel<DT, D>;
+  auto kern = cache_weights_tile_kernel<DT, D, CAP>;
   cudaError_t e = once_per_device([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes); },
-                                  weights_ready[(DT == SPEC_DTYPE_BF16) * 2 + (D == 128)]);
+                                  weights_ready[CAP * 4 + (DT == SPEC_DTYPE_BF16) * 2 + (D == 128)]);
   if (e != cudaSuccess) return e;
   const int page_rows = std::min(1 << P.c.page_shift, kTilePositions);
   CUtensorMap map;
@@ -520,13 +519,19 @@ cudaError_t launch_weight_tiles(const CacheWeightsParams &P, cudaStream_t st) {
   return cudaSuccess;
 }
 
+template <int DT>
+cudaError_t launch_weight_tiles(const CacheWeightsParams &P, cudaStream_t st) {
+  if (P.c.head_dim == 128) return P.softcap > 0.0f ? launch_weight_tiles<DT, 128, true>(P, st) : launch_weight_tiles<DT, 128, false>(P, st);
+  return P.softcap > 0.0f ? launch_weight_tiles<DT, 64, true>(P, st) : launch_weight_tiles<DT, 64, false>(P, st);
+}
+
 }  // namespace
 
 cudaError_t launch_cache_weights(const CacheWeightsParams &P, cudaStream_t st) {
   // (a row's number times the group stays below 2^32: the multiplication that divides by it is exact)
   const bool tiles = static_cast<int64_t>(P.n_rows) * P.group * P.group < (1LL << 32);
-  if (tiles && P.c.head_dim == 128) return P.dtype == SPEC_DTYPE_BF16 ? launch_weight_tiles<SPEC_DTYPE_BF16, 128>(P, st) : launch_weight_tiles<SPEC_DTYPE_F16, 128>(P, st);
-  if (tiles && P.c.head_dim == 64) return P.dtype == SPEC_DTYPE_BF16 ? launch_weight_tiles<SPEC_DTYPE_BF16, 64>(P, st) : launch_weight_tiles<SPEC_DTYPE_F16, 64>(P, st);
+  if (tiles && (P.c.head_dim == 64 || P.c.head_dim == 128))
+    return P.dtype == SPEC_DTYPE_BF16 ? launch_weight_tiles<SPEC_DTYPE_BF16>(P, st) : launch_weight_tiles<SPEC_DTYPE_F16>(P, st);
   const int64_t most = static_cast<int64_t>(P.c.table_stride) << P.c.page_shift;
   const int spans = most > 0 ? static_cast<int>((most + kSpan - 1) / kSpan) : 1;
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(spans) * P.c.kv_heads * P.B);

@@ -443,6 +443,58 @@ def test_weights_of_normalisers_in_any_strides(api, D):
         assert bool((got["weights"].sum(-1) > 0).all())
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D,rows", [(64, 1), (64, 9), (80, 1), (128, 2), (128, 40)])
+def test_small_capped_scores_keep_their_digits(api, D, rows, dtype):
+    """Scores of one product each, so known exactly, far below the cap and around half of it: their weights to a few roundings."""
+    T, P, cap, scale = 256, 128, 30.0, 2.0 ** -4
+    codes = torch.zeros(2, 1, P, D, dtype=torch.uint8)
+    codes[..., 0] = torch.cat([torch.arange(0, 0x7f), torch.arange(0x80, 0xff), torch.zeros(2)]).reshape(2, 1, P).to(torch.uint8)
+    k = codes.cuda().view(ref.F8)
+    one = torch.ones(2, 1, device="cuda")
+    cache = [k, k.clone(), one, one.clone()]
+    table = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda")
+    q = torch.zeros(1, rows, 1, D, dtype=dtype, device="cuda")
+    q[..., 0] = 1.0
+    # all rows see the context alone: no tokens of their own among the positions
+    lens = torch.tensor([T - rows], dtype=torch.int32, device="cuda")
+    lse = torch.full((1, rows, 1), 2.0, device="cuda")
+    w = api.spec_cache_weights(q, lse, cache, table, lens, scale=scale, softcap=cap)["weights"][0, 0].cpu().double()
+    x = k.reshape(T, D)[:, 0].cpu().double() * scale
+    s = cap * torch.tanh(x / cap)
+    seen = torch.tensor([rows if j < T - rows else T - j for j in range(T)]).double()
+    want = seen * torch.exp(s - 2.0)
+    # a score: the polynomial, 8 roundings, and past half the cap a quotient of exponentials to 2^-20 of the cap; the weight: the
+    # exponent's roundings and the exponential's
+    off = s.abs() * (3e-8 + 8 * 2.0 ** -24) + torch.where(x.abs() > 14.9, cap * 2.0 ** -20, 0.0)
+    off += (s.abs() + 2.0) * 1.4427 * 2.0 ** -22 + 2.0 ** -21 + rows * 2.0 ** -24
+    worst = ((w - want).abs() / (want * off)).max()
+    assert worst <= 1, float(worst)
+    o = api.spec_cache_attend(q[:, :1].contiguous(), cache, table, torch.tensor([T - 1], dtype=torch.int32, device="cuda"), scale=scale, softcap=cap)
+    # the largest scores rule the sum: at 448 / 16 those are past half the cap
+    assert abs(float(o["lse"]) - float(torch.logsumexp(s, 0))) <= cap * 2.0 ** -20 + 30 * 2.0 ** -22
+
+
+@pytest.mark.parametrize("N,D", [(1, 64), (3, 64), (1, 128), (9, 128), (20, 128)])
+def test_normalisers_of_small_capped_scores(api, N, D):
+    """Two positions or so, scores near zero: the normaliser is off by a few roundings of 1."""
+    G, P, cap = 4, 16, 30.0
+    codes = torch.zeros(2, 1, P, D, dtype=torch.uint8)
+    codes[..., 0] = torch.randint(0, 0x38, (2, 1, P), generator=gen(120)).to(torch.uint8)
+    k = codes.cuda().view(ref.F8)
+    one = torch.ones(2, 1, device="cuda")
+    table = torch.tensor([[1, 0]], dtype=torch.int32, device="cuda")
+    q = torch.zeros(1, N, G, D, dtype=BF, device="cuda")
+    q[..., 0] = torch.rand(1, N, G, generator=gen(121)).to(BF).cuda()
+    o = api.spec_cache_attend(q, [k, k.clone(), one, one.clone()], table, torch.tensor([1], dtype=torch.int32, device="cuda"), scale=1.0, softcap=cap)
+    x = q[0, ..., 0].cpu().double()[..., None] * k.flip(0).reshape(2 * P, D)[:, 0].cpu().double()
+    s = cap * torch.tanh(x / cap)
+    for i in range(N):
+        want = torch.logsumexp(s[i, :, :i + 2], -1)
+        # (scores up to 1, sums up to 21 e: roundings of the score, the exponentials, the sum and the logarithm)
+        assert bool(((o["lse"][0, i].cpu().double() - want).abs() <= 3e-8 + 16 * 2.0 ** -24 + 2.0 ** -21 + want.abs() * 2.0 ** -22).all())
+
+
 def test_weights_of_an_attention_sum_to_its_rows(api):
     """Every row's weights sum to 1: the operators agree on what a score is."""
     B, N, H, G, D, P, W = 2, 4, 2, 3, 128, 64, 5
