@@ -27,7 +27,7 @@ constexpr int kAtOnce = 4;       // positions that a group of lanes has in fligh
 // end.  Keys and values are read once and never staged, and one launch does
 // all, without a workspace; the arithmetic is scalar, so its time goes with the
 // rows.  32 requests of one row, 16 heads of 64, 375 to 1,501 positions, capped:
-// 25 us, 2.4 TB/s (the tensor-core kernel: 50 us); one request of four rows,
+// 24 us, 2.5 TB/s (the tensor-core kernel: 50 us); one request of four rows,
 // 8 heads of 128, 2,000 positions: 13.3 us (16 us).
 template <int DT, int LANES, int ROWS, bool CAP>
 __global__ void __launch_bounds__(kRowThreads) cache_attend_rows_kernel(const CacheAttendParams P, int chunks) {
@@ -303,12 +303,20 @@ int rows_of(const CacheAttendParams &P) {
   return rows <= 1 ? 1 : rows <= 2 ? 2 : 4;
 }
 
-// CTAs to a unit: enough for two to every SM, eight at most, and no share of
-// the positions below 64.
+// CTAs that are on the GPU at once: their registers allow 2 of four rows to an
+// SM, 3 of two, 4 of one.
+int row_ctas(const CacheAttendParams &P) {
+  const int rows = rows_of(P);
+  return device_sm_count() * (rows == 4 ? 2 : rows == 2 ? 3 : 4);
+}
+
+// CTAs to a unit: as many as are on the GPU at once, eight at most, and no share
+// of the positions below 64.  (64 units of four rows, 64 wide, 600 positions:
+// 11.5 us with 256 CTAs, 17.8 with 512, which take two turns.)
 int row_splits(const CacheAttendParams &P) {
   const int64_t units = row_units(P, rows_of(P)), most = capacity_of(P.c);
   int n = 1;
-  while (n < 8 && units * n < 2 * device_sm_count() && most / (2 * n) >= 64) n *= 2;
+  while (n < 8 && units * 2 * n <= row_ctas(P) && most / (2 * n) >= 64) n *= 2;
   return n;
 }
 
@@ -388,11 +396,18 @@ bool cache_attend_on_tensor_cores(const CacheAttendParams &P) {
   // The tensor cores work on 128 rows whatever there are, and their kernel starts and joins its units slowly; the scalar kernel's
   // time goes with the rows and the components.  Measured (scalar against tensor cores, us): one row, 64 wide, 32 requests of 16
   // heads and 1,500 positions 26 and 38, 64 of 8 and 4,000 54 and 58; 128 wide, 1,500: 42 and 45, 4,000: 97 and 72; four rows,
-  // 128 wide, 8 heads: 300 positions 10 and 11, 2,000: 12 and 13, 16,000: 33 and 19.
+  // 128 wide, 8 heads: 300 positions 10 and 11, 2,000: 12 and 13, 16,000: 33 and 19.  More rows are chunks of four, each reading
+  // the positions again: worth it while all chunks are on the GPU at once and a CTA's share is short.  8 heads, 8 rows, 64 wide,
+  // 40 positions: 7.4 and 8.8, 600: 9.1 and 10.9, 6,000: 20 and 15; 36 rows, 128 wide, 40: 8.0 and 10.4, 2,000: 31 and 19; 64
+  // units of 16 rows, 64 wide, 150 positions: 10.1 and 12.0, of 36 rows (two turns): 19 and 13.
   const int64_t rows = static_cast<int64_t>(P.N) * P.group, D = P.c.head_dim;
   if (rows == 1 && D == 64) return false;
   const int64_t work = static_cast<int64_t>(P.B) * P.c.kv_heads * capacity_of(P.c) * D * rows;
-  return rows > 4 || work > (rows == 1 ? 100000000 : 16000000);
+  if (rows > 4) {
+    const int splits = row_splits(P);
+    return row_units(P, 4) * splits > row_ctas(P) || capacity_of(P.c) * D > 24000LL * splits;
+  }
+  return work > (rows == 1 ? 100000000 : 16000000);
 }
 
 size_t cache_attend_workspace(const CacheAttendParams &P) {

@@ -317,6 +317,41 @@ def test_attend_strides(api):
     assert bool((y[..., :3] == 7).all()) and bool((y[..., D + 3:] == 7).all())
 
 
+@pytest.fixture
+def roomy(monkeypatch):
+    """Page tables with room for thousands of further positions, their entries not yet given: short contexts, but the choice of the
+    kernel goes by the room, so more than four rows are the tensor cores' here and the scalar kernel's without."""
+    narrow = rand_table
+    monkeypatch.setitem(globals(), "rand_table",
+                        lambda *a: torch.nn.functional.pad(narrow(*a), (0, 200), value=-1).contiguous())
+
+
+@pytest.mark.parametrize("B,N,H,G,D,P,lens", SHAPES)
+@pytest.mark.parametrize("dtype,cap", [(BF, 0.0), (HF, 0.0), (BF, 30.0), (HF, 5.0)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_attend_with_room_to_grow(api, roomy, B, N, H, G, D, P, lens, dtype, cap, tree):
+    test_attend(api, B, N, H, G, D, P, lens, dtype, cap, tree)
+
+
+@pytest.mark.parametrize("test", [test_attend_masked_places_hold_anything, test_attend_nan_in_the_context_shows, test_attend_strides,
+                                  test_attend_scales_far_apart, test_attend_sharp_and_flat_scores])
+def test_attend_cases_with_room_to_grow(api, roomy, test):
+    test(api)
+
+
+@pytest.mark.parametrize("D,G,N,cap", [(64, 8, 1, 0.0), (128, 3, 3, 30.0), (64, 1, 60, 0.0), (128, 4, 9, 0.0)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_attend_more_rows_over_short_contexts(api, D, G, N, cap, tree):
+    """Chunks of four rows over whole contexts, one of them the last and ragged, in clusters and alone."""
+    B, H, P = 5, 2, 16
+    lens = [0, 1, 130, 270, 64]
+    W = -(-(max(lens) + N) // P)
+    cache = rand_cache(api, B * W, H, P, D, 121)
+    table = rand_table(B, W, B * W, 122)
+    q = (torch.randn(B, N, H * G, D, generator=gen(123)) * 2).to(BF).cuda()
+    check_attend(api, q, cache, table, lens, n_query=[N, N, max(N - 1, 0), N, 0], mask=tree_mask(B, N, 124) if tree else None, cap=cap)
+
+
 def test_attend_pool_past_two_gigabytes(api):
     H, P, D = 1, 256, 128
     pages = (1 << 31) // (H * P * D) + 3
