@@ -121,6 +121,7 @@ constexpr int kThreads = 320;  // two sides of 4 summing warps, 1 loading, 1 iss
 constexpr int kRing = 8;
 constexpr int kMaxRows = 64;   // rows at a time
 constexpr int kUnitCost = 4;   // what a unit costs besides its tiles, in tiles
+constexpr int kNoRow = -2147483647 - 1;  // the place of a row that sees no position
 
 template <int DT, int D>
 struct WeightShape {
@@ -137,7 +138,7 @@ struct WeightSmall {
   int start[kTileRequests + 1];  // running sum of the requests' tiles
   int2 lens[kTileRequests];      // context, rows
   alignas(16) float2 row[kMaxRows];          // factor of a row's scores, its lse negated; both in units of log 2
-  int token[kMaxRows];           // its place behind the context
+  int token[kMaxRows];           // its place behind the context; kNoRow: adds nothing
   float ring[kRing][16];         // k_scale of 16 positions
   uint64_t k_full[6], k_empty[6], s_full[2], s_empty[2], q_full, meet, ring_full[kRing], ring_empty[kRing];
   uint32_t tmem;
@@ -176,6 +177,32 @@ __device__ __forceinline__ bool weight_lengths(const CacheWeightsParams &P, int 
   cnt = P.counts ? P.counts[b] : P.n_rows;
   return base >= 0 && cnt >= 0 && cnt <= P.n_rows &&
          base + static_cast<int64_t>(cnt) <= min(capacity(P.c), static_cast<int64_t>(P.positions));
+}
+
+// A position's sum where the kernel's came out as NaN.  exp2(x - inf) is the 0 that a row of lse -inf, or none, has to add, unless
+// x is NaN or infinite (of what such a row's q holds, or of 0 times a NaN key); here only rows that see the position count.
+// at: the warp's lanes of the tile's scores.  The whole warp calls.
+template <int PIECES, bool CAP>
+__device__ __noinline__ float sum_of_seers(const WeightSmall &sm, uint32_t at, int padded, int place, float ks, float in_cap, float cap2) {
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int r = 0; r < padded; r += 16, at += 16) {
+    float x[16], y[16], z[16];
+    tmem_ld16(at, x);
+    tmem_ld16(at + padded, y);
+    if (PIECES == 3) tmem_ld16(at + 2 * padded, z);
+    tc_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      if (PIECES == 3) y[e] = fmaf(z[e], 1.0f / 16, y[e]);
+      x[e] = fmaf(y[e], 1.0f / 16, x[e]) * (sm.row[r + e].x * ks);
+    }
+    if (CAP) cap_scores<16>(x, in_cap, cap2);
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (place <= sm.token[r + e]) sum += ex2(x[e] + sm.row[r + e].y);
+  }
+  return sum;
 }
 
 template <int DT, int D, bool CAP>
@@ -416,8 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int h = u.head * P.group + row0 + r - tok[k] * P.group;
               const float z = at[k] >= 0 ? P.lse[b * P.ls[0] + at[k] * P.ls[1] + h * P.ls[2]] : -INFINITY;
               sm.row[r] = make_float2(fabsf(P.scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(ex[k] + 127) << 23),
-                                      z == -INFINITY ? -INFINITY : -z * kLog2e);  // (nothing comes of a row without positions)
-              sm.token[r] = tok[k];
+                                      z == -INFINITY ? -INFINITY : -z * kLog2e);
+              sm.token[r] = z == -INFINITY ? kNoRow : tok[k];
             }
           }
         }
@@ -477,6 +504,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               part[1] += p1;
             }
             sum += part[0] + part[1];
+          }
+          if (__any_sync(~0u, mine && sum != sum)) [[unlikely]] {
+            const float seen = sum_of_seers<S::kPieces, CAP>(sm, tmem + lanes + (buffer * 2 + side) * kSideCols, padded, j - u.base, ks, in_cap, cap2);
+            if (sum != sum) sum = seen;
           }
           tc_fence_before();
           bar_arrive(&sm.s_empty[buffer]);

@@ -1,0 +1,107 @@
+"""The 8-bit cache's operators where rows, keys or buffers are of the odd kind: against their 64-bit definitions."""
+import math
+
+import pytest
+import torch
+
+import cache_oracle as ref
+from test_gpu_cache import BF, HF, api, gen, rand_cache, rand_table  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+NAN_CODE = 0x7f
+
+
+def nan_key(cache, table, b, t, P):
+    """A NaN in one component of every head's key at position t of request b."""
+    cache[0].view(torch.uint8)[int(table[b, t // P]), :, t % P, 3] = NAN_CODE
+
+
+def check_weights(got, cache, table, q, lse, lens, counts, index, cap, prev):
+    want, tol = ref.weights(ref.Cache64(cache, table), q, lse, lens, counts, index, q.shape[3] ** -0.5, cap, prev)
+    got = got.cpu().double()
+    assert torch.equal(got.isnan(), want.isnan())
+    off = (got - want).abs() / tol
+    some = ~want.isnan()
+    assert bool((off[some] <= 1).all()), float(off[some].max())
+    return want
+
+
+# ------------------------------------------------------------------ rows that add nothing
+
+@pytest.mark.parametrize("D", [64, 80, 128])
+@pytest.mark.parametrize("dtype,cap", [(BF, 0.0), (HF, 0.0), (BF, 20.0)])
+@pytest.mark.parametrize("N,G", [(5, 2), (40, 4)])
+def test_rows_of_no_weight_hold_anything(api, D, dtype, cap, N, G):  # noqa: F811
+    """A row whose lse is -inf adds nothing, whatever its q: NaN, infinities, the largest numbers."""
+    B, H, P = 3, 2, 32
+    lens = [0, 130, 300]
+    W = -(-(max(lens) + N) // P)
+    cache = rand_cache(api, B * W, H, P, D, 200)
+    table = rand_table(B, W, B * W, 201)
+    g = gen(202)
+    q = torch.randn(B, N, H * G, D, generator=g).to(dtype).cuda()
+    lse = (torch.rand(B, N, H * G, generator=g) * 3 + 3).cuda()
+    prev = torch.rand(B, H, W * P, generator=g).cuda()
+    for row, what in ((1, math.nan), (2, math.inf), (3, -math.inf), (N - 1, torch.finfo(dtype).max)):
+        q[:, row, ::2] = what
+        lse[:, row, ::2] = -math.inf
+    q[1, 0, 1, 7] = math.nan  # one element of one head's row
+    lse[1, 0, 1] = -math.inf
+    o = api.spec_cache_weights(q, lse, cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), prev=prev, softcap=cap)
+    assert o["status"].tolist() == [0] * B
+    want = check_weights(o["weights"], cache, table, q, lse, lens, [N] * B, None, cap, prev)
+    assert not bool(want.isnan().any())
+
+
+@pytest.mark.parametrize("D", [64, 80, 128])
+@pytest.mark.parametrize("dtype,cap", [(BF, 0.0), (HF, 0.0), (HF, 20.0)])
+@pytest.mark.parametrize("picked", [False, True])
+def test_keys_of_nan_reach_the_rows_that_see_them(api, D, dtype, cap, picked):  # noqa: F811
+    """A NaN key: NaN where a row that counts sees it, nothing where none does -- all of lse -inf, or every one before it."""
+    B, N, H, G, P = 4, 6, 2, 3, 32
+    lens = [70, 200, 33, 270]
+    W = -(-(max(lens) + N) // P)
+    cache = rand_cache(api, B * W, H, P, D, 203)
+    table = rand_table(B, W, B * W, 204)
+    g = gen(205)
+    q = torch.randn(B, N, H * G, D, generator=g).to(dtype).cuda()
+    lse = (torch.rand(B, N, H * G, generator=g) * 3 + 3).cuda()
+    prev = torch.rand(B, H, W * P, generator=g).cuda()
+    counts, index = [6, 4, 0, 6], None
+    if picked:
+        index = torch.stack([torch.randperm(N, generator=g) for _ in range(B)]).to(torch.int32).cuda()
+    at = torch.arange(N).expand(B, N) if index is None else index.cpu().long()
+    nan_key(cache, table, 0, 5, P)  # in the context, seen by rows that count
+    nan_key(cache, table, 1, 7, P)
+    lse[1] = -math.inf              # ... by none that does
+    nan_key(cache, table, 2, 20, P)  # ... by no row at all
+    nan_key(cache, table, 3, lens[3] + 2, P)  # a drafted one: rows 2 and later see it and do not count
+    for i in range(2, N):
+        lse[3, at[3, i]] = -math.inf
+    o = api.spec_cache_weights(q, lse, cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), prev=prev, softcap=cap, index=index,
+                               counts=torch.tensor(counts, dtype=torch.int32, device="cuda"))
+    assert o["status"].tolist() == [0] * B
+    want = check_weights(o["weights"], cache, table, q, lse, lens, counts, index, cap, prev)
+    assert int(want.isnan().sum()) == H and bool(want[0, :, 5].isnan().all())
+    for b in (1, 2):  # what was there, to the bit
+        T = lens[b] + counts[b]
+        assert torch.equal(o["weights"][b, :, :T], prev[b, :, :T])
+
+
+def test_weights_after_an_attention_of_fewer_rows(api):  # noqa: F811
+    """Rows past n_query have lse -inf from the attention, and a q that nothing wrote."""
+    B, N, H, G, D, P = 2, 6, 2, 4, 128, 64
+    lens, rows = [700, 420], [6, 2]
+    W = 12
+    cache = rand_cache(api, B * W, H, P, D, 206)
+    table = rand_table(B, W, B * W, 207)
+    q = torch.randn(B, N, H * G, D, generator=gen(208)).to(BF).cuda()
+    q[1, 2:] = math.nan
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    prev = torch.zeros(B, H, W * P, device="cuda")
+    lse = ref.attend(ref.Cache64(cache, table), q.nan_to_num(nan=0.0), lens, rows, None, D ** -0.5, 0.0)[1].float().cuda()
+    w = api.spec_cache_weights(q, lse, cache, table, ln, prev=prev)
+    check_weights(w["weights"], cache, table, q, lse, lens, [N] * B, None, 0.0, prev)
+    total = w["weights"].double().sum(2)
+    assert bool(((total - torch.tensor(rows, device="cuda")[:, None] * G).abs() < 0.01).all())
