@@ -73,7 +73,7 @@ struct TileShape {
   static constexpr int kV8 = kK + kStagesK * kStage;
   static constexpr int kV16 = kV8 + kStagesV * kStage;
   static constexpr int kSmall = kV16 + 2 * 2 * kStage;
-  static constexpr int kBytes = kSmall + 12288 + 1024;  // (1024: alignment of the base)
+  static constexpr int kBytes = kSmall + 13312 + 1024;  // (1024: alignment of the base)
 };
 
 // What a CTA keeps of the launch's requests.
@@ -90,7 +90,7 @@ struct TileSmall {
   float tops[2][2][128];  // the two threads' maxima of a row, for two tiles
   float2 ml[2][128];      // reference and sum of a thread's positions
   int4 begun;  // the unit that begins here and ends in a later CTA
-  float row_factor[128];
+  float row_factor[2][128];  // by the unit's number: a warp may write the next unit's before another has read this one's
   float weight[128];   // of a copy's row when the copies are summed
   int64_t out_at[128];  // element offset of a row in out
   uint32_t poison[2][4];
@@ -100,7 +100,7 @@ struct TileSmall {
   uint32_t tmem;
   int dead;
 };
-static_assert(sizeof(TileSmall) <= 12288);
+static_assert(sizeof(TileSmall) <= 13312);
 
 struct Unit {
   int b, head, row0, rows;  // request, kv head, first row, rows
@@ -584,8 +584,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       bar_arrive(&sm.meet);
       return warp_wait(&sm.meet, meetings++ & 1, dead);
     };
-    // A unit's rows of q as e4m3 pieces; every earlier score product that reads them has completed.
-    auto write_q = [&](const Unit &u) {
+    // The number-th unit's rows of q as e4m3 pieces; every earlier score product that reads them has completed.
+    auto write_q = [&](const Unit &u, int number) {
       constexpr int kEach = D / 32, kWarpsQ = 4 * HALVES;  // elements to a lane
       // Four rows side by side in a loop that is not unrolled: its instructions are fetched once, and fetching is what a unit's
       // start and end spend most on.  (Rows past the last one repeat it.)
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int mine = first + kWarpsQ * lane;
         if (lane < 4 && mine < u.rows) {
           const int e = lane == 0 ? ex[0] : lane == 1 ? ex[1] : lane == 2 ? ex[2] : ex[3];
-          sm.row_factor[mine] = fmaxf(fabsf(P.scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(e + 127) << 23), 1e-30f);
+          sm.row_factor[number & 1][mine] = fmaxf(fabsf(P.scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(e + 127) << 23), 1e-30f);
         }
       }
       fence_async_shared();
@@ -665,14 +665,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     Unit next{};
     if (lo < hi) {
       next = find_unit(A, sm.q, RT, lo);
-      ok = write_q(next);
+      ok = write_q(next, 0);
     }
     for (int t = lo, i = 0; t < hi && ok;) {
       const Unit u = next;
       t = max(t, u.tile0);
       const int t_begin = t, t_end = min(hi, u.tile0 + u.tiles);
       const bool live = r < u.rows;
-      const float factor = live ? sm.row_factor[r] : 0.0f;
+      const float factor = live ? sm.row_factor[unit & 1][r] : 0.0f;
       const int token = live ? by_group(A, u.row0 + r) : 0;
       const uint8_t *mask = P.mask ? P.mask + (static_cast<int64_t>(u.b) * P.N + token) * P.N : nullptr;
       const float cap2 = P.softcap * kLog2e;                // the cap in units of log 2
@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // the next unit's q, while this one's last values are being summed
       if (t < hi) {
         next = find_unit(A, sm.q, RT, t);
-        if (!(ok = write_q(next))) break;
+        if (!(ok = write_q(next, unit + 1))) break;
       }
       // The unit's end in this CTA: the rows' sums over copies and halves, and what each copy's O is multiplied by.
       const bool whole = t_begin == u.tile0 && t == u.tile0 + u.tiles;

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import cache_oracle as ref
-from test_gpu_cache import BF, HF, api, gen, rand_cache, rand_table  # noqa: F401
+from test_gpu_cache import BF, HF, api, check_attend, gen, rand_cache, rand_table  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +105,19 @@ def test_weights_after_an_attention_of_fewer_rows(api):  # noqa: F811
     check_weights(w["weights"], cache, table, q, lse, lens, [N] * B, None, 0.0, prev)
     total = w["weights"].double().sum(2)
     assert bool(((total - torch.tensor(rows, device="cuda")[:, None] * G).abs() < 0.01).all())
+
+
+# ------------------------------------------------------------------ many short units
+
+@pytest.mark.parametrize("N,G,D,dtype", [(3, 4, 128, BF), (9, 4, 128, HF), (16, 4, 64, BF), (40, 4, 64, HF)])
+def test_units_of_a_tile_or_two_keep_their_own_factors(api, N, G, D, dtype):  # noqa: F811
+    """Requests of up to two tiles, many to a CTA, whose rows of q differ in magnitude: four copies, two and one of the rows."""
+    B, H, P = 320, 2, 16
+    g = gen(210)
+    lens = torch.randint(0, 250 - N, (B,), generator=g).tolist()
+    W = -(-250 // P)
+    cache = rand_cache(api, B * W, H, P, D, 211)
+    table = rand_table(B, W, B * W, 212)
+    size = torch.exp2(-3.0 * torch.randint(0, 4, (B, N, 1, 1), generator=g))
+    q = (torch.randn(B, N, H * G, D, generator=g) * 4 * size).to(dtype).cuda()
+    check_attend(api, q, cache, table, lens)
