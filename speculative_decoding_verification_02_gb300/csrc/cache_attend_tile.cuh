@@ -99,6 +99,7 @@ struct TileSmall {
   uint64_t q_full, o_free[2], meet, ring_full[kRing], ring_empty[kRing];
   uint32_t tmem;
   int dead;
+  int copies_k, copies_v, products_s, products_o;  // how many were begun
 };
 static_assert(sizeof(TileSmall) <= 13312);
 
@@ -269,6 +270,15 @@ __device__ void zero_row(const CacheAttendParams &P, int b, int x) {
   if (P.lse) P.lse[static_cast<int64_t>(b) * P.N * P.Hq + x] = -INFINITY;
 }
 
+// Waits for every copy and product that the CTA began.
+__device__ __noinline__ void land_all(TileSmall &sm, int stages_k, int stages_v) {
+  ring_land(sm.k_full, stages_k, sm.copies_k);
+  ring_land(sm.v_full, stages_v, sm.copies_v);
+  ring_land(sm.k_empty, stages_k, sm.products_s);
+  ring_land(sm.s_full, 2, sm.products_s);
+  ring_land(sm.pv_done, 2, sm.products_o);
+}
+
 template <int DT, int D, int REPL, bool CAP>
 __global__ void __launch_bounds__(kTileThreads, 1)
     cache_attend_tile_kernel(const CacheTilePlan A, const __grid_constant__ CUtensorMap k_map) {
@@ -347,7 +357,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     TileWalk walk(A, sm.q, RT, lo, hi, lane);
     walk.advance(0);
     walk.advance(1);
-    for (int sk = 0, lap = 0; walk.more[0];) {
+    int sk = 0, lap = 0;
+    while (walk.more[0]) {
       const int pos = walk.pos[0], page = walk.page[0], head = walk.head[0];
       if (walk.shift()) [[unlikely]] {  // a unit some tiles ahead: its rows of q into L2, which the stream of keys keeps emptying
 #pragma unroll 1
@@ -368,10 +379,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                        (head << P.c.page_shift) + (pos & ((1 << P.c.page_shift) - 1)), page, &sm.k_full[sk]);
       if (++sk == S::kStagesK) sk = 0, ++lap;
     }
-    __syncwarp();
-    if (*dead)  // the copies in flight land before the CTA leaves
-      for (int s = 0; s < S::kStagesK; ++s)
-        for (int k = 0; k < 4096 && !bar_try(&sm.k_full[s], 0) && !bar_try(&sm.k_full[s], 1); ++k) {}
+    sm.copies_k = lap * S::kStagesK + sk;
   } else if (warp == 11) {
     // ---- loading V and the blocks' scales, likewise; the scales one tile ahead
     TileWalk walk(A, sm.q, RT, lo, hi, lane);
@@ -379,7 +387,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     walk.advance(1);
     float ks, vs, ks1, vs1;
     walk.scales(0, ks, vs);
-    for (int i = 0, sv = 0, lap = 0; walk.more[0]; ++i) {
+    int sv = 0, lap = 0;
+    for (int i = 0; walk.more[0]; ++i) {
       const int r = i % kRing;
       const int pos = walk.pos[0], page = walk.page[0], head = walk.head[0];
       walk.scales(1, ks1, vs1);
@@ -399,18 +408,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ks = ks1, vs = vs1;
       if (++sv == S::kStagesV) sv = 0, ++lap;
     }
-    __syncwarp();
-    if (*dead)
-      for (int s = 0; s < S::kStagesV; ++s)
-        for (int k = 0; k < 4096 && !bar_try(&sm.v_full[s], 0) && !bar_try(&sm.v_full[s], 1); ++k) {}
+    sm.copies_v = lap * S::kStagesV + sv;
   } else if (warp == 14) {
     // ---- issuing S = Q K^T
     constexpr uint32_t kId = mma_desc(kTile, false);
     constexpr uint64_t kSw = D == 128 ? kSwizzle128 : kSwizzle64;
     const uint64_t q_desc = matrix_desc(smem_u32(smem + S::kQ), 16, 8 * D, kSw);
     const uint64_t k_desc = matrix_desc(smem_u32(smem + S::kK), 16, 8 * D, kSw);
-    int unit_end = lo, units = 0;
-    for (int t = lo, i = 0, sk = 0, lap = 0; t < hi; ++t, ++i) {
+    int unit_end = lo, units = 0, i = 0, sk = 0, lap = 0;
+    for (int t = lo; t < hi; ++t, ++i) {
       if (t >= unit_end) {
         const Unit u = find_unit(A, sm.q, RT, t);
         unit_end = u.tile0 + u.tiles;
@@ -436,12 +442,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       __syncwarp();
       if (++sk == S::kStagesK) sk = 0, ++lap;
     }
+    sm.products_s = i;
   } else if (warp == 15) {
     // ---- issuing O += P V
     constexpr uint32_t kId = mma_desc(D, true);
     const uint64_t v_desc = matrix_desc(smem_u32(smem + S::kV16), kTile * 128, 1024, kSwizzle128);
-    int unit_end = lo, units = 0;
-    for (int t = lo, i = 0; t < hi; ++t, ++i) {
+    int unit_end = lo, units = 0, i = 0;
+    for (int t = lo; t < hi; ++t, ++i) {
       const int w = i & 1;
       const bool fresh = t >= unit_end;
       if (fresh) {
@@ -462,6 +469,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       __syncwarp();
     }
+    sm.products_o = i;
   } else if (warp >= 8) {
     // ---- widening V: 16 bytes of a position to 16 halves, in the MN-major layout of the operand
     const int w4 = (warp >> 1 & 2) | (warp & 1), wide = w4 * 32 + lane;  // warps 8, 9, 12, 13
@@ -900,11 +908,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ++unit;
       ok = together();  // the shared arrays have been read
     }
+    if (!ok) tc_wait_st();  // (a warp that gave up may have stores to tensor memory in flight)
     // a warp that gave up lets its partner, which may be waiting for its maxima, go on to give up too
     if (HALVES == 2 && !ok) asm volatile("bar.arrive %0, 64;" ::"r"(3 + quarter) : "memory");
   }
   tc_fence_before();
   __syncthreads();
+  if (*dead) [[unlikely]] {  // nothing that was begun may reach shared or tensor memory that the CTA has left (else all was waited for)
+    if (warp == 0) land_all(sm, S::kStagesK, S::kStagesV);
+    __syncthreads();
+  }
   pdl_launch_dependents();  // (not earlier: the merge's blocks would crowd onto the SMs that finish first)
   if (tid == 0) {
     A.range[cta] = make_int2(lo, sm.dead);

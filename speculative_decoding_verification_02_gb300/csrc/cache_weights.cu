@@ -143,6 +143,7 @@ struct WeightSmall {
   uint64_t k_full[6], k_empty[6], s_full[2], s_empty[2], q_full, meet, ring_full[kRing], ring_empty[kRing];
   uint32_t tmem;
   int bad[2], dead;
+  int copies, products;  // how many were begun
 };
 static_assert(sizeof(WeightSmall) <= 8192);
 
@@ -302,10 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       t = end;
     }
-    __syncwarp();
-    if (*dead)  // the copies in flight land before the CTA leaves
-      for (int s = 0; s < S::kStages; ++s)
-        for (int k = 0; k < 4096 && !bar_try(&sm.k_full[s], 0) && !bar_try(&sm.k_full[s], 1); ++k) {}
+    sm.copies = lap * S::kStages + stage;
   } else if (warp == 9) {
     // ---- issuing S^T = K Q^T
     constexpr uint64_t kSw = D == 128 ? kSwizzle128 : kSwizzle64;
@@ -343,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       t = end;
     }
+    sm.products = i;
   } else {
     // ---- summing
     const int side = warp >> 2, quarter = warp & 3, spot = quarter * 32 + lane;
@@ -519,7 +518,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (sm.dead && P.status)  // a wait ran out: what the CTA worked on is void
+  if (*dead) [[unlikely]] {  // nothing that was begun may reach shared or tensor memory that the CTA has left (else all was waited for)
+    if (warp == 0) {
+      ring_land(sm.k_full, S::kStages, sm.copies);
+      ring_land(sm.k_empty, S::kStages, sm.products);
+      ring_land(sm.s_full, kBuffers, sm.products);
+    }
+    __syncthreads();
+  }
+  if (*dead && P.status)  // a wait ran out: what the CTA worked on is void
     for (int b = tid; b < count; b += kThreads) P.status[first + b] = SPEC_STATUS_TIMEOUT;
   if (warp == 9) {
     tc_fence_after();

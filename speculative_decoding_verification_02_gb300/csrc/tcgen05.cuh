@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "ring.h"
+
 namespace sv {
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -50,6 +52,12 @@ static __device__ __noinline__ bool warp_wait_long(uint64_t *bar, uint32_t parit
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *dead) {
   if (__all_sync(~0u, bar_try(bar, parity))) [[likely]] return true;
   return warp_wait_long(bar, parity, dead);
+}
+
+// A whole warp waits, for a bounded number of tries, until every phase that was
+// begun on a ring -- a copy armed, a product committed -- has completed.
+static __device__ __noinline__ void ring_land(uint64_t *ring, int stages, int begun) {
+  ring_landed(stages, begun, 1 << 18, [&](int s, int parity) { return __all_sync(~0u, bar_try(&ring[s], parity)) != 0; });
 }
 
 // ---------------------------------------------------------------- copies
