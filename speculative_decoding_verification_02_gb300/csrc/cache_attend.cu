@@ -12,6 +12,7 @@
 #include "cache.cuh"
 #include "common.cuh"
 #include "launch.h"
+#include "ring.h"
 
 namespace sv {
 namespace {
@@ -87,10 +88,10 @@ __global__ void __launch_bounds__(kRowThreads) cache_attend_rows_kernel(const Ca
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[k][e] = 0.0f;
   }
-  for (int s0 = from >> shift << shift; s0 < to; s0 += kSpanPages << shift) {
-    const int s1 = min(to, s0 + (kSpanPages << shift));
+  for (int s0 = from >> shift << shift, s1; s0 < to; s0 = s1) {
+    s1 = next_span(s0, to, kSpanPages << shift);
     __syncthreads();
-    for (int i = tid; s0 + (i << shift) < s1; i += kRowThreads) {
+    for (int i = tid; i << shift < s1 - s0; i += kRowThreads) {
       const int page = page_at(P.c, b, (s0 >> shift) + i);
       const int64_t at = page * P.c.scale_stride + head;
       s_at[i] = block_offset(P.c, page, head);

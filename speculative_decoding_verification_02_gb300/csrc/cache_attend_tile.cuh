@@ -238,7 +238,7 @@ struct TileWalk {
       end = u.tile0 + u.tiles;
       t = max(t, u.tile0);
     }
-    const int at = (t - u.tile0) * kTile + lane * 16;
+    const int at = (t - u.tile0) * kTile + (lane & 7) * 16;  // (of all lanes it could pass an int at the longest contexts)
     head[slot] = u.head;
     if (lane < 8 && at < u.T) {
       pos[slot] = at;

@@ -277,8 +277,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       t = max(t, u.tile0);
       for (int c = 0; c < chunks && ok; ++c) {
         auto page_of = [&](int k) {
+          if (k >= end || lane >= 16) return -1;  // (past the last tile a position could pass an int)
           const int pos = (k - u.tile0) * kTile + lane * 16;
-          return k < end && lane < 16 && pos < u.T ? page_at(P.c, first + u.b, pos >> shift) : -1;
+          return pos < u.T ? page_at(P.c, first + u.b, pos >> shift) : -1;
         };
         auto scale_of = [&](int page) { return page >= 0 ? P.c.k_scale[page * P.c.scale_stride + u.head] : 1.0f; };
         int page = page_of(t), page1 = page_of(t + 1);

@@ -1,5 +1,5 @@
-// Rings of barriers: which phase of each stage is the last that was begun.
-// Plain C++, so that it is tested on the host.
+// Index arithmetic of the cache kernels in plain C++, so that it is tested on
+// the host: the phases of a ring of barriers, walks over positions.
 #pragma once
 
 #ifdef __CUDACC__
@@ -26,5 +26,9 @@ SV_HOST_DEVICE bool ring_landed(int stages, int begun, int tries, Done &&done) {
   }
   return all;
 }
+
+// Where a walk over [at, to) that takes `step` positions at a time goes next:
+// positions go up to 2^31 - 257, from where a step would pass an int.
+SV_HOST_DEVICE int next_span(int at, int to, int step) { return to - at > step ? at + step : to; }
 
 }  // namespace sv

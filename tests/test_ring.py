@@ -1,4 +1,5 @@
-"""What a CTA waits for before it leaves (csrc/ring.h), compiled for the host against barriers that complete with time."""
+"""Index arithmetic of the cache kernels (csrc/ring.h) compiled for the host: what a CTA waits for before it leaves, against
+barriers that complete with time, and walks over positions up to the longest context."""
 import os
 import subprocess
 
@@ -47,12 +48,45 @@ int main() {
 """
 
 
-def test_a_cta_waits_for_what_it_began(tmp_path):
+SPANS = r"""
+#include <cstdio>
+#include "ring.h"
+
+// Spans of 256 pages over the last positions that a table can hold: they meet, cover what is left, and end.
+int main() {
+  for (int page = 16; page <= 256; page *= 2) {
+    const int step = 256 * page, most = (2147483647 - 256) / page * page;
+    for (int k = 0; k < 6; ++k)
+      for (int spans = 1; spans <= 3; ++spans) {
+        const int less[6] = {0, 1, page, step - 1, step, step + 1}, to = most - less[k];
+        int at = (most - spans * step) / page * page, rounds = 0;
+        while (at < to) {
+          const int next = sv::next_span(at, to, step);
+          if (next <= at || next > to || next - at > step || ++rounds > 4) return std::printf("page %d: %d to %d\n", page, at, next), 1;
+          at = next;
+        }
+        if (at < to) return 1;
+      }
+  }
+  return 0;
+}
+"""
+
+
+def run(tmp_path, program):
     src, exe = tmp_path / "ring.cpp", tmp_path / "ring"
-    src.write_text(PROGRAM)
-    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I" + CSRC, str(src), "-o", str(exe)], check=True)
+    src.write_text(program)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-ftrapv", "-Wall", "-Werror", "-I" + CSRC, str(src), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, r.stdout
+
+
+def test_a_cta_waits_for_what_it_began(tmp_path):
+    run(tmp_path, PROGRAM)
+
+
+def test_walks_end_at_the_longest_context(tmp_path):
+    run(tmp_path, SPANS)
 
 
 @pytest.mark.parametrize("name,rings", [("cache_attend_tile.cuh", ["k_full", "v_full", "k_empty", "s_full", "pv_done"]),
