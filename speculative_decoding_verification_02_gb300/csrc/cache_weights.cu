@@ -206,6 +206,15 @@ __device__ __noinline__ float sum_of_seers(const WeightSmall &sm, uint32_t at, i
   return sum;
 }
 
+// The requests' status before the kernel below, whose CTAs then raise it, in any
+// order and several to a request: SPEC_STATUS_TIMEOUT is the largest and stays.
+__global__ void cache_weights_status_kernel(int32_t *status, int count) {
+  pdl_launch_dependents();
+  for (int b = threadIdx.x; b < count; b += blockDim.x) status[b] = SPEC_STATUS_OK;
+}
+static_assert(SPEC_STATUS_TIMEOUT > SPEC_STATUS_BAD_INDEX && SPEC_STATUS_TIMEOUT > SPEC_STATUS_BAD_PAGE &&
+              SPEC_STATUS_TIMEOUT > SPEC_STATUS_BAD_LENGTH && SPEC_STATUS_OK == 0);
+
 template <int DT, int D, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_weights_tile_kernel(const CacheWeightsParams P, int first, int count, uint32_t group_inverse, int page_rows, bool q_vec,
@@ -227,13 +236,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm.dead = sm.bad[0] = sm.bad[1] = 0;
   }
   if (warp == 9) tmem_alloc(&sm.tmem, 512);
+  pdl_wait();
   for (int b = tid; b < count; b += kThreads) {
     int base, cnt;
     const bool ok = weight_lengths(P, first + b, base, cnt);
     sm.lens[b] = make_int2(base, cnt);
     sm.start[b + 1] = ok && base + cnt > 0 ? ((base + cnt + kTile - 1) / kTile + kUnitCost) * heads : 0;
-    // (a request without positions has its status from here)
-    if (cta == 0 && P.status && !(ok && base + cnt > 0)) P.status[first + b] = ok ? SPEC_STATUS_OK : SPEC_STATUS_BAD_LENGTH;
+    if (cta == 0 && P.status && !ok) atomicMax(&P.status[first + b], SPEC_STATUS_BAD_LENGTH);
   }
   tc_fence_before();
   __syncthreads();
@@ -376,8 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c == 0) {
           bad = sm.bad[segment & 1];
           if (tid == 0) sm.bad[(segment + 1) & 1] = 0;  // (the segment before's; the next one's is set after the next meeting)
-          if (tid == 0 && u.head == 0 && t0 == u.tile0 && P.status)
-            P.status[b] = bad & 1 ? SPEC_STATUS_BAD_PAGE : bad & 2 ? SPEC_STATUS_BAD_INDEX : SPEC_STATUS_OK;
+          if (bad && tid == 0 && u.head == 0 && t0 == u.tile0 && P.status)
+            atomicMax(&P.status[b], bad & 1 ? SPEC_STATUS_BAD_PAGE : SPEC_STATUS_BAD_INDEX);
         }
         constexpr int kEach = D / 32;
 #pragma unroll 1
@@ -528,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   if (*dead && P.status)  // a wait ran out: what the CTA worked on is void
-    for (int b = tid; b < count; b += kThreads) P.status[first + b] = SPEC_STATUS_TIMEOUT;
+    for (int b = tid; b < count; b += kThreads) atomicMax(&P.status[first + b], SPEC_STATUS_TIMEOUT);
   if (warp == 9) {
     tc_fence_after();
     tmem_free(tmem, 512);
@@ -551,8 +560,22 @@ cudaError_t launch_weight_tiles(const CacheWeightsParams &P, cudaStream_t st) {
   const bool q_vec = reinterpret_cast<uintptr_t>(P.q) % 8 == 0 && P.qs[0] % 4 == 0 && P.qs[1] % 4 == 0 && P.qs[2] % 4 == 0;
   for (int first = 0; first < P.B; first += kTileRequests) {
     const int count = std::min(kTileRequests, P.B - first);
-    e = trace_launch("cache_weights_tile", st,
-                     [&] { kern<<<device_sm_count(), kThreads, S::kBytes, st>>>(P, first, count, group_inverse, page_rows, q_vec, map); });
+    if (P.status) {
+      e = trace_launch("cache_weights_status", st, [&] { cache_weights_status_kernel<<<1, kTileRequests, 0, st>>>(P.status + first, count); });
+      if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(device_sm_count()));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::kBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = P.status && !trace_enabled() ? 1 : 0;
+    e = trace_launch_ex("cache_weights_tile", st,
+                        [&] { return cudaLaunchKernelEx(&cfg, kern, P, first, count, group_inverse, page_rows, q_vec, map); });
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -121,3 +121,41 @@ def test_units_of_a_tile_or_two_keep_their_own_factors(api, N, G, D, dtype):  # 
     size = torch.exp2(-3.0 * torch.randint(0, 4, (B, N, 1, 1), generator=g))
     q = (torch.randn(B, N, H * G, D, generator=g) * 4 * size).to(dtype).cuda()
     check_attend(api, q, cache, table, lens)
+
+
+# ------------------------------------------------------------------ status
+
+@pytest.mark.parametrize("B", [3, 300])
+@pytest.mark.parametrize("D", [64, 80, 128])
+def test_a_status_from_before_does_not_stay(api, B, D):  # noqa: F811
+    """Whatever the caller's status held, each request gets its own of this call: good ones, empty ones, and every kind of bad one."""
+    N, H, G, P, W = 4, 2, 2, 16, 4
+    cache = rand_cache(api, 64, H, P, D, 220)
+    table = torch.randint(0, 64, (B, W), generator=gen(221)).to(torch.int32).cuda()
+    lens = torch.randint(0, W * P - N, (B,), generator=gen(222)).to(torch.int32).cuda()
+    index = torch.arange(N, dtype=torch.int32, device="cuda").repeat(B, 1).contiguous()
+    counts = torch.full((B,), N, dtype=torch.int32, device="cuda")
+    q = torch.randn(B, N, H * G, D, generator=gen(223)).to(BF).cuda()
+    lse = torch.full((B, N, H * G), 4.0, device="cuda")
+    prev = torch.rand(B, H, W * P, generator=gen(224)).cuda()
+    want = [0] * B
+    for b, kind in zip((1, B - 1, B // 2, B // 3, 2 * B // 3), ("page", "length", "index", "count", "empty")):
+        want[b] = {"page": api.STATUS_BAD_PAGE, "index": api.STATUS_BAD_INDEX, "empty": 0}.get(kind, api.STATUS_BAD_LENGTH)
+        lens[b], counts[b], index[b], table[b] = 20, N, torch.arange(N), torch.arange(W)
+        if kind == "page":
+            table[b, 1] = 64
+        elif kind == "length":
+            lens[b] = W * P
+        elif kind == "index":
+            index[b, 2] = N
+        elif kind == "count":
+            counts[b] = N + 1
+        else:
+            lens[b], counts[b] = 0, 0
+    for before in (-5, 0, api.STATUS_TIMEOUT, 1 << 30):
+        o = dict(weights=prev.clone(), status=torch.full((B,), before, dtype=torch.int32, device="cuda"))
+        api.spec_cache_weights(q, lse, cache, table, lens, prev=prev, counts=counts, index=index, out=o)
+        assert o["status"].tolist() == want
+        for b in range(B):
+            if want[b]:
+                assert torch.equal(o["weights"][b], prev[b])

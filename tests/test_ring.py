@@ -97,3 +97,10 @@ def test_every_ring_of_copies_and_products_is_waited_for(name, rings):
     for ring in rings:
         assert f"ring_land(sm.{ring}," in text, ring
     assert "bar_try(" not in text
+
+
+def test_a_weights_status_is_only_raised():
+    """The CTAs that share a request set its status in any order: each by a maximum, of which the code of a wait that ran out is the largest."""
+    text = open(os.path.join(CSRC, "cache_weights.cu")).read()
+    kernel = text[text.index("cache_weights_tile_kernel(const"):text.index("cudaError_t launch_weight_tiles")]
+    assert kernel.count("P.status[") == kernel.count("atomicMax(&P.status[") == 3
