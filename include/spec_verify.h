@@ -572,7 +572,9 @@ const char *spec_last_error(void);
  * event pair, so the bracket divided by reps approaches the kernel's own
  * duration (one launch's set-up no longer in it).  Every kernel of the
  * library gives the same outputs when launched again on its own inputs, so
- * the results do not change; the launch count grows by the repeats.
+ * the results do not change; the launch count grows by the repeats.  The one
+ * that does not, spec_cache_weights with out the same memory as prev, is
+ * launched once in its pair.
  */
 int spec_trace_enable(int on);
 int spec_trace_repeat(int reps);

@@ -544,6 +544,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// The sums go where they were: a second launch would add the rows once more.
+bool in_place(const CacheWeightsParams &P) { return P.prev == P.out; }
+
 std::atomic<uint64_t> weights_ready[8];
 
 template <int DT, int D, bool CAP>
@@ -575,7 +578,7 @@ cudaError_t launch_weight_tiles(const CacheWeightsParams &P, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = P.status && !trace_enabled() ? 1 : 0;
     e = trace_launch_ex("cache_weights_tile", st,
-                        [&] { return cudaLaunchKernelEx(&cfg, kern, P, first, count, group_inverse, page_rows, q_vec, map); });
+                        [&] { return cudaLaunchKernelEx(&cfg, kern, P, first, count, group_inverse, page_rows, q_vec, map); }, !in_place(P));
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -600,7 +603,7 @@ cudaError_t launch_cache_weights(const CacheWeightsParams &P, cudaStream_t st) {
   return trace_launch("cache_weights_rows", st, [&] {
     if (P.dtype == SPEC_DTYPE_BF16) cache_weights_rows_kernel<SPEC_DTYPE_BF16><<<grid, kSpan, 0, st>>>(P, spans);
     else cache_weights_rows_kernel<SPEC_DTYPE_F16><<<grid, kSpan, 0, st>>>(P, spans);
-  });
+  }, !in_place(P));
 }
 
 }  // namespace sv

@@ -121,10 +121,12 @@ bool trace_enabled();
 // Launches of each kernel inside its event pair while tracing (1 otherwise).
 int trace_repeats();
 
+// again: the kernel leaves its own inputs alone, so that the repeats of
+// spec_trace_repeat change nothing.
 template <class F>
-cudaError_t trace_launch(const char *name, cudaStream_t st, F &&launch) {
+cudaError_t trace_launch(const char *name, cudaStream_t st, F &&launch, bool again = true) {
   const int slot = trace_begin(name, st);
-  const int reps = slot >= 0 ? trace_repeats() : 1;
+  const int reps = slot >= 0 && again ? trace_repeats() : 1;
   cudaError_t e = cudaSuccess;
   for (int r = 0; r < reps && e == cudaSuccess; ++r) {
     launch();
@@ -136,9 +138,9 @@ cudaError_t trace_launch(const char *name, cudaStream_t st, F &&launch) {
 }
 
 template <class F>
-cudaError_t trace_launch_ex(const char *name, cudaStream_t st, F &&launch) {
+cudaError_t trace_launch_ex(const char *name, cudaStream_t st, F &&launch, bool again = true) {
   const int slot = trace_begin(name, st);
-  const int reps = slot >= 0 ? trace_repeats() : 1;
+  const int reps = slot >= 0 && again ? trace_repeats() : 1;
   cudaError_t e = cudaSuccess;
   for (int r = 0; r < reps && e == cudaSuccess; ++r) {
     e = launch();

@@ -159,3 +159,42 @@ def test_a_status_from_before_does_not_stay(api, B, D):  # noqa: F811
         for b in range(B):
             if want[b]:
                 assert torch.equal(o["weights"][b], prev[b])
+
+
+# ------------------------------------------------------------------ tracing
+
+@pytest.mark.parametrize("D", [64, 80, 128])
+def test_repeats_of_a_traced_call_change_nothing(api, D):  # noqa: F811
+    """Every operator under spec_trace_repeat gives the bits of an untraced call; weights in place as well."""
+    B, N, H, G, P, W = 2, 5, 2, 3, 32, 8
+    lens = torch.tensor([200, 37], dtype=torch.int32, device="cuda")
+    q = torch.randn(B, N, H * G, D, generator=gen(230)).to(BF).cuda()
+    k, v = (torch.randn(B, N, H, D, generator=gen(s)).to(BF).cuda() * 9 for s in (231, 232))
+    prev = torch.rand(B, H, W * P, generator=gen(233)).cuda()
+
+    def step():
+        cache = rand_cache(api, B * W + B * 2, H, P, D, 234)
+        every = torch.randperm(B * W + B * 2, generator=gen(235)).to(torch.int32).cuda()
+        table, dst = every[:B * W].reshape(B, W).contiguous(), every[B * W:].reshape(B, 2).contiguous()
+        a = api.spec_cache_append(cache, table, lens, k, v)
+        o = api.spec_cache_attend(q, cache, table, lens)
+        w = api.spec_cache_weights(q, o["lse"], cache, table, lens, prev=prev)
+        room = prev.clone()
+        i = api.spec_cache_weights(q, o["lse"], cache, table, lens, prev=room, out=dict(weights=room))
+        e = api.spec_cache_evict(cache, table, a["new_len"], i["weights"], 50, 5, dst)
+        return [t.clone() for x in (a, o, w, i, e) for t in x.values()] + [x.view(torch.uint8) for x in cache[:2]] + cache[2:], w, i
+
+    want, w, i = step()
+    assert torch.equal(w["weights"], i["weights"])
+    api.trace_enable(True)
+    api.trace_repeat(3)
+    try:
+        got = step()[0]
+        torch.cuda.synchronize()
+        times = api.trace_collect(32)
+    finally:
+        api.trace_repeat(1)
+        api.trace_enable(False)
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    assert all(ms > 0 for ms, _ in times.values()) and len(times) >= 5
