@@ -34,7 +34,9 @@
  *    256-byte aligned.  It needs no initialisation: every call first writes
  *    whatever it later reads.  A workspace may be reused by any later call
  *    of any shape; calls that may overlap on the GPU (other streams) must
- *    not share one.
+ *    not share one, nor calls that several host threads make at the same
+ *    time, even on one stream: a call's kernels would be launched between
+ *    another's.
  *  - p = softmax(target_logits / T), q = softmax(draft_logits / T), the
  *    target's and the draft's next-token distributions at a position
  *    ("投机解码:为什么一个字都不改", section "一轮能出几个 token", the box

@@ -32,6 +32,7 @@ TREE_SIBLINGS_WITHOUT_REPLACEMENT = 1
 _lock = threading.Lock()
 _lib = None
 _workspaces: dict = {}
+_stream_locks: dict = {}
 
 
 class SpecError(RuntimeError):
@@ -120,11 +121,19 @@ def _check(rc: int, what: str):
 
 
 def _call(dev, fn, *args):
-    """fn(*args) with the tensors' device current: the library sizes its
-    launches for the current device, and the no-allocation entry point looks
-    up its scratch array there."""
-    with torch.cuda.device(dev):
+    """fn(*args), a stream last, with the tensors' device current: the library
+    sizes its launches for the current device, and the no-allocation entry
+    point looks up its scratch array there."""
+    with torch.cuda.device(dev), _stream_lock(dev.index, args[-1].value or 0):
         return fn(*args)
+
+
+def _stream_lock(device: int, stream: int):
+    """Held while a call launches: several kernels of it use the stream's
+    workspace, and another host thread's on the same stream must not come
+    between them."""
+    lock = _stream_locks.get((device, stream))
+    return lock if lock is not None else _stream_locks.setdefault((device, stream), threading.RLock())
 
 
 def _i32(t, shape, name, device):
@@ -163,8 +172,8 @@ def workspace(nbytes: int, device, stream=None) -> torch.Tensor:
     """A 256-byte aligned workspace of at least nbytes.
 
     One buffer is cached per (device, stream): calls on one stream are
-    ordered, so they may share it, while calls on different streams could
-    overlap and must not."""
+    ordered (those of several host threads by a lock), so they may share it,
+    while calls on different streams could overlap and must not."""
     device = torch.device(device)
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return _workspace(nbytes, device, s.cuda_stream)
@@ -588,7 +597,8 @@ def _on(dev, fn, *args):
     """fn(*args) with dev current."""
     if torch._C._cuda_getDevice() == dev.index:
         return fn(*args)
-    return _call(dev, fn, *args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def _lengths(t, B, name, dev):
@@ -609,12 +619,13 @@ def _ptr(t):
 def _with_workspace(fn, what, op, cs, B, N, Hq, dev, ws, stream, *args):
     """fn(*args, workspace, its size, stream) with the stream's workspace as it is; the size that the call needs is asked for only
     when that is too small (the library looks at it before it does anything)."""
-    have = ws if ws is not None else _workspaces.get((dev.index, stream))
-    p, n = (None, 0) if have is None else (have.data_ptr(), have.numel())
-    rc = _on(dev, fn, *args, p, n, stream)
-    if rc == SPEC_EWORKSPACE and ws is None:
-        have = _workspace(_on(dev, lib().spec_cache_workspace_size, op, cs, B, N, Hq), dev, stream)
-        rc = _on(dev, fn, *args, have.data_ptr(), have.numel(), stream)
+    with _stream_lock(dev.index, stream):
+        have = ws if ws is not None else _workspaces.get((dev.index, stream))
+        p, n = (None, 0) if have is None else (have.data_ptr(), have.numel())
+        rc = _on(dev, fn, *args, p, n, stream)
+        if rc == SPEC_EWORKSPACE and ws is None:
+            have = _workspace(_on(dev, lib().spec_cache_workspace_size, op, cs, B, N, Hq), dev, stream)
+            rc = _on(dev, fn, *args, have.data_ptr(), have.numel(), stream)
     _check(rc, what)
 
 
