@@ -80,9 +80,19 @@ cudaError_t cache_k_map(const CacheView &c, int page_rows, CUtensorMap *map) {
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.page_stride)};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(c.head_dim), static_cast<cuuint32_t>(page_rows), 1};
   const cuuint32_t ones[3] = {1, 1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.k, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  auto make = [&] {
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.k, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = make();
+  if (r != CUDA_SUCCESS) {  // a driver's call wants a context, which a host thread has after its first call of the runtime that needs one
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return e;
+    r = make();
+  }
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 

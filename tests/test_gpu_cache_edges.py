@@ -198,3 +198,67 @@ def test_repeats_of_a_traced_call_change_nothing(api, D):  # noqa: F811
     for x, y in zip(got, want):
         assert torch.equal(x, y)
     assert all(ms > 0 for ms, _ in times.values()) and len(times) >= 5
+
+
+# ------------------------------------------------------------------ host threads
+
+def test_threads_on_one_stream_get_their_own_answers(api):  # noqa: F811
+    """Attention of two shapes, each from a thread of its own, over the workspace of the stream that they share."""
+    import threading
+
+    jobs = []
+    for seed, (B, N, H, G, D, W) in ((240, (2, 9, 2, 4, 128, 40)), (241, (24, 20, 2, 4, 64, 12))):
+        cache = rand_cache(api, B * W, H, 64, D, seed)
+        table = rand_table(B, W, B * W, seed)
+        lens = torch.randint(0, W * 64 - N, (B,), generator=gen(seed)).to(torch.int32).cuda()
+        q = torch.randn(B, N, H * G, D, generator=gen(seed)).to(BF).cuda()
+        jobs.append((q, cache, table, lens))
+    want = [api.spec_cache_attend(*j) for j in jobs]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        for _ in range(200):
+            got[i].append(api.spec_cache_attend(*jobs[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert len(got[i]) == 200
+        for o in got[i]:
+            for name in ("out", "lse", "status"):
+                assert torch.equal(o[name], want[i][name]), (i, name)
+
+
+@pytest.mark.parametrize("name", ["append", "attend", "few", "weights", "evict"])
+def test_a_threads_first_call(api, name):  # noqa: F811
+    """An operator as the first thing that a host thread does with the GPU."""
+    import threading
+
+    B, N, H, G, P, D, W = 2, 9, 2, 4, 64, 128, 40
+    cache = rand_cache(api, B * W, H, P, D, 250)
+    table = rand_table(B, W, B * W, 251)
+    lens = torch.tensor([2500, 1200], dtype=torch.int32, device="cuda")
+    q = torch.randn(B, N, H * G, D, generator=gen(252)).to(BF).cuda()
+    lse = torch.full((B, N, H * G), 4.0, device="cuda")
+    w = torch.rand(B, H, W * P, generator=gen(253)).cuda()
+    one = q[:, :1, :2].contiguous()
+    dst = api.spec_cache_new(B, H, P, D)
+    to = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    call = {"append": lambda: api.spec_cache_append(cache, table, lens, q[:, :, :H], q[:, :, H:2 * H]),
+            "attend": lambda: api.spec_cache_attend(q, cache, table, lens),
+            "few": lambda: api.spec_cache_attend(one, cache, table, lens),
+            "weights": lambda: api.spec_cache_weights(q, lse, cache, table, lens, prev=w),
+            "evict": lambda: api.spec_cache_evict(cache, table, lens, w, 50, 5, to, dst_cache=dst)}[name]
+    want = call()
+    torch.cuda.synchronize()
+    got = []
+    thread = threading.Thread(target=lambda: got.append(call()))
+    thread.start()
+    thread.join()
+    torch.cuda.synchronize()
+    assert got and all(torch.equal(got[0][x], want[x]) for x in want)
