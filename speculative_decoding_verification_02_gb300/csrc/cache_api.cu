@@ -149,8 +149,8 @@ int spec_cache_attend(const spec_cache *cache, const void *q, const int64_t *q_s
     return SPEC_EINVAL;
   if (!std::isfinite(scale) || !cap_ok(softcap)) return SPEC_EINVAL;
   if ((rc = check_rows(dtype, false, q)) != SPEC_OK || (rc = check_rows(dtype, false, out)) != SPEC_OK) return rc;
-  if (B == 0 || N == 0) return SPEC_OK;
-  if (!q || !out || !cache_len || static_cast<int64_t>(B) * N * Hq > kMaxGrid / 8) return SPEC_EINVAL;
+  if (B == 0 || (N == 0 && !status)) return SPEC_OK;
+  if ((N > 0 && (!q || !out)) || !cache_len || static_cast<int64_t>(B) * std::max(N, 1) * Hq > kMaxGrid / 8) return SPEC_EINVAL;
   P.q = static_cast<const char *>(q);
   P.out = static_cast<char *>(out);
   std::copy(q_stride, q_stride + 3, P.qs);

@@ -295,8 +295,13 @@ __global__ void __launch_bounds__(kRowThreads) cache_attend_rows_kernel(const Ca
 
 // ------------------------------------------------------------------- host
 
+// Chunks of rows of a kv head: one at least, which sets the status.
+int64_t row_chunks(const CacheAttendParams &P, int rows_to_a_chunk) {
+  return std::max<int64_t>(1, (static_cast<int64_t>(P.N) * P.group + rows_to_a_chunk - 1) / rows_to_a_chunk);
+}
+
 int64_t row_units(const CacheAttendParams &P, int rows_to_a_unit) {
-  return static_cast<int64_t>(P.B) * P.c.kv_heads * ((static_cast<int64_t>(P.N) * P.group + rows_to_a_unit - 1) / rows_to_a_unit);
+  return static_cast<int64_t>(P.B) * P.c.kv_heads * row_chunks(P, rows_to_a_unit);
 }
 
 int rows_of(const CacheAttendParams &P) {
@@ -324,7 +329,7 @@ int row_splits(const CacheAttendParams &P) {
 template <int DT, int LANES, int ROWS>
 cudaError_t launch_rows(const CacheAttendParams &P, cudaStream_t st) {
   const int splits = row_splits(P);
-  const int chunks = static_cast<int>((static_cast<int64_t>(P.N) * P.group + ROWS - 1) / ROWS);
+  const int chunks = static_cast<int>(row_chunks(P, ROWS));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(row_units(P, ROWS) * splits));
   cfg.blockDim = dim3(kRowThreads);
@@ -391,7 +396,7 @@ size_t lay_out(CacheTilePlan &A, char *ws, int D) {
 
 bool cache_attend_on_tensor_cores(const CacheAttendParams &P) {
   // (a row's number times the group stays below 2^32: the multiplication that divides by it is exact)
-  if ((P.c.head_dim != 64 && P.c.head_dim != 128) || static_cast<int64_t>(P.N) * P.group * P.group >= (1LL << 32) ||
+  if (P.N == 0 || (P.c.head_dim != 64 && P.c.head_dim != 128) || static_cast<int64_t>(P.N) * P.group * P.group >= (1LL << 32) ||
       requests_at_once(P) <= 0)
     return false;
   // The tensor cores work on 128 rows whatever there are, and their kernel starts and joins its units slowly; the scalar kernel's

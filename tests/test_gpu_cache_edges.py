@@ -262,3 +262,34 @@ def test_a_threads_first_call(api, name):  # noqa: F811
     thread.join()
     torch.cuda.synchronize()
     assert got and all(torch.equal(got[0][x], want[x]) for x in want)
+
+
+# ------------------------------------------------------------------ no rows at all
+
+@pytest.mark.parametrize("D", [64, 80, 128])
+def test_calls_without_rows_say_what_is_wrong(api, D):  # noqa: F811
+    """N = 0: nothing to write but the status (and the new length), which tell good requests from bad ones as ever."""
+    B, H, G, P, W = 4, 2, 2, 16, 4
+    cache = rand_cache(api, 16, H, P, D, 260)
+    table = torch.arange(16, dtype=torch.int32, device="cuda").reshape(B, W)
+    table[2, 1] = 99
+    lens = torch.tensor([30, W * P + 1, 40, 0], dtype=torch.int32, device="cuda")
+    q = torch.empty(B, 0, H * G, D, dtype=BF, device="cuda")
+    k = torch.empty(B, 0, H, D, dtype=BF, device="cuda")
+    prev = torch.rand(B, H, W * P, generator=gen(261)).cuda()
+    want = [0, api.STATUS_BAD_LENGTH, api.STATUS_BAD_PAGE, 0]
+    for before in (-3, 77):
+        status = torch.full((B,), before, dtype=torch.int32, device="cuda")
+        out = dict(out=torch.empty_like(q), lse=torch.empty(B, 0, H * G, device="cuda"), status=status)
+        assert api.spec_cache_attend(q, cache, table, lens, out=out)["status"].tolist() == want
+        status.fill_(before)
+        mask = torch.ones(B, 0, 0, dtype=torch.uint8, device="cuda")
+        assert api.spec_cache_attend(q, cache, table, lens, mask=mask, lse=False, out=dict(out=out["out"], status=status))["status"].tolist() == want
+        status.fill_(before)
+        w = api.spec_cache_weights(q, out["lse"], cache, table, lens, prev=prev, out=dict(weights=prev.clone(), status=status))
+        assert w["status"].tolist() == want and torch.equal(w["weights"], prev)
+        new = torch.full((B,), before, dtype=torch.int32, device="cuda")
+        status.fill_(before)
+        a = api.spec_cache_append(cache, table, lens, k, k, out=dict(new_len=new, status=status))
+        # (no page is written, so none is looked at)
+        assert a["status"].tolist() == [0, api.STATUS_BAD_LENGTH, 0, 0] and a["new_len"].tolist() == lens.tolist()
