@@ -489,7 +489,7 @@ int spec_tree_rerank(const int32_t *parents, const float *conf, const int32_t *n
  *               b*stride[0] + h*stride[1] elements; they may be the same
  *               memory.
  *   positions   how many a head of prev and out holds: a request of more is
- *               SPEC_STATUS_BAD_LENGTH.
+ *               SPEC_STATUS_BAD_LENGTH.  0: out may be NULL.
  *   workspace   spec_cache_workspace_size(SPEC_OP_CACHE_WEIGHTS, ...) bytes.
  *
  * spec_cache_evict -- copy what is worth keeping of each request's cache to
@@ -497,7 +497,7 @@ int spec_tree_rerank(const int32_t *parents, const float *conf, const int32_t *n
  * those of the largest weight (ties to the lower position, NaN below every
  * number), min(keep, cache_len[b]) in all, in their order.
  *   weights     fp32, strides as above, `positions` to a head: a longer
- *               cache_len[b] is SPEC_STATUS_BAD_LENGTH.
+ *               cache_len[b] is SPEC_STATUS_BAD_LENGTH.  0: may be NULL.
  *   keep >= 1, 0 <= recent <= keep.
  *   dst         the cache written (its table: the new pages); the same
  *               kv_heads, page_size and head_dim.  It may be the same pool,

@@ -178,7 +178,7 @@ int spec_cache_weights(const spec_cache *cache, const void *q, const int64_t *q_
   if (!std::isfinite(scale) || !cap_ok(softcap)) return SPEC_EINVAL;
   if ((rc = check_rows(dtype, false, q)) != SPEC_OK) return rc;
   if (B == 0) return SPEC_OK;
-  if (!cache_len || !out || (N > 0 && (!q || !lse))) return SPEC_EINVAL;
+  if (!cache_len || (positions > 0 && !out) || (N > 0 && (!q || !lse))) return SPEC_EINVAL;
   // (tiles of a launch, and blocks of the general kernel, are numbered by an int)
   if (static_cast<int64_t>(B) * P.c.kv_heads * ((static_cast<int64_t>(P.c.table_stride) << P.c.page_shift) / 128 + 8) > kMaxGrid)
     return SPEC_EINVAL;
@@ -207,7 +207,7 @@ int spec_cache_evict(const spec_cache *cache, const spec_cache *dst, int B, cons
   if (P.c.kv_heads != P.d.kv_heads || P.c.page_shift != P.d.page_shift || P.c.head_dim != P.d.head_dim) return SPEC_EINVAL;
   if (B < 0 || positions < 0 || keep < 1 || keep > (1 << 30) || recent < 0 || recent > keep || !strides_ok(weights_stride, 2)) return SPEC_EINVAL;
   if (B == 0) return SPEC_OK;
-  if (!cache_len || !weights || !kept || !new_len || cache_len == new_len) return SPEC_EINVAL;
+  if (!cache_len || (positions > 0 && !weights) || !kept || !new_len || cache_len == new_len) return SPEC_EINVAL;
   const int64_t pages = (static_cast<int64_t>(keep) + (1 << P.c.page_shift) - 1) >> P.c.page_shift;
   if (2LL * B * P.c.kv_heads * std::max<int64_t>(pages, 16) > kMaxGrid) return SPEC_EINVAL;
   P.B = B, P.positions = positions, P.keep = keep, P.recent = recent, P.cache_len = cache_len, P.weights = weights;

@@ -293,3 +293,26 @@ def test_calls_without_rows_say_what_is_wrong(api, D):  # noqa: F811
         a = api.spec_cache_append(cache, table, lens, k, k, out=dict(new_len=new, status=status))
         # (no page is written, so none is looked at)
         assert a["status"].tolist() == [0, api.STATUS_BAD_LENGTH, 0, 0] and a["new_len"].tolist() == lens.tolist()
+
+
+@pytest.mark.parametrize("D", [64, 80])
+def test_empty_contexts_with_room_for_nothing(api, D):  # noqa: F811
+    """Weights of no positions at all (an empty tensor has no address): nothing is kept, and a longer request is told so."""
+    B, H, G, P = 3, 2, 2, 16
+    cache = rand_cache(api, 8, H, P, D, 270)
+    none = torch.empty(B, H, 0, device="cuda")
+    table = torch.arange(3, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    lens = torch.tensor([0, 2, 0], dtype=torch.int32, device="cuda")
+    want = [0, api.STATUS_BAD_LENGTH, 0]
+    e = api.spec_cache_evict(cache, table, lens, none, 4, 1, table + 3)
+    assert e["status"].tolist() == want and e["new_len"].tolist() == [0, 0, 0] and bool((e["kept"] == -1).all())
+    q = torch.randn(B, 1, H * G, D, generator=gen(271)).to(BF).cuda()
+    lse = torch.zeros(B, 1, H * G, device="cuda")
+    counts = torch.zeros(B, dtype=torch.int32, device="cuda")
+    for prev in (None, none):
+        w = api.spec_cache_weights(q, lse, cache, table, lens, prev=prev, counts=counts,
+                                   out=dict(weights=none, status=torch.full((B,), 9, dtype=torch.int32, device="cuda")))
+        assert w["status"].tolist() == want
+    # a table of no pages
+    w = api.spec_cache_weights(q, lse, cache, table[:, :0].contiguous(), counts, counts=counts)
+    assert w["status"].tolist() == [0, 0, 0] and w["weights"].shape == (B, H, 0)
