@@ -158,6 +158,19 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
   return finite_e4m3x2(a, b);
 }
 
+// y with its last bit set where rounding to it left something out (`rest`: the
+// exact value less y, of which the sign counts), and cut off instead of rounded.
+// Rounding that to e4m3 gives what one rounding of the exact value does; of y
+// itself, a value close to the middle of two would have become the middle.
+__device__ __forceinline__ float round_to_odd(float y, float rest) {
+  if (!(fabsf(rest) > 0.0f) || y == 0.0f) return y;
+  return __uint_as_float((__float_as_uint(y) - ((rest > 0.0f) != (y > 0.0f) ? 1u : 0u)) | 1u);
+}
+__device__ __forceinline__ float product_to_odd(float a, float b) {
+  const float y = a * b;
+  return round_to_odd(y, fmaf(a, b, -y));
+}
+
 // Two e4m3 bytes (low byte first) to two halves: exact.
 __device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t two) {
   uint32_t r;

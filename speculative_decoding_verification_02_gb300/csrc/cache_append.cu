@@ -90,6 +90,35 @@ struct Piece {
   }
 };
 
+// The rare cases are functions of their own: inlined, they took a tenth of the
+// kernel's time for their instructions alone.
+
+// A piece that holds an infinity or NaN, or goes into a block whose scale of a
+// caller's own stays: the quotients rounded to odd, and so once, as the
+// definition has it.
+template <int DT>
+__device__ __noinline__ uint2 odd_codes(uint4 v, float scale) {
+  using W = Piece<DT>;
+  float x[W::kValues];
+  W::unpack(v, x);
+#pragma unroll
+  for (int e = 0; e < W::kValues; ++e) {
+    const float y = x[e] / scale;
+    x[e] = fabsf(x[e]) == INFINITY ? NAN : round_to_odd(y, fmaf(-y, scale, x[e]));
+  }
+  uint32_t code[2] = {};
+#pragma unroll
+  for (int e = 0; e < W::kValues; e += 2) code[e / 4] |= finite_e4m3x2(x[e], x[e + 1]) << (8 * (e & 2));
+  return make_uint2(code[0], code[1]);
+}
+
+// Four stored values of a block whose scale grows from `was` to the power of two 1 / inv.
+__device__ __noinline__ uint32_t rounded_again(uint32_t v, float was, float inv) {
+  const float2 a = e4m3x2_to_float2(v & 0xffff), c = e4m3x2_to_float2(v >> 16);
+  return to_e4m3x2(product_to_odd(a.x, was) * inv, product_to_odd(a.y, was) * inv) |
+         to_e4m3x2(product_to_odd(c.x, was) * inv, product_to_odd(c.y, was) * inv) << 16;
+}
+
 // VEC: every row starts on a 16-byte boundary.  A thread keeps up to kHeld
 // pieces of the block in registers between the maximum and the rounding, which
 // at 128 tokens of 128 values is all of them: the rows are read once.
@@ -172,18 +201,14 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
   for (int i = 0; i < kAppendThreads / 32; ++i) amax = fmaxf(amax, s_max[i]);
   const float need = block_scale(amax);
   const float now = lo > 0 ? fmaxf(was, need) : need;
-  // a power of two but where a caller's own scale stays: then the quotient is rounded once, as the definition has it
+  // a power of two but where a caller's own scale stays
   const float inv = 1.0f / now;
   const bool exact = (__float_as_uint(now) & 0x7fffffu) == 0;
 
   uint8_t *dst = (is_v ? P.c.v : P.c.k) + block_offset(P.c, page, head);
   if (lo > 0 && now > was) {  // tokens already there, rounded again (now is a power of two)
     uint32_t *old = reinterpret_cast<uint32_t *>(dst);
-    for (int i = tid; i < lo * D / 4; i += kAppendThreads) {
-      const uint32_t v = old[i];
-      const float2 a = e4m3x2_to_float2(v & 0xffff), c = e4m3x2_to_float2(v >> 16);
-      old[i] = to_e4m3x2(a.x * was * inv, a.y * was * inv) | to_e4m3x2(c.x * was * inv, c.y * was * inv) << 16;
-    }
+    for (int i = tid; i < lo * D / 4; i += kAppendThreads) old[i] = rounded_again(old[i], was, inv);
   }
   uint8_t *to = dst + static_cast<int64_t>(lo) * D;
   auto put = [&](int i, const uint4 &v) {
@@ -192,16 +217,13 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
     uint32_t code[W::kValues / 4];
 #pragma unroll
     for (int e = 0; e < W::kValues; ++e) x[e] *= inv;
-    if (odd || !exact) [[unlikely]] {
-      W::unpack(v, x);
-#pragma unroll
-      for (int e = 0; e < W::kValues; ++e) x[e] = fabsf(x[e]) == INFINITY ? NAN : x[e] / now;
-    }
 #pragma unroll
     for (int e = 0; e < W::kValues / 4; ++e)
       code[e] = finite_e4m3x2(x[4 * e], x[4 * e + 1]) | finite_e4m3x2(x[4 * e + 2], x[4 * e + 3]) << 16;
-    if constexpr (W::kValues == 8) reinterpret_cast<uint2 *>(to)[i] = make_uint2(code[0], code[1]);
-    else reinterpret_cast<uint32_t *>(to)[i] = code[0];
+    uint2 two = make_uint2(code[0], W::kValues == 8 ? code[W::kValues / 4 - 1] : 0);
+    if (odd || !exact) [[unlikely]] two = odd_codes<DT>(v, now);
+    if constexpr (W::kValues == 8) reinterpret_cast<uint2 *>(to)[i] = two;
+    else reinterpret_cast<uint32_t *>(to)[i] = two.x;
   };
 #pragma unroll
   for (int k = 0; k < kHeld; ++k)

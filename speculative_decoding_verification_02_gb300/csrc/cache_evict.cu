@@ -262,29 +262,38 @@ __device__ __forceinline__ uint32_t most_of(const uint4 &v) {
   return max(most & 0xff, most >> 8 & 0xff);
 }
 
-// 16 stored values times a power of two, rounded again.  Through halves: the
-// product of four bits and a power of two is exact in them, or so far below
-// e4m3's smallest step that it rounds to zero either way.
+// 16 stored values times a ratio of scales, rounded again: for any ratio (a
+// function of its own, which few caches need).
+__device__ __noinline__ uint4 rescaled_by_any(uint4 v, float ratio) {
+  const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+  uint32_t out[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 a = e4m3x2_to_float2(in[e] & 0xffff), b = e4m3x2_to_float2(in[e] >> 16);
+    out[e] = to_e4m3x2(product_to_odd(a.x, ratio), product_to_odd(a.y, ratio)) |
+             to_e4m3x2(product_to_odd(b.x, ratio), product_to_odd(b.y, ratio)) << 16;
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// A power of two goes through halves: the product of four bits and a power of
+// two is exact in them, or so far below e4m3's smallest step that it rounds to
+// zero either way.
 __device__ __forceinline__ uint4 rescaled(const uint4 &v, float ratio) {
+  if (!(ratio <= 32768.0f && (__float_as_uint(ratio) & 0x7fffffu) == 0)) [[unlikely]] return rescaled_by_any(v, ratio);
   uint4 r;
   const uint32_t in[4] = {v.x, v.y, v.z, v.w};
   uint32_t *out = reinterpret_cast<uint32_t *>(&r);
-  const bool halves = ratio <= 32768.0f && (__float_as_uint(ratio) & 0x7fffffu) == 0;
-  const __half2 k = __float2half2_rn(halves ? ratio : 0.0f);
+  const __half2 k = __float2half2_rn(ratio);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    if (halves) [[likely]] {
-      uint16_t c[2];
+    uint16_t c[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const __half2 x = __hmul2(e4m3x2_to_half2(h ? in[e] >> 16 : in[e] & 0xffff), k);
-        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c[h]) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
-      }
-      out[e] = c[0] | static_cast<uint32_t>(c[1]) << 16;
-    } else {
-      const float2 a = e4m3x2_to_float2(in[e] & 0xffff), b = e4m3x2_to_float2(in[e] >> 16);
-      out[e] = to_e4m3x2(a.x * ratio, a.y * ratio) | to_e4m3x2(b.x * ratio, b.y * ratio) << 16;
+    for (int h = 0; h < 2; ++h) {
+      const __half2 x = __hmul2(e4m3x2_to_half2(h ? in[e] >> 16 : in[e] & 0xffff), k);
+      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c[h]) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
     }
+    out[e] = c[0] | static_cast<uint32_t>(c[1]) << 16;
   }
   return r;
 }
@@ -321,7 +330,7 @@ __global__ void __launch_bounds__(kGatherThreads, 5) cache_gather_kernel(const C
     s = scales[page * P.c.scale_stride];
   };
   uint4 held[kGatherHeld];
-  float from[kGatherHeld], amax = 0.0f;
+  float from[kGatherHeld], amax = 0.0f;  // (of products rounded up: one just above what a scale holds asks for the next)
   int token[kGatherHeld];
 #pragma unroll
   for (int k = 0; k < kGatherHeld; ++k) {
@@ -333,12 +342,12 @@ __global__ void __launch_bounds__(kGatherThreads, 5) cache_gather_kernel(const C
     if (token[k] >= 0) load(token[k], (tid + k * TEAM) % per_row, held[k], from[k]);
 #pragma unroll
   for (int k = 0; k < kGatherHeld; ++k)
-    if (token[k] >= 0) amax = fmaxf(amax, e4m3x2_to_float2(most_of(held[k])).x * from[k]);
+    if (token[k] >= 0) amax = fmaxf(amax, __fmul_ru(e4m3x2_to_float2(most_of(held[k])).x, from[k]));
   for (int i = tid + kGatherHeld * TEAM; i < pieces; i += TEAM) {
     uint4 v;
     float s;
     load(kept[i / per_row], i % per_row, v, s);
-    amax = fmaxf(amax, e4m3x2_to_float2(most_of(v)).x * s);
+    amax = fmaxf(amax, __fmul_ru(e4m3x2_to_float2(most_of(v)).x, s));
   }
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
   if (TEAM > 32) {

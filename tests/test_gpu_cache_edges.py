@@ -316,3 +316,114 @@ def test_empty_contexts_with_room_for_nothing(api, D):  # noqa: F811
     # a table of no pages
     w = api.spec_cache_weights(q, lse, cache, table[:, :0].contiguous(), counts, counts=counts)
     assert w["status"].tolist() == [0, 0, 0] and w["weights"].shape == (B, H, 0)
+
+
+# ------------------------------------------------------------------ scales that are no powers of two
+
+def e4m3_values():
+    """Every positive number of e4m3 and the points half way between neighbours."""
+    x = torch.arange(1, 127, dtype=torch.uint8).view(ref.F8).double()
+    return x, (x[1:] + x[:-1]) / 2
+
+
+def near_ties(limit):
+    """(a, half, s): s the float32 nearest half / a, so that the product a s is the half-way point `half` in float32 but not exactly; s < 1."""
+    values, halves = e4m3_values()
+    found = []
+    for a in values.tolist():
+        for half in halves.tolist():
+            if not 0.5 < half / a < 1:
+                continue
+            s = float(torch.tensor(half / a, dtype=torch.float64).float())
+            if a * s != half and float(torch.tensor(a).float() * torch.tensor(s).float()) == half:
+                found.append((a, half, s))
+    return found[::max(1, len(found) // limit)][:limit]
+
+
+def codes(x):
+    return torch.tensor(x, dtype=torch.float64).float().to(ref.F8).view(torch.uint8)
+
+
+def same_cells(cache, table, want):
+    got = ref.Cache64(cache, table)
+    for w in (0, 1):
+        assert torch.equal(got.scale[w], want.scale[w])
+        assert torch.equal(got.val[w], want.val[w])
+
+
+@pytest.mark.parametrize("D", [64, 80, 128])
+@pytest.mark.parametrize("s", [0.7, 1.0 / 3, 0.013])
+def test_append_rounds_a_quotient_once(api, D, s):  # noqa: F811
+    """New rows behind a token whose block keeps a scale of the caller's own: values whose quotient is half way in float32, not in truth."""
+    P, H = 16, 1
+    _, halves = e4m3_values()
+    s = float(torch.tensor(s).float())
+    reach = 448 * 2.0 ** math.floor(math.log2(s))  # what asks for no scale above s
+    x = (halves * s).float()
+    x = x[x < reach]
+    x = torch.cat([x, -x, x.nextafter(torch.tensor(math.inf)), x.nextafter(torch.tensor(0.0))])
+    x = torch.nn.functional.pad(x, (0, -len(x) % D)).reshape(1, -1, H, D)
+    x = x[:, :P - 1] if x.shape[1] >= P else x
+    cache = rand_cache(api, 1, H, P, D, 280)
+    for i in (2, 3):
+        cache[i].fill_(s)
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    want = ref.Cache64(cache, table)
+    want.append(0, 1, x[0], x[0])
+    assert float(want.scale[0]) == s
+    api.spec_cache_append(cache, table, torch.ones(1, dtype=torch.int32, device="cuda"), x.cuda(), x.cuda())
+    same_cells(cache, table, want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_rounds_old_tokens_once(api, D):  # noqa: F811
+    """A block whose scale of the caller's own grows to a power of two: old values half way in float32, not in truth."""
+    ties = near_ties(60)
+    P, H, B = 16, 1, len(ties)
+    cache = rand_cache(api, B, H, P, D, 281)
+    for b, (a, _, s) in enumerate(ties):
+        for w in (0, 1):
+            cache[w].view(torch.uint8)[b, 0, :3] = codes([a, -a])[torch.arange(3 * D) % 2].reshape(3, D).cuda()
+            cache[2 + w][b] = s
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    x = torch.full((B, 1, H, D), 448.0).to(BF)  # asks for a scale of 1
+    want = ref.Cache64(cache, table)
+    for b in range(B):
+        want.append(b, 3, x[b], x[b])
+    assert bool((want.scale[0] == 1).all())
+    api.spec_cache_append(cache, table, torch.full((B,), 3, dtype=torch.int32, device="cuda"), x.cuda(), x.cuda())
+    same_cells(cache, table, want)
+
+
+@pytest.mark.parametrize("D", [64, 80, 128])
+def test_evict_rounds_once(api, D):  # noqa: F811
+    """Kept rows of a block with a scale of the caller's own: values half way in float32, and largest ones just above a scale's reach."""
+    ties = near_ties(60)
+    values, _ = e4m3_values()
+    for a in values.tolist():  # a s is 448 in float32 and more in truth: the scale has to be 2
+        s = float(torch.tensor(448.0 / a, dtype=torch.float64).float())
+        if a < 448 and a * s > 448 and float(torch.tensor(a).float() * torch.tensor(s).float()) == 448:
+            ties.append((a, None, s))
+    assert ties[-1][1] is None
+    P, H, B = 16, 1, len(ties)
+    cache = rand_cache(api, B, H, P, D, 282)
+    pool = rand_cache(api, B, H, P, D, 283)
+    for b, (a, half, s) in enumerate(ties):
+        for w in (0, 1):
+            x = codes([a, -a])[torch.arange(5 * D) % 2].reshape(5, D)
+            if half is not None:
+                x[4, 7] = codes([448.0])[0]  # scale 1
+            cache[w].view(torch.uint8)[b, 0, :5] = x.cuda()
+            cache[2 + w][b] = s
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    before, want = ref.Cache64(cache, table), ref.Cache64(pool, table)
+    lens = torch.full((B,), 5, dtype=torch.int32, device="cuda")
+    api.spec_cache_evict(cache, table, lens, torch.ones(B, H, P, device="cuda"), 5, 0, table, dst_cache=pool)
+    for b, (_, half, _) in enumerate(ties):
+        for w in (0, 1):
+            rows = before.rows(w, b, 5)[0]
+            scale = ref.block_scale(rows)
+            assert scale == (2 if half is None else 1)
+            want.scale[w][b, 0] = scale
+            want.val[w][b, 0, :5] = ref.e4m3(rows / scale)
+    same_cells(pool, table, want)
