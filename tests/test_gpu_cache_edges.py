@@ -427,3 +427,61 @@ def test_evict_rounds_once(api, D):  # noqa: F811
             want.scale[w][b, 0] = scale
             want.val[w][b, 0, :5] = ref.e4m3(rows / scale)
     same_cells(pool, table, want)
+
+
+# ------------------------------------------------------------------ wrong requests on the tensor cores
+
+@pytest.mark.parametrize("N,G,D", [(5, 4, 128), (16, 4, 64), (40, 4, 128)])
+@pytest.mark.parametrize("kind", ["page", "page below", "length", "negative", "count"])
+def test_wrong_requests_among_long_ones(api, kind, N, G, D):  # noqa: F811
+    """Requests cut over several CTAs, every third of them wrong: those give zeros and their status, the others the bits they had."""
+    B, H, P = 9, 2, 64
+    lens = torch.tensor([3000, 2100, 900, 64, 5000, 1, 700, 4000, 2500], dtype=torch.int32, device="cuda")
+    W = -(-(5000 + N) // P)
+    cache = rand_cache(api, B * W, H, P, D, 290)
+    table = rand_table(B, W, B * W, 291)
+    q = torch.randn(B, N, H * G, D, generator=gen(292)).to(BF).cuda()
+    n = torch.full((B,), N, dtype=torch.int32, device="cuda")
+    lse = torch.full((B, N, H * G), 5.0, device="cuda")
+    prev = torch.rand(B, H, W * P, generator=gen(293)).cuda()
+
+    def both():
+        return (api.spec_cache_attend(q, cache, table, lens, n_query=n),
+                api.spec_cache_weights(q, lse, cache, table, lens, prev=prev, counts=n))
+
+    good = both()
+    wrong = [1, 4, 7]
+    for b in wrong:
+        if kind == "page":
+            table[b, int(lens[b]) // P] = B * W
+        elif kind == "page below":
+            table[b, 0] = -7
+        elif kind == "length":
+            lens[b] = W * P
+        elif kind == "negative":
+            lens[b] = -(1 << 31)
+        else:
+            n[b] = N + 1
+    status = api.STATUS_BAD_PAGE if "page" in kind else api.STATUS_BAD_LENGTH
+    o, w = both()
+    for x in (o, w):
+        assert x["status"].tolist() == [status if b in wrong else 0 for b in range(B)]
+    for b in range(B):
+        if b in wrong:
+            assert bool((o["out"][b] == 0).all()) and bool((o["lse"][b] == -math.inf).all()) and torch.equal(w["weights"][b], prev[b])
+        else:
+            assert torch.equal(w["weights"][b], good[1]["weights"][b])
+            if "page" in kind:  # (a request without a length moves the cuts, and with them the order of sums)
+                assert torch.equal(o["out"][b], good[0]["out"][b]) and torch.equal(o["lse"][b], good[0]["lse"][b])
+    check_attend_of_good(o, q, cache, table, lens, n, wrong)
+
+
+def check_attend_of_good(o, q, cache, table, lens, n, wrong):
+    lens, n = lens.tolist(), n.tolist()
+    for b in wrong:
+        lens[b], n[b] = 0, 0
+    out, lse, t_out, t_lse = ref.attend(ref.Cache64(cache, table), q, lens, n, None, q.shape[3] ** -0.5, 0.0)
+    for b in range(len(lens)):
+        if b not in wrong:
+            assert bool(((o["out"][b].cpu().double() - out[b]).abs() <= t_out[b]).all())
+            assert bool(((o["lse"][b].cpu().double() - lse[b]).abs() <= t_lse[b]).all())
