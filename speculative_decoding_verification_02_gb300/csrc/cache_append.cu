@@ -5,10 +5,13 @@
 //
 // 2 bytes are read and 1 written a value.  A block's scale needs all of its new
 // rows, so the unit of work is one block (request, page, head, K or V), a CTA to
-// each.  Four prompts of 3,000 to 8,001 tokens, 8 heads of 128 in bf16: 31 us,
-// 4.8 TB/s, bound by instruction issue (73% of the slots); with a division for
+// each.  Four prompts of 3,000 to 8,001 tokens, 8 heads of 128 in bf16: 30 us,
+// 5.1 TB/s, bound by instruction issue (74% of the slots); with a division for
 // each 16 bytes' row it was 36 us, reading the rows twice 73 us.  A batch's nine
-// rows a request: 9 us for 64 requests, a block's chain of loads.
+// rows a request: 8.7 us for 64 requests.  16 requests are one turn of CTAs, a
+// block's chain of loads (4.3 us); 64 are 2,048 CTAs, four of them to an SM at
+// 64 registers, so more than three turns, half of them for second pages that
+// few requests' rows reach.
 #include "cache.cuh"
 #include "launch.h"
 

@@ -406,6 +406,9 @@ bool cache_attend_on_tensor_cores(const CacheAttendParams &P) {
   // the positions again: worth it while all chunks are on the GPU at once and a CTA's share is short.  8 heads, 8 rows, 64 wide,
   // 40 positions: 7.4 and 8.8, 600: 9.1 and 10.9, 6,000: 20 and 15; 36 rows, 128 wide, 40: 8.0 and 10.4, 2,000: 31 and 19; 64
   // units of 16 rows, 64 wide, 150 positions: 10.1 and 12.0, of 36 rows (two turns): 19 and 13.
+  // The bound on one row does not fit few units over long contexts, since a unit has eight CTAs at most: 64 wide, 131,067 positions,
+  // 1 unit 134 and 68, 8 units 182 and 51, 32 units 195 and 136; 128 wide, 1 unit 324 and 86; 16,000 positions, 8 units, 64 wide 20
+  // and 20, 128 wide 48 and 24.  It goes by the room in the table, as all of these do: the lengths are on the GPU.
   const int64_t rows = static_cast<int64_t>(P.N) * P.group, D = P.c.head_dim;
   if (rows == 1 && D == 64) return false;
   const int64_t work = static_cast<int64_t>(P.B) * P.c.kv_heads * capacity_of(P.c) * D * rows;

@@ -42,13 +42,14 @@ namespace {
 // half of the positions, which agree on their rows' reference: that costs a
 // barrier, and halves what a thread does between the two products.
 
-// Heads of 128, 8 of them.  One request, 131,072 positions, 20 rows (four copies):
-// 57 us, 4.7 TB/s, the tensor pipe active for most of a tile's 1,500 cycles
-// (16 instructions of about 77).  64 requests of up to 12,000 positions, 36 rows
-// (two copies): 175 us, 5.6 TB/s, a tile takes as long as its softmax
-// (1,450 cycles) and a fifth goes to units' starts and ends.  16 trees of 60
-// nodes, 240 rows, up to 6,000 positions: 106 us, 566 TFLOP/s, bound by the
-// exponentials and the chain around them.
+// Heads of 128, 8 of them, in a graph of calls.  One request, 131,072 positions,
+// 20 rows (four copies): 57 us, 4.7 TB/s, bound by the tensor pipe: a tile takes
+// 1,220 cycles, its 16 instructions of about 77.  64 requests of up to 12,000
+// positions, 36 rows (two copies): 175 us, 5.4 TB/s, a tile takes as long as its
+// softmax (1,350 cycles) and 13% goes to units' starts and ends.  16 trees of 60
+// nodes, 240 rows, up to 6,000 positions: 106 us, 600 TFLOP/s, bound by the
+// exponentials and the chain around them (2,290 cycles a tile; 27% starts and
+// ends).
 
 constexpr int kTile = 128;         // positions to a tile
 // What a unit costs a CTA besides its tiles (its q, its end), in tiles: the cuts

@@ -11,7 +11,7 @@
 //
 // 131,071 positions of 8 heads to 4,096: 35 us, of them about 24 the selection
 // (eight CTAs to a head, bound by its barriers).  32 requests of up to 7,001 to
-// 1,000, 8 heads of 64: 48 us, about half of it the gathering of 64-byte rows.
+// 1,000, 8 heads of 64: 47 us, about half of it the gathering of 64-byte rows.
 #include <algorithm>
 #include <cooperative_groups.h>
 

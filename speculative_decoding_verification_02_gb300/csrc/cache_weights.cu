@@ -113,8 +113,9 @@ __global__ void __launch_bounds__(kSpan) cache_weights_rows_kernel(const CacheWe
 // most of them waits that were over already) than its bytes take to arrive.
 // Bound by reading K (head_dim bytes a position and kv head) for few rows, by
 // the exponentials for many.  One row over 131,068 positions, 8 heads of 128:
-// 29 us, 4.8 TB/s; 64 requests of up to 5,000 positions, 20 rows on average:
-// 67 us, a third of it the units' starts.
+// 30 us, 4.7 TB/s; 64 requests of up to 5,000 positions, 20 rows on average:
+// 67 us, a third of it the units' starts.  1 us of each is the status's own
+// kernel, which a call without a status does not launch.
 
 constexpr int kTile = 256;      // positions to a tile
 constexpr int kThreads = 320;  // two sides of 4 summing warps, 1 loading, 1 issuing
