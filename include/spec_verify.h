@@ -67,10 +67,11 @@ extern "C" {
 #define SPEC_STATUS_BAD_PAGE 5    /* a page of the cache outside its pool */
 #define SPEC_STATUS_BAD_INDEX 6   /* a row index outside the rows */
 #define SPEC_STATUS_TIMEOUT 7     /* a wait inside a kernel ran out; the call's outputs are void */
+#define SPEC_STATUS_BAD_SLOT 8    /* a slot outside the pool of states */
 
 #define SPEC_DTYPE_F32 0
 #define SPEC_DTYPE_BF16 1
-#define SPEC_DTYPE_F16 2 /* rows of the spec_cache_* entry points only */
+#define SPEC_DTYPE_F16 2 /* rows of the spec_cache_* and spec_state_* entry points only */
 
 /* `op` argument of spec_workspace_size */
 #define SPEC_OP_NGRAM 0
@@ -83,6 +84,9 @@ extern "C" {
 #define SPEC_OP_CACHE_ATTEND 6
 #define SPEC_OP_CACHE_WEIGHTS 7
 #define SPEC_OP_CACHE_EVICT 8
+/* `op` argument of spec_state_workspace_size */
+#define SPEC_OP_STATE_FORWARD 9
+#define SPEC_OP_STATE_ATTEND 10
 
 /* Limits checked on the host. */
 #define SPEC_MAX_K 64        /* draft length of a chain */
@@ -541,6 +545,106 @@ int spec_cache_evict(const spec_cache *cache, const spec_cache *dst, int B, cons
                      float *kept_weights, int32_t *new_len, int32_t *status, void *workspace,
                      size_t workspace_bytes, void *stream);
 size_t spec_cache_workspace_size(int op, const spec_cache *cache, int B, int N, int Hq);
+
+/*
+ * Linear attention with a decay for each head, and its state through a
+ * rejected draft.
+ *
+ * A layer of this kind keeps, in place of a cache, one fp32 matrix for each
+ * head of a request, which its tokens update one after another:
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,     o_t = scale * q_t^T S_t.
+ * A cache takes a rejected draft back by its length; a state cannot, and
+ * ("投机解码:为什么一个字都不改", the passage on hybrid models, whose state is
+ * 144 MiB a request) a snapshot for every drafted token costs as much memory
+ * as it moves.  So the verify step's rows are computed over a state that stays
+ * as it is (spec_state_attend), and the accepted rows' own k, v and decay
+ * then advance it in one pass (spec_state_commit): no snapshots.
+ *
+ * struct spec_state (HOST memory, read during the call; its pointers are
+ * device memory).  A pool of num_slots slots; a slot holds one request:
+ *   state       fp32 [num_slots][heads][key_dim][value_dim]; slots are
+ *               slot_stride floats apart (a multiple of 4, at least
+ *               heads * key_dim * value_dim); 16-byte aligned.
+ *   slots       int32 [B], each request's slot, or NULL (request b: slot b).
+ *   key_dim and value_dim are multiples of 16, at most 256.
+ * A slot that a call writes is that of one request alone, and no other
+ * request of the call reads it.
+ *
+ * Rows: dtype SPEC_DTYPE_BF16 or SPEC_DTYPE_F16; strides in elements, in the
+ * order request, token, head; a head's values are contiguous.  Any strides are
+ * served; rows that start on 16-byte boundaries are faster.
+ *   q, k        key_heads heads (a divisor of heads) of key_dim; state head h
+ *               reads key head h / (heads / key_heads).
+ *   v           heads heads of value_dim.
+ *   decay       fp32 natural logarithms g of the factors, strides (request,
+ *               token, head) as they come, 0 for what is shared.  -inf is a
+ *               factor of 0, which forgets every finite thing before the token.
+ * status[b] (out int32 [B] or NULL): SPEC_STATUS_BAD_LENGTH (a count out of
+ * range), SPEC_STATUS_BAD_SLOT (a slot outside the pool), SPEC_STATUS_BAD_INDEX
+ * or SPEC_STATUS_BAD_TREE.  Such a request's state is not written and its rows
+ * of out are 0.
+ *
+ * spec_state_forward -- n tokens behind each request's state: a prompt, a
+ * part of one, a single token.
+ *   from        the states before; slot -1, and every slot when from->state is
+ *               NULL: a state of zeros.
+ *   to          the states after (heads, key_dim and value_dim as in from), or
+ *               NULL: not written.  It may be the same memory, each request
+ *               reading and writing one slot.
+ *   counts      int32 [B] or NULL (= n), each in [0, n]: a request's tokens.
+ *   scale       finite.
+ *   out         the rows' dtype, [B][n][heads][value_dim]; rows from the
+ *               count on are 0.  A row has no part in an earlier one, whatever
+ *               it holds.
+ *   workspace   spec_state_workspace_size(SPEC_OP_STATE_FORWARD, ...) bytes.
+ *
+ * spec_state_attend -- the outputs of N drafted rows, the state not written.
+ *   parents     int32 [B][N] or NULL.  NULL: a chain, row i follows row i - 1.
+ *               Else a tree as in spec_verify_tree (parents[b][0] = -1,
+ *               0 <= parents[b][i] < i, depth at most SPEC_MAX_DEPTH): row i
+ *               follows row parents[b][i], the root the state.
+ *               N <= SPEC_MAX_NODES.
+ *   n_query     int32 [B] or NULL (= N), each in [0, N]: rows of a request
+ *               (later ones get 0, their parents are not read).
+ *   workspace   spec_state_workspace_size(SPEC_OP_STATE_ATTEND, ...) bytes.
+ *
+ * spec_state_commit -- the state advanced by rows that were accepted.
+ *   index       NULL, or int32 [B][index_stride]: the i-th row committed is
+ *               token index[b][i] of k, v and decay (path_nodes of
+ *               spec_verify_tree).
+ *   n_rows      rows a request at most: n without index, else the entries of
+ *               index (<= index_stride).
+ *   counts      int32 [B] or NULL (= n_rows): n_emit of spec_verify_*.
+ *   from, to    as above (to is required).  A request of no rows keeps its
+ *               state (it is copied where the two differ).
+ *
+ * spec_state_workspace_size -- bytes for a call of op (B requests, n tokens or
+ * nodes) over states of this geometry (its pointers are not read); 0 for
+ * invalid arguments and for calls that need none.  The workspace needs no
+ * initialisation.
+ */
+typedef struct spec_state {
+  float *state;
+  int64_t slot_stride;
+  int32_t num_slots, heads, key_dim, value_dim;
+  const int32_t *slots;
+} spec_state;
+
+int spec_state_forward(const spec_state *from, const spec_state *to, const void *q, const int64_t *q_stride,
+                       const void *k, const int64_t *k_stride, const void *v, const int64_t *v_stride, int dtype,
+                       int B, int n, int key_heads, const float *decay, const int64_t *decay_stride,
+                       const int32_t *counts, float scale, void *out, const int64_t *out_stride, int32_t *status,
+                       void *workspace, size_t workspace_bytes, void *stream);
+int spec_state_attend(const spec_state *from, const void *q, const int64_t *q_stride, const void *k,
+                      const int64_t *k_stride, const void *v, const int64_t *v_stride, int dtype, int B, int N,
+                      int key_heads, const float *decay, const int64_t *decay_stride, const int32_t *parents,
+                      const int32_t *n_query, float scale, void *out, const int64_t *out_stride, int32_t *status,
+                      void *workspace, size_t workspace_bytes, void *stream);
+int spec_state_commit(const spec_state *from, const spec_state *to, const void *k, const int64_t *k_stride,
+                      const void *v, const int64_t *v_stride, int dtype, int B, int n, int key_heads,
+                      const float *decay, const int64_t *decay_stride, const int32_t *index, int index_stride,
+                      int n_rows, const int32_t *counts, int32_t *status, void *stream);
+size_t spec_state_workspace_size(int op, const spec_state *state, int B, int n);
 
 /*
  * spec_workspace_size -- bytes of workspace a call needs.

@@ -22,10 +22,11 @@ LIB_PATH = os.path.join(_HERE, "libspecverify.so")
 
 SPEC_OK, SPEC_EINVAL, SPEC_EDTYPE, SPEC_EWORKSPACE, SPEC_ECUDA = 0, -1, -2, -3, -4
 STATUS_OK, STATUS_TOKEN_RANGE, STATUS_BAD_TREE, STATUS_BAD_LENGTH = 0, 1, 2, 3
-STATUS_BAD_PAGE, STATUS_BAD_INDEX, STATUS_TIMEOUT = 5, 6, 7
+STATUS_BAD_PAGE, STATUS_BAD_INDEX, STATUS_TIMEOUT, STATUS_BAD_SLOT = 5, 6, 7, 8
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 OP_NGRAM, OP_GREEDY, OP_SAMPLE, OP_TREE, OP_DRAW, OP_FILTER = 0, 1, 2, 3, 4, 5
 OP_CACHE_ATTEND, OP_CACHE_WEIGHTS, OP_CACHE_EVICT = 6, 7, 8
+OP_STATE_FORWARD, OP_STATE_ATTEND = 9, 10
 CHAIN_AUTO, CHAIN_TWO_PASS, CHAIN_FUSED, CHAIN_CHUNKED = 0, 1, 2, 3
 TREE_SIBLINGS_WITHOUT_REPLACEMENT = 1
 
@@ -88,6 +89,11 @@ def lib():
         L.spec_cache_evict.argtypes = [P, P, I, P, P, P, I, I, I, P, P, P, P, P, Z, P]
         L.spec_cache_workspace_size.argtypes = [I, P, I, I, I]
         L.spec_cache_workspace_size.restype = Z
+        L.spec_state_forward.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, P, P, P, F, P, P, P, P, Z, P]
+        L.spec_state_attend.argtypes = [P, P, P, P, P, P, P, I, I, I, I, P, P, P, P, F, P, P, P, P, Z, P]
+        L.spec_state_commit.argtypes = [P, P, P, P, P, P, I, I, I, I, P, P, P, I, I, P, P, P]
+        L.spec_state_workspace_size.argtypes = [I, P, I, I]
+        L.spec_state_workspace_size.restype = Z
         _lib = L
         return L
 
@@ -776,4 +782,154 @@ def spec_cache_evict(cache, table: torch.Tensor, cache_len: torch.Tensor, weight
     _with_workspace((_lib or lib()).spec_cache_evict, "spec_cache_evict", OP_CACHE_EVICT, cs, B, keep, 0, dev, ws, st,
                     cs, ds, B, lp, weights.data_ptr(), wst, weights.shape[2], keep, int(recent), kept.data_ptr(),
                     _ptr(o.get("weights")), _lengths(o["new_len"], B, "new_len", dev), _status(o, B, dev))
+    return o
+
+
+# ------------------------------------------------------- linear attention
+
+class _StateStruct(ctypes.Structure):  # struct spec_state
+    _fields_ = [("state", ctypes.c_void_p), ("slot_stride", ctypes.c_int64), ("num_slots", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("key_dim", ctypes.c_int32), ("value_dim", ctypes.c_int32), ("slots", ctypes.c_void_p)]
+
+
+_pack_state = struct.Struct("@PqiiiiP").pack
+
+
+def spec_state_new(slots: int, heads: int, key_dim: int, value_dim: int, device="cuda") -> torch.Tensor:
+    """A pool of states of zeros: fp32 [slots, heads, key_dim, value_dim]."""
+    return torch.zeros((slots, heads, key_dim, value_dim), device=device)
+
+
+def _state_struct(state, slots, B, dims, dev, name):
+    """packed struct spec_state"""
+    H, Dk, Dv = dims
+    if state is None:
+        return _pack_state(0, 0, 0, H, Dk, Dv, 0)
+    if state.dtype is not _F32 or state.get_device() != dev.index:
+        raise TypeError(f"{name} must be a float32 tensor on {dev}")
+    shape, st = state.shape, state.stride()
+    if len(shape) != 4 or shape[1:] != dims or st[3] != 1 or st[2] != Dv or (H > 1 and st[1] != Dk * Dv):
+        raise ValueError(f"{name} must be [slots, {H}, {Dk}, {Dv}], the heads of a slot side by side")
+    return _pack_state(state.data_ptr(), st[0] if shape[0] > 1 else H * Dk * Dv, shape[0], H, Dk, Dv,
+                       0 if slots is None else _lengths(slots, B, "slots", dev))
+
+
+def _state_rows(k, v, decay, dev):
+    """Checks of the rows that every call has -> (dtype code, k's strides, v's strides, decay's strides)"""
+    code, kst = _rows(k, "k", dev, (DTYPE_BF16, DTYPE_F16))
+    vcode, vst = _rows(v, "v", dev, (DTYPE_BF16, DTYPE_F16))
+    B, n, H, _ = v.shape
+    if vcode != code or k.shape[:2] != (B, n):
+        raise ValueError("k and v must be rows of the same tokens, of one dtype")
+    if decay.dtype is not _F32 or decay.get_device() != dev.index or decay.shape != (B, n, H):
+        raise TypeError(f"decay must be a float32 {[B, n, H]} tensor on {dev}")
+    return code, kst, vst, _pack3(*decay.stride())
+
+
+def _state_out(o, q, v, code, dev):
+    """Strides of the outputs [B, n, heads, value_dim]."""
+    if o["out"].shape != v.shape:
+        raise ValueError("out must have v's shape")
+    return _rows(o["out"], "out", dev, (code,))[1]
+
+
+def _state_pools(state, slots, dst, dst_slots, B, dims, dev):
+    """The states before and after: in place unless dst is given."""
+    if dst is None and dst_slots is not None:
+        if state is None:
+            raise ValueError("dst_slots without a state to write")
+        dst = state
+    elif dst is None:
+        dst, dst_slots = state, slots
+    return _state_struct(state, slots, B, dims, dev, "state"), None if dst is None else _state_struct(dst, dst_slots, B, dims, dev, "dst")
+
+
+def spec_state_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.Tensor, state, *, slots=None, dst=None,
+                       dst_slots=None, counts=None, scale=None, write: bool = True, out=None, ws=None, stream=None) -> dict:
+    """Linear attention S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = scale q_t^T S_t over the tokens of q, k [B, n, key_heads, key_dim]
+    and v [B, n, heads, value_dim] (bf16 or fp16) with decay g, fp32 [B, n, heads]: n of them, or counts int32 [B].
+    state: fp32 [slots, heads, key_dim, value_dim] (spec_state_new), of which request b has slot b, or slots int32 [B] (-1: a
+    state of zeros); None: zeros, whatever slots says.  The states after go to dst (its slots: dst_slots), by default to the same slots of state; with
+    write=False nowhere.  scale: key_dim ** -0.5 by default.
+    -> out (as v; rows past a count are 0), status.  ws: as in spec_cache_attend."""
+    dev = q.device
+    if stream is not None:
+        return _on_stream(stream, spec_state_forward, q, k, v, decay, state, slots=slots, dst=dst, dst_slots=dst_slots, counts=counts,
+                          scale=scale, write=write, out=out, ws=ws)
+    st = _raw_stream(dev)
+    code, kst, vst, gst = _state_rows(k, v, decay, dev)
+    qcode, qst = _rows(q, "q", dev, (code,))
+    B, n, Hk, Dk = q.shape
+    if k.shape != q.shape:
+        raise ValueError("q and k must have one shape")
+    before, after = _state_pools(state, slots, dst, dst_slots, B, (v.shape[2], Dk, v.shape[3]), dev)
+    if write and after is None:
+        raise ValueError("no state to write: give dst, or write=False")
+    cp = None if counts is None else _lengths(counts, B, "counts", dev)
+    o = out or dict(out=torch.empty(v.shape, dtype=v.dtype, device=dev), status=torch.empty(B, dtype=torch.int32, device=dev))
+    ost = _state_out(o, q, v, code, dev)
+    _state_call((_lib or lib()).spec_state_forward, "spec_state_forward", OP_STATE_FORWARD, before, B, n, dev, ws, st,
+                before, after if write else None, q.data_ptr(), qst, k.data_ptr(), kst, v.data_ptr(), vst, code, B, n, Hk,
+                decay.data_ptr(), gst, cp, Dk ** -0.5 if scale is None else float(scale), o["out"].data_ptr(), ost, _status(o, B, dev))
+    return o
+
+
+def spec_state_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.Tensor, state, *, slots=None, parents=None,
+                      n_query=None, scale=None, out=None, ws=None, stream=None) -> dict:
+    """The outputs of N drafted rows behind each request's state, which stays as it is: a chain, or with parents int32 [B, N]
+    (spec_tree_rerank's sel_parents, spec_verify_tree's parents) a tree, whose row i follows row parents[b, i].  n_query int32
+    [B]: rows of a request (default N).  The rest as in spec_state_forward -> out, status."""
+    dev = q.device
+    if stream is not None:
+        return _on_stream(stream, spec_state_attend, q, k, v, decay, state, slots=slots, parents=parents, n_query=n_query,
+                          scale=scale, out=out, ws=ws)
+    st = _raw_stream(dev)
+    code, kst, vst, gst = _state_rows(k, v, decay, dev)
+    qcode, qst = _rows(q, "q", dev, (code,))
+    B, n, Hk, Dk = q.shape
+    if k.shape != q.shape:
+        raise ValueError("q and k must have one shape")
+    before = _state_pools(state, slots, None, None, B, (v.shape[2], Dk, v.shape[3]), dev)[0]
+    if parents is not None and (parents.dtype is not _I32 or parents.get_device() != dev.index or parents.shape != (B, n) or
+                                not parents.is_contiguous()):
+        raise TypeError(f"parents must be a contiguous int32 {[B, n]} tensor on {dev}")
+    np_ = None if n_query is None else _lengths(n_query, B, "n_query", dev)
+    o = out or dict(out=torch.empty(v.shape, dtype=v.dtype, device=dev), status=torch.empty(B, dtype=torch.int32, device=dev))
+    ost = _state_out(o, q, v, code, dev)
+    _state_call((_lib or lib()).spec_state_attend, "spec_state_attend", OP_STATE_ATTEND, before, B, n, dev, ws, st,
+                before, q.data_ptr(), qst, k.data_ptr(), kst, v.data_ptr(), vst, code, B, n, Hk, decay.data_ptr(), gst,
+                _ptr(parents), np_, Dk ** -0.5 if scale is None else float(scale), o["out"].data_ptr(), ost, _status(o, B, dev))
+    return o
+
+
+def _state_call(fn, what, op, before, B, n, dev, ws, stream, *args):
+    """As _with_workspace."""
+    with _stream_lock(dev.index, stream):
+        have = ws if ws is not None else _workspaces.get((dev.index, stream))
+        p, size = (None, 0) if have is None else (have.data_ptr(), have.numel())
+        rc = _on(dev, fn, *args, p, size, stream)
+        if rc == SPEC_EWORKSPACE and ws is None:
+            have = _workspace(_on(dev, lib().spec_state_workspace_size, op, before, B, n), dev, stream)
+            rc = _on(dev, fn, *args, have.data_ptr(), have.numel(), stream)
+    _check(rc, what)
+
+
+def spec_state_commit(k: torch.Tensor, v: torch.Tensor, decay: torch.Tensor, state, *, slots=None, dst=None, dst_slots=None,
+                      counts=None, index=None, out=None, stream=None) -> dict:
+    """Advances each request's state by rows of k, v and decay: all of them, or counts int32 [B]; with index int32 [B, rows], row
+    i is token index[b, i] (the accepted path: index = path_nodes, counts = n_emit of a verify call).  The states as in
+    spec_state_forward -> status."""
+    dev = k.device
+    if stream is not None:
+        return _on_stream(stream, spec_state_commit, k, v, decay, state, slots=slots, dst=dst, dst_slots=dst_slots, counts=counts,
+                          index=index, out=out)
+    st = _raw_stream(dev)
+    code, kst, vst, gst = _state_rows(k, v, decay, dev)
+    B, n, Hk, Dk = k.shape
+    before, after = _state_pools(state, slots, dst, dst_slots, B, (v.shape[2], Dk, v.shape[3]), dev)
+    ip, ist, rows = _index_rows(index, counts, B, n, dev)
+    o = out or dict(status=torch.empty(B, dtype=torch.int32, device=dev))
+    rc = _on(dev, (_lib or lib()).spec_state_commit, before, after, k.data_ptr(), kst, v.data_ptr(), vst, code, B, n, Hk,
+             decay.data_ptr(), gst, ip, ist, rows, _ptr(counts), _status(o, B, dev), st)
+    _check(rc, "spec_state_commit")
     return o

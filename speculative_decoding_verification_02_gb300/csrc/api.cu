@@ -238,6 +238,7 @@ const char *spec_status_string(int code) {
     case 100 + SPEC_STATUS_BAD_PAGE: return "request has a cache page outside the pool";
     case 100 + SPEC_STATUS_BAD_INDEX: return "request has a row index outside the rows";
     case 100 + SPEC_STATUS_TIMEOUT: return "a wait inside a kernel ran out";
+    case 100 + SPEC_STATUS_BAD_SLOT: return "request has a slot outside the pool of states";
     default: return "unknown code";
   }
 }

@@ -1,0 +1,98 @@
+// Shared parts of the linear-attention kernels: the pool of states, the
+// parameter blocks, packed arithmetic.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "spec_verify.h"
+
+namespace sv {
+
+struct StatePool {
+  float *state;  // null: states of zeros (read), or none to write
+  int64_t slot_stride;
+  int num_slots;
+  const int32_t *slots;
+};
+
+struct StateParams {
+  StatePool from, to;
+  int heads, key_heads, group, key_dim, value_dim;  // group: state heads to a key head
+  const char *q, *k, *v;
+  char *out;
+  int64_t qs[3], ks[3], vs[3], os[3], gs[3];  // element strides: request, token, head
+  int dtype, B, n, n_rows, index_stride;
+  const float *decay;
+  const int32_t *counts, *parents, *index;
+  float scale;
+  int32_t *status;
+  bool vec;  // rows of q, k, v and out start on 16-byte boundaries
+};
+
+// A launch of the kernels for a few rows: chains (q given: with outputs), commits (q null), trees (parents given).
+cudaError_t launch_state_rows(const StateParams &P, cudaStream_t st);
+
+#ifdef __CUDACC__
+
+// Slot of request b, -1 for a state of zeros; ok is false when there is none.
+__device__ __forceinline__ int state_slot(const StatePool &p, int b, bool may_lack, bool &ok) {
+  if (!p.state) return -1;
+  const int s = p.slots ? p.slots[b] : b;
+  if (s >= p.num_slots || s < (may_lack ? -1 : 0)) ok = false;
+  return s;
+}
+
+// Two fp32 values to a register pair, and arithmetic on both at once.
+using pair_t = unsigned long long;
+__device__ __forceinline__ pair_t pack2(float a, float b) {
+  pair_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(pair_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c) {
+  pair_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b) {
+  pair_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ pair_t add2(pair_t a, pair_t b) {
+  pair_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Two values of a row in one word to fp32, exactly.
+template <int DT>
+__device__ __forceinline__ float2 widen2(uint32_t w) {
+  if constexpr (DT == SPEC_DTYPE_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+template <int DT>
+__device__ __forceinline__ float widen(uint16_t w) {
+  if constexpr (DT == SPEC_DTYPE_BF16) return __uint_as_float(static_cast<uint32_t>(w) << 16);
+  else return __half2float(__ushort_as_half(w));
+}
+// Rounded once, to nearest even.
+template <int DT>
+__device__ __forceinline__ uint16_t narrow(float x) {
+  if constexpr (DT == SPEC_DTYPE_BF16) return __bfloat16_as_ushort(__float2bfloat16(x));
+  else return __half_as_ushort(__float2half(x));
+}
+
+#endif
+
+}  // namespace sv
