@@ -24,7 +24,8 @@ LIB = os.path.join(HERE, "libspecverify.so")
 SOURCES = ["api.cu", "chain.cu", "chain_fused.cu", "filter.cu", "tree.cu", "rerank.cu", "ngram.cu", "noalloc.cu",
            "host_analysis.cu", "cache_api.cu", "cache_append.cu", "cache_attend.cu", "cache_attend_bf16.cu",
            "cache_attend_f16.cu", "cache_weights.cu",
-           "cache_evict.cu", "state_api.cu", "state_rows.cu"]
+           "cache_evict.cu", "state_api.cu", "state_rows.cu", "state_chunk.cu",
+           "state_chunk_bf16.cu", "state_chunk_f16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++20", "-Xcompiler", "-fPIC", "-I" + INCLUDE,
                      "-I" + CSRC]

@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -33,6 +34,30 @@ struct StateParams {
   int32_t *status;
   bool vec;  // rows of q, k, v and out start on 16-byte boundaries
 };
+
+// A call of the tensor-core kernels: each request's chunks cut into segs runs, the states before all but the first of them from
+// a launch of their own.
+struct StateChunkPlan {
+  StateParams p;
+  int segs, launch_segs;
+  int *verdict;   // [B] the requests' status
+  float *total;   // [B][heads][segs] the decay over a segment
+  float *local;   // [B][heads][segs][key_dim][value_dim] what a segment adds to zeros; then the state before it
+};
+
+// Whether the states written lie where some are read: such a call is not the same call when it is made again.
+inline bool state_overlaps(const StateParams &P) {
+  if (!P.from.state || !P.to.state) return false;
+  const float *a = P.from.state, *b = P.to.state;
+  return a < b + P.to.num_slots * P.to.slot_stride && b < a + P.from.num_slots * P.from.slot_stride;
+}
+
+// Whether the tensor-core kernels take a call, from its sizes and layout; the workspace that they need (for any layout).
+bool state_on_tensor_cores(const StateParams &P);
+size_t state_chunk_workspace(const StateParams &P);
+cudaError_t launch_state_chunks(const StateParams &P, void *workspace, cudaStream_t st);
+cudaError_t launch_state_chunk_bf16(const StateChunkPlan &A, bool outputs, const CUtensorMap *maps, cudaStream_t st);
+cudaError_t launch_state_chunk_f16(const StateChunkPlan &A, bool outputs, const CUtensorMap *maps, cudaStream_t st);
 
 // A launch of the kernels for a few rows: chains (q given: with outputs), commits (q null), trees (parents given).
 cudaError_t launch_state_rows(const StateParams &P, cudaStream_t st);
@@ -87,6 +112,13 @@ __device__ __forceinline__ float widen(uint16_t w) {
   else return __half2float(__ushort_as_half(w));
 }
 // Rounded once, to nearest even.
+template <int DT>
+__device__ __forceinline__ uint32_t narrow2(float2 x) {
+  uint32_t r;
+  if constexpr (DT == SPEC_DTYPE_BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x.y), "f"(x.x));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x.y), "f"(x.x));
+  return r;
+}
 template <int DT>
 __device__ __forceinline__ uint16_t narrow(float x) {
   if constexpr (DT == SPEC_DTYPE_BF16) return __bfloat16_as_ushort(__float2bfloat16(x));

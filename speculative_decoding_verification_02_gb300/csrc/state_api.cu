@@ -75,6 +75,13 @@ int check_call(StateParams &P, const spec_state *from, const spec_state *to, con
   return SPEC_OK;
 }
 
+int run(const StateParams &P, void *workspace, size_t workspace_bytes, void *stream, const char *what) {
+  const bool chunks = state_on_tensor_cores(P);
+  if (chunks && (!workspace || workspace_bytes < state_chunk_workspace(P) || !on_grain(workspace, 256))) return SPEC_EWORKSPACE;
+  const cudaError_t e = chunks ? launch_state_chunks(P, workspace, stream_of(stream)) : launch_state_rows(P, stream_of(stream));
+  return e == cudaSuccess ? SPEC_OK : state_fail(e, what);
+}
+
 }  // namespace
 }  // namespace sv
 
@@ -83,8 +90,11 @@ using namespace sv;
 extern "C" {
 
 size_t spec_state_workspace_size(int op, const spec_state *state, int B, int n) {
-  (void)op, (void)state, (void)B, (void)n;
-  return 0;
+  if (check_geometry(state) != SPEC_OK || B < 0 || n < 0) return 0;
+  if (op != SPEC_OP_STATE_FORWARD && (op != SPEC_OP_STATE_ATTEND || n > SPEC_MAX_NODES)) return 0;
+  StateParams P{};
+  P.B = B, P.n = n, P.heads = state->heads, P.key_dim = state->key_dim, P.value_dim = state->value_dim;
+  return state_chunk_workspace(P);
 }
 
 int spec_state_forward(const spec_state *from, const spec_state *to, const void *q, const int64_t *q_stride,
@@ -99,9 +109,7 @@ int spec_state_forward(const spec_state *from, const spec_state *to, const void 
   if (!std::isfinite(scale)) return SPEC_EINVAL;
   if (B == 0) return SPEC_OK;
   P.counts = counts, P.scale = scale, P.status = status;
-  (void)workspace, (void)workspace_bytes;
-  const cudaError_t e = launch_state_rows(P, stream_of(stream));
-  return e == cudaSuccess ? SPEC_OK : state_fail(e, "spec_state_forward");
+  return run(P, workspace, workspace_bytes, stream, "spec_state_forward");
 }
 
 int spec_state_attend(const spec_state *from, const void *q, const int64_t *q_stride, const void *k,
@@ -116,9 +124,7 @@ int spec_state_attend(const spec_state *from, const void *q, const int64_t *q_st
   if (!std::isfinite(scale) || N > SPEC_MAX_NODES) return SPEC_EINVAL;
   if (B == 0) return SPEC_OK;
   P.counts = n_query, P.parents = parents, P.scale = scale, P.status = status;
-  (void)workspace, (void)workspace_bytes;
-  const cudaError_t e = launch_state_rows(P, stream_of(stream));
-  return e == cudaSuccess ? SPEC_OK : state_fail(e, "spec_state_attend");
+  return run(P, workspace, workspace_bytes, stream, "spec_state_attend");
 }
 
 int spec_state_commit(const spec_state *from, const spec_state *to, const void *k, const int64_t *k_stride,

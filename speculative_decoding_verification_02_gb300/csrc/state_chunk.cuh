@@ -1,0 +1,789 @@
+// Linear attention over states on the tensor cores: prompts, and drafted rows
+// and trees of up to 64 nodes.
+#pragma once
+
+#include <algorithm>
+#include <atomic>
+
+#include "cache.cuh"
+#include "launch.h"
+#include "state.cuh"
+#include "tcgen05.cuh"
+
+namespace sv {
+namespace {
+
+// A CTA has one state head of one request, 128 columns of value_dim (lanes of
+// tensor memory) and a run of chunks of 64 tokens.  With G the running sum of
+// the decays within a chunk, everything is held transposed, a lane to a column
+// of value_dim:
+//   O1 = S^T Q^T            [dv x i]   S as two pieces of 16 bits in tensor memory, Q as it came
+//   P  = Q K^T              [i x j]
+//   A  = P e^{G_i - G_j}, 0 where row i does not follow row j, as two pieces in shared memory
+//   O2 = V^T A^T            [dv x i]   V as it came
+//   dS = V^T K'             [dv x dk]  K' = e^{G_last - G_j} k_j as two pieces in shared memory
+//   out_i = scale (e^{G_i} O1_i + O2_i),   S <- e^{G_last} S + dS
+// S itself stays in fp32 registers; what a product takes of it, of A and of
+// K' is the sum of two pieces of the rows' type, off by 2^-18 of a value at
+// most in bf16 and 2^-22 in fp16, whose pieces are scaled by powers of two (a lane
+// of S, a row of A, a chunk's K') to stay within its range.
+//
+// e^{G_i - G_j} is taken from differences, of running sums held in 64 bits and
+// handed on as a multiple of 1/8 and a rest, so that a difference of large sums
+// is as exact as one of small ones.
+//
+// Warps (their number modulo 4 is the quarter of the lanes that they can reach,
+// and their scheduler): 2 loads, 3 decays, 10 issues P, O1 and O2, 11 issues dS;
+// 4, 5, 8, 9 make A; 0, 1, 6, 7 make K' (two chunks ahead) and write the
+// outputs; 12 to 19 hold S.
+//
+// A long prompt of few heads is cut into segments: a first launch (OUT false)
+// computes what each but the last adds to a state of zeros, state_join_kernel
+// turns that into the state before each, and the main launch has a CTA for
+// every segment.
+constexpr int kChunk = 64;
+constexpr int kChunkThreads = 640;
+constexpr int kDecayRing = 4;
+
+template <int DK, bool OUT>
+struct ChunkShape {
+  static constexpr int kHalf = kChunk * 128;  // bytes of 64 columns of a tile
+  static constexpr int kTileK = DK / 64 * kHalf, kTileV = 2 * kHalf;
+  static constexpr int kStagesK = OUT ? (DK == 128 ? 2 : 4) : 4;
+  static constexpr int kStagesQ = OUT ? (DK == 128 ? 3 : 4) : 0;
+  static constexpr int kStagesV = OUT ? (DK == 128 ? 3 : 4) : 4;
+  static constexpr int kK = 0;
+  static constexpr int kQ = kK + kStagesK * kTileK;
+  static constexpr int kV = kQ + kStagesQ * kTileK;  // (P's product reads 64 rows past a half of Q: of Q, or of V)
+  static constexpr int kKt = kV + kStagesV * kTileV;
+  static constexpr int kA = kKt + 2 * 2 * kTileK;
+  static constexpr int kSmall = kA + (OUT ? 2 * kHalf : 0);
+  static constexpr int kBytes = kSmall + 12288 + 1024;  // (1024: alignment of the base)
+};
+
+struct ChunkSmall {
+  struct alignas(16) Decays {
+    float nhi[kChunk], nlo[kChunk];  // minus the running sum in units of log 2: multiples of 1/8, rest
+    float ei[kChunk];                // scale e^{G_i}
+    float left[kChunk];              // e^{G_last - G_j}, 0 past the request's rows
+    float afac[kChunk];              // scale, times what row i of A was divided by
+    float sfac[128];                 // fp16: what a lane of S was divided by
+    float lam;                       // e^{G_last}
+    float kfac;                      // fp16: what K' was divided by
+  } d[kDecayRing];
+  uint32_t follows[kChunk][2];  // trees: the rows that a row follows, itself among them
+  uint32_t smax[2][2][128], amax[2][2][kChunk], kmax[2][4];  // (by the chunk's number: the next one's may be written before these are read)
+  uint64_t k_full[4], k_empty[4], q_full[4], q_empty[4], v_full[4], v_empty[4];
+  uint64_t kt_full[2], kt_empty[2], p_full[2], p_empty[2], a_full, a_empty, ds_full, ds_empty, s_full, s_empty, o_full, o_empty;
+  uint64_t dec_full[kDecayRing], dec_empty[kDecayRing], meet_s, meet_a, meet_k;
+  uint32_t tmem;
+  int dead;
+  int copies_k, copies_q, copies_v, products_p, products_o1, products_o2, products_s;  // how many were begun
+};
+static_assert(sizeof(ChunkSmall) <= 12288);
+
+// Arrival of a warp whose lanes have all done what the barrier stands for.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
+  __syncwarp();
+  if (lane == 0) bar_arrive(bar);
+}
+
+// The rows' type: code in an instruction descriptor (fp16 0, bf16 1).
+template <int DT>
+__device__ __forceinline__ constexpr uint32_t rows_desc(int n, bool a_mn, bool b_mn) {
+  return mma_desc(n, b_mn) | (DT == SPEC_DTYPE_BF16 ? 1u << 7 | 1u << 10 : 0u) | (a_mn ? 1u << 15 : 0u);
+}
+
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+
+__device__ __forceinline__ void tensor_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Two values rounded to the rows' type, and the same rounding of what that left out.
+template <int DT>
+__device__ __forceinline__ void split2(pair_t x, uint32_t &hi, uint32_t &lo) {
+  hi = narrow2<DT>(unpack2(x));
+  const float2 h = widen2<DT>(hi);
+  lo = narrow2<DT>(unpack2(fma2(pack2(h.x, h.y), pack2(-1.0f, -1.0f), x)));
+}
+
+// The power of two that brings a largest magnitude (as bits) to [2^14, 2^15), and its inverse; 1 for zero, infinities and NaN.
+__device__ __forceinline__ float fit_half(uint32_t amax, float &back) {
+  const int e = static_cast<int>(amax >> 23) - 127;
+  const int s = amax == 0 || e == 128 ? 0 : max(-112, min(112, 14 - e));
+  back = __uint_as_float(static_cast<uint32_t>(127 - s) << 23);
+  return __uint_as_float(static_cast<uint32_t>(127 + s) << 23);
+}
+
+// Row i's weight for row j without what P held: e^{G_i - G_j} from the handed-on parts.
+__device__ __forceinline__ float between(const ChunkSmall::Decays &d, int i, int j) {
+  return ex2((d.nhi[j] - d.nhi[i]) + (d.nlo[j] - d.nlo[i]));
+}
+
+// A row's sum over the rows that it follows, taken again from memory without
+// those that it does not: where a value of theirs is infinite or NaN, the
+// product of a weight of 0 is not 0.  A warp: lane = column of value_dim.
+template <int DT>
+__device__ __noinline__ float row_again(const StateParams &P, const ChunkSmall::Decays &d, uint64_t sees, int b, int h, int t0, int i, int col) {
+  const int hk = h / P.group, lane = threadIdx.x & 31;
+  const uint16_t *q = reinterpret_cast<const uint16_t *>(P.q) + b * P.qs[0] + (t0 + i) * P.qs[1] + hk * P.qs[2];
+  float sum = 0.0f;
+  for (int j = 0; j <= i; ++j) {
+    if (!(sees >> j & 1)) continue;
+    const uint16_t *k = reinterpret_cast<const uint16_t *>(P.k) + b * P.ks[0] + (t0 + j) * P.ks[1] + hk * P.ks[2];
+    float s = 0.0f;
+    for (int e = lane; e < P.key_dim; e += 32) s = fmaf(widen<DT>(q[e]), widen<DT>(k[e]), s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+    if (col < P.value_dim) {
+      const uint16_t *v = reinterpret_cast<const uint16_t *>(P.v) + b * P.vs[0] + (t0 + j) * P.vs[1] + h * P.vs[2];
+      sum = fmaf(s * between(d, i, j), widen<DT>(v[col]), sum);
+    }
+  }
+  return sum;
+}
+
+// Waits for every copy and product that the CTA began.
+template <int DK, bool OUT>
+__device__ __noinline__ void land_chunks(ChunkSmall &sm) {
+  using S = ChunkShape<DK, OUT>;
+  ring_land(sm.k_full, S::kStagesK, sm.copies_k);
+  if (OUT) ring_land(sm.q_full, S::kStagesQ, sm.copies_q);
+  ring_land(sm.v_full, S::kStagesV, sm.copies_v);
+  ring_land(sm.p_full, 2, sm.products_p);
+  ring_land(&sm.s_empty, 1, sm.products_o1);
+  ring_land(&sm.o_full, 1, sm.products_o2);
+  ring_land(&sm.ds_full, 1, sm.products_s);
+}
+
+template <int DT, int DK, bool OUT>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    state_chunk_kernel(const StateChunkPlan A, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                       const __grid_constant__ CUtensorMap v_map) {
+  using S = ChunkShape<DK, OUT>;
+  constexpr bool F16 = DT == SPEC_DTYPE_F16;
+  constexpr uint32_t kDS = 0, kSHi = 128, kSLo = 192, kO1 = 256, kO2 = 320, kP = 384;  // tensor memory; P twice
+  extern __shared__ char raw[];
+  char *const smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  ChunkSmall &sm = *reinterpret_cast<ChunkSmall *>(smem + S::kSmall);
+  const StateParams &P = A.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // ---- the unit: heads next to one another share keys, so they run side by side
+  const int blocks = (P.value_dim + 127) >> 7;
+  int u = blockIdx.x;
+  const int h = u % P.heads;
+  u /= P.heads;
+  const int dv0 = u % blocks * 128;
+  u /= blocks;
+  const int seg = u % A.launch_segs, b = u / A.launch_segs;
+  const int hk = h / P.group;
+  const bool ok = A.verdict[b] == SPEC_STATUS_OK;
+  const int len = ok ? (P.counts ? P.counts[b] : P.n) : 0;
+  const int all = (len + kChunk - 1) / kChunk;
+  const int c0 = static_cast<int>(static_cast<int64_t>(all) * seg / A.segs);
+  const int chunks = static_cast<int>(static_cast<int64_t>(all) * (seg + 1) / A.segs) - c0;
+  const bool last_seg = seg + 1 == A.segs;
+  // (a chunk's state is needed by the next, and by whoever reads the state written)
+  const bool writes = OUT ? last_seg && P.to.state && ok : true;
+  const int updates = writes ? chunks : max(chunks - 1, 0);
+
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) {
+      bar_init(&sm.k_full[i], 1), bar_init(&sm.k_empty[i], OUT ? 5 : 4);
+      bar_init(&sm.q_full[i], 1), bar_init(&sm.q_empty[i], 1);
+      bar_init(&sm.v_full[i], 1), bar_init(&sm.v_empty[i], OUT ? 2 : 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&sm.kt_full[i], 4), bar_init(&sm.kt_empty[i], 1);
+      bar_init(&sm.p_full[i], 1), bar_init(&sm.p_empty[i], 4);
+    }
+    bar_init(&sm.a_full, 4), bar_init(&sm.a_empty, 1);
+    bar_init(&sm.ds_full, 1), bar_init(&sm.ds_empty, 8);
+    bar_init(&sm.s_full, 8), bar_init(&sm.s_empty, 1);
+    bar_init(&sm.o_full, 1), bar_init(&sm.o_empty, 4);
+    for (int i = 0; i < kDecayRing; ++i) bar_init(&sm.dec_full[i], 1), bar_init(&sm.dec_empty[i], OUT ? 16 : 12);
+    bar_init(&sm.meet_s, 8), bar_init(&sm.meet_a, 4), bar_init(&sm.meet_k, 4);
+    bar_init_fence();
+    sm.dead = 0;
+    sm.copies_k = sm.copies_q = sm.copies_v = sm.products_p = sm.products_o1 = sm.products_o2 = sm.products_s = 0;
+  }
+  if (warp == 10) tmem_alloc(&sm.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  volatile int *dead = &sm.dead;
+
+  if (warp == 2) {
+    // ---- loading
+    int c = 0, kc = 0, qc = 0, vc = 0;
+    for (; c < chunks; ++c) {
+      const int t0 = (c0 + c) * kChunk;
+      const int sk = c % S::kStagesK, sv = c % S::kStagesV;
+      if (c >= S::kStagesK && !warp_wait(&sm.k_empty[sk], (c / S::kStagesK - 1) & 1, dead)) break;
+      if (lane == 0) {
+        bar_expect(&sm.k_full[sk], S::kTileK);
+        for (int e = 0; e < DK / 64; ++e)
+          tensor_load_4d(smem + S::kK + sk * S::kTileK + e * S::kHalf, &k_map, e * 64, hk, t0, b, &sm.k_full[sk]);
+      }
+      ++kc;
+      if constexpr (OUT) {
+        const int sq = c % S::kStagesQ;
+        if (c >= S::kStagesQ && !warp_wait(&sm.q_empty[sq], (c / S::kStagesQ - 1) & 1, dead)) break;
+        if (lane == 0) {
+          bar_expect(&sm.q_full[sq], S::kTileK);
+          for (int e = 0; e < DK / 64; ++e)
+            tensor_load_4d(smem + S::kQ + sq * S::kTileK + e * S::kHalf, &q_map, e * 64, hk, t0, b, &sm.q_full[sq]);
+        }
+        ++qc;
+      }
+      if (c >= S::kStagesV && !warp_wait(&sm.v_empty[sv], (c / S::kStagesV - 1) & 1, dead)) break;
+      if (lane == 0) {
+        bar_expect(&sm.v_full[sv], S::kTileV);
+        for (int e = 0; e < 2; ++e)
+          tensor_load_4d(smem + S::kV + sv * S::kTileV + e * S::kHalf, &v_map, dv0 + e * 64, h, t0, b, &sm.v_full[sv]);
+      }
+      ++vc;
+      __syncwarp();
+    }
+    if (lane == 0) sm.copies_k = kc, sm.copies_q = qc, sm.copies_v = vc;
+  } else if (warp == 3) {
+    // ---- decays: two tokens to a lane
+    const float *gp = P.decay + b * P.gs[0] + h * P.gs[2];
+    double sum = 0.0;
+    auto fetch = [&](int c, float &x0, float &x1) {
+      const int t = (c0 + c) * kChunk + lane;
+      x0 = c < chunks && t < len ? gp[t * P.gs[1]] : 0.0f;
+      x1 = c < chunks && t + 32 < len ? gp[(t + 32) * P.gs[1]] : 0.0f;
+    };
+    float x0, x1;
+    fetch(0, x0, x1);
+    for (int c = 0; c < chunks; ++c) {
+      const int r = c % kDecayRing, t0 = (c0 + c) * kChunk;
+      const int m = min(kChunk, len - t0);
+      // (a factor below 2^-173 is 0 in fp32 whatever it multiplies; NaN stays)
+      double g0 = x0 < -120.0f ? -120.0f : x0, g1 = x1 < -120.0f ? -120.0f : x1;
+      float own[2] = {x0, x1};
+      fetch(c + 1, x0, x1);
+      if (OUT && P.parents) {  // the sums over each row's path, and which rows lie on it
+        const int32_t *parents = P.parents + static_cast<int64_t>(b) * P.n;
+        for (int e = 0; e < 2; ++e) {
+          const int i = lane + 32 * e;
+          uint32_t bits[2] = {0, 0};
+          double path = 0.0;
+          if (i < m) {
+            for (int p = i; p >= 0; p = parents[p]) {
+              const float y = p == i ? own[e] : gp[p * P.gs[1]];
+              path += y < -120.0f ? -120.0f : y;
+              bits[p >> 5] |= 1u << (p & 31);
+            }
+          }
+          sm.follows[i][0] = bits[0], sm.follows[i][1] = bits[1];
+          (e ? g1 : g0) = path;
+        }
+      } else {
+        for (int o = 1; o < 32; o <<= 1) {
+          const double y0 = __shfl_up_sync(~0u, g0, o), y1 = __shfl_up_sync(~0u, g1, o);
+          if (lane >= o) g0 += y0, g1 += y1;
+        }
+        g1 += __shfl_sync(~0u, g0, 31);
+      }
+      const double total = __shfl_sync(~0u, g1, 31);
+      sum += total;
+      if (c >= kDecayRing && !warp_wait(&sm.dec_empty[r], (c / kDecayRing - 1) & 1, dead)) break;
+      ChunkSmall::Decays &d = sm.d[r];
+      for (int e = 0; e < 2; ++e) {
+        const double g = e ? g1 : g0, y = g * 1.4426950408889634074;
+        const float hi = rintf(static_cast<float>(y) * 8.0f) * 0.125f;
+        const int i = lane + 32 * e;
+        d.nhi[i] = -hi;
+        d.nlo[i] = static_cast<float>(hi - y);
+        d.ei[i] = expf(static_cast<float>(g)) * P.scale;
+        d.left[i] = i < m ? expf(static_cast<float>(total - g)) : 0.0f;
+        d.afac[i] = P.scale;
+      }
+      if (lane == 0) d.lam = expf(static_cast<float>(total)), d.kfac = 1.0f;
+      warp_arrive(&sm.dec_full[r], lane);
+    }
+    if (!OUT && lane == 0 && dv0 == 0) A.total[(static_cast<int64_t>(b) * P.heads + h) * A.segs + seg] = static_cast<float>(exp(sum));
+  } else if (warp == 10) {
+    // ---- issuing P, O1, O2
+    if constexpr (OUT) {
+      constexpr uint32_t kIdP = rows_desc<DT>(kChunk, false, false), kIdO2 = rows_desc<DT>(kChunk, true, false);
+      const uint64_t q_desc = matrix_desc(smem_u32(smem + S::kQ), 16, 1024, kSwizzle128);
+      const uint64_t k_desc = matrix_desc(smem_u32(smem + S::kK), 16, 1024, kSwizzle128);
+      const uint64_t v_desc = matrix_desc(smem_u32(smem + S::kV), S::kHalf, 1024, kSwizzle128);
+      const uint64_t a_desc = matrix_desc(smem_u32(smem + S::kA), 16, 1024, kSwizzle128);
+      int np = 0, n1 = 0, n2 = 0;
+      auto issue_p = [&](int c) -> bool {
+        const int sk = c % S::kStagesK, sq = c % S::kStagesQ;
+        if (c >= 2 && !warp_wait(&sm.p_empty[c & 1], (c / 2 - 1) & 1, dead)) return false;
+        if (!warp_wait(&sm.k_full[sk], (c / S::kStagesK) & 1, dead)) return false;
+        if (!warp_wait(&sm.q_full[sq], (c / S::kStagesQ) & 1, dead)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < DK / 16; ++k)
+            mma_f16_ss(tmem + kP + (c & 1) * 64, q_desc + ((sq * S::kTileK + k / 4 * S::kHalf + k % 4 * 32) >> 4),
+                       k_desc + ((sk * S::kTileK + k / 4 * S::kHalf + k % 4 * 32) >> 4), kIdP, k > 0);
+          tc_commit(&sm.k_empty[sk]);
+          tc_commit(&sm.p_full[c & 1]);
+        }
+        __syncwarp();
+        ++np;
+        return true;
+      };
+      if (chunks > 0 && issue_p(0)) {
+        for (int c = 0; c < chunks; ++c) {
+          const int sq = c % S::kStagesQ, sv = c % S::kStagesV;
+          if (!warp_wait(&sm.s_full, c & 1, dead)) break;
+          if (c > 0 && !warp_wait(&sm.o_empty, (c - 1) & 1, dead)) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+              for (int k = 0; k < DK / 16; ++k)
+                mma_f16_ta(tmem + kO1, tmem + (piece ? kSLo : kSHi) + k * 8, q_desc + ((sq * S::kTileK + k / 4 * S::kHalf + k % 4 * 32) >> 4),
+                           kIdP, piece + k > 0);
+            tc_commit(&sm.q_empty[sq]);
+            tc_commit(&sm.s_empty);
+          }
+          __syncwarp();
+          ++n1;
+          if (c + 1 < chunks && !issue_p(c + 1)) break;
+          if (!warp_wait(&sm.v_full[sv], (c / S::kStagesV) & 1, dead)) break;
+          if (!warp_wait(&sm.a_full, c & 1, dead)) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+              for (int k = 0; k < kChunk / 16; ++k)
+                mma_f16_ss(tmem + kO2, v_desc + ((sv * S::kTileV + k * 2048) >> 4), a_desc + ((piece * S::kHalf + k * 32) >> 4), kIdO2,
+                           piece + k > 0);
+            tc_commit(&sm.v_empty[sv]);
+            tc_commit(&sm.a_empty);
+            tc_commit(&sm.o_full);
+          }
+          __syncwarp();
+          ++n2;
+        }
+      }
+      if (lane == 0) sm.products_p = np, sm.products_o1 = n1, sm.products_o2 = n2;
+    }
+  } else if (warp == 11) {
+    // ---- issuing dS
+    constexpr uint32_t kId = rows_desc<DT>(DK, true, true);
+    const uint64_t v_desc = matrix_desc(smem_u32(smem + S::kV), S::kHalf, 1024, kSwizzle128);
+    const uint64_t kt_desc = matrix_desc(smem_u32(smem + S::kKt), S::kHalf, 1024, kSwizzle128);
+    int n = 0;
+    for (int c = 0; c < chunks; ++c) {
+      const int sv = c % S::kStagesV;
+      if (!warp_wait(&sm.v_full[sv], (c / S::kStagesV) & 1, dead)) break;
+      if (c >= updates) {
+        if (lane == 0) bar_arrive(&sm.v_empty[sv]);
+        continue;
+      }
+      if (!warp_wait(&sm.kt_full[c & 1], (c >> 1) & 1, dead)) break;
+      if (c > 0 && !warp_wait(&sm.ds_empty, (c - 1) & 1, dead)) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+          for (int k = 0; k < kChunk / 16; ++k)
+            mma_f16_ss(tmem + kDS, v_desc + ((sv * S::kTileV + k * 2048) >> 4),
+                       kt_desc + ((((c & 1) * 2 + piece) * S::kTileK + k * 2048) >> 4), kId, piece + k > 0);
+        tc_commit(&sm.kt_empty[c & 1]);
+        tc_commit(&sm.v_empty[sv]);
+        tc_commit(&sm.ds_full);
+      }
+      __syncwarp();
+      ++n;
+    }
+    if (lane == 0) sm.products_s = n;
+  } else if (warp >= 12) {
+    // ---- the state: half of a lane's row to a thread, in pairs of columns
+    constexpr int OWN = DK / 2;
+    const int half = (warp - 12) >> 2, at = (warp & 3) * 32 + lane, dv = dv0 + at;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+    const int64_t size = static_cast<int64_t>(P.key_dim) * P.value_dim;
+    pair_t s[OWN / 2];
+#pragma unroll
+    for (int e = 0; e < OWN / 2; ++e) s[e] = 0;
+    const float *from = nullptr;
+    if (OUT && A.segs > 1) {
+      from = A.local + ((static_cast<int64_t>(b) * P.heads + h) * A.segs + seg) * size;
+    } else if (OUT && ok && P.from.state) {
+      const int slot = P.from.slots ? P.from.slots[b] : b;
+      if (slot >= 0) from = P.from.state + slot * P.from.slot_stride + h * size;
+    }
+    if (from && ok && dv < P.value_dim) {
+#pragma unroll
+      for (int e = 0; e < OWN / 2; ++e) {
+        const int d = half * OWN + 2 * e;
+        if (d < P.key_dim) s[e] = pack2(from[static_cast<int64_t>(d) * P.value_dim + dv], from[static_cast<int64_t>(d + 1) * P.value_dim + dv]);
+      }
+    }
+    int met = 0;
+    // the pieces of S that chunk c's product takes
+    auto hand_on = [&](int c) -> bool {
+      pair_t f = 0;
+      if constexpr (F16) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int e = 0; e < OWN / 2; ++e) {
+          const float2 x = unpack2(s[e]);
+          most = max(most, max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu));
+        }
+        sm.smax[c & 1][half][at] = most;
+        warp_arrive(&sm.meet_s, lane);
+        if (!warp_wait(&sm.meet_s, met++ & 1, dead)) return false;
+        float back;
+        const float fit = fit_half(max(most, sm.smax[c & 1][half ^ 1][at]), back);
+        f = pack2(fit, fit);
+        if (half == 0) sm.d[c % kDecayRing].sfac[at] = back;
+      }
+      if (c > 0 && !warp_wait(&sm.s_empty, (c - 1) & 1, dead)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < OWN / 16; ++k) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) split2<DT>(F16 ? mul2(s[8 * k + e], f) : s[8 * k + e], hi[e], lo[e]);
+        tmem_st8(tmem + lanes + kSHi + half * (OWN / 2) + k * 8, hi);
+        tmem_st8(tmem + lanes + kSLo + half * (OWN / 2) + k * 8, lo);
+      }
+      tc_wait_st();
+      tc_fence_before();
+      warp_arrive(&sm.s_full, lane);
+      return true;
+    };
+    bool going = !OUT || chunks == 0 || hand_on(0);
+    for (int c = 0; going && c < chunks; ++c) {
+      const int r = c % kDecayRing;
+      if (!(going = warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead))) break;
+      if (c < updates) {
+        if (!(going = warp_wait(&sm.ds_full, c & 1, dead))) break;
+        tc_fence_after();
+        const float lam = sm.d[r].lam, kf = F16 ? sm.d[r].kfac : 1.0f;
+        const pair_t l2 = pack2(lam, lam), k2 = pack2(kf, kf);
+#pragma unroll
+        for (int k = 0; k < OWN / 16; ++k) {
+          float x[16];
+          tmem_ld16(tmem + lanes + kDS + half * OWN + k * 16, x);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            pair_t &y = s[8 * k + e];
+            if constexpr (F16) y = fma2(pack2(x[2 * e], x[2 * e + 1]), k2, mul2(y, l2));
+            else y = fma2(y, l2, pack2(x[2 * e], x[2 * e + 1]));
+          }
+        }
+        tc_fence_before();
+        warp_arrive(&sm.ds_empty, lane);
+      }
+      warp_arrive(&sm.dec_empty[r], lane);
+      if (OUT && c + 1 < chunks) going = hand_on(c + 1);
+    }
+    float *to = nullptr;
+    if (!OUT) {
+      to = A.local + ((static_cast<int64_t>(b) * P.heads + h) * A.segs + seg) * size;
+    } else if (writes && going) {
+      to = P.to.state + (P.to.slots ? P.to.slots[b] : b) * P.to.slot_stride + h * size;
+    }
+    if (to && dv < P.value_dim) {
+#pragma unroll
+      for (int e = 0; e < OWN / 2; ++e) {
+        const int d = half * OWN + 2 * e;
+        const float2 x = unpack2(s[e]);
+        if (d < P.key_dim) to[static_cast<int64_t>(d) * P.value_dim + dv] = x.x, to[static_cast<int64_t>(d + 1) * P.value_dim + dv] = x.y;
+      }
+    }
+  } else if (warp == 4 || warp == 5 || warp == 8 || warp == 9) {
+    // ---- A: half of a row to a thread
+    if constexpr (OUT) {
+      const int i = (warp & 1) * 32 + lane, half = warp >> 3, j0 = half * 32;
+      const int group = (warp >> 3) * 64 + i;  // the thread among the 128
+      const bool tree = P.parents != nullptr;
+      int met = 0;
+      for (int c = 0; c < chunks; ++c) {
+        const int r = c % kDecayRing, m = min(kChunk, len - (c0 + c) * kChunk);
+        if (!warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead)) break;
+        if (!warp_wait(&sm.p_full[c & 1], (c >> 1) & 1, dead)) break;
+        tc_fence_after();
+        const ChunkSmall::Decays &d = sm.d[r];
+        // which of the half's rows this one follows
+        const uint32_t sees = tree ? sm.follows[i][half] : i >= j0 + 31 ? ~0u : i < j0 ? 0u : (2u << (i - j0)) - 1;
+        uint32_t hi[16], lo[16];
+        float back = 1.0f;
+        if (__any_sync(~0u, sees != 0)) {
+          float x[32];
+          tmem_ld32(tmem + (static_cast<uint32_t>(warp & 3) << 21) + kP + (c & 1) * 64 + j0, x);
+          const float mh = -d.nhi[i], ml = -d.nlo[i];
+          const pair_t h2 = pack2(mh, mh), l2 = pack2(ml, ml);
+          const bool every = __all_sync(~0u, sees == ~0u);
+          tc_wait_ld();
+          uint32_t most = 0;
+          pair_t y[16];
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const ulonglong2 nh = *reinterpret_cast<const ulonglong2 *>(&d.nhi[j0 + 2 * e]);
+            const ulonglong2 nl = *reinterpret_cast<const ulonglong2 *>(&d.nlo[j0 + 2 * e]);
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const float2 g = unpack2(add2(add2(h2, w ? nh.y : nh.x), add2(l2, w ? nl.y : nl.x)));
+              float2 z = unpack2(mul2(pack2(x[2 * (e + w)], x[2 * (e + w) + 1]), pack2(ex2(g.x), ex2(g.y))));
+              if (!every) {
+                z.x = sees >> (2 * (e + w)) & 1 ? z.x : 0.0f;
+                z.y = sees >> (2 * (e + w) + 1) & 1 ? z.y : 0.0f;
+              }
+              if constexpr (F16) most = max(most, max(__float_as_uint(z.x) & 0x7fffffffu, __float_as_uint(z.y) & 0x7fffffffu));
+              y[e + w] = pack2(z.x, z.y);
+            }
+          }
+          if constexpr (F16) sm.amax[c & 1][half][i] = most;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if constexpr (!F16) split2<DT>(y[e], hi[e], lo[e]);
+          tc_fence_before();
+          warp_arrive(&sm.p_empty[c & 1], lane);
+          if constexpr (F16) {
+            warp_arrive(&sm.meet_a, lane);
+            if (!warp_wait(&sm.meet_a, met++ & 1, dead)) break;
+            const float fit = fit_half(max(most, sm.amax[c & 1][half ^ 1][i]), back);
+            const pair_t f = pack2(fit, fit);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) split2<DT>(mul2(y[e], f), hi[e], lo[e]);
+          }
+        } else {
+          warp_arrive(&sm.p_empty[c & 1], lane);
+          if constexpr (F16) {
+            sm.amax[c & 1][half][i] = 0;
+            warp_arrive(&sm.meet_a, lane);
+            if (!warp_wait(&sm.meet_a, met++ & 1, dead)) break;
+            fit_half(sm.amax[c & 1][half ^ 1][i], back);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0;
+        }
+        if (F16 && half == 0) sm.d[r].afac[i] = back * P.scale;
+        if (c > 0 && !warp_wait(&sm.a_empty, (c - 1) & 1, dead)) break;
+        char *row = smem + S::kA + i * 128;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int to = ((half * 4 + e) ^ (i & 7)) << 4;
+          *reinterpret_cast<uint4 *>(row + to) = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
+          *reinterpret_cast<uint4 *>(row + S::kHalf + to) = make_uint4(lo[4 * e], lo[4 * e + 1], lo[4 * e + 2], lo[4 * e + 3]);
+        }
+        if (m < kChunk) {  // values past the request's rows take no part, whatever they are
+          const int sv = c % S::kStagesV;
+          if (!warp_wait(&sm.v_full[sv], (c / S::kStagesV) & 1, dead)) break;
+          for (int e = group; e < (kChunk - m) * 16; e += 128)
+            *reinterpret_cast<uint4 *>(smem + S::kV + sv * S::kTileV + (e & 1) * S::kHalf + (m + (e >> 4)) * 128 + (e >> 1 & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_shared();
+        warp_arrive(&sm.a_full, lane);
+        warp_arrive(&sm.dec_empty[r], lane);
+      }
+    }
+  } else {
+    // ---- K', two chunks ahead, and the outputs
+    const int quarter = warp & 3, at = quarter * 32 + lane;
+    const int row = at & 63, part = at >> 6;  // K': a row's 64 columns (a half of the tile), or half of them
+    int met = 0;
+    auto keys = [&](int c) -> bool {
+      const int r = c % kDecayRing, sk = c % S::kStagesK, m = min(kChunk, len - (c0 + c) * kChunk);
+      if (!warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead)) return false;
+      if (!warp_wait(&sm.k_full[sk], (c / S::kStagesK) & 1, dead)) return false;
+      if (c < updates) {
+        if (c >= 2 && !warp_wait(&sm.kt_empty[c & 1], (c / 2 - 1) & 1, dead)) return false;
+        float left = sm.d[r].left[row];
+        const bool past = row >= m;
+        constexpr int kPieces = DK / 16;  // 16-byte pieces to a thread
+        const int base = DK == 128 ? part * S::kHalf + row * 128 : row * 128, first = DK == 128 ? 0 : part * 4;
+        const char *from = smem + S::kK + sk * S::kTileK + base;
+        char *to = smem + S::kKt + (c & 1) * 2 * S::kTileK + base;
+        if constexpr (F16) {
+          uint32_t most = 0;
+#pragma unroll
+          for (int e = 0; e < kPieces; ++e) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(from + (((first + e) ^ (row & 7)) << 4));
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) most = max(most, max(w[y] & 0x7fffu, w[y] >> 16 & 0x7fffu));
+          }
+          const uint32_t mine = past ? 0u : __float_as_uint(fabsf(__half2float(__ushort_as_half(static_cast<uint16_t>(most))) * left)) & 0x7fffffffu;
+          const uint32_t warps = __reduce_max_sync(~0u, mine);
+          if (lane == 0) sm.kmax[c & 1][quarter] = warps;
+          warp_arrive(&sm.meet_k, lane);
+          if (!warp_wait(&sm.meet_k, met++ & 1, dead)) return false;
+          const uint32_t *km = sm.kmax[c & 1];
+          float back;
+          left *= fit_half(max(max(km[0], km[1]), max(km[2], km[3])), back);
+          if (at == 0) sm.d[r].kfac = back;
+        }
+        const pair_t f = pack2(left, left);
+#pragma unroll
+        for (int e = 0; e < kPieces; ++e) {
+          const int o = ((first + e) ^ (row & 7)) << 4;
+          const uint4 x = *reinterpret_cast<const uint4 *>(from + o);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float2 k = widen2<DT>(w[y]);
+            split2<DT>(mul2(pack2(k.x, k.y), f), hi[y], lo[y]);
+            if (past) hi[y] = lo[y] = 0;
+          }
+          *reinterpret_cast<uint4 *>(to + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4 *>(to + S::kTileK + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        if (m < kChunk) {
+          const int sv = c % S::kStagesV;
+          if (!warp_wait(&sm.v_full[sv], (c / S::kStagesV) & 1, dead)) return false;
+          for (int e = at; e < (kChunk - m) * 16; e += 128)
+            *reinterpret_cast<uint4 *>(smem + S::kV + sv * S::kTileV + (e & 1) * S::kHalf + (m + (e >> 4)) * 128 + (e >> 1 & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_shared();
+        warp_arrive(&sm.kt_full[c & 1], lane);
+      }
+      warp_arrive(&sm.k_empty[sk], lane);
+      if (!OUT) warp_arrive(&sm.dec_empty[r], lane);
+      return true;
+    };
+    bool going = true;
+    if constexpr (OUT) {
+      const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
+      const int dv = dv0 + at;
+      uint16_t *out = reinterpret_cast<uint16_t *>(P.out) + b * P.os[0] + h * P.os[2] + dv;
+      for (int c = 0; going && c < 2 && c < chunks; ++c) going = keys(c);
+      for (int c = 0; going && c < chunks; ++c) {
+        if (c + 2 < chunks && !(going = keys(c + 2))) break;
+        const int r = c % kDecayRing, t0 = (c0 + c) * kChunk, m = min(kChunk, len - t0);
+        if (!(going = warp_wait(&sm.o_full, c & 1, dead))) break;
+        tc_fence_after();
+        const ChunkSmall::Decays &d = sm.d[r];
+        const float sf = F16 ? d.sfac[at] : 1.0f;
+        const pair_t sf2 = pack2(sf, sf), scale2 = pack2(P.scale, P.scale), none = 0;
+        pair_t bad = 0;
+        uint16_t *o = out + t0 * P.os[1];
+        uint32_t rows[32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float x[16], y[16];
+          tmem_ld16(tmem + lanes + kO1 + k * 16, x);
+          tmem_ld16(tmem + lanes + kO2 + k * 16, y);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const ulonglong2 ei = *reinterpret_cast<const ulonglong2 *>(&d.ei[k * 16 + 2 * e]);
+            const ulonglong2 af = *reinterpret_cast<const ulonglong2 *>(&d.afac[k * 16 + 2 * e]);
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const int z = 2 * (e + w);
+              pair_t f = w ? ei.y : ei.x;
+              if constexpr (F16) f = mul2(f, sf2);
+              const pair_t o2 = pack2(y[z], y[z + 1]);
+              const pair_t v = fma2(pack2(x[z], x[z + 1]), f, mul2(o2, F16 ? (w ? af.y : af.x) : scale2));
+              if (m == kChunk) bad = fma2(o2, none, bad);
+              else if (z < m) bad = fma2(pack2(y[z], z + 1 < m ? y[z + 1] : 0.0f), none, bad);
+              rows[k * 8 + e + w] = narrow2<DT>(unpack2(v));
+            }
+          }
+        }
+        const float2 b2 = unpack2(bad);
+        const bool spoilt = __any_sync(~0u, !(b2.x == 0.0f && b2.y == 0.0f));
+        if (!spoilt) {
+          tc_fence_before();
+          warp_arrive(&sm.o_empty, lane);
+        }
+        if (dv < P.value_dim) {
+          if (m == kChunk) {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+              *o = static_cast<uint16_t>(rows[i >> 1] >> (16 * (i & 1)));
+              o += P.os[1];
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+              if (i < m) *o = static_cast<uint16_t>(rows[i >> 1] >> (16 * (i & 1)));
+              o += P.os[1];
+            }
+          }
+        }
+        if (spoilt) [[unlikely]] {  // rows with a result that is no number: without the rows that they do not follow
+#pragma unroll 1
+          for (int i = 0; i < m; ++i) {
+            const uint64_t sees = P.parents ? static_cast<uint64_t>(sm.follows[i][1]) << 32 | sm.follows[i][0] : (2ull << i) - 1;
+            float x[8];
+            tmem_ld8(tmem + lanes + kO1 + (i & ~7), x);
+            tc_wait_ld();
+            float v = x[0];
+#pragma unroll
+            for (int e = 1; e < 8; ++e) v = (i & 7) == e ? x[e] : v;
+            v = fmaf(v, d.ei[i] * sf, row_again<DT>(P, d, sees, b, h, t0, i, dv) * P.scale);
+            if (dv < P.value_dim) out[(t0 + i) * P.os[1]] = narrow<DT>(v);
+          }
+          tc_fence_before();
+          warp_arrive(&sm.o_empty, lane);
+        }
+        warp_arrive(&sm.dec_empty[r], lane);
+      }
+      // rows past the count: each segment's share of them
+      const int pieces = min(128, P.value_dim - dv0) >> 3;
+      const int64_t gap = P.n - len, z0 = gap * seg / A.segs, z1 = gap * (seg + 1) / A.segs;
+      uint16_t *o = reinterpret_cast<uint16_t *>(P.out) + b * P.os[0] + h * P.os[2] + dv0;
+      for (int64_t e = at; e < (z1 - z0) * pieces; e += 128)
+        *reinterpret_cast<uint4 *>(o + (len + z0 + e / pieces) * P.os[1] + e % pieces * 8) = make_uint4(0, 0, 0, 0);
+    } else {
+      for (int c = 0; going && c < chunks; ++c) going = keys(c);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*dead) [[unlikely]] {  // nothing that was begun may reach shared or tensor memory that the CTA has left (else all was waited for)
+    if (warp == 0) land_chunks<DK, OUT>(sm);
+    __syncthreads();
+    if (tid == 0 && P.status) atomicMax(&P.status[b], SPEC_STATUS_TIMEOUT);
+  }
+  tc_fence_after();
+  if (warp == 10) tmem_free(tmem, 512);
+}
+
+template <int DT, int DK, bool OUT>
+std::atomic<uint64_t> chunk_smem{0};
+
+template <int DT, int DK, bool OUT>
+cudaError_t launch_chunks(const StateChunkPlan &A, const CUtensorMap *maps, cudaStream_t st) {
+  using S = ChunkShape<DK, OUT>;
+  auto kern = state_chunk_kernel<DT, DK, OUT>;
+  const cudaError_t e =
+      once_per_device([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes); }, chunk_smem<DT, DK, OUT>);
+  if (e != cudaSuccess) return e;
+  StateChunkPlan B = A;
+  B.launch_segs = OUT ? A.segs : A.segs - 1;
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(A.p.B) * B.launch_segs * ((A.p.value_dim + 127) / 128) * A.p.heads);
+  const bool again = !state_overlaps(A.p);
+  return trace_launch(OUT ? "state_chunk" : "state_chunk_local", st, [&] { kern<<<grid, kChunkThreads, S::kBytes, st>>>(B, maps[0], maps[1], maps[2]); },
+                      again || !OUT);
+}
+
+}  // namespace
+}  // namespace sv

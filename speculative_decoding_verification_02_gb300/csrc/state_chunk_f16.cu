@@ -1,0 +1,12 @@
+// The tensor-core kernels of linear attention for fp16 rows.
+#include "state_chunk.cuh"
+
+namespace sv {
+
+cudaError_t launch_state_chunk_f16(const StateChunkPlan &A, bool outputs, const CUtensorMap *maps, cudaStream_t st) {
+  constexpr int DT = SPEC_DTYPE_F16;
+  if (A.p.key_dim <= 64) return outputs ? launch_chunks<DT, 64, true>(A, maps, st) : launch_chunks<DT, 64, false>(A, maps, st);
+  return outputs ? launch_chunks<DT, 128, true>(A, maps, st) : launch_chunks<DT, 128, false>(A, maps, st);
+}
+
+}  // namespace sv

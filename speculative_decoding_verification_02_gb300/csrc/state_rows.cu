@@ -346,13 +346,6 @@ __global__ void __launch_bounds__(32 * kMaxWarps) state_rows_kernel(const StateP
   }
 }
 
-// Whether the states written lie where some are read: such a call is not the same call when it is made again.
-bool state_overlaps(const StateParams &P) {
-  if (!P.from.state || !P.to.state) return false;
-  const float *a = P.from.state, *b = P.to.state;
-  return a < b + P.to.num_slots * P.to.slot_stride && b < a + P.from.num_slots * P.from.slot_stride;
-}
-
 template <int DT, int RPL>
 cudaError_t launch_rows(const StateParams &P, cudaStream_t st) {
   const int groups = P.value_dim / 16;
