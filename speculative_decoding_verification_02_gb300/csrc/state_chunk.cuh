@@ -127,6 +127,38 @@ __device__ __forceinline__ float fit_half(uint32_t amax, float &back) {
   return __uint_as_float(static_cast<uint32_t>(127 + s) << 23);
 }
 
+// A sum of decays in units of log 2, in fixed point: whole units, and 2^-25ths
+// (of which 64 tokens' halves fit an int).  A token's is off by half of one of
+// them, sums and differences not at all, however large: what 64-bit floats
+// would do at many times the cost.
+constexpr int kLog2Bits = 25;
+struct Log2Parts {
+  float hi, lo;  // a whole number and a rest in [-1/2, 1/2]
+  __device__ __forceinline__ float power() const {  // 2^(hi + lo); 0 below the least normal number
+    const float f = exp2f(lo);
+    if (!(hi >= -125.0f)) return hi < 0.0f ? 0.0f : hi + lo;  // (NaN stays)
+    return hi > 127.0f ? INFINITY : f * __uint_as_float(static_cast<uint32_t>(static_cast<int>(hi) + 127) << 23);
+  }
+};
+struct Log2Sum {
+  int whole, rest;
+  __device__ __forceinline__ Log2Sum &operator+=(const Log2Sum &x) {
+    whole += x.whole, rest += x.rest;
+    return *this;
+  }
+  __device__ __forceinline__ Log2Parts parts(bool nan) const {
+    const int carry = (rest + (1 << (kLog2Bits - 1))) >> kLog2Bits;
+    return Log2Parts{nan ? NAN : static_cast<float>(whole + carry), static_cast<float>(rest - (carry << kLog2Bits)) * (1.0f / (1 << kLog2Bits))};
+  }
+};
+// A natural logarithm; beyond +-120 (1e52) a factor is 0 or infinite in fp32 whatever it is.  NaN gives 0.
+__device__ __forceinline__ Log2Sum log2_of(float g) {
+  const float x = fminf(fmaxf(g, -120.0f), 120.0f);
+  const float y = x * 1.44269502f, e = fmaf(x, 1.44269502f, -y) + x * 1.92596303e-8f;  // log2(e) in two parts
+  const float w = rintf(y);
+  return g == g ? Log2Sum{static_cast<int>(w), static_cast<int>(rintf(((y - w) + e) * (1 << kLog2Bits)))} : Log2Sum{0, 0};
+}
+
 // Row i's weight for row j without what P held: e^{G_i - G_j} from the handed-on parts.
 __device__ __forceinline__ float between(const ChunkSmall::Decays &d, int i, int j) {
   return ex2((d.nhi[j] - d.nhi[i]) + (d.nlo[j] - d.nlo[i]));
@@ -261,64 +293,77 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     if (lane == 0) sm.copies_k = kc, sm.copies_q = qc, sm.copies_v = vc;
   } else if (warp == 3) {
-    // ---- decays: two tokens to a lane
+    // ---- decays: two tokens next to one another to a lane
     const float *gp = P.decay + b * P.gs[0] + h * P.gs[2];
-    double sum = 0.0;
+    long long whole = 0, rest = 0;  // of the segment's sum
     auto fetch = [&](int c, float &x0, float &x1) {
-      const int t = (c0 + c) * kChunk + lane;
+      const int t = (c0 + c) * kChunk + 2 * lane;
       x0 = c < chunks && t < len ? gp[t * P.gs[1]] : 0.0f;
-      x1 = c < chunks && t + 32 < len ? gp[(t + 32) * P.gs[1]] : 0.0f;
+      x1 = c < chunks && t + 1 < len ? gp[(t + 1) * P.gs[1]] : 0.0f;
     };
     float x0, x1;
+    bool lost = false;
     fetch(0, x0, x1);
     for (int c = 0; c < chunks; ++c) {
       const int r = c % kDecayRing, t0 = (c0 + c) * kChunk;
       const int m = min(kChunk, len - t0);
-      // (a factor below 2^-173 is 0 in fp32 whatever it multiplies; NaN stays)
-      double g0 = x0 < -120.0f ? -120.0f : x0, g1 = x1 < -120.0f ? -120.0f : x1;
-      float own[2] = {x0, x1};
+      Log2Sum g0 = log2_of(x0), g1 = log2_of(x1);
+      // from the first NaN on every sum is one
+      uint32_t nan0 = __ballot_sync(~0u, x0 != x0), nan1 = __ballot_sync(~0u, x1 != x1);
       fetch(c + 1, x0, x1);
+      bool bad0, bad1;
       if (OUT && P.parents) {  // the sums over each row's path, and which rows lie on it
         const int32_t *parents = P.parents + static_cast<int64_t>(b) * P.n;
         for (int e = 0; e < 2; ++e) {
-          const int i = lane + 32 * e;
+          const int i = 2 * lane + e;
           uint32_t bits[2] = {0, 0};
-          double path = 0.0;
+          Log2Sum path{0, 0};
+          bool bad = false;
           if (i < m) {
             for (int p = i; p >= 0; p = parents[p]) {
-              const float y = p == i ? own[e] : gp[p * P.gs[1]];
-              path += y < -120.0f ? -120.0f : y;
+              path += log2_of(gp[p * P.gs[1]]);
+              bad |= (p & 1 ? nan1 : nan0) >> (p >> 1) & 1;
               bits[p >> 5] |= 1u << (p & 31);
             }
           }
           sm.follows[i][0] = bits[0], sm.follows[i][1] = bits[1];
-          (e ? g1 : g0) = path;
+          (e ? g1 : g0) = path, (e ? bad1 : bad0) = bad;
         }
       } else {
+        g1 += g0;  // the lane's two, then the lanes before it
+        Log2Sum upto = g1;
+#pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const double y0 = __shfl_up_sync(~0u, g0, o), y1 = __shfl_up_sync(~0u, g1, o);
-          if (lane >= o) g0 += y0, g1 += y1;
+          const Log2Sum y{__shfl_up_sync(~0u, upto.whole, o), __shfl_up_sync(~0u, upto.rest, o)};
+          if (lane >= o) upto += y;
         }
-        g1 += __shfl_sync(~0u, g0, 31);
+        const Log2Sum before{upto.whole - g1.whole, upto.rest - g1.rest};
+        g0 += before, g1 += before;
+        const uint32_t to = (2u << lane) - 1, under = to >> 1;
+        bad0 = nan0 & to || nan1 & under, bad1 = nan0 & to || nan1 & to;
       }
-      const double total = __shfl_sync(~0u, g1, 31);
-      sum += total;
+      const Log2Sum total{__shfl_sync(~0u, g1.whole, 31), __shfl_sync(~0u, g1.rest, 31)};
+      const bool spoilt = nan0 || nan1;
+      whole += total.whole, rest += total.rest, lost |= spoilt;
       if (c >= kDecayRing && !warp_wait(&sm.dec_empty[r], (c / kDecayRing - 1) & 1, dead)) break;
       ChunkSmall::Decays &d = sm.d[r];
-      for (int e = 0; e < 2; ++e) {
-        const double g = e ? g1 : g0, y = g * 1.4426950408889634074;
-        const float hi = rintf(static_cast<float>(y) * 8.0f) * 0.125f;
-        const int i = lane + 32 * e;
-        d.nhi[i] = -hi;
-        d.nlo[i] = static_cast<float>(hi - y);
-        d.ei[i] = expf(static_cast<float>(g)) * P.scale;
-        d.left[i] = i < m ? expf(static_cast<float>(total - g)) : 0.0f;
-        d.afac[i] = P.scale;
-      }
-      if (lane == 0) d.lam = expf(static_cast<float>(total)), d.kfac = 1.0f;
+      const Log2Parts p0 = g0.parts(bad0), p1 = g1.parts(bad1);
+      const Log2Parts q0 = Log2Sum{total.whole - g0.whole, total.rest - g0.rest}.parts(spoilt);
+      const Log2Parts q1 = Log2Sum{total.whole - g1.whole, total.rest - g1.rest}.parts(spoilt);
+      *reinterpret_cast<float2 *>(&d.nhi[2 * lane]) = make_float2(-p0.hi, -p1.hi);
+      *reinterpret_cast<float2 *>(&d.nlo[2 * lane]) = make_float2(-p0.lo, -p1.lo);
+      *reinterpret_cast<float2 *>(&d.ei[2 * lane]) = make_float2(p0.power() * P.scale, p1.power() * P.scale);
+      *reinterpret_cast<float2 *>(&d.left[2 * lane]) = make_float2(2 * lane < m ? q0.power() : 0.0f, 2 * lane + 1 < m ? q1.power() : 0.0f);
+      *reinterpret_cast<float2 *>(&d.afac[2 * lane]) = make_float2(P.scale, P.scale);
+      if (lane == 0) d.lam = total.parts(spoilt).power(), d.kfac = 1.0f;
       warp_arrive(&sm.dec_full[r], lane);
     }
-    if (!OUT && lane == 0 && dv0 == 0) A.total[(static_cast<int64_t>(b) * P.heads + h) * A.segs + seg] = static_cast<float>(exp(sum));
+    if (!OUT && lane == 0 && dv0 == 0) {  // (segments of many chunks: the sums in 64 bits, the whole part no further than fp32's exponents)
+      whole += rest >> kLog2Bits;
+      rest &= (1 << kLog2Bits) - 1;
+      const Log2Sum all_of{static_cast<int>(max(-4096ll, min(4096ll, whole))), static_cast<int>(rest)};
+      A.total[(static_cast<int64_t>(b) * P.heads + h) * A.segs + seg] = all_of.parts(lost).power();
+    }
   } else if (warp == 10) {
     // ---- issuing P, O1, O2
     if constexpr (OUT) {
@@ -328,27 +373,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const uint64_t v_desc = matrix_desc(smem_u32(smem + S::kV), S::kHalf, 1024, kSwizzle128);
       const uint64_t a_desc = matrix_desc(smem_u32(smem + S::kA), 16, 1024, kSwizzle128);
       int np = 0, n1 = 0, n2 = 0;
-      auto issue_p = [&](int c) -> bool {
-        const int sk = c % S::kStagesK, sq = c % S::kStagesQ;
-        if (c >= 2 && !warp_wait(&sm.p_empty[c & 1], (c / 2 - 1) & 1, dead)) return false;
-        if (!warp_wait(&sm.k_full[sk], (c / S::kStagesK) & 1, dead)) return false;
-        if (!warp_wait(&sm.q_full[sq], (c / S::kStagesQ) & 1, dead)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < DK / 16; ++k)
-            mma_f16_ss(tmem + kP + (c & 1) * 64, q_desc + ((sq * S::kTileK + k / 4 * S::kHalf + k % 4 * 32) >> 4),
-                       k_desc + ((sk * S::kTileK + k / 4 * S::kHalf + k % 4 * 32) >> 4), kIdP, k > 0);
-          tc_commit(&sm.k_empty[sk]);
-          tc_commit(&sm.p_full[c & 1]);
-        }
-        __syncwarp();
-        ++np;
-        return true;
-      };
-      if (chunks > 0 && issue_p(0)) {
-        for (int c = 0; c < chunks; ++c) {
-          const int sq = c % S::kStagesQ, sv = c % S::kStagesV;
+#pragma unroll 1
+      for (int c = -1; c < chunks; ++c) {  // O1 of a chunk, P of the next, O2 of the chunk
+        if (c >= 0) {
+          const int sq = c % S::kStagesQ;
           if (!warp_wait(&sm.s_full, c & 1, dead)) break;
           if (c > 0 && !warp_wait(&sm.o_empty, (c - 1) & 1, dead)) break;
           tc_fence_after();
@@ -364,7 +392,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
           __syncwarp();
           ++n1;
-          if (c + 1 < chunks && !issue_p(c + 1)) break;
+        }
+        if (c + 1 < chunks) {
+          const int d = c + 1, sk = d % S::kStagesK, sq = d % S::kStagesQ;
+          if (d >= 2 && !warp_wait(&sm.p_empty[d & 1], (d / 2 - 1) & 1, dead)) break;
+          if (!warp_wait(&sm.k_full[sk], (d / S::kStagesK) & 1, dead)) break;
+          if (!warp_wait(&sm.q_full[sq], (d / S::kStagesQ) & 1, dead)) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k)
+              mma_f16_ss(tmem + kP + (d & 1) * 64, q_desc + ((sq * S::kTileK + k / 4 * S::kHalf + k % 4 * 32) >> 4),
+                         k_desc + ((sk * S::kTileK + k / 4 * S::kHalf + k % 4 * 32) >> 4), kIdP, k > 0);
+            tc_commit(&sm.k_empty[sk]);
+            tc_commit(&sm.p_full[d & 1]);
+          }
+          __syncwarp();
+          ++np;
+        }
+        if (c >= 0) {
+          const int sv = c % S::kStagesV;
           if (!warp_wait(&sm.v_full[sv], (c / S::kStagesV) & 1, dead)) break;
           if (!warp_wait(&sm.a_full, c & 1, dead)) break;
           tc_fence_after();
@@ -473,9 +520,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       warp_arrive(&sm.s_full, lane);
       return true;
     };
-    bool going = !OUT || chunks == 0 || hand_on(0);
-    for (int c = 0; going && c < chunks; ++c) {
+    bool going = true;
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
       const int r = c % kDecayRing;
+      if (OUT && !(going = hand_on(c))) break;
       if (!(going = warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead))) break;
       if (c < updates) {
         if (!(going = warp_wait(&sm.ds_full, c & 1, dead))) break;
@@ -498,7 +547,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         warp_arrive(&sm.ds_empty, lane);
       }
       warp_arrive(&sm.dec_empty[r], lane);
-      if (OUT && c + 1 < chunks) going = hand_on(c + 1);
     }
     float *to = nullptr;
     if (!OUT) {
@@ -521,6 +569,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int group = (warp >> 3) * 64 + i;  // the thread among the 128
       const bool tree = P.parents != nullptr;
       int met = 0;
+#pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
         const int r = c % kDecayRing, m = min(kChunk, len - (c0 + c) * kChunk);
         if (!warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead)) break;
@@ -620,7 +669,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         char *to = smem + S::kKt + (c & 1) * 2 * S::kTileK + base;
         if constexpr (F16) {
           uint32_t most = 0;
-#pragma unroll
+#pragma unroll 2
           for (int e = 0; e < kPieces; ++e) {
             const uint4 x = *reinterpret_cast<const uint4 *>(from + (((first + e) ^ (row & 7)) << 4));
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -638,7 +687,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (at == 0) sm.d[r].kfac = back;
         }
         const pair_t f = pack2(left, left);
-#pragma unroll
+#pragma unroll 2
         for (int e = 0; e < kPieces; ++e) {
           const int o = ((first + e) ^ (row & 7)) << 4;
           const uint4 x = *reinterpret_cast<const uint4 *>(from + o);
@@ -671,9 +720,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
       const int dv = dv0 + at;
       uint16_t *out = reinterpret_cast<uint16_t *>(P.out) + b * P.os[0] + h * P.os[2] + dv;
-      for (int c = 0; going && c < 2 && c < chunks; ++c) going = keys(c);
-      for (int c = 0; going && c < chunks; ++c) {
+#pragma unroll 1
+      for (int c = -2; c < chunks; ++c) {
         if (c + 2 < chunks && !(going = keys(c + 2))) break;
+        if (c < 0) continue;
         const int r = c % kDecayRing, t0 = (c0 + c) * kChunk, m = min(kChunk, len - t0);
         if (!(going = warp_wait(&sm.o_full, c & 1, dead))) break;
         tc_fence_after();
@@ -682,52 +732,39 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const pair_t sf2 = pack2(sf, sf), scale2 = pack2(P.scale, P.scale), none = 0;
         pair_t bad = 0;
         uint16_t *o = out + t0 * P.os[1];
-        uint32_t rows[32];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
+#pragma unroll 1
+        for (int k = 0; k < kChunk; k += 16) {
           float x[16], y[16];
-          tmem_ld16(tmem + lanes + kO1 + k * 16, x);
-          tmem_ld16(tmem + lanes + kO2 + k * 16, y);
+          tmem_ld16(tmem + lanes + kO1 + k, x);
+          tmem_ld16(tmem + lanes + kO2 + k, y);
           tc_wait_ld();
+          if (k + 16 > m) [[unlikely]] {
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const ulonglong2 ei = *reinterpret_cast<const ulonglong2 *>(&d.ei[k * 16 + 2 * e]);
-            const ulonglong2 af = *reinterpret_cast<const ulonglong2 *>(&d.afac[k * 16 + 2 * e]);
+            for (int e = 0; e < 16; ++e) y[e] = k + e < m ? y[e] : 0.0f;
+          }
+          const bool store = dv < P.value_dim;
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const ulonglong2 ei = *reinterpret_cast<const ulonglong2 *>(&d.ei[k + e]);
+            ulonglong2 af;
+            if constexpr (F16) af = *reinterpret_cast<const ulonglong2 *>(&d.afac[k + e]);
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-              const int z = 2 * (e + w);
+              const int z = e + 2 * w;
               pair_t f = w ? ei.y : ei.x;
               if constexpr (F16) f = mul2(f, sf2);
               const pair_t o2 = pack2(y[z], y[z + 1]);
-              const pair_t v = fma2(pack2(x[z], x[z + 1]), f, mul2(o2, F16 ? (w ? af.y : af.x) : scale2));
-              if (m == kChunk) bad = fma2(o2, none, bad);
-              else if (z < m) bad = fma2(pack2(y[z], z + 1 < m ? y[z + 1] : 0.0f), none, bad);
-              rows[k * 8 + e + w] = narrow2<DT>(unpack2(v));
+              bad = fma2(o2, none, bad);
+              const uint32_t u2 = narrow2<DT>(unpack2(fma2(pack2(x[z], x[z + 1]), f, mul2(o2, F16 ? (w ? af.y : af.x) : scale2))));
+              if (store && k + z < m) o[0] = static_cast<uint16_t>(u2);
+              o += P.os[1];
+              if (store && k + z + 1 < m) o[0] = static_cast<uint16_t>(u2 >> 16);
+              o += P.os[1];
             }
           }
         }
         const float2 b2 = unpack2(bad);
-        const bool spoilt = __any_sync(~0u, !(b2.x == 0.0f && b2.y == 0.0f));
-        if (!spoilt) {
-          tc_fence_before();
-          warp_arrive(&sm.o_empty, lane);
-        }
-        if (dv < P.value_dim) {
-          if (m == kChunk) {
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-              *o = static_cast<uint16_t>(rows[i >> 1] >> (16 * (i & 1)));
-              o += P.os[1];
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-              if (i < m) *o = static_cast<uint16_t>(rows[i >> 1] >> (16 * (i & 1)));
-              o += P.os[1];
-            }
-          }
-        }
-        if (spoilt) [[unlikely]] {  // rows with a result that is no number: without the rows that they do not follow
+        if (__any_sync(~0u, !(b2.x == 0.0f && b2.y == 0.0f))) [[unlikely]] {  // a row's sum that is no number: without the rows that it does not follow
 #pragma unroll 1
           for (int i = 0; i < m; ++i) {
             const uint64_t sees = P.parents ? static_cast<uint64_t>(sm.follows[i][1]) << 32 | sm.follows[i][0] : (2ull << i) - 1;
@@ -740,9 +777,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             v = fmaf(v, d.ei[i] * sf, row_again<DT>(P, d, sees, b, h, t0, i, dv) * P.scale);
             if (dv < P.value_dim) out[(t0 + i) * P.os[1]] = narrow<DT>(v);
           }
-          tc_fence_before();
-          warp_arrive(&sm.o_empty, lane);
         }
+        tc_fence_before();
+        warp_arrive(&sm.o_empty, lane);
         warp_arrive(&sm.dec_empty[r], lane);
       }
       // rows past the count: each segment's share of them
