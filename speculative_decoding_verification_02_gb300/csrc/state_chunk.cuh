@@ -33,9 +33,11 @@ namespace {
 // is as exact as one of small ones.
 //
 // Warps (their number modulo 4 is the quarter of the lanes that they can reach,
-// and their scheduler): 2 loads, 3 decays, 10 issues P, O1 and O2, 11 issues dS;
-// 4, 5, 8, 9 make A; 0, 1, 6, 7 make K' (two chunks ahead) and write the
-// outputs; 12 to 19 hold S.
+// and their scheduler): 2 loads, 3 decays, 10 issues O1 and O2, 11 issues P and dS;
+// 4, 5, 8, 9 make A; 0, 1, 6, 7 write the outputs; 12 to 19 hold S and make K',
+// two chunks ahead.  The code of the roles is kept short, one site to each and
+// loops rolled where registers allow: unrolled further, warps waited for their
+// instructions (a chunk 7,700 cycles, not 5,300).
 //
 // A long prompt of few heads is cut into segments: a first launch (OUT false)
 // computes what each but the last adds to a state of zeros, state_join_kernel
@@ -50,8 +52,8 @@ struct ChunkShape {
   static constexpr int kHalf = kChunk * 128;  // bytes of 64 columns of a tile
   static constexpr int kTileK = DK / 64 * kHalf, kTileV = 2 * kHalf;
   static constexpr int kStagesK = OUT ? (DK == 128 ? 2 : 4) : 4;
-  static constexpr int kStagesQ = OUT ? (DK == 128 ? 3 : 4) : 0;
   static constexpr int kStagesV = OUT ? (DK == 128 ? 3 : 4) : 4;
+  static constexpr int kStagesQ = OUT ? kStagesV : 0;
   static constexpr int kK = 0;
   static constexpr int kQ = kK + kStagesK * kTileK;
   static constexpr int kV = kQ + kStagesQ * kTileK;  // (P's product reads 64 rows past a half of Q: of Q, or of V)
@@ -72,13 +74,16 @@ struct ChunkSmall {
     float kfac;                      // fp16: what K' was divided by
   } d[kDecayRing];
   uint32_t follows[kChunk][2];  // trees: the rows that a row follows, itself among them
-  uint32_t smax[2][2][128], amax[2][2][kChunk], kmax[2][4];  // (by the chunk's number: the next one's may be written before these are read)
-  uint64_t k_full[4], k_empty[4], q_full[4], q_empty[4], v_full[4], v_empty[4];
-  uint64_t kt_full[2], kt_empty[2], p_full[2], p_empty[2], a_full, a_empty, ds_full, ds_empty, s_full, s_empty, o_full, o_empty;
+  uint32_t smax[2][2][128], amax[2][2][kChunk], kmax[2][8];  // (by the chunk's number: the next one's may be written before these are read)
+  // One barrier for each product, counted by chunk (four of them in turn, so that whoever waits for a chunk's phase is never a
+  // lap behind): that P, O1, O2, dS are there, and so that their operands are free.
+  uint64_t p_full[4], o1_full[4], o2_full[4], ds_full[4];
+  uint64_t full[4], k_read[4];  // a chunk's rows loaded; its keys read by those who make K'
+  uint64_t kt_full[2], p_empty, a_full, ds_empty, s_full, o_empty;
   uint64_t dec_full[kDecayRing], dec_empty[kDecayRing], meet_s, meet_a, meet_k;
   uint32_t tmem;
   int dead;
-  int copies_k, copies_q, copies_v, products_p, products_o1, products_o2, products_s;  // how many were begun
+  int copies, products_p, products_o1, products_o2, products_s;  // how many were begun
 };
 static_assert(sizeof(ChunkSmall) <= 12288);
 
@@ -188,16 +193,12 @@ __device__ __noinline__ float row_again(const StateParams &P, const ChunkSmall::
 }
 
 // Waits for every copy and product that the CTA began.
-template <int DK, bool OUT>
-__device__ __noinline__ void land_chunks(ChunkSmall &sm) {
-  using S = ChunkShape<DK, OUT>;
-  ring_land(sm.k_full, S::kStagesK, sm.copies_k);
-  if (OUT) ring_land(sm.q_full, S::kStagesQ, sm.copies_q);
-  ring_land(sm.v_full, S::kStagesV, sm.copies_v);
-  ring_land(sm.p_full, 2, sm.products_p);
-  ring_land(&sm.s_empty, 1, sm.products_o1);
-  ring_land(&sm.o_full, 1, sm.products_o2);
-  ring_land(&sm.ds_full, 1, sm.products_s);
+static __device__ __noinline__ void land_chunks(ChunkSmall &sm) {
+  ring_land(sm.full, 4, sm.copies);
+  ring_land(sm.p_full, 4, sm.products_p);
+  ring_land(sm.o1_full, 4, sm.products_o1);
+  ring_land(sm.o2_full, 4, sm.products_o2);
+  ring_land(sm.ds_full, 4, sm.products_s);
 }
 
 template <int DT, int DK, bool OUT>
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                        const __grid_constant__ CUtensorMap v_map) {
   using S = ChunkShape<DK, OUT>;
   constexpr bool F16 = DT == SPEC_DTYPE_F16;
-  constexpr uint32_t kDS = 0, kSHi = 128, kSLo = 192, kO1 = 256, kO2 = 320, kP = 384;  // tensor memory; P twice
+  constexpr uint32_t kDS = 0, kSHi = 128, kSLo = 192, kO1 = 256, kO2 = 384, kP = 448;  // tensor memory; O1 twice
   extern __shared__ char raw[];
   char *const smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   ChunkSmall &sm = *reinterpret_cast<ChunkSmall *>(smem + S::kSmall);
@@ -234,23 +235,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      bar_init(&sm.k_full[i], 1), bar_init(&sm.k_empty[i], OUT ? 5 : 4);
-      bar_init(&sm.q_full[i], 1), bar_init(&sm.q_empty[i], 1);
-      bar_init(&sm.v_full[i], 1), bar_init(&sm.v_empty[i], OUT ? 2 : 1);
+      bar_init(&sm.full[i], 1), bar_init(&sm.k_read[i], 8);
+      bar_init(&sm.p_full[i], 1), bar_init(&sm.o1_full[i], 1), bar_init(&sm.o2_full[i], 1), bar_init(&sm.ds_full[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      bar_init(&sm.kt_full[i], 4), bar_init(&sm.kt_empty[i], 1);
-      bar_init(&sm.p_full[i], 1), bar_init(&sm.p_empty[i], 4);
-    }
-    bar_init(&sm.a_full, 4), bar_init(&sm.a_empty, 1);
-    bar_init(&sm.ds_full, 1), bar_init(&sm.ds_empty, 8);
-    bar_init(&sm.s_full, 8), bar_init(&sm.s_empty, 1);
-    bar_init(&sm.o_full, 1), bar_init(&sm.o_empty, 4);
-    for (int i = 0; i < kDecayRing; ++i) bar_init(&sm.dec_full[i], 1), bar_init(&sm.dec_empty[i], OUT ? 16 : 12);
-    bar_init(&sm.meet_s, 8), bar_init(&sm.meet_a, 4), bar_init(&sm.meet_k, 4);
+    for (int i = 0; i < 2; ++i) bar_init(&sm.kt_full[i], 8);
+    bar_init(&sm.p_empty, 4), bar_init(&sm.a_full, 4), bar_init(&sm.ds_empty, 8), bar_init(&sm.s_full, 8), bar_init(&sm.o_empty, 4);
+    for (int i = 0; i < kDecayRing; ++i) bar_init(&sm.dec_full[i], 1), bar_init(&sm.dec_empty[i], OUT ? 16 : 8);
+    bar_init(&sm.meet_s, 8), bar_init(&sm.meet_a, 4), bar_init(&sm.meet_k, 8);
     bar_init_fence();
     sm.dead = 0;
-    sm.copies_k = sm.copies_q = sm.copies_v = sm.products_p = sm.products_o1 = sm.products_o2 = sm.products_s = 0;
+    sm.copies = sm.products_p = sm.products_o1 = sm.products_o2 = sm.products_s = 0;
   }
   if (warp == 10) tmem_alloc(&sm.tmem, 512);
   tc_fence_before();
@@ -258,40 +252,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   volatile int *dead = &sm.dead;
+  // of the barriers counted by chunk
+  auto wait4 = [&](uint64_t *bars, int c) -> bool { return warp_wait(&bars[c & 3], c >> 2 & 1, dead); };
 
   if (warp == 2) {
     // ---- loading
-    int c = 0, kc = 0, qc = 0, vc = 0;
-    for (; c < chunks; ++c) {
+    int n = 0;
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
       const int t0 = (c0 + c) * kChunk;
       const int sk = c % S::kStagesK, sv = c % S::kStagesV;
-      if (c >= S::kStagesK && !warp_wait(&sm.k_empty[sk], (c / S::kStagesK - 1) & 1, dead)) break;
+      // the stages' last products: P and K' of the keys, O1 of the queries, O2 and dS of the values
+      const int k = c - S::kStagesK, v = c - S::kStagesV;
+      if (k >= 0 && !(wait4(sm.k_read, k) && (!OUT || wait4(sm.p_full, k)))) break;
+      if (v >= 0 && !((v >= updates || wait4(sm.ds_full, v)) && (!OUT || (wait4(sm.o1_full, v) && wait4(sm.o2_full, v))))) break;
       if (lane == 0) {
-        bar_expect(&sm.k_full[sk], S::kTileK);
-        for (int e = 0; e < DK / 64; ++e)
-          tensor_load_4d(smem + S::kK + sk * S::kTileK + e * S::kHalf, &k_map, e * 64, hk, t0, b, &sm.k_full[sk]);
-      }
-      ++kc;
-      if constexpr (OUT) {
-        const int sq = c % S::kStagesQ;
-        if (c >= S::kStagesQ && !warp_wait(&sm.q_empty[sq], (c / S::kStagesQ - 1) & 1, dead)) break;
-        if (lane == 0) {
-          bar_expect(&sm.q_full[sq], S::kTileK);
-          for (int e = 0; e < DK / 64; ++e)
-            tensor_load_4d(smem + S::kQ + sq * S::kTileK + e * S::kHalf, &q_map, e * 64, hk, t0, b, &sm.q_full[sq]);
+        uint64_t *full = &sm.full[c & 3];
+        bar_expect(full, (OUT ? 2 : 1) * S::kTileK + S::kTileV);
+        for (int e = 0; e < DK / 64; ++e) {
+          tensor_load_4d(smem + S::kK + sk * S::kTileK + e * S::kHalf, &k_map, e * 64, hk, t0, b, full);
+          if (OUT) tensor_load_4d(smem + S::kQ + sv * S::kTileK + e * S::kHalf, &q_map, e * 64, hk, t0, b, full);
         }
-        ++qc;
+        for (int e = 0; e < 2; ++e) tensor_load_4d(smem + S::kV + sv * S::kTileV + e * S::kHalf, &v_map, dv0 + e * 64, h, t0, b, full);
       }
-      if (c >= S::kStagesV && !warp_wait(&sm.v_empty[sv], (c / S::kStagesV - 1) & 1, dead)) break;
-      if (lane == 0) {
-        bar_expect(&sm.v_full[sv], S::kTileV);
-        for (int e = 0; e < 2; ++e)
-          tensor_load_4d(smem + S::kV + sv * S::kTileV + e * S::kHalf, &v_map, dv0 + e * 64, h, t0, b, &sm.v_full[sv]);
-      }
-      ++vc;
+      ++n;
       __syncwarp();
     }
-    if (lane == 0) sm.copies_k = kc, sm.copies_q = qc, sm.copies_v = vc;
+    if (lane == 0) sm.copies = n;
   } else if (warp == 3) {
     // ---- decays: two tokens next to one another to a lane
     const float *gp = P.decay + b * P.gs[0] + h * P.gs[2];
@@ -365,104 +352,94 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       A.total[(static_cast<int64_t>(b) * P.heads + h) * A.segs + seg] = all_of.parts(lost).power();
     }
   } else if (warp == 10) {
-    // ---- issuing P, O1, O2
+    // ---- issuing O1 and O2
     if constexpr (OUT) {
-      constexpr uint32_t kIdP = rows_desc<DT>(kChunk, false, false), kIdO2 = rows_desc<DT>(kChunk, true, false);
+      constexpr uint32_t kId1 = rows_desc<DT>(kChunk, false, false), kId2 = rows_desc<DT>(kChunk, true, false);
       const uint64_t q_desc = matrix_desc(smem_u32(smem + S::kQ), 16, 1024, kSwizzle128);
-      const uint64_t k_desc = matrix_desc(smem_u32(smem + S::kK), 16, 1024, kSwizzle128);
       const uint64_t v_desc = matrix_desc(smem_u32(smem + S::kV), S::kHalf, 1024, kSwizzle128);
       const uint64_t a_desc = matrix_desc(smem_u32(smem + S::kA), 16, 1024, kSwizzle128);
-      int np = 0, n1 = 0, n2 = 0;
+      int n1 = 0, n2 = 0;
 #pragma unroll 1
-      for (int c = -1; c < chunks; ++c) {  // O1 of a chunk, P of the next, O2 of the chunk
-        if (c >= 0) {
-          const int sq = c % S::kStagesQ;
-          if (!warp_wait(&sm.s_full, c & 1, dead)) break;
-          if (c > 0 && !warp_wait(&sm.o_empty, (c - 1) & 1, dead)) break;
-          tc_fence_after();
-          if (elect_one()) {
+      for (int c = 0; c < chunks; ++c) {
+        const int sv = c % S::kStagesV;
+        if (!wait4(sm.full, c)) break;
+        if (!warp_wait(&sm.s_full, c & 1, dead)) break;
+        tc_fence_after();
+        if (elect_one()) {  // (into the half that chunk c - 2 left: its outputs were waited for before the last O2)
+#pragma unroll 1
+          for (int x = 0; x < DK / 32; ++x) {  // a piece's 64 columns of a half of Q
+            const uint32_t piece = tmem + (x & 1 ? kSLo : kSHi) + (x >> 1) * 32;
+            const uint64_t q = q_desc + ((sv * S::kTileK + (x >> 1) * S::kHalf) >> 4);
 #pragma unroll
-            for (int piece = 0; piece < 2; ++piece)
-#pragma unroll
-              for (int k = 0; k < DK / 16; ++k)
-                mma_f16_ta(tmem + kO1, tmem + (piece ? kSLo : kSHi) + k * 8, q_desc + ((sq * S::kTileK + k / 4 * S::kHalf + k % 4 * 32) >> 4),
-                           kIdP, piece + k > 0);
-            tc_commit(&sm.q_empty[sq]);
-            tc_commit(&sm.s_empty);
+            for (int k = 0; k < 4; ++k) mma_f16_ta(tmem + kO1 + (c & 1) * 64, piece + k * 8, q + 2 * k, kId1, x + k > 0);
           }
-          __syncwarp();
-          ++n1;
+          tc_commit(&sm.o1_full[c & 3]);
         }
-        if (c + 1 < chunks) {
-          const int d = c + 1, sk = d % S::kStagesK, sq = d % S::kStagesQ;
-          if (d >= 2 && !warp_wait(&sm.p_empty[d & 1], (d / 2 - 1) & 1, dead)) break;
-          if (!warp_wait(&sm.k_full[sk], (d / S::kStagesK) & 1, dead)) break;
-          if (!warp_wait(&sm.q_full[sq], (d / S::kStagesQ) & 1, dead)) break;
-          tc_fence_after();
-          if (elect_one()) {
+        __syncwarp();
+        ++n1;
+        if (!warp_wait(&sm.a_full, c & 1, dead)) break;
+        if (c > 0 && !warp_wait(&sm.o_empty, (c - 1) & 1, dead)) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll 1
+          for (int piece = 0; piece < 2; ++piece) {
+            const uint64_t v = v_desc + ((sv * S::kTileV) >> 4), a = a_desc + ((piece * S::kHalf) >> 4);
 #pragma unroll
-            for (int k = 0; k < DK / 16; ++k)
-              mma_f16_ss(tmem + kP + (d & 1) * 64, q_desc + ((sq * S::kTileK + k / 4 * S::kHalf + k % 4 * 32) >> 4),
-                         k_desc + ((sk * S::kTileK + k / 4 * S::kHalf + k % 4 * 32) >> 4), kIdP, k > 0);
-            tc_commit(&sm.k_empty[sk]);
-            tc_commit(&sm.p_full[d & 1]);
+            for (int k = 0; k < 4; ++k) mma_f16_ss(tmem + kO2, v + 128 * k, a + 2 * k, kId2, piece + k > 0);
           }
-          __syncwarp();
-          ++np;
+          tc_commit(&sm.o2_full[c & 3]);
         }
-        if (c >= 0) {
-          const int sv = c % S::kStagesV;
-          if (!warp_wait(&sm.v_full[sv], (c / S::kStagesV) & 1, dead)) break;
-          if (!warp_wait(&sm.a_full, c & 1, dead)) break;
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int piece = 0; piece < 2; ++piece)
-#pragma unroll
-              for (int k = 0; k < kChunk / 16; ++k)
-                mma_f16_ss(tmem + kO2, v_desc + ((sv * S::kTileV + k * 2048) >> 4), a_desc + ((piece * S::kHalf + k * 32) >> 4), kIdO2,
-                           piece + k > 0);
-            tc_commit(&sm.v_empty[sv]);
-            tc_commit(&sm.a_empty);
-            tc_commit(&sm.o_full);
-          }
-          __syncwarp();
-          ++n2;
-        }
+        __syncwarp();
+        ++n2;
       }
-      if (lane == 0) sm.products_p = np, sm.products_o1 = n1, sm.products_o2 = n2;
+      if (lane == 0) sm.products_o1 = n1, sm.products_o2 = n2;
     }
   } else if (warp == 11) {
-    // ---- issuing dS
-    constexpr uint32_t kId = rows_desc<DT>(DK, true, true);
+    // ---- issuing P and dS
+    constexpr uint32_t kIdP = rows_desc<DT>(kChunk, false, false), kIdS = rows_desc<DT>(DK, true, true);
+    const uint64_t q_desc = matrix_desc(smem_u32(smem + S::kQ), 16, 1024, kSwizzle128);
+    const uint64_t k_desc = matrix_desc(smem_u32(smem + S::kK), 16, 1024, kSwizzle128);
     const uint64_t v_desc = matrix_desc(smem_u32(smem + S::kV), S::kHalf, 1024, kSwizzle128);
     const uint64_t kt_desc = matrix_desc(smem_u32(smem + S::kKt), S::kHalf, 1024, kSwizzle128);
-    int n = 0;
-    for (int c = 0; c < chunks; ++c) {
-      const int sv = c % S::kStagesV;
-      if (!warp_wait(&sm.v_full[sv], (c / S::kStagesV) & 1, dead)) break;
-      if (c >= updates) {
-        if (lane == 0) bar_arrive(&sm.v_empty[sv]);
-        continue;
-      }
-      if (!warp_wait(&sm.kt_full[c & 1], (c >> 1) & 1, dead)) break;
-      if (c > 0 && !warp_wait(&sm.ds_empty, (c - 1) & 1, dead)) break;
-      tc_fence_after();
-      if (elect_one()) {
+    int np = 0, ns = 0;
+#pragma unroll 1
+    for (int c = -1; c < chunks; ++c) {  // dS of a chunk, P of the next
+      if (c >= 0 && c < updates) {
+        if (!OUT && !wait4(sm.full, c)) break;
+        if (!warp_wait(&sm.kt_full[c & 1], c >> 1 & 1, dead)) break;
+        if (c > 0 && !warp_wait(&sm.ds_empty, (c - 1) & 1, dead)) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll 1
+          for (int piece = 0; piece < 2; ++piece) {
+            const uint64_t v = v_desc + ((c % S::kStagesV * S::kTileV) >> 4), kt = kt_desc + ((((c & 1) * 2 + piece) * S::kTileK) >> 4);
 #pragma unroll
-        for (int piece = 0; piece < 2; ++piece)
-#pragma unroll
-          for (int k = 0; k < kChunk / 16; ++k)
-            mma_f16_ss(tmem + kDS, v_desc + ((sv * S::kTileV + k * 2048) >> 4),
-                       kt_desc + ((((c & 1) * 2 + piece) * S::kTileK + k * 2048) >> 4), kId, piece + k > 0);
-        tc_commit(&sm.kt_empty[c & 1]);
-        tc_commit(&sm.v_empty[sv]);
-        tc_commit(&sm.ds_full);
+            for (int k = 0; k < 4; ++k) mma_f16_ss(tmem + kDS, v + 128 * k, kt + 128 * k, kIdS, piece + k > 0);
+          }
+          tc_commit(&sm.ds_full[c & 3]);
+        }
+        __syncwarp();
+        ++ns;
       }
-      __syncwarp();
-      ++n;
+      if (OUT && c + 1 < chunks) {
+        const int d = c + 1, sk = d % S::kStagesK, sq = d % S::kStagesV;
+        if (!wait4(sm.full, d)) break;
+        if (c >= 0 && !warp_wait(&sm.p_empty, c & 1, dead)) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll 1
+          for (int x = 0; x < DK / 64; ++x) {
+            const uint64_t q = q_desc + ((sq * S::kTileK + x * S::kHalf) >> 4), k0 = k_desc + ((sk * S::kTileK + x * S::kHalf) >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_f16_ss(tmem + kP, q + 2 * k, k0 + 2 * k, kIdP, x + k > 0);
+          }
+          tc_commit(&sm.p_full[d & 3]);
+        }
+        __syncwarp();
+        ++np;
+      }
     }
-    if (lane == 0) sm.products_s = n;
+    if (lane == 0) sm.products_p = np, sm.products_s = ns;
   } else if (warp >= 12) {
     // ---- the state: half of a lane's row to a thread, in pairs of columns
     constexpr int OWN = DK / 2;
@@ -505,7 +482,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         f = pack2(fit, fit);
         if (half == 0) sm.d[c % kDecayRing].sfac[at] = back;
       }
-      if (c > 0 && !warp_wait(&sm.s_empty, (c - 1) & 1, dead)) return false;
+      if (c > 0 && !wait4(sm.o1_full, c - 1)) return false;
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < OWN / 16; ++k) {
@@ -520,14 +497,76 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       warp_arrive(&sm.s_full, lane);
       return true;
     };
+    // K' of chunk c
+    const int own = (warp - 12) * 32 + lane, row = own & 63, part = own >> 6;  // a quarter of a row to a thread
+    auto keys = [&](int c) -> bool {
+      const int r = c % kDecayRing, sk = c % S::kStagesK, m = min(kChunk, len - (c0 + c) * kChunk);
+      if (!warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead)) return false;
+      if (!wait4(sm.full, c)) return false;
+      if (c < updates) {
+        if (c >= 2 && !wait4(sm.ds_full, c - 2)) return false;
+        float left = sm.d[r].left[row];
+        const bool past = row >= m;
+        constexpr int kPieces = DK / 32;  // 16-byte pieces to a thread
+        const int base = DK == 128 ? (part >> 1) * S::kHalf + row * 128 : row * 128, first = DK == 128 ? (part & 1) * 4 : part * 2;
+        const char *from = smem + S::kK + sk * S::kTileK + base;
+        char *to = smem + S::kKt + (c & 1) * 2 * S::kTileK + base;
+        if constexpr (F16) {
+          uint32_t most = 0;
+#pragma unroll 2
+          for (int e = 0; e < kPieces; ++e) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(from + (((first + e) ^ (row & 7)) << 4));
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) most = max(most, max(w[y] & 0x7fffu, w[y] >> 16 & 0x7fffu));
+          }
+          const uint32_t mine = past ? 0u : __float_as_uint(fabsf(__half2float(__ushort_as_half(static_cast<uint16_t>(most))) * left)) & 0x7fffffffu;
+          const uint32_t warps = __reduce_max_sync(~0u, mine);
+          if (lane == 0) sm.kmax[c & 1][warp - 12] = warps;
+          warp_arrive(&sm.meet_k, lane);
+          if (!warp_wait(&sm.meet_k, c & 1, dead)) return false;
+          const uint32_t *km = sm.kmax[c & 1];
+          float back;
+          left *= fit_half(max(max(max(km[0], km[1]), max(km[2], km[3])), max(max(km[4], km[5]), max(km[6], km[7]))), back);
+          if (own == 0) sm.d[r].kfac = back;
+        }
+        const pair_t f = pack2(left, left);
+#pragma unroll 2
+        for (int e = 0; e < kPieces; ++e) {
+          const int o = ((first + e) ^ (row & 7)) << 4;
+          const uint4 x = *reinterpret_cast<const uint4 *>(from + o);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float2 k = widen2<DT>(w[y]);
+            split2<DT>(mul2(pack2(k.x, k.y), f), hi[y], lo[y]);
+            if (past) hi[y] = lo[y] = 0;
+          }
+          *reinterpret_cast<uint4 *>(to + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4 *>(to + S::kTileK + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        if (m < kChunk) {
+          const int sv = c % S::kStagesV;
+          for (int e = own; e < (kChunk - m) * 16; e += 256)
+            *reinterpret_cast<uint4 *>(smem + S::kV + sv * S::kTileV + (e & 1) * S::kHalf + (m + (e >> 4)) * 128 + (e >> 1 & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_shared();
+        warp_arrive(&sm.kt_full[c & 1], lane);
+      }
+      warp_arrive(&sm.k_read[c & 3], lane);
+      return true;
+    };
     bool going = true;
 #pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
+    for (int c = -2; c < chunks; ++c) {
       const int r = c % kDecayRing;
-      if (OUT && !(going = hand_on(c))) break;
+      if (OUT && c >= 0 && !(going = hand_on(c))) break;
+      if (c + 2 < chunks && !(going = keys(c + 2))) break;
+      if (c < 0) continue;
       if (!(going = warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead))) break;
       if (c < updates) {
-        if (!(going = warp_wait(&sm.ds_full, c & 1, dead))) break;
+        if (!(going = wait4(sm.ds_full, c))) break;
         tc_fence_after();
         const float lam = sm.d[r].lam, kf = F16 ? sm.d[r].kfac : 1.0f;
         const pair_t l2 = pack2(lam, lam), k2 = pack2(kf, kf);
@@ -573,7 +612,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       for (int c = 0; c < chunks; ++c) {
         const int r = c % kDecayRing, m = min(kChunk, len - (c0 + c) * kChunk);
         if (!warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead)) break;
-        if (!warp_wait(&sm.p_full[c & 1], (c >> 1) & 1, dead)) break;
+        if (!wait4(sm.p_full, c)) break;
         tc_fence_after();
         const ChunkSmall::Decays &d = sm.d[r];
         // which of the half's rows this one follows
@@ -582,7 +621,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         float back = 1.0f;
         if (__any_sync(~0u, sees != 0)) {
           float x[32];
-          tmem_ld32(tmem + (static_cast<uint32_t>(warp & 3) << 21) + kP + (c & 1) * 64 + j0, x);
+          tmem_ld32(tmem + (static_cast<uint32_t>(warp & 3) << 21) + kP + j0, x);
           const float mh = -d.nhi[i], ml = -d.nlo[i];
           const pair_t h2 = pack2(mh, mh), l2 = pack2(ml, ml);
           const bool every = __all_sync(~0u, sees == ~0u);
@@ -610,7 +649,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int e = 0; e < 16; ++e)
             if constexpr (!F16) split2<DT>(y[e], hi[e], lo[e]);
           tc_fence_before();
-          warp_arrive(&sm.p_empty[c & 1], lane);
+          warp_arrive(&sm.p_empty, lane);
           if constexpr (F16) {
             warp_arrive(&sm.meet_a, lane);
             if (!warp_wait(&sm.meet_a, met++ & 1, dead)) break;
@@ -620,7 +659,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             for (int e = 0; e < 16; ++e) split2<DT>(mul2(y[e], f), hi[e], lo[e]);
           }
         } else {
-          warp_arrive(&sm.p_empty[c & 1], lane);
+          warp_arrive(&sm.p_empty, lane);
           if constexpr (F16) {
             sm.amax[c & 1][half][i] = 0;
             warp_arrive(&sm.meet_a, lane);
@@ -631,7 +670,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0;
         }
         if (F16 && half == 0) sm.d[r].afac[i] = back * P.scale;
-        if (c > 0 && !warp_wait(&sm.a_empty, (c - 1) & 1, dead)) break;
+        if (c > 0 && !wait4(sm.o2_full, c - 1)) break;
         char *row = smem + S::kA + i * 128;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -641,7 +680,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         if (m < kChunk) {  // values past the request's rows take no part, whatever they are
           const int sv = c % S::kStagesV;
-          if (!warp_wait(&sm.v_full[sv], (c / S::kStagesV) & 1, dead)) break;
+          if (!wait4(sm.full, c)) break;
           for (int e = group; e < (kChunk - m) * 16; e += 128)
             *reinterpret_cast<uint4 *>(smem + S::kV + sv * S::kTileV + (e & 1) * S::kHalf + (m + (e >> 4)) * 128 + (e >> 1 & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
@@ -651,91 +690,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
     }
   } else {
-    // ---- K', two chunks ahead, and the outputs
+    // ---- the outputs
     const int quarter = warp & 3, at = quarter * 32 + lane;
-    const int row = at & 63, part = at >> 6;  // K': a row's 64 columns (a half of the tile), or half of them
-    int met = 0;
-    auto keys = [&](int c) -> bool {
-      const int r = c % kDecayRing, sk = c % S::kStagesK, m = min(kChunk, len - (c0 + c) * kChunk);
-      if (!warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead)) return false;
-      if (!warp_wait(&sm.k_full[sk], (c / S::kStagesK) & 1, dead)) return false;
-      if (c < updates) {
-        if (c >= 2 && !warp_wait(&sm.kt_empty[c & 1], (c / 2 - 1) & 1, dead)) return false;
-        float left = sm.d[r].left[row];
-        const bool past = row >= m;
-        constexpr int kPieces = DK / 16;  // 16-byte pieces to a thread
-        const int base = DK == 128 ? part * S::kHalf + row * 128 : row * 128, first = DK == 128 ? 0 : part * 4;
-        const char *from = smem + S::kK + sk * S::kTileK + base;
-        char *to = smem + S::kKt + (c & 1) * 2 * S::kTileK + base;
-        if constexpr (F16) {
-          uint32_t most = 0;
-#pragma unroll 2
-          for (int e = 0; e < kPieces; ++e) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(from + (((first + e) ^ (row & 7)) << 4));
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) most = max(most, max(w[y] & 0x7fffu, w[y] >> 16 & 0x7fffu));
-          }
-          const uint32_t mine = past ? 0u : __float_as_uint(fabsf(__half2float(__ushort_as_half(static_cast<uint16_t>(most))) * left)) & 0x7fffffffu;
-          const uint32_t warps = __reduce_max_sync(~0u, mine);
-          if (lane == 0) sm.kmax[c & 1][quarter] = warps;
-          warp_arrive(&sm.meet_k, lane);
-          if (!warp_wait(&sm.meet_k, met++ & 1, dead)) return false;
-          const uint32_t *km = sm.kmax[c & 1];
-          float back;
-          left *= fit_half(max(max(km[0], km[1]), max(km[2], km[3])), back);
-          if (at == 0) sm.d[r].kfac = back;
-        }
-        const pair_t f = pack2(left, left);
-#pragma unroll 2
-        for (int e = 0; e < kPieces; ++e) {
-          const int o = ((first + e) ^ (row & 7)) << 4;
-          const uint4 x = *reinterpret_cast<const uint4 *>(from + o);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float2 k = widen2<DT>(w[y]);
-            split2<DT>(mul2(pack2(k.x, k.y), f), hi[y], lo[y]);
-            if (past) hi[y] = lo[y] = 0;
-          }
-          *reinterpret_cast<uint4 *>(to + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4 *>(to + S::kTileK + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-        if (m < kChunk) {
-          const int sv = c % S::kStagesV;
-          if (!warp_wait(&sm.v_full[sv], (c / S::kStagesV) & 1, dead)) return false;
-          for (int e = at; e < (kChunk - m) * 16; e += 128)
-            *reinterpret_cast<uint4 *>(smem + S::kV + sv * S::kTileV + (e & 1) * S::kHalf + (m + (e >> 4)) * 128 + (e >> 1 & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_async_shared();
-        warp_arrive(&sm.kt_full[c & 1], lane);
-      }
-      warp_arrive(&sm.k_empty[sk], lane);
-      if (!OUT) warp_arrive(&sm.dec_empty[r], lane);
-      return true;
-    };
-    bool going = true;
     if constexpr (OUT) {
       const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
       const int dv = dv0 + at;
       uint16_t *out = reinterpret_cast<uint16_t *>(P.out) + b * P.os[0] + h * P.os[2] + dv;
+      const bool odd = lane & 1;
 #pragma unroll 1
-      for (int c = -2; c < chunks; ++c) {
-        if (c + 2 < chunks && !(going = keys(c + 2))) break;
-        if (c < 0) continue;
+      for (int c = 0; c < chunks; ++c) {
         const int r = c % kDecayRing, t0 = (c0 + c) * kChunk, m = min(kChunk, len - t0);
-        if (!(going = warp_wait(&sm.o_full, c & 1, dead))) break;
+        if (!wait4(sm.o2_full, c)) break;
         tc_fence_after();
         const ChunkSmall::Decays &d = sm.d[r];
         const float sf = F16 ? d.sfac[at] : 1.0f;
         const pair_t sf2 = pack2(sf, sf), scale2 = pack2(P.scale, P.scale), none = 0;
         pair_t bad = 0;
-        uint16_t *o = out + t0 * P.os[1];
+        char *o = reinterpret_cast<char *>(out + (t0 + odd) * P.os[1] - odd);  // two columns of every other row to a lane
 #pragma unroll 1
         for (int k = 0; k < kChunk; k += 16) {
           float x[16], y[16];
-          tmem_ld16(tmem + lanes + kO1 + k, x);
+          tmem_ld16(tmem + lanes + kO1 + (c & 1) * 64 + k, x);
           tmem_ld16(tmem + lanes + kO2 + k, y);
           tc_wait_ld();
           if (k + 16 > m) [[unlikely]] {
@@ -756,10 +731,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               const pair_t o2 = pack2(y[z], y[z + 1]);
               bad = fma2(o2, none, bad);
               const uint32_t u2 = narrow2<DT>(unpack2(fma2(pack2(x[z], x[z + 1]), f, mul2(o2, F16 ? (w ? af.y : af.x) : scale2))));
-              if (store && k + z < m) o[0] = static_cast<uint16_t>(u2);
-              o += P.os[1];
-              if (store && k + z + 1 < m) o[0] = static_cast<uint16_t>(u2 >> 16);
-              o += P.os[1];
+              const uint32_t other = __shfl_xor_sync(~0u, u2, 1);
+              if (store && k + z + odd < m) *reinterpret_cast<uint32_t *>(o) = odd ? __byte_perm(other, u2, 0x7632) : __byte_perm(u2, other, 0x5410);
+              o += P.os[1] * 4;
             }
           }
         }
@@ -769,7 +743,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int i = 0; i < m; ++i) {
             const uint64_t sees = P.parents ? static_cast<uint64_t>(sm.follows[i][1]) << 32 | sm.follows[i][0] : (2ull << i) - 1;
             float x[8];
-            tmem_ld8(tmem + lanes + kO1 + (i & ~7), x);
+            tmem_ld8(tmem + lanes + kO1 + (c & 1) * 64 + (i & ~7), x);
             tc_wait_ld();
             float v = x[0];
 #pragma unroll
@@ -788,15 +762,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       uint16_t *o = reinterpret_cast<uint16_t *>(P.out) + b * P.os[0] + h * P.os[2] + dv0;
       for (int64_t e = at; e < (z1 - z0) * pieces; e += 128)
         *reinterpret_cast<uint4 *>(o + (len + z0 + e / pieces) * P.os[1] + e % pieces * 8) = make_uint4(0, 0, 0, 0);
-    } else {
-      for (int c = 0; going && c < chunks; ++c) going = keys(c);
     }
   }
 
   tc_fence_before();
   __syncthreads();
   if (*dead) [[unlikely]] {  // nothing that was begun may reach shared or tensor memory that the CTA has left (else all was waited for)
-    if (warp == 0) land_chunks<DK, OUT>(sm);
+    if (warp == 0) land_chunks(sm);
     __syncthreads();
     if (tid == 0 && P.status) atomicMax(&P.status[b], SPEC_STATUS_TIMEOUT);
   }
