@@ -34,7 +34,7 @@ namespace {
 //
 // Warps (their number modulo 4 is the quarter of the lanes that they can reach,
 // and their scheduler): 2 loads, 3 decays, 10 issues O1 and O2, 11 issues P and dS;
-// 4, 5, 8, 9 make A; 0, 1, 6, 7 write the outputs; 12 to 19 hold S and make K',
+// 4, 5, 8, 9 make A; 0, 1, 6, 7 write the outputs; 12 to 27 hold S and make K',
 // two chunks ahead.  The code of the roles is kept short, one site to each and
 // loops rolled where registers allow: unrolled further, warps waited for their
 // instructions (a chunk 7,700 cycles, not 5,300).
@@ -44,7 +44,8 @@ namespace {
 // turns that into the state before each, and the main launch has a CTA for
 // every segment.
 constexpr int kChunk = 64;
-constexpr int kChunkThreads = 640;
+constexpr int kChunkThreads = 896;
+constexpr int kStateWarps = 16;
 constexpr int kDecayRing = 4;
 
 template <int DK, bool OUT>
@@ -60,7 +61,7 @@ struct ChunkShape {
   static constexpr int kKt = kV + kStagesV * kTileV;
   static constexpr int kA = kKt + 2 * 2 * kTileK;
   static constexpr int kSmall = kA + (OUT ? 2 * kHalf : 0);
-  static constexpr int kBytes = kSmall + 12288 + 1024;  // (1024: alignment of the base)
+  static constexpr int kBytes = kSmall + 14336 + 1024;  // (1024: alignment of the base)
 };
 
 struct ChunkSmall {
@@ -74,7 +75,7 @@ struct ChunkSmall {
     float kfac;                      // fp16: what K' was divided by
   } d[kDecayRing];
   uint32_t follows[kChunk][2];  // trees: the rows that a row follows, itself among them
-  uint32_t smax[2][2][128], amax[2][2][kChunk], kmax[2][8];  // (by the chunk's number: the next one's may be written before these are read)
+  uint32_t smax[2][4][128], amax[2][2][kChunk], kmax[2][kStateWarps];  // (by the chunk's number: the next one's may be written before these are read)
   // One barrier for each product, counted by chunk (four of them in turn, so that whoever waits for a chunk's phase is never a
   // lap behind): that P, O1, O2, dS are there, and so that their operands are free.
   uint64_t p_full[4], o1_full[4], o2_full[4], ds_full[4];
@@ -85,7 +86,7 @@ struct ChunkSmall {
   int dead;
   int copies, products_p, products_o1, products_o2, products_s;  // how many were begun
 };
-static_assert(sizeof(ChunkSmall) <= 12288);
+static_assert(sizeof(ChunkSmall) <= 14336);
 
 // Arrival of a warp whose lanes have all done what the barrier stands for.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
@@ -235,13 +236,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      bar_init(&sm.full[i], 1), bar_init(&sm.k_read[i], 8);
+      bar_init(&sm.full[i], 1), bar_init(&sm.k_read[i], kStateWarps);
       bar_init(&sm.p_full[i], 1), bar_init(&sm.o1_full[i], 1), bar_init(&sm.o2_full[i], 1), bar_init(&sm.ds_full[i], 1);
     }
-    for (int i = 0; i < 2; ++i) bar_init(&sm.kt_full[i], 8);
-    bar_init(&sm.p_empty, 4), bar_init(&sm.a_full, 4), bar_init(&sm.ds_empty, 8), bar_init(&sm.s_full, 8), bar_init(&sm.o_empty, 4);
-    for (int i = 0; i < kDecayRing; ++i) bar_init(&sm.dec_full[i], 1), bar_init(&sm.dec_empty[i], OUT ? 16 : 8);
-    bar_init(&sm.meet_s, 8), bar_init(&sm.meet_a, 4), bar_init(&sm.meet_k, 8);
+    for (int i = 0; i < 2; ++i) bar_init(&sm.kt_full[i], kStateWarps);
+    bar_init(&sm.p_empty, 4), bar_init(&sm.a_full, 4), bar_init(&sm.ds_empty, kStateWarps), bar_init(&sm.s_full, kStateWarps), bar_init(&sm.o_empty, 4);
+    for (int i = 0; i < kDecayRing; ++i) bar_init(&sm.dec_full[i], 1), bar_init(&sm.dec_empty[i], OUT ? kStateWarps + 8 : kStateWarps);
+    bar_init(&sm.meet_s, kStateWarps), bar_init(&sm.meet_a, 4), bar_init(&sm.meet_k, kStateWarps);
     bar_init_fence();
     sm.dead = 0;
     sm.copies = sm.products_p = sm.products_o1 = sm.products_o2 = sm.products_s = 0;
@@ -441,9 +442,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     if (lane == 0) sm.products_p = np, sm.products_s = ns;
   } else if (warp >= 12) {
-    // ---- the state: half of a lane's row to a thread, in pairs of columns
-    constexpr int OWN = DK / 2;
-    const int half = (warp - 12) >> 2, at = (warp & 3) * 32 + lane, dv = dv0 + at;
+    // ---- the state: a quarter of a lane's row to a thread, in pairs of columns
+    constexpr int OWN = DK / 4;
+    const int four = (warp - 12) >> 2, at = (warp & 3) * 32 + lane, dv = dv0 + at;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     const int64_t size = static_cast<int64_t>(P.key_dim) * P.value_dim;
     pair_t s[OWN / 2];
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (from && ok && dv < P.value_dim) {
 #pragma unroll
       for (int e = 0; e < OWN / 2; ++e) {
-        const int d = half * OWN + 2 * e;
+        const int d = four * OWN + 2 * e;
         if (d < P.key_dim) s[e] = pack2(from[static_cast<int64_t>(d) * P.value_dim + dv], from[static_cast<int64_t>(d + 1) * P.value_dim + dv]);
       }
     }
@@ -474,13 +475,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const float2 x = unpack2(s[e]);
           most = max(most, max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu));
         }
-        sm.smax[c & 1][half][at] = most;
+        sm.smax[c & 1][four][at] = most;
         warp_arrive(&sm.meet_s, lane);
         if (!warp_wait(&sm.meet_s, met++ & 1, dead)) return false;
         float back;
-        const float fit = fit_half(max(most, sm.smax[c & 1][half ^ 1][at]), back);
+        const auto &tops = sm.smax[c & 1];
+        const float fit = fit_half(max(max(tops[0][at], tops[1][at]), max(tops[2][at], tops[3][at])), back);
         f = pack2(fit, fit);
-        if (half == 0) sm.d[c % kDecayRing].sfac[at] = back;
+        if (four == 0) sm.d[c % kDecayRing].sfac[at] = back;
       }
       if (c > 0 && !wait4(sm.o1_full, c - 1)) return false;
       tc_fence_after();
@@ -489,8 +491,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) split2<DT>(F16 ? mul2(s[8 * k + e], f) : s[8 * k + e], hi[e], lo[e]);
-        tmem_st8(tmem + lanes + kSHi + half * (OWN / 2) + k * 8, hi);
-        tmem_st8(tmem + lanes + kSLo + half * (OWN / 2) + k * 8, lo);
+        tmem_st8(tmem + lanes + kSHi + four * (OWN / 2) + k * 8, hi);
+        tmem_st8(tmem + lanes + kSLo + four * (OWN / 2) + k * 8, lo);
       }
       tc_wait_st();
       tc_fence_before();
@@ -498,7 +500,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       return true;
     };
     // K' of chunk c
-    const int own = (warp - 12) * 32 + lane, row = own & 63, part = own >> 6;  // a quarter of a row to a thread
+    const int own = (warp - 12) * 32 + lane, row = own & 63, part = own >> 6;  // an eighth of a row to a thread
     auto keys = [&](int c) -> bool {
       const int r = c % kDecayRing, sk = c % S::kStagesK, m = min(kChunk, len - (c0 + c) * kChunk);
       if (!warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead)) return false;
@@ -507,8 +509,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (c >= 2 && !wait4(sm.ds_full, c - 2)) return false;
         float left = sm.d[r].left[row];
         const bool past = row >= m;
-        constexpr int kPieces = DK / 32;  // 16-byte pieces to a thread
-        const int base = DK == 128 ? (part >> 1) * S::kHalf + row * 128 : row * 128, first = DK == 128 ? (part & 1) * 4 : part * 2;
+        constexpr int kPieces = DK / 64;  // 16-byte pieces to a thread
+        const int base = DK == 128 ? (part >> 2) * S::kHalf + row * 128 : row * 128, first = DK == 128 ? (part & 3) * 2 : part;
         const char *from = smem + S::kK + sk * S::kTileK + base;
         char *to = smem + S::kKt + (c & 1) * 2 * S::kTileK + base;
         if constexpr (F16) {
@@ -525,9 +527,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (lane == 0) sm.kmax[c & 1][warp - 12] = warps;
           warp_arrive(&sm.meet_k, lane);
           if (!warp_wait(&sm.meet_k, c & 1, dead)) return false;
-          const uint32_t *km = sm.kmax[c & 1];
+          const uint32_t top = __reduce_max_sync(~0u, sm.kmax[c & 1][lane & (kStateWarps - 1)]);
           float back;
-          left *= fit_half(max(max(max(km[0], km[1]), max(km[2], km[3])), max(max(km[4], km[5]), max(km[6], km[7]))), back);
+          left *= fit_half(top, back);
           if (own == 0) sm.d[r].kfac = back;
         }
         const pair_t f = pack2(left, left);
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         if (m < kChunk) {
           const int sv = c % S::kStagesV;
-          for (int e = own; e < (kChunk - m) * 16; e += 256)
+          for (int e = own; e < (kChunk - m) * 16; e += 32 * kStateWarps)
             *reinterpret_cast<uint4 *>(smem + S::kV + sv * S::kTileV + (e & 1) * S::kHalf + (m + (e >> 4)) * 128 + (e >> 1 & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_async_shared();
@@ -573,7 +575,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
         for (int k = 0; k < OWN / 16; ++k) {
           float x[16];
-          tmem_ld16(tmem + lanes + kDS + half * OWN + k * 16, x);
+          tmem_ld16(tmem + lanes + kDS + four * OWN + k * 16, x);
           tc_wait_ld();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -596,7 +598,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (to && dv < P.value_dim) {
 #pragma unroll
       for (int e = 0; e < OWN / 2; ++e) {
-        const int d = half * OWN + 2 * e;
+        const int d = four * OWN + 2 * e;
         const float2 x = unpack2(s[e]);
         if (d < P.key_dim) to[static_cast<int64_t>(d) * P.value_dim + dv] = x.x, to[static_cast<int64_t>(d + 1) * P.value_dim + dv] = x.y;
       }
