@@ -36,13 +36,15 @@ struct StateParams {
 };
 
 // A call of the tensor-core kernels: each request's chunks cut into segs runs, the states before all but the first of them from
-// a launch of their own.
+// a launch of their own, which has parts CTAs for each run but the last.
 struct StateChunkPlan {
   StateParams p;
-  int segs, launch_segs;
+  int segs, parts, pieces;  // pieces: of a request, a launch's
   int *verdict;   // [B] the requests' status
-  float *total;   // [B][heads][segs] the decay over a segment
-  float *local;   // [B][heads][segs][key_dim][value_dim] what a segment adds to zeros; then the state before it
+  int *order;     // [B] the requests, longest first
+  float *total;   // [B][heads][slots] the decay over a part
+  float *local;   // [B][heads][slots][key_dim][value_dim] what a part adds to zeros; then, where a run begins, the state before it
+  __host__ __device__ int slots() const { return (segs - 1) * parts + 1; }
 };
 
 // Whether the states written lie where some are read: such a call is not the same call when it is made again.

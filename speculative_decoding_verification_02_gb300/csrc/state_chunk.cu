@@ -1,6 +1,7 @@
 // Linear attention on the tensor cores: which calls, the launches around the
 // main one (state_chunk.cuh).
 #include <algorithm>
+#include <utility>
 
 #include "launch.h"
 #include "state.cuh"
@@ -10,9 +11,18 @@ namespace {
 
 constexpr int kChunkRows = 64;
 
+__device__ __forceinline__ int block_sum64(int x) {
+  __shared__ int part[2];
+  x = __reduce_add_sync(~0u, x);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+  __syncthreads();
+  return part[0] + part[1];
+}
+
 // Each request's status, before any of its units runs: several CTAs share a
 // request, and one that gave up a wait must not be overwritten by another's OK.
-__global__ void __launch_bounds__(64) state_verdict_kernel(const StateParams P, int *verdict) {
+// And the requests' order, longest first, so that the launch's last CTAs are short.
+__global__ void __launch_bounds__(64) state_verdict_kernel(const StateParams P, int *verdict, int *order) {
   const int b = blockIdx.x, tid = threadIdx.x;
   bool ok = true;
   state_slot(P.from, b, true, ok);
@@ -24,7 +34,12 @@ __global__ void __launch_bounds__(64) state_verdict_kernel(const StateParams P, 
     const int p = tid < count ? P.parents[static_cast<int64_t>(b) * P.n + tid] : -1;
     if (__syncthreads_or(tid < count && (tid == 0 ? p != -1 : p < 0 || p >= tid))) status = SPEC_STATUS_BAD_TREE;
   }
+  int before = 0;
+  if (P.counts)
+    for (int i = tid; i < P.B; i += 64) before += P.counts[i] > count || (P.counts[i] == count && i < b);
+  before = P.counts ? block_sum64(before) : b;
   if (tid == 0) {
+    order[before] = b;
     verdict[b] = status;
     if (P.status) P.status[b] = status;
   }
@@ -43,17 +58,14 @@ __global__ void __launch_bounds__(256) state_join_kernel(const StateChunkPlan A)
     const int slot = P.from.slots ? P.from.slots[b] : b;
     if (slot >= 0) s = *reinterpret_cast<const float4 *>(P.from.state + slot * P.from.slot_stride + static_cast<int64_t>(h) * size + e);
   }
-  float *p = A.local + static_cast<int64_t>(unit) * A.segs * size + e;
-  for (int g = 0; g < A.segs; ++g, p += size) {
-    float4 x = {};
-    float f = 0.0f;
-    if (g + 1 < A.segs) {
-      x = *reinterpret_cast<const float4 *>(p);
-      f = A.total[static_cast<int64_t>(unit) * A.segs + g];
-    }
-    *reinterpret_cast<float4 *>(p) = s;
-    s = make_float4(fmaf(s.x, f, x.x), fmaf(s.y, f, x.y), fmaf(s.z, f, x.z), fmaf(s.w, f, x.w));
+  float *p = A.local + static_cast<int64_t>(unit) * A.slots() * size + e;
+  const float *f = A.total + static_cast<int64_t>(unit) * A.slots();
+  for (int g = 0; g + 1 < A.slots(); ++g, p += size) {
+    const float4 x = *reinterpret_cast<const float4 *>(p);
+    if (g % A.parts == 0) *reinterpret_cast<float4 *>(p) = s;
+    s = make_float4(fmaf(s.x, f[g], x.x), fmaf(s.y, f[g], x.y), fmaf(s.z, f[g], x.z), fmaf(s.w, f[g], x.w));
   }
+  *reinterpret_cast<float4 *>(p) = s;
 }
 
 int value_blocks(const StateParams &P) { return (P.value_dim + 127) / 128; }
@@ -65,7 +77,41 @@ int segments(const StateParams &P) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(device_sm_count() / std::max<int64_t>(units, 1), chunks / 4)));
 }
 
+// CTAs to a segment in the launch before: the finer, the fewer SMs stay without one in its last turn.
+int segment_parts(const StateParams &P, int segs) {
+  if (segs < 2) return 1;
+  const int64_t units = static_cast<int64_t>(P.B) * P.heads * value_blocks(P) * (segs - 1), sms = device_sm_count();
+  const int64_t chunks = (static_cast<int64_t>(P.n) + kChunkRows - 1) / kChunkRows / segs;
+  int best = 1;
+  double least = 1e30;
+  for (int p = 1; p <= 4 && p * 4 <= std::max<int64_t>(chunks, 4); ++p) {
+    const double turns = static_cast<double>((units * p + sms - 1) / sms) / p;
+    if (turns < least * 0.95) best = p, least = turns;
+  }
+  return best;
+}
+
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+// A call's plan over a workspace, and the workspace's size.
+std::pair<StateChunkPlan, size_t> chunk_plan(const StateParams &P, void *workspace) {
+  StateChunkPlan A{};
+  A.p = P;
+  A.segs = segments(P);
+  A.parts = segment_parts(P, A.segs);
+  const size_t per_head = A.segs > 1 ? static_cast<size_t>(P.B) * P.heads * A.slots() : 0;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char *p = static_cast<char *>(workspace) + at;
+    at += round256(bytes);
+    return workspace ? p : nullptr;
+  };
+  A.verdict = reinterpret_cast<int *>(take(P.B * sizeof(int)));
+  A.order = reinterpret_cast<int *>(take(P.B * sizeof(int)));
+  A.total = reinterpret_cast<float *>(take(per_head * sizeof(float)));
+  A.local = reinterpret_cast<float *>(take(per_head * P.key_dim * P.value_dim * sizeof(float)));
+  return {A, at};
+}
 
 bool taken_sizes(const StateParams &P) {
   return P.key_dim <= 128 && P.n > 16 && (!P.parents || P.n <= kChunkRows) && static_cast<int64_t>(P.B) * P.heads * 2 < (1 << 26);
@@ -115,34 +161,24 @@ bool map_strides(const int64_t *s, int heads, int n, int B) {
 }  // namespace
 
 bool state_on_tensor_cores(const StateParams &P) {
-  return P.vec && taken_sizes(P) && map_strides(P.qs, P.key_heads, P.n, P.B) && map_strides(P.ks, P.key_heads, P.n, P.B) &&
+  return P.vec && taken_sizes(P) && P.scale > 1e-30f && P.scale < 1e30f && map_strides(P.qs, P.key_heads, P.n, P.B) && map_strides(P.ks, P.key_heads, P.n, P.B) &&
          map_strides(P.vs, P.heads, P.n, P.B);
 }
 
 size_t state_chunk_workspace(const StateParams &P) {
   if (!taken_sizes(P)) return 0;
-  const size_t units = static_cast<size_t>(P.B) * P.heads;
-  const int segs = segments(P);
-  return round256(P.B * sizeof(int)) +
-         (segs > 1 ? round256(units * segs * sizeof(float)) + units * segs * P.key_dim * P.value_dim * sizeof(float) : 0);
+  return chunk_plan(P, nullptr).second;
 }
 
 cudaError_t launch_state_chunks(const StateParams &P, void *workspace, cudaStream_t st) {
-  StateChunkPlan A{};
-  A.p = P;
-  A.segs = segments(P);
-  char *ws = static_cast<char *>(workspace);
-  A.verdict = reinterpret_cast<int *>(ws);
-  ws += round256(P.B * sizeof(int));
+  const StateChunkPlan A = chunk_plan(P, workspace).first;
   const size_t units = static_cast<size_t>(P.B) * P.heads;
-  A.total = reinterpret_cast<float *>(ws);
-  A.local = reinterpret_cast<float *>(ws + round256(units * A.segs * sizeof(float)));
   CUtensorMap maps[3];
   cudaError_t e = rows_map(P.q, P.qs, P.key_dim, P.key_heads, P.n, P.B, &maps[0]);
   if (e == cudaSuccess) e = rows_map(P.k, P.ks, P.key_dim, P.key_heads, P.n, P.B, &maps[1]);
   if (e == cudaSuccess) e = rows_map(P.v, P.vs, P.value_dim, P.heads, P.n, P.B, &maps[2]);
   if (e != cudaSuccess) return e;
-  e = trace_launch("state_verdict", st, [&] { state_verdict_kernel<<<P.B, 64, 0, st>>>(P, A.verdict); });
+  e = trace_launch("state_verdict", st, [&] { state_verdict_kernel<<<P.B, 64, 0, st>>>(P, A.verdict, A.order); });
   auto chunks = P.dtype == SPEC_DTYPE_BF16 ? launch_state_chunk_bf16 : launch_state_chunk_f16;
   if (e == cudaSuccess && A.segs > 1) {
     e = chunks(A, false, maps, st);

@@ -61,7 +61,7 @@ struct ChunkShape {
   static constexpr int kKt = kV + kStagesV * kTileV;
   static constexpr int kA = kKt + 2 * 2 * kTileK;
   static constexpr int kSmall = kA + (OUT ? 2 * kHalf : 0);
-  static constexpr int kBytes = kSmall + 14336 + 1024;  // (1024: alignment of the base)
+  static constexpr int kBytes = kSmall + 17920 + 1024;  // (1024: alignment of the base)
 };
 
 struct ChunkSmall {
@@ -69,11 +69,12 @@ struct ChunkSmall {
     float nhi[kChunk], nlo[kChunk];  // minus the running sum in units of log 2: multiples of 1/8, rest
     float ei[kChunk];                // scale e^{G_i}
     float left[kChunk];              // e^{G_last - G_j}, 0 past the request's rows
-    float afac[kChunk];              // scale, times what row i of A was divided by
+    float afac[kChunk];              // fp16: what row i of A was divided by
     float sfac[128];                 // fp16: what a lane of S was divided by
     float lam;                       // e^{G_last}
     float kfac;                      // fp16: what K' was divided by
   } d[kDecayRing];
+  alignas(16) uint16_t stage[4][16][32];  // outputs on their way
   uint32_t follows[kChunk][2];  // trees: the rows that a row follows, itself among them
   uint32_t smax[2][4][128], amax[2][2][kChunk], kmax[2][kStateWarps];  // (by the chunk's number: the next one's may be written before these are read)
   // One barrier for each product, counted by chunk (four of them in turn, so that whoever waits for a chunk's phase is never a
@@ -86,7 +87,7 @@ struct ChunkSmall {
   int dead;
   int copies, products_p, products_o1, products_o2, products_s;  // how many were begun
 };
-static_assert(sizeof(ChunkSmall) <= 14336);
+static_assert(sizeof(ChunkSmall) <= 17920 && ChunkShape<128, true>::kBytes <= 232448 && ChunkShape<64, true>::kBytes <= 232448);
 
 // Arrival of a warp whose lanes have all done what the barrier stands for.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
@@ -222,13 +223,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   u /= P.heads;
   const int dv0 = u % blocks * 128;
   u /= blocks;
-  const int seg = u % A.launch_segs, b = u / A.launch_segs;
+  // (the longest requests first)
+  const int piece = u % A.pieces, b = A.order[u / A.pieces], seg = OUT ? piece : piece / A.parts;
   const int hk = h / P.group;
   const bool ok = A.verdict[b] == SPEC_STATUS_OK;
   const int len = ok ? (P.counts ? P.counts[b] : P.n) : 0;
   const int all = (len + kChunk - 1) / kChunk;
-  const int c0 = static_cast<int>(static_cast<int64_t>(all) * seg / A.segs);
-  const int chunks = static_cast<int>(static_cast<int64_t>(all) * (seg + 1) / A.segs) - c0;
+  int c0 = static_cast<int>(static_cast<int64_t>(all) * seg / A.segs);
+  int chunks = static_cast<int>(static_cast<int64_t>(all) * (seg + 1) / A.segs) - c0;
+  if (!OUT) {  // a part of the segment
+    const int part = piece - seg * A.parts, of = chunks;
+    c0 += static_cast<int>(static_cast<int64_t>(of) * part / A.parts);
+    chunks = static_cast<int>(static_cast<int64_t>(of) * (part + 1) / A.parts) - static_cast<int>(static_cast<int64_t>(of) * part / A.parts);
+  }
   const bool last_seg = seg + 1 == A.segs;
   // (a chunk's state is needed by the next, and by whoever reads the state written)
   const bool writes = OUT ? last_seg && P.to.state && ok : true;
@@ -342,7 +349,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       *reinterpret_cast<float2 *>(&d.nlo[2 * lane]) = make_float2(-p0.lo, -p1.lo);
       *reinterpret_cast<float2 *>(&d.ei[2 * lane]) = make_float2(p0.power() * P.scale, p1.power() * P.scale);
       *reinterpret_cast<float2 *>(&d.left[2 * lane]) = make_float2(2 * lane < m ? q0.power() : 0.0f, 2 * lane + 1 < m ? q1.power() : 0.0f);
-      *reinterpret_cast<float2 *>(&d.afac[2 * lane]) = make_float2(P.scale, P.scale);
       if (lane == 0) d.lam = total.parts(spoilt).power(), d.kfac = 1.0f;
       warp_arrive(&sm.dec_full[r], lane);
     }
@@ -350,7 +356,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       whole += rest >> kLog2Bits;
       rest &= (1 << kLog2Bits) - 1;
       const Log2Sum all_of{static_cast<int>(max(-4096ll, min(4096ll, whole))), static_cast<int>(rest)};
-      A.total[(static_cast<int64_t>(b) * P.heads + h) * A.segs + seg] = all_of.parts(lost).power();
+      A.total[(static_cast<int64_t>(b) * P.heads + h) * A.slots() + piece] = all_of.parts(lost).power();
     }
   } else if (warp == 10) {
     // ---- issuing O1 and O2
@@ -452,7 +458,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     for (int e = 0; e < OWN / 2; ++e) s[e] = 0;
     const float *from = nullptr;
     if (OUT && A.segs > 1) {
-      from = A.local + ((static_cast<int64_t>(b) * P.heads + h) * A.segs + seg) * size;
+      from = A.local + ((static_cast<int64_t>(b) * P.heads + h) * A.slots() + seg * A.parts) * size;
     } else if (OUT && ok && P.from.state) {
       const int slot = P.from.slots ? P.from.slots[b] : b;
       if (slot >= 0) from = P.from.state + slot * P.from.slot_stride + h * size;
@@ -543,7 +549,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int y = 0; y < 4; ++y) {
             const float2 k = widen2<DT>(w[y]);
             split2<DT>(mul2(pack2(k.x, k.y), f), hi[y], lo[y]);
-            if (past) hi[y] = lo[y] = 0;
+          }
+          if (past) [[unlikely]] {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) hi[y] = lo[y] = 0;
           }
           *reinterpret_cast<uint4 *>(to + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4 *>(to + S::kTileK + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -591,7 +600,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     float *to = nullptr;
     if (!OUT) {
-      to = A.local + ((static_cast<int64_t>(b) * P.heads + h) * A.segs + seg) * size;
+      to = A.local + ((static_cast<int64_t>(b) * P.heads + h) * A.slots() + piece) * size;
     } else if (writes && going) {
       to = P.to.state + (P.to.slots ? P.to.slots[b] : b) * P.to.slot_stride + h * size;
     }
@@ -609,6 +618,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int i = (warp & 1) * 32 + lane, half = warp >> 3, j0 = half * 32;
       const int group = (warp >> 3) * 64 + i;  // the thread among the 128
       const bool tree = P.parents != nullptr;
+      const float log2_scale = log2f(P.scale);
       int met = 0;
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
@@ -624,7 +634,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (__any_sync(~0u, sees != 0)) {
           float x[32];
           tmem_ld32(tmem + (static_cast<uint32_t>(warp & 3) << 21) + kP + j0, x);
-          const float mh = -d.nhi[i], ml = -d.nlo[i];
+          const float mh = -d.nhi[i], ml = log2_scale - d.nlo[i];
           const pair_t h2 = pack2(mh, mh), l2 = pack2(ml, ml);
           const bool every = __all_sync(~0u, sees == ~0u);
           tc_wait_ld();
@@ -671,7 +681,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0;
         }
-        if (F16 && half == 0) sm.d[r].afac[i] = back * P.scale;
+        if (F16 && half == 0) sm.d[r].afac[i] = back;
         if (c > 0 && !wait4(sm.o2_full, c - 1)) break;
         char *row = smem + S::kA + i * 128;
 #pragma unroll
@@ -698,7 +708,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
       const int dv = dv0 + at;
       uint16_t *out = reinterpret_cast<uint16_t *>(P.out) + b * P.os[0] + h * P.os[2] + dv;
-      const bool odd = lane & 1;
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
         const int r = c % kDecayRing, t0 = (c0 + c) * kChunk, m = min(kChunk, len - t0);
@@ -706,9 +715,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tc_fence_after();
         const ChunkSmall::Decays &d = sm.d[r];
         const float sf = F16 ? d.sfac[at] : 1.0f;
-        const pair_t sf2 = pack2(sf, sf), scale2 = pack2(P.scale, P.scale), none = 0;
+        const pair_t sf2 = pack2(sf, sf), none = 0;
         pair_t bad = 0;
-        char *o = reinterpret_cast<char *>(out + (t0 + odd) * P.os[1] - odd);  // two columns of every other row to a lane
+        // 16 tokens at a time through shared memory, from a column to a lane to 16 bytes of a token's row to a lane
+        uint16_t *const stage = sm.stage[quarter][0];
+        const int token = lane >> 2, col = quarter * 32 + (lane & 3) * 8;
+        char *o = reinterpret_cast<char *>(P.out) + (b * P.os[0] + h * P.os[2] + (t0 + token) * P.os[1] + dv0 + col) * 2;
+        const bool store = dv0 + col < P.value_dim;
 #pragma unroll 1
         for (int k = 0; k < kChunk; k += 16) {
           float x[16], y[16];
@@ -719,7 +732,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) y[e] = k + e < m ? y[e] : 0.0f;
           }
-          const bool store = dv < P.value_dim;
+          __syncwarp();
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
             const ulonglong2 ei = *reinterpret_cast<const ulonglong2 *>(&d.ei[k + e]);
@@ -728,15 +741,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               const int z = e + 2 * w;
-              pair_t f = w ? ei.y : ei.x;
-              if constexpr (F16) f = mul2(f, sf2);
-              const pair_t o2 = pack2(y[z], y[z + 1]);
+              pair_t f = w ? ei.y : ei.x, o2 = pack2(y[z], y[z + 1]);
               bad = fma2(o2, none, bad);
-              const uint32_t u2 = narrow2<DT>(unpack2(fma2(pack2(x[z], x[z + 1]), f, mul2(o2, F16 ? (w ? af.y : af.x) : scale2))));
-              const uint32_t other = __shfl_xor_sync(~0u, u2, 1);
-              if (store && k + z + odd < m) *reinterpret_cast<uint32_t *>(o) = odd ? __byte_perm(other, u2, 0x7632) : __byte_perm(u2, other, 0x5410);
-              o += P.os[1] * 4;
+              if constexpr (F16) f = mul2(f, sf2), o2 = mul2(o2, w ? af.y : af.x);
+              const uint32_t u2 = narrow2<DT>(unpack2(fma2(pack2(x[z], x[z + 1]), f, o2)));
+              stage[z * 32 + lane] = static_cast<uint16_t>(u2);
+              stage[(z + 1) * 32 + lane] = static_cast<uint16_t>(u2 >> 16);
             }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (store && k + token + 8 * e < m) *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(stage + e * 256 + lane * 8);
+            o += P.os[1] * 16;
           }
         }
         const float2 b2 = unpack2(bad);
@@ -789,8 +806,8 @@ cudaError_t launch_chunks(const StateChunkPlan &A, const CUtensorMap *maps, cuda
       once_per_device([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes); }, chunk_smem<DT, DK, OUT>);
   if (e != cudaSuccess) return e;
   StateChunkPlan B = A;
-  B.launch_segs = OUT ? A.segs : A.segs - 1;
-  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(A.p.B) * B.launch_segs * ((A.p.value_dim + 127) / 128) * A.p.heads);
+  B.pieces = OUT ? A.segs : (A.segs - 1) * A.parts;
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(A.p.B) * B.pieces * ((A.p.value_dim + 127) / 128) * A.p.heads);
   const bool again = !state_overlaps(A.p);
   return trace_launch(OUT ? "state_chunk" : "state_chunk_local", st, [&] { kern<<<grid, kChunkThreads, S::kBytes, st>>>(B, maps[0], maps[1], maps[2]); },
                       again || !OUT);
