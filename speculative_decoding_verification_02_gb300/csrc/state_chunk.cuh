@@ -134,38 +134,6 @@ __device__ __forceinline__ float fit_half(uint32_t amax, float &back) {
   return __uint_as_float(static_cast<uint32_t>(127 + s) << 23);
 }
 
-// A sum of decays in units of log 2, in fixed point: whole units, and 2^-25ths
-// (of which 64 tokens' halves fit an int).  A token's is off by half of one of
-// them, sums and differences not at all, however large: what 64-bit floats
-// would do at many times the cost.
-constexpr int kLog2Bits = 25;
-struct Log2Parts {
-  float hi, lo;  // a whole number and a rest in [-1/2, 1/2]
-  __device__ __forceinline__ float power() const {  // 2^(hi + lo); 0 below the least normal number
-    const float f = exp2f(lo);
-    if (!(hi >= -125.0f)) return hi < 0.0f ? 0.0f : hi + lo;  // (NaN stays)
-    return hi > 127.0f ? INFINITY : f * __uint_as_float(static_cast<uint32_t>(static_cast<int>(hi) + 127) << 23);
-  }
-};
-struct Log2Sum {
-  int whole, rest;
-  __device__ __forceinline__ Log2Sum &operator+=(const Log2Sum &x) {
-    whole += x.whole, rest += x.rest;
-    return *this;
-  }
-  __device__ __forceinline__ Log2Parts parts(bool nan) const {
-    const int carry = (rest + (1 << (kLog2Bits - 1))) >> kLog2Bits;
-    return Log2Parts{nan ? NAN : static_cast<float>(whole + carry), static_cast<float>(rest - (carry << kLog2Bits)) * (1.0f / (1 << kLog2Bits))};
-  }
-};
-// A natural logarithm; beyond +-120 (1e52) a factor is 0 or infinite in fp32 whatever it is.  NaN gives 0.
-__device__ __forceinline__ Log2Sum log2_of(float g) {
-  const float x = fminf(fmaxf(g, -120.0f), 120.0f);
-  const float y = x * 1.44269502f, e = fmaf(x, 1.44269502f, -y) + x * 1.92596303e-8f;  // log2(e) in two parts
-  const float w = rintf(y);
-  return g == g ? Log2Sum{static_cast<int>(w), static_cast<int>(rintf(((y - w) + e) * (1 << kLog2Bits)))} : Log2Sum{0, 0};
-}
-
 // Row i's weight for row j without what P held: e^{G_i - G_j} from the handed-on parts.
 __device__ __forceinline__ float between(const ChunkSmall::Decays &d, int i, int j) {
   return ex2((d.nhi[j] - d.nhi[i]) + (d.nlo[j] - d.nlo[i]));

@@ -10,10 +10,14 @@
 //   o_i = scale (e^{G_i} q_i S + sum_{j <= i} e^{G_i - G_j} (q_i . k_j) v_j)
 //   S  <- e^{G_last} S + sum_j k_j (e^{G_last - G_j} v_j)^T
 // so a row costs one packed multiply-add for two elements of S (the recurrence
-// token by token: three), and decays are sums of the g's between two tokens,
-// never a difference of running sums: -inf and long blocks lose nothing.
-// A tree's row takes its ancestors' terms instead, one after another along its
-// path, with k and v from memory.
+// token by token: three).  Lane group g adds the terms of tokens g and g + 8 to
+// its part of q_i S, so one reduction over the groups serves both.  The sums
+// are exact (fixed point), so their differences are: -inf and long blocks lose
+// nothing.  A tree's row takes its ancestors' terms instead, one after another
+// along its path, with k and v from memory.
+//
+// The rows' copies to shared memory are under way before the state's loads
+// wait for the request's slot.
 #include <algorithm>
 
 #include "launch.h"
@@ -23,7 +27,7 @@ namespace sv {
 namespace {
 
 constexpr int kBlock = 16;  // tokens to a block
-constexpr int kMaxWarps = 8;
+constexpr int kMaxWarps = 4;
 constexpr int kMaxPath = SPEC_MAX_DEPTH + 1;
 
 enum Mode { kCommit, kChain, kTree };
@@ -34,56 +38,70 @@ __device__ __forceinline__ float warp_add(float x) {
   return x;
 }
 
-// Rows of q or k in shared memory: RPL values of each of the 8 lane groups,
-// padded by 4 (a warp's reads then meet no bank twice).
+// Rows in shared memory, in their own type: RPL values to each of the 8 lane
+// groups, and 16 bytes more, so that 8 rows' same pieces lie in different banks.
 template <int RPL>
 struct RowTile {
-  static constexpr int kStride = 8 * (RPL + 4);
-  static __device__ __forceinline__ int at(int d) { return d / RPL * (RPL + 4) + d % RPL; }
+  static constexpr int kStride = 8 * RPL * 2 + 16;
 };
 
-// Row `row` of a key head (or, COLS, columns of a state head's v) as fp32.
-template <int DT>
-__device__ __forceinline__ void load_piece(const char *p, bool vec, float *x) {  // 8 values
-  uint32_t w[4];
+__device__ __forceinline__ void copy_piece(void *to, const char *from, bool vec) {  // 8 values
   if (vec) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    cp_async16(to, from);
   } else {
-    const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+    const uint16_t *h = reinterpret_cast<const uint16_t *>(from);
+    uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = h[2 * e] | static_cast<uint32_t>(h[2 * e + 1]) << 16;
+    *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+}
+
+// Eight values of a row in 16 bytes to four register pairs.
+template <int DT>
+__device__ __forceinline__ void widen8(const uint4 &v, pair_t *x) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float2 f = widen2<DT>(w[e]);
-    x[2 * e] = f.x, x[2 * e + 1] = f.y;
+    x[e] = pack2(f.x, f.y);
   }
 }
 
-// q_i . k_j, a warp: both rows in shared memory.
-template <int RPL>
-__device__ __forceinline__ float dot_rows(const float *a, const float *b, int lane) {
-  float sum = 0.0f;
+// q_i S for the four columns of a lane, summed over its group's rows of S.
+template <int DT, int RPL>
+__device__ __forceinline__ float4 row_product(const char *q, int g, const pair_t (&S)[RPL / 2][4]) {
+  pair_t o[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int e = 0; e < (RPL * 8 + 127) / 128; ++e) {
-    const int d = (e * 32 + lane) * 4;
-    if (RPL >= 16 || d < RPL * 8) {
-      const float4 x = *reinterpret_cast<const float4 *>(a + RowTile<RPL>::at(d));
-      const float4 y = *reinterpret_cast<const float4 *>(b + RowTile<RPL>::at(d));
-      sum = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, sum))));
-    }
+  for (int r = 0; r < RPL / 8; ++r) {
+    pair_t x[4];
+    widen8<DT>(*reinterpret_cast<const uint4 *>(q + (g * RPL + 8 * r) * 2), x);
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = fma2(x[y], S[4 * r + y][e], o[e]);
   }
-  return warp_add(sum);
+  const float2 a = unpack2(o[0]), b = unpack2(o[1]), c = unpack2(o[2]), d = unpack2(o[3]);
+  return make_float4(a.x + a.y, b.x + b.y, c.x + c.y, d.x + d.y);
+}
+
+// The sum over a warp's 8 lane groups: lane 4 g + c ends with column
+// 4 c + 2 (g >> 2) + (g >> 1 & 1), as does the lane whose g differs by one.
+__device__ __forceinline__ float group_sum(const float4 &f, int g) {
+  const bool hi2 = g & 4, hi1 = g & 2;
+  const float s0 = __shfl_xor_sync(~0u, hi2 ? f.x : f.z, 16), s1 = __shfl_xor_sync(~0u, hi2 ? f.y : f.w, 16);
+  const float a0 = (hi2 ? f.z : f.x) + s0, a1 = (hi2 ? f.w : f.y) + s1;
+  const float sum = (hi1 ? a1 : a0) + __shfl_xor_sync(~0u, hi1 ? a0 : a1, 8);
+  return sum + __shfl_xor_sync(~0u, sum, 4);
 }
 
 template <int DT, int RPL, Mode MODE>
-__global__ void __launch_bounds__(32 * kMaxWarps) state_rows_kernel(const StateParams P, const int blocks_x) {
+__global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_kernel(const StateParams P, const int blocks_x) {
   using Tile = RowTile<RPL>;
-  __shared__ __align__(16) float qs[MODE == kCommit ? 1 : kBlock][Tile::kStride];
-  __shared__ __align__(16) float ks[MODE == kTree ? 1 : kBlock][Tile::kStride];
-  __shared__ __align__(16) float vs[MODE == kTree ? 1 : kBlock][kMaxWarps * 16];
-  __shared__ float gs[kBlock], left[kBlock], from_state[kBlock];
+  __shared__ __align__(16) char qs[MODE == kCommit ? 1 : kBlock][MODE == kCommit ? 16 : Tile::kStride];
+  __shared__ __align__(16) char ks[MODE == kTree ? 1 : kBlock][MODE == kTree ? 16 : Tile::kStride];
+  __shared__ __align__(16) uint16_t vs[MODE == kTree ? 1 : kBlock][kMaxWarps * 16];
+  __shared__ float gs[2][kBlock], left[kBlock], from_state[kBlock];
   __shared__ float total;
   __shared__ float pair[MODE == kChain ? kBlock : 1][kBlock];
   __shared__ float path_w[MODE == kTree ? kBlock : 1][kMaxPath];
@@ -101,13 +119,49 @@ __global__ void __launch_bounds__(32 * kMaxWarps) state_rows_kernel(const StateP
   int status = SPEC_STATUS_OK;
   const int slot = state_slot(P.from, b, true, ok);
   const int to_slot = state_slot(P.to, b, false, ok);
-  if (!ok) status = SPEC_STATUS_BAD_SLOT;
   int count = P.counts ? P.counts[b] : P.n_rows;
-  if (count < 0 || count > P.n_rows) status = SPEC_STATUS_BAD_LENGTH;
 
-  // its part of the state, on the way while the rows are fetched
+  const char *qp = P.q + (b * P.qs[0] + hk * P.qs[2]) * 2;
+  const char *kp = P.k + (b * P.ks[0] + hk * P.ks[2]) * 2;
+  const char *vp = P.v + (b * P.vs[0] + h * P.vs[2]) * 2;
+  const float *gp = P.decay + b * P.gs[0] + h * P.gs[2];
+  const int dpieces = P.key_dim >> 3, vpieces = min(warps * 16, P.value_dim - first_col) >> 3;
+  const int32_t *index = MODE == kCommit && P.index ? P.index + static_cast<int64_t>(b) * P.index_stride : nullptr;
+  auto token = [&](int i) -> int64_t {
+    if (!index) return i;
+    const int r = index[i];  // (an entry that names no row is refused below, or lies past the count)
+    return r < 0 || r >= P.n ? 0 : r;
+  };
+  // Rows [t0, t0 + m): on their way to shared memory.
+  auto fetch = [&](int t0, int m, int side) {
+    for (int i = tid; i < m * dpieces; i += blockDim.x) {
+      const int r = i / dpieces, d = (i - r * dpieces) * 8;
+      const int64_t t = token(t0 + r);
+      if (MODE != kCommit) copy_piece(&qs[r][d * 2], qp + (t * P.qs[1] + d) * 2, P.vec);
+      if (MODE != kTree) copy_piece(&ks[r][d * 2], kp + (t * P.ks[1] + d) * 2, P.vec);
+    }
+    if (MODE != kTree) {
+      for (int i = tid; i < m * vpieces; i += blockDim.x) {
+        const int r = i / vpieces, d = (i - r * vpieces) * 8;
+        copy_piece(&vs[r][d], vp + (token(t0 + r) * P.vs[1] + first_col + d) * 2, P.vec);
+      }
+      if (tid < m) gs[side][tid] = gp[token(t0 + tid) * P.gs[1]];
+    }
+  };
+  if (P.key_dim < 8 * RPL) {  // the rows' ends, which no copy fills
+    const int pad = 8 * RPL - P.key_dim;
+    for (int i = tid; i < kBlock * pad; i += blockDim.x) {
+      const int r = i / pad, d = P.key_dim + i % pad;
+      if (MODE != kCommit) *reinterpret_cast<uint16_t *>(&qs[r][d * 2]) = 0;
+      if (MODE != kTree) *reinterpret_cast<uint16_t *>(&ks[r][d * 2]) = 0;
+    }
+  }
+  fetch(0, P.n > 0 ? min(kBlock, P.n_rows) : 0, 0);  // (whatever the count: the rows exist)
+
+  // its part of the state
+  if (!ok) status = SPEC_STATUS_BAD_SLOT;
   pair_t S[RPL / 2][4];
-  if (slot >= 0 && status == SPEC_STATUS_OK && live) {
+  if (slot >= 0 && ok && live) {
     const float *p = P.from.state + slot * P.from.slot_stride + static_cast<int64_t>(h) * P.key_dim * P.value_dim + col0 + 4 * c;
 #pragma unroll
     for (int r = 0; r < RPL; r += 2) {
@@ -125,14 +179,12 @@ __global__ void __launch_bounds__(32 * kMaxWarps) state_rows_kernel(const StateP
 #pragma unroll
       for (int e = 0; e < 4; ++e) S[r][e] = 0;
   }
+  if (count < 0 || count > P.n_rows) status = SPEC_STATUS_BAD_LENGTH;
 
   // rows that a request names: all of them are looked at before anything is written
-  if (status == SPEC_STATUS_OK && MODE == kCommit && P.index) {
+  if (status == SPEC_STATUS_OK && index) {
     bool bad = false;
-    for (int i = tid; i < count; i += blockDim.x) {
-      const int r = P.index[static_cast<int64_t>(b) * P.index_stride + i];
-      bad |= r < 0 || r >= P.n;
-    }
+    for (int i = tid; i < count; i += blockDim.x) bad |= index[i] < 0 || index[i] >= P.n;
     if (__syncthreads_or(bad)) status = SPEC_STATUS_BAD_INDEX;
   }
   const int32_t *parents = MODE == kTree ? P.parents + static_cast<int64_t>(b) * P.n : nullptr;
@@ -156,68 +208,50 @@ __global__ void __launch_bounds__(32 * kMaxWarps) state_rows_kernel(const StateP
   if (P.status && x == 0 && h == 0 && tid == 0) P.status[b] = status;
   if (status != SPEC_STATUS_OK) count = 0;
 
-  const char *qp = P.q + (b * P.qs[0] + hk * P.qs[2]) * 2;
-  const char *kp = P.k + (b * P.ks[0] + hk * P.ks[2]) * 2;
-  const char *vp = P.v + (b * P.vs[0] + h * P.vs[2]) * 2;
-  const float *gp = P.decay + b * P.gs[0] + h * P.gs[2];
-  if (P.key_dim < 8 * RPL) {  // the rows' ends, which no load fills
-    const int pad = 8 * RPL - P.key_dim;
-    for (int i = tid; i < kBlock * pad; i += blockDim.x) {
-      const int r = i / pad, d = P.key_dim + i % pad;
-      if (MODE != kCommit) qs[r][Tile::at(d)] = 0.0f;
-      if (MODE != kTree) ks[r][Tile::at(d)] = 0.0f;
-    }
-  }
-
-  const int dpieces = P.key_dim >> 3, vpieces = min(warps * 16, P.value_dim - first_col) >> 3;
 #pragma unroll 1
   for (int t0 = 0; t0 < count; t0 += kBlock) {
-    const int m = min(kBlock, count - t0);
-    auto token = [&](int i) -> int64_t {
-      return MODE == kCommit && P.index ? P.index[static_cast<int64_t>(b) * P.index_stride + t0 + i] : t0 + i;
-    };
-    // ---- the block's rows
-    for (int i = tid; i < m * dpieces; i += blockDim.x) {
-      const int r = i / dpieces, d = (i - r * dpieces) * 8;
-      const int64_t t = token(r);
-      float f[8];
-      if (MODE != kCommit) {
-        load_piece<DT>(qp + (t * P.qs[1] + d) * 2, P.vec, f);
-        *reinterpret_cast<float4 *>(&qs[r][Tile::at(d)]) = make_float4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<float4 *>(&qs[r][Tile::at(d + 4)]) = make_float4(f[4], f[5], f[6], f[7]);
-      }
-      if (MODE != kTree) {
-        load_piece<DT>(kp + (t * P.ks[1] + d) * 2, P.vec, f);
-        *reinterpret_cast<float4 *>(&ks[r][Tile::at(d)]) = make_float4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<float4 *>(&ks[r][Tile::at(d + 4)]) = make_float4(f[4], f[5], f[6], f[7]);
-      }
-    }
+    const int m = min(kBlock, count - t0), side = t0 / kBlock & 1;
+    if (t0 > 0) fetch(t0, m, side);
+    cp_async_wait_all();
+    __syncthreads();
     if (MODE != kTree) {
-      for (int i = tid; i < m * vpieces; i += blockDim.x) {
-        const int r = i / vpieces, d = (i - r * vpieces) * 8;
-        float f[8];
-        load_piece<DT>(vp + (token(r) * P.vs[1] + first_col + d) * 2, P.vec, f);
-        *reinterpret_cast<float4 *>(&vs[r][d]) = make_float4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<float4 *>(&vs[r][d + 4]) = make_float4(f[4], f[5], f[6], f[7]);
+      // ---- decays: every warp the sums it needs, the first the factors
+      Log2Sum upto = lane < m ? log2_of(gs[side][lane]) : Log2Sum{0, 0};
+      const uint32_t nan = __ballot_sync(~0u, lane < m && gs[side][lane & 15] != gs[side][lane & 15]);
+#pragma unroll
+      for (int o = 1; o < kBlock; o <<= 1) {
+        const Log2Sum y{__shfl_up_sync(~0u, upto.whole, o), __shfl_up_sync(~0u, upto.rest, o)};
+        if (lane >= o) upto += y;
       }
-      if (tid < m) gs[tid] = gp[token(tid) * P.gs[1]];
-      __syncthreads();
-      if (tid < m) {  // e^ of the sums up to and from a token on
-        float to = 0.0f, past = 0.0f;
-        for (int j = 0; j <= tid; ++j) to += gs[j];
-        for (int j = tid + 1; j < m; ++j) past += gs[j];
-        from_state[tid] = expf(to) * (MODE == kChain ? P.scale : 1.0f);
-        left[tid] = expf(past);
-        if (tid == m - 1) total = expf(to);
+      const Log2Sum all{__shfl_sync(~0u, upto.whole, m - 1), __shfl_sync(~0u, upto.rest, m - 1)};
+      if (warp == 0 && lane < m) {
+        from_state[lane] = upto.parts(nan & ((2u << lane) - 1)).power() * (MODE == kChain ? P.scale : 1.0f);
+        left[lane] = Log2Sum{all.whole - upto.whole, all.rest - upto.rest}.parts(nan >> lane >> 1).power();
+        if (lane == m - 1) total = all.parts(nan).power();
       }
       if constexpr (MODE == kChain) {
-        int i = 0, at = 0;  // pair number `at` is (i, 0)
-        for (int p = warp; p < m * (m + 1) / 2; p += warps) {
-          while (p > at + i) at += i + 1, ++i;
-          const int j = p - at;
-          const float s = dot_rows<RPL>(qs[i], ks[j], lane);
-          const float between = warp_add(lane > j && lane <= i ? gs[lane] : 0.0f);
-          if (lane == 0) pair[i][j] = s * expf(between) * P.scale;
+        // ---- the pairs' weights: a row to a warp, a token before it to two lanes, each of half of key_dim
+        for (int i = warp; i < m; i += warps) {
+          const int j = lane & 15, half = lane >> 4;
+          float s0 = 0.0f, s1 = 0.0f;
+          if (j <= i) {
+            const char *q = &qs[i][half * RPL * 8], *k = &ks[j][half * RPL * 8];
+#pragma unroll 4
+            for (int e = 0; e < RPL / 2; ++e) {
+              pair_t a[4], d[4];
+              widen8<DT>(*reinterpret_cast<const uint4 *>(q + e * 16), a);
+              widen8<DT>(*reinterpret_cast<const uint4 *>(k + e * 16), d);
+              const float2 u = unpack2(fma2(a[0], d[0], mul2(a[1], d[1]))), w = unpack2(fma2(a[2], d[2], mul2(a[3], d[3])));
+              s0 += u.x + u.y, s1 += w.x + w.y;
+            }
+          }
+          float s = s0 + s1;
+          s += __shfl_xor_sync(~0u, s, 16);
+          const int w = __shfl_sync(~0u, upto.whole, i), r = __shfl_sync(~0u, upto.rest, i);
+          const int wj = __shfl_sync(~0u, upto.whole, j), rj = __shfl_sync(~0u, upto.rest, j);
+          // (tokens j + 1 to i)
+          const bool lost = nan & ((2u << i) - 1) & ~((2u << j) - 1);
+          if (lane < 16) pair[i][j] = j <= i ? s * Log2Sum{w - wj, r - rj}.parts(lost).power() * P.scale : 0.0f;
         }
       }
       __syncthreads();
@@ -241,8 +275,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps) state_rows_kernel(const StateP
           float s = 0.0f;
           for (int d = lane * 2; d < P.key_dim; d += 64) {
             const uint16_t *u = reinterpret_cast<const uint16_t *>(row) + d;
-            const int at = Tile::at(d);
-            s = fmaf(qs[i][at], widen<DT>(u[0]), fmaf(qs[i][at + 1], widen<DT>(u[1]), s));
+            const float2 f = widen2<DT>(*reinterpret_cast<const uint32_t *>(&qs[i][d * 2]));
+            s = fmaf(f.x, widen<DT>(u[0]), fmaf(f.y, widen<DT>(u[1]), s));
           }
           s = warp_add(s);
           if (lane == 0) path_w[i][p] = s * expf(path_w[i][p]) * P.scale;
@@ -253,40 +287,54 @@ __global__ void __launch_bounds__(32 * kMaxWarps) state_rows_kernel(const StateP
 
     // ---- outputs
     if (MODE != kCommit && live) {
-      const int col = 4 * c + 2 * (g >> 2) + (g >> 1 & 1);  // the column that this lane ends up with, and the lane whose g differs by one
+      const int col = 4 * c + 2 * (g >> 2) + (g >> 1 & 1);
+      uint16_t *o16 = reinterpret_cast<uint16_t *>(P.out) + b * P.os[0] + static_cast<int64_t>(t0) * P.os[1] + h * P.os[2] + col0 + col;
+      if constexpr (MODE == kChain) {
+        // the lane's columns of tokens g and g + 8 (zeros where there are none: their weights are, and no row sees them)
+        float4 v0 = {}, v1 = {};
+        auto load_v = [&](int j) -> float4 {
+          const uint2 w = *reinterpret_cast<const uint2 *>(&vs[j][warp * 16 + 4 * c]);
+          const float2 y = widen2<DT>(w.x), z = widen2<DT>(w.y);
+          return make_float4(y.x, y.y, z.x, z.y);
+        };
+        if (g < m) v0 = load_v(g);
+        if (g + 8 < m) v1 = load_v(g + 8);
+        auto row = [&](int i) -> float {
+          const float4 s = row_product<DT, RPL>(qs[i], g, S);
+          const float e = from_state[i];
+          float4 f = make_float4(s.x * e, s.y * e, s.z * e, s.w * e);
+          if (g <= i) {
+            const float w = pair[i][g];
+            f = make_float4(fmaf(w, v0.x, f.x), fmaf(w, v0.y, f.y), fmaf(w, v0.z, f.z), fmaf(w, v0.w, f.w));
+          }
+          if (g + 8 <= i) {
+            const float w = pair[i][g + 8];
+            f = make_float4(fmaf(w, v1.x, f.x), fmaf(w, v1.y, f.y), fmaf(w, v1.z, f.z), fmaf(w, v1.w, f.w));
+          }
+          return group_sum(f, g);
+        };
+        int i = 0;
 #pragma unroll 1
-      for (int i = 0; i < m; ++i) {
-        pair_t o[4] = {0, 0, 0, 0};
-        const ulonglong2 *q = reinterpret_cast<const ulonglong2 *>(&qs[i][g * (RPL + 4)]);
-#pragma unroll
-        for (int r = 0; r < RPL / 4; ++r) {
-          const ulonglong2 u = q[r];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = fma2(u.y, S[2 * r + 1][e], fma2(u.x, S[2 * r][e], o[e]));
+        for (; i + 2 <= m; i += 2) {  // two rows side by side: the one's reduction behind the other's products
+          const float a = row(i), d = row(i + 1);
+          o16[(g & 1) * P.os[1]] = narrow<DT>(g & 1 ? d : a);
+          o16 += 2 * P.os[1];
         }
-        float f[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 w = unpack2(o[e]);
-          f[e] = w.x + w.y;
+        if (i < m) {
+          const float a = row(i);
+          if (!(g & 1)) *o16 = narrow<DT>(a);
         }
-        const bool hi2 = g & 4, hi1 = g & 2;
-        const float s0 = __shfl_xor_sync(~0u, hi2 ? f[0] : f[2], 16), s1 = __shfl_xor_sync(~0u, hi2 ? f[1] : f[3], 16);
-        const float a0 = (hi2 ? f[2] : f[0]) + s0, a1 = (hi2 ? f[3] : f[1]) + s1;
-        float sum = (hi1 ? a1 : a0) + __shfl_xor_sync(~0u, hi1 ? a0 : a1, 8);
-        sum *= from_state[i];
-        if constexpr (MODE == kChain) {
-          for (int j = g & 1; j <= i; j += 2) sum = fmaf(pair[i][j], vs[j][warp * 16 + col], sum);
-        } else {
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < m; ++i) {
+          float sum = group_sum(row_product<DT, RPL>(qs[i], g, S), g) * from_state[i], terms = 0.0f;
           for (int p = g & 1; p < path_len[i]; p += 2) {
             const uint16_t v = *reinterpret_cast<const uint16_t *>(vp + (static_cast<int64_t>(path[i][p]) * P.vs[1] + col0 + col) * 2);
-            sum = fmaf(path_w[i][p], widen<DT>(v), sum);
+            terms = fmaf(path_w[i][p], widen<DT>(v), terms);
           }
-        }
-        sum += __shfl_xor_sync(~0u, sum, 4);
-        if (!(g & 1)) {
-          uint16_t *o16 = reinterpret_cast<uint16_t *>(P.out) + b * P.os[0] + static_cast<int64_t>(t0 + i) * P.os[1] + h * P.os[2] + col0 + col;
-          *o16 = narrow<DT>(sum);
+          sum += terms + __shfl_xor_sync(~0u, terms, 4);
+          if (!(g & 1)) *o16 = narrow<DT>(sum);
+          o16 += P.os[1];
         }
       }
     }
@@ -300,26 +348,24 @@ __global__ void __launch_bounds__(32 * kMaxWarps) state_rows_kernel(const StateP
         for (int e = 0; e < 4; ++e) S[r][e] = mul2(S[r][e], f2);
 #pragma unroll 1
       for (int j = 0; j < m; ++j) {
-        const float4 v = *reinterpret_cast<const float4 *>(&vs[j][warp * 16 + 4 * c]);
+        const uint2 v = *reinterpret_cast<const uint2 *>(&vs[j][warp * 16 + 4 * c]);
+        const float2 y0 = widen2<DT>(v.x), y1 = widen2<DT>(v.y);
         const float w = left[j];
-        const float f[4] = {v.x * w, v.y * w, v.z * w, v.w * w};
-        const ulonglong2 *k = reinterpret_cast<const ulonglong2 *>(&ks[j][g * (RPL + 4)]);
-        pair_t v2[4];
+        const pair_t v2[4] = {pack2(y0.x * w, y0.x * w), pack2(y0.y * w, y0.y * w), pack2(y1.x * w, y1.x * w), pack2(y1.y * w, y1.y * w)};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v2[e] = pack2(f[e], f[e]);
+        for (int r = 0; r < RPL / 8; ++r) {
+          pair_t k[4];
+          widen8<DT>(*reinterpret_cast<const uint4 *>(&ks[j][(g * RPL + 8 * r) * 2]), k);
 #pragma unroll
-        for (int r = 0; r < RPL / 4; ++r) {
-          const ulonglong2 u = k[r];
+          for (int y = 0; y < 4; ++y)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            S[2 * r][e] = fma2(u.x, v2[e], S[2 * r][e]);
-            S[2 * r + 1][e] = fma2(u.y, v2[e], S[2 * r + 1][e]);
-          }
+            for (int e = 0; e < 4; ++e) S[4 * r + y][e] = fma2(k[y], v2[e], S[4 * r + y][e]);
         }
       }
     }
-    __syncthreads();  // before the next block's rows
+    if (t0 + kBlock < count) __syncthreads();  // before the next block's rows
   }
+  cp_async_wait_all();
 
   if (MODE != kCommit) {  // rows past the count
     const int cols = min(warps * 16, P.value_dim - first_col);
@@ -350,7 +396,7 @@ template <int DT, int RPL>
 cudaError_t launch_rows(const StateParams &P, cudaStream_t st) {
   const int groups = P.value_dim / 16;
   const int64_t units = static_cast<int64_t>(P.B) * P.heads;
-  // eight warps share a block's rows; fewer when that leaves SMs without a CTA
+  // four warps share a block's rows, fewer when that leaves SMs without a CTA (eight: 64 requests' single tokens 92 us, not 81)
   int warps = kMaxWarps;
   while (warps > 2 && units * ((groups + warps - 1) / warps) < device_sm_count()) warps /= 2;
   const int x = (groups + warps - 1) / warps;

@@ -249,6 +249,46 @@ def test_nothing_to_do(api):
     assert o["out"].shape == (0, 4, 1, 64)
 
 
+@pytest.mark.parametrize("Dk,Dv,Hk,G,dtype", [(128, 128, 8, 3, BF), (64, 64, 20, 1, HF), (112, 48, 10, 2, BF), (16, 128, 10, 1, HF), (128, 80, 7, 2, HF)])
+@pytest.mark.parametrize("n", [1, 5, 16])
+def test_many_requests(api, Dk, Dv, Hk, G, dtype, n):
+    """Enough (request, head)s that a CTA takes several: ragged, wrong ones among them, slots in any order, in place and not."""
+    B = 64
+    r = Rows(B, n, Hk, G, Dk, Dv, dtype, 500 + n, slots=B + 3)
+    g = torch.Generator().manual_seed(n)
+    slots = torch.randperm(B + 3, generator=g)[:B].tolist()
+    counts = torch.randint(0, n + 1, (B,), generator=g).tolist()
+    slots[7], slots[20], counts[30] = -1, B + 3, n + 1
+    pool, dst = r.pool.cuda(), torch.full((B, r.H, Dk, Dv), 3.0, device="cuda")
+    out = torch.full(r.v.shape, 5.0, dtype=dtype, device="cuda")
+    o = api.spec_state_forward(*r.gpu("q", "k", "v", "g"), pool, slots=i32(slots), dst=dst, counts=i32(counts), out=dict(out=out, status=i32([9] * B)))
+    bad = {20: api.STATUS_BAD_SLOT, 30: api.STATUS_BAD_LENGTH}
+    assert o["status"].tolist() == [bad.get(b, 0) for b in range(B)]
+    d = api.spec_state_attend(*r.gpu("q", "k", "v", "g"), pool, slots=i32(slots), n_query=i32(counts))
+    assert torch.equal(d["out"], out) and d["status"].tolist() == o["status"].tolist()
+    for b in list(range(0, B, 9)) + [7, 20, 30, B - 1]:
+        if b in bad:
+            assert not out[b].any() and bool((dst[b] == 3).all())
+            continue
+        outs, last = r.want(b, r.pool[slots[b]] if slots[b] >= 0 else r.zeros(), list(range(counts[b])))
+        ref.check_out(out[b, :counts[b]], outs, Dk, n, dtype)
+        assert not out[b, counts[b]:].any()
+        ref.check_state(dst[b], last, Dk, n)
+    rows = max(1, n - 1)
+    index = torch.stack([torch.randperm(n, generator=g)[:rows].sort().values for _ in range(B)]).to(torch.int32)
+    counts = torch.randint(0, rows + 1, (B,), generator=g).tolist()
+    slots[7], slots[20], counts[9] = next(s for s in range(B + 3) if s not in slots), next(s for s in range(B + 2, -1, -1) if s not in slots), rows
+    index[9, 0] = n
+    was = pool.clone()
+    o = api.spec_state_commit(*r.gpu("k", "v", "g"), pool, slots=i32(slots), counts=i32(counts), index=index.cuda())
+    assert o["status"].tolist() == [api.STATUS_BAD_INDEX if b == 9 else 0 for b in range(B)]
+    assert torch.equal(pool[slots[9]], was[slots[9]])
+    for b in list(range(0, B, 8)) + [7, 20]:
+        ref.check_state(pool[slots[b]], r.want(b, r.pool[slots[b]], index[b, :counts[b]].tolist())[1], Dk, n)
+    for s in set(range(B + 3)) - set(slots):
+        assert torch.equal(pool[s], was[s])
+
+
 # ------------------------------------------------------------------ drafted rows
 
 def random_tree(n, seed, reach=10, depth=64):
