@@ -60,6 +60,8 @@ size_t state_chunk_workspace(const StateParams &P);
 cudaError_t launch_state_chunks(const StateParams &P, void *workspace, cudaStream_t st);
 cudaError_t launch_state_chunk_bf16(const StateChunkPlan &A, bool outputs, const CUtensorMap *maps, cudaStream_t st);
 cudaError_t launch_state_chunk_f16(const StateChunkPlan &A, bool outputs, const CUtensorMap *maps, cudaStream_t st);
+cudaError_t launch_state_short_bf16(const StateChunkPlan &A, const CUtensorMap *maps, cudaStream_t st);
+cudaError_t launch_state_short_f16(const StateChunkPlan &A, const CUtensorMap *maps, cudaStream_t st);
 
 // A launch of the kernels for a few rows: chains (q given: with outputs), commits (q null), trees (parents given).
 cudaError_t launch_state_rows(const StateParams &P, cudaStream_t st);

@@ -23,6 +23,7 @@ __device__ __forceinline__ int block_sum64(int x) {
 // request, and one that gave up a wait must not be overwritten by another's OK.
 // And the requests' order, longest first, so that the launch's last CTAs are short.
 __global__ void __launch_bounds__(64) state_verdict_kernel(const StateParams P, int *verdict, int *order) {
+  pdl_launch_dependents();
   const int b = blockIdx.x, tid = threadIdx.x;
   bool ok = true;
   state_slot(P.from, b, true, ok);
@@ -47,6 +48,7 @@ __global__ void __launch_bounds__(64) state_verdict_kernel(const StateParams P, 
 
 // From what each segment adds to zeros, the state before each: a thread to four elements of a head.
 __global__ void __launch_bounds__(256) state_join_kernel(const StateChunkPlan A) {
+  pdl_launch_dependents();
   const StateParams &P = A.p;
   const int size = P.key_dim * P.value_dim;
   const int per = (size / 4 + 255) / 256;
@@ -69,6 +71,9 @@ __global__ void __launch_bounds__(256) state_join_kernel(const StateChunkPlan A)
 }
 
 int value_blocks(const StateParams &P) { return (P.value_dim + 127) / 128; }
+
+// One chunk's rows over states that are only read.
+bool is_short(const StateParams &P) { return P.n <= kChunkRows && !P.to.state; }
 
 // Segments to a request: as many as leave no SM with a second CTA, of four chunks each at least.
 int segments(const StateParams &P) {
@@ -179,6 +184,7 @@ cudaError_t launch_state_chunks(const StateParams &P, void *workspace, cudaStrea
   if (e == cudaSuccess) e = rows_map(P.v, P.vs, P.value_dim, P.heads, P.n, P.B, &maps[2]);
   if (e != cudaSuccess) return e;
   e = trace_launch("state_verdict", st, [&] { state_verdict_kernel<<<P.B, 64, 0, st>>>(P, A.verdict, A.order); });
+  if (e == cudaSuccess && is_short(P)) return (P.dtype == SPEC_DTYPE_BF16 ? launch_state_short_bf16 : launch_state_short_f16)(A, maps, st);
   auto chunks = P.dtype == SPEC_DTYPE_BF16 ? launch_state_chunk_bf16 : launch_state_chunk_f16;
   if (e == cudaSuccess && A.segs > 1) {
     e = chunks(A, false, maps, st);

@@ -64,18 +64,19 @@ struct ChunkShape {
   static constexpr int kBytes = kSmall + 17920 + 1024;  // (1024: alignment of the base)
 };
 
+struct alignas(16) Decays {
+  float nhi[kChunk], nlo[kChunk];  // minus the running sum in units of log 2: multiples of 1/8, rest
+  float ei[kChunk];                // scale e^{G_i}
+  float left[kChunk];              // e^{G_last - G_j}, 0 past the request's rows
+  float afac[kChunk];              // fp16: what row i of A was divided by
+  float sfac[128];                 // fp16: what a lane of S was divided by
+  float lam;                       // e^{G_last}
+  float kfac;                      // fp16: what K' was divided by
+};
+
 struct ChunkSmall {
-  struct alignas(16) Decays {
-    float nhi[kChunk], nlo[kChunk];  // minus the running sum in units of log 2: multiples of 1/8, rest
-    float ei[kChunk];                // scale e^{G_i}
-    float left[kChunk];              // e^{G_last - G_j}, 0 past the request's rows
-    float afac[kChunk];              // fp16: what row i of A was divided by
-    float sfac[128];                 // fp16: what a lane of S was divided by
-    float lam;                       // e^{G_last}
-    float kfac;                      // fp16: what K' was divided by
-  } d[kDecayRing];
+  Decays d[kDecayRing];
   alignas(16) uint16_t stage[4][16][32];  // outputs on their way
-  uint32_t follows[kChunk][2];  // trees: the rows that a row follows, itself among them
   uint32_t smax[2][4][128], amax[2][2][kChunk], kmax[2][kStateWarps];  // (by the chunk's number: the next one's may be written before these are read)
   // One barrier for each product, counted by chunk (four of them in turn, so that whoever waits for a chunk's phase is never a
   // lap behind): that P, O1, O2, dS are there, and so that their operands are free.
@@ -135,15 +136,127 @@ __device__ __forceinline__ float fit_half(uint32_t amax, float &back) {
 }
 
 // Row i's weight for row j without what P held: e^{G_i - G_j} from the handed-on parts.
-__device__ __forceinline__ float between(const ChunkSmall::Decays &d, int i, int j) {
+__device__ __forceinline__ float between(const Decays &d, int i, int j) {
   return ex2((d.nhi[j] - d.nhi[i]) + (d.nlo[j] - d.nlo[i]));
+}
+
+// The decays of a chunk: two tokens next to one another to a lane.  Sums up to each of them, the whole's, and where a NaN has a part.
+struct ChunkSums {
+  Log2Sum g0, g1, total;
+  bool bad0, bad1, spoilt;
+};
+
+__device__ __forceinline__ ChunkSums chunk_sums(float x0, float x1, int lane) {
+  ChunkSums s{log2_of(x0), log2_of(x1)};
+  const uint32_t nan0 = __ballot_sync(~0u, x0 != x0), nan1 = __ballot_sync(~0u, x1 != x1);
+  s.g1 += s.g0;  // the lane's two, then the lanes before it
+  Log2Sum upto = s.g1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Log2Sum y{__shfl_up_sync(~0u, upto.whole, o), __shfl_up_sync(~0u, upto.rest, o)};
+    if (lane >= o) upto += y;
+  }
+  const Log2Sum before{upto.whole - s.g1.whole, upto.rest - s.g1.rest};
+  s.g0 += before, s.g1 += before;
+  s.total = Log2Sum{__shfl_sync(~0u, s.g1.whole, 31), __shfl_sync(~0u, s.g1.rest, 31)};
+  const uint32_t to = (2u << lane) - 1, under = to >> 1;
+  s.bad0 = nan0 & to || nan1 & under, s.bad1 = nan0 & to || nan1 & to;
+  s.spoilt = nan0 || nan1;
+  return s;
+}
+
+__device__ __forceinline__ void put_sums(Decays &d, const ChunkSums &s, float scale, int lane) {
+  const Log2Parts p0 = s.g0.parts(s.bad0), p1 = s.g1.parts(s.bad1);
+  *reinterpret_cast<float2 *>(&d.nhi[2 * lane]) = make_float2(-p0.hi, -p1.hi);
+  *reinterpret_cast<float2 *>(&d.nlo[2 * lane]) = make_float2(-p0.lo, -p1.lo);
+  *reinterpret_cast<float2 *>(&d.ei[2 * lane]) = make_float2(p0.power() * scale, p1.power() * scale);
+}
+
+// 32 weights of a row of A from what P's product left in tensor memory: scale P e^{G_i - G_j}, 0 for rows that it does not follow
+// (bits of sees), in pairs; the largest magnitude's bits.  A whole warp.
+template <int DT>
+__device__ __forceinline__ uint32_t pair_weights(uint32_t p, const Decays &d, int i, int j0, uint32_t sees, float log2_scale, pair_t *y) {
+  float x[32];
+  tmem_ld32(p + j0, x);
+  const float mh = -d.nhi[i], ml = log2_scale - d.nlo[i];
+  const pair_t h2 = pack2(mh, mh), l2 = pack2(ml, ml);
+  const bool every = __all_sync(~0u, sees == ~0u);
+  tc_wait_ld();
+  uint32_t most = 0;
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) {
+    const ulonglong2 nh = *reinterpret_cast<const ulonglong2 *>(&d.nhi[j0 + 2 * e]);
+    const ulonglong2 nl = *reinterpret_cast<const ulonglong2 *>(&d.nlo[j0 + 2 * e]);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const float2 g = unpack2(add2(add2(h2, w ? nh.y : nh.x), add2(l2, w ? nl.y : nl.x)));
+      float2 z = unpack2(mul2(pack2(x[2 * (e + w)], x[2 * (e + w) + 1]), pack2(ex2(g.x), ex2(g.y))));
+      if (!every) {
+        z.x = sees >> (2 * (e + w)) & 1 ? z.x : 0.0f;
+        z.y = sees >> (2 * (e + w) + 1) & 1 ? z.y : 0.0f;
+      }
+      if constexpr (DT == SPEC_DTYPE_F16) most = max(most, max(__float_as_uint(z.x) & 0x7fffffffu, __float_as_uint(z.y) & 0x7fffffffu));
+      y[e + w] = pack2(z.x, z.y);
+    }
+  }
+  return most;
+}
+
+// Half of a row of A's two pieces (kHalf bytes apart) to shared memory.
+__device__ __forceinline__ void put_weights(char *a, int i, int half, const uint32_t *hi, const uint32_t *lo) {
+  char *row = a + i * 128;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int to = ((half * 4 + e) ^ (i & 7)) << 4;
+    *reinterpret_cast<uint4 *>(row + to) = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
+    *reinterpret_cast<uint4 *>(row + kChunk * 128 + to) = make_uint4(lo[4 * e], lo[4 * e + 1], lo[4 * e + 2], lo[4 * e + 3]);
+  }
+}
+
+// 16 tokens' outputs from k on, from a column of value_dim to a lane through shared memory to 16 bytes of a token's row to a lane
+// (of this token and the eighth after it).  bad: no number where a sum of O2 is none.
+template <int DT>
+__device__ __forceinline__ void put_outputs(uint32_t o1, uint32_t o2, const Decays &d, int k, int m, float sf, uint16_t *stage, char *out,
+                                            int64_t stride, bool store, pair_t &bad) {
+  const int lane = threadIdx.x & 31, token = lane >> 2;
+  const pair_t sf2 = pack2(sf, sf), none = 0;
+  float x[16], y[16];
+  tmem_ld16(o1 + k, x);
+  tmem_ld16(o2 + k, y);
+  tc_wait_ld();
+  if (k + 16 > m) [[unlikely]] {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) y[e] = k + e < m ? y[e] : 0.0f;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < 16; e += 4) {
+    const ulonglong2 ei = *reinterpret_cast<const ulonglong2 *>(&d.ei[k + e]);
+    ulonglong2 af;
+    if constexpr (DT == SPEC_DTYPE_F16) af = *reinterpret_cast<const ulonglong2 *>(&d.afac[k + e]);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const int z = e + 2 * w;
+      pair_t f = w ? ei.y : ei.x, v = pack2(y[z], y[z + 1]);
+      bad = fma2(v, none, bad);
+      if constexpr (DT == SPEC_DTYPE_F16) f = mul2(f, sf2), v = mul2(v, w ? af.y : af.x);
+      const uint32_t u2 = narrow2<DT>(unpack2(fma2(pack2(x[z], x[z + 1]), f, v)));
+      stage[z * 32 + lane] = static_cast<uint16_t>(u2);
+      stage[(z + 1) * 32 + lane] = static_cast<uint16_t>(u2 >> 16);
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    if (store && k + token + 8 * e < m)
+      *reinterpret_cast<uint4 *>(out + (k + 8 * e) * stride * 2) = *reinterpret_cast<const uint4 *>(stage + e * 256 + lane * 8);
 }
 
 // A row's sum over the rows that it follows, taken again from memory without
 // those that it does not: where a value of theirs is infinite or NaN, the
 // product of a weight of 0 is not 0.  A warp: lane = column of value_dim.
 template <int DT>
-__device__ __noinline__ float row_again(const StateParams &P, const ChunkSmall::Decays &d, uint64_t sees, int b, int h, int t0, int i, int col) {
+__device__ __noinline__ float row_again(const StateParams &P, const Decays &d, uint64_t sees, int b, int h, int t0, int i, int col) {
   const int hk = h / P.group, lane = threadIdx.x & 31;
   const uint16_t *q = reinterpret_cast<const uint16_t *>(P.q) + b * P.qs[0] + (t0 + i) * P.qs[1] + hk * P.qs[2];
   float sum = 0.0f;
@@ -184,6 +297,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const StateParams &P = A.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  pdl_wait();
   // ---- the unit: heads next to one another share keys, so they run side by side
   const int blocks = (P.value_dim + 127) >> 7;
   int u = blockIdx.x;
@@ -270,54 +384,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     for (int c = 0; c < chunks; ++c) {
       const int r = c % kDecayRing, t0 = (c0 + c) * kChunk;
       const int m = min(kChunk, len - t0);
-      Log2Sum g0 = log2_of(x0), g1 = log2_of(x1);
-      // from the first NaN on every sum is one
-      uint32_t nan0 = __ballot_sync(~0u, x0 != x0), nan1 = __ballot_sync(~0u, x1 != x1);
+      const ChunkSums sums = chunk_sums(x0, x1, lane);
       fetch(c + 1, x0, x1);
-      bool bad0, bad1;
-      if (OUT && P.parents) {  // the sums over each row's path, and which rows lie on it
-        const int32_t *parents = P.parents + static_cast<int64_t>(b) * P.n;
-        for (int e = 0; e < 2; ++e) {
-          const int i = 2 * lane + e;
-          uint32_t bits[2] = {0, 0};
-          Log2Sum path{0, 0};
-          bool bad = false;
-          if (i < m) {
-            for (int p = i; p >= 0; p = parents[p]) {
-              path += log2_of(gp[p * P.gs[1]]);
-              bad |= (p & 1 ? nan1 : nan0) >> (p >> 1) & 1;
-              bits[p >> 5] |= 1u << (p & 31);
-            }
-          }
-          sm.follows[i][0] = bits[0], sm.follows[i][1] = bits[1];
-          (e ? g1 : g0) = path, (e ? bad1 : bad0) = bad;
-        }
-      } else {
-        g1 += g0;  // the lane's two, then the lanes before it
-        Log2Sum upto = g1;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const Log2Sum y{__shfl_up_sync(~0u, upto.whole, o), __shfl_up_sync(~0u, upto.rest, o)};
-          if (lane >= o) upto += y;
-        }
-        const Log2Sum before{upto.whole - g1.whole, upto.rest - g1.rest};
-        g0 += before, g1 += before;
-        const uint32_t to = (2u << lane) - 1, under = to >> 1;
-        bad0 = nan0 & to || nan1 & under, bad1 = nan0 & to || nan1 & to;
-      }
-      const Log2Sum total{__shfl_sync(~0u, g1.whole, 31), __shfl_sync(~0u, g1.rest, 31)};
-      const bool spoilt = nan0 || nan1;
-      whole += total.whole, rest += total.rest, lost |= spoilt;
+      whole += sums.total.whole, rest += sums.total.rest, lost |= sums.spoilt;
       if (c >= kDecayRing && !warp_wait(&sm.dec_empty[r], (c / kDecayRing - 1) & 1, dead)) break;
-      ChunkSmall::Decays &d = sm.d[r];
-      const Log2Parts p0 = g0.parts(bad0), p1 = g1.parts(bad1);
-      const Log2Parts q0 = Log2Sum{total.whole - g0.whole, total.rest - g0.rest}.parts(spoilt);
-      const Log2Parts q1 = Log2Sum{total.whole - g1.whole, total.rest - g1.rest}.parts(spoilt);
-      *reinterpret_cast<float2 *>(&d.nhi[2 * lane]) = make_float2(-p0.hi, -p1.hi);
-      *reinterpret_cast<float2 *>(&d.nlo[2 * lane]) = make_float2(-p0.lo, -p1.lo);
-      *reinterpret_cast<float2 *>(&d.ei[2 * lane]) = make_float2(p0.power() * P.scale, p1.power() * P.scale);
+      Decays &d = sm.d[r];
+      put_sums(d, sums, P.scale, lane);
+      const Log2Parts q0 = Log2Sum{sums.total.whole - sums.g0.whole, sums.total.rest - sums.g0.rest}.parts(sums.spoilt);
+      const Log2Parts q1 = Log2Sum{sums.total.whole - sums.g1.whole, sums.total.rest - sums.g1.rest}.parts(sums.spoilt);
       *reinterpret_cast<float2 *>(&d.left[2 * lane]) = make_float2(2 * lane < m ? q0.power() : 0.0f, 2 * lane + 1 < m ? q1.power() : 0.0f);
-      if (lane == 0) d.lam = total.parts(spoilt).power(), d.kfac = 1.0f;
+      if (lane == 0) d.lam = sums.total.parts(sums.spoilt).power(), d.kfac = 1.0f;
       warp_arrive(&sm.dec_full[r], lane);
     }
     if (!OUT && lane == 0 && dv0 == 0) {  // (segments of many chunks: the sums in 64 bits, the whole part no further than fp32's exponents)
@@ -585,7 +661,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if constexpr (OUT) {
       const int i = (warp & 1) * 32 + lane, half = warp >> 3, j0 = half * 32;
       const int group = (warp >> 3) * 64 + i;  // the thread among the 128
-      const bool tree = P.parents != nullptr;
       const float log2_scale = log2f(P.scale);
       int met = 0;
 #pragma unroll 1
@@ -594,36 +669,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (!warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead)) break;
         if (!wait4(sm.p_full, c)) break;
         tc_fence_after();
-        const ChunkSmall::Decays &d = sm.d[r];
+        const Decays &d = sm.d[r];
         // which of the half's rows this one follows
-        const uint32_t sees = tree ? sm.follows[i][half] : i >= j0 + 31 ? ~0u : i < j0 ? 0u : (2u << (i - j0)) - 1;
+        const uint32_t sees = i >= j0 + 31 ? ~0u : i < j0 ? 0u : (2u << (i - j0)) - 1;
         uint32_t hi[16], lo[16];
         float back = 1.0f;
         if (__any_sync(~0u, sees != 0)) {
-          float x[32];
-          tmem_ld32(tmem + (static_cast<uint32_t>(warp & 3) << 21) + kP + j0, x);
-          const float mh = -d.nhi[i], ml = log2_scale - d.nlo[i];
-          const pair_t h2 = pack2(mh, mh), l2 = pack2(ml, ml);
-          const bool every = __all_sync(~0u, sees == ~0u);
-          tc_wait_ld();
-          uint32_t most = 0;
           pair_t y[16];
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const ulonglong2 nh = *reinterpret_cast<const ulonglong2 *>(&d.nhi[j0 + 2 * e]);
-            const ulonglong2 nl = *reinterpret_cast<const ulonglong2 *>(&d.nlo[j0 + 2 * e]);
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              const float2 g = unpack2(add2(add2(h2, w ? nh.y : nh.x), add2(l2, w ? nl.y : nl.x)));
-              float2 z = unpack2(mul2(pack2(x[2 * (e + w)], x[2 * (e + w) + 1]), pack2(ex2(g.x), ex2(g.y))));
-              if (!every) {
-                z.x = sees >> (2 * (e + w)) & 1 ? z.x : 0.0f;
-                z.y = sees >> (2 * (e + w) + 1) & 1 ? z.y : 0.0f;
-              }
-              if constexpr (F16) most = max(most, max(__float_as_uint(z.x) & 0x7fffffffu, __float_as_uint(z.y) & 0x7fffffffu));
-              y[e + w] = pack2(z.x, z.y);
-            }
-          }
+          const uint32_t most = pair_weights<DT>(tmem + (static_cast<uint32_t>(warp & 3) << 21) + kP, d, i, j0, sees, log2_scale, y);
           if constexpr (F16) sm.amax[c & 1][half][i] = most;
 #pragma unroll
           for (int e = 0; e < 16; ++e)
@@ -651,13 +704,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         if (F16 && half == 0) sm.d[r].afac[i] = back;
         if (c > 0 && !wait4(sm.o2_full, c - 1)) break;
-        char *row = smem + S::kA + i * 128;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int to = ((half * 4 + e) ^ (i & 7)) << 4;
-          *reinterpret_cast<uint4 *>(row + to) = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
-          *reinterpret_cast<uint4 *>(row + S::kHalf + to) = make_uint4(lo[4 * e], lo[4 * e + 1], lo[4 * e + 2], lo[4 * e + 3]);
-        }
+        put_weights(smem + S::kA, i, half, hi, lo);
         if (m < kChunk) {  // values past the request's rows take no part, whatever they are
           const int sv = c % S::kStagesV;
           if (!wait4(sm.full, c)) break;
@@ -681,54 +728,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int r = c % kDecayRing, t0 = (c0 + c) * kChunk, m = min(kChunk, len - t0);
         if (!wait4(sm.o2_full, c)) break;
         tc_fence_after();
-        const ChunkSmall::Decays &d = sm.d[r];
+        const Decays &d = sm.d[r];
         const float sf = F16 ? d.sfac[at] : 1.0f;
-        const pair_t sf2 = pack2(sf, sf), none = 0;
         pair_t bad = 0;
-        // 16 tokens at a time through shared memory, from a column to a lane to 16 bytes of a token's row to a lane
-        uint16_t *const stage = sm.stage[quarter][0];
-        const int token = lane >> 2, col = quarter * 32 + (lane & 3) * 8;
-        char *o = reinterpret_cast<char *>(P.out) + (b * P.os[0] + h * P.os[2] + (t0 + token) * P.os[1] + dv0 + col) * 2;
-        const bool store = dv0 + col < P.value_dim;
+        const int col = quarter * 32 + (lane & 3) * 8;
+        char *o = reinterpret_cast<char *>(P.out) + (b * P.os[0] + h * P.os[2] + (t0 + (lane >> 2)) * P.os[1] + dv0 + col) * 2;
 #pragma unroll 1
-        for (int k = 0; k < kChunk; k += 16) {
-          float x[16], y[16];
-          tmem_ld16(tmem + lanes + kO1 + (c & 1) * 64 + k, x);
-          tmem_ld16(tmem + lanes + kO2 + k, y);
-          tc_wait_ld();
-          if (k + 16 > m) [[unlikely]] {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = k + e < m ? y[e] : 0.0f;
-          }
-          __syncwarp();
-#pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const ulonglong2 ei = *reinterpret_cast<const ulonglong2 *>(&d.ei[k + e]);
-            ulonglong2 af;
-            if constexpr (F16) af = *reinterpret_cast<const ulonglong2 *>(&d.afac[k + e]);
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              const int z = e + 2 * w;
-              pair_t f = w ? ei.y : ei.x, o2 = pack2(y[z], y[z + 1]);
-              bad = fma2(o2, none, bad);
-              if constexpr (F16) f = mul2(f, sf2), o2 = mul2(o2, w ? af.y : af.x);
-              const uint32_t u2 = narrow2<DT>(unpack2(fma2(pack2(x[z], x[z + 1]), f, o2)));
-              stage[z * 32 + lane] = static_cast<uint16_t>(u2);
-              stage[(z + 1) * 32 + lane] = static_cast<uint16_t>(u2 >> 16);
-            }
-          }
-          __syncwarp();
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (store && k + token + 8 * e < m) *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(stage + e * 256 + lane * 8);
-            o += P.os[1] * 16;
-          }
-        }
+        for (int k = 0; k < kChunk; k += 16)
+          put_outputs<DT>(tmem + lanes + kO1 + (c & 1) * 64, tmem + lanes + kO2, d, k, m, sf, sm.stage[quarter][0], o, P.os[1],
+                          dv0 + col < P.value_dim, bad);
         const float2 b2 = unpack2(bad);
         if (__any_sync(~0u, !(b2.x == 0.0f && b2.y == 0.0f))) [[unlikely]] {  // a row's sum that is no number: without the rows that it does not follow
 #pragma unroll 1
           for (int i = 0; i < m; ++i) {
-            const uint64_t sees = P.parents ? static_cast<uint64_t>(sm.follows[i][1]) << 32 | sm.follows[i][0] : (2ull << i) - 1;
+            const uint64_t sees = (2ull << i) - 1;
             float x[8];
             tmem_ld8(tmem + lanes + kO1 + (c & 1) * 64 + (i & ~7), x);
             tc_wait_ld();
@@ -763,6 +776,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (warp == 10) tmem_free(tmem, 512);
 }
 
+// A launch whose blocks may start before the kernel in front of it has ended (they wait for it before they read anything it wrote).
+template <class Kernel>
+cudaError_t launch_behind(Kernel kern, unsigned grid, int threads, int bytes, cudaStream_t st, const StateChunkPlan &A, const CUtensorMap *maps) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = trace_enabled() ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, A, maps[0], maps[1], maps[2]);
+}
+
 template <int DT, int DK, bool OUT>
 std::atomic<uint64_t> chunk_smem{0};
 
@@ -777,8 +806,281 @@ cudaError_t launch_chunks(const StateChunkPlan &A, const CUtensorMap *maps, cuda
   B.pieces = OUT ? A.segs : (A.segs - 1) * A.parts;
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(A.p.B) * B.pieces * ((A.p.value_dim + 127) / 128) * A.p.heads);
   const bool again = !state_overlaps(A.p);
-  return trace_launch(OUT ? "state_chunk" : "state_chunk_local", st, [&] { kern<<<grid, kChunkThreads, S::kBytes, st>>>(B, maps[0], maps[1], maps[2]); },
-                      again || !OUT);
+  return trace_launch_ex(OUT ? "state_chunk" : "state_chunk_local", st, [&] { return launch_behind(kern, grid, kChunkThreads, S::kBytes, st, B, maps); },
+                         again || !OUT);
+}
+
+// ------------------------------------------------------------------ up to 64 rows over states that stay
+//
+// A chain or a tree of one chunk, nothing written but outputs: a CTA for each
+// (request, head, 128 columns) goes through the steps above once, P's columns
+// of tensor memory becoming O2's, so that two CTAs share an SM and one loads
+// its state while the other computes.  16 trees of 60 nodes, 48 heads: 64 us
+// as a chunk of the kernel above (one CTA to an SM), 31 us so.
+constexpr int kShortThreads = 256;
+
+template <int DK>
+struct ShortShape {
+  static constexpr int kHalf = kChunk * 128;
+  static constexpr int kTileK = DK / 64 * kHalf, kTileV = 2 * kHalf;
+  static constexpr int kQ = 0, kK = kQ + kTileK, kV = kK + kTileK, kA = kV + kTileV, kSmall = kA + 2 * kHalf;
+  static constexpr int kBytes = kSmall + 14336 + 1024;
+};
+
+struct ShortSmall {
+  Decays d;
+  alignas(16) uint16_t stage[8][16][32];
+  uint32_t follows[kChunk][2];  // the rows that a row follows, itself among them
+  uint32_t smax[2][128], amax[2][kChunk];
+  uint64_t full, p_full, o1_full, o2_full;
+  uint32_t tmem;
+  int dead;
+};
+static_assert(sizeof(ShortSmall) <= 14336 && ShortShape<128>::kBytes <= 113 * 1024);
+
+template <int DT, int DK>
+__global__ void __launch_bounds__(kShortThreads, 2)
+    state_short_kernel(const StateChunkPlan A, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                       const __grid_constant__ CUtensorMap v_map) {
+  using S = ShortShape<DK>;
+  constexpr bool F16 = DT == SPEC_DTYPE_F16;
+  constexpr uint32_t kSHi = 0, kSLo = 64, kO1 = 128, kP = 192;  // tensor memory; O2 in P's place
+  extern __shared__ char raw[];
+  char *const smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  ShortSmall &sm = *reinterpret_cast<ShortSmall *>(smem + S::kSmall);
+  const StateParams &P = A.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3, half = warp >> 2, at = quarter * 32 + lane;
+  const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
+  if (tid == 0) {
+    bar_init(&sm.full, 1), bar_init(&sm.p_full, 1), bar_init(&sm.o1_full, 1), bar_init(&sm.o2_full, 1);
+    bar_init_fence();
+    sm.dead = 0;
+  }
+  if (warp == 0) tmem_alloc(&sm.tmem, 256);
+  pdl_wait();
+  const int blocks = (P.value_dim + 127) >> 7;
+  int u = blockIdx.x;
+  const int h = u % P.heads;
+  u /= P.heads;
+  const int dv0 = u % blocks * 128, b = u / blocks, hk = h / P.group, dv = dv0 + at;
+  const bool ok = A.verdict[b] == SPEC_STATUS_OK;
+  const int m = ok ? (P.counts ? P.counts[b] : P.n) : 0;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  volatile int *dead = &sm.dead;
+
+  if (m > 0) {
+    if (tid == 0) {
+      bar_expect(&sm.full, 2 * S::kTileK + S::kTileV);
+      for (int e = 0; e < DK / 64; ++e) {
+        tensor_load_4d(smem + S::kQ + e * S::kHalf, &q_map, e * 64, hk, 0, b, &sm.full);
+        tensor_load_4d(smem + S::kK + e * S::kHalf, &k_map, e * 64, hk, 0, b, &sm.full);
+      }
+      for (int e = 0; e < 2; ++e) tensor_load_4d(smem + S::kV + e * S::kHalf, &v_map, dv0 + e * 64, h, 0, b, &sm.full);
+    }
+    __syncwarp();
+    // ---- the state: half of a lane's row to a thread, its pieces to tensor memory
+    constexpr int OWN = DK / 2;
+    float s[OWN];
+    const float *from = nullptr;
+    const int64_t size = static_cast<int64_t>(P.key_dim) * P.value_dim;
+    if (P.from.state) {
+      const int slot = P.from.slots ? P.from.slots[b] : b;
+      if (slot >= 0) from = P.from.state + slot * P.from.slot_stride + h * size;
+    }
+    const bool mine = from && dv < P.value_dim;
+#pragma unroll
+    for (int e = 0; e < OWN; ++e) {
+      const int d = half * OWN + e;
+      s[e] = mine && d < P.key_dim ? from[static_cast<int64_t>(d) * P.value_dim + dv] : 0.0f;
+    }
+    // ---- the decays, while the state is on its way
+    if (warp == 1) {
+      const float *gp = P.decay + b * P.gs[0] + h * P.gs[2];
+      ChunkSums sums;
+      if (P.parents) {  // over each row's path, and which rows lie on it
+        const int32_t *parents = P.parents + static_cast<int64_t>(b) * P.n;
+        for (int e = 0; e < 2; ++e) {
+          const int i = 2 * lane + e;
+          uint32_t bits[2] = {0, 0};
+          Log2Sum path{0, 0};
+          bool bad = false;
+          if (i < m) {
+            for (int p = i; p >= 0; p = parents[p]) {
+              const float x = gp[p * P.gs[1]];
+              path += log2_of(x);
+              bad |= x != x;
+              bits[p >> 5] |= 1u << (p & 31);
+            }
+          }
+          sm.follows[i][0] = bits[0], sm.follows[i][1] = bits[1];
+          (e ? sums.g1 : sums.g0) = path, (e ? sums.bad1 : sums.bad0) = bad;
+        }
+      } else {
+        sums = chunk_sums(2 * lane < m ? gp[2 * lane * P.gs[1]] : 0.0f, 2 * lane + 1 < m ? gp[(2 * lane + 1) * P.gs[1]] : 0.0f, lane);
+        for (int e = 0; e < 2; ++e) {
+          const uint64_t bits = (2ull << (2 * lane + e)) - 1;
+          sm.follows[2 * lane + e][0] = static_cast<uint32_t>(bits), sm.follows[2 * lane + e][1] = static_cast<uint32_t>(bits >> 32);
+        }
+      }
+      put_sums(sm.d, sums, P.scale, lane);
+    }
+    float sf = 1.0f;
+    if constexpr (F16) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int e = 0; e < OWN; ++e) most = max(most, __float_as_uint(s[e]) & 0x7fffffffu);
+      sm.smax[half][at] = most;
+      __syncthreads();
+      const float fit = fit_half(max(most, sm.smax[half ^ 1][at]), sf);
+#pragma unroll
+      for (int e = 0; e < OWN; ++e) s[e] *= fit;
+    }
+#pragma unroll
+    for (int k = 0; k < OWN / 16; ++k) {
+      uint32_t hi[8], lo[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) split2<DT>(pack2(s[16 * k + 2 * e], s[16 * k + 2 * e + 1]), hi[e], lo[e]);
+      tmem_st8(tmem + lanes + kSHi + half * (OWN / 2) + k * 8, hi);
+      tmem_st8(tmem + lanes + kSLo + half * (OWN / 2) + k * 8, lo);
+    }
+    tc_wait_st();
+    tc_fence_before();
+    __syncthreads();
+    // ---- P, O1
+    int begun = 0;  // products (warp 0)
+    if (warp == 0 && warp_wait(&sm.full, 0, dead)) {
+      tc_fence_after();
+      if (elect_one()) {
+        constexpr uint32_t kId = rows_desc<DT>(kChunk, false, false);
+        const uint64_t q_desc = matrix_desc(smem_u32(smem + S::kQ), 16, 1024, kSwizzle128);
+        const uint64_t k_desc = matrix_desc(smem_u32(smem + S::kK), 16, 1024, kSwizzle128);
+#pragma unroll 1
+        for (int x = 0; x < DK / 64; ++x)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_ss(tmem + kP, q_desc + ((x * S::kHalf) >> 4) + 2 * k, k_desc + ((x * S::kHalf) >> 4) + 2 * k, kId, x + k > 0);
+        tc_commit(&sm.p_full);
+#pragma unroll 1
+        for (int x = 0; x < DK / 32; ++x)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_ta(tmem + kO1, tmem + (x & 1 ? kSLo : kSHi) + (x >> 1) * 32 + k * 8, q_desc + (((x >> 1) * S::kHalf) >> 4) + 2 * k, kId, x + k > 0);
+        tc_commit(&sm.o1_full);
+      }
+      begun = 2;
+    }
+    __syncwarp();
+    // ---- A: half of a row to a thread of the lower lanes
+    const int i = at;
+    uint32_t hi[16], lo[16], most = 0;
+    pair_t y[16];
+    bool any = false;
+    if (quarter < 2 && warp_wait(&sm.p_full, 0, dead)) {
+      tc_fence_after();
+      const uint32_t sees = sm.follows[i][half];
+      any = __any_sync(~0u, sees != 0);
+      if (any) most = pair_weights<DT>(tmem + lanes + kP, sm.d, i, half * 32, sees, log2f(P.scale), y);
+    }
+    float fit = 1.0f;
+    if constexpr (F16) {
+      if (quarter < 2) sm.amax[half][i] = most;
+      __syncthreads();
+      if (quarter < 2) {
+        float back;
+        fit = fit_half(max(most, sm.amax[half ^ 1][i]), back);
+        if (half == 0) sm.d.afac[i] = back;
+      }
+    }
+    if (quarter < 2) {
+      const pair_t f = pack2(fit, fit);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        if (any) split2<DT>(F16 ? mul2(y[e], f) : y[e], hi[e], lo[e]);
+        else hi[e] = lo[e] = 0;
+      }
+      put_weights(smem + S::kA, i, half, hi, lo);
+    } else {  // values past the request's rows take no part, whatever they are (their copy has landed when P has)
+      if (warp_wait(&sm.full, 0, dead))
+        for (int e = (half * 2 + quarter - 2) * 32 + lane; e < (kChunk - m) * 16; e += 128)
+          *reinterpret_cast<uint4 *>(smem + S::kV + (e & 1) * S::kHalf + (m + (e >> 4)) * 128 + (e >> 1 & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_async_shared();
+    tc_fence_before();
+    __syncthreads();
+    // ---- O2
+    const bool off = __any_sync(~0u, *dead);
+    if (warp == 0 && !off) {
+      tc_fence_after();
+      if (elect_one()) {
+        constexpr uint32_t kId = rows_desc<DT>(kChunk, true, false);
+        const uint64_t v_desc = matrix_desc(smem_u32(smem + S::kV), S::kHalf, 1024, kSwizzle128);
+        const uint64_t a_desc = matrix_desc(smem_u32(smem + S::kA), 16, 1024, kSwizzle128);
+#pragma unroll 1
+        for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_f16_ss(tmem + kP, v_desc + 128 * k, a_desc + ((piece * S::kHalf) >> 4) + 2 * k, kId, piece + k > 0);
+        tc_commit(&sm.o2_full);
+      }
+      begun = 3;
+    }
+    __syncwarp();
+    // ---- the outputs: half of the tokens to a warp
+    if (!off && warp_wait(&sm.o1_full, 0, dead) && warp_wait(&sm.o2_full, 0, dead)) {
+      tc_fence_after();
+      pair_t bad = 0;
+      const int col = quarter * 32 + (lane & 3) * 8;
+      char *o = reinterpret_cast<char *>(P.out) + (b * P.os[0] + h * P.os[2] + (lane >> 2) * P.os[1] + dv0 + col) * 2;
+#pragma unroll 1
+      for (int k = half * 32; k < half * 32 + 32 && k < m; k += 16)
+        put_outputs<DT>(tmem + lanes + kO1, tmem + lanes + kP, sm.d, k, m, sf, sm.stage[warp][0], o, P.os[1], dv0 + col < P.value_dim, bad);
+      const float2 b2 = unpack2(bad);
+      if (__any_sync(~0u, !(b2.x == 0.0f && b2.y == 0.0f))) [[unlikely]] {  // as in the kernel above
+#pragma unroll 1
+        for (int r = half * 32; r < min(m, half * 32 + 32); ++r) {
+          float x[8];
+          tmem_ld8(tmem + lanes + kO1 + (r & ~7), x);
+          tc_wait_ld();
+          float v = x[0];
+#pragma unroll
+          for (int e = 1; e < 8; ++e) v = (r & 7) == e ? x[e] : v;
+          const uint64_t sees = static_cast<uint64_t>(sm.follows[r][1]) << 32 | sm.follows[r][0];
+          v = fmaf(v, sm.d.ei[r] * sf, row_again<DT>(P, sm.d, sees, b, h, 0, r, dv) * P.scale);
+          if (dv < P.value_dim) reinterpret_cast<uint16_t *>(P.out)[b * P.os[0] + r * P.os[1] + h * P.os[2] + dv] = narrow<DT>(v);
+        }
+      }
+    }
+    if (warp == 0 && __any_sync(~0u, *dead)) [[unlikely]] {  // (nothing that was begun may reach memory that the CTA has left)
+      ring_land(&sm.full, 1, 1);
+      if (begun >= 1) ring_land(&sm.p_full, 1, 1), ring_land(&sm.o1_full, 1, 1);
+      if (begun == 3) ring_land(&sm.o2_full, 1, 1);
+    }
+  }
+  // rows past the count
+  const int pieces = min(128, P.value_dim - dv0) >> 3;
+  uint16_t *o = reinterpret_cast<uint16_t *>(P.out) + b * P.os[0] + h * P.os[2] + dv0;
+  for (int e = tid; e < (P.n - m) * pieces; e += kShortThreads)
+    *reinterpret_cast<uint4 *>(o + (m + e / pieces) * P.os[1] + e % pieces * 8) = make_uint4(0, 0, 0, 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0 && *dead && P.status) atomicMax(&P.status[b], SPEC_STATUS_TIMEOUT);
+  if (warp == 0) tmem_free(tmem, 256);
+}
+
+template <int DT, int DK>
+std::atomic<uint64_t> short_smem{0};
+
+template <int DT, int DK>
+cudaError_t launch_short(const StateChunkPlan &A, const CUtensorMap *maps, cudaStream_t st) {
+  auto kern = state_short_kernel<DT, DK>;
+  const int bytes = ShortShape<DK>::kBytes;
+  const cudaError_t e = once_per_device([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); }, short_smem<DT, DK>);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(A.p.B) * ((A.p.value_dim + 127) / 128) * A.p.heads);
+  return trace_launch_ex("state_short", st, [&] { return launch_behind(kern, grid, kShortThreads, bytes, st, A, maps); });
 }
 
 }  // namespace

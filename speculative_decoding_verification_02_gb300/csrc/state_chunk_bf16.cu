@@ -9,4 +9,9 @@ cudaError_t launch_state_chunk_bf16(const StateChunkPlan &A, bool outputs, const
   return outputs ? launch_chunks<DT, 128, true>(A, maps, st) : launch_chunks<DT, 128, false>(A, maps, st);
 }
 
+cudaError_t launch_state_short_bf16(const StateChunkPlan &A, const CUtensorMap *maps, cudaStream_t st) {
+  constexpr int DT = SPEC_DTYPE_BF16;
+  return A.p.key_dim <= 64 ? launch_short<DT, 64>(A, maps, st) : launch_short<DT, 128>(A, maps, st);
+}
+
 }  // namespace sv
