@@ -584,8 +584,8 @@ size_t spec_cache_workspace_size(int op, const spec_cache *cache, int B, int N, 
  * or SPEC_STATUS_BAD_TREE.  Such a request's state is not written and its rows
  * of out are 0.
  *
- * spec_state_forward -- n tokens behind each request's state: a prompt, a
- * part of one, a single token.
+ * spec_state_forward -- n tokens (at most 2^30) behind each request's state: a
+ * prompt, a part of one, a single token.
  *   from        the states before; slot -1, and every slot when from->state is
  *               NULL: a state of zeros.
  *   to          the states after (heads, key_dim and value_dim as in from), or

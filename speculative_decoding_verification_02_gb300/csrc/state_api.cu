@@ -10,6 +10,7 @@ namespace sv {
 namespace {
 
 constexpr int64_t kMaxGrid = 2147483647;
+constexpr int kMaxTokens = 1 << 30;  // (tokens are numbered by an int, a chunk past the last among them)
 
 int state_fail(cudaError_t e, const char *where) {
   char text[256];
@@ -54,7 +55,7 @@ int check_call(StateParams &P, const spec_state *from, const spec_state *to, con
     if (to->heads != from->heads || to->key_dim != from->key_dim || to->value_dim != from->value_dim) return SPEC_EINVAL;
   }
   if (dtype != SPEC_DTYPE_BF16 && dtype != SPEC_DTYPE_F16) return SPEC_EDTYPE;
-  if (B < 0 || n < 0 || key_heads < 1 || from->heads % key_heads || !strides_ok(k_stride) || !strides_ok(v_stride) ||
+  if (B < 0 || n < 0 || n > kMaxTokens || key_heads < 1 || from->heads % key_heads || !strides_ok(k_stride) || !strides_ok(v_stride) ||
       !strides_ok(decay_stride) || (outputs && (!strides_ok(q_stride) || !strides_ok(out_stride))))
     return SPEC_EINVAL;
   if (!on_grain(k, 2) || !on_grain(v, 2) || !on_grain(decay, 4) || !on_grain(q, 2) || !on_grain(out, 2)) return SPEC_EINVAL;
@@ -90,7 +91,7 @@ using namespace sv;
 extern "C" {
 
 size_t spec_state_workspace_size(int op, const spec_state *state, int B, int n) {
-  if (check_geometry(state) != SPEC_OK || B < 0 || n < 0) return 0;
+  if (check_geometry(state) != SPEC_OK || B < 0 || n < 0 || n > kMaxTokens) return 0;
   if (op != SPEC_OP_STATE_FORWARD && (op != SPEC_OP_STATE_ATTEND || n > SPEC_MAX_NODES)) return 0;
   StateParams P{};
   P.B = B, P.n = n, P.heads = state->heads, P.key_dim = state->key_dim, P.value_dim = state->value_dim;

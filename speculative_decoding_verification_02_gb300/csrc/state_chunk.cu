@@ -10,6 +10,8 @@ namespace sv {
 namespace {
 
 constexpr int kChunkRows = 64;
+constexpr int64_t kMostUnits = 1 << 26;  // (CTAs are numbered by an int, segments and halves of value_dim among them)
+constexpr int kSortedRequests = 4096;  // (each counts those before it)
 
 __device__ __forceinline__ int block_sum64(int x) {
   __shared__ int part[2];
@@ -36,9 +38,10 @@ __global__ void __launch_bounds__(64) state_verdict_kernel(const StateParams P, 
     if (__syncthreads_or(tid < count && (tid == 0 ? p != -1 : p < 0 || p >= tid))) status = SPEC_STATUS_BAD_TREE;
   }
   int before = 0;
-  if (P.counts)
+  const bool sorted = P.counts && P.B <= kSortedRequests;
+  if (sorted)
     for (int i = tid; i < P.B; i += 64) before += P.counts[i] > count || (P.counts[i] == count && i < b);
-  before = P.counts ? block_sum64(before) : b;
+  before = sorted ? block_sum64(before) : b;
   if (tid == 0) {
     order[before] = b;
     verdict[b] = status;
@@ -118,8 +121,22 @@ std::pair<StateChunkPlan, size_t> chunk_plan(const StateParams &P, void *workspa
   return {A, at};
 }
 
+// Fewest tokens of a call.  48 heads of 128 x 128, in a graph of calls, the kernel for few rows against these, us (1, 8 and 64
+// requests):
+//   chains, states only read  8 rows 6.6 / 7.6, 13 / 14, 74 / 73; 12 rows 8.0 / 7.7, 16 / 14, 95 / 74.  Of drafts of different lengths
+//                             the one for few rows does those that there are: 9 rows at most, 69 / 75 at 64 requests
+//   trees (a path of rows)    4 rows 8.7 / 8.0, 16 / 15, 111 / 80; 8 rows 16 / 8.6, 28 / 17, 201 / 88
+//   states written            16 tokens 11.5 / 11.7, 27 / 30, 166 / 255; 24: 16 / 11.5, 38 / 30, 238 / 256; 32: 20 / 11.5, 48 / 30,
+//                             303 / 256 (a CTA of the main kernel has an SM to itself, and its start is not hidden: the more units,
+//                             the later it pays)
+int fewest_tokens(const StateParams &P) {
+  if (P.parents) return 4;
+  if (is_short(P)) return P.counts ? 12 : 9;
+  return static_cast<int64_t>(P.B) * P.heads * value_blocks(P) > 4 * device_sm_count() ? 25 : 17;
+}
+
 bool taken_sizes(const StateParams &P) {
-  return P.key_dim <= 128 && P.n > 16 && (!P.parents || P.n <= kChunkRows) && static_cast<int64_t>(P.B) * P.heads * 2 < (1 << 26);
+  return P.key_dim <= 128 && P.n >= fewest_tokens(P) && (!P.parents || P.n <= kChunkRows) && static_cast<int64_t>(P.B) * P.heads * 2 < kMostUnits;
 }
 
 // A copy reads 64 columns of 64 tokens of one head.
@@ -170,9 +187,9 @@ bool state_on_tensor_cores(const StateParams &P) {
          map_strides(P.vs, P.heads, P.n, P.B);
 }
 
+// (whatever the call: with or without parents, counts and states to write)
 size_t state_chunk_workspace(const StateParams &P) {
-  if (!taken_sizes(P)) return 0;
-  return chunk_plan(P, nullptr).second;
+  return P.key_dim <= 128 && P.n >= 4 && static_cast<int64_t>(P.B) * P.heads * 2 < kMostUnits ? chunk_plan(P, nullptr).second : 0;
 }
 
 cudaError_t launch_state_chunks(const StateParams &P, void *workspace, cudaStream_t st) {

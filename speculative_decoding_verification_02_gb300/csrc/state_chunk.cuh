@@ -214,9 +214,9 @@ __device__ __forceinline__ void put_weights(char *a, int i, int half, const uint
 }
 
 // 16 tokens' outputs from k on, from a column of value_dim to a lane through shared memory to 16 bytes of a token's row to a lane
-// (of this token and the eighth after it).  bad: no number where a sum of O2 is none.
+// (of the token that out points at and the eighth after it; out goes on to the sixteenth).  bad: no number where a sum of O2 is none.
 template <int DT>
-__device__ __forceinline__ void put_outputs(uint32_t o1, uint32_t o2, const Decays &d, int k, int m, float sf, uint16_t *stage, char *out,
+__device__ __forceinline__ void put_outputs(uint32_t o1, uint32_t o2, const Decays &d, int k, int m, float sf, uint16_t *stage, char *&out,
                                             int64_t stride, bool store, pair_t &bad) {
   const int lane = threadIdx.x & 31, token = lane >> 2;
   const pair_t sf2 = pack2(sf, sf), none = 0;
@@ -247,9 +247,10 @@ __device__ __forceinline__ void put_outputs(uint32_t o1, uint32_t o2, const Deca
   }
   __syncwarp();
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
-    if (store && k + token + 8 * e < m)
-      *reinterpret_cast<uint4 *>(out + (k + 8 * e) * stride * 2) = *reinterpret_cast<const uint4 *>(stage + e * 256 + lane * 8);
+  for (int e = 0; e < 2; ++e) {
+    if (store && k + token + 8 * e < m) *reinterpret_cast<uint4 *>(out) = *reinterpret_cast<const uint4 *>(stage + e * 256 + lane * 8);
+    out += stride * 16;
+  }
 }
 
 // A row's sum over the rows that it follows, taken again from memory without
@@ -832,6 +833,8 @@ struct ShortSmall {
   alignas(16) uint16_t stage[8][16][32];
   uint32_t follows[kChunk][2];  // the rows that a row follows, itself among them
   uint32_t smax[2][128], amax[2][kChunk];
+  int parent[kChunk];
+  float g[kChunk];
   uint64_t full, p_full, o1_full, o2_full;
   uint32_t tmem;
   int dead;
@@ -901,15 +904,19 @@ __global__ void __launch_bounds__(kShortThreads, 2)
       const float *gp = P.decay + b * P.gs[0] + h * P.gs[2];
       ChunkSums sums;
       if (P.parents) {  // over each row's path, and which rows lie on it
-        const int32_t *parents = P.parents + static_cast<int64_t>(b) * P.n;
+        for (int i = lane; i < m; i += 32) {
+          sm.parent[i] = P.parents[static_cast<int64_t>(b) * P.n + i];
+          sm.g[i] = gp[i * P.gs[1]];
+        }
+        __syncwarp();
         for (int e = 0; e < 2; ++e) {
           const int i = 2 * lane + e;
           uint32_t bits[2] = {0, 0};
           Log2Sum path{0, 0};
           bool bad = false;
           if (i < m) {
-            for (int p = i; p >= 0; p = parents[p]) {
-              const float x = gp[p * P.gs[1]];
+            for (int p = i; p >= 0; p = sm.parent[p]) {
+              const float x = sm.g[p];
               path += log2_of(x);
               bad |= x != x;
               bits[p >> 5] |= 1u << (p & 31);
@@ -1032,7 +1039,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
       tc_fence_after();
       pair_t bad = 0;
       const int col = quarter * 32 + (lane & 3) * 8;
-      char *o = reinterpret_cast<char *>(P.out) + (b * P.os[0] + h * P.os[2] + (lane >> 2) * P.os[1] + dv0 + col) * 2;
+      char *o = reinterpret_cast<char *>(P.out) + (b * P.os[0] + h * P.os[2] + (half * 32 + (lane >> 2)) * P.os[1] + dv0 + col) * 2;
 #pragma unroll 1
       for (int k = half * 32; k < half * 32 + 32 && k < m; k += 16)
         put_outputs<DT>(tmem + lanes + kO1, tmem + lanes + kP, sm.d, k, m, sf, sm.stage[warp][0], o, P.os[1], dv0 + col < P.value_dim, bad);

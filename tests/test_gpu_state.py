@@ -265,12 +265,14 @@ def test_many_requests(api, Dk, Dv, Hk, G, dtype, n):
     bad = {20: api.STATUS_BAD_SLOT, 30: api.STATUS_BAD_LENGTH}
     assert o["status"].tolist() == [bad.get(b, 0) for b in range(B)]
     d = api.spec_state_attend(*r.gpu("q", "k", "v", "g"), pool, slots=i32(slots), n_query=i32(counts))
-    assert torch.equal(d["out"], out) and d["status"].tolist() == o["status"].tolist()
+    assert d["status"].tolist() == o["status"].tolist()  # (which may be another kernel's work: the same to their bounds)
     for b in list(range(0, B, 9)) + [7, 20, 30, B - 1]:
         if b in bad:
-            assert not out[b].any() and bool((dst[b] == 3).all())
+            assert not out[b].any() and not d["out"][b].any() and bool((dst[b] == 3).all())
             continue
         outs, last = r.want(b, r.pool[slots[b]] if slots[b] >= 0 else r.zeros(), list(range(counts[b])))
+        ref.check_out(d["out"][b, :counts[b]], outs, Dk, n, dtype, PIECES)
+        assert not d["out"][b, counts[b]:].any()
         ref.check_out(out[b, :counts[b]], outs, Dk, n, dtype)
         assert not out[b, counts[b]:].any()
         ref.check_state(dst[b], last, Dk, n)
@@ -287,6 +289,34 @@ def test_many_requests(api, Dk, Dv, Hk, G, dtype, n):
         ref.check_state(pool[slots[b]], r.want(b, r.pool[slots[b]], index[b, :counts[b]].tolist())[1], Dk, n)
     for s in set(range(B + 3)) - set(slots):
         assert torch.equal(pool[s], was[s])
+
+
+@pytest.mark.parametrize("n", [3, 90])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-38, 3e30])
+def test_scales(api, n, scale):
+    """Scales that are zero, negative, or far from 1 (the values so that the outputs stay within their type)."""
+    r = Rows(1, n, 1, 2, 64, 64, BF, 35)
+    if scale > 1:
+        r.q = (r.q.float() * 1e-30).to(BF)
+    o = api.spec_state_forward(*r.gpu("q", "k", "v", "g"), r.pool.cuda(), write=False, scale=scale)
+    ref.check_out(o["out"][0], [x if i == 0 else x.abs() for i, x in enumerate(r.want(0, r.pool[0], scale=scale)[0])], 64, n, BF, PIECES)
+
+
+def test_very_many_requests(api):
+    """More requests than are put in order of their lengths."""
+    B, n = 4100, 40
+    r = Rows(1, n, 1, 1, 16, 16, BF, 36)
+    q, k, v, g = (x.cuda().expand(B, *x.shape[1:]).contiguous() for x in (r.q, r.k, r.v, r.g))
+    counts = torch.arange(B) % (n + 1)
+    pool = torch.zeros(B, 1, 16, 16, device="cuda")
+    o = api.spec_state_forward(q, k, v, g, None, dst=pool, counts=counts.int().cuda())
+    outs, _ = r.want(0, r.zeros())
+    for b in (0, 1, 40, 41, 2000, B - 1):
+        m = int(counts[b])
+        ref.check_out(o["out"][b, :m], [x[:m] for x in outs], 16, n, BF, PIECES)
+        ref.check_state(pool[b], r.want(0, r.zeros(), list(range(m)))[1], 16, n, PIECES)
+        assert not o["out"][b, m:].any()
+    assert not o["status"].any()
 
 
 # ------------------------------------------------------------------ drafted rows
@@ -432,6 +462,55 @@ def test_a_round_of_each(api):
         every = [torch.cat(x) for x in rows[b]]
         _, last = ref.walk(*every, torch.zeros(Hk * G, D, D), ref.chain(len(every[0])), D ** -0.5)
         ref.check_state(pool[b], last, D, len(every[0]), PIECES)
+
+
+@pytest.mark.parametrize("keep", [12, 40])
+def test_with_the_verify_step(api, keep):
+    """The layer of a verify step between its tree's rerank and its verdict: sel_parents in, path_nodes and n_emit out."""
+    B, N, V, Hk, G, D = 3, 48, 512, 2, 2, 128
+    g = torch.Generator().manual_seed(keep)
+    trees = torch.tensor([random_tree(N, 60 + b, reach=6, depth=6) for b in range(B)], dtype=torch.int32)
+    conf = torch.rand(B, N, generator=g)
+    tok = torch.randint(0, V, (B, N), generator=g, dtype=torch.int32)
+    tree = api.spec_tree_rerank(trees.cuda(), conf.cuda(), keep, node_tok=tok.cuda())
+    d = Rows(B, keep, Hk, G, D, D, BF, 37)
+    pool = d.pool.cuda()
+    o = api.spec_state_attend(*d.gpu("q", "k", "v", "g"), pool, parents=tree["sel_parents"], n_query=tree["n_sel"])
+    assert o["status"].tolist() == [0] * B
+    for b in range(B):
+        m = int(tree["n_sel"][b])
+        ref.check_out(o["out"][b, :m], d.want(b, d.pool[b], list(range(m)), tree["sel_parents"][b, :m].tolist())[0], D, keep, BF, PIECES)
+    target = torch.randn(B, keep, V, generator=g)
+    for b in range(B):  # a target that wants some path of the tree
+        at = keep - 1 - b
+        while at > 0:
+            p = int(tree["sel_parents"][b, at])
+            target[b, p, int(tree["sel_tok"][b, at])] = 50.0
+            at = p
+    verdict = api.spec_verify_tree(target.cuda(), None, tree["sel_parents"], tree["sel_tok"], torch.zeros(B, keep + 1, device="cuda"), 0.0, 64)
+    assert verdict["status"].tolist() == [0] * B and bool((verdict["n_emit"] > 1).any())
+    c = api.spec_state_commit(*d.gpu("k", "v", "g"), pool, index=verdict["path_nodes"], counts=verdict["n_emit"])
+    assert c["status"].tolist() == [0] * B
+    for b in range(B):
+        ref.check_state(pool[b], d.want(b, d.pool[b], verdict["path_nodes"][b, :int(verdict["n_emit"][b])].tolist())[1], D, keep)
+
+
+def test_workspace(api):
+    """A call that needs a workspace is refused one that is too small or badly placed, and gives the same with its own."""
+    r = Rows(2, 200, 2, 1, 128, 128, BF, 38)
+    x = r.gpu("q", "k", "v", "g", "pool")
+    want = api.spec_state_forward(*x, write=False)["out"]
+    need = api.lib().spec_state_workspace_size(api.OP_STATE_FORWARD, api._state_struct(x[4], None, 2, tuple(x[4].shape[1:]), x[4].device, "s"), 2, 200)
+    assert need > 0
+    n0 = api.launch_count()
+    room = torch.empty(need + 512, dtype=torch.uint8, device="cuda")
+    for bad in (room[:need - 256], room[16:]):
+        with pytest.raises(api.SpecError, match="workspace"):
+            api.spec_state_forward(*x, write=False, ws=bad)
+    assert api.launch_count() == n0
+    guard = torch.full((need + 4096,), 77, dtype=torch.uint8, device="cuda")
+    assert torch.equal(api.spec_state_forward(*x, write=False, ws=guard[:need])["out"], want)
+    assert bool((guard[need:] == 77).all())
 
 
 @pytest.mark.parametrize("n", [1, 20, 300])
