@@ -65,8 +65,10 @@ __global__ void __launch_bounds__(256) state_join_kernel(const StateChunkPlan A)
   }
   float *p = A.local + static_cast<int64_t>(unit) * A.slots() * size + e;
   const float *f = A.total + static_cast<int64_t>(unit) * A.slots();
+  float4 ahead = *reinterpret_cast<const float4 *>(p);
   for (int g = 0; g + 1 < A.slots(); ++g, p += size) {
-    const float4 x = *reinterpret_cast<const float4 *>(p);
+    const float4 x = ahead;
+    if (g + 2 < A.slots()) ahead = *reinterpret_cast<const float4 *>(p + size);
     if (g % A.parts == 0) *reinterpret_cast<float4 *>(p) = s;
     s = make_float4(fmaf(s.x, f[g], x.x), fmaf(s.y, f[g], x.y), fmaf(s.z, f[g], x.z), fmaf(s.w, f[g], x.w));
   }

@@ -77,13 +77,13 @@ struct alignas(16) Decays {
 struct ChunkSmall {
   Decays d[kDecayRing];
   alignas(16) uint16_t stage[4][16][32];  // outputs on their way
-  uint32_t smax[2][4][128], amax[2][2][kChunk], kmax[2][kStateWarps];  // (by the chunk's number: the next one's may be written before these are read)
+  uint32_t smax[2][4][128], amax[2][2][kChunk];  // (by the chunk's number: the next one's may be written before these are read)
   // One barrier for each product, counted by chunk (four of them in turn, so that whoever waits for a chunk's phase is never a
   // lap behind): that P, O1, O2, dS are there, and so that their operands are free.
   uint64_t p_full[4], o1_full[4], o2_full[4], ds_full[4];
   uint64_t full[4], k_read[4];  // a chunk's rows loaded; its keys read by those who make K'
   uint64_t kt_full[2], p_empty, a_full, ds_empty, s_full, o_empty;
-  uint64_t dec_full[kDecayRing], dec_empty[kDecayRing], meet_s, meet_a, meet_k;
+  uint64_t dec_full[kDecayRing], dec_empty[kDecayRing], meet_s, meet_a;
   uint32_t tmem;
   int dead;
   int copies, products_p, products_o1, products_o2, products_s;  // how many were begun
@@ -326,13 +326,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      bar_init(&sm.full[i], 1), bar_init(&sm.k_read[i], kStateWarps);
+      bar_init(&sm.full[i], 1), bar_init(&sm.k_read[i], kStateWarps + (F16 ? 1 : 0));
       bar_init(&sm.p_full[i], 1), bar_init(&sm.o1_full[i], 1), bar_init(&sm.o2_full[i], 1), bar_init(&sm.ds_full[i], 1);
     }
     for (int i = 0; i < 2; ++i) bar_init(&sm.kt_full[i], kStateWarps);
     bar_init(&sm.p_empty, 4), bar_init(&sm.a_full, 4), bar_init(&sm.ds_empty, kStateWarps), bar_init(&sm.s_full, kStateWarps), bar_init(&sm.o_empty, 4);
     for (int i = 0; i < kDecayRing; ++i) bar_init(&sm.dec_full[i], 1), bar_init(&sm.dec_empty[i], OUT ? kStateWarps + 8 : kStateWarps);
-    bar_init(&sm.meet_s, kStateWarps), bar_init(&sm.meet_a, 4), bar_init(&sm.meet_k, kStateWarps);
+    bar_init(&sm.meet_s, kStateWarps), bar_init(&sm.meet_a, 4);
     bar_init_fence();
     sm.dead = 0;
     sm.copies = sm.products_p = sm.products_o1 = sm.products_o2 = sm.products_s = 0;
@@ -394,7 +394,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const Log2Parts q0 = Log2Sum{sums.total.whole - sums.g0.whole, sums.total.rest - sums.g0.rest}.parts(sums.spoilt);
       const Log2Parts q1 = Log2Sum{sums.total.whole - sums.g1.whole, sums.total.rest - sums.g1.rest}.parts(sums.spoilt);
       *reinterpret_cast<float2 *>(&d.left[2 * lane]) = make_float2(2 * lane < m ? q0.power() : 0.0f, 2 * lane + 1 < m ? q1.power() : 0.0f);
-      if (lane == 0) d.lam = sums.total.parts(sums.spoilt).power(), d.kfac = 1.0f;
+      if (lane == 0) d.lam = sums.total.parts(sums.spoilt).power();
+      if constexpr (F16) {  // K' divided by the power of two that its largest value asks for, as these factors go into it
+        if (!wait4(sm.full, c)) break;
+        const char *keys = smem + S::kK + c % S::kStagesK * S::kTileK;
+        __half2 most = __half2half2(__ushort_as_half(0));
+#pragma unroll 4
+        for (int e = lane; e < S::kTileK / 16; e += 32) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(keys + e * 16);
+          if ((e & 511) >> 3 < m) {
+            const __half2 *x = reinterpret_cast<const __half2 *>(&v);
+            most = __hmax2(most, __hmax2(__hmax2(__habs2(x[0]), __habs2(x[1])), __hmax2(__habs2(x[2]), __habs2(x[3]))));
+          }
+        }
+        warp_arrive(&sm.k_read[c & 3], lane);
+        const float2 two = __half22float2(most);
+        float l0 = 2 * lane < m ? q0.power() : 0.0f, l1 = 2 * lane + 1 < m ? q1.power() : 0.0f;
+        const float key = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(fmaxf(two.x, two.y))));
+        const float factor = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(fmaxf(l0, l1))));
+        float back;
+        const float fit = fit_half(__float_as_uint(key * factor), back);
+        *reinterpret_cast<float2 *>(&d.left[2 * lane]) = make_float2(l0 * fit, l1 * fit);
+        if (lane == 0) d.kfac = back;
+      }
       warp_arrive(&sm.dec_full[r], lane);
     }
     if (!OUT && lane == 0 && dv0 == 0) {  // (segments of many chunks: the sums in 64 bits, the whole part no further than fp32's exponents)
@@ -515,20 +537,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (d < P.key_dim) s[e] = pack2(from[static_cast<int64_t>(d) * P.value_dim + dv], from[static_cast<int64_t>(d + 1) * P.value_dim + dv]);
       }
     }
-    int met = 0;
+    // fp16: a thread's part of what the scale of chunk c's pieces is taken from
+    auto show_most = [&](int c) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int e = 0; e < OWN / 2; ++e) {
+        const float2 x = unpack2(s[e]);
+        most = max(most, max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu));
+      }
+      sm.smax[c & 1][four][at] = most;
+      warp_arrive(&sm.meet_s, lane);
+    };
     // the pieces of S that chunk c's product takes
     auto hand_on = [&](int c) -> bool {
       pair_t f = 0;
       if constexpr (F16) {
-        uint32_t most = 0;
-#pragma unroll
-        for (int e = 0; e < OWN / 2; ++e) {
-          const float2 x = unpack2(s[e]);
-          most = max(most, max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu));
-        }
-        sm.smax[c & 1][four][at] = most;
-        warp_arrive(&sm.meet_s, lane);
-        if (!warp_wait(&sm.meet_s, met++ & 1, dead)) return false;
+        if (!warp_wait(&sm.meet_s, c & 1, dead)) return false;
         float back;
         const auto &tops = sm.smax[c & 1];
         const float fit = fit_half(max(max(tops[0][at], tops[1][at]), max(tops[2][at], tops[3][at])), back);
@@ -558,31 +582,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (!wait4(sm.full, c)) return false;
       if (c < updates) {
         if (c >= 2 && !wait4(sm.ds_full, c - 2)) return false;
-        float left = sm.d[r].left[row];
+        const float left = sm.d[r].left[row];
         const bool past = row >= m;
         constexpr int kPieces = DK / 64;  // 16-byte pieces to a thread
         const int base = DK == 128 ? (part >> 2) * S::kHalf + row * 128 : row * 128, first = DK == 128 ? (part & 3) * 2 : part;
         const char *from = smem + S::kK + sk * S::kTileK + base;
         char *to = smem + S::kKt + (c & 1) * 2 * S::kTileK + base;
-        if constexpr (F16) {
-          uint32_t most = 0;
-#pragma unroll 2
-          for (int e = 0; e < kPieces; ++e) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(from + (((first + e) ^ (row & 7)) << 4));
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) most = max(most, max(w[y] & 0x7fffu, w[y] >> 16 & 0x7fffu));
-          }
-          const uint32_t mine = past ? 0u : __float_as_uint(fabsf(__half2float(__ushort_as_half(static_cast<uint16_t>(most))) * left)) & 0x7fffffffu;
-          const uint32_t warps = __reduce_max_sync(~0u, mine);
-          if (lane == 0) sm.kmax[c & 1][warp - 12] = warps;
-          warp_arrive(&sm.meet_k, lane);
-          if (!warp_wait(&sm.meet_k, c & 1, dead)) return false;
-          const uint32_t top = __reduce_max_sync(~0u, sm.kmax[c & 1][lane & (kStateWarps - 1)]);
-          float back;
-          left *= fit_half(top, back);
-          if (own == 0) sm.d[r].kfac = back;
-        }
         const pair_t f = pack2(left, left);
 #pragma unroll 2
         for (int e = 0; e < kPieces; ++e) {
@@ -614,34 +619,39 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       return true;
     };
     bool going = true;
+    if (OUT && F16 && chunks > 0) show_most(0);
 #pragma unroll 1
     for (int c = -2; c < chunks; ++c) {
-      const int r = c % kDecayRing;
+      const int r = c & (kDecayRing - 1);
       if (OUT && c >= 0 && !(going = hand_on(c))) break;
-      if (c + 2 < chunks && !(going = keys(c + 2))) break;
-      if (c < 0) continue;
-      if (!(going = warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead))) break;
-      if (c < updates) {
-        if (!(going = wait4(sm.ds_full, c))) break;
-        tc_fence_after();
-        const float lam = sm.d[r].lam, kf = F16 ? sm.d[r].kfac : 1.0f;
-        const pair_t l2 = pack2(lam, lam), k2 = pack2(kf, kf);
+      // K' before the update (a document 390 us, behind it 413); behind it in fp16, where the maxima have that time to meet
+      if (!F16 && c + 2 < chunks && !(going = keys(c + 2))) break;
+      if (c >= 0) {
+        if (!(going = warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead))) break;
+        if (c < updates) {
+          if (!(going = wait4(sm.ds_full, c))) break;
+          tc_fence_after();
+          const float lam = sm.d[r].lam, kf = F16 ? sm.d[r].kfac : 1.0f;
+          const pair_t l2 = pack2(lam, lam), k2 = pack2(kf, kf);
 #pragma unroll
-        for (int k = 0; k < OWN / 16; ++k) {
-          float x[16];
-          tmem_ld16(tmem + lanes + kDS + four * OWN + k * 16, x);
-          tc_wait_ld();
+          for (int k = 0; k < OWN / 16; ++k) {
+            float x[16];
+            tmem_ld16(tmem + lanes + kDS + four * OWN + k * 16, x);
+            tc_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            pair_t &y = s[8 * k + e];
-            if constexpr (F16) y = fma2(pack2(x[2 * e], x[2 * e + 1]), k2, mul2(y, l2));
-            else y = fma2(y, l2, pack2(x[2 * e], x[2 * e + 1]));
+            for (int e = 0; e < 8; ++e) {
+              pair_t &y = s[8 * k + e];
+              if constexpr (F16) y = fma2(pack2(x[2 * e], x[2 * e + 1]), k2, mul2(y, l2));
+              else y = fma2(y, l2, pack2(x[2 * e], x[2 * e + 1]));
+            }
           }
+          tc_fence_before();
+          warp_arrive(&sm.ds_empty, lane);
         }
-        tc_fence_before();
-        warp_arrive(&sm.ds_empty, lane);
+        warp_arrive(&sm.dec_empty[r], lane);
+        if (OUT && F16 && c + 1 < chunks) show_most(c + 1);
       }
-      warp_arrive(&sm.dec_empty[r], lane);
+      if (F16 && c + 2 < chunks && !(going = keys(c + 2))) break;
     }
     float *to = nullptr;
     if (!OUT) {
