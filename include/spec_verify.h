@@ -579,6 +579,8 @@ size_t spec_cache_workspace_size(int op, const spec_cache *cache, int B, int N, 
  *   decay       fp32 natural logarithms g of the factors, strides (request,
  *               token, head) as they come, 0 for what is shared.  -inf is a
  *               factor of 0, which forgets every finite thing before the token.
+ *               Values beyond +-120 may count as +-120 (e^120 = 1e52: in fp32
+ *               such a factor is 0 or infinite).
  * status[b] (out int32 [B] or NULL): SPEC_STATUS_BAD_LENGTH (a count out of
  * range), SPEC_STATUS_BAD_SLOT (a slot outside the pool), SPEC_STATUS_BAD_INDEX
  * or SPEC_STATUS_BAD_TREE.  Such a request's state is not written and its rows

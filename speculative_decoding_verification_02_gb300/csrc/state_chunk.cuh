@@ -21,23 +21,35 @@ namespace {
 //   P  = Q K^T              [i x j]
 //   A  = P e^{G_i - G_j}, 0 where row i does not follow row j, as two pieces in shared memory
 //   O2 = V^T A^T            [dv x i]   V as it came
-//   dS = V^T K'             [dv x dk]  K' = e^{G_last - G_j} k_j as two pieces in shared memory
+//   dS = V^T K'             [dv x dk]  K' = e^{G_last - G_j} k_j as two or three pieces in shared memory
 //   out_i = scale (e^{G_i} O1_i + O2_i),   S <- e^{G_last} S + dS
 // S itself stays in fp32 registers; what a product takes of it, of A and of
-// K' is the sum of two pieces of the rows' type, off by 2^-18 of a value at
-// most in bf16 and 2^-22 in fp16, whose pieces are scaled by powers of two (a lane
-// of S, a row of A, a chunk's K') to stay within its range.
+// K' is the sum of pieces of the rows' type.  The first leaves out half of its
+// step, the second half of its own: 2^-17 of a value at most in bf16, 2^-23 in
+// fp16, whose pieces are scaled by powers of two (a lane of S, a row of A, a
+// chunk's K') to stay within its range.  Outputs, which are rounded to the
+// rows' type, take two; the state, which stays in fp32, a third of K' in bf16,
+// the smallest first: after 500 chunks it is 3.6e-7 off on the whole where two
+// left 2.4e-6 (32-bit sums: 1.8e-7).
 //
-// e^{G_i - G_j} is taken from differences, of running sums held in 64 bits and
-// handed on as a multiple of 1/8 and a rest, so that a difference of large sums
-// is as exact as one of small ones.
+// e^{G_i - G_j} is taken from differences of running sums in fixed point,
+// handed on as whole units of log 2 and a rest, so that a difference of large
+// sums is as exact as one of small ones.
 //
 // Warps (their number modulo 4 is the quarter of the lanes that they can reach,
 // and their scheduler): 2 loads, 3 decays, 10 issues O1 and O2, 11 issues P and dS;
 // 4, 5, 8, 9 make A; 0, 1, 6, 7 write the outputs; 12 to 27 hold S and make K',
-// two chunks ahead.  The code of the roles is kept short, one site to each and
+// kAhead chunks ahead.  The code of the roles is kept short, one site to each and
 // loops rolled where registers allow: unrolled further, warps waited for their
 // instructions (a chunk 7,700 cycles, not 5,300).
+//
+// One request of 32,003 tokens, 48 heads of 128 x 128 (three to a key head), in
+// a graph of calls: 575 us, of which this kernel takes 398 on 144 SMs (2.4 us a
+// chunk, some 3,900 cycles) and the launch before it 176; the bytes are 156 us
+// at the copy rate.  A chunk's products take 2,200 cycles of the tensor pipe
+// when nothing waits; 9,300 instructions of the warps around them, a quarter of
+// which are S's pieces, use 60% of the issue slots.
+// 256 prompts' heads of up to 8,001 tokens: 490 us, 3.1 TB/s.
 //
 // A long prompt of few heads is cut into segments: a first launch (OUT false)
 // computes what each but the last adds to a state of zeros, state_join_kernel
@@ -48,18 +60,22 @@ constexpr int kChunkThreads = 896;
 constexpr int kStateWarps = 16;
 constexpr int kDecayRing = 4;
 
-template <int DK, bool OUT>
+template <int DT, int DK, bool OUT>
 struct ChunkShape {
+  static constexpr int kKeyPieces = DT == SPEC_DTYPE_BF16 ? 3 : 2;  // of K'
   static constexpr int kHalf = kChunk * 128;  // bytes of 64 columns of a tile
   static constexpr int kTileK = DK / 64 * kHalf, kTileV = 2 * kHalf;
-  static constexpr int kStagesK = OUT ? (DK == 128 ? 2 : 4) : 4;
-  static constexpr int kStagesV = OUT ? (DK == 128 ? 3 : 4) : 4;
+  // Chunks that K' is made ahead of its use, and buffers of it: two of three pieces would leave room for two stages of values (a
+  // document 761 us, one with three stages 595; in the launch before the main one, 196 of these with one buffer, 179 with two)
+  static constexpr int kAhead = DK == 128 && OUT && kKeyPieces == 3 ? 1 : 2;
+  static constexpr int kStagesK = DK == 64 ? 4 : OUT ? 2 : 3;
+  static constexpr int kStagesV = DK == 128 && OUT ? 3 : 4;
   static constexpr int kStagesQ = OUT ? kStagesV : 0;
   static constexpr int kK = 0;
   static constexpr int kQ = kK + kStagesK * kTileK;
   static constexpr int kV = kQ + kStagesQ * kTileK;  // (P's product reads 64 rows past a half of Q: of Q, or of V)
   static constexpr int kKt = kV + kStagesV * kTileV;
-  static constexpr int kA = kKt + 2 * 2 * kTileK;
+  static constexpr int kA = kKt + kAhead * kKeyPieces * kTileK;
   static constexpr int kSmall = kA + (OUT ? 2 * kHalf : 0);
   static constexpr int kBytes = kSmall + 17920 + 1024;  // (1024: alignment of the base)
 };
@@ -88,7 +104,13 @@ struct ChunkSmall {
   int dead;
   int copies, products_p, products_o1, products_o2, products_s;  // how many were begun
 };
-static_assert(sizeof(ChunkSmall) <= 17920 && ChunkShape<128, true>::kBytes <= 232448 && ChunkShape<64, true>::kBytes <= 232448);
+static_assert(sizeof(ChunkSmall) <= 17920);
+template <int DT>
+constexpr bool chunks_fit() {
+  return ChunkShape<DT, 128, true>::kBytes <= 232448 && ChunkShape<DT, 128, false>::kBytes <= 232448 && ChunkShape<DT, 64, true>::kBytes <= 232448 &&
+         ChunkShape<DT, 64, false>::kBytes <= 232448;
+}
+static_assert(chunks_fit<SPEC_DTYPE_BF16>() && chunks_fit<SPEC_DTYPE_F16>());
 
 // Arrival of a warp whose lanes have all done what the barrier stands for.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
@@ -125,6 +147,14 @@ __device__ __forceinline__ void split2(pair_t x, uint32_t &hi, uint32_t &lo) {
   hi = narrow2<DT>(unpack2(x));
   const float2 h = widen2<DT>(hi);
   lo = narrow2<DT>(unpack2(fma2(pack2(h.x, h.y), pack2(-1.0f, -1.0f), x)));
+}
+
+// And a third time.
+template <int DT>
+__device__ __forceinline__ void split3(pair_t x, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+  hi = narrow2<DT>(unpack2(x));
+  const float2 h = widen2<DT>(hi);
+  split2<DT>(fma2(pack2(h.x, h.y), pack2(-1.0f, -1.0f), x), mid, lo);
 }
 
 // The power of two that brings a largest magnitude (as bits) to [2^14, 2^15), and its inverse; 1 for zero, infinities and NaN.
@@ -289,7 +319,7 @@ template <int DT, int DK, bool OUT>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     state_chunk_kernel(const StateChunkPlan A, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                        const __grid_constant__ CUtensorMap v_map) {
-  using S = ChunkShape<DK, OUT>;
+  using S = ChunkShape<DT, DK, OUT>;
   constexpr bool F16 = DT == SPEC_DTYPE_F16;
   constexpr uint32_t kDS = 0, kSHi = 128, kSLo = 192, kO1 = 256, kO2 = 384, kP = 448;  // tensor memory; O1 twice
   extern __shared__ char raw[];
@@ -480,15 +510,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     for (int c = -1; c < chunks; ++c) {  // dS of a chunk, P of the next
       if (c >= 0 && c < updates) {
         if (!OUT && !wait4(sm.full, c)) break;
-        if (!warp_wait(&sm.kt_full[c & 1], c >> 1 & 1, dead)) break;
+        if (!warp_wait(&sm.kt_full[c % S::kAhead], c / S::kAhead & 1, dead)) break;
         if (c > 0 && !warp_wait(&sm.ds_empty, (c - 1) & 1, dead)) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll 1
-          for (int piece = 0; piece < 2; ++piece) {
-            const uint64_t v = v_desc + ((c % S::kStagesV * S::kTileV) >> 4), kt = kt_desc + ((((c & 1) * 2 + piece) * S::kTileK) >> 4);
+          for (int piece = S::kKeyPieces - 1; piece >= 0; --piece) {  // (the smallest first: the accumulator cuts off)
+            const uint64_t v = v_desc + ((c % S::kStagesV * S::kTileV) >> 4);
+            const uint64_t kt = kt_desc + (((c % S::kAhead * S::kKeyPieces + piece) * S::kTileK) >> 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16_ss(tmem + kDS, v + 128 * k, kt + 128 * k, kIdS, piece + k > 0);
+            for (int k = 0; k < 4; ++k) mma_f16_ss(tmem + kDS, v + 128 * k, kt + 128 * k, kIdS, piece + 1 < S::kKeyPieces || k > 0);
           }
           tc_commit(&sm.ds_full[c & 3]);
         }
@@ -581,31 +612,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (!warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead)) return false;
       if (!wait4(sm.full, c)) return false;
       if (c < updates) {
-        if (c >= 2 && !wait4(sm.ds_full, c - 2)) return false;
+        if (c >= S::kAhead && !wait4(sm.ds_full, c - S::kAhead)) return false;
         const float left = sm.d[r].left[row];
         const bool past = row >= m;
         constexpr int kPieces = DK / 64;  // 16-byte pieces to a thread
         const int base = DK == 128 ? (part >> 2) * S::kHalf + row * 128 : row * 128, first = DK == 128 ? (part & 3) * 2 : part;
         const char *from = smem + S::kK + sk * S::kTileK + base;
-        char *to = smem + S::kKt + (c & 1) * 2 * S::kTileK + base;
+        char *to = smem + S::kKt + c % S::kAhead * S::kKeyPieces * S::kTileK + base;
         const pair_t f = pack2(left, left);
 #pragma unroll 2
         for (int e = 0; e < kPieces; ++e) {
           const int o = ((first + e) ^ (row & 7)) << 4;
           const uint4 x = *reinterpret_cast<const uint4 *>(from + o);
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          uint32_t hi[4], lo[4];
+          uint32_t pieces[3][4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const float2 k = widen2<DT>(w[y]);
-            split2<DT>(mul2(pack2(k.x, k.y), f), hi[y], lo[y]);
+            const pair_t z = mul2(pack2(k.x, k.y), f);
+            if constexpr (S::kKeyPieces == 3) split3<DT>(z, pieces[0][y], pieces[1][y], pieces[2][y]);
+            else split2<DT>(z, pieces[0][y], pieces[1][y]);
           }
           if (past) [[unlikely]] {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) hi[y] = lo[y] = 0;
+            for (int y = 0; y < 4; ++y) pieces[0][y] = pieces[1][y] = pieces[2][y] = 0;
           }
-          *reinterpret_cast<uint4 *>(to + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4 *>(to + S::kTileK + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+          for (int y = 0; y < S::kKeyPieces; ++y)
+            *reinterpret_cast<uint4 *>(to + y * S::kTileK + o) = make_uint4(pieces[y][0], pieces[y][1], pieces[y][2], pieces[y][3]);
         }
         if (m < kChunk) {
           const int sv = c % S::kStagesV;
@@ -613,7 +647,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             *reinterpret_cast<uint4 *>(smem + S::kV + sv * S::kTileV + (e & 1) * S::kHalf + (m + (e >> 4)) * 128 + (e >> 1 & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_async_shared();
-        warp_arrive(&sm.kt_full[c & 1], lane);
+        warp_arrive(&sm.kt_full[c % S::kAhead], lane);
       }
       warp_arrive(&sm.k_read[c & 3], lane);
       return true;
@@ -621,11 +655,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     bool going = true;
     if (OUT && F16 && chunks > 0) show_most(0);
 #pragma unroll 1
-    for (int c = -2; c < chunks; ++c) {
+    for (int c = -S::kAhead; c < chunks; ++c) {
       const int r = c & (kDecayRing - 1);
       if (OUT && c >= 0 && !(going = hand_on(c))) break;
-      // K' before the update (a document 390 us, behind it 413); behind it in fp16, where the maxima have that time to meet
-      if (!F16 && c + 2 < chunks && !(going = keys(c + 2))) break;
+      // K' before the update where it is two chunks ahead; fp16's maxima have its time to meet
+      constexpr bool kKeysFirst = S::kAhead == 2 && !F16;
+      if (kKeysFirst && c + S::kAhead < chunks && !(going = keys(c + S::kAhead))) break;
       if (c >= 0) {
         if (!(going = warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead))) break;
         if (c < updates) {
@@ -651,7 +686,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         warp_arrive(&sm.dec_empty[r], lane);
         if (OUT && F16 && c + 1 < chunks) show_most(c + 1);
       }
-      if (F16 && c + 2 < chunks && !(going = keys(c + 2))) break;
+      if (!kKeysFirst && c + S::kAhead < chunks && !(going = keys(c + S::kAhead))) break;
     }
     float *to = nullptr;
     if (!OUT) {
@@ -808,7 +843,7 @@ std::atomic<uint64_t> chunk_smem{0};
 
 template <int DT, int DK, bool OUT>
 cudaError_t launch_chunks(const StateChunkPlan &A, const CUtensorMap *maps, cudaStream_t st) {
-  using S = ChunkShape<DK, OUT>;
+  using S = ChunkShape<DT, DK, OUT>;
   auto kern = state_chunk_kernel<DT, DK, OUT>;
   const cudaError_t e =
       once_per_device([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes); }, chunk_smem<DT, DK, OUT>);

@@ -7,9 +7,10 @@ import state_oracle as ref
 pytestmark = pytest.mark.gpu
 
 BF, HF = torch.bfloat16, torch.float16
-# What the tensor-core kernels' operands leave out of S, of the pairs' weights and of the keys: two pieces of 8 bits of each, cut
-# to half a step of the second, 2^-18 of a value and less; three such factors can meet in an output, and each of them may be
-# made of the others' results, so four times that.
+# What the tensor-core kernels' operands leave out of S, of the pairs' weights and of the keys, each the sum of two pieces of the
+# rows' type.  In bf16 the first leaves out at most half of its step, 2^(e - 8) of a value from 2^e on; that lies in the binade
+# below, so the second, of 8 bits too, leaves out at most half of 2^(e - 9 - 7): 2^-17 of the value (fp16: 2^-23).  An output
+# passes S's pieces, and S is made of keys' pieces: twice that.
 PIECES = 2.0 ** -16
 
 
@@ -84,6 +85,41 @@ def test_forward_in_place(api, n):
         ref.check_state(pool[s], r.want(b, r.pool[s])[1], 128, n, PIECES)
     for s in (0, 2, 3, 4):
         assert torch.equal(pool[s].cpu(), r.pool[s])
+
+
+@pytest.mark.parametrize("Dk,Dv,Hk,G,dtype", [(128, 128, 1, 2, BF), (64, 64, 1, 1, HF), (128, 64, 2, 1, HF), (112, 240, 1, 1, BF)])
+@pytest.mark.parametrize("n,counts", [(1000, None), (1300, [1300, 70, 0]), (2111, [520, 2111, 1])])
+def test_forward_in_segments(api, Dk, Dv, Hk, G, dtype, n, counts):
+    """Long prompts of few heads, which several CTAs share: behind a state and from none, in place and not."""
+    r = Rows(3, n, Hk, G, Dk, Dv, dtype, 600 + n, slots=4, remember=7.0)
+    slots = [2, -1, 0]
+    pool, dst = r.pool.cuda(), torch.full((3, r.H, Dk, Dv), 7.0, device="cuda")
+    args, c = r.gpu("q", "k", "v", "g"), None if counts is None else i32(counts)
+    o = api.spec_state_forward(*args, pool, slots=i32(slots), dst=dst, counts=c)
+    assert o["status"].tolist() == [0, 0, 0] and torch.equal(pool.cpu(), r.pool)
+    for b in range(3):
+        m = n if counts is None else counts[b]
+        outs, last = r.want(b, r.pool[slots[b]] if slots[b] >= 0 else r.zeros(), list(range(m)))
+        ref.check_out(o["out"][b, :m], outs, Dk, n, dtype, PIECES)
+        assert not o["out"][b, m:].any()
+        ref.check_state(dst[b], last, Dk, n, PIECES)
+    again = api.spec_state_forward(*args, pool, slots=i32([2, 1, 0]), counts=c)
+    assert torch.equal(again["out"][0], o["out"][0]) and torch.equal(again["out"][2], o["out"][2]) and torch.equal(pool[[2, 0]], dst[[0, 2]])
+    pool.copy_(r.pool)
+    bad = api.spec_state_forward(*args, pool, slots=i32([1, 9, 3]), counts=i32([n, n, n + 1]))
+    assert bad["status"].tolist() == [0, api.STATUS_BAD_SLOT, api.STATUS_BAD_LENGTH] and not bad["out"][1:].any()
+    assert torch.equal(pool[3].cpu(), r.pool[3])
+
+
+def test_forward_in_parts_of_segments(api):
+    """As many heads as leave the launch before the main one several CTAs to a segment."""
+    n = 3001
+    r = Rows(1, n, 16, 3, 32, 16, BF, 40, remember=7.0)
+    pool = r.pool.cuda()
+    o = api.spec_state_forward(*r.gpu("q", "k", "v", "g"), pool)
+    outs, last = r.want(0, r.pool[0])
+    ref.check_out(o["out"][0], outs, 32, n, BF, PIECES)
+    ref.check_state(pool[0], last, 32, n, PIECES)
 
 
 @pytest.mark.parametrize("n", [3, 90])
@@ -513,7 +549,7 @@ def test_workspace(api):
     assert bool((guard[need:] == 77).all())
 
 
-@pytest.mark.parametrize("n", [1, 20, 300])
+@pytest.mark.parametrize("n", [1, 20, 300, 900])
 def test_captured_and_replayed(api, n):
     """Two captured calls of different sizes on one stream, replayed in turn over new inputs, against calls outside a graph."""
     a, b = Rows(2, n, 2, 1, 128, 128, BF, 30), Rows(1, n + 130, 2, 1, 128, 128, BF, 31)
