@@ -44,12 +44,12 @@ namespace {
 // instructions (a chunk 7,700 cycles, not 5,300).
 //
 // One request of 32,003 tokens, 48 heads of 128 x 128 (three to a key head), in
-// a graph of calls: 575 us, of which this kernel takes 398 on 144 SMs (2.4 us a
+// a graph of calls: 574 us, of which this kernel takes 398 on 144 SMs (2.4 us a
 // chunk, some 3,900 cycles) and the launch before it 176; the bytes are 156 us
 // at the copy rate.  A chunk's products take 2,200 cycles of the tensor pipe
 // when nothing waits; 9,300 instructions of the warps around them, a quarter of
 // which are S's pieces, use 60% of the issue slots.
-// 256 prompts' heads of up to 8,001 tokens: 490 us, 3.1 TB/s.
+// 256 prompts' heads of up to 8,001 tokens: 488 us, 3.2 TB/s.
 //
 // A long prompt of few heads is cut into segments: a first launch (OUT false)
 // computes what each but the last adds to a state of zeros, state_join_kernel
@@ -862,7 +862,7 @@ cudaError_t launch_chunks(const StateChunkPlan &A, const CUtensorMap *maps, cuda
 // (request, head, 128 columns) goes through the steps above once, P's columns
 // of tensor memory becoming O2's, so that two CTAs share an SM and one loads
 // its state while the other computes.  16 trees of 60 nodes, 48 heads: 64 us
-// as a chunk of the kernel above (one CTA to an SM), 31 us so.
+// as a chunk of the kernel above (one CTA to an SM), 32 us so.
 constexpr int kShortThreads = 256;
 
 template <int DK>
