@@ -21,9 +21,9 @@
 //
 // Bound by the state's bytes: 64 requests' single tokens, 48 heads of 128 x 128,
 // 70 us in a graph of calls (5.7 TB/s; copying the states alone 60 us, as fast
-// as a plain copy), their commits of up to 9 rows 76 us; 9 rows read only 69 us
+// as a plain copy), their commits of up to 9 rows 76 us; as many read only 68 us
 // (3.1 TB/s): the rows' arithmetic, some 60 instructions a row and warp, is not
-// hidden.  One request's token 4.7 us, 5 rows 5.6 us: a chain of loads.  CTAs
+// hidden.  One request's token 4.7 us, 5 rows 5.7 us: a chain of loads.  CTAs
 // that stay and fetch the next unit's state ahead were slower (82, 90, 119 us):
 // fewer warps.
 #include <algorithm>
@@ -238,28 +238,26 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
         if (lane == m - 1) total = all.parts(nan).power();
       }
       if constexpr (MODE == kChain) {
-        // ---- the pairs' weights: a row to a warp, a token before it to two lanes, each of half of key_dim
+        // ---- the pairs' weights: a row to a warp, a token before it to 2, 4 or 8 lanes, each of its share of key_dim's pieces
+        const int shift = m <= 4 ? 2 : m <= 8 ? 3 : 4, j = lane & ((1 << shift) - 1);
         for (int i = warp; i < m; i += warps) {
-          const int j = lane & 15, half = lane >> 4;
-          float s0 = 0.0f, s1 = 0.0f;
+          float s = 0.0f;
           if (j <= i) {
-            const char *q = &qs[i][half * RPL * 8], *k = &ks[j][half * RPL * 8];
-#pragma unroll 4
-            for (int e = 0; e < RPL / 2; ++e) {
+#pragma unroll 2
+            for (int e = lane >> shift; e < RPL; e += 32 >> shift) {
               pair_t a[4], d[4];
-              widen8<DT>(*reinterpret_cast<const uint4 *>(q + e * 16), a);
-              widen8<DT>(*reinterpret_cast<const uint4 *>(k + e * 16), d);
-              const float2 u = unpack2(fma2(a[0], d[0], mul2(a[1], d[1]))), w = unpack2(fma2(a[2], d[2], mul2(a[3], d[3])));
-              s0 += u.x + u.y, s1 += w.x + w.y;
+              widen8<DT>(*reinterpret_cast<const uint4 *>(&qs[i][e * 16]), a);
+              widen8<DT>(*reinterpret_cast<const uint4 *>(&ks[j][e * 16]), d);
+              const float2 u = unpack2(fma2(a[0], d[0], fma2(a[1], d[1], fma2(a[2], d[2], mul2(a[3], d[3])))));
+              s += u.x + u.y;
             }
           }
-          float s = s0 + s1;
-          s += __shfl_xor_sync(~0u, s, 16);
+          for (int o = 1 << shift; o < 32; o <<= 1) s += __shfl_xor_sync(~0u, s, o);
           const int w = __shfl_sync(~0u, upto.whole, i), r = __shfl_sync(~0u, upto.rest, i);
           const int wj = __shfl_sync(~0u, upto.whole, j), rj = __shfl_sync(~0u, upto.rest, j);
           // (tokens j + 1 to i)
           const bool lost = nan & ((2u << i) - 1) & ~((2u << j) - 1);
-          if (lane < 16) pair[i][j] = j <= i ? s * Log2Sum{w - wj, r - rj}.parts(lost).power() * P.scale : 0.0f;
+          if (lane >> shift == 0) pair[i][j] = j <= i ? s * Log2Sum{w - wj, r - rj}.parts(lost).power() * P.scale : 0.0f;
         }
       }
       __syncthreads();
