@@ -652,3 +652,30 @@ def test_binding_refuses(api):
     with pytest.raises(api.SpecError):
         api.spec_state_forward(q, k, v, g, pool, scale=float("nan"))
     assert api.launch_count() == n0
+
+
+def test_two_host_threads(api):
+    """Two host threads on one stream, whose calls share its workspace, and on streams of their own."""
+    import threading
+    sets = [Rows(2, n, 2, 1, 128, 128, BF, 70 + n).gpu("q", "k", "v", "g", "pool") for n in (130, 700)]
+    want = [api.spec_state_forward(*x, write=False)["out"] for x in sets]
+    torch.cuda.synchronize()
+    for streams in ([torch.cuda.current_stream()] * 2, [torch.cuda.Stream(), torch.cuda.Stream()]):
+        got, failed = [[], []], []
+
+        def work(i):
+            try:
+                for _ in range(20):
+                    got[i].append(api.spec_state_forward(*sets[i], write=False, stream=streams[i])["out"])
+            except Exception as e:  # noqa: BLE001 (told to the test's own thread)
+                failed.append(e)
+
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        assert not failed
+        for i in range(2):
+            assert len(got[i]) == 20 and all(torch.equal(x, want[i]) for x in got[i])
