@@ -17,20 +17,20 @@ namespace {
 // tensor memory) and a run of chunks of 64 tokens.  With G the running sum of
 // the decays within a chunk, everything is held transposed, a lane to a column
 // of value_dim:
-//   O1 = S^T Q^T            [dv x i]   S as two pieces of 16 bits in tensor memory, Q as it came
+//   O1 = S^T Q^T            [dv x i]   S in pieces of 16 bits in tensor memory, Q as it came
 //   P  = Q K^T              [i x j]
-//   A  = P e^{G_i - G_j}, 0 where row i does not follow row j, as two pieces in shared memory
+//   A  = P e^{G_i - G_j}, 0 where row i does not follow row j, in pieces in shared memory
 //   O2 = V^T A^T            [dv x i]   V as it came
-//   dS = V^T K'             [dv x dk]  K' = e^{G_last - G_j} k_j as two or three pieces in shared memory
+//   dS = V^T K'             [dv x dk]  K' = e^{G_last - G_j} k_j in pieces in shared memory
 //   out_i = scale (e^{G_i} O1_i + O2_i),   S <- e^{G_last} S + dS
 // S itself stays in fp32 registers; what a product takes of it, of A and of
-// K' is the sum of pieces of the rows' type.  The first leaves out half of its
-// step, the second half of its own: 2^-17 of a value at most in bf16, 2^-23 in
-// fp16, whose pieces are scaled by powers of two (a lane of S, a row of A, a
-// chunk's K') to stay within its range.  Outputs, which are rounded to the
-// rows' type, take two; the state, which stays in fp32, a third of K' in bf16,
-// the smallest first: after 500 chunks it is 3.6e-7 off on the whole where two
-// left 2.4e-6 (32-bit sums: 1.8e-7).
+// K' is the sum of pieces of the rows' type, each what those before it left
+// out: three in bf16, which hold all 24 digits, two in fp16, which leave out
+// 2^-23 of a value at most, scaled by powers of two (a lane of S, a row of A,
+// a chunk's K') to stay within its range.  The smallest pieces are added
+// first, since the accumulator cuts off: after 500 chunks a state is 3.6e-7
+// off on the whole (two pieces of K' in bf16: 2.4e-6; 32-bit sums: 1.8e-7),
+// and bf16 outputs are as near to the plain form's as those of 32-bit sums.
 //
 // e^{G_i - G_j} is taken from differences of running sums in fixed point,
 // handed on as whole units of log 2 and a rest, so that a difference of large
@@ -38,8 +38,9 @@ namespace {
 //
 // Warps (their number modulo 4 is the quarter of the lanes that they can reach,
 // and their scheduler): 2 loads, 3 decays, 10 issues O1 and O2, 11 issues P and dS;
-// 4, 5, 8, 9 make A; 0, 1, 6, 7 write the outputs; 12 to 27 hold S and make K',
-// kAhead chunks ahead.  The code of the roles is kept short, one site to each and
+// 4, 5, 8, 9 make A; 0, 1, 6, 7 write the outputs; 12 to 27 hold S, and make K'
+// kAhead chunks ahead: with outputs, those of the two schedulers that have no
+// warps with A (a document 671 us with all of them, 623 so).  The code of the roles is kept short, one site to each and
 // loops rolled where registers allow: unrolled further, warps waited for their
 // instructions (a chunk 7,700 cycles, not 5,300).
 //
@@ -58,11 +59,17 @@ namespace {
 constexpr int kChunk = 64;
 constexpr int kChunkThreads = 896;
 constexpr int kStateWarps = 16;
+template <bool OUT>
+constexpr int kKeyWarps = OUT ? 8 : 16;  // those of them that make K'
 constexpr int kDecayRing = 4;
+
+// Pieces of a value that a product takes.
+template <int DT>
+constexpr int kPieces = DT == SPEC_DTYPE_BF16 ? 3 : 2;
 
 template <int DT, int DK, bool OUT>
 struct ChunkShape {
-  static constexpr int kKeyPieces = DT == SPEC_DTYPE_BF16 ? 3 : 2;  // of K'
+  static constexpr int kKeyPieces = kPieces<DT>;  // of K'
   static constexpr int kHalf = kChunk * 128;  // bytes of 64 columns of a tile
   static constexpr int kTileK = DK / 64 * kHalf, kTileV = 2 * kHalf;
   // Chunks that K' is made ahead of its use, and buffers of it: two of three pieces would leave room for two stages of values (a
@@ -76,8 +83,12 @@ struct ChunkShape {
   static constexpr int kV = kQ + kStagesQ * kTileK;  // (P's product reads 64 rows past a half of Q: of Q, or of V)
   static constexpr int kKt = kV + kStagesV * kTileV;
   static constexpr int kA = kKt + kAhead * kKeyPieces * kTileK;
-  static constexpr int kSmall = kA + (OUT ? 2 * kHalf : 0);
+  static constexpr int kSmall = kA + (OUT ? kPieces<DT> * kHalf : 0);
   static constexpr int kBytes = kSmall + 17920 + 1024;  // (1024: alignment of the base)
+  // Tensor memory: dS, P in its place while K' is made; S's pieces; O1, two in turn; O2.  (One O1 and a place for P alone: a document
+  // 701 us, since the outputs then stand between two chunks' O1.)
+  static constexpr uint32_t kDS = 0, kP = 0, kS = 128, kPieceS = DK / 2, kO1 = 320, kO2 = 448;
+  static_assert(kS + kPieces<DT> * kPieceS <= kO1);
 };
 
 struct alignas(16) Decays {
@@ -141,20 +152,24 @@ __device__ __forceinline__ void tensor_load_4d(void *dst, const CUtensorMap *map
       : "memory");
 }
 
-// Two values rounded to the rows' type, and the same rounding of what that left out.
+// What a value of the rows' type leaves out of an fp32 one: an instruction that takes both.
 template <int DT>
-__device__ __forceinline__ void split2(pair_t x, uint32_t &hi, uint32_t &lo) {
-  hi = narrow2<DT>(unpack2(x));
-  const float2 h = widen2<DT>(hi);
-  lo = narrow2<DT>(unpack2(fma2(pack2(h.x, h.y), pack2(-1.0f, -1.0f), x)));
+__device__ __forceinline__ float left_out(uint16_t piece, float x) {
+  float r;
+  if constexpr (DT == SPEC_DTYPE_BF16) asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(r) : "h"(piece), "h"(static_cast<uint16_t>(0xbf80)), "f"(x));
+  else asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(r) : "h"(piece), "h"(static_cast<uint16_t>(0xbc00)), "f"(x));
+  return r;
 }
 
-// And a third time.
+// Two values in pieces of the rows' type: each rounds what the ones before it left out.
 template <int DT>
-__device__ __forceinline__ void split3(pair_t x, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-  hi = narrow2<DT>(unpack2(x));
-  const float2 h = widen2<DT>(hi);
-  split2<DT>(fma2(pack2(h.x, h.y), pack2(-1.0f, -1.0f), x), mid, lo);
+__device__ __forceinline__ void split(pair_t v, uint32_t *piece, int stride) {
+  float2 x = unpack2(v);
+#pragma unroll
+  for (int p = 0; p < kPieces<DT>; ++p) {
+    const uint32_t w = piece[p * stride] = narrow2<DT>(x);
+    if (p + 1 < kPieces<DT>) x = make_float2(left_out<DT>(static_cast<uint16_t>(w), x.x), left_out<DT>(static_cast<uint16_t>(w >> 16), x.y));
+  }
 }
 
 // The power of two that brings a largest magnitude (as bits) to [2^14, 2^15), and its inverse; 1 for zero, infinities and NaN.
@@ -232,14 +247,22 @@ __device__ __forceinline__ uint32_t pair_weights(uint32_t p, const Decays &d, in
   return most;
 }
 
-// Half of a row of A's two pieces (kHalf bytes apart) to shared memory.
-__device__ __forceinline__ void put_weights(char *a, int i, int half, const uint32_t *hi, const uint32_t *lo) {
+// Half of a row of A, scaled by fit, to shared memory: its pieces lie kHalf bytes apart.  Zeros where any is false (one for a warp).
+template <int DT>
+__device__ __forceinline__ void put_weights(char *a, int i, int half, const pair_t *y, float fit, bool any) {
   char *row = a + i * 128;
+  const pair_t f = pack2(fit, fit);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
+    uint32_t w[kPieces<DT>][4] = {};
+    if (any) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) split<DT>(DT == SPEC_DTYPE_F16 ? mul2(y[4 * e + x], f) : y[4 * e + x], &w[0][x], 4);
+    }
     const int to = ((half * 4 + e) ^ (i & 7)) << 4;
-    *reinterpret_cast<uint4 *>(row + to) = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
-    *reinterpret_cast<uint4 *>(row + kChunk * 128 + to) = make_uint4(lo[4 * e], lo[4 * e + 1], lo[4 * e + 2], lo[4 * e + 3]);
+#pragma unroll
+    for (int p = 0; p < kPieces<DT>; ++p)
+      *reinterpret_cast<uint4 *>(row + p * kChunk * 128 + to) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
   }
 }
 
@@ -321,7 +344,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                        const __grid_constant__ CUtensorMap v_map) {
   using S = ChunkShape<DT, DK, OUT>;
   constexpr bool F16 = DT == SPEC_DTYPE_F16;
-  constexpr uint32_t kDS = 0, kSHi = 128, kSLo = 192, kO1 = 256, kO2 = 384, kP = 448;  // tensor memory; O1 twice
+  constexpr uint32_t kDS = S::kDS, kO2 = S::kO2, kP = S::kP;
   extern __shared__ char raw[];
   char *const smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   ChunkSmall &sm = *reinterpret_cast<ChunkSmall *>(smem + S::kSmall);
@@ -356,10 +379,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      bar_init(&sm.full[i], 1), bar_init(&sm.k_read[i], kStateWarps + (F16 ? 1 : 0));
+      bar_init(&sm.full[i], 1), bar_init(&sm.k_read[i], kKeyWarps<OUT> + (F16 ? 1 : 0));
       bar_init(&sm.p_full[i], 1), bar_init(&sm.o1_full[i], 1), bar_init(&sm.o2_full[i], 1), bar_init(&sm.ds_full[i], 1);
     }
-    for (int i = 0; i < 2; ++i) bar_init(&sm.kt_full[i], kStateWarps);
+    for (int i = 0; i < 2; ++i) bar_init(&sm.kt_full[i], kKeyWarps<OUT>);
     bar_init(&sm.p_empty, 4), bar_init(&sm.a_full, 4), bar_init(&sm.ds_empty, kStateWarps), bar_init(&sm.s_full, kStateWarps), bar_init(&sm.o_empty, 4);
     for (int i = 0; i < kDecayRing; ++i) bar_init(&sm.dec_full[i], 1), bar_init(&sm.dec_empty[i], OUT ? kStateWarps + 8 : kStateWarps);
     bar_init(&sm.meet_s, kStateWarps), bar_init(&sm.meet_a, 4);
@@ -373,6 +396,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   volatile int *dead = &sm.dead;
+  auto o1_of = [&](int c) -> uint32_t { return tmem + S::kO1 + (c & 1) * 64; };
   // of the barriers counted by chunk
   auto wait4 = [&](uint64_t *bars, int c) -> bool { return warp_wait(&bars[c & 3], c >> 2 & 1, dead); };
 
@@ -469,13 +493,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (!wait4(sm.full, c)) break;
         if (!warp_wait(&sm.s_full, c & 1, dead)) break;
         tc_fence_after();
-        if (elect_one()) {  // (into the half that chunk c - 2 left: its outputs were waited for before the last O2)
+        if (elect_one()) {  // (into the one that chunk c - 2 left: its outputs were waited for before the last O2)
 #pragma unroll 1
-          for (int x = 0; x < DK / 32; ++x) {  // a piece's 64 columns of a half of Q
-            const uint32_t piece = tmem + (x & 1 ? kSLo : kSHi) + (x >> 1) * 32;
-            const uint64_t q = q_desc + ((sv * S::kTileK + (x >> 1) * S::kHalf) >> 4);
+          for (int x = 0; x < kPieces<DT> * DK / 64; ++x) {  // a piece's 64 columns of a half of Q, the smallest piece first
+            const int half = x % (DK / 64), p = kPieces<DT> - 1 - x / (DK / 64);
+            const uint32_t piece = tmem + S::kS + p * S::kPieceS + half * 32;
+            const uint64_t q = q_desc + ((sv * S::kTileK + half * S::kHalf) >> 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16_ta(tmem + kO1 + (c & 1) * 64, piece + k * 8, q + 2 * k, kId1, x + k > 0);
+            for (int k = 0; k < 4; ++k) mma_f16_ta(o1_of(c), piece + k * 8, q + 2 * k, kId1, x + k > 0);
           }
           tc_commit(&sm.o1_full[c & 3]);
         }
@@ -486,10 +511,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll 1
-          for (int piece = 0; piece < 2; ++piece) {
-            const uint64_t v = v_desc + ((sv * S::kTileV) >> 4), a = a_desc + ((piece * S::kHalf) >> 4);
+          for (int p = kPieces<DT> - 1; p >= 0; --p) {
+            const uint64_t v = v_desc + ((sv * S::kTileV) >> 4), a = a_desc + ((p * S::kHalf) >> 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16_ss(tmem + kO2, v + 128 * k, a + 2 * k, kId2, piece + k > 0);
+            for (int k = 0; k < 4; ++k) mma_f16_ss(tmem + kO2, v + 128 * k, a + 2 * k, kId2, p + 1 < kPieces<DT> || k > 0);
           }
           tc_commit(&sm.o2_full[c & 3]);
         }
@@ -507,11 +532,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint64_t kt_desc = matrix_desc(smem_u32(smem + S::kKt), S::kHalf, 1024, kSwizzle128);
     int np = 0, ns = 0;
 #pragma unroll 1
-    for (int c = -1; c < chunks; ++c) {  // dS of a chunk, P of the next
-      if (c >= 0 && c < updates) {
-        if (!OUT && !wait4(sm.full, c)) break;
+    for (int c = 0; c < chunks; ++c) {
+      if (!wait4(sm.full, c)) break;
+      if (c > 0 && !warp_wait(&sm.ds_empty, (c - 1) & 1, dead)) break;  // (every chunk but the last has a dS)
+      if (OUT) {
+        const int sk = c % S::kStagesK, sq = c % S::kStagesV;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll 1
+          for (int x = 0; x < DK / 64; ++x) {
+            const uint64_t q = q_desc + ((sq * S::kTileK + x * S::kHalf) >> 4), k0 = k_desc + ((sk * S::kTileK + x * S::kHalf) >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_f16_ss(tmem + kP, q + 2 * k, k0 + 2 * k, kIdP, x + k > 0);
+          }
+          tc_commit(&sm.p_full[c & 3]);
+        }
+        __syncwarp();
+        ++np;
+      }
+      if (c < updates) {
+        if (OUT && !warp_wait(&sm.p_empty, c & 1, dead)) break;
         if (!warp_wait(&sm.kt_full[c % S::kAhead], c / S::kAhead & 1, dead)) break;
-        if (c > 0 && !warp_wait(&sm.ds_empty, (c - 1) & 1, dead)) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll 1
@@ -525,23 +566,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         __syncwarp();
         ++ns;
-      }
-      if (OUT && c + 1 < chunks) {
-        const int d = c + 1, sk = d % S::kStagesK, sq = d % S::kStagesV;
-        if (!wait4(sm.full, d)) break;
-        if (c >= 0 && !warp_wait(&sm.p_empty, c & 1, dead)) break;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll 1
-          for (int x = 0; x < DK / 64; ++x) {
-            const uint64_t q = q_desc + ((sq * S::kTileK + x * S::kHalf) >> 4), k0 = k_desc + ((sk * S::kTileK + x * S::kHalf) >> 4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16_ss(tmem + kP, q + 2 * k, k0 + 2 * k, kIdP, x + k > 0);
-          }
-          tc_commit(&sm.p_full[d & 3]);
-        }
-        __syncwarp();
-        ++np;
       }
     }
     if (lane == 0) sm.products_p = np, sm.products_s = ns;
@@ -594,11 +618,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < OWN / 16; ++k) {
-        uint32_t hi[8], lo[8];
+        uint32_t w[kPieces<DT>][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) split2<DT>(F16 ? mul2(s[8 * k + e], f) : s[8 * k + e], hi[e], lo[e]);
-        tmem_st8(tmem + lanes + kSHi + four * (OWN / 2) + k * 8, hi);
-        tmem_st8(tmem + lanes + kSLo + four * (OWN / 2) + k * 8, lo);
+        for (int e = 0; e < 8; ++e) split<DT>(F16 ? mul2(s[8 * k + e], f) : s[8 * k + e], &w[0][e], 8);
+#pragma unroll
+        for (int p = 0; p < kPieces<DT>; ++p) tmem_st8(tmem + lanes + S::kS + p * S::kPieceS + four * (OWN / 2) + k * 8, w[p]);
       }
       tc_wait_st();
       tc_fence_before();
@@ -606,7 +630,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       return true;
     };
     // K' of chunk c
-    const int own = (warp - 12) * 32 + lane, row = own & 63, part = own >> 6;  // an eighth of a row to a thread
+    constexpr int kParts = DK / 4 / kKeyWarps<OUT>;  // 16 bytes each, of a row to a thread
+    const bool makes = !OUT || (warp & 2);
+    const int own = (OUT ? four * 2 + (warp & 1) : warp - 12) * 32 + lane, row = own & 63, part = (own >> 6) * kParts;
     auto keys = [&](int c) -> bool {
       const int r = c % kDecayRing, sk = c % S::kStagesK, m = min(kChunk, len - (c0 + c) * kChunk);
       if (!warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead)) return false;
@@ -615,27 +641,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (c >= S::kAhead && !wait4(sm.ds_full, c - S::kAhead)) return false;
         const float left = sm.d[r].left[row];
         const bool past = row >= m;
-        constexpr int kPieces = DK / 64;  // 16-byte pieces to a thread
-        const int base = DK == 128 ? (part >> 2) * S::kHalf + row * 128 : row * 128, first = DK == 128 ? (part & 3) * 2 : part;
+        const int base = (part >> 3) * S::kHalf + row * 128, first = part & 7;
         const char *from = smem + S::kK + sk * S::kTileK + base;
         char *to = smem + S::kKt + c % S::kAhead * S::kKeyPieces * S::kTileK + base;
         const pair_t f = pack2(left, left);
 #pragma unroll 2
-        for (int e = 0; e < kPieces; ++e) {
+        for (int e = 0; e < kParts; ++e) {
           const int o = ((first + e) ^ (row & 7)) << 4;
           const uint4 x = *reinterpret_cast<const uint4 *>(from + o);
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          uint32_t pieces[3][4];
+          uint32_t pieces[S::kKeyPieces][4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const float2 k = widen2<DT>(w[y]);
-            const pair_t z = mul2(pack2(k.x, k.y), f);
-            if constexpr (S::kKeyPieces == 3) split3<DT>(z, pieces[0][y], pieces[1][y], pieces[2][y]);
-            else split2<DT>(z, pieces[0][y], pieces[1][y]);
+            split<DT>(mul2(pack2(k.x, k.y), f), &pieces[0][y], 4);
           }
           if (past) [[unlikely]] {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) pieces[0][y] = pieces[1][y] = pieces[2][y] = 0;
+            for (int y = 0; y < 4 * S::kKeyPieces; ++y) pieces[0][y] = 0;
           }
 #pragma unroll
           for (int y = 0; y < S::kKeyPieces; ++y)
@@ -643,7 +666,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         if (m < kChunk) {
           const int sv = c % S::kStagesV;
-          for (int e = own; e < (kChunk - m) * 16; e += 32 * kStateWarps)
+          for (int e = own; e < (kChunk - m) * 16; e += 32 * kKeyWarps<OUT>)
             *reinterpret_cast<uint4 *>(smem + S::kV + sv * S::kTileV + (e & 1) * S::kHalf + (m + (e >> 4)) * 128 + (e >> 1 & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_async_shared();
@@ -660,7 +683,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (OUT && c >= 0 && !(going = hand_on(c))) break;
       // K' before the update where it is two chunks ahead; fp16's maxima have its time to meet
       constexpr bool kKeysFirst = S::kAhead == 2 && !F16;
-      if (kKeysFirst && c + S::kAhead < chunks && !(going = keys(c + S::kAhead))) break;
+      if (kKeysFirst && makes && c + S::kAhead < chunks && !(going = keys(c + S::kAhead))) break;
       if (c >= 0) {
         if (!(going = warp_wait(&sm.dec_full[r], (c / kDecayRing) & 1, dead))) break;
         if (c < updates) {
@@ -686,7 +709,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         warp_arrive(&sm.dec_empty[r], lane);
         if (OUT && F16 && c + 1 < chunks) show_most(c + 1);
       }
-      if (!kKeysFirst && c + S::kAhead < chunks && !(going = keys(c + S::kAhead))) break;
+      if (!kKeysFirst && makes && c + S::kAhead < chunks && !(going = keys(c + S::kAhead))) break;
     }
     float *to = nullptr;
     if (!OUT) {
@@ -718,24 +741,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const Decays &d = sm.d[r];
         // which of the half's rows this one follows
         const uint32_t sees = i >= j0 + 31 ? ~0u : i < j0 ? 0u : (2u << (i - j0)) - 1;
-        uint32_t hi[16], lo[16];
-        float back = 1.0f;
-        if (__any_sync(~0u, sees != 0)) {
-          pair_t y[16];
+        pair_t y[16];
+        float fit = 1.0f, back = 1.0f;
+        const bool any = __any_sync(~0u, sees != 0);
+        if (any) {
           const uint32_t most = pair_weights<DT>(tmem + (static_cast<uint32_t>(warp & 3) << 21) + kP, d, i, j0, sees, log2_scale, y);
           if constexpr (F16) sm.amax[c & 1][half][i] = most;
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if constexpr (!F16) split2<DT>(y[e], hi[e], lo[e]);
           tc_fence_before();
           warp_arrive(&sm.p_empty, lane);
           if constexpr (F16) {
             warp_arrive(&sm.meet_a, lane);
             if (!warp_wait(&sm.meet_a, met++ & 1, dead)) break;
-            const float fit = fit_half(max(most, sm.amax[c & 1][half ^ 1][i]), back);
-            const pair_t f = pack2(fit, fit);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) split2<DT>(mul2(y[e], f), hi[e], lo[e]);
+            fit = fit_half(max(most, sm.amax[c & 1][half ^ 1][i]), back);
           }
         } else {
           warp_arrive(&sm.p_empty, lane);
@@ -745,12 +762,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (!warp_wait(&sm.meet_a, met++ & 1, dead)) break;
             fit_half(sm.amax[c & 1][half ^ 1][i], back);
           }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0;
         }
         if (F16 && half == 0) sm.d[r].afac[i] = back;
         if (c > 0 && !wait4(sm.o2_full, c - 1)) break;
-        put_weights(smem + S::kA, i, half, hi, lo);
+        put_weights<DT>(smem + S::kA, i, half, y, fit, any);
         if (m < kChunk) {  // values past the request's rows take no part, whatever they are
           const int sv = c % S::kStagesV;
           if (!wait4(sm.full, c)) break;
@@ -781,7 +796,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         char *o = reinterpret_cast<char *>(P.out) + (b * P.os[0] + h * P.os[2] + (t0 + (lane >> 2)) * P.os[1] + dv0 + col) * 2;
 #pragma unroll 1
         for (int k = 0; k < kChunk; k += 16)
-          put_outputs<DT>(tmem + lanes + kO1 + (c & 1) * 64, tmem + lanes + kO2, d, k, m, sf, sm.stage[quarter][0], o, P.os[1],
+          put_outputs<DT>(o1_of(c) + lanes, tmem + lanes + kO2, d, k, m, sf, sm.stage[quarter][0], o, P.os[1],
                           dv0 + col < P.value_dim, bad);
         const float2 b2 = unpack2(bad);
         if (__any_sync(~0u, !(b2.x == 0.0f && b2.y == 0.0f))) [[unlikely]] {  // a row's sum that is no number: without the rows that it does not follow
@@ -789,7 +804,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int i = 0; i < m; ++i) {
             const uint64_t sees = (2ull << i) - 1;
             float x[8];
-            tmem_ld8(tmem + lanes + kO1 + (c & 1) * 64 + (i & ~7), x);
+            tmem_ld8(o1_of(c) + lanes + (i & ~7), x);
             tc_wait_ld();
             float v = x[0];
 #pragma unroll
@@ -862,14 +877,16 @@ cudaError_t launch_chunks(const StateChunkPlan &A, const CUtensorMap *maps, cuda
 // (request, head, 128 columns) goes through the steps above once, P's columns
 // of tensor memory becoming O2's, so that two CTAs share an SM and one loads
 // its state while the other computes.  16 trees of 60 nodes, 48 heads: 64 us
-// as a chunk of the kernel above (one CTA to an SM), 32 us so.
+// as a chunk of the kernel above (one CTA to an SM), 32 us so.  Half of tensor
+// memory holds two of S's pieces at a time: in bf16 the largest waits in
+// registers until O1 has taken the others.
 constexpr int kShortThreads = 256;
 
-template <int DK>
+template <int DT, int DK>
 struct ShortShape {
   static constexpr int kHalf = kChunk * 128;
   static constexpr int kTileK = DK / 64 * kHalf, kTileV = 2 * kHalf;
-  static constexpr int kQ = 0, kK = kQ + kTileK, kV = kK + kTileK, kA = kV + kTileV, kSmall = kA + 2 * kHalf;
+  static constexpr int kQ = 0, kK = kQ + kTileK, kV = kK + kTileK, kA = kV + kTileV, kSmall = kA + kPieces<DT> * kHalf;
   static constexpr int kBytes = kSmall + 14336 + 1024;
 };
 
@@ -884,15 +901,15 @@ struct ShortSmall {
   uint32_t tmem;
   int dead;
 };
-static_assert(sizeof(ShortSmall) <= 14336 && ShortShape<128>::kBytes <= 113 * 1024);
+static_assert(sizeof(ShortSmall) <= 14336 && ShortShape<SPEC_DTYPE_BF16, 128>::kBytes <= 113 * 1024);
 
 template <int DT, int DK>
 __global__ void __launch_bounds__(kShortThreads, 2)
     state_short_kernel(const StateChunkPlan A, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                        const __grid_constant__ CUtensorMap v_map) {
-  using S = ShortShape<DK>;
+  using S = ShortShape<DT, DK>;
   constexpr bool F16 = DT == SPEC_DTYPE_F16;
-  constexpr uint32_t kSHi = 0, kSLo = 64, kO1 = 128, kP = 192;  // tensor memory; O2 in P's place
+  constexpr uint32_t kS = 0, kO1 = 128, kP = 192;  // tensor memory: two of S's pieces, the smaller first; O2 in P's place
   extern __shared__ char raw[];
   char *const smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   ShortSmall &sm = *reinterpret_cast<ShortSmall *>(smem + S::kSmall);
@@ -990,44 +1007,63 @@ __global__ void __launch_bounds__(kShortThreads, 2)
 #pragma unroll
       for (int e = 0; e < OWN; ++e) s[e] *= fit;
     }
+    constexpr int kLast = kPieces<DT> - 1;
+    uint32_t largest[kLast == 2 ? OWN / 2 : 1];
 #pragma unroll
     for (int k = 0; k < OWN / 16; ++k) {
-      uint32_t hi[8], lo[8];
+      uint32_t w[kPieces<DT>][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) split2<DT>(pack2(s[16 * k + 2 * e], s[16 * k + 2 * e + 1]), hi[e], lo[e]);
-      tmem_st8(tmem + lanes + kSHi + half * (OWN / 2) + k * 8, hi);
-      tmem_st8(tmem + lanes + kSLo + half * (OWN / 2) + k * 8, lo);
+      for (int e = 0; e < 8; ++e) split<DT>(pack2(s[16 * k + 2 * e], s[16 * k + 2 * e + 1]), &w[0][e], 8);
+      tmem_st8(tmem + lanes + kS + half * (OWN / 2) + k * 8, w[kLast]);
+      tmem_st8(tmem + lanes + kS + 64 + half * (OWN / 2) + k * 8, w[kLast - 1]);
+      if constexpr (kLast == 2) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) largest[8 * k + e] = w[0][e];
+      }
     }
     tc_wait_st();
     tc_fence_before();
     __syncthreads();
-    // ---- P, O1
+    // ---- O1 of two pieces, P
     int begun = 0;  // products (warp 0)
+    constexpr uint32_t kId = rows_desc<DT>(kChunk, false, false);
+    const uint64_t q_desc = matrix_desc(smem_u32(smem + S::kQ), 16, 1024, kSwizzle128);
+    auto piece_product = [&](int place, bool more) {  // (one lane)
+#pragma unroll 1
+      for (int x = 0; x < DK / 64; ++x)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_f16_ta(tmem + kO1, tmem + kS + place * 64 + x * 32 + k * 8, q_desc + ((x * S::kHalf) >> 4) + 2 * k, kId, more || x + k > 0);
+    };
     if (warp == 0 && warp_wait(&sm.full, 0, dead)) {
       tc_fence_after();
       if (elect_one()) {
-        constexpr uint32_t kId = rows_desc<DT>(kChunk, false, false);
-        const uint64_t q_desc = matrix_desc(smem_u32(smem + S::kQ), 16, 1024, kSwizzle128);
         const uint64_t k_desc = matrix_desc(smem_u32(smem + S::kK), 16, 1024, kSwizzle128);
+#pragma unroll 1
+        for (int place = 0; place < 2; ++place) piece_product(place, place > 0);
+        tc_commit(&sm.o1_full);
 #pragma unroll 1
         for (int x = 0; x < DK / 64; ++x)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_f16_ss(tmem + kP, q_desc + ((x * S::kHalf) >> 4) + 2 * k, k_desc + ((x * S::kHalf) >> 4) + 2 * k, kId, x + k > 0);
         tc_commit(&sm.p_full);
-#pragma unroll 1
-        for (int x = 0; x < DK / 32; ++x)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_ta(tmem + kO1, tmem + (x & 1 ? kSLo : kSHi) + (x >> 1) * 32 + k * 8, q_desc + (((x >> 1) * S::kHalf) >> 4) + 2 * k, kId, x + k > 0);
-        tc_commit(&sm.o1_full);
       }
       begun = 2;
     }
     __syncwarp();
+    if constexpr (kLast == 2) {  // the largest piece in the smallest's place
+      if (warp_wait(&sm.o1_full, 0, dead)) {
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < OWN / 16; ++k) tmem_st8(tmem + lanes + kS + half * (OWN / 2) + k * 8, largest + 8 * k);
+        tc_wait_st();
+        tc_fence_before();
+      }
+    }
     // ---- A: half of a row to a thread of the lower lanes
     const int i = at;
-    uint32_t hi[16], lo[16], most = 0;
+    uint32_t most = 0;
     pair_t y[16];
     bool any = false;
     if (quarter < 2 && warp_wait(&sm.p_full, 0, dead)) {
@@ -1047,13 +1083,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
       }
     }
     if (quarter < 2) {
-      const pair_t f = pack2(fit, fit);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        if (any) split2<DT>(F16 ? mul2(y[e], f) : y[e], hi[e], lo[e]);
-        else hi[e] = lo[e] = 0;
-      }
-      put_weights(smem + S::kA, i, half, hi, lo);
+      put_weights<DT>(smem + S::kA, i, half, y, fit, any);
     } else {  // values past the request's rows take no part, whatever they are (their copy has landed when P has)
       if (warp_wait(&sm.full, 0, dead))
         for (int e = (half * 2 + quarter - 2) * 32 + lane; e < (kChunk - m) * 16; e += 128)
@@ -1062,18 +1092,19 @@ __global__ void __launch_bounds__(kShortThreads, 2)
     fence_async_shared();
     tc_fence_before();
     __syncthreads();
-    // ---- O2
+    // ---- O1 of the largest piece, O2
     const bool off = __any_sync(~0u, *dead);
     if (warp == 0 && !off) {
       tc_fence_after();
       if (elect_one()) {
-        constexpr uint32_t kId = rows_desc<DT>(kChunk, true, false);
+        if (kLast == 2) piece_product(0, true);
+        constexpr uint32_t kIdO = rows_desc<DT>(kChunk, true, false);
         const uint64_t v_desc = matrix_desc(smem_u32(smem + S::kV), S::kHalf, 1024, kSwizzle128);
         const uint64_t a_desc = matrix_desc(smem_u32(smem + S::kA), 16, 1024, kSwizzle128);
 #pragma unroll 1
-        for (int piece = 0; piece < 2; ++piece)
+        for (int p = kLast; p >= 0; --p)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_f16_ss(tmem + kP, v_desc + 128 * k, a_desc + ((piece * S::kHalf) >> 4) + 2 * k, kId, piece + k > 0);
+          for (int k = 0; k < 4; ++k) mma_f16_ss(tmem + kP, v_desc + 128 * k, a_desc + ((p * S::kHalf) >> 4) + 2 * k, kIdO, p < kLast || k > 0);
         tc_commit(&sm.o2_full);
       }
       begun = 3;
@@ -1128,7 +1159,7 @@ std::atomic<uint64_t> short_smem{0};
 template <int DT, int DK>
 cudaError_t launch_short(const StateChunkPlan &A, const CUtensorMap *maps, cudaStream_t st) {
   auto kern = state_short_kernel<DT, DK>;
-  const int bytes = ShortShape<DK>::kBytes;
+  const int bytes = ShortShape<DT, DK>::kBytes;
   const cudaError_t e = once_per_device([&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); }, short_smem<DT, DK>);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(A.p.B) * ((A.p.value_dim + 127) / 128) * A.p.heads);

@@ -1,0 +1,181 @@
+"""How many digits the linear-attention kernels keep, and over which range: each kernel against the recurrence in 64 bits."""
+import pytest
+import torch
+
+import state_oracle as ref
+
+pytestmark = pytest.mark.gpu
+
+BF, HF = torch.bfloat16, torch.float16
+U = ref.U
+
+
+@pytest.fixture(scope="module")
+def api():
+    from speculative_decoding_verification_02_gb300 import api, build
+    build.build()
+    torch.cuda.set_device(0)
+    return api
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ what the products take
+
+# Outputs that are differences of two terms next to one another: whatever an operand's pieces leave out stands alone in them.  The
+# terms' sums have at most eight addends other than zero (three pieces of each term, the two parts of an output); an accumulator
+# that cuts off loses 2^-23 of the largest for each, the factors e^G are off by 2^-22, and a term in two fp16 pieces by 2^-22: 2^-19
+# of a term in all.  Two bf16 pieces leave out 2^-18 to 2^-17 of every other term, which 128 columns cannot miss.
+NEXT_TO = 2.0 ** -19
+
+
+def rounded(want, tol, dtype):
+    """tol, and the result's own rounding: half a step of a value, or of fp16's subnormals (they lie 2^-24 apart)."""
+    return tol + torch.finfo(dtype).eps / 2 * (want.abs() + tol) + (2.0 ** -25 if dtype == HF else 0.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,write", [(40, False), (64, False), (64, True), (150, True)])
+def test_digits_of_the_state(api, dtype, D, n, write):
+    """o = S[a] - S[b], in a lane each: S's digits as the products take them."""
+    g = torch.Generator().manual_seed(n + D)
+    S = torch.zeros(1, 1, D, D)
+    S[0, 0, 5] = 1 + torch.rand(D, generator=g)
+    S[0, 0, 9] = S[0, 0, 5] * (1 + 2.0 ** -10 * torch.randn(D, generator=g))
+    q = torch.zeros(1, n, 1, D)
+    q[..., 5], q[..., 9] = 1, -1
+    k = torch.zeros(1, n, 1, D)
+    v = torch.randn(1, n, 1, D, generator=g)
+    decay = torch.zeros(1, n, 1)
+    args = [x.to(dtype).cuda() for x in (q, k, v)] + [decay.cuda(), S.cuda()]
+    o = api.spec_state_forward(*args, scale=1.0, write=write)["out"] if write else api.spec_state_attend(*args, scale=1.0)["out"]
+    want = (S[0, 0, 5].double() - S[0, 0, 9].double()).expand(n, D)
+    tol = NEXT_TO * S[0, 0, 5].double()
+    worst = (o[0, :, 0].double().cpu() - want).abs() - rounded(want, tol, dtype)
+    assert float(worst.max()) <= 0, float(worst.max())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,write", [(40, False), (64, False), (64, True), (150, True)])
+def test_digits_of_the_weights(api, dtype, D, n, write):
+    """Rows 2 i and 2 i + 1 hold values v and -v: what an odd row adds of its pair is the difference of two weights."""
+    g = torch.Generator().manual_seed(n + D)
+    k = torch.zeros(1, n, 1, D)
+    k[..., 3] = 1
+    q = torch.zeros(1, n, 1, D)
+    q[..., 3] = 1.5
+    v = torch.randn(1, n, 1, D, generator=g).to(dtype).float()
+    v[:, 1::2] = -v[:, 0:n - n % 2:2]
+    decay = torch.zeros(1, n, 1)
+    decay[:, 1::2, 0] = -2.0 ** -9 * (1 + torch.rand(n // 2, generator=g))
+    decay[:, 0::2, 0] = -200.0  # nothing but the pair itself
+    args = [x.to(dtype).cuda() for x in (q, k, v)] + [decay.cuda()]
+    if write:
+        o = api.spec_state_forward(*args, None, dst=torch.zeros(1, 1, D, D, device="cuda"), scale=1.0)["out"]
+    else:
+        o = api.spec_state_attend(*args, torch.zeros(1, 1, D, D, device="cuda"), scale=1.0)["out"]
+    for i in range(1, n, 2):
+        w = 1.5 * torch.expm1(decay[0, i].double()) * v[0, i - 1].double()
+        tol = NEXT_TO * 1.5 * v[0, i - 1].double().abs() + 2.0 ** -80
+        worst = (o[0, i].double().cpu() - w).abs() - rounded(w, tol, dtype)
+        assert float(worst.max()) <= 0, (i, float(worst.max()))
+
+
+# ------------------------------------------------------------------ every kernel
+
+KINDS = ["rows", "blocks", "chunk", "segments", "short", "short_tree", "large_tree", "commit"]
+TOKENS = dict(rows=12, blocks=24, chunk=150, segments=600, short=40, short_tree=50, large_tree=100, commit=40)
+
+
+def random_tree(n, seed, reach=3, depth=60):
+    g = torch.Generator().manual_seed(seed)
+    parents, d = [-1], [0]
+    for i in range(1, n):
+        may = [j for j in range(max(0, i - reach), i) if d[j] < depth] or [0]
+        parents.append(may[int(torch.randint(len(may), (1,), generator=g))])
+        d.append(d[parents[-1]] + 1)
+    return parents
+
+
+class Call:
+    """Rows of one request for a kernel: q, k, v, g in the order of its nodes, depth the tokens in front of each."""
+
+    def __init__(self, kind, dtype, D, seed, Hk=1, G=2):
+        g = torch.Generator().manual_seed(seed)
+        self.kind, self.dtype, self.D, self.n = kind, dtype, D, TOKENS[kind]
+        self.tree = kind.endswith("tree")
+        self.parents = random_tree(self.n, seed) if self.tree else ref.chain(self.n)
+        self.depth = []
+        for p in self.parents:
+            self.depth.append(0 if p < 0 else self.depth[p] + 1)
+        n, H = self.n, Hk * G
+        self.q = torch.randn(n, Hk, D, generator=g).to(dtype)
+        self.k = (torch.randn(n, Hk, D, generator=g) / D ** 0.5).to(dtype)
+        self.v = torch.randn(n, H, D, generator=g).to(dtype)
+        self.g = -0.3 * torch.rand(n, H, generator=g)
+        self.S0 = torch.randn(H, D, D, generator=g)
+        self.scale = D ** -0.5
+
+    def run(self, api):
+        """-> out [n, H, D] or None, the state after or None"""
+        q, k, v, g = (x[None].cuda() for x in (self.q, self.k, self.v, self.g))
+        pool = self.S0[None].cuda()
+        if self.kind == "commit":
+            o, out = api.spec_state_commit(k, v, g, pool), None
+        elif self.kind.startswith("short") or self.tree:
+            o = api.spec_state_attend(q, k, v, g, pool, parents=i32([self.parents]) if self.tree else None)
+            out, pool = o["out"][0], None
+        elif self.kind == "blocks":  # rows that start off 16-byte boundaries: the kernel for a few rows, block after block
+            room = [torch.zeros(x.numel() + 1, dtype=x.dtype, device="cuda")[1:].view(x.shape) for x in (q, k, v)]
+            for x, y in zip(room, (q, k, v)):
+                x.copy_(y)
+            o = api.spec_state_forward(*room, g, pool)
+            out = o["out"][0]
+        else:
+            o = api.spec_state_forward(q, k, v, g, pool)
+            out = o["out"][0]
+        assert o["status"].tolist() == [0]
+        return out, None if pool is None else pool[0]
+
+    def want(self):
+        g = torch.where(self.g < -120, -float("inf"), self.g.double())  # such a factor is 0
+        return ref.walk(self.q, self.k, self.v, g, self.S0, self.parents, self.scale)
+
+    def check(self, api):
+        out, state = self.run(api)
+        outs, last = self.want()
+        if out is not None:
+            ref.check_out(out, outs, self.D, self.n, self.dtype)
+        if state is not None:
+            ref.check_state(state, last, self.n, self.n)
+
+
+# The states on the whole, in the root of their squares.  A token's term: its factor e^G (2^-22), K' exactly in three bf16 pieces (in
+# two fp16 pieces, 2^-23 of the chunk's largest), the products' sum, which cuts off 2^-23 of itself at each of its last four steps
+# (the steps before add pieces of 2^-8 of it), and one rounded addition for each block that it stays in, whose errors add up as the
+# root of their number (150 tokens: 3 chunks or 10 blocks; 600: 10, joined once more): 2^-20 = 9.5e-7.  Two pieces of K' in bf16
+# leave out 2^-18 of a value in the root of squares.
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind", ["rows", "blocks", "chunk", "segments", "commit"])
+def test_states_on_the_whole(api, kind, D, dtype):
+    c = Call(kind, dtype, D, 40, Hk=2)
+    c.g *= torch.tensor([1.0, 0.1, 1e-2, 1e-3])
+    state = c.run(api)[1].double().cpu()
+    run = c.g.double().cumsum(0)
+    for h in range(4):
+        k = c.k[:, h // 2].double() * torch.exp(run[-1, h] - run[:, h])[:, None]
+        last = torch.exp(run[-1, h]) * c.S0[h].double() + k.T @ c.v[:, h].double()
+        off = float((state[h] - last).norm() / last.norm())
+        assert off <= 2.0 ** -20, (h, off)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("kind", KINDS)
+def test_ordinary_rows(api, kind, dtype):
+    """The bounds of 32-bit sums, with nothing for operands of fewer bits."""
+    Call(kind, dtype, 128, 41).check(api)
