@@ -161,13 +161,15 @@ __device__ __forceinline__ float left_out(uint16_t piece, float x) {
   return r;
 }
 
-// Two values in pieces of the rows' type: each rounds what the ones before it left out.
+// Two values in pieces of the rows' type.  fp16: each rounds what the ones before it left out.  bf16: each cuts off what follows its 8
+// digits, so that no finite value becomes an infinity.
 template <int DT>
 __device__ __forceinline__ void split(pair_t v, uint32_t *piece, int stride) {
   float2 x = unpack2(v);
 #pragma unroll
   for (int p = 0; p < kPieces<DT>; ++p) {
-    const uint32_t w = piece[p * stride] = narrow2<DT>(x);
+    const uint32_t w = DT == SPEC_DTYPE_BF16 ? __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632) : narrow2<DT>(x);
+    piece[p * stride] = w;
     if (p + 1 < kPieces<DT>) x = make_float2(left_out<DT>(static_cast<uint16_t>(w), x.x), left_out<DT>(static_cast<uint16_t>(w >> 16), x.y));
   }
 }

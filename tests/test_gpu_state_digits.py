@@ -179,3 +179,24 @@ def test_states_on_the_whole(api, kind, D, dtype):
 def test_ordinary_rows(api, kind, dtype):
     """The bounds of 32-bit sums, with nothing for operands of fewer bits."""
     Call(kind, dtype, 128, 41).check(api)
+
+
+# ------------------------------------------------------------------ fp16's scales, and what is no number
+
+@pytest.mark.parametrize("n,write", [(5, False), (5, True), (40, False), (64, True), (150, True), (900, True)])
+def test_states_next_to_the_largest_number(api, n, write):
+    """bf16: values beyond its largest number (3.3895e38), finite in fp32, give finite outputs and come out as they went in."""
+    D = 128
+    g = torch.Generator().manual_seed(n)
+    S = 3.4e38 * (1 - 2e-3 * torch.rand(1, 1, D, D, generator=g)) * torch.where(torch.rand(1, 1, D, D, generator=g) < 0.5, -1.0, 1.0)
+    q = torch.zeros(1, n, 1, D)
+    for i in range(n):
+        q[0, i, 0, i % D] = 2.0 ** -10
+    q, k, v = q.to(BF), torch.zeros(1, n, 1, D, dtype=BF), torch.randn(1, n, 1, D, generator=g).to(BF)
+    pool = S.cuda()
+    args = [x.cuda() for x in (q, k, v)] + [torch.zeros(1, n, 1, device="cuda"), pool]
+    o = api.spec_state_forward(*args, scale=1.0) if write else api.spec_state_attend(*args, scale=1.0)
+    assert torch.equal(pool.cpu(), S)
+    want = torch.stack([S[0, 0, i % D].double() * 2.0 ** -10 for i in range(n)])
+    worst = ((o["out"][0, :, 0].double().cpu() - want).abs() / want.abs()).max()
+    assert float(worst) <= 2.0 ** -8 + 2.0 ** -20
