@@ -25,9 +25,10 @@ namespace {
 //   out_i = scale (e^{G_i} O1_i + O2_i),   S <- e^{G_last} S + dS
 // S itself stays in fp32 registers; what a product takes of it, of A and of
 // K' is the sum of pieces of the rows' type, each what those before it left
-// out: three in bf16, which hold all 24 digits, two in fp16, which leave out
-// 2^-23 of a value at most, scaled by powers of two (a lane of S, a row of A,
-// a chunk's K') to stay within its range.  The smallest pieces are added
+// out: three in bf16, which hold all 24 digits, two in fp16, scaled by a power
+// of two (one for a lane of S, a row of A, a chunk's K') that brings the
+// largest of them to 2^14: they leave out 2^-23 of a value, or 2^-39 of that
+// largest where a value is less than 2^-16 of it.  The smallest pieces are added
 // first, since the accumulator cuts off: after 500 chunks a state is 3.6e-7
 // off on the whole (two pieces of K' in bf16: 2.4e-6; 32-bit sums: 1.8e-7),
 // and bf16 outputs are as near to the plain form's as those of 32-bit sums.
@@ -180,6 +181,30 @@ __device__ __forceinline__ float fit_half(uint32_t amax, float &back) {
   const int s = amax == 0 || e == 128 ? 0 : max(-112, min(112, 14 - e));
   back = __uint_as_float(static_cast<uint32_t>(127 - s) << 23);
   return __uint_as_float(static_cast<uint32_t>(127 + s) << 23);
+}
+
+// The largest finite magnitude of a key in fp16 (its 16-byte pieces from another one on in each lane: other banks).
+template <int DK>
+__device__ __forceinline__ float largest_key(const char *keys, int row) {
+  const char *at = keys + row * 128;
+  __half2 most = __half2half2(__ushort_as_half(0));
+#pragma unroll 4
+  for (int e = 0; e < DK / 8; ++e) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(at + (e >> 3) * kChunk * 128 + ((e ^ threadIdx.x) & 7) * 16);
+    const __half2 *x = reinterpret_cast<const __half2 *>(&v);
+    most = __hmax2(most, __hmax2(__hmax2(__habs2(x[0]), __habs2(x[1])), __hmax2(__habs2(x[2]), __habs2(x[3]))));
+  }
+  const float2 two = __half22float2(most);
+  float top = fmaxf(two.x, two.y);
+  if (!(top < INFINITY)) [[unlikely]] {
+    top = 0.0f;
+#pragma unroll 1
+    for (int e = 0; e < DK; ++e) {
+      const float x = fabsf(__half2float(*reinterpret_cast<const __half *>(at + (e >> 6) * kChunk * 128 + (e & 63) * 2)));
+      top = x < INFINITY ? fmaxf(top, x) : top;
+    }
+  }
+  return top;
 }
 
 // Row i's weight for row j without what P held: e^{G_i - G_j} from the handed-on parts.
@@ -451,26 +476,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const Log2Parts q1 = Log2Sum{sums.total.whole - sums.g1.whole, sums.total.rest - sums.g1.rest}.parts(sums.spoilt);
       *reinterpret_cast<float2 *>(&d.left[2 * lane]) = make_float2(2 * lane < m ? q0.power() : 0.0f, 2 * lane + 1 < m ? q1.power() : 0.0f);
       if (lane == 0) d.lam = sums.total.parts(sums.spoilt).power();
-      if constexpr (F16) {  // K' divided by the power of two that its largest value asks for, as these factors go into it
+      if constexpr (F16) {  // K' divided by the power of two that its largest finite value asks for, as these factors go into it
         if (!wait4(sm.full, c)) break;
         const char *keys = smem + S::kK + c % S::kStagesK * S::kTileK;
-        __half2 most = __half2half2(__ushort_as_half(0));
-#pragma unroll 4
-        for (int e = lane; e < S::kTileK / 16; e += 32) {
-          const uint4 v = *reinterpret_cast<const uint4 *>(keys + e * 16);
-          if ((e & 511) >> 3 < m) {
-            const __half2 *x = reinterpret_cast<const __half2 *>(&v);
-            most = __hmax2(most, __hmax2(__hmax2(__habs2(x[0]), __habs2(x[1])), __hmax2(__habs2(x[2]), __habs2(x[3]))));
-          }
-        }
+        const float2 left = *reinterpret_cast<const float2 *>(&d.left[2 * lane]);
+        const float most = fmaxf(largest_key<DK>(keys, 2 * lane) * left.x, largest_key<DK>(keys, 2 * lane + 1) * left.y);
         warp_arrive(&sm.k_read[c & 3], lane);
-        const float2 two = __half22float2(most);
-        float l0 = 2 * lane < m ? q0.power() : 0.0f, l1 = 2 * lane + 1 < m ? q1.power() : 0.0f;
-        const float key = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(fmaxf(two.x, two.y))));
-        const float factor = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(fmaxf(l0, l1))));
         float back;
-        const float fit = fit_half(__float_as_uint(key * factor), back);
-        *reinterpret_cast<float2 *>(&d.left[2 * lane]) = make_float2(l0 * fit, l1 * fit);
+        const float fit = fit_half(__reduce_max_sync(~0u, __float_as_uint(fmaxf(most, 0.0f))), back);
+        *reinterpret_cast<float2 *>(&d.left[2 * lane]) = make_float2(left.x * fit, left.y * fit);
         if (lane == 0) d.kfac = back;
       }
       warp_arrive(&sm.dec_full[r], lane);

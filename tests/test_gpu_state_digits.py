@@ -183,6 +183,35 @@ def test_ordinary_rows(api, kind, dtype):
 
 # ------------------------------------------------------------------ fp16's scales, and what is no number
 
+@pytest.mark.parametrize("large", [3e4, float("inf")])
+@pytest.mark.parametrize("n", [40, 150, 1300])
+def test_small_keys_beside_large_ones(api, n, large):
+    """fp16: a chunk's K' has one power of two for all, by its largest e^G k.  A key of 3e4 whose token is all but forgotten (e^-28)
+    takes no digits from keys of 1e-3; nor does an infinite key, whose row of the state alone is no number."""
+    D = 64
+    g = torch.Generator().manual_seed(n)
+    k = 1e-3 * torch.randn(1, n, 1, D, generator=g)
+    v = torch.randn(1, n, 1, D, generator=g).to(HF)
+    decay = torch.full((1, n, 1), -0.01)
+    for at in range(2, n, 64):
+        k[0, at] = 0
+        k[0, at, 0, 0] = large
+        decay[0, at + 1] = -28.0
+    k = k.to(HF)
+    pool = torch.zeros(1, 1, D, D, device="cuda")
+    api.spec_state_forward(k.cuda(), k.cuda(), v.cuda(), decay.cuda(), None, dst=pool)
+    G = torch.flip(torch.cumsum(torch.flip(decay[0, :, 0].double(), [0]), 0), [0]) - decay[0, :, 0].double()
+    want = (k[0, :, 0].double() * torch.exp(G)[:, None]).T @ v[0, :, 0].double()
+    got = pool[0, 0].double().cpu()
+    # (as in test_states_on_the_whole)
+    off = float((got[1:] - want[1:]).norm() / want[1:].norm())
+    assert off <= 2.0 ** -20, off
+    if large > 1e5:
+        assert not got[0].isfinite().any()
+    else:
+        assert float((got[0] - want[0]).norm() / want[0].norm()) <= 2.0 ** -20
+
+
 @pytest.mark.parametrize("n,write", [(5, False), (5, True), (40, False), (64, True), (150, True), (900, True)])
 def test_states_next_to_the_largest_number(api, n, write):
     """bf16: values beyond its largest number (3.3895e38), finite in fp32, give finite outputs and come out as they went in."""
