@@ -577,10 +577,10 @@ size_t spec_cache_workspace_size(int op, const spec_cache *cache, int B, int N, 
  *               reads key head h / (heads / key_heads).
  *   v           heads heads of value_dim.
  *   decay       fp32 natural logarithms g of the factors, strides (request,
- *               token, head) as they come, 0 for what is shared.  -inf is a
- *               factor of 0, which forgets every finite thing before the token.
- *               Values beyond +-120 may count as +-120 (e^120 = 1e52: in fp32
- *               such a factor is 0 or infinite).
+ *               token, head) as they come, 0 for what is shared.  A value
+ *               below -120 (-inf among them) is a factor of 0, which forgets every
+ *               finite thing before the token.  One above 120 may count as 120
+ *               (e^120 = 1e52: in fp32 such a factor is infinite).
  * status[b] (out int32 [B] or NULL): SPEC_STATUS_BAD_LENGTH (a count out of
  * range), SPEC_STATUS_BAD_SLOT (a slot outside the pool), SPEC_STATUS_BAD_INDEX
  * or SPEC_STATUS_BAD_TREE.  Such a request's state is not written and its rows

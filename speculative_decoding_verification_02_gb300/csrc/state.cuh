@@ -153,9 +153,12 @@ struct Log2Sum {
     return Log2Parts{nan ? NAN : static_cast<float>(whole + carry), static_cast<float>(rest - (carry << kLog2Bits)) * (1.0f / (1 << kLog2Bits))};
   }
 };
-// A natural logarithm; beyond +-120 (1e52) a factor is 0 or infinite in fp32 whatever it is.  NaN gives 0.
+// A natural logarithm.  Below -120 the factor is 0, and so is every product with it, whatever grows behind it: 64 tokens' growth, of
+// 174 units at most each (beyond 120 an infinite factor in fp32 whatever it is), stays far below kForgets.  NaN gives 0.
+constexpr int kForgets = -(1 << 15);
 __device__ __forceinline__ Log2Sum log2_of(float g) {
-  const float x = fminf(fmaxf(g, -120.0f), 120.0f);
+  if (g < -120.0f) return Log2Sum{kForgets, 0};
+  const float x = fminf(g, 120.0f);
   const float y = x * 1.44269502f, e = fmaf(x, 1.44269502f, -y) + x * 1.92596303e-8f;  // log2(e) in two parts
   const float w = rintf(y);
   return g == g ? Log2Sum{static_cast<int>(w), static_cast<int>(rintf(((y - w) + e) * (1 << kLog2Bits)))} : Log2Sum{0, 0};

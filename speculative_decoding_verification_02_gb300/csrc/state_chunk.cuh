@@ -461,14 +461,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       x1 = c < chunks && t + 1 < len ? gp[(t + 1) * P.gs[1]] : 0.0f;
     };
     float x0, x1;
-    bool lost = false;
+    bool lost = false, forgot = false;
     fetch(0, x0, x1);
     for (int c = 0; c < chunks; ++c) {
       const int r = c % kDecayRing, t0 = (c0 + c) * kChunk;
       const int m = min(kChunk, len - t0);
       const ChunkSums sums = chunk_sums(x0, x1, lane);
       fetch(c + 1, x0, x1);
-      whole += sums.total.whole, rest += sums.total.rest, lost |= sums.spoilt;
+      whole += sums.total.whole, rest += sums.total.rest, lost |= sums.spoilt, forgot |= sums.total.whole < kForgets / 2;
       if (c >= kDecayRing && !warp_wait(&sm.dec_empty[r], (c / kDecayRing - 1) & 1, dead)) break;
       Decays &d = sm.d[r];
       put_sums(d, sums, P.scale, lane);
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (!OUT && lane == 0 && dv0 == 0) {  // (segments of many chunks: the sums in 64 bits, the whole part no further than fp32's exponents)
       whole += rest >> kLog2Bits;
       rest &= (1 << kLog2Bits) - 1;
-      const Log2Sum all_of{static_cast<int>(max(-4096ll, min(4096ll, whole))), static_cast<int>(rest)};
+      const Log2Sum all_of{forgot ? -4096 : static_cast<int>(max(-4096ll, min(4096ll, whole))), static_cast<int>(rest)};
       A.total[(static_cast<int64_t>(b) * P.heads + h) * A.slots() + piece] = all_of.parts(lost).power();
     }
   } else if (warp == 10) {

@@ -12,8 +12,8 @@
 // so a row costs one packed multiply-add for two elements of S (the recurrence
 // token by token: three).  Lane group g adds the terms of tokens g and g + 8 to
 // its part of q_i S, so one reduction over the groups serves both.  The sums
-// are exact (fixed point), so their differences are: -inf and long blocks lose
-// nothing.  A tree's row takes its ancestors' terms instead, one after another
+// are exact (fixed point), so their differences are: forgetful tokens and long
+// blocks lose nothing.  A tree's row takes its ancestors' terms instead, one after another
 // along its path, with k and v from memory.
 //
 // The rows' copies to shared memory are under way before the state's loads
@@ -264,15 +264,17 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
     } else {
       if (tid < m) {  // the row's path from itself up, and the decays that lie before each node of it
         int len = 0;
-        float sum = 0.0f;
+        Log2Sum sum{0, 0};
+        bool nan = false;
         for (int p = t0 + tid; p >= 0; p = parents[p]) {
           path[tid][len] = p;
-          path_w[tid][len] = sum;
+          path_w[tid][len] = sum.parts(nan).power();
           ++len;
-          sum += gp[p * P.gs[1]];
+          const float x = gp[p * P.gs[1]];
+          sum += log2_of(x), nan |= x != x;
         }
         path_len[tid] = len;
-        from_state[tid] = expf(sum) * P.scale;
+        from_state[tid] = sum.parts(nan).power() * P.scale;
       }
       __syncthreads();
       for (int i = 0; i < m; ++i) {
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
             s = fmaf(f.x, widen<DT>(u[0]), fmaf(f.y, widen<DT>(u[1]), s));
           }
           s = warp_add(s);
-          if (lane == 0) path_w[i][p] = s * expf(path_w[i][p]) * P.scale;
+          if (lane == 0) path_w[i][p] = s * path_w[i][p] * P.scale;
         }
       }
       __syncthreads();

@@ -181,6 +181,26 @@ def test_ordinary_rows(api, kind, dtype):
     Call(kind, dtype, 128, 41).check(api)
 
 
+# ------------------------------------------------------------------ decays
+
+@pytest.mark.parametrize("forget", [-float("inf"), -1e30, -150.0, torch.finfo(torch.float32).min])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("kind", KINDS)
+def test_forgotten_stays_forgotten(api, kind, dtype, forget):
+    """A factor of 0, then growth by e^69: nothing from before comes back, however large it was."""
+    c = Call(kind, dtype, 64, 42)
+    d = torch.tensor(c.depth) % 70
+    c.S0 *= 1e24
+    c.q[torch.tensor(c.depth) < 3] = 0  # (fp16 has no such outputs)
+    for at, x in ((3, forget), (4, 40.0), (5, 29.0)):
+        c.g[d == at] = x
+    c.k[(d >= 3) & (d <= 5)] = 0
+    c.check(api)
+    out, _ = c.run(api)
+    if out is not None:  # nothing at all between the reset and the first key after it
+        assert not out[((torch.tensor(c.depth) >= 3) & (torch.tensor(c.depth) <= 5)).cuda()].any()
+
+
 # ------------------------------------------------------------------ fp16's scales, and what is no number
 
 @pytest.mark.parametrize("large", [3e4, float("inf")])
