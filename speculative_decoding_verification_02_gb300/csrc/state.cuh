@@ -129,11 +129,11 @@ __device__ __forceinline__ uint16_t narrow(float x) {
   else return __half_as_ushort(__float2half(x));
 }
 
-// A sum of decays in units of log 2, in fixed point: whole units, and 2^-25ths
-// (of which 64 tokens' halves fit an int).  A token's is off by half of one of
-// them, sums and differences not at all, however large: what 64-bit floats
-// would do at many times the cost.
-constexpr int kLog2Bits = 25;
+// A sum of decays in units of log 2, in fixed point of 64 bits: 2^-40ths.  A
+// token's is off by one of them (1e-12, which a decay that is the same for a
+// million tokens adds up to 1e-6), sums and differences not at all, however
+// large: what 64-bit floats would do at many times the cost.
+constexpr int kLog2Bits = 40;
 struct Log2Parts {
   float hi, lo;  // a whole number and a rest in [-1/2, 1/2]
   __device__ __forceinline__ float power() const {  // 2^(hi + lo); 0 below the least normal number
@@ -143,25 +143,39 @@ struct Log2Parts {
   }
 };
 struct Log2Sum {
-  int whole, rest;
+  long long units;
   __device__ __forceinline__ Log2Sum &operator+=(const Log2Sum &x) {
-    whole += x.whole, rest += x.rest;
+    units += x.units;
     return *this;
   }
+  __device__ __forceinline__ Log2Sum operator-(const Log2Sum &x) const { return Log2Sum{units - x.units}; }
   __device__ __forceinline__ Log2Parts parts(bool nan) const {
-    const int carry = (rest + (1 << (kLog2Bits - 1))) >> kLog2Bits;
-    return Log2Parts{nan ? NAN : static_cast<float>(whole + carry), static_cast<float>(rest - (carry << kLog2Bits)) * (1.0f / (1 << kLog2Bits))};
+    const int whole = static_cast<int>((units + (1ll << (kLog2Bits - 1))) >> kLog2Bits);
+    const int rest = static_cast<int>((units - (static_cast<long long>(whole) << kLog2Bits)) >> (kLog2Bits - 32));  // 2^-32ths
+    return Log2Parts{nan ? NAN : static_cast<float>(whole), static_cast<float>(rest) * 0x1p-32f};
   }
 };
+__device__ __forceinline__ Log2Sum of_lane(const Log2Sum &x, int lane) { return Log2Sum{__shfl_sync(~0u, x.units, lane)}; }
+// The sum over a lane's own and those of the lanes below it.
+template <int LANES>
+__device__ __forceinline__ Log2Sum running(Log2Sum x, int lane) {
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) {
+    const Log2Sum y{__shfl_up_sync(~0u, x.units, o)};
+    if (lane >= o) x += y;
+  }
+  return x;
+}
 // A natural logarithm.  Below -120 the factor is 0, and so is every product with it, whatever grows behind it: 64 tokens' growth, of
 // 174 units at most each (beyond 120 an infinite factor in fp32 whatever it is), stays far below kForgets.  NaN gives 0.
-constexpr int kForgets = -(1 << 15);
+constexpr long long kForgets = -(1ll << (kLog2Bits + 15));
 __device__ __forceinline__ Log2Sum log2_of(float g) {
-  if (g < -120.0f) return Log2Sum{kForgets, 0};
+  if (g < -120.0f) return Log2Sum{kForgets};
   const float x = fminf(g, 120.0f);
   const float y = x * 1.44269502f, e = fmaf(x, 1.44269502f, -y) + x * 1.92596303e-8f;  // log2(e) in two parts
   const float w = rintf(y);
-  return g == g ? Log2Sum{static_cast<int>(w), static_cast<int>(rintf(((y - w) + e) * (1 << kLog2Bits)))} : Log2Sum{0, 0};
+  const long long units = (static_cast<long long>(static_cast<int>(w)) << kLog2Bits) + __float2ll_rn((y - w) * 0x1p40f) + __float2int_rn(e * 0x1p40f);
+  return Log2Sum{g == g ? units : 0};
 }
 
 #endif

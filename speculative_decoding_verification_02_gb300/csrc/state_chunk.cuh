@@ -222,15 +222,9 @@ __device__ __forceinline__ ChunkSums chunk_sums(float x0, float x1, int lane) {
   ChunkSums s{log2_of(x0), log2_of(x1)};
   const uint32_t nan0 = __ballot_sync(~0u, x0 != x0), nan1 = __ballot_sync(~0u, x1 != x1);
   s.g1 += s.g0;  // the lane's two, then the lanes before it
-  Log2Sum upto = s.g1;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const Log2Sum y{__shfl_up_sync(~0u, upto.whole, o), __shfl_up_sync(~0u, upto.rest, o)};
-    if (lane >= o) upto += y;
-  }
-  const Log2Sum before{upto.whole - s.g1.whole, upto.rest - s.g1.rest};
+  const Log2Sum before = running<32>(s.g1, lane) - s.g1;
   s.g0 += before, s.g1 += before;
-  s.total = Log2Sum{__shfl_sync(~0u, s.g1.whole, 31), __shfl_sync(~0u, s.g1.rest, 31)};
+  s.total = of_lane(s.g1, 31);
   const uint32_t to = (2u << lane) - 1, under = to >> 1;
   s.bad0 = nan0 & to || nan1 & under, s.bad1 = nan0 & to || nan1 & to;
   s.spoilt = nan0 || nan1;
@@ -454,7 +448,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   } else if (warp == 3) {
     // ---- decays: two tokens next to one another to a lane
     const float *gp = P.decay + b * P.gs[0] + h * P.gs[2];
-    long long whole = 0, rest = 0;  // of the segment's sum
+    long long whole = 0, rest = 0;  // of the segment's sum: units of log 2, 2^-40ths
     auto fetch = [&](int c, float &x0, float &x1) {
       const int t = (c0 + c) * kChunk + 2 * lane;
       x0 = c < chunks && t < len ? gp[t * P.gs[1]] : 0.0f;
@@ -468,12 +462,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int m = min(kChunk, len - t0);
       const ChunkSums sums = chunk_sums(x0, x1, lane);
       fetch(c + 1, x0, x1);
-      whole += sums.total.whole, rest += sums.total.rest, lost |= sums.spoilt, forgot |= sums.total.whole < kForgets / 2;
+      rest += sums.total.units;
+      whole += rest >> kLog2Bits, rest &= (1ll << kLog2Bits) - 1;
+      lost |= sums.spoilt, forgot |= sums.total.units < kForgets / 2;
       if (c >= kDecayRing && !warp_wait(&sm.dec_empty[r], (c / kDecayRing - 1) & 1, dead)) break;
       Decays &d = sm.d[r];
       put_sums(d, sums, P.scale, lane);
-      const Log2Parts q0 = Log2Sum{sums.total.whole - sums.g0.whole, sums.total.rest - sums.g0.rest}.parts(sums.spoilt);
-      const Log2Parts q1 = Log2Sum{sums.total.whole - sums.g1.whole, sums.total.rest - sums.g1.rest}.parts(sums.spoilt);
+      const Log2Parts q0 = (sums.total - sums.g0).parts(sums.spoilt), q1 = (sums.total - sums.g1).parts(sums.spoilt);
       *reinterpret_cast<float2 *>(&d.left[2 * lane]) = make_float2(2 * lane < m ? q0.power() : 0.0f, 2 * lane + 1 < m ? q1.power() : 0.0f);
       if (lane == 0) d.lam = sums.total.parts(sums.spoilt).power();
       if constexpr (F16) {  // K' divided by the power of two that its largest finite value asks for, as these factors go into it
@@ -489,10 +484,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       warp_arrive(&sm.dec_full[r], lane);
     }
-    if (!OUT && lane == 0 && dv0 == 0) {  // (segments of many chunks: the sums in 64 bits, the whole part no further than fp32's exponents)
-      whole += rest >> kLog2Bits;
-      rest &= (1 << kLog2Bits) - 1;
-      const Log2Sum all_of{forgot ? -4096 : static_cast<int>(max(-4096ll, min(4096ll, whole))), static_cast<int>(rest)};
+    if (!OUT && lane == 0 && dv0 == 0) {  // (the whole part no further than fp32's exponents)
+      const Log2Sum all_of{((forgot ? -4096ll : max(-4096ll, min(4096ll, whole))) << kLog2Bits) + rest};
       A.total[(static_cast<int64_t>(b) * P.heads + h) * A.slots() + piece] = all_of.parts(lost).power();
     }
   } else if (warp == 10) {
@@ -912,7 +905,7 @@ struct ShortSmall {
   uint32_t follows[kChunk][2];  // the rows that a row follows, itself among them
   uint32_t smax[2][128], amax[2][kChunk];
   int parent[kChunk];
-  float g[kChunk];
+  long long units[kChunk];  // the nodes' decays
   uint64_t full, p_full, o1_full, o2_full;
   uint32_t tmem;
   int dead;
@@ -982,26 +975,26 @@ __global__ void __launch_bounds__(kShortThreads, 2)
       const float *gp = P.decay + b * P.gs[0] + h * P.gs[2];
       ChunkSums sums;
       if (P.parents) {  // over each row's path, and which rows lie on it
-        for (int i = lane; i < m; i += 32) {
-          sm.parent[i] = P.parents[static_cast<int64_t>(b) * P.n + i];
-          sm.g[i] = gp[i * P.gs[1]];
+        uint32_t nan[2];
+        for (int e = 0; e < 2; ++e) {
+          const int i = lane + 32 * e;
+          const float x = i < m ? gp[i * P.gs[1]] : 0.0f;
+          if (i < m) sm.parent[i] = P.parents[static_cast<int64_t>(b) * P.n + i], sm.units[i] = log2_of(x).units;
+          nan[e] = __ballot_sync(~0u, x != x);
         }
         __syncwarp();
         for (int e = 0; e < 2; ++e) {
           const int i = 2 * lane + e;
           uint32_t bits[2] = {0, 0};
-          Log2Sum path{0, 0};
-          bool bad = false;
+          Log2Sum path{0};
           if (i < m) {
             for (int p = i; p >= 0; p = sm.parent[p]) {
-              const float x = sm.g[p];
-              path += log2_of(x);
-              bad |= x != x;
+              path += Log2Sum{sm.units[p]};
               bits[p >> 5] |= 1u << (p & 31);
             }
           }
           sm.follows[i][0] = bits[0], sm.follows[i][1] = bits[1];
-          (e ? sums.g1 : sums.g0) = path, (e ? sums.bad1 : sums.bad0) = bad;
+          (e ? sums.g1 : sums.g0) = path, (e ? sums.bad1 : sums.bad0) = bits[0] & nan[0] || bits[1] & nan[1];
         }
       } else {
         sums = chunk_sums(2 * lane < m ? gp[2 * lane * P.gs[1]] : 0.0f, 2 * lane + 1 < m ? gp[(2 * lane + 1) * P.gs[1]] : 0.0f, lane);

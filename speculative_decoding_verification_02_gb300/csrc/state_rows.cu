@@ -224,17 +224,12 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
     __syncthreads();
     if (MODE != kTree) {
       // ---- decays: every warp the sums it needs, the first the factors
-      Log2Sum upto = lane < m ? log2_of(gs[side][lane]) : Log2Sum{0, 0};
+      const Log2Sum upto = running<kBlock>(lane < m ? log2_of(gs[side][lane]) : Log2Sum{0}, lane);
       const uint32_t nan = __ballot_sync(~0u, lane < m && gs[side][lane & 15] != gs[side][lane & 15]);
-#pragma unroll
-      for (int o = 1; o < kBlock; o <<= 1) {
-        const Log2Sum y{__shfl_up_sync(~0u, upto.whole, o), __shfl_up_sync(~0u, upto.rest, o)};
-        if (lane >= o) upto += y;
-      }
-      const Log2Sum all{__shfl_sync(~0u, upto.whole, m - 1), __shfl_sync(~0u, upto.rest, m - 1)};
+      const Log2Sum all = of_lane(upto, m - 1);
       if (warp == 0 && lane < m) {
         from_state[lane] = upto.parts(nan & ((2u << lane) - 1)).power() * (MODE == kChain ? P.scale : 1.0f);
-        left[lane] = Log2Sum{all.whole - upto.whole, all.rest - upto.rest}.parts(nan >> lane >> 1).power();
+        left[lane] = (all - upto).parts(nan >> lane >> 1).power();
         if (lane == m - 1) total = all.parts(nan).power();
       }
       if constexpr (MODE == kChain) {
@@ -253,18 +248,17 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
             }
           }
           for (int o = 1 << shift; o < 32; o <<= 1) s += __shfl_xor_sync(~0u, s, o);
-          const int w = __shfl_sync(~0u, upto.whole, i), r = __shfl_sync(~0u, upto.rest, i);
-          const int wj = __shfl_sync(~0u, upto.whole, j), rj = __shfl_sync(~0u, upto.rest, j);
+          const Log2Sum after = of_lane(upto, i) - of_lane(upto, j);
           // (tokens j + 1 to i)
           const bool lost = nan & ((2u << i) - 1) & ~((2u << j) - 1);
-          if (lane >> shift == 0) pair[i][j] = j <= i ? s * Log2Sum{w - wj, r - rj}.parts(lost).power() * P.scale : 0.0f;
+          if (lane >> shift == 0) pair[i][j] = j <= i ? s * after.parts(lost).power() * P.scale : 0.0f;
         }
       }
       __syncthreads();
     } else {
       if (tid < m) {  // the row's path from itself up, and the decays that lie before each node of it
         int len = 0;
-        Log2Sum sum{0, 0};
+        Log2Sum sum{0};
         bool nan = false;
         for (int p = t0 + tid; p >= 0; p = parents[p]) {
           path[tid][len] = p;

@@ -201,6 +201,29 @@ def test_forgotten_stays_forgotten(api, kind, dtype, forget):
         assert not out[((torch.tensor(c.depth) >= 3) & (torch.tensor(c.depth) <= 5)).cuda()].any()
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("n", [8192, 16384])
+def test_constant_decays(api, dtype, n):
+    """One decay for all tokens, whose rounding is the same for each and adds up over all of them.  A chunk's factor is one fp32
+    power, off by 2^-22 at most (two units in the last place): a term that is m chunks old is off by m 2^-22, n / 128 on average;
+    and 2^-20 for all else.  A token's decay in units of 2^-25 log 2 would be off by up to 1e-8, n / 2 of them on average."""
+    H, D = 8, 64
+    g = torch.Generator().manual_seed(n)
+    # 0.45 of such a unit beside a whole number of them, tokens that stay for the whole length or a tenth of it
+    units = torch.tensor([3.0, 17.0, 40.0, 48.0, 300.0, 1000.0, 4000.0, 10000.0], dtype=torch.float64) + 0.45
+    decay = (-units * 2.0 ** -25 * 0.6931471805599453).float()
+    k = (torch.randn(1, n, H, D, generator=g) / 8).to(dtype)
+    v = torch.randn(1, n, H, D, generator=g).to(dtype)
+    pool = torch.zeros(1, H, D, D, device="cuda")
+    api.spec_state_forward(k.cuda(), k.cuda(), v.cuda(), decay.cuda().expand(1, n, H), None, dst=pool)
+    age = torch.arange(n - 1, -1, -1, dtype=torch.float64)
+    for h in range(H):
+        w = torch.exp(age * decay[h].double())
+        want = (k[0, :, h].double() * w[:, None]).T @ v[0, :, h].double()
+        off = float((pool[0, h].double().cpu() - want).norm() / want.norm())
+        assert off <= n / 128 * 2.0 ** -22 + 2.0 ** -20, (h, off)
+
+
 # ------------------------------------------------------------------ fp16's scales, and what is no number
 
 @pytest.mark.parametrize("large", [3e4, float("inf")])
