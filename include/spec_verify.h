@@ -581,6 +581,9 @@ size_t spec_cache_workspace_size(int op, const spec_cache *cache, int B, int N, 
  *               below -120 (-inf among them) is a factor of 0, which forgets every
  *               finite thing before the token.  One above 120 may count as 120
  *               (e^120 = 1e52: in fp32 such a factor is infinite).
+ *               A state may grow by any factor; what a token adds, by e^70 at
+ *               most over the 64 tokens (or the path of a tree) behind it:
+ *               beyond, a 0 in k or v may become NaN, a small term infinite.
  * status[b] (out int32 [B] or NULL): SPEC_STATUS_BAD_LENGTH (a count out of
  * range), SPEC_STATUS_BAD_SLOT (a slot outside the pool), SPEC_STATUS_BAD_INDEX
  * or SPEC_STATUS_BAD_TREE.  Such a request's state is not written and its rows

@@ -14,6 +14,9 @@
 
 namespace sv {
 
+// Bits of a decay's fraction in fixed point (units of log 2).
+constexpr int kLog2Bits = 40;
+
 struct StatePool {
   float *state;  // null: states of zeros (read), or none to write
   int64_t slot_stride;
@@ -30,7 +33,8 @@ struct StateParams {
   int dtype, B, n, n_rows, index_stride;
   const float *decay;
   const int32_t *counts, *parents, *index;
-  float scale;
+  float scale, scale_log2;  // |scale| < 2^scale_log2, which is not below 0
+  int64_t most_units;       // of a decay of the state's that one factor holds beside the scale: 2^-40ths of log 2
   int32_t *status;
   bool vec;  // rows of q, k, v and out start on 16-byte boundaries
 };
@@ -42,7 +46,7 @@ struct StateChunkPlan {
   int segs, parts, pieces;  // pieces: of a request, a launch's
   int *verdict;   // [B] the requests' status
   int *order;     // [B] the requests, longest first
-  float *total;   // [B][heads][slots] the decay over a part
+  float2 *total;  // [B][heads][slots] the decay over a part: whole units of log 2, rest
   float *local;   // [B][heads][slots][key_dim][value_dim] what a part adds to zeros; then, where a run begins, the state before it
   __host__ __device__ int slots() const { return (segs - 1) * parts + 1; }
 };
@@ -133,7 +137,6 @@ __device__ __forceinline__ uint16_t narrow(float x) {
 // token's is off by one of them (1e-12, which a decay that is the same for a
 // million tokens adds up to 1e-6), sums and differences not at all, however
 // large: what 64-bit floats would do at many times the cost.
-constexpr int kLog2Bits = 40;
 struct Log2Parts {
   float hi, lo;  // a whole number and a rest in [-1/2, 1/2]
   __device__ __forceinline__ float power() const {  // 2^(hi + lo); 0 below the least normal number
@@ -142,6 +145,18 @@ struct Log2Parts {
     return hi > 127.0f ? INFINITY : f * __uint_as_float(static_cast<uint32_t>(static_cast<int>(hi) + 127) << 23);
   }
 };
+// scale 2^(hi + lo), by which sums over the state are multiplied, in two finite
+// factors, so that a state of zeros stays one and a small one grows to what it
+// should: the second is 1 unless the first alone would be no number.
+// scale_log2: 0 or above, scale is below its power of two.
+__device__ __forceinline__ float state_factor(const Log2Parts &p, float scale, float scale_log2, float &second) {
+  second = 1.0f;
+  if (!(p.hi + scale_log2 > 126.0f)) [[likely]] return p.power() * scale;
+  const int half = min(127, (static_cast<int>(p.hi + scale_log2) + 1) >> 1);
+  const float hi = p.hi - static_cast<float>(half);
+  second = __uint_as_float(static_cast<uint32_t>(half + 127) << 23);
+  return Log2Parts{fminf(hi, 127.0f), p.lo}.power() * scale;
+}
 struct Log2Sum {
   long long units;
   __device__ __forceinline__ Log2Sum &operator+=(const Log2Sum &x) {

@@ -76,6 +76,13 @@ int check_call(StateParams &P, const spec_state *from, const spec_state *to, con
   return SPEC_OK;
 }
 
+void set_scale(StateParams &P, float scale) {
+  int e = 0;
+  std::frexp(scale, &e);
+  P.scale = scale, P.scale_log2 = static_cast<float>(std::max(e, 0));
+  P.most_units = static_cast<int64_t>(126 - std::max(e, 0)) * (int64_t{1} << kLog2Bits);
+}
+
 int run(const StateParams &P, void *workspace, size_t workspace_bytes, void *stream, const char *what) {
   const bool chunks = state_on_tensor_cores(P);
   if (chunks && (!workspace || workspace_bytes < state_chunk_workspace(P) || !on_grain(workspace, 256))) return SPEC_EWORKSPACE;
@@ -109,7 +116,8 @@ int spec_state_forward(const spec_state *from, const spec_state *to, const void 
   if (rc != SPEC_OK) return rc;
   if (!std::isfinite(scale)) return SPEC_EINVAL;
   if (B == 0) return SPEC_OK;
-  P.counts = counts, P.scale = scale, P.status = status;
+  P.counts = counts, P.status = status;
+  set_scale(P, scale);
   return run(P, workspace, workspace_bytes, stream, "spec_state_forward");
 }
 
@@ -124,7 +132,8 @@ int spec_state_attend(const spec_state *from, const void *q, const int64_t *q_st
   if (rc != SPEC_OK) return rc;
   if (!std::isfinite(scale) || N > SPEC_MAX_NODES) return SPEC_EINVAL;
   if (B == 0) return SPEC_OK;
-  P.counts = n_query, P.parents = parents, P.scale = scale, P.status = status;
+  P.counts = n_query, P.parents = parents, P.status = status;
+  set_scale(P, scale);
   return run(P, workspace, workspace_bytes, stream, "spec_state_attend");
 }
 
@@ -139,6 +148,7 @@ int spec_state_commit(const spec_state *from, const spec_state *to, const void *
   if (!P.to.state || n_rows < 0 || (index ? n_rows > index_stride : n_rows != n)) return SPEC_EINVAL;
   if (B == 0) return SPEC_OK;
   P.index = index, P.index_stride = index_stride, P.n_rows = n_rows, P.counts = counts, P.status = status;
+  set_scale(P, 1.0f);
   const cudaError_t e = launch_state_rows(P, stream_of(stream));
   return e == cudaSuccess ? SPEC_OK : state_fail(e, "spec_state_commit");
 }

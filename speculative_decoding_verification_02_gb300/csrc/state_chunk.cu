@@ -64,13 +64,15 @@ __global__ void __launch_bounds__(256) state_join_kernel(const StateChunkPlan A)
     if (slot >= 0) s = *reinterpret_cast<const float4 *>(P.from.state + slot * P.from.slot_stride + static_cast<int64_t>(h) * size + e);
   }
   float *p = A.local + static_cast<int64_t>(unit) * A.slots() * size + e;
-  const float *f = A.total + static_cast<int64_t>(unit) * A.slots();
+  const float2 *f = A.total + static_cast<int64_t>(unit) * A.slots();
   float4 ahead = *reinterpret_cast<const float4 *>(p);
   for (int g = 0; g + 1 < A.slots(); ++g, p += size) {
     const float4 x = ahead;
     if (g + 2 < A.slots()) ahead = *reinterpret_cast<const float4 *>(p + size);
     if (g % A.parts == 0) *reinterpret_cast<float4 *>(p) = s;
-    s = make_float4(fmaf(s.x, f[g], x.x), fmaf(s.y, f[g], x.y), fmaf(s.z, f[g], x.z), fmaf(s.w, f[g], x.w));
+    float more;
+    const float w = state_factor(Log2Parts{f[g].x, f[g].y}, 1.0f, 0.0f, more);
+    s = make_float4(fmaf(s.x * more, w, x.x), fmaf(s.y * more, w, x.y), fmaf(s.z * more, w, x.z), fmaf(s.w * more, w, x.w));
   }
   *reinterpret_cast<float4 *>(p) = s;
 }
@@ -118,7 +120,7 @@ std::pair<StateChunkPlan, size_t> chunk_plan(const StateParams &P, void *workspa
   };
   A.verdict = reinterpret_cast<int *>(take(P.B * sizeof(int)));
   A.order = reinterpret_cast<int *>(take(P.B * sizeof(int)));
-  A.total = reinterpret_cast<float *>(take(per_head * sizeof(float)));
+  A.total = reinterpret_cast<float2 *>(take(per_head * sizeof(float2)));
   A.local = reinterpret_cast<float *>(take(per_head * P.key_dim * P.value_dim * sizeof(float)));
   return {A, at};
 }

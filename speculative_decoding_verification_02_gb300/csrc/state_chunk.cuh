@@ -94,11 +94,12 @@ struct ChunkShape {
 
 struct alignas(16) Decays {
   float nhi[kChunk], nlo[kChunk];  // minus the running sum in units of log 2: multiples of 1/8, rest
-  float ei[kChunk];                // scale e^{G_i}
+  float ei[kChunk], more[kChunk];  // scale e^{G_i}: the product of both; more is written where grows is true, else all are 1
   float left[kChunk];              // e^{G_last - G_j}, 0 past the request's rows
   float afac[kChunk];              // fp16: what row i of A was divided by
   float sfac[128];                 // fp16: what a lane of S was divided by
-  float lam;                       // e^{G_last}
+  float lam, lam_more;             // e^{G_last}: the product of both
+  int grows;
   float kfac;                      // fp16: what K' was divided by
 };
 
@@ -231,11 +232,15 @@ __device__ __forceinline__ ChunkSums chunk_sums(float x0, float x1, int lane) {
   return s;
 }
 
-__device__ __forceinline__ void put_sums(Decays &d, const ChunkSums &s, float scale, int lane) {
+__device__ __forceinline__ void put_sums(Decays &d, const ChunkSums &s, float scale, float scale_log2, int lane) {
   const Log2Parts p0 = s.g0.parts(s.bad0), p1 = s.g1.parts(s.bad1);
   *reinterpret_cast<float2 *>(&d.nhi[2 * lane]) = make_float2(-p0.hi, -p1.hi);
   *reinterpret_cast<float2 *>(&d.nlo[2 * lane]) = make_float2(-p0.lo, -p1.lo);
-  *reinterpret_cast<float2 *>(&d.ei[2 * lane]) = make_float2(p0.power() * scale, p1.power() * scale);
+  float2 more;
+  *reinterpret_cast<float2 *>(&d.ei[2 * lane]) = make_float2(state_factor(p0, scale, scale_log2, more.x), state_factor(p1, scale, scale_log2, more.y));
+  const bool grows = __any_sync(~0u, more.x != 1.0f || more.y != 1.0f);
+  if (grows) [[unlikely]] *reinterpret_cast<float2 *>(&d.more[2 * lane]) = more;
+  if (lane == 0) d.grows = grows;
 }
 
 // 32 weights of a row of A from what P's product left in tensor memory: scale P e^{G_i - G_j}, 0 for rows that it does not follow
@@ -467,10 +472,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       lost |= sums.spoilt, forgot |= sums.total.units < kForgets / 2;
       if (c >= kDecayRing && !warp_wait(&sm.dec_empty[r], (c / kDecayRing - 1) & 1, dead)) break;
       Decays &d = sm.d[r];
-      put_sums(d, sums, P.scale, lane);
+      put_sums(d, sums, P.scale, P.scale_log2, lane);
       const Log2Parts q0 = (sums.total - sums.g0).parts(sums.spoilt), q1 = (sums.total - sums.g1).parts(sums.spoilt);
       *reinterpret_cast<float2 *>(&d.left[2 * lane]) = make_float2(2 * lane < m ? q0.power() : 0.0f, 2 * lane + 1 < m ? q1.power() : 0.0f);
-      if (lane == 0) d.lam = sums.total.parts(sums.spoilt).power();
+      if (lane == 0) d.lam = state_factor(sums.total.parts(sums.spoilt), 1.0f, 0.0f, d.lam_more);
       if constexpr (F16) {  // K' divided by the power of two that its largest finite value asks for, as these factors go into it
         if (!wait4(sm.full, c)) break;
         const char *keys = smem + S::kK + c % S::kStagesK * S::kTileK;
@@ -486,7 +491,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     if (!OUT && lane == 0 && dv0 == 0) {  // (the whole part no further than fp32's exponents)
       const Log2Sum all_of{((forgot ? -4096ll : max(-4096ll, min(4096ll, whole))) << kLog2Bits) + rest};
-      A.total[(static_cast<int64_t>(b) * P.heads + h) * A.slots() + piece] = all_of.parts(lost).power();
+      const Log2Parts p = all_of.parts(lost);
+      A.total[(static_cast<int64_t>(b) * P.heads + h) * A.slots() + piece] = make_float2(p.hi, p.lo);
     }
   } else if (warp == 10) {
     // ---- issuing O1 and O2
@@ -700,6 +706,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           tc_fence_after();
           const float lam = sm.d[r].lam, kf = F16 ? sm.d[r].kfac : 1.0f;
           const pair_t l2 = pack2(lam, lam), k2 = pack2(kf, kf);
+          if (sm.d[r].grows) [[unlikely]] {
+            const pair_t more = pack2(sm.d[r].lam_more, sm.d[r].lam_more);
+#pragma unroll
+            for (int e = 0; e < OWN / 2; ++e) s[e] = mul2(s[e], more);
+          }
 #pragma unroll
           for (int k = 0; k < OWN / 16; ++k) {
             float x[16];
@@ -808,7 +819,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           put_outputs<DT>(o1_of(c) + lanes, tmem + lanes + kO2, d, k, m, sf, sm.stage[quarter][0], o, P.os[1],
                           dv0 + col < P.value_dim, bad);
         const float2 b2 = unpack2(bad);
-        if (__any_sync(~0u, !(b2.x == 0.0f && b2.y == 0.0f))) [[unlikely]] {  // a row's sum that is no number: without the rows that it does not follow
+        if (__any_sync(~0u, !(b2.x == 0.0f && b2.y == 0.0f)) || d.grows) [[unlikely]] {  // a row's sum that is no number: without the rows that it does not follow
 #pragma unroll 1
           for (int i = 0; i < m; ++i) {
             const uint64_t sees = (2ull << i) - 1;
@@ -818,7 +829,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             float v = x[0];
 #pragma unroll
             for (int e = 1; e < 8; ++e) v = (i & 7) == e ? x[e] : v;
-            v = fmaf(v, d.ei[i] * sf, row_again<DT>(P, d, sees, b, h, t0, i, dv) * P.scale);
+            v = fmaf(d.grows ? v * d.more[i] : v, d.ei[i] * sf, row_again<DT>(P, d, sees, b, h, t0, i, dv) * P.scale);
             if (dv < P.value_dim) out[(t0 + i) * P.os[1]] = narrow<DT>(v);
           }
         }
@@ -1003,7 +1014,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
           sm.follows[2 * lane + e][0] = static_cast<uint32_t>(bits), sm.follows[2 * lane + e][1] = static_cast<uint32_t>(bits >> 32);
         }
       }
-      put_sums(sm.d, sums, P.scale, lane);
+      put_sums(sm.d, sums, P.scale, P.scale_log2, lane);
     }
     float sf = 1.0f;
     if constexpr (F16) {
@@ -1129,7 +1140,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
       for (int k = half * 32; k < half * 32 + 32 && k < m; k += 16)
         put_outputs<DT>(tmem + lanes + kO1, tmem + lanes + kP, sm.d, k, m, sf, sm.stage[warp][0], o, P.os[1], dv0 + col < P.value_dim, bad);
       const float2 b2 = unpack2(bad);
-      if (__any_sync(~0u, !(b2.x == 0.0f && b2.y == 0.0f))) [[unlikely]] {  // as in the kernel above
+      if (__any_sync(~0u, !(b2.x == 0.0f && b2.y == 0.0f)) || sm.d.grows) [[unlikely]] {  // as in the kernel above
 #pragma unroll 1
         for (int r = half * 32; r < min(m, half * 32 + 32); ++r) {
           float x[8];
@@ -1139,7 +1150,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
 #pragma unroll
           for (int e = 1; e < 8; ++e) v = (r & 7) == e ? x[e] : v;
           const uint64_t sees = static_cast<uint64_t>(sm.follows[r][1]) << 32 | sm.follows[r][0];
-          v = fmaf(v, sm.d.ei[r] * sf, row_again<DT>(P, sm.d, sees, b, h, 0, r, dv) * P.scale);
+          v = fmaf(sm.d.grows ? v * sm.d.more[r] : v, sm.d.ei[r] * sf, row_again<DT>(P, sm.d, sees, b, h, 0, r, dv) * P.scale);
           if (dv < P.value_dim) reinterpret_cast<uint16_t *>(P.out)[b * P.os[0] + r * P.os[1] + h * P.os[2] + dv] = narrow<DT>(v);
         }
       }

@@ -110,9 +110,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
   __shared__ __align__(16) char ks[MODE == kTree ? 1 : kBlock][MODE == kTree ? 16 : Tile::kStride];
   __shared__ __align__(16) uint16_t vs[MODE == kTree ? 1 : kBlock][kMaxWarps * 16];
   __shared__ float gs[2][kBlock], left[kBlock], from_state[kBlock];
-  __shared__ float total;
+  __shared__ float total, more;
   __shared__ float pair[MODE == kChain ? kBlock : 1][kBlock];
-  __shared__ float path_w[MODE == kTree ? kBlock : 1][kMaxPath];
+  __shared__ float path_w[MODE == kTree ? kBlock : 1][kMaxPath], path_more[kBlock];
   __shared__ int path[MODE == kTree ? kBlock : 1][kMaxPath], path_len[kBlock];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
@@ -217,20 +217,25 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
   if (status != SPEC_STATUS_OK) count = 0;
 
 #pragma unroll 1
-  for (int t0 = 0; t0 < count; t0 += kBlock) {
-    const int m = min(kBlock, count - t0), side = t0 / kBlock & 1;
+  for (int t0 = 0, m, side = 0; t0 < count; t0 += m, side ^= 1) {
+    m = min(kBlock, count - t0);
     if (t0 > 0) fetch(t0, m, side);
     cp_async_wait_all();
     __syncthreads();
     if (MODE != kTree) {
       // ---- decays: every warp the sums it needs, the first the factors
       const Log2Sum upto = running<kBlock>(lane < m ? log2_of(gs[side][lane]) : Log2Sum{0}, lane);
-      const uint32_t nan = __ballot_sync(~0u, lane < m && gs[side][lane & 15] != gs[side][lane & 15]);
+      uint32_t nan = __ballot_sync(~0u, lane < m && gs[side][lane & 15] != gs[side][lane & 15]);
+      // growth that no factor of the state's can hold: a token alone, the state first by one part of its factor
+      const bool grows = __any_sync(~0u, lane < m && upto.units > P.most_units);
+      if (grows) [[unlikely]] m = 1, nan &= 1;
       const Log2Sum all = of_lane(upto, m - 1);
       if (warp == 0 && lane < m) {
-        from_state[lane] = upto.parts(nan & ((2u << lane) - 1)).power() * (MODE == kChain ? P.scale : 1.0f);
+        const Log2Parts p = upto.parts(nan & ((2u << lane) - 1));
+        float second;
+        from_state[lane] = state_factor(p, MODE == kChain ? P.scale : 1.0f, P.scale_log2, second);
         left[lane] = (all - upto).parts(nan >> lane >> 1).power();
-        if (lane == m - 1) total = all.parts(nan).power();
+        if (lane == m - 1) total = state_factor(p, 1.0f, P.scale_log2, second), more = second;
       }
       if constexpr (MODE == kChain) {
         // ---- the pairs' weights: a row to a warp, a token before it to 2, 4 or 8 lanes, each of its share of key_dim's pieces
@@ -255,6 +260,13 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
         }
       }
       __syncthreads();
+      if (grows) [[unlikely]] {
+        const pair_t f2 = pack2(more, more);
+#pragma unroll
+        for (int r = 0; r < RPL / 2; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[r][e] = mul2(S[r][e], f2);
+      }
     } else {
       if (tid < m) {  // the row's path from itself up, and the decays that lie before each node of it
         int len = 0;
@@ -268,7 +280,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
           sum += log2_of(x), nan |= x != x;
         }
         path_len[tid] = len;
-        from_state[tid] = sum.parts(nan).power() * P.scale;
+        from_state[tid] = state_factor(sum.parts(nan), P.scale, P.scale_log2, path_more[tid]);
       }
       __syncthreads();
       for (int i = 0; i < m; ++i) {
@@ -329,7 +341,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
       } else {
 #pragma unroll 1
         for (int i = 0; i < m; ++i) {
-          float sum = group_sum(row_product<DT, RPL>(qs[i], g, S), g) * from_state[i], terms = 0.0f;
+          float sum = group_sum(row_product<DT, RPL>(qs[i], g, S), g) * path_more[i] * from_state[i], terms = 0.0f;
           for (int p = g & 1; p < path_len[i]; p += 2) {
             const uint16_t v = *reinterpret_cast<const uint16_t *>(vp + (static_cast<int64_t>(path[i][p]) * P.vs[1] + col0 + col) * 2);
             terms = fmaf(path_w[i][p], widen<DT>(v), terms);
@@ -342,7 +354,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
     }
 
     // ---- the state behind the block
-    if (MODE != kTree && live && (P.to.state || t0 + kBlock < count)) {
+    if (MODE != kTree && live && (P.to.state || t0 + m < count)) {
       const pair_t f2 = pack2(total, total);
 #pragma unroll
       for (int r = 0; r < RPL / 2; ++r)
@@ -365,7 +377,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
         }
       }
     }
-    if (t0 + kBlock < count) __syncthreads();  // before the next block's rows
+    if (t0 + m < count) __syncthreads();  // before the next block's rows
   }
   cp_async_wait_all();
 

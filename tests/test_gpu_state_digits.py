@@ -202,6 +202,53 @@ def test_forgotten_stays_forgotten(api, kind, dtype, forget):
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("n", [60, 1300, 3001])
+def test_forgotten_before_long_growth(api, dtype, n):
+    """A reset in one part of a long prompt and growth in all that follow: without keys, a state of zeros and outputs of zeros."""
+    c = Call("chunk", dtype, 64, 43)
+    c.q, c.k, c.v, c.g = (x[:1].repeat(n, 1, 1) if x.dim() == 3 else x[:1].repeat(n, 1) for x in (c.q, c.k, c.v, c.g))
+    c.g[40] = -float("inf")
+    c.g[41:] = 0.5
+    c.k[40:] = 0
+    c.n = n
+    out, state = c.run(api)
+    assert not state.any() and not out[40:].any()
+    assert bool(out[:40].any(-1).all())
+
+
+@pytest.mark.parametrize("size", [0.0, 1e-30])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_state_that_grows(api, kind, dtype, size):
+    """The state times e^115, which is no fp32 number: zeros stay zeros, a small state becomes what it should."""
+    c = Call(kind, dtype, 64, 44)
+    c.S0 *= size
+    d = torch.tensor(c.depth)
+    c.g[d == 0] = 60.0
+    c.g[(d > 0) & (d < 12)] = 5.0
+    out, state = c.run(api)
+    outs, last = c.want()
+    if state is not None:
+        assert bool(state.isfinite().all())
+        ref.check_state(state, last, c.n, c.n)
+    if out is not None and dtype == BF:  # (fp16 has no such outputs)
+        ref.check_out(out, outs, c.D, c.n, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_two_tokens_of_growth(api, dtype):
+    """A fresh request, two factors of e^50: k_1 v_1 e^50 + k_2 v_2, whichever kernel."""
+    for n in (2, 20, 70):
+        c = Call("chunk", dtype, 128, 45)
+        c.q, c.k, c.v, c.g = c.q[:n], c.k[:n], c.v[:n], torch.zeros(n, 2)
+        c.g[:2] = 50.0
+        c.n, c.parents = n, ref.chain(n)
+        c.S0 *= 0
+        _, state = c.run(api)
+        ref.check_state(state, c.want()[1], n, n)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("n", [8192, 16384])
 def test_constant_decays(api, dtype, n):
     """One decay for all tokens, whose rounding is the same for each and adds up over all of them.  A chunk's factor is one fp32
