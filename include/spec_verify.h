@@ -584,6 +584,9 @@ size_t spec_cache_workspace_size(int op, const spec_cache *cache, int B, int N, 
  *               A state may grow by any factor; what a token adds, by e^70 at
  *               most over the 64 tokens (or the path of a tree) behind it:
  *               beyond, a 0 in k or v may become NaN, a small term infinite.
+ * Infinities and NaN in the state, q, k, v or decay: outputs and states are
+ * finite where the recurrence's are; where it gives an infinity, some calls
+ * give NaN (a product takes its operands in pieces).
  * status[b] (out int32 [B] or NULL): SPEC_STATUS_BAD_LENGTH (a count out of
  * range), SPEC_STATUS_BAD_SLOT (a slot outside the pool), SPEC_STATUS_BAD_INDEX
  * or SPEC_STATUS_BAD_TREE.  Such a request's state is not written and its rows

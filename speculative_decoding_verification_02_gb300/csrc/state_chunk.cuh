@@ -820,6 +820,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                           dv0 + col < P.value_dim, bad);
         const float2 b2 = unpack2(bad);
         if (__any_sync(~0u, !(b2.x == 0.0f && b2.y == 0.0f)) || d.grows) [[unlikely]] {  // a row's sum that is no number: without the rows that it does not follow
+          __syncwarp();  // (other lanes' stores of the same rows)
 #pragma unroll 1
           for (int i = 0; i < m; ++i) {
             const uint64_t sees = (2ull << i) - 1;
@@ -1141,6 +1142,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
         put_outputs<DT>(tmem + lanes + kO1, tmem + lanes + kP, sm.d, k, m, sf, sm.stage[warp][0], o, P.os[1], dv0 + col < P.value_dim, bad);
       const float2 b2 = unpack2(bad);
       if (__any_sync(~0u, !(b2.x == 0.0f && b2.y == 0.0f)) || sm.d.grows) [[unlikely]] {  // as in the kernel above
+        __syncwarp();
 #pragma unroll 1
         for (int r = half * 32; r < min(m, half * 32 + 32); ++r) {
           float x[8];

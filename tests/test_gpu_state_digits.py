@@ -319,3 +319,51 @@ def test_states_next_to_the_largest_number(api, n, write):
     want = torch.stack([S[0, 0, i % D].double() * 2.0 ** -10 for i in range(n)])
     worst = ((o["out"][0, :, 0].double().cpu() - want).abs() / want.abs()).max()
     assert float(worst) <= 2.0 ** -8 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("where", ["state", "k", "v", "q", "g"])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("kind", KINDS)
+def test_no_numbers_where_the_recurrence_has_none(api, kind, dtype, value, where):
+    """An infinity or a NaN: outputs and states are finite where the recurrence's are, and only there."""
+    if where == "g" and value == -float("inf"):
+        pytest.skip("a factor of 0 is an ordinary one")
+    c = Call(kind, dtype, 64, 46)
+    at = min(c.n // 2 + 3, c.n - 2)
+    if where == "state":
+        c.S0[1, 7, 20] = value
+    elif where == "g":
+        c.g[at, 1] = value
+    else:
+        getattr(c, where)[at, 0, 20] = value
+    out, state = c.run(api)
+    outs, last = c.want()
+    if state is not None:
+        assert torch.equal(state.isfinite().cpu(), last[0].isfinite())
+        ok = last[0].isfinite()
+        assert float((state.double().cpu() - last[0])[ok].norm() / last[0][ok].norm()) <= 2.0 ** -18
+    if out is not None:
+        assert torch.equal(out.isfinite().cpu(), outs[0].isfinite())
+        ok = outs[0].isfinite()
+        assert float((out.double().cpu() - outs[0])[ok].norm() / outs[0][ok].norm()) <= torch.finfo(dtype).eps
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("n", [60, 150, 1300])
+def test_rows_before_a_spoilt_one(api, n, dtype, D):
+    """Infinities and NaN in a token's k or v: the rows before it as they are without it, prompts cut into segments too."""
+    g = torch.Generator().manual_seed(n + D)
+    q, k, v = (torch.randn(1, n, 1, D, generator=g).to(dtype) for _ in range(3))
+    k = (k.float() / D ** 0.5).to(dtype)
+    decay = -0.2 * torch.rand(1, n, 1, generator=g)
+    S0 = torch.randn(1, D, D, generator=g)
+    outs, _ = ref.walk(q[0], k[0], v[0], decay[0], S0, ref.chain(n), D ** -0.5)
+    for at in (1, 37, n - 30, n - 1):
+        for name in ("k", "v"):
+            x = dict(k=k.clone(), v=v.clone())
+            x[name][0, at, 0, 5], x[name][0, at, 0, 40] = float("inf"), float("nan")
+            got = api.spec_state_forward(q.cuda(), x["k"].cuda(), x["v"].cuda(), decay.cuda(), S0[None].cuda())["out"]
+            ref.check_out(got[0, :at], [y[:at] for y in outs], D, n, dtype)
+            assert bool(got[0, at].isnan().any())
