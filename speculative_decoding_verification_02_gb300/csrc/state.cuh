@@ -139,10 +139,10 @@ __device__ __forceinline__ uint16_t narrow(float x) {
 // large: what 64-bit floats would do at many times the cost.
 struct Log2Parts {
   float hi, lo;  // a whole number and a rest in [-1/2, 1/2]
-  __device__ __forceinline__ float power() const {  // 2^(hi + lo); 0 below the least normal number
-    const float f = exp2f(lo);
-    if (!(hi >= -125.0f)) return hi < 0.0f ? 0.0f : hi + lo;  // (NaN stays)
-    return hi > 127.0f ? INFINITY : f * __uint_as_float(static_cast<uint32_t>(static_cast<int>(hi) + 127) << 23);
+  __device__ __forceinline__ float power() const {  // 2^(hi + lo), subnormal or infinite where fp32 is; NaN stays
+    const int h = static_cast<int>(fminf(fmaxf(hi, -252.0f), 254.0f)), most = min(max(h, -126), 127);
+    const float f = exp2f(lo) * __uint_as_float(static_cast<uint32_t>(most + 127) << 23) * __uint_as_float(static_cast<uint32_t>(h - most + 127) << 23);
+    return hi == hi ? f : hi;
   }
 };
 // scale 2^(hi + lo), by which sums over the state are multiplied, in two finite

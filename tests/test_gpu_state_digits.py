@@ -236,6 +236,29 @@ def test_a_state_that_grows(api, kind, dtype, size):
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("forget,off", [(-87.4, 2.0 ** -18), (-92.0, 2.0 ** -16)])
+def test_a_large_state_all_but_forgotten(api, kind, dtype, forget, off):
+    """A state next to the largest number times a factor next to the least: ordinary numbers.  e^-92 is 2^-132.7, whose digits end at
+    2^-149: half a step is 2^-17.3 of it (e^-87.4, 2^-126.1: 2^-23.9), beside 2^-20 for all else."""
+    c = Call(kind, dtype, 64, 47)
+    d = torch.tensor(c.depth)
+    c.S0 = 1e38 * (1 + torch.rand(c.S0.shape, generator=torch.Generator().manual_seed(1)))
+    c.q = (c.q.float() * 2.0 ** -10).to(dtype)
+    c.k[:] = 0
+    c.g[:] = 0
+    c.g[d == 2] = forget
+    c.q[d < 2] = 0  # (fp16 has no such outputs)
+    out, state = c.run(api)
+    outs, last = c.want()
+    if state is not None:
+        assert bool(((state.double().cpu() - last[0]).abs() <= off * last[0].abs()).all())
+    if out is not None:
+        tol = off * outs[1]
+        assert bool(((out.double().cpu() - outs[0]).abs() <= rounded(outs[0], tol, dtype)).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
 def test_two_tokens_of_growth(api, dtype):
     """A fresh request, two factors of e^50: k_1 v_1 e^50 + k_2 v_2, whichever kernel."""
     for n in (2, 20, 70):
