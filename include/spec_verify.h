@@ -548,7 +548,9 @@ size_t spec_cache_workspace_size(int op, const spec_cache *cache, int B, int N, 
 
 /*
  * Linear attention with a decay for each head, and its state through a
- * rejected draft.
+ * rejected draft.  Layers of a decay alone, one number to a head and token:
+ * one with a delta rule, whose written value depends on the state before it,
+ * or with a decay for each channel, is not served.
  *
  * A layer of this kind keeps, in place of a cache, one fp32 matrix for each
  * head of a request, which its tokens update one after another:
@@ -572,7 +574,10 @@ size_t spec_cache_workspace_size(int op, const spec_cache *cache, int B, int N, 
  *
  * Rows: dtype SPEC_DTYPE_BF16 or SPEC_DTYPE_F16; strides in elements, in the
  * order request, token, head; a head's values are contiguous.  Any strides are
- * served; rows that start on 16-byte boundaries are faster.
+ * served.  Prompts take the tensor cores where key_dim is at most 128, scale
+ * lies between 1e-30 and 1e30, strides are above 0 (of an axis of more than one
+ * entry) and rows start on 16-byte boundaries (every stride a multiple of 8);
+ * else they take some ten times as long.
  *   q, k        key_heads heads (a divisor of heads) of key_dim; state head h
  *               reads key head h / (heads / key_heads).
  *   v           heads heads of value_dim.

@@ -125,14 +125,19 @@ std::pair<StateChunkPlan, size_t> chunk_plan(const StateParams &P, void *workspa
   return {A, at};
 }
 
-// Fewest tokens of a call.  48 heads of 128 x 128, in a graph of calls, the kernel for few rows against these, us (1, 8 and 64
+// Fewest tokens of a call.  48 heads of 128 x 128, bf16, in a graph of calls, the kernel for few rows against these, us (1, 8 and 64
 // requests):
-//   chains, states only read  8 rows 6.6 / 7.6, 13 / 14, 74 / 73; 12 rows 8.0 / 7.7, 16 / 14, 95 / 74.  Of drafts of different lengths
-//                             the one for few rows does those that there are: 9 rows at most, 69 / 75 at 64 requests
-//   trees (a path of rows)    4 rows 8.7 / 8.0, 16 / 15, 111 / 80; 8 rows 16 / 8.6, 28 / 17, 201 / 88
-//   states written            16 tokens 11.5 / 11.7, 27 / 30, 166 / 255; 24: 16 / 11.5, 38 / 30, 238 / 256; 32: 20 / 11.5, 48 / 30,
-//                             303 / 256 (a CTA of the main kernel has an SM to itself, and its start is not hidden: the more units,
-//                             the later it pays)
+//   chains, states only read  8 rows 6.6 / 8.2, 13 / 15, 72 / 82; 9 rows 7.7 / 8.3, 15 / 15, 86 / 83; 12 rows 8.7 / 8.2, 17 / 15, 98 / 83.
+//                             Of drafts of different lengths the one for few rows does those that there are: 9 rows at most
+//                             6.3 / 8.7, 13 / 16, 70 / 84; 12 rows 8.3 / 8.6, 15 / 16, 80 / 85; 16 rows 7.2 / 8.6, 18 / 16, 94 / 85
+//   trees (a path of rows)    4 rows 8.7 / 8.3, 16 / 16, 113 / 84; 8 rows 16 / 8.7, 28 / 16, 202 / 88
+//   states written            16 tokens 12 / 12, 29 / 32, 173 / 256; 24: 17 / 12, 40 / 32, 244 / 257; 32: 21 / 12, 50 / 32, 317 / 257
+//                             (a CTA of the main kernel has an SM to itself, and its start is not hidden: the more units, the later
+//                             it pays)
+// A state of 16 heads of 64 x 64, fp16, is a twelfth of that, and the kernels meet later where there are many:
+//   chains                    12 rows 6.8 / 7.2, 6.9 / 7.4, 14 / 24; 16 rows 8.0 / 7.2, 8.1 / 7.5, 17 / 24; 24 rows 12 / 7.4, 12 / 7.7, 29 / 26
+//   states written            24 tokens 13 / 10, 13 / 10, 33 / 55; 64: 29 / 10, 30 / 10, 78 / 55
+// n is the padded length: of a batch whose requests have few of it, the one for few rows does those that there are.
 int fewest_tokens(const StateParams &P) {
   if (P.parents) return 4;
   if (is_short(P)) return P.counts ? 12 : 9;

@@ -29,9 +29,10 @@ namespace {
 // of two (one for a lane of S, a row of A, a chunk's K') that brings the
 // largest of them to 2^14: they leave out 2^-23 of a value, or 2^-39 of that
 // largest where a value is less than 2^-16 of it.  The smallest pieces are added
-// first, since the accumulator cuts off: after 500 chunks a state is 3.6e-7
+// first, since the accumulator cuts off: after 500 chunks a state is 2.3e-7
 // off on the whole (two pieces of K' in bf16: 2.4e-6; 32-bit sums: 1.8e-7),
-// and bf16 outputs are as near to the plain form's as those of 32-bit sums.
+// and bf16 outputs are as near to the plain form's as those of 32-bit sums
+// (4e-5 in the root of squares; with two pieces of S and A 1e-4).
 //
 // e^{G_i - G_j} is taken from differences of running sums in fixed point,
 // handed on as whole units of log 2 and a rest, so that a difference of large
@@ -41,17 +42,17 @@ namespace {
 // and their scheduler): 2 loads, 3 decays, 10 issues O1 and O2, 11 issues P and dS;
 // 4, 5, 8, 9 make A; 0, 1, 6, 7 write the outputs; 12 to 27 hold S, and make K'
 // kAhead chunks ahead: with outputs, those of the two schedulers that have no
-// warps with A (a document 671 us with all of them, 623 so).  The code of the roles is kept short, one site to each and
-// loops rolled where registers allow: unrolled further, warps waited for their
-// instructions (a chunk 7,700 cycles, not 5,300).
+// warps with A (a document 671 us with all of them, 623 so).  The code of the
+// roles is kept short, one site to each and loops rolled where registers allow:
+// unrolled further, warps waited for their instructions.
 //
 // One request of 32,003 tokens, 48 heads of 128 x 128 (three to a key head), in
-// a graph of calls: 574 us, of which this kernel takes 398 on 144 SMs (2.4 us a
-// chunk, some 3,900 cycles) and the launch before it 176; the bytes are 156 us
-// at the copy rate.  A chunk's products take 2,200 cycles of the tensor pipe
-// when nothing waits; 9,300 instructions of the warps around them, a quarter of
-// which are S's pieces, use 60% of the issue slots.
-// 256 prompts' heads of up to 8,001 tokens: 488 us, 3.2 TB/s.
+// a graph of calls: 640 us, of which this kernel takes 455 on 144 SMs (2.7 us a
+// chunk) and the launch before it 178; the bytes are 156 us at the copy rate.
+// A chunk's products take 2,600 cycles of the tensor pipe when nothing waits,
+// and some 2,100 cycles of shared memory's reads, which the other warps' loads
+// and stores queue behind; issue slots are used at 54%.
+// 256 prompts' heads of up to 8,001 tokens: 544 us, 2.8 TB/s.
 //
 // A long prompt of few heads is cut into segments: a first launch (OUT false)
 // computes what each but the last adds to a state of zeros, state_join_kernel
@@ -93,7 +94,7 @@ struct ChunkShape {
 };
 
 struct alignas(16) Decays {
-  float nhi[kChunk], nlo[kChunk];  // minus the running sum in units of log 2: multiples of 1/8, rest
+  float nhi[kChunk], nlo[kChunk];  // minus the running sum in units of log 2: whole ones, rest
   float ei[kChunk], more[kChunk];  // scale e^{G_i}: the product of both; more is written where grows is true, else all are 1
   float left[kChunk];              // e^{G_last - G_j}, 0 past the request's rows
   float afac[kChunk];              // fp16: what row i of A was divided by
@@ -819,7 +820,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           put_outputs<DT>(o1_of(c) + lanes, tmem + lanes + kO2, d, k, m, sf, sm.stage[quarter][0], o, P.os[1],
                           dv0 + col < P.value_dim, bad);
         const float2 b2 = unpack2(bad);
-        if (__any_sync(~0u, !(b2.x == 0.0f && b2.y == 0.0f)) || d.grows) [[unlikely]] {  // a row's sum that is no number: without the rows that it does not follow
+        if (__any_sync(~0u, !(b2.x == 0.0f && b2.y == 0.0f)) || d.grows) [[unlikely]] {  // a row's sum that is no number: without the rows that it
+          // does not follow; or growth beyond one factor
           __syncwarp();  // (other lanes' stores of the same rows)
 #pragma unroll 1
           for (int i = 0; i < m; ++i) {
@@ -898,7 +900,7 @@ cudaError_t launch_chunks(const StateChunkPlan &A, const CUtensorMap *maps, cuda
 // (request, head, 128 columns) goes through the steps above once, P's columns
 // of tensor memory becoming O2's, so that two CTAs share an SM and one loads
 // its state while the other computes.  16 trees of 60 nodes, 48 heads: 64 us
-// as a chunk of the kernel above (one CTA to an SM), 32 us so.  Half of tensor
+// as a chunk of the kernel above (one CTA to an SM), 34 us so.  Half of tensor
 // memory holds two of S's pieces at a time: in bf16 the largest waits in
 // registers until O1 has taken the others.
 constexpr int kShortThreads = 256;

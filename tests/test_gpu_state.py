@@ -11,6 +11,7 @@ BF, HF = torch.bfloat16, torch.float16
 # rows' type.  In bf16 the first leaves out at most half of its step, 2^(e - 8) of a value from 2^e on; that lies in the binade
 # below, so the second, of 8 bits too, leaves out at most half of 2^(e - 9 - 7): 2^-17 of the value (fp16: 2^-23).  An output
 # passes S's pieces, and S is made of keys' pieces: twice that.
+# Three pieces hold all of a bf16 operand's digits now; tests/test_gpu_state_digits.py holds every kernel to what it reaches, without this.
 PIECES = 2.0 ** -16
 
 
