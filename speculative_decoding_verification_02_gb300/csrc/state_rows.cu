@@ -27,6 +27,7 @@
 // that stay and fetch the next unit's state ahead were slower (82, 90, 119 us):
 // fewer warps.
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.h"
 #include "state.cuh"
@@ -110,9 +111,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
   __shared__ __align__(16) char ks[MODE == kTree ? 1 : kBlock][MODE == kTree ? 16 : Tile::kStride];
   __shared__ __align__(16) uint16_t vs[MODE == kTree ? 1 : kBlock][kMaxWarps * 16];
   __shared__ float gs[2][kBlock], left[kBlock], from_state[kBlock];
-  __shared__ float total, more;
+  __shared__ float total, total_more, from_more[kBlock];  // (more: a second factor, 1 unless the first alone would be no number)
   __shared__ float pair[MODE == kChain ? kBlock : 1][kBlock];
-  __shared__ float path_w[MODE == kTree ? kBlock : 1][kMaxPath], path_more[kBlock];
+  __shared__ float path_w[MODE == kTree ? kBlock : 1][kMaxPath];
   __shared__ int path[MODE == kTree ? kBlock : 1][kMaxPath], path_len[kBlock];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
@@ -217,25 +218,25 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
   if (status != SPEC_STATUS_OK) count = 0;
 
 #pragma unroll 1
-  for (int t0 = 0, m, side = 0; t0 < count; t0 += m, side ^= 1) {
-    m = min(kBlock, count - t0);
+  for (int t0 = 0; t0 < count; t0 += kBlock) {
+    const int m = min(kBlock, count - t0), side = t0 / kBlock & 1;
     if (t0 > 0) fetch(t0, m, side);
     cp_async_wait_all();
     __syncthreads();
+    bool grows = false;  // some factor of the block's on the state takes two
     if (MODE != kTree) {
       // ---- decays: every warp the sums it needs, the first the factors
       const Log2Sum upto = running<kBlock>(lane < m ? log2_of(gs[side][lane]) : Log2Sum{0}, lane);
-      uint32_t nan = __ballot_sync(~0u, lane < m && gs[side][lane & 15] != gs[side][lane & 15]);
-      // growth that no factor of the state's can hold: a token alone, the state first by one part of its factor
-      const bool grows = __any_sync(~0u, lane < m && upto.units > P.most_units);
-      if (grows) [[unlikely]] m = 1, nan &= 1;
+      const uint32_t nan = __ballot_sync(~0u, lane < m && gs[side][lane & 15] != gs[side][lane & 15]);
+      grows = __any_sync(~0u, lane < m && upto.units > P.most_units);
       const Log2Sum all = of_lane(upto, m - 1);
       if (warp == 0 && lane < m) {
         const Log2Parts p = upto.parts(nan & ((2u << lane) - 1));
-        float second;
-        from_state[lane] = state_factor(p, MODE == kChain ? P.scale : 1.0f, P.scale_log2, second);
+        float more;
+        from_state[lane] = state_factor(p, MODE == kChain ? P.scale : 1.0f, P.scale_log2, more);
+        from_more[lane] = more;
         left[lane] = (all - upto).parts(nan >> lane >> 1).power();
-        if (lane == m - 1) total = state_factor(p, 1.0f, P.scale_log2, second), more = second;
+        if (lane == m - 1) total = state_factor(p, 1.0f, 0.0f, more), total_more = more;
       }
       if constexpr (MODE == kChain) {
         // ---- the pairs' weights: a row to a warp, a token before it to 2, 4 or 8 lanes, each of its share of key_dim's pieces
@@ -260,13 +261,6 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
         }
       }
       __syncthreads();
-      if (grows) [[unlikely]] {
-        const pair_t f2 = pack2(more, more);
-#pragma unroll
-        for (int r = 0; r < RPL / 2; ++r)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) S[r][e] = mul2(S[r][e], f2);
-      }
     } else {
       if (tid < m) {  // the row's path from itself up, and the decays that lie before each node of it
         int len = 0;
@@ -280,7 +274,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
           sum += log2_of(x), nan |= x != x;
         }
         path_len[tid] = len;
-        from_state[tid] = state_factor(sum.parts(nan), P.scale, P.scale_log2, path_more[tid]);
+        from_state[tid] = state_factor(sum.parts(nan), P.scale, P.scale_log2, from_more[tid]);
       }
       __syncthreads();
       for (int i = 0; i < m; ++i) {
@@ -313,8 +307,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
         };
         if (g < m) v0 = load_v(g);
         if (g + 8 < m) v1 = load_v(g + 8);
-        auto row = [&](int i) -> float {
-          const float4 s = row_product<DT, RPL>(qs[i], g, S);
+        auto row = [&](int i, auto grown) -> float {
+          float4 s = row_product<DT, RPL>(qs[i], g, S);
+          if constexpr (decltype(grown)::value) s = make_float4(s.x * from_more[i], s.y * from_more[i], s.z * from_more[i], s.w * from_more[i]);
           const float e = from_state[i];
           float4 f = make_float4(s.x * e, s.y * e, s.z * e, s.w * e);
           if (g <= i) {
@@ -328,20 +323,27 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
           return group_sum(f, g);
         };
         int i = 0;
+        if (grows) [[unlikely]] {
+#pragma unroll 1
+          for (; i < m; ++i, o16 += P.os[1]) {
+            const float a = row(i, std::true_type{});
+            if (!(g & 1)) *o16 = narrow<DT>(a);
+          }
+        }
 #pragma unroll 1
         for (; i + 2 <= m; i += 2) {  // two rows side by side: the one's reduction behind the other's products
-          const float a = row(i), d = row(i + 1);
+          const float a = row(i, std::false_type{}), d = row(i + 1, std::false_type{});
           o16[(g & 1) * P.os[1]] = narrow<DT>(g & 1 ? d : a);
           o16 += 2 * P.os[1];
         }
         if (i < m) {
-          const float a = row(i);
+          const float a = row(i, std::false_type{});
           if (!(g & 1)) *o16 = narrow<DT>(a);
         }
       } else {
 #pragma unroll 1
         for (int i = 0; i < m; ++i) {
-          float sum = group_sum(row_product<DT, RPL>(qs[i], g, S), g) * path_more[i] * from_state[i], terms = 0.0f;
+          float sum = group_sum(row_product<DT, RPL>(qs[i], g, S), g) * from_more[i] * from_state[i], terms = 0.0f;
           for (int p = g & 1; p < path_len[i]; p += 2) {
             const uint16_t v = *reinterpret_cast<const uint16_t *>(vp + (static_cast<int64_t>(path[i][p]) * P.vs[1] + col0 + col) * 2);
             terms = fmaf(path_w[i][p], widen<DT>(v), terms);
@@ -354,7 +356,14 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
     }
 
     // ---- the state behind the block
-    if (MODE != kTree && live && (P.to.state || t0 + m < count)) {
+    if (MODE != kTree && live && (P.to.state || t0 + kBlock < count)) {
+      if (grows) [[unlikely]] {
+        const pair_t more = pack2(total_more, total_more);
+#pragma unroll
+        for (int r = 0; r < RPL / 2; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[r][e] = mul2(S[r][e], more);
+      }
       const pair_t f2 = pack2(total, total);
 #pragma unroll
       for (int r = 0; r < RPL / 2; ++r)
@@ -377,7 +386,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, RPL == 32 ? 2 : 4) state_rows_
         }
       }
     }
-    if (t0 + m < count) __syncthreads();  // before the next block's rows
+    if (t0 + kBlock < count) __syncthreads();  // before the next block's rows
   }
   cp_async_wait_all();
 

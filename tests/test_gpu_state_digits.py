@@ -258,6 +258,21 @@ def test_a_large_state_all_but_forgotten(api, kind, dtype, forget, off):
         assert bool(((out.double().cpu() - outs[0]).abs() <= rounded(outs[0], tol, dtype)).all())
 
 
+@pytest.mark.parametrize("forget", [-90.0, -float("inf")])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("kind", KINDS)
+def test_growth_that_is_taken_back(api, kind, dtype, forget):
+    """A state that would pass the largest number by e^100 and is forgotten, or comes back to e^10 of itself, within a block."""
+    c = Call(kind, dtype, 64, 48)
+    d = torch.tensor(c.depth)
+    c.S0 *= 1e3
+    c.g[d == 0] = 100.0
+    c.g[d == 3] = forget
+    c.q[d < 3] = 0  # (no such outputs)
+    c.v[d == 0] = 0
+    c.check(api)
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_two_tokens_of_growth(api, dtype):
     """A fresh request, two factors of e^50: k_1 v_1 e^50 + k_2 v_2, whichever kernel."""
