@@ -485,7 +485,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         warp_arrive(&sm.k_read[c & 3], lane);
         float back;
         const float fit = fit_half(__reduce_max_sync(~0u, __float_as_uint(fmaxf(most, 0.0f))), back);
-        *reinterpret_cast<float2 *>(&d.left[2 * lane]) = make_float2(left.x * fit, left.y * fit);
+        // (no infinity for a key of zeros: the others' stay below 2^39; NaN stays)
+        auto kept = [](float x) { return x > 0x1p126f ? 0x1p126f : x; };
+        *reinterpret_cast<float2 *>(&d.left[2 * lane]) = make_float2(kept(left.x * fit), kept(left.y * fit));
         if (lane == 0) d.kfac = back;
       }
       warp_arrive(&sm.dec_full[r], lane);

@@ -270,7 +270,12 @@ def test_growth_that_is_taken_back(api, kind, dtype, forget):
     c.g[d == 3] = forget
     c.q[d < 3] = 0  # (no such outputs)
     c.v[d == 0] = 0
-    c.check(api)
+    out, state = c.run(api)
+    outs, last = c.want()
+    if state is not None:
+        ref.check_state(state, last, c.n, c.n)
+    if out is not None and dtype == BF:  # (1e3 e^10 is 2.2e7, an infinity in fp16: no value to compare)
+        ref.check_out(out, outs, c.D, c.n, dtype)
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
@@ -338,6 +343,19 @@ def test_small_keys_beside_large_ones(api, n, large):
         assert not got[0].isfinite().any()
     else:
         assert float((got[0] - want[0]).norm() / want[0].norm()) <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("kind", KINDS)
+def test_keys_of_zeros_before_growth(api, kind, dtype):
+    """Tokens without keys whose factor is e^60 beside keys whose factor is e^-40: nothing times the one, all digits of the other."""
+    c = Call(kind, dtype, 64, 49)
+    d = torch.tensor(c.depth)
+    c.S0 *= 0
+    c.g[d == 4] = -100.0
+    c.k[d >= 4] = 0
+    c.g[d == 8] = 60.0
+    c.check(api)
 
 
 @pytest.mark.parametrize("n,write", [(5, False), (5, True), (40, False), (64, True), (150, True), (900, True)])
