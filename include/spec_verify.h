@@ -633,8 +633,9 @@ size_t spec_cache_workspace_size(int op, const spec_cache *cache, int B, int N, 
  *
  * spec_state_workspace_size -- bytes for a call of op (B requests, n tokens or
  * nodes) over states of this geometry (its pointers are not read); 0 for
- * invalid arguments and for calls that need none.  The workspace needs no
- * initialisation.
+ * invalid arguments and for calls that need none.  A call of fewer requests may
+ * need more: a long prompt of few heads is cut into segments.  The workspace
+ * needs no initialisation.
  */
 typedef struct spec_state {
   float *state;

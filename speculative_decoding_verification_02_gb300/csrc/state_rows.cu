@@ -13,15 +13,15 @@
 // token by token: three).  Lane group g adds the terms of tokens g and g + 8 to
 // its part of q_i S, so one reduction over the groups serves both.  The sums
 // are exact (fixed point), so their differences are: forgetful tokens and long
-// blocks lose nothing.  A tree's row takes its ancestors' terms instead, one after another
-// along its path, with k and v from memory.
+// blocks lose nothing.  A tree's row takes its ancestors' terms instead, one
+// after another along its path, with k and v from memory.
 //
 // The rows' copies to shared memory are under way before the state's loads
 // wait for the request's slot.
 //
 // Bound by the state's bytes: 64 requests' single tokens, 48 heads of 128 x 128,
 // 71 us in a graph of calls (5.7 TB/s; copying the states alone 60 us, as fast
-// as a plain copy), their commits of up to 9 rows 77 us; as many read only 69 us
+// as a plain copy), their commits of up to 9 rows 76 us; as many read only 69 us
 // (3.1 TB/s): the rows' arithmetic, some 60 instructions a row and warp, is not
 // hidden.  One request's token 4.8 us, 5 rows 5.7 us: a chain of loads.  CTAs
 // that stay and fetch the next unit's state ahead were slower (82, 90, 119 us):
